@@ -1,4 +1,5 @@
-"""ctypes binding of libcsbp (include/csbp.h): argument marshalling only.
+"""ctypes binding of libcsbp (include/csbp.h, csbp_vocab_ce.h,
+csbp_generate.h): argument marshalling only.
 
 Every step of the attention path runs in the library's kernels; PyTorch is
 used here only to own device memory and to name the current CUDA stream.
@@ -59,6 +60,38 @@ class ScheduleInfo(ctypes.Structure):
                 ("problem_key", ctypes.c_uint64)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class CacheRows(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("table_pages", ctypes.c_int32), ("table", ctypes.c_void_p),
+                ("start", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("stride_tok", ctypes.c_int64 * 2), ("stride_batch", ctypes.c_int64 * 2)]
+
+
+class PrefixProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "queries", "prefix_len", "own_max", "Hq", "Hkv", "d", "causal")] + [
+                    ("scale", ctypes.c_float)]
+
+
+class PrefixInputs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("q", "k_prefix", "v_prefix", "k_own", "v_own", "own_len")] + [
+                    ("stride_tok", ctypes.c_int64 * 5), ("stride_batch", ctypes.c_int64 * 5)]
+
+
+class VerifyProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("drafts", ctypes.c_int32),
+                ("vocab", ctypes.c_int32)] + [
+                    (n, ctypes.c_int64) for n in ("p_row", "p_batch", "q_row", "q_batch")]
+
+
 _lib = None
 _lib_path = LIB_PATH
 DEBUG_LIB_PATH = os.path.join(_PKG, "libcsbp_debug.so")
@@ -108,7 +141,14 @@ def lib():
         L.csbp_ce_workspace_bytes.argtypes = [P(CeProblem)]
         L.csbp_ce_workspace_bytes.restype = sz
         L.csbp_vocab_ce.argtypes = [P(CeProblem), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        for fn in ("csbp_block_schedule", "csbp_attn_fwd", "csbp_attn_bwd", "csbp_lse_merge",
+        L.csbp_cache_write.argtypes = [P(KvCache), P(CacheRows), vp, vp, vp]
+        L.csbp_cache_read.argtypes = [P(KvCache), P(CacheRows), vp, vp, vp]
+        L.csbp_prefix_workspace_bytes.argtypes = [P(PrefixProblem)]
+        L.csbp_prefix_workspace_bytes.restype = sz
+        L.csbp_attn_prefix.argtypes = [P(PrefixProblem), P(PrefixInputs), vp, vp, vp, sz, vp]
+        L.csbp_draft_verify.argtypes = [P(VerifyProblem)] + [vp] * 9
+        for fn in ("csbp_cache_write", "csbp_cache_read", "csbp_attn_prefix",
+                   "csbp_draft_verify", "csbp_block_schedule", "csbp_attn_fwd", "csbp_attn_bwd", "csbp_lse_merge",
                    "csbp_check_status", "csbp_kernel_timing", "csbp_kernel_timing_read",
                    "csbp_kernel_timing_read_kind", "csbp_vocab_ce", "csbp_wait_selftest"):
             getattr(L, fn).restype = ctypes.c_int
@@ -527,3 +567,281 @@ class VocabCrossEntropy:
 
     def check(self, stream=None):
         check_status(self.ws, stream)
+
+
+# ----------------------------------------------------------------- generation
+class _Call:
+    """Argument checks of the generation operators: dtype, shape and layout of
+    every tensor first, then (in `stream`) that all of them are on one CUDA
+    device, which the call makes current."""
+
+    def __init__(self, fn):
+        self.fn = fn
+        self.seen = []
+
+    def tensor(self, name, t, dtype, shape):
+        """A contiguous tensor."""
+        self.shaped(name, t, dtype, shape)
+        if not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {name} must be contiguous")
+        return t.data_ptr()
+
+    def shaped(self, name, t, dtype, shape):
+        if t is None:
+            raise ValueError(f"{self.fn}: {name} is required")
+        if t.dtype != dtype:
+            raise ValueError(f"{self.fn}: {name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{self.fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
+        self.seen.append((name, t))
+
+    def strided(self, name, t, shape):
+        """A bf16 [batch][rows][heads][d] tensor (or [rows][heads][d]) whose
+        tokens and batch entries may be strided: (pointer, token stride, batch
+        stride), 0 where the dimension has one entry."""
+        import torch
+        self.shaped(name, t, torch.bfloat16, shape)
+        st = t.stride()
+        H, d = shape[-2:]
+        row = H * d
+        if t.numel() == 0:
+            return t.data_ptr(), 0, 0
+        if st[-1] != 1 or (H > 1 and st[-2] != d):
+            raise ValueError(f"{self.fn}: {name} must have contiguous heads and features "
+                             f"(strides [..., d, 1]), got {tuple(st)}")
+        tok = st[-3] if shape[-3] > 1 else 0
+        if shape[-3] > 1 and (tok < row or tok % 8):
+            raise ValueError(f"{self.fn}: {name} token stride {tok} must be >= H*d = {row} and "
+                             f"a multiple of 8")
+        bat = st[0] if len(shape) == 4 and shape[0] > 1 else 0
+        if len(shape) == 4 and shape[0] > 1 and (bat < shape[1] * (tok or row) or bat % 8):
+            raise ValueError(f"{self.fn}: {name} batch entries must not interleave (batch stride "
+                             f">= rows x token stride, a multiple of 8), got {bat}")
+        return t.data_ptr(), tok, bat
+
+    def device(self):
+        """The CUDA device of all tensors."""
+        dev = None
+        for name, t in self.seen:
+            if not t.is_cuda:
+                raise ValueError(f"{self.fn}: {name} must be a CUDA tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{self.fn}: {name} is on {t.device}, other tensors on {dev}")
+        return dev
+
+    def run(self, stream, *args):
+        """Call the library on `stream` (default: the device's current one)."""
+        import torch
+        dev = self.device()
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"{self.fn}: the stream is on {stream.device}, the tensors on {dev}")
+        f = getattr(lib(), self.fn)
+        if torch.cuda.current_device() == dev.index:
+            _check(self.fn, f(*args, stream.cuda_stream))
+        else:
+            with torch.cuda.device(dev):
+                _check(self.fn, f(*args, stream.cuda_stream))
+
+
+class QuantCache:
+    """One layer's paged K/V cache in E4M3 with a power-of-two scale per 32
+    features of a head (csbp_cache_write / csbp_cache_read).
+
+    Owns (or, with `storage`, wraps) the uint8 tensors k, v [pages][page_size]
+    [Hkv][d] and k_scale, v_scale [pages][page_size][Hkv][d / 32].  Which pages
+    a sequence has is the caller's: `table` int32 [batch][n] names them in
+    order, `start` int32 [batch] is the position of row 0 of each sequence.
+    """
+
+    def __init__(self, pages, page_size, Hkv, d, device="cuda", storage=None):
+        import torch
+        if min(pages, page_size, Hkv) < 1 or d < 32 or d > 1024 or d % 32:
+            raise ValueError("QuantCache: pages, page_size and Hkv must be positive and d a "
+                             "multiple of 32 up to 1024")
+        code = (pages, page_size, Hkv, d)
+        scale = (pages, page_size, Hkv, d // 32)
+        if storage is None:
+            storage = [torch.zeros(s, dtype=torch.uint8, device=device)
+                       for s in (code, code, scale, scale)]
+        self.k, self.v, self.k_scale, self.v_scale = storage
+        c = _Call("QuantCache")
+        self._tensors = list(zip(("k", "v", "k_scale", "v_scale"), storage))
+        ptrs = [c.tensor(n, t, torch.uint8, s)
+                for (n, t), s in zip(self._tensors, (code, code, scale, scale))]
+        self.Hkv, self.d = Hkv, d
+        self.struct = KvCache(pages, page_size, Hkv, d, *ptrs)
+
+    def _rows(self, c, k, v, table, start, count):
+        import torch
+        if k is None or k.dim() != 4:
+            raise ValueError(f"{c.fn}: k must be a [batch][rows][Hkv][d] tensor")
+        batch, rows = k.shape[:2]
+        shape = (batch, rows, self.Hkv, self.d)
+        kp, kt, kb = c.strided("k", k, shape)
+        vp, vt, vb = c.strided("v", v, shape)
+        if table is None or table.dim() != 2:
+            raise ValueError(f"{c.fn}: table must be a [batch][pages] tensor")
+        r = CacheRows(batch, rows, table.shape[1],
+                      c.tensor("table", table, torch.int32, (batch, table.shape[1])),
+                      c.tensor("start", start, torch.int32, (batch,)),
+                      None if count is None else c.tensor("count", count, torch.int32, (batch,)),
+                      (kt, vt), (kb, vb))
+        c.seen += self._tensors
+        return r, kp, vp, batch * rows
+
+    def write(self, k, v, table, start, count=None, stream=None):
+        """Quantise bf16 k, v [batch][rows][Hkv][d] (token and batch strides
+        free) into the pages; rows i >= count[b] are not written."""
+        c = _Call("csbp_cache_write")
+        r, kp, vp, n = self._rows(c, k, v, table, start, count)
+        if n:
+            c.run(stream, ctypes.byref(self.struct), ctypes.byref(r), kp, vp)
+
+    def read(self, table, start, count=None, rows=None, out=None, stream=None):
+        """bf16 (k, v) [batch][rows][Hkv][d] of positions start[b] .. ; `out`
+        receives them (rows i >= count[b] keep what they hold), else two
+        tensors of `rows` rows are allocated (zero beyond count)."""
+        import torch
+        c = _Call("csbp_cache_read")
+        if out is None:
+            if rows is None or table is None:
+                raise ValueError("csbp_cache_read: needs `rows` or `out`")
+            shape = (table.shape[0], rows, self.Hkv, self.d)
+            out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=self.k.device)
+                        for _ in range(2))
+        r, kp, vp, n = self._rows(c, out[0], out[1], table, start, count)
+        if n:
+            # an expanded output would take several rows at one place
+            for name, t in (("k", out[0]), ("v", out[1])):
+                if any(s == 0 and e > 1 for s, e in zip(t.stride(), t.shape)):
+                    raise ValueError(f"csbp_cache_read: {name} has a broadcast dimension")
+            c.run(stream, ctypes.byref(self.struct), ctypes.byref(r), kp, vp)
+        return out
+
+
+class PrefixAttention:
+    """Attention of `batch` sequences of `queries` tokens that share a prefix
+    of prefix_len keys and have up to own_max keys of their own
+    (csbp_attn_prefix).  Owns the workspace of one shape.
+
+    forward(q, k_prefix, v_prefix, k_own, v_own, own_len) takes bf16 q
+    [batch][queries][Hq][d], prefix K/V [prefix_len][Hkv][d], own K/V
+    [batch][own_max][Hkv][d] and int32 own_len [batch], and returns (o, lse):
+    bf16 [batch][queries][Hq][d] and fp32 [batch][Hq][queries].  causal: the
+    queries are the last tokens of own_len and read own keys up to themselves;
+    otherwise (a block being denoised) they read all own_len keys.  The prefix
+    (own) tensors may be None when prefix_len (own_max) is 0.
+    """
+
+    def __init__(self, batch, queries, prefix_len, own_max, Hq, Hkv, d, causal=False,
+                 scale=None, device="cuda"):
+        import torch
+        self.problem = PrefixProblem(batch, queries, prefix_len, own_max, Hq, Hkv, d,
+                                     1 if causal else 0,
+                                     float(scale if scale is not None else d ** -0.5))
+        if torch.device(device).type == "cuda":
+            with torch.cuda.device(device):
+                n = prefix_workspace_bytes(self.problem)
+        else:
+            n = prefix_workspace_bytes(self.problem)
+        if n == 0:
+            raise CsbpError("csbp_prefix_workspace_bytes", -1)
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.device = device
+
+    def alloc_outputs(self):
+        import torch
+        p = self.problem
+        return (torch.empty((p.batch, p.queries, p.Hq, p.d), dtype=torch.bfloat16,
+                            device=self.device),
+                torch.empty((p.batch, p.Hq, p.queries), dtype=torch.float32, device=self.device))
+
+    def forward(self, q, k_prefix, v_prefix, k_own, v_own, own_len, out=None, stream=None):
+        o, lse = out if out is not None else self.alloc_outputs()
+        attn_prefix(self.problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, self.ws,
+                    stream)
+        return o, lse
+
+    def check(self, stream=None):
+        check_status(self.ws, stream)
+
+
+def prefix_workspace_bytes(problem: PrefixProblem) -> int:
+    return int(lib().csbp_prefix_workspace_bytes(ctypes.byref(problem)))
+
+
+def attn_prefix(problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, workspace,
+                stream=None):
+    import torch
+    c = _Call("csbp_attn_prefix")
+    p = problem
+    pre = (p.prefix_len, p.Hkv, p.d)
+    mine = (p.batch, p.own_max, p.Hkv, p.d)
+    none = (None, 0, 0)
+    s = [c.strided("q", q, (p.batch, p.queries, p.Hq, p.d)),
+         c.strided("k_prefix", k_prefix, pre) if p.prefix_len else none,
+         c.strided("v_prefix", v_prefix, pre) if p.prefix_len else none,
+         c.strided("k_own", k_own, mine) if p.own_max else none,
+         c.strided("v_own", v_own, mine) if p.own_max else none]
+    lens = c.tensor("own_len", own_len, torch.int32, (p.batch,)) if p.own_max else None
+    inp = PrefixInputs(*(x[0] for x in s), lens, tuple(x[1] for x in s), tuple(x[2] for x in s))
+    po = c.tensor("o", o, torch.bfloat16, (p.batch, p.queries, p.Hq, p.d))
+    pl = c.tensor("lse", lse, torch.float32, (p.batch, p.Hq, p.queries))
+    if workspace is None:
+        raise ValueError("csbp_attn_prefix: workspace is required")
+    n = workspace.numel()
+    pw = c.tensor("workspace", workspace, torch.uint8, (n,))
+    c.run(stream, ctypes.byref(problem), ctypes.byref(inp), po, pl, pw, n)
+
+
+def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
+    """csbp_draft_verify: fp32 p [batch][drafts + 1][vocab] and q [batch]
+    [drafts][vocab] (rows and batch entries may be strided), int32 token and
+    fp32 u [batch][drafts], fp32 r [batch], int32 length [batch] or None.
+    Returns int32 (accepted [batch], tokens [batch][drafts + 1]: the accepted
+    drafts, the next token, then -1); `out` receives them if given.  q, token
+    and u may be None when p has one row per sequence (plain sampling)."""
+    import torch
+    c = _Call("csbp_draft_verify")
+    if p is None or p.dim() != 3 or p.shape[1] < 1:
+        raise ValueError("csbp_draft_verify: p must be a [batch][drafts + 1][vocab] tensor")
+    batch, K, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+
+    def rows(name, t, n):
+        c.shaped(name, t, torch.float32, (batch, n, V))
+        if t.numel() == 0:
+            return t.data_ptr(), 0, 0
+        st = t.stride()
+        if V > 1 and st[2] != 1:
+            raise ValueError(f"csbp_draft_verify: {name} must have contiguous rows")
+        row = st[1] if n > 1 else V
+        if row < V:
+            raise ValueError(f"csbp_draft_verify: {name} rows must not overlap (stride {row})")
+        if batch > 1 and st[0] < n * row:
+            raise ValueError(f"csbp_draft_verify: {name} batch entries must not interleave "
+                             f"(stride {st[0]})")
+        return t.data_ptr(), row, st[0] if batch > 1 else 0
+
+    pp, p_row, p_batch = rows("p", p, K + 1)
+    qp, q_row, q_batch, tp, up = None, 0, 0, None, None
+    if K > 0:
+        qp, q_row, q_batch = rows("q", q, K)
+        tp = c.tensor("token", token, torch.int32, (batch, K))
+        up = c.tensor("u", u, torch.float32, (batch, K))
+    rp = c.tensor("r", r, torch.float32, (batch,))
+    lp = None if length is None else c.tensor("length", length, torch.int32, (batch,))
+    if out is None:
+        accepted = torch.empty((batch,), dtype=torch.int32, device=p.device)
+        tokens = torch.empty((batch, K + 1), dtype=torch.int32, device=p.device)
+    else:
+        accepted, tokens = out
+    ap = c.tensor("accepted", accepted, torch.int32, (batch,))
+    op = c.tensor("tokens", tokens, torch.int32, (batch, K + 1))
+    if batch:
+        prob = VerifyProblem(batch, K, V, p_row, p_batch, q_row, q_batch)
+        c.run(stream, ctypes.byref(prob), pp, qp, tp, up, rp, lp, ap, op)
+    return accepted, tokens

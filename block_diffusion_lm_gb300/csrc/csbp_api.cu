@@ -322,7 +322,7 @@ extern "C" csbp_status csbp_kernel_timing_read_kind(int32_t kind, double* ms, in
   return CSBP_OK;
 }
 
-extern "C" int32_t csbp_version(void) { return 400; }  // 0.4.0: per-rank query rows
+extern "C" int32_t csbp_version(void) { return 500; }  // 0.5.0: generation operators
 
 extern "C" const char* csbp_status_string(csbp_status s) {
   switch (s) {

@@ -329,7 +329,9 @@ csbp_status csbp_kernel_timing_read(double* fwd_ms, int32_t* n_fwd, double* bwd_
  * of the attention calls: 6 the LSE merge (one per query stream and batch
  * entry), 7 the backward preprocess and 8 the dQ convert (one per query
  * stream), 9 the dK/dV converts of a windowed backward (one pair per key
- * stream); 10 csbp_e4m3_to_bf16.  One event pair per launch.
+ * stream); 10 csbp_e4m3_to_bf16; and (csbp_generate.h) 11 csbp_cache_write,
+ * 12 csbp_cache_read, 13 the attention kernel of csbp_attn_prefix and 14 the
+ * joining of its key ranges, 15 csbp_draft_verify.  One event pair per launch.
  * CSBP_ERR_INVALID for another kind. */
 csbp_status csbp_kernel_timing_read_kind(int32_t kind, double* ms, int32_t* n);
 
@@ -351,7 +353,8 @@ const char* csbp_status_string(csbp_status status);
  * csbp_vocab_ce.h), csbp_wait_selftest and csbp_kernel_timing_read_kind.
  * 0.3.0 (300) added the token and batch strides of csbp_inputs and
  * csbp_schedule_info.problem_key.  0.4.0 (400) added csbp_problem.per_rank
- * and rank (one CSBP rank's query rows) and csbp_attn_bwd_noalloc_status. */
+ * and rank (one CSBP rank's query rows) and csbp_attn_bwd_noalloc_status.
+ * 0.5.0 (500) added csbp_generate.h. */
 int32_t csbp_version(void);
 
 #ifdef __cplusplus
