@@ -249,6 +249,24 @@ bool encode_map_2d(void* map, bool f32, const void* base, uint64_t inner, uint64
   return r == CUDA_SUCCESS;
 }
 
+bool encode_map_bf16(void* map, int rank, const void* base, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box) {
+  auto enc = encode_fn();
+  if (!enc || rank < 2 || rank > 4) return false;
+  cuuint64_t dm[4], st[3];
+  cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    dm[i] = dims[i];
+    bx[i] = box[i];
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             static_cast<cuuint32_t>(rank), const_cast<void*>(base), dm, st, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace csbp
 
 using namespace csbp;
