@@ -2,15 +2,16 @@
 // sm_103a: softmax(scale q K^T) V over the prefix keys, which all sequences
 // read, and each sequence's own keys.
 //
-// Rows.  A KV head's query rows are (sequence, token, head of its group).  A
-// row tile packs up to 128 of them: whole sequences while they fit (`tb` of
-// `tn` = queries tokens), else tokens of one sequence (tb = 1).  One 4-D TMA
-// box {64 features, heads, tn tokens, tb sequences} loads it in that order, so
-// the prefix K/V pass through the tensor cores once per 128 rows however they
-// divide into sequences, tokens and heads, and any token or batch stride of q
-// goes into the map.  With tb = 1 a tile's keys are the prefix, then its
-// sequence's own keys, in one softmax; with tb > 1 the own keys are separate
-// units with a row tile per sequence.
+// Rows.  The query rows of one KV head are (sequence, token, head of the
+// group), flattened in that order; a row tile is 128 consecutive ones, so the
+// prefix K/V pass through the tensor cores once per 128 rows however they
+// divide into sequences, tokens and heads.  The softmax warps copy the tile's
+// rows into shared memory themselves (a row per thread, zeros for the rest),
+// which takes any token or batch stride and any group size.  Where row tiles
+// kept inside sequences need (nearly) no more of them than tiles packed over
+// sequences, a tile's keys are the prefix and then its sequence's own keys, in
+// one softmax (`fused`); else the prefix runs on packed tiles and the own keys
+// on separate units with tiles inside sequences.
 //
 // Units.  One CTA owns two row tiles ("slots") of one head group and a range
 // of their key tiles; a key tile that both read is loaded once.  Each slot has
@@ -60,21 +61,24 @@ constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsSoftmax;
 
 // How the rows and keys of a problem are cut up (host and device).
 struct Plan {
-  int32_t gs, n_groups;     // query heads per row tile, groups of them
-  int32_t tn, tb;           // tokens and sequences per row tile
-  int32_t tiles_seq;        // row tiles per sequence (tb == 1)
-  int32_t row_tiles;        // per head group
-  int32_t pairs;            // CTAs per head group and key range
-  int32_t splits;           // key ranges of the shared units
-  int32_t own_pairs;        // CTAs per head group and range of the own units; 0: none (tb == 1)
+  int32_t gs, n_groups;   // query heads per row group, groups of them
+  int32_t seq_rows;       // rows of one sequence: queries x gs
+  int32_t tiles_seq;      // row tiles of one sequence
+  int32_t fused;          // 1: tiles inside sequences read the prefix and the own keys
+  int32_t row_tiles;      // of the shared units, per head group
+  int32_t pairs;          // CTAs of the shared units per head group and key range
+  int32_t splits;         // key ranges of the shared units
+  int32_t own_pairs;      // CTAs per head group and range of the own units; 0: none
   int32_t own_splits;
-  int32_t parts;            // splits + own splits; 1: written directly
+  int32_t parts;          // splits + own splits; 1: written directly
 };
 
 struct PrefixParams {
   Plan plan;
   int32_t batch, queries, prefix_len, own_max, Hq, G, causal;
   float scale_log2;
+  const __nv_bfloat16* q;
+  int64_t q_tok, q_bat;  // element strides
   const int32_t* own_len;
   __nv_bfloat16* o;   // [batch][queries][Hq][d]
   float* lse;         // [batch][Hq][queries]
@@ -113,12 +117,13 @@ struct PrefixLayout {
 // One CTA's work, the same for all its threads.
 struct Unit {
   int group, part;
-  bool own;          // an own-keys unit (tb > 1): no prefix
-  bool alternate;    // one row tile, both slots
-  int tile[2];       // row tile (shared unit) or sequence (own unit) of a slot
-  int np;            // prefix key tiles
-  int c[2], nc[2];   // own keys and key tiles of a slot's sequence (tb == 1 or own)
-  int m0, m1;        // this CTA's range of the key-tile list
+  bool alternate;      // one row tile, both slots
+  int64_t row0[2];     // first flattened row of a slot's tile
+  int rows[2];         // its rows
+  int seq[2];          // its sequence (fused and own units)
+  int np;              // prefix key tiles
+  int c[2], nc[2];     // own keys and key tiles of a slot's sequence
+  int m0, m1;          // this CTA's range of the key-tile list
 
   // The m-th key tile of the list: prefix tiles first, then the two slots'
   // own tiles in turn.  Returns which slots read it.
@@ -143,74 +148,50 @@ struct Unit {
   }
 };
 
-__device__ __forceinline__ int sequence_of(const PrefixParams& p, int row_tile) {
-  return p.plan.tb == 1 ? row_tile / p.plan.tiles_seq : row_tile * p.plan.tb;
-}
-
-__device__ __forceinline__ int own_keys(const PrefixParams& p, int b) {
-  return p.own_max > 0 ? min(max(__ldg(p.own_len + b), 0), p.own_max) : 0;
-}
-
 __device__ __forceinline__ Unit unit_of(const PrefixParams& p) {
   const Plan& pl = p.plan;
   Unit u;
   int64_t i = blockIdx.x;
   const int64_t shared = static_cast<int64_t>(pl.pairs) * pl.n_groups * pl.splits;
-  u.own = i >= shared;
-  if (u.own) i -= shared;
-  const int per = u.own ? pl.own_pairs : pl.pairs;
+  const bool own = i >= shared;
+  if (own) i -= shared;
+  const int per = own ? pl.own_pairs : pl.pairs;
   const int pair = static_cast<int>(i % per);
   i /= per;
   u.group = static_cast<int>(i % pl.n_groups);
   const int split = static_cast<int>(i / pl.n_groups);
-  u.part = u.own ? pl.splits + split : split;
-  const int count = u.own ? p.batch : pl.row_tiles;
-  u.tile[0] = 2 * pair;
-  u.alternate = 2 * pair + 1 >= count;
-  u.tile[1] = u.alternate ? u.tile[0] : 2 * pair + 1;
-  u.np = u.own ? 0 : (p.prefix_len + kTile - 1) / kTile;
+  u.part = own ? pl.splits + split : split;
+  u.alternate = 2 * pair + 1 >= (own ? p.batch * pl.tiles_seq : pl.row_tiles);
+  u.np = own ? 0 : (p.prefix_len + kTile - 1) / kTile;
+  const bool inside = own || pl.fused;  // tiles inside sequences
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const bool has = u.own || pl.tb == 1;
-    u.c[s] = has ? own_keys(p, u.own ? u.tile[s] : sequence_of(p, u.tile[s])) : 0;
+    const int tile = 2 * pair + (u.alternate ? 0 : s);
+    int64_t end;
+    if (inside) {
+      u.seq[s] = tile / pl.tiles_seq;
+      const int64_t first = static_cast<int64_t>(u.seq[s]) * pl.seq_rows;
+      u.row0[s] = first + static_cast<int64_t>(tile - u.seq[s] * pl.tiles_seq) * kTile;
+      end = first + pl.seq_rows;
+    } else {
+      u.seq[s] = 0;
+      u.row0[s] = static_cast<int64_t>(tile) * kTile;
+      end = static_cast<int64_t>(p.batch) * pl.seq_rows;
+    }
+    u.rows[s] = static_cast<int>(min(static_cast<int64_t>(kTile), end - u.row0[s]));
+    u.c[s] = inside && p.own_max > 0 ? min(max(__ldg(p.own_len + u.seq[s]), 0), p.own_max) : 0;
     u.nc[s] = (u.c[s] + kTile - 1) / kTile;
   }
   const int64_t total = static_cast<int64_t>(u.np) + u.nc[0] + (u.alternate ? 0 : u.nc[1]);
-  const int n = u.own ? pl.own_splits : pl.splits;
+  const int n = own ? pl.own_splits : pl.splits;
   u.m0 = static_cast<int>(total * split / n);
   u.m1 = static_cast<int>(total * (split + 1) / n);
   return u;
 }
 
-// Row `r` of a slot's tile: its sequence, token and head; false if none.
-__device__ __forceinline__ bool row_of(const PrefixParams& p, const Unit& u, int s, int r, int& b,
-                                       int& i, int& h) {
-  const Plan& pl = p.plan;
-  const int t = r / pl.gs;
-  h = u.group * pl.gs + (r - t * pl.gs);
-  if (u.own) {
-    b = u.tile[s];
-    i = t;
-    return t < p.queries;
-  }
-  if (pl.tb == 1) {
-    b = u.tile[s] / pl.tiles_seq;
-    i = (u.tile[s] - b * pl.tiles_seq) * pl.tn + t;
-    return t < pl.tn && i < p.queries;
-  }
-  b = u.tile[s] * pl.tb + t / pl.tn;
-  i = t % pl.tn;
-  return t < pl.tn * pl.tb && b < p.batch;
-}
-
-__device__ __forceinline__ int rows_of(const PrefixParams& p, const Unit& u) {
-  return p.plan.gs * (u.own ? p.queries : p.plan.tn * p.plan.tb);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qo,
-                  const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                   const __grid_constant__ CUtensorMap tm_ko, const __grid_constant__ CUtensorMap tm_vo,
                   const PrefixParams p) {
   using Lay = PrefixLayout<D>;
@@ -228,13 +209,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const Unit u = unit_of(p);
-  const int tile_rows = rows_of(p, u);
 
   if (threadIdx.x == 0) {
-    const int softmax_warps = (tile_rows + 31) / 32;
-    for (int i = 0; i < Lay::kBars; ++i)
-      mbar_init(&bars[i],
-                (i >= Lay::bPFull && i < Lay::bPFull + 2) || i == Lay::bMerge ? softmax_warps : 1);
+    for (int i = 0; i < Lay::kBars; ++i) mbar_init(&bars[i], 1);
+    // arrivals of a slot's warps: all four load Q, those with rows make P
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[Lay::bQFull + s], 4);
+      mbar_init(&bars[Lay::bPFull + s], (u.rows[s] + 31) / 32);
+    }
+    mbar_init(&bars[Lay::bMerge], (u.rows[1] + 31) / 32);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -252,16 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_dec<kRegsLow>();
     if (warp == 0 && lane == 0 && u.m0 < u.m1) {
       // ===================== TMA producer
-      for (int s = 0; s < (u.alternate ? 1 : 2); ++s) {
-        const CUtensorMap* tq = u.own ? &tm_qo : &tm_q;
-        const int b = u.own ? u.tile[s] : sequence_of(p, u.tile[s]);
-        const int i = u.own || p.plan.tb > 1 ? 0 : (u.tile[s] - b * p.plan.tiles_seq) * p.plan.tn;
-        mbar_arrive_expect_tx(&bars[Lay::bQFull + s], tile_rows * D * 2);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(smem + Lay::kQ + s * Lay::kTileBytes + c * Lay::kBoxBytes, tq,
-                      &bars[Lay::bQFull + s], c * 64, u.group * p.plan.gs, i, b);
-      }
       int nk = 0, nv = 0;  // K / V tiles whose loads were issued
       bool ok = true;
       auto load = [&](int buf, int full, const CUtensorMap* map, int st, int tile, int z) {
@@ -276,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool prefix, in0, in1;
         int tile;
         u.at(m, prefix, tile, in0, in1);
-        const int z = prefix ? 0
-                             : (u.own ? u.tile[in0 ? 0 : 1] : sequence_of(p, u.tile[in0 ? 0 : 1]));
+        const int z = prefix ? 0 : in0 ? u.seq[0] : u.seq[1];
         if (use > 0)
           ok = mbar_wait(&bars[Lay::bKEmpty + st], (use - 1) & 1, p.status, abort_flag);
         if (!ok) break;
@@ -291,8 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         // drain: wait (ignoring the abort flag) for the loads already issued
-        for (int s = 0; s < (u.alternate ? 1 : 2); ++s)
-          mbar_wait(&bars[Lay::bQFull + s], 0, nullptr, nullptr, 200000000ull);
         for (int j = max(0, nk - kStages); j < nk; ++j)
           mbar_wait(&bars[Lay::bKFull + j % kStages], (j / kStages) & 1, nullptr, nullptr,
                     200000000ull);
@@ -405,12 +375,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t colS = s * 128;
     const uint32_t colO = Lay::kColO + s * D;
-    if ((warp & 3) * 32 < tile_rows) {  // a warp with rows
-      int b, i, h;
-      const bool row_valid = row_of(p, u, s, row, b, i, h);
+    const int rows = s ? u.rows[1] : u.rows[0];
+    const int c_own = s ? u.c[1] : u.c[0];
+    // this thread's row: (sequence b, token i, head h)
+    const bool row_valid = row < rows;
+    const int64_t flat = (s ? u.row0[1] : u.row0[0]) + (row_valid ? row : 0);
+    const int64_t token = flat / p.plan.gs;
+    const int b = static_cast<int>(token / p.queries);
+    const int i = static_cast<int>(token - static_cast<int64_t>(b) * p.queries);
+    const int h = u.group * p.plan.gs + static_cast<int>(flat - token * p.plan.gs);
+    if (s == 0 || !u.alternate) {
+      // Q row into the 128-byte-swizzled tile, zeros below the last row
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.q_bat + i * p.q_tok +
+                                                        static_cast<int64_t>(h) * D);
+      uint8_t* dst = smem + Lay::kQ + s * Lay::kTileBytes;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const uint4 v = row_valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + (k >> 3) * Lay::kBoxBytes + sw128_offset(row, k & 7)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Lay::bQFull + s]);
+    }
+    if ((warp & 3) * 32 < rows) {  // a warp with rows
       const float sl2 = p.scale_log2;
       // own keys this row reads: positions [0, own_hi)
-      const int own_hi = p.causal ? min(u.c[s], u.c[s] - p.queries + i + 1) : u.c[s];
+      const int own_hi = p.causal ? min(c_own, c_own - p.queries + i + 1) : c_own;
       float m_ref = -INFINITY;
       float l = 0.f;
       int n_tiles = 0;  // of this slot, so far
@@ -433,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this row reads columns [0, hi) of the tile
         const int64_t left = static_cast<int64_t>(prefix ? p.prefix_len : own_hi) -
                              static_cast<int64_t>(tile) * kTile;
-        const int hi = row_valid ? static_cast<int>(min(left, static_cast<int64_t>(kTile))) : 0;
+        const int hi = static_cast<int>(min(left, static_cast<int64_t>(kTile)));
         // bit q: no row of this warp reads 32-column chunk q (warp-uniform)
         uint32_t dead = 0;
         if (__any_sync(0xffffffffu, hi < kTile)) {
@@ -508,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float rs0, rs1;
         f2_unpack(rs2, rs0, rs1);
         l += rs0 + rs1;
-        const int v_rows = u.c[s] - tile * kTile;  // V rows of this own tile that exist
+        const int v_rows = c_own - tile * kTile;  // V rows of this own tile that exist
         if (!prefix && v_rows < kTile) {
           // the rest may hold NaN, and P = 0 would not keep it out: clear it
           const int j = m - u.m0, st = j % kStages;
@@ -516,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const int warps = (tile_rows + 31) / 32;
+          const int warps = (rows + 31) / 32;
           uint8_t* v = smem + Lay::kV + st * Lay::kTileBytes;
           const uint4 zero = make_uint4(0, 0, 0, 0);
           // 16-byte chunks [v_rows x 8, 128 x 8) of each 64-feature box
@@ -568,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         w1 *= inv_l;
         const float lse = (l > 0.f) ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
         const bool direct = p.plan.parts == 1;
-        const int64_t r = (static_cast<int64_t>(b) * p.queries + i) * p.Hq + h;
-        const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
+        const int64_t r = token * p.Hq + h;
+        const int64_t all = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
         if (direct || __any_sync(0xffffffffu, l > 0.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -600,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(dst + k) = v;
               }
             } else if (row_valid) {
-              float* dst = p.part_o + (u.part * rows + r) * D + c * 32;
+              float* dst = p.part_o + (u.part * all + r) * D + c * 32;
 #pragma unroll
               for (int k = 0; k < 32; k += 4)
                 *reinterpret_cast<float4*>(dst + k) =
@@ -612,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (direct)
             p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + i] = lse;
           else
-            p.part_lse[u.part * rows + r] = lse;
+            p.part_lse[u.part * all + r] = lse;
         }
       }
     }
@@ -678,22 +669,17 @@ Plan make_plan(const csbp_prefix_problem& p, int sms) {
   pl.gs = G;
   while (pl.gs > kTile || G % pl.gs != 0) --pl.gs;  // the largest divisor up to 128
   pl.n_groups = p.Hq / pl.gs;
-  const int fit = kTile / pl.gs;  // tokens that fit a row tile
+  pl.seq_rows = p.queries * pl.gs;
+  pl.tiles_seq = static_cast<int32_t>((static_cast<int64_t>(pl.seq_rows) + kTile - 1) / kTile);
+  const int64_t packed = (static_cast<int64_t>(p.batch) * pl.seq_rows + kTile - 1) / kTile;
+  const int64_t inside = static_cast<int64_t>(p.batch) * pl.tiles_seq;
   const int np = (p.prefix_len + kTile - 1) / kTile;
-  pl.tb = p.prefix_len == 0 ? 1 : std::max(1, std::min(p.batch, fit / p.queries));
-  if (pl.tb == 1) {
-    pl.tiles_seq = (p.queries + fit - 1) / fit;
-    pl.tn = (p.queries + pl.tiles_seq - 1) / pl.tiles_seq;
-    pl.row_tiles = p.batch * pl.tiles_seq;
-  } else {
-    pl.tiles_seq = 1;
-    pl.tn = p.queries;
-    pl.row_tiles = (p.batch + pl.tb - 1) / pl.tb;
-  }
-  pl.pairs = (pl.row_tiles + 1) / 2;
   const int own_tiles = (p.own_max + kTile - 1) / kTile;
-  const bool own_units = pl.tb > 1 && p.own_max > 0;
-  pl.own_pairs = own_units ? (p.batch + 1) / 2 : 0;
+  pl.fused = p.prefix_len == 0 || (p.own_max > 0 && inside * 7 <= packed * 8) ? 1 : 0;
+  pl.row_tiles = static_cast<int32_t>(pl.fused ? inside : packed);
+  pl.pairs = (pl.row_tiles + 1) / 2;
+  const bool own_units = !pl.fused && p.own_max > 0;
+  pl.own_pairs = own_units ? static_cast<int32_t>((inside + 1) / 2) : 0;
   // Key ranges.  Costs in key-tile times of one CTA: a CTA costs its tiles
   // and about kOver more to start and store, and the partials of each range
   // are written and read once at the rate at which K/V stream in.
@@ -714,7 +700,7 @@ Plan make_plan(const csbp_prefix_problem& p, int sms) {
     }
     return pick;
   };
-  const int fused_tiles = np + (pl.tb == 1 ? own_tiles * 2 : 0);
+  const int fused_tiles = np + (pl.fused ? own_tiles * 2 : 0);
   pl.splits = best(static_cast<int64_t>(pl.pairs) * pl.n_groups, fused_tiles, !own_units);
   pl.own_splits =
       own_units ? best(static_cast<int64_t>(pl.own_pairs) * pl.n_groups, 2 * own_tiles, false) : 0;
@@ -768,7 +754,7 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, unsigned grid
   if (launch_regs[dev] * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
   const int timed = timer_begin(13, stream);
   prefix_kernel<D><<<grid, kThreads, Lay::kDynSmem, stream>>>(maps[0], maps[1], maps[2], maps[3],
-                                                              maps[4], maps[5], p);
+                                                              p);
   e = cudaGetLastError();
   timer_end(timed, stream);
   if (e != cudaSuccess || p.plan.parts == 1) return e;
@@ -801,6 +787,8 @@ csbp_status validate(const csbp_prefix_problem* p) {
   if (p->Hq > lim || rows > lim / p->Hq || p->prefix_len > lim / p->Hkv ||
       static_cast<int64_t>(p->batch) * p->own_max > lim / p->Hkv)
     return CSBP_ERR_UNSUPPORTED;
+  // row and tile counts of a head group fit 32 bits
+  if (rows * (p->Hq / p->Hkv) > 0x3fffffff) return CSBP_ERR_UNSUPPORTED;
   return CSBP_OK;
 }
 
@@ -841,19 +829,7 @@ bool kv_map(CUtensorMap* m, const Tensors& t, int i, const csbp_prefix_problem& 
   const uint64_t strides[2] = {static_cast<uint64_t>(t.tok[i]) * 2,
                                static_cast<uint64_t>(t.bat[i]) * 2};
   const uint32_t box[3] = {64, kTile, 1};
-  return encode_map_bf16(m, 3, t.t[i], dims, strides, box);
-}
-
-// q [batch][queries][Hq][d] as {d, Hq, queries, batch}: boxes of 64 features x
-// gs heads x tn tokens x tb sequences are one row tile.
-bool q_map(CUtensorMap* m, const Tensors& t, const csbp_prefix_problem& p, int gs, int tn, int tb) {
-  const uint64_t dims[4] = {static_cast<uint64_t>(p.d), static_cast<uint64_t>(p.Hq),
-                            static_cast<uint64_t>(p.queries), static_cast<uint64_t>(p.batch)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(p.d) * 2, static_cast<uint64_t>(t.tok[0]) * 2,
-                               static_cast<uint64_t>(t.bat[0]) * 2};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(gs), static_cast<uint32_t>(tn),
-                           static_cast<uint32_t>(tb)};
-  return encode_map_bf16(m, 4, t.t[0], dims, strides, box);
+  return encode_map_3d(m, t.t[i], dims, strides, box);
 }
 
 }  // namespace
@@ -889,20 +865,16 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
   if (grid > 0x7fffffff || rows / 8 >= 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
 
-  CUtensorMap maps[6];  // q, q by sequence, prefix K and V, own K and V
-  if (!q_map(&maps[0], t, p, pl.gs, pl.tn, pl.tb) ||
-      (pl.own_pairs > 0 && !q_map(&maps[1], t, p, pl.gs, p.queries, 1)))
+  CUtensorMap maps[4] = {};  // prefix K and V, own K and V
+  if (p.prefix_len > 0 && (!kv_map(&maps[0], t, 1, p, p.prefix_len, 1) ||
+                           !kv_map(&maps[1], t, 2, p, p.prefix_len, 1)))
     return CSBP_ERR_CUDA;
-  if (p.prefix_len > 0 && (!kv_map(&maps[2], t, 1, p, p.prefix_len, 1) ||
-                           !kv_map(&maps[3], t, 2, p, p.prefix_len, 1)))
+  if (p.own_max > 0 && (!kv_map(&maps[2], t, 3, p, p.own_max, p.batch) ||
+                        !kv_map(&maps[3], t, 4, p, p.own_max, p.batch)))
     return CSBP_ERR_CUDA;
-  if (p.own_max > 0 && (!kv_map(&maps[4], t, 3, p, p.own_max, p.batch) ||
-                        !kv_map(&maps[5], t, 4, p, p.own_max, p.batch)))
-    return CSBP_ERR_CUDA;
-  // maps of absent tensors are never used: any valid one in their place
-  if (pl.own_pairs == 0) maps[1] = maps[0];
-  if (p.prefix_len == 0) maps[2] = maps[3] = maps[0];
-  if (p.own_max == 0) maps[4] = maps[5] = maps[0];
+  // the maps of absent tensors are never used
+  if (p.prefix_len == 0 && p.own_max > 0) maps[0] = maps[1] = maps[2];
+  if (p.own_max == 0 && p.prefix_len > 0) maps[2] = maps[3] = maps[0];
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PrefixParams a{};
@@ -915,6 +887,9 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.G = p.Hq / p.Hkv;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.q = static_cast<const __nv_bfloat16*>(t.t[0]);
+  a.q_tok = t.tok[0];
+  a.q_bat = t.bat[0];
   a.own_len = in->own_len;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;

@@ -249,21 +249,15 @@ bool encode_map_2d(void* map, bool f32, const void* base, uint64_t inner, uint64
   return r == CUDA_SUCCESS;
 }
 
-bool encode_map_bf16(void* map, int rank, const void* base, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box) {
+bool encode_map_3d(void* map, const void* base, const uint64_t dims[3], const uint64_t strides[2],
+                   const uint32_t box[3]) {
   auto enc = encode_fn();
-  if (!enc || rank < 2 || rank > 4) return false;
-  cuuint64_t dm[4], st[3];
-  cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    dm[i] = dims[i];
-    bx[i] = box[i];
-    if (i + 1 < rank) st[i] = strides[i];
-  }
-  return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-             static_cast<cuuint32_t>(rank), const_cast<void*>(base), dm, st, bx, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  if (!enc) return false;
+  const cuuint64_t dm[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
+  const cuuint32_t bx[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
+  return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dm, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

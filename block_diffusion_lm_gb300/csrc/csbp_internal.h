@@ -50,11 +50,10 @@ void timer_end(int i, void* stream);
 // if `swizzle128`; out-of-range elements read as zero.
 bool encode_map_2d(void* map, bool f32, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
-// The same for a bf16 tensor of `rank` 2 .. 4 dimensions (innermost first):
-// strides[i] is the byte stride of dimension i + 1; box[0] = 64 elements, 128-
-// byte swizzle.
-bool encode_map_bf16(void* map, int rank, const void* base, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box);
+// The same for a 3-D bf16 tensor (innermost dimension first): strides[i] is the
+// byte stride of dimension i + 1; box[0] = 64 elements, 128-byte swizzle.
+bool encode_map_3d(void* map, const void* base, const uint64_t dims[3], const uint64_t strides[2],
+                   const uint32_t box[3]);
 int classify_tile(int q_stream, int64_t qt, int k_stream, int64_t kt, int64_t L, int64_t M,
                   int64_t T);
 
