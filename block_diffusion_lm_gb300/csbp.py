@@ -620,7 +620,7 @@ class _Call:
         return t.data_ptr(), tok, bat
 
     def device(self):
-        """The CUDA device of all tensors."""
+        """The index of the CUDA device that all tensors are on."""
         dev = None
         for name, t in self.seen:
             if not t.is_cuda:
@@ -629,22 +629,46 @@ class _Call:
                 dev = t.device
             elif t.device != dev:
                 raise ValueError(f"{self.fn}: {name} is on {t.device}, other tensors on {dev}")
-        return dev
+        return dev.index
 
-    def run(self, stream, *args):
-        """Call the library on `stream` (default: the device's current one)."""
-        import torch
-        dev = self.device()
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"{self.fn}: the stream is on {stream.device}, the tensors on {dev}")
-        f = getattr(lib(), self.fn)
-        if torch.cuda.current_device() == dev.index:
-            _check(self.fn, f(*args, stream.cuda_stream))
-        else:
-            with torch.cuda.device(dev):
-                _check(self.fn, f(*args, stream.cuda_stream))
+
+# Layouts that passed the checks, by function, problem and the (shape, strides,
+# dtype, device) of every tensor: a decoding loop calls with the same few, and
+# the checks in Python cost more than the launch.  Addresses are not part of it.
+_LAYOUTS = {}
+
+
+def _layout(fn, problem, tensors, check):
+    """What `check()` returned for this layout, now or before."""
+    key = (fn, problem, *[None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+                          for t in tensors])
+    made = _LAYOUTS.get(key)
+    if made is None:
+        made = check()
+        if len(_LAYOUTS) >= 1024:
+            _LAYOUTS.clear()
+        _LAYOUTS[key] = made
+    return made
+
+
+def _run(fn, dev, stream, *args):
+    """Call the library on `stream` (default: device `dev`'s current one) with
+    that device current."""
+    import torch
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    else:
+        raw = stream.cuda_stream
+    f = getattr(_lib, fn)
+    if torch._C._cuda_getDevice() == dev:
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    if st != OK:
+        raise CsbpError(fn, st)
 
 
 class QuantCache:
@@ -674,52 +698,61 @@ class QuantCache:
                 for (n, t), s in zip(self._tensors, (code, code, scale, scale))]
         self.Hkv, self.d = Hkv, d
         self.struct = KvCache(pages, page_size, Hkv, d, *ptrs)
+        self._ref = ctypes.byref(self.struct)
+        self._key = (Hkv, d, str(self.k.device))
 
-    def _rows(self, c, k, v, table, start, count):
+    def _check(self, fn, k, v, table, start, count):
+        """(CacheRows without pointers, rows, device index)."""
         import torch
+        c = _Call(fn)
         if k is None or k.dim() != 4:
-            raise ValueError(f"{c.fn}: k must be a [batch][rows][Hkv][d] tensor")
+            raise ValueError(f"{fn}: k must be a [batch][rows][Hkv][d] tensor")
         batch, rows = k.shape[:2]
         shape = (batch, rows, self.Hkv, self.d)
-        kp, kt, kb = c.strided("k", k, shape)
-        vp, vt, vb = c.strided("v", v, shape)
+        _, kt, kb = c.strided("k", k, shape)
+        _, vt, vb = c.strided("v", v, shape)
         if table is None or table.dim() != 2:
-            raise ValueError(f"{c.fn}: table must be a [batch][pages] tensor")
-        r = CacheRows(batch, rows, table.shape[1],
-                      c.tensor("table", table, torch.int32, (batch, table.shape[1])),
-                      c.tensor("start", start, torch.int32, (batch,)),
-                      None if count is None else c.tensor("count", count, torch.int32, (batch,)),
-                      (kt, vt), (kb, vb))
+            raise ValueError(f"{fn}: table must be a [batch][pages] tensor")
+        c.tensor("table", table, torch.int32, (batch, table.shape[1]))
+        c.tensor("start", start, torch.int32, (batch,))
+        if count is not None:
+            c.tensor("count", count, torch.int32, (batch,))
         c.seen += self._tensors
-        return r, kp, vp, batch * rows
+        if batch * rows == 0:
+            return None, 0
+        r = CacheRows(batch, rows, table.shape[1], None, None, None, (kt, vt), (kb, vb))
+        return r, c.device()
+
+    def _call(self, fn, k, v, table, start, count, stream):
+        lib()
+        r, dev = _layout(fn, self._key, (k, v, table, start, count),
+                         lambda: self._check(fn, k, v, table, start, count))
+        if r is None:
+            return
+        r = CacheRows.from_buffer_copy(r)
+        r.table = table.data_ptr()
+        r.start = start.data_ptr()
+        if count is not None:
+            r.count = count.data_ptr()
+        _run(fn, dev, stream, self._ref, ctypes.byref(r), k.data_ptr(), v.data_ptr())
 
     def write(self, k, v, table, start, count=None, stream=None):
         """Quantise bf16 k, v [batch][rows][Hkv][d] (token and batch strides
         free) into the pages; rows i >= count[b] are not written."""
-        c = _Call("csbp_cache_write")
-        r, kp, vp, n = self._rows(c, k, v, table, start, count)
-        if n:
-            c.run(stream, ctypes.byref(self.struct), ctypes.byref(r), kp, vp)
+        self._call("csbp_cache_write", k, v, table, start, count, stream)
 
     def read(self, table, start, count=None, rows=None, out=None, stream=None):
         """bf16 (k, v) [batch][rows][Hkv][d] of positions start[b] .. ; `out`
         receives them (rows i >= count[b] keep what they hold), else two
         tensors of `rows` rows are allocated (zero beyond count)."""
         import torch
-        c = _Call("csbp_cache_read")
         if out is None:
             if rows is None or table is None:
                 raise ValueError("csbp_cache_read: needs `rows` or `out`")
             shape = (table.shape[0], rows, self.Hkv, self.d)
             out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=self.k.device)
                         for _ in range(2))
-        r, kp, vp, n = self._rows(c, out[0], out[1], table, start, count)
-        if n:
-            # an expanded output would take several rows at one place
-            for name, t in (("k", out[0]), ("v", out[1])):
-                if any(s == 0 and e > 1 for s, e in zip(t.stride(), t.shape)):
-                    raise ValueError(f"csbp_cache_read: {name} has a broadcast dimension")
-            c.run(stream, ctypes.byref(self.struct), ctypes.byref(r), kp, vp)
+        self._call("csbp_cache_read", out[0], out[1], table, start, count, stream)
         return out
 
 
@@ -777,25 +810,46 @@ def prefix_workspace_bytes(problem: PrefixProblem) -> int:
 def attn_prefix(problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, workspace,
                 stream=None):
     import torch
-    c = _Call("csbp_attn_prefix")
     p = problem
-    pre = (p.prefix_len, p.Hkv, p.d)
-    mine = (p.batch, p.own_max, p.Hkv, p.d)
-    none = (None, 0, 0)
-    s = [c.strided("q", q, (p.batch, p.queries, p.Hq, p.d)),
-         c.strided("k_prefix", k_prefix, pre) if p.prefix_len else none,
-         c.strided("v_prefix", v_prefix, pre) if p.prefix_len else none,
-         c.strided("k_own", k_own, mine) if p.own_max else none,
-         c.strided("v_own", v_own, mine) if p.own_max else none]
-    lens = c.tensor("own_len", own_len, torch.int32, (p.batch,)) if p.own_max else None
-    inp = PrefixInputs(*(x[0] for x in s), lens, tuple(x[1] for x in s), tuple(x[2] for x in s))
-    po = c.tensor("o", o, torch.bfloat16, (p.batch, p.queries, p.Hq, p.d))
-    pl = c.tensor("lse", lse, torch.float32, (p.batch, p.Hq, p.queries))
-    if workspace is None:
-        raise ValueError("csbp_attn_prefix: workspace is required")
-    n = workspace.numel()
-    pw = c.tensor("workspace", workspace, torch.uint8, (n,))
-    c.run(stream, ctypes.byref(problem), ctypes.byref(inp), po, pl, pw, n)
+    if not p.prefix_len:
+        k_prefix = v_prefix = None
+    if not p.own_max:
+        k_own = v_own = own_len = None
+
+    def check():
+        c = _Call("csbp_attn_prefix")
+        pre = (p.prefix_len, p.Hkv, p.d)
+        mine = (p.batch, p.own_max, p.Hkv, p.d)
+        none = (None, 0, 0)
+        s = [c.strided("q", q, (p.batch, p.queries, p.Hq, p.d)),
+             c.strided("k_prefix", k_prefix, pre) if p.prefix_len else none,
+             c.strided("v_prefix", v_prefix, pre) if p.prefix_len else none,
+             c.strided("k_own", k_own, mine) if p.own_max else none,
+             c.strided("v_own", v_own, mine) if p.own_max else none]
+        if p.own_max:
+            c.tensor("own_len", own_len, torch.int32, (p.batch,))
+        c.tensor("o", o, torch.bfloat16, (p.batch, p.queries, p.Hq, p.d))
+        c.tensor("lse", lse, torch.float32, (p.batch, p.Hq, p.queries))
+        if workspace is None:
+            raise ValueError("csbp_attn_prefix: workspace is required")
+        c.tensor("workspace", workspace, torch.uint8, (workspace.numel(),))
+        return (PrefixInputs(None, None, None, None, None, None, tuple(x[1] for x in s),
+                             tuple(x[2] for x in s)), c.device())
+
+    lib()
+    inp, dev = _layout("csbp_attn_prefix", bytes(p),
+                       (q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, workspace), check)
+    inp = PrefixInputs.from_buffer_copy(inp)
+    inp.q = q.data_ptr()
+    if k_prefix is not None:
+        inp.k_prefix = k_prefix.data_ptr()
+        inp.v_prefix = v_prefix.data_ptr()
+    if k_own is not None:
+        inp.k_own = k_own.data_ptr()
+        inp.v_own = v_own.data_ptr()
+        inp.own_len = own_len.data_ptr()
+    _run("csbp_attn_prefix", dev, stream, ctypes.byref(p), ctypes.byref(inp), o.data_ptr(),
+         lse.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
@@ -806,42 +860,57 @@ def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
     drafts, the next token, then -1); `out` receives them if given.  q, token
     and u may be None when p has one row per sequence (plain sampling)."""
     import torch
-    c = _Call("csbp_draft_verify")
     if p is None or p.dim() != 3 or p.shape[1] < 1:
         raise ValueError("csbp_draft_verify: p must be a [batch][drafts + 1][vocab] tensor")
     batch, K, V = p.shape[0], p.shape[1] - 1, p.shape[2]
-
-    def rows(name, t, n):
-        c.shaped(name, t, torch.float32, (batch, n, V))
-        if t.numel() == 0:
-            return t.data_ptr(), 0, 0
-        st = t.stride()
-        if V > 1 and st[2] != 1:
-            raise ValueError(f"csbp_draft_verify: {name} must have contiguous rows")
-        row = st[1] if n > 1 else V
-        if row < V:
-            raise ValueError(f"csbp_draft_verify: {name} rows must not overlap (stride {row})")
-        if batch > 1 and st[0] < n * row:
-            raise ValueError(f"csbp_draft_verify: {name} batch entries must not interleave "
-                             f"(stride {st[0]})")
-        return t.data_ptr(), row, st[0] if batch > 1 else 0
-
-    pp, p_row, p_batch = rows("p", p, K + 1)
-    qp, q_row, q_batch, tp, up = None, 0, 0, None, None
-    if K > 0:
-        qp, q_row, q_batch = rows("q", q, K)
-        tp = c.tensor("token", token, torch.int32, (batch, K))
-        up = c.tensor("u", u, torch.float32, (batch, K))
-    rp = c.tensor("r", r, torch.float32, (batch,))
-    lp = None if length is None else c.tensor("length", length, torch.int32, (batch,))
+    if K == 0:
+        q = token = u = None
     if out is None:
         accepted = torch.empty((batch,), dtype=torch.int32, device=p.device)
         tokens = torch.empty((batch, K + 1), dtype=torch.int32, device=p.device)
     else:
         accepted, tokens = out
-    ap = c.tensor("accepted", accepted, torch.int32, (batch,))
-    op = c.tensor("tokens", tokens, torch.int32, (batch, K + 1))
-    if batch:
-        prob = VerifyProblem(batch, K, V, p_row, p_batch, q_row, q_batch)
-        c.run(stream, ctypes.byref(prob), pp, qp, tp, up, rp, lp, ap, op)
+
+    def check():
+        c = _Call("csbp_draft_verify")
+
+        def rows(name, t, n):
+            """Row and batch stride of fp32 [batch][n][vocab]."""
+            c.shaped(name, t, torch.float32, (batch, n, V))
+            if t.numel() == 0:
+                return 0, 0
+            st = t.stride()
+            if V > 1 and st[2] != 1:
+                raise ValueError(f"csbp_draft_verify: {name} must have contiguous rows")
+            row = st[1] if n > 1 else V
+            if row < V:
+                raise ValueError(f"csbp_draft_verify: {name} rows must not overlap (stride {row})")
+            if batch > 1 and st[0] < n * row:
+                raise ValueError(f"csbp_draft_verify: {name} batch entries must not interleave "
+                                 f"(stride {st[0]})")
+            return row, st[0] if batch > 1 else 0
+
+        strides = rows("p", p, K + 1)
+        if K:
+            strides += rows("q", q, K)
+            c.tensor("token", token, torch.int32, (batch, K))
+            c.tensor("u", u, torch.float32, (batch, K))
+        else:
+            strides += (0, 0)
+        c.tensor("r", r, torch.float32, (batch,))
+        if length is not None:
+            c.tensor("length", length, torch.int32, (batch,))
+        c.tensor("accepted", accepted, torch.int32, (batch,))
+        c.tensor("tokens", tokens, torch.int32, (batch, K + 1))
+        return (VerifyProblem(batch, K, V, *strides), c.device()) if batch else (None, 0)
+
+    lib()
+    prob, dev = _layout("csbp_draft_verify", None, (p, q, token, u, r, length, accepted, tokens),
+                        check)
+    if prob is not None:
+        _run("csbp_draft_verify", dev, stream, ctypes.byref(prob), p.data_ptr(),
+             q.data_ptr() if K else None, token.data_ptr() if K else None,
+             u.data_ptr() if K else None, r.data_ptr(),
+             None if length is None else length.data_ptr(), accepted.data_ptr(),
+             tokens.data_ptr())
     return accepted, tokens

@@ -209,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const Unit u = unit_of(p);
+  // the kernel that joins the parts may take its place on the GPU; it waits
+  // for this one's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lay::kBars; ++i) mbar_init(&bars[i], 1);
@@ -615,36 +618,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the key ranges' partials: one warp per (query, head) row.  Lanes hold
-// the parts' LSE in turn for the maximum and the weights, then d / 32
-// features each.
-template <int D>
+// Joins the key ranges' partials: `W` warps per (query, head) row, each for
+// every W-th part.  Lanes hold the parts' LSE in turn for the maximum and the
+// weights, then d / 32 features each.  It is launched while the attention
+// kernel still runs and waits for it here, so its own start costs nothing.
+// Few rows have many parts (the GPU was filled by splitting the keys), so a row
+// gets a CTA of its own and its parts are loaded side by side.
+template <int D, int W>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
   constexpr int kN = D / 32;
-  const int lane = threadIdx.x & 31;
+  __shared__ float4 joined[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
-  const int64_t r = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (r >= rows) return;
+  const int64_t r = blockIdx.x * static_cast<int64_t>(8 / W) + warp / W;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (W == 1 && r >= rows) return;
   const int parts = p.plan.parts;
+  const float* z = p.part_lse + r;
   float top = -INFINITY;
-  for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_lse[k * rows + r]);
+  for (int k = lane; k < parts; k += 32) top = fmaxf(top, z[k * rows]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
   float acc[kN] = {};
   float sum = 0.f;
-  for (int k0 = 0; k0 < parts && top != -INFINITY; k0 += 32) {
-    const float z = k0 + lane < parts ? p.part_lse[(k0 + lane) * rows + r] : -INFINITY;
-    const float w = z == -INFINITY ? 0.f : expf(z - top);
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    const float zk = k0 + lane < parts ? z[(k0 + lane) * rows] : -INFINITY;
+    const float w = expf(zk - ref);
+    sum += w;
     const int n = min(32, parts - k0);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      if (wk == 0.f) continue;  // that range holds no key of this row
-      sum += wk;
-      const float* src = p.part_o + ((k0 + k) * rows + r) * D + lane * kN;
+    for (int k1 = warp % W; k1 < n; k1 += 4 * W) {
+      float v[4][kN];
+      float wk[4];
 #pragma unroll
-      for (int c = 0; c < kN; ++c) acc[c] = fmaf(wk, src[c], acc[c]);
+      for (int t = 0; t < 4; ++t) {
+        const int k = k1 + t * W;
+        wk[t] = __shfl_sync(0xffffffffu, w, k & 31);
+        if (k >= n) wk[t] = 0.f;
+        // a range without a key of this row left no partial
+        const float* src = p.part_o + ((k0 + k) * rows + r) * D + lane * kN;
+#pragma unroll
+        for (int c = 0; c < kN; c += 2) {
+          const float2 x = wk[t] > 0.f ? *reinterpret_cast<const float2*>(src + c)
+                                       : make_float2(0.f, 0.f);
+          v[t][c] = x.x;
+          v[t][c + 1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int c = 0; c < kN; ++c) acc[c] = fmaf(wk[t], v[t][c], acc[c]);
     }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (W > 1) {
+    float* mine = reinterpret_cast<float*>(&joined[warp][lane]);
+#pragma unroll
+    for (int c = 0; c < kN; ++c) mine[c] = acc[c];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k)
+#pragma unroll
+      for (int c = 0; c < kN; ++c) acc[c] += reinterpret_cast<const float*>(&joined[k][lane])[c];
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   uint32_t out[kN / 2];
@@ -759,9 +797,19 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, unsigned grid
   timer_end(timed, stream);
   if (e != cudaSuccess || p.plan.parts == 1) return e;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
+  const bool wide = rows <= 4096;  // a CTA per row
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
   const int joined = timer_begin(14, stream);
-  prefix_merge_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = wide ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p)
+           : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p);
   timer_end(joined, stream);
   return e;
 }
