@@ -30,69 +30,118 @@ struct CacheArgs {
   int64_t tok[2], bat[2];
 };
 
-// Token slot (page x page_size + place) of row i of sequence b, -1 if its
-// position or page is out of range.
-__device__ __forceinline__ int64_t slot_of(const CacheArgs& a, int b, int i) {
-  const int64_t pos = static_cast<int64_t>(__ldg(a.start + b)) + i;
+// Row `i` of sequence `b`, and whether it takes part.
+struct Row {
+  int b, i;
+  bool takes_part;
+};
+
+// The rows of a CTA are consecutive; `k` is one of them, the same for the
+// lanes that share it.
+__device__ __forceinline__ Row row_of(const CacheArgs& a, int64_t first, int k) {
+  const int64_t b0 = first / a.rows;  // the same in all threads
+  const uint32_t i = static_cast<uint32_t>(first - b0 * a.rows) + static_cast<uint32_t>(k);
+  const uint32_t more = i / static_cast<uint32_t>(a.rows);
+  Row r;
+  const int64_t b = b0 + more;
+  r.takes_part = b < a.batch;
+  r.b = r.takes_part ? static_cast<int>(b) : 0;
+  r.i = static_cast<int>(i - more * static_cast<uint32_t>(a.rows));
+  if (r.takes_part && a.count) r.takes_part = r.i < __ldg(a.count + r.b);
+  return r;
+}
+
+// Token slot (page x page_size + place) of a row, -1 if its position or page
+// is out of range.
+__device__ __forceinline__ int64_t slot_of(const CacheArgs& a, const Row& r) {
+  const int64_t pos = static_cast<int64_t>(__ldg(a.start + r.b)) + r.i;
   if (pos < 0) return -1;
-  const int64_t entry = pos / a.page_size;
-  if (entry >= a.table_pages) return -1;
-  const int64_t page = __ldg(a.table + static_cast<int64_t>(b) * a.table_pages + entry);
+  const uint32_t at = static_cast<uint32_t>(pos);  // below 2^32
+  const uint32_t entry = at / static_cast<uint32_t>(a.page_size);
+  if (entry >= static_cast<uint32_t>(a.table_pages)) return -1;
+  const int64_t page = __ldg(a.table + static_cast<int64_t>(r.b) * a.table_pages + entry);
   if (page < 0 || page >= a.pages) return -1;
-  return page * a.page_size + (pos - entry * a.page_size);
+  return page * a.page_size + (at - entry * static_cast<uint32_t>(a.page_size));
 }
 
-__device__ __forceinline__ bool takes_part(const CacheArgs& a, int b, int i) {
-  return !a.count || i < __ldg(a.count + b);
+// E4M3 codes of 8 bf16 values (two per word) under the scale byte `byte`.
+__device__ __forceinline__ uint2 encode8(const uint32_t w[4], int byte) {
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);  // 2^-e
+  uint32_t two[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo = __uint_as_float(w[k] << 16) * inv, hi = __uint_as_float(w[k] & 0xffff0000u) * inv;
+    // the conversion would make infinities 448
+    if ((w[k] & 0x7fffu) == 0x7f80u) lo = NAN;
+    if ((w[k] & 0x7fff0000u) == 0x7f800000u) hi = NAN;
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    two[k] = c;
+  }
+  return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
 }
 
-// One thread per 8 consecutive features; 4 lanes hold a group.
-__global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
-  const int chunks = a.row_values >> 3;  // a multiple of 4: groups never cross a warp
-  const int64_t total = static_cast<int64_t>(a.batch) * a.rows * chunks;
-  const int kv = blockIdx.y;
-  for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
-       idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = idx / chunks;
-    const int c = static_cast<int>(idx - row * chunks);
-    const int b = static_cast<int>(row / a.rows);
-    const int i = static_cast<int>(row - static_cast<int64_t>(b) * a.rows);
-    if (!takes_part(a, b, i)) continue;  // the same for the 4 lanes of a group
-    const int64_t slot = slot_of(a, b, i);
-    if (slot < 0) continue;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.src[kv] + b * a.bat[kv] +
-                                                         i * a.tok[kv]) + c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;  // bits of the largest finite magnitude
+// Bits of the largest finite magnitude of 8 bf16 values.
+__device__ __forceinline__ uint32_t top8(const uint32_t w[4]) {
+  uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-      if (lo < 0x7f80u) top = max(top, lo);
-      if (hi < 0x7f80u) top = max(top, hi);
-    }
-    const unsigned mask = 0xfu << (threadIdx.x & 28);
-    top = max(top, __shfl_xor_sync(mask, top, 1));
-    top = max(top, __shfl_xor_sync(mask, top, 2));
-    // 448 = 1.75 x 2^8: e = exponent - 8, one more above 1.75
-    const int byte = max(0, static_cast<int>(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
-    const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);  // 2^-e
-    uint32_t out[2];
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+    if (lo < 0x7f80u) top = max(top, lo);
+    if (hi < 0x7f80u) top = max(top, hi);
+  }
+  return top;
+}
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+// `L` lanes per row (4 .. 32, so that a group of 32 features is 4 lanes of one
+// row), 8 features a lane and step, K and V of a row in turn with all loads of
+// up to kUnroll steps issued before the first is used: 32 lanes x 16 bytes x 8
+// loads in flight per warp.
+template <int L>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
+  constexpr int kRows = kThreads / L;
+  const int lane = threadIdx.x % L;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
+  const Row r = row_of(a, first, threadIdx.x / L);
+  const int chunks = a.row_values >> 3;  // a multiple of 4
+  const int64_t slot = r.takes_part ? slot_of(a, r) : -1;
+  // the lanes of a row decide alike, those of a warp need not: no early return
+  // before the shuffles
+  const bool on = slot >= 0;
+  for (int c0 = 0; c0 < chunks; c0 += L * kUnroll) {
+    uint4 v[2][kUnroll];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
-      lo = (w[k] & 0x7fffu) < 0x7f80u ? lo * inv : NAN;
-      hi = ((w[k] >> 16) & 0x7fffu) < 0x7f80u ? hi * inv : NAN;
-      uint16_t two;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
-      if (k & 1)
-        out[k >> 1] |= static_cast<uint32_t>(two) << 16;
-      else
-        out[k >> 1] = two;
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.src[kv] + r.b * a.bat[kv] +
+                                                        r.i * a.tok[kv]);
+#pragma unroll
+      for (int t = 0; t < kUnroll; ++t) {
+        const int c = c0 + t * L + lane;
+        v[kv][t] = on && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+      }
     }
-    *reinterpret_cast<uint2*>(a.codes[kv] + slot * a.row_values + c * 8) =
-        make_uint2(out[0], out[1]);
-    if ((c & 3) == 0)
-      a.scales[kv][slot * (a.row_values / kGroup) + (c >> 2)] = static_cast<uint8_t>(byte);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint8_t* codes = a.codes[kv] + slot * a.row_values;
+      uint8_t* scales = a.scales[kv] + slot * (a.row_values / kGroup);
+#pragma unroll
+      for (int t = 0; t < kUnroll; ++t) {
+        const int c = c0 + t * L + lane;
+        const uint32_t w[4] = {v[kv][t].x, v[kv][t].y, v[kv][t].z, v[kv][t].w};
+        uint32_t top = top8(w);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 448 = 1.75 x 2^8: e = exponent - 8, one more above 1.75
+        const int byte = max(0, static_cast<int>(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
+        if (on && c < chunks) {
+          *reinterpret_cast<uint2*>(codes + c * 8) = encode8(w, byte);
+          if ((c & 3) == 0) scales[c >> 2] = static_cast<uint8_t>(byte);
+        }
+      }
+    }
   }
 }
 
@@ -112,29 +161,43 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
 }
 
-// One thread per 8 consecutive features.
-__global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
+// The same lanes and steps as the write.
+template <int L>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {
+  constexpr int kRows = kThreads / L;
+  const int lane = threadIdx.x % L;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
+  const Row r = row_of(a, first, threadIdx.x / L);
+  if (!r.takes_part) return;
   const int chunks = a.row_values >> 3;
-  const int64_t total = static_cast<int64_t>(a.batch) * a.rows * chunks;
-  const int kv = blockIdx.y;
-  for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
-       idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = idx / chunks;
-    const int c = static_cast<int>(idx - row * chunks);
-    const int b = static_cast<int>(row / a.rows);
-    const int i = static_cast<int>(row - static_cast<int64_t>(b) * a.rows);
-    if (!takes_part(a, b, i)) continue;
-    const int64_t slot = slot_of(a, b, i);
-    uint4 r = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-    if (slot >= 0) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.codes[kv] + slot * a.row_values) + c);
-      const float s = scale_of(__ldg(a.scales[kv] + slot * (a.row_values / kGroup) + (c >> 2)));
-      r.x = decode2(v.x, s);
-      r.y = decode2(v.x >> 16, s);
-      r.z = decode2(v.y, s);
-      r.w = decode2(v.y >> 16, s);
+  const int64_t slot = slot_of(a, r);
+  for (int c0 = 0; c0 < chunks; c0 += L * kUnroll) {
+    uint2 v[2][kUnroll];
+    uint32_t sb[2][kUnroll];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int t = 0; t < kUnroll; ++t) {
+        const int c = c0 + t * L + lane;
+        v[kv][t] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN
+        sb[kv][t] = 127;
+        if (slot >= 0 && c < chunks) {
+          v[kv][t] = __ldcs(reinterpret_cast<const uint2*>(a.codes[kv] + slot * a.row_values) + c);
+          sb[kv][t] = __ldg(a.scales[kv] + slot * (a.row_values / kGroup) + (c >> 2));
+        }
+      }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint4* dst = reinterpret_cast<uint4*>(a.dst[kv] + r.b * a.bat[kv] + r.i * a.tok[kv]);
+#pragma unroll
+      for (int t = 0; t < kUnroll; ++t) {
+        const int c = c0 + t * L + lane;
+        const float s = scale_of(sb[kv][t]);
+        const uint4 out = make_uint4(decode2(v[kv][t].x, s), decode2(v[kv][t].x >> 16, s),
+                                     decode2(v[kv][t].y, s), decode2(v[kv][t].y >> 16, s));
+        if (c < chunks) dst[c] = out;
+      }
     }
-    reinterpret_cast<uint4*>(a.dst[kv] + b * a.bat[kv] + i * a.tok[kv])[c] = r;
   }
 }
 
@@ -187,15 +250,33 @@ csbp_status make_args(const csbp_kv_cache* c, const csbp_cache_rows* r, const vo
   return CSBP_OK;
 }
 
-csbp_status grid_of(const CacheArgs& a, dim3& grid) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return CSBP_ERR_CUDA;
-  const int64_t total = static_cast<int64_t>(a.batch) * a.rows * (a.row_values >> 3);
-  const int64_t blocks = (total + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
-  grid = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 2);
-  return CSBP_OK;
+// One launch over all rows with the fewest lanes per row that cover it in one
+// step (so that short rows share a warp), at most a warp.
+template <bool kWrite>
+csbp_status launch(const CacheArgs& a, void* stream) {
+  const int chunks = a.row_values >> 3;
+  const int lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+  const int64_t per = kThreads / lanes;
+  const int64_t grid = (static_cast<int64_t>(a.batch) * a.rows + per - 1) / per;
+  if (grid > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned g = static_cast<unsigned>(grid);
+  const int timed = timer_begin(kWrite ? 11 : 12, stream);
+  if (lanes == 4)
+    kWrite ? cache_write_kernel<4><<<g, kThreads, 0, s>>>(a)
+           : cache_read_kernel<4><<<g, kThreads, 0, s>>>(a);
+  else if (lanes == 8)
+    kWrite ? cache_write_kernel<8><<<g, kThreads, 0, s>>>(a)
+           : cache_read_kernel<8><<<g, kThreads, 0, s>>>(a);
+  else if (lanes == 16)
+    kWrite ? cache_write_kernel<16><<<g, kThreads, 0, s>>>(a)
+           : cache_read_kernel<16><<<g, kThreads, 0, s>>>(a);
+  else
+    kWrite ? cache_write_kernel<32><<<g, kThreads, 0, s>>>(a)
+           : cache_read_kernel<32><<<g, kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  timer_end(timed, stream);
+  return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }
 
 }  // namespace
@@ -210,13 +291,7 @@ extern "C" csbp_status csbp_cache_write(const csbp_kv_cache* cache, const csbp_c
   if (st != CSBP_OK || a.batch == 0) return st;
   a.src[0] = static_cast<const __nv_bfloat16*>(k);
   a.src[1] = static_cast<const __nv_bfloat16*>(v);
-  dim3 grid;
-  if ((st = grid_of(a, grid)) != CSBP_OK) return st;
-  const int timed = timer_begin(11, stream);
-  cache_write_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  timer_end(timed, stream);
-  return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
+  return launch<true>(a, stream);
 }
 
 extern "C" csbp_status csbp_cache_read(const csbp_kv_cache* cache, const csbp_cache_rows* rows,
@@ -226,11 +301,5 @@ extern "C" csbp_status csbp_cache_read(const csbp_kv_cache* cache, const csbp_ca
   if (st != CSBP_OK || a.batch == 0) return st;
   a.dst[0] = static_cast<__nv_bfloat16*>(k);
   a.dst[1] = static_cast<__nv_bfloat16*>(v);
-  dim3 grid;
-  if ((st = grid_of(a, grid)) != CSBP_OK) return st;
-  const int timed = timer_begin(12, stream);
-  cache_read_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  timer_end(timed, stream);
-  return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
+  return launch<false>(a, stream);
 }
