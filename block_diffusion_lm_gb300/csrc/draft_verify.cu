@@ -61,14 +61,30 @@ __device__ __forceinline__ void add_weight(Pair& s, float p, float q) {
     add(s, p, 0.f);
 }
 
-// This lane's share of w over [v0, v1), v0 a multiple of 4.  Rows that start on
-// 16 bytes are read four at a time, with 4 loads of each row in flight.
+// a + b of two such sums
+__device__ __forceinline__ Pair join(Pair a, Pair b) {
+  add(a, b.hi, b.lo);
+  return a;
+}
+
+// Sum over the warp, in lane 0 (other lanes have partial sums).
+__device__ __forceinline__ double warp_sum(Pair s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Pair x{__shfl_down_sync(0xffffffffu, s.hi, o), __shfl_down_sync(0xffffffffu, s.lo, o)};
+    s = join(s, x);
+  }
+  return static_cast<double>(s.hi) + static_cast<double>(s.lo);
+}
+
+// This lane's share of w over [v0, v1).  Rows that start on 16 bytes (v0 does
+// too) are read four at a time, with 4 loads of each row in flight.
 template <bool kResidual>
-__device__ __forceinline__ double lane_sum(const float* p, const float* q, int64_t v0, int64_t v1,
-                                           int lane) {
+__device__ __forceinline__ Pair lane_sum(const float* p, const float* q, int64_t v0, int64_t v1,
+                                         int lane) {
   Pair s{0.f, 0.f};
-  const uintptr_t low = reinterpret_cast<uintptr_t>(p) | (kResidual ? reinterpret_cast<uintptr_t>(q)
-                                                                    : 0);
+  const uintptr_t low = reinterpret_cast<uintptr_t>(p + v0) |
+                        (kResidual ? reinterpret_cast<uintptr_t>(q + v0) : 0);
   int64_t v = v0;
   if ((low & 15u) == 0) {
     constexpr int kUnroll = 4;
@@ -92,13 +108,12 @@ __device__ __forceinline__ double lane_sum(const float* p, const float* q, int64
 #pragma unroll 4
   for (v += lane; v < v1; v += 32)
     add_weight<kResidual>(s, __ldg(p + v), kResidual ? __ldg(q + v) : 0.f);
-  return static_cast<double>(s.hi) + static_cast<double>(s.lo);
+  return s;
 }
 
-__device__ __forceinline__ double warp_sum(double t) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
+__device__ __forceinline__ Pair lane_sum(const float* p, const float* q, int64_t v0, int64_t v1,
+                                         int lane) {
+  return q ? lane_sum<true>(p, q, v0, v1, lane) : lane_sum<false>(p, q, v0, v1, lane);
 }
 
 __device__ __forceinline__ double weight(const float* p, const float* q, int64_t v) {
@@ -108,28 +123,33 @@ __device__ __forceinline__ double weight(const float* p, const float* q, int64_t
 
 // Shared memory of a CTA.
 struct Shared {
-  double seg[kWarps];         // sums of the warps' segments, then of their parts
-  double cta[kCluster];       // sums of the cluster's CTAs (each writes all copies)
+  double seg[kWarps];    // sums of the warps' segments, then of their pieces
+  double cta[kCluster];  // sums of the cluster's CTAs (each writes all copies)
+  double target, before;
   int first_bad;
   int found;
 };
 
-// Of n sums that follow a sum of `before`: the first one that carries it past
-// `target`, with `before` moved to its start.  If rounding leaves none, the last
-// with any weight.
-__device__ __forceinline__ int crossing(const double* sums, int n, double target, double& before) {
-  int last = 0;
-  double at = before, last_at = before;
-  for (int k = 0; k < n; ++k) {
-    if (sums[k] > 0.0) {
-      last = k;
-      last_at = at;
-      if (at + sums[k] > target) break;
-    }
-    at += sums[k];
+// x_0 + .. + x_lane
+__device__ __forceinline__ double scan(double x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  before = last_at;
-  return last;
+  return x;
+}
+
+// A warp's lanes hold sums x that follow a sum of `before`: the first lane that
+// carries it past `target`, with `before` moved to its start.  If rounding leaves
+// none, the last with any weight.
+__device__ __forceinline__ int crossing(double x, int lane, double target, double& before) {
+  const double upto = before + scan(x, lane);
+  const unsigned any = __ballot_sync(0xffffffffu, x > 0.0);
+  const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && upto > target);
+  const int k = over ? __ffs(over) - 1 : 31 - __clz(any | 1u);
+  if (k > 0) before = __shfl_sync(0xffffffffu, upto, k - 1);
+  return k;
 }
 
 __device__ __forceinline__ void store_cluster(double* local, uint32_t rank, double x) {
@@ -144,90 +164,90 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
-}
 
-constexpr int kNobody = -3;  // another CTA of the cluster has the answer
-constexpr int kNoWeight = -2;
+constexpr int kNobody = -3;    // another CTA of the cluster has the answer
+constexpr int kNoWeight = -2;  // all weights are 0
+constexpr int kSearch = 0;     // in this CTA's part
 
-// Smallest v with w_0 + .. + w_v > r x total (in one CTA of the cluster, kNobody
-// in the others); -1 when the total is not finite, kNoWeight when it is 0.
-// Every warp sums one contiguous segment of the vocabulary; the CTA whose part
-// holds the answer finds the segment, lets its warps sum pieces of it in 64
-// bits, and scans the piece.
-// On entry the cluster's CTAs have arrived at its barrier (they all run, and
-// have read what an earlier draw left).
 template <int C>
 __device__ int draw(const float* p, const float* q, int V, float r, int rank, Shared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t seg = (static_cast<int64_t>(V) + C * kWarps * 128 - 1) / (C * kWarps * 128) * 128;
   const int64_t start = (static_cast<int64_t>(rank) * kWarps + warp) * seg;
   const int64_t end = min(start + seg, static_cast<int64_t>(V));
-  double t = 0.0;
-  if (start < end)
-    t = q ? lane_sum<true>(p, q, start, end, lane) : lane_sum<false>(p, q, start, end, lane);
-  t = warp_sum(t);
+  Pair mine{0.f, 0.f};
+  if (start < end) mine = lane_sum(p, q, start, end, lane);
+  const double t = warp_sum(mine);
   if (lane == 0) sh.seg[warp] = t;
   __syncthreads();
   if (C > 1) cluster_wait();
+  // 64-bit arithmetic from here, in one warp only
   if (warp == 0) {
-    double mine = 0.0;
-    for (int k = 0; k < kWarps; ++k) mine += sh.seg[k];
+    const double all = scan(lane < kWarps ? sh.seg[lane] : 0.0, lane);
+    const double x = __shfl_sync(0xffffffffu, all, kWarps - 1);
     if (C == 1) {
-      if (lane == 0) sh.cta[0] = mine;
+      if (lane == 0) sh.cta[0] = x;
+      __syncwarp();
     } else if (lane < C) {
-      store_cluster(&sh.cta[rank], lane, mine);
+      store_cluster(&sh.cta[rank], lane, x);
     }
   }
-  if (C > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  double total = 0.0;
-#pragma unroll
-  for (int k = 0; k < C; ++k) total += sh.cta[k];
-  if (!(total > 0.0)) return total == 0.0 ? kNoWeight : -1;
-  if (!(total < 1e300)) return -1;
-  const double target = static_cast<double>(r) * total;
-  double before = 0.0;
-  if (crossing(sh.cta, C, target, before) != rank) return kNobody;
-  const int k = crossing(sh.seg, kWarps, target, before);
-  __syncthreads();  // all have read the segments' sums
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp == 0) {
+    const double x = lane < C ? sh.cta[lane] : 0.0;
+    const double total = __shfl_sync(0xffffffffu, scan(x, lane), 31);
+    const double target = static_cast<double>(r) * total;
+    double before = 0.0;
+    int state = kSearch;
+    if (!(total > 0.0 && total < 1e300))
+      state = total == 0.0 ? kNoWeight : -1;
+    else if (crossing(x, lane, target, before) != rank)
+      state = kNobody;
+    int k = 0;
+    if (state == kSearch)
+      k = crossing(lane < kWarps ? sh.seg[lane] : 0.0, lane, target, before);
+    __syncwarp();
+    if (lane == 0) {
+      sh.target = target;
+      sh.before = before;
+      sh.found = state == kSearch ? k : state;
+    }
+  }
+  __syncthreads();
+  const int k = sh.found;
+  if (k < 0) return k;
   // pieces of segment k, one per warp
   const int64_t s0 = (static_cast<int64_t>(rank) * kWarps + k) * seg;
   const int64_t s1 = min(s0 + seg, static_cast<int64_t>(V));
-  const int64_t piece = (seg + kWarps - 1) / kWarps;  // a multiple of 8
+  const int64_t piece = seg / kWarps;  // a multiple of 8
   {
-    double w = 0.0;
-    const int64_t e = min(s0 + (warp + 1) * piece, s1);
-    for (int64_t v = s0 + warp * piece + lane; v < e; v += 32) w += weight(p, q, v);
-    w = warp_sum(w);
+    const int64_t v0 = s0 + warp * piece, v1 = min(v0 + piece, s1);
+    const double w = warp_sum(v0 < v1 ? lane_sum(p, q, v0, v1, lane) : Pair{0.f, 0.f});
     if (lane == 0) sh.seg[warp] = w;
   }
   __syncthreads();
   if (warp == 0) {
-    const int m = crossing(sh.seg, kWarps, target, before);
+    const double target = sh.target;
+    double before = sh.before;
+    const int m = crossing(lane < kWarps ? sh.seg[lane] : 0.0, lane, target, before);
     const int64_t p0 = s0 + m * piece, p1 = min(p0 + piece, s1);
     int found = -1, positive = -1;
     for (int64_t c = p0; c < p1 && found < 0; c += 32) {
       const double w = c + lane < p1 ? weight(p, q, c + lane) : 0.0;
-      double sum = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
-      }
-      const unsigned over = __ballot_sync(0xffffffffu, w > 0.0 && before + sum > target);
+      const double upto = before + scan(w, lane);
+      const unsigned over = __ballot_sync(0xffffffffu, w > 0.0 && upto > target);
       const unsigned any = __ballot_sync(0xffffffffu, w > 0.0);
       if (over)
         found = static_cast<int>(c) + __ffs(over) - 1;
       else if (any)
         positive = static_cast<int>(c) + 31 - __clz(any);
-      before += __shfl_sync(0xffffffffu, sum, 31);
+      before = __shfl_sync(0xffffffffu, upto, 31);
     }
     // two roundings of one sum can differ in their last bits
+    __syncwarp();
     if (lane == 0) sh.found = found >= 0 ? found : positive;
   }
   __syncthreads();

@@ -28,6 +28,7 @@ struct CacheArgs {
   const __nv_bfloat16* src[2];
   __nv_bfloat16* dst[2];
   int64_t tok[2], bat[2];
+  bool wide;  // rows of the bf16 side start on 32 bytes
 };
 
 // Row `i` of sequence `b`, and whether it takes part.
@@ -64,65 +65,129 @@ __device__ __forceinline__ int64_t slot_of(const CacheArgs& a, const Row& r) {
   return page * a.page_size + (at - entry * static_cast<uint32_t>(a.page_size));
 }
 
-// E4M3 codes of 8 bf16 values (two per word) under the scale byte `byte`.
-__device__ __forceinline__ uint2 encode8(const uint32_t w[4], int byte) {
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);  // 2^-e
-  uint32_t two[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float lo = __uint_as_float(w[k] << 16) * inv, hi = __uint_as_float(w[k] & 0xffff0000u) * inv;
-    // the conversion would make infinities 448
-    if ((w[k] & 0x7fffu) == 0x7f80u) lo = NAN;
-    if ((w[k] & 0x7fff0000u) == 0x7f800000u) hi = NAN;
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
-    two[k] = c;
+// 16 bf16 values (two per word), or their codes (four per word).
+struct Values16 {
+  uint32_t w[8];
+};
+struct Codes16 {
+  uint32_t w[4];
+};
+
+// 32 bytes: one access, or two of 16 where rows start on 16 only (`wide`, the
+// same for all threads).  Streamed: nobody comes back soon.
+__device__ __forceinline__ Values16 load16(const void* p, bool wide) {
+  Values16 v;
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                   "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                 : "l"(p));
+  } else {
+    const uint4 lo = __ldg(static_cast<const uint4*>(p));
+    const uint4 hi = __ldg(static_cast<const uint4*>(p) + 1);
+    v = Values16{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
   }
-  return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+  return v;
+}
+__device__ __forceinline__ void store16(void* p, const Values16& v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.w[0]),
+                 "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+                 "r"(v.w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+  }
 }
 
-// Bits of the largest finite magnitude of 8 bf16 values.
-__device__ __forceinline__ uint32_t top8(const uint32_t w[4]) {
-  uint32_t top = 0;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bits of the largest magnitude (NaN and infinities, the largest bit patterns,
+// among them).
+__device__ __forceinline__ uint32_t top16(const Values16& v) {
+  uint32_t m = v.w[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-    if (lo < 0x7f80u) top = max(top, lo);
-    if (hi < 0x7f80u) top = max(top, hi);
+  for (int k = 1; k < 8; ++k) m = max_u16x2(m, v.w[k] & 0x7fff7fffu);
+  return max(m & 0xffffu, m >> 16);
+}
+
+// The values with NaN and infinities replaced by zero.
+__device__ __forceinline__ Values16 finite16(Values16 v) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if ((v.w[k] & 0x7f80u) == 0x7f80u) v.w[k] &= 0xffff0000u;
+    if ((v.w[k] & 0x7f800000u) == 0x7f800000u) v.w[k] &= 0xffffu;
   }
-  return top;
+  return v;
+}
+
+// E4M3 of finite values under the scale byte `byte`.  x 2^-e is exact in bf16
+// (e is the group's own, so only what rounds to zero anyway can underflow).
+__device__ __forceinline__ Codes16 encode16(const Values16& v, int byte) {
+  const uint32_t inv = static_cast<uint32_t>(254 - byte) << 7;  // 2^-e
+  uint32_t two[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t x = mul_bf16x2(v.w[k], inv | inv << 16);
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(c)
+        : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
+    two[k] = c;
+  }
+  Codes16 r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.w[k] = two[2 * k] | two[2 * k + 1] << 16;
+  return r;
+}
+
+// NaN codes in the place of values that are not finite.
+__device__ __noinline__ Codes16 mark16(const Values16& v, Codes16 r) {
+  for (int k = 0; k < 16; ++k)
+    if ((v.w[k >> 1] >> (k & 1) * 16 & 0x7f80u) == 0x7f80u) r.w[k >> 2] |= 0x7fu << (k & 3) * 8;
+  return r;
 }
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
-// `L` lanes per row (4 .. 32, so that a group of 32 features is 4 lanes of one
-// row), 8 features a lane and step, K and V of a row in turn with all loads of
-// up to kUnroll steps issued before the first is used: 32 lanes x 16 bytes x 8
-// loads in flight per warp.
+// `L` lanes per row (2 .. 32, so that a group of 32 features is 2 lanes of one
+// row), 16 features a lane and step; all loads of K and V of up to kUnroll
+// steps are issued before the first is used: 32 lanes x 32 bytes x 4 in flight
+// per warp.  HBM bounds it: 3 + 1/32 bytes per value at 4 to 5 instructions per
+// value, about half the issue rate (one value at a time took 10 and was bound
+// by them: 154 us where this takes 105, 65,521 x 2 rows of 8 x 128).
 template <int L>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
   constexpr int kRows = kThreads / L;
   const int lane = threadIdx.x % L;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
   const Row r = row_of(a, first, threadIdx.x / L);
-  const int chunks = a.row_values >> 3;  // a multiple of 4
-  const int64_t slot = r.takes_part ? slot_of(a, r) : -1;
+  const int chunks = a.row_values >> 4;  // a multiple of 2
   // the lanes of a row decide alike, those of a warp need not: no early return
   // before the shuffles
-  const bool on = slot >= 0;
   for (int c0 = 0; c0 < chunks; c0 += L * kUnroll) {
-    uint4 v[2][kUnroll];
+    Values16 v[2][kUnroll];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.src[kv] + r.b * a.bat[kv] +
-                                                        r.i * a.tok[kv]);
+      const __nv_bfloat16* src = a.src[kv] + r.b * a.bat[kv] + r.i * a.tok[kv];
 #pragma unroll
       for (int t = 0; t < kUnroll; ++t) {
         const int c = c0 + t * L + lane;
-        v[kv][t] = on && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+        v[kv][t] = r.takes_part && c < chunks ? load16(src + c * 16, a.wide) : Values16{};
       }
     }
+    const int64_t slot = r.takes_part ? slot_of(a, r) : -1;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       uint8_t* codes = a.codes[kv] + slot * a.row_values;
@@ -130,35 +195,41 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
 #pragma unroll
       for (int t = 0; t < kUnroll; ++t) {
         const int c = c0 + t * L + lane;
-        const uint32_t w[4] = {v[kv][t].x, v[kv][t].y, v[kv][t].z, v[kv][t].w};
-        uint32_t top = top8(w);
+        uint32_t top = top16(v[kv][t]);
+        const bool bad = __any_sync(0xffffffffu, top >= 0x7f80u);
+        const Values16 x = bad ? finite16(v[kv][t]) : v[kv][t];
+        if (bad) top = top16(x);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 448 = 1.75 x 2^8: e = exponent - 8, one more above 1.75
-        const int byte = max(0, static_cast<int>(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
-        if (on && c < chunks) {
-          *reinterpret_cast<uint2*>(codes + c * 8) = encode8(w, byte);
-          if ((c & 3) == 0) scales[c >> 2] = static_cast<uint8_t>(byte);
+        const int byte = max(0, static_cast<int>((top + 0x1fu) >> 7) - 8);
+        Codes16 out = encode16(x, byte);
+        if (bad) out = mark16(v[kv][t], out);
+        if (slot >= 0 && c < chunks) {
+          *reinterpret_cast<uint4*>(codes + c * 16) =
+              make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]);
+          if ((c & 1) == 0) scales[c >> 1] = static_cast<uint8_t>(byte);
         }
       }
     }
   }
 }
 
-__device__ __forceinline__ uint32_t decode2(uint32_t two, float scale) {
-  uint32_t h2;
-  const uint16_t v = static_cast<uint16_t>(two & 0xffffu);
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(v));
-  __half2 h;
-  *reinterpret_cast<uint32_t*>(&h) = h2;
-  const float2 f = __half22float2(h);
-  __nv_bfloat162 r = __floats2bfloat162_rn(f.x * scale, f.y * scale);
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-
-// 2^(byte - 127) as fp32: byte 0 is the subnormal 2^-127, 255 is NaN.
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
+// 16 values of codes times 2^(byte - 127).  Codes are exact in bf16, so the one
+// rounding is that of a product below bf16's smallest.
+__device__ __forceinline__ Values16 decode16(const uint4& codes, uint32_t byte) {
+  const uint32_t s = byte == 0 ? 0x0040u : byte == 255 ? 0x7fffu : byte << 7;  // bf16
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  Values16 r;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t h2;
+    const uint16_t two = static_cast<uint16_t>(w[k >> 1] >> (k & 1) * 16);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    const __nv_bfloat162 x = __floats2bfloat162_rn(f.x, f.y);
+    r.w[k] = mul_bf16x2(*reinterpret_cast<const uint32_t*>(&x), s | s << 16);
+  }
+  return r;
 }
 
 // The same lanes and steps as the write.
@@ -169,33 +240,30 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
   const Row r = row_of(a, first, threadIdx.x / L);
   if (!r.takes_part) return;
-  const int chunks = a.row_values >> 3;
+  const int chunks = a.row_values >> 4;
   const int64_t slot = slot_of(a, r);
   for (int c0 = 0; c0 < chunks; c0 += L * kUnroll) {
-    uint2 v[2][kUnroll];
+    uint4 v[2][kUnroll];
     uint32_t sb[2][kUnroll];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
       for (int t = 0; t < kUnroll; ++t) {
         const int c = c0 + t * L + lane;
-        v[kv][t] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN
-        sb[kv][t] = 127;
+        v[kv][t] = make_uint4(0, 0, 0, 0);
+        sb[kv][t] = 255;  // NaN, for a row that has no place
         if (slot >= 0 && c < chunks) {
-          v[kv][t] = __ldcs(reinterpret_cast<const uint2*>(a.codes[kv] + slot * a.row_values) + c);
-          sb[kv][t] = __ldg(a.scales[kv] + slot * (a.row_values / kGroup) + (c >> 2));
+          v[kv][t] = __ldcs(reinterpret_cast<const uint4*>(a.codes[kv] + slot * a.row_values) + c);
+          sb[kv][t] = __ldg(a.scales[kv] + slot * (a.row_values / kGroup) + (c >> 1));
         }
       }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      uint4* dst = reinterpret_cast<uint4*>(a.dst[kv] + r.b * a.bat[kv] + r.i * a.tok[kv]);
+      __nv_bfloat16* dst = a.dst[kv] + r.b * a.bat[kv] + r.i * a.tok[kv];
 #pragma unroll
       for (int t = 0; t < kUnroll; ++t) {
         const int c = c0 + t * L + lane;
-        const float s = scale_of(sb[kv][t]);
-        const uint4 out = make_uint4(decode2(v[kv][t].x, s), decode2(v[kv][t].x >> 16, s),
-                                     decode2(v[kv][t].y, s), decode2(v[kv][t].y >> 16, s));
-        if (c < chunks) dst[c] = out;
+        if (c < chunks) store16(dst + c * 16, decode16(v[kv][t], sb[kv][t]), a.wide);
       }
     }
   }
@@ -234,6 +302,8 @@ csbp_status make_args(const csbp_kv_cache* c, const csbp_cache_rows* r, const vo
     a.bat[i] = (r->batch > 1 && sb != 0) ? sb : span;
     if (a.bat[i] < span || a.bat[i] % 8 != 0 || a.bat[i] >= kMaxElems) return CSBP_ERR_INVALID;
   }
+  a.wide = aligned(k, 32) && aligned(v, 32) &&
+           ((a.tok[0] | a.tok[1] | a.bat[0] | a.bat[1]) & 15) == 0;
   a.pages = c->pages;
   a.page_size = c->page_size;
   a.row_values = static_cast<int32_t>(row);
@@ -254,15 +324,18 @@ csbp_status make_args(const csbp_kv_cache* c, const csbp_cache_rows* r, const vo
 // step (so that short rows share a warp), at most a warp.
 template <bool kWrite>
 csbp_status launch(const CacheArgs& a, void* stream) {
-  const int chunks = a.row_values >> 3;
-  const int lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+  const int chunks = a.row_values >> 4;
+  const int lanes = chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
   const int64_t per = kThreads / lanes;
   const int64_t grid = (static_cast<int64_t>(a.batch) * a.rows + per - 1) / per;
   if (grid > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned g = static_cast<unsigned>(grid);
   const int timed = timer_begin(kWrite ? 11 : 12, stream);
-  if (lanes == 4)
+  if (lanes == 2)
+    kWrite ? cache_write_kernel<2><<<g, kThreads, 0, s>>>(a)
+           : cache_read_kernel<2><<<g, kThreads, 0, s>>>(a);
+  else if (lanes == 4)
     kWrite ? cache_write_kernel<4><<<g, kThreads, 0, s>>>(a)
            : cache_read_kernel<4><<<g, kThreads, 0, s>>>(a);
   else if (lanes == 8)
