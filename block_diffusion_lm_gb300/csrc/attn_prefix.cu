@@ -6,22 +6,23 @@
 // group), flattened in that order; a row tile is 128 consecutive ones, so the
 // prefix K/V pass through the tensor cores once per 128 rows however they
 // divide into sequences, tokens and heads.  The softmax warps copy the tile's
-// rows into shared memory themselves (a row per thread, zeros for the rest),
-// which takes any token or batch stride and any group size.  Where row tiles
-// kept inside sequences need (nearly) no more of them than tiles packed over
-// sequences, a tile's keys are the prefix and then its sequence's own keys, in
-// one softmax (`fused`); else the prefix runs on packed tiles and the own keys
-// on separate units with tiles inside sequences.
+// rows into shared memory themselves (zeros below the last), which takes any
+// token or batch stride and any group size.
 //
-// Units.  One CTA owns two row tiles ("slots") of one head group and a range
-// of their key tiles; a key tile that both read is loaded once.  Each slot has
-// its own softmax warpgroup, so that one slot's MMAs run under the other's
-// softmax.  A CTA with one row tile left gives it to both slots, which take
-// the key tiles in turn and are joined at the end (`alternate`).  Where the
-// row tiles alone do not fill the GPU, the key tiles are split over CTAs too,
-// each of which leaves a normalised fp32 partial and its LSE in the
-// workspace, and a second kernel joins them exactly ([Blog] "在线 softmax 合并：
-// 为什么分两段算仍是同一个注意力").
+// Keys.  A row tile reads all prefix key tiles, then the own key tiles of each
+// sequence that has rows in it, masked to that sequence's rows.  Own keys of
+// short sequences fill few rows of the MMA, but no more than they would in
+// row tiles of their own, and one softmax covers all of a row's keys.
+//
+// Work.  A job is two row tiles ("slots") of one head group with all their key
+// tiles; a prefix key tile is loaded once for both, and each slot has its own
+// softmax warpgroup, so that one slot's MMAs run under the other's softmax.  A
+// job with one row tile left gives it to both slots, which take the key tiles
+// in turn and are joined at the end (`alternate`).  The jobs, end to end, form
+// one list that is cut into equal shares, one per CTA and SM, wherever the cuts
+// fall: a CTA works through the pieces of its share.  A job that is cut leaves
+// a normalised fp32 partial and its LSE per piece in the workspace, and a
+// second kernel joins them exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
 //
 // Roles (384 threads), as in the training forward: warp 0 lane 0 TMA
 // producer, warp 1 lane 0 MMA issuer, warps 4..7 and 8..11 softmax of slot 0
@@ -59,23 +60,71 @@ constexpr uint32_t kRegsLow = 112;
 constexpr uint32_t kRegsSoftmax = 192;
 constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsSoftmax;
 
+// tma_load_3d with an L2 policy.
+__device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const void* tmap, uint64_t* bar,
+                                                 int x, int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
+// Division of 0 <= n < 2^31 by an invariant d >= 1 (Granlund and Montgomery,
+// "Division by invariant integers using multiplication").
+struct Divisor {
+  uint32_t mul, shift;
+  static Divisor of(uint32_t d) {
+    Divisor r{0, 0};
+    while ((uint64_t(1) << r.shift) < d) ++r.shift;
+    r.mul = static_cast<uint32_t>((((uint64_t(1) << r.shift) - d) << 32) / d + 1);
+    return r;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (__umulhi(mul, n) + n) >> shift;
+  }
+};
+
 // How the rows and keys of a problem are cut up (host and device).
 struct Plan {
   int32_t gs, n_groups;   // query heads per row group, groups of them
   int32_t seq_rows;       // rows of one sequence: queries x gs
-  int32_t tiles_seq;      // row tiles of one sequence
-  int32_t fused;          // 1: tiles inside sequences read the prefix and the own keys
-  int32_t row_tiles;      // of the shared units, per head group
-  int32_t pairs;          // CTAs of the shared units per head group and key range
-  int32_t splits;         // key ranges of the shared units
-  int32_t own_pairs;      // CTAs per head group and range of the own units; 0: none
-  int32_t own_splits;
-  int32_t parts;          // splits + own splits; 1: written directly
+  int32_t row_tiles;      // per head group
+  int32_t pairs;          // jobs per head group
+  int32_t parts;          // most pieces of a job
+  int32_t cut;            // 1: some job has more than one piece
+  int32_t ctas;           // shares
+  // the list: jobs of equal length in units of time, the first `len_prefix` of
+  // each for its prefix tiles and the rest for the own tiles
+  uint32_t jobs, len, len_prefix, total;
+  // share length in 32.32 fixed point, and reciprocals that only guess or cut
+  // the same way everywhere
+  uint64_t step;
+  float inv_step;
+  float inv_prefix, inv_own;
+  Divisor by_gs, by_queries, by_seq_rows, by_pairs, by_len, by_heads, by_per_kv;
+
+  // start of share c
+  __host__ __device__ uint32_t share(uint32_t c) const {
+    return c >= static_cast<uint32_t>(ctas) ? total : static_cast<uint32_t>((c * step) >> 32);
+  }
+  // the share that holds place x of the list
+  __host__ __device__ int share_of(uint32_t x) const {
+    int c = static_cast<int>(static_cast<float>(x) * inv_step);
+    c = c < ctas ? c : ctas - 1;
+    while (share(c) > x) --c;
+    while (share(c + 1) <= x) ++c;
+    return c;
+  }
+  // pieces that a job is cut into
+  __host__ __device__ int pieces(uint32_t job) const {
+    return share_of(job * len + len - 1) - share_of(job * len) + 1;
+  }
 };
 
 struct PrefixParams {
   Plan plan;
-  int32_t batch, queries, prefix_len, own_max, Hq, G, causal;
+  int32_t batch, queries, prefix_len, own_max, Hq, causal;
   float scale_log2;
   const __nv_bfloat16* q;
   int64_t q_tok, q_bat;  // element strides
@@ -86,6 +135,75 @@ struct PrefixParams {
   float* part_lse;    // [parts][batch x queries x Hq]
   int* status;
 };
+
+// A CTA's piece of a job.  Warp 2 works the pieces out ahead of the others and
+// leaves them in a ring of two in shared memory.
+struct Unit {
+  int valid;           // 0: the share is done
+  int group, part;
+  int direct;          // the whole of its rows' keys
+  int alternate;       // one row tile, both slots
+  int m0, m1;          // range of the job's key-tile list
+  int np;              // prefix key tiles of the job
+  int row0[2];         // first flattened row of a slot's tile
+  int rows[2];         // its rows
+  int seq0[2];         // first of the sequences with rows in it
+  int seqs[2];         // their number
+  int own[2];          // their own key tiles, together
+  // a slot's key tiles in the range: n_pre prefix tiles from t_pre on, then
+  // n_own own tiles from t_own on, in steps of 1 (alternate: 2)
+  int n_pre[2], t_pre[2], n_own[2], t_own[2];
+  int keys[2][kTile];       // own keys of each sequence
+  int upto[2][kTile + 1];   // own key tiles of the sequences before it
+
+  // Which slots read the m-th key tile of the list, and its number among the
+  // prefix tiles or the slot's own tiles: prefix tiles first, then the two
+  // slots' own tiles in turn.
+  __device__ __forceinline__ void at(int m, bool& prefix, int& t, bool& in0, bool& in1) const {
+    prefix = m < np;
+    if (prefix) {
+      t = m;
+      in0 = !alternate || !(m & 1);
+      in1 = !alternate || (m & 1);
+      return;
+    }
+    const int x = m - np;
+    if (alternate) {
+      t = x;
+      in0 = !(m & 1);
+    } else {
+      const int both = min(own[0], own[1]);
+      in0 = x < 2 * both ? !(x & 1) : own[0] > own[1];
+      t = x < 2 * both ? x >> 1 : x - both;
+    }
+    in1 = !in0;
+  }
+  // Place in the list of slot s's own tile t.
+  __device__ __forceinline__ int place(int s, int t) const {
+    const int both = min(own[0], own[1]);
+    return np + (alternate ? t : t < both ? 2 * t + s : t + both);
+  }
+  // Own tiles of slot s among the first x of the list's own tiles.
+  __device__ __forceinline__ int own_before(int s, int x) const {
+    const int both = min(own[0], own[1]);
+    if (x < 2 * both) return (x + 1 - s) >> 1;
+    return own[s] > own[1 - s] ? x - both : both;
+  }
+  // Sequence (from seq0 on) that slot s's own tile t belongs to.
+  __device__ __forceinline__ int sequence(int s, int t) const {
+    int lo = 0, hi = seqs[s] - 1;
+    while (lo < hi) {  // last one that starts at or before t
+      const int mid = (lo + hi + 1) >> 1;
+      if (upto[s][mid] <= t)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+constexpr int kUnitBytes = (sizeof(Unit) + 15) / 16 * 16;
 
 template <int D>
 struct PrefixLayout {
@@ -106,88 +224,153 @@ struct PrefixLayout {
   static constexpr int bPFull = bSFull + 2;         // [2] (the slot's softmax warps)
   static constexpr int bPvDone = bPFull + 2;        // [2]
   static constexpr int bMerge = bPvDone + 2;        // slot 1's (max, sum) are in shared memory
-  static constexpr int bDrain = bMerge + 1;
+  static constexpr int bJoined = bMerge + 1;        // slot 0 has read them and slot 1's O
+  static constexpr int bUnitFull = bJoined + 1;     // [2] pieces worked out
+  static constexpr int bUnitEmpty = bUnitFull + 2;  // [2] and used by all roles
+  static constexpr int bDrain = bUnitEmpty + 2;
   static constexpr int kBars = bDrain + 1;
   static constexpr int kMisc = kBar + kBars * 8;    // tmem base, abort flag
   static constexpr int kMl = (kMisc + 8 + 15) / 16 * 16;  // slot 1's max and sum, 128 rows
-  static constexpr int kDynSmem = kMl + kTile * 8;
+  static constexpr int kUnits = kMl + kTile * 8;    // ring of two pieces
+  static constexpr int kDynSmem = kUnits + 2 * kUnitBytes;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
 };
 
-// One CTA's work, the same for all its threads.
-struct Unit {
-  int group, part;
-  bool alternate;      // one row tile, both slots
-  int64_t row0[2];     // first flattened row of a slot's tile
-  int rows[2];         // its rows
-  int seq[2];          // its sequence (fused and own units)
-  int np;              // prefix key tiles
-  int c[2], nc[2];     // own keys and key tiles of a slot's sequence
-  int m0, m1;          // this CTA's range of the key-tile list
+// Key tiles before place x of a job: prefix tiles by place alone (so that
+// loading can start before any own length is known), own tiles by share.
+__device__ __forceinline__ int prefix_before(const Plan& pl, int np, uint32_t x) {
+  if (x >= pl.len_prefix) return np;
+  return min(np, static_cast<int>(static_cast<float>(x) * pl.inv_prefix * static_cast<float>(np)));
+}
+__device__ __forceinline__ int tiles_before(const Plan& pl, int np, int own, uint32_t x) {
+  if (x < pl.len_prefix) return prefix_before(pl, np, x);
+  if (x == pl.len) return np + own;
+  return np + min(own, static_cast<int>(static_cast<float>(x - pl.len_prefix) * pl.inv_own *
+                                        static_cast<float>(own)));
+}
 
-  // The m-th key tile of the list: prefix tiles first, then the two slots'
-  // own tiles in turn.  Returns which slots read it.
-  __device__ void at(int m, bool& prefix, int& tile, bool& in0, bool& in1) const {
-    prefix = m < np;
-    if (prefix) {
-      tile = m;
-      in0 = !alternate || !(m & 1);
-      in1 = !alternate || (m & 1);
-      return;
-    }
-    const int x = m - np;
-    if (alternate) {
-      tile = x;
-      in0 = !(m & 1);
-    } else {
-      const int both = 2 * min(nc[0], nc[1]);
-      in0 = x < both ? !(x & 1) : nc[0] > nc[1];
-      tile = x < both ? x >> 1 : x - (both >> 1);
-    }
-    in1 = !in0;
-  }
-};
-
-__device__ __forceinline__ Unit unit_of(const PrefixParams& p) {
+// The piece at place `at` of the list, in a share that ends at `end`; moves
+// `at` to its end.  One whole warp.
+__device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, uint32_t end,
+                                          Unit& u) {
+  const int lane = threadIdx.x & 31;
   const Plan& pl = p.plan;
-  Unit u;
-  int64_t i = blockIdx.x;
-  const int64_t shared = static_cast<int64_t>(pl.pairs) * pl.n_groups * pl.splits;
-  const bool own = i >= shared;
-  if (own) i -= shared;
-  const int per = own ? pl.own_pairs : pl.pairs;
-  const int pair = static_cast<int>(i % per);
-  i /= per;
-  u.group = static_cast<int>(i % pl.n_groups);
-  const int split = static_cast<int>(i / pl.n_groups);
-  u.part = own ? pl.splits + split : split;
-  u.alternate = 2 * pair + 1 >= (own ? p.batch * pl.tiles_seq : pl.row_tiles);
-  u.np = own ? 0 : (p.prefix_len + kTile - 1) / kTile;
-  const bool inside = own || pl.fused;  // tiles inside sequences
+  if (at >= end) {
+    if (lane == 0) u.valid = 0;
+    __syncwarp();
+    return;
+  }
+  const uint32_t job = pl.by_len(at), start = job * pl.len;
+  const uint32_t x0 = at - start, x1 = min(end - start, pl.len);
+  at = start + x1;
+  const int group = pl.by_pairs(job);
+  const int pair = job - group * pl.pairs;
+  const bool alternate = 2 * pair + 1 >= pl.row_tiles;
+  const int np = (p.prefix_len + kTile - 1) / kTile;
+  int own[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const int tile = 2 * pair + (u.alternate ? 0 : s);
-    int64_t end;
-    if (inside) {
-      u.seq[s] = tile / pl.tiles_seq;
-      const int64_t first = static_cast<int64_t>(u.seq[s]) * pl.seq_rows;
-      u.row0[s] = first + static_cast<int64_t>(tile - u.seq[s] * pl.tiles_seq) * kTile;
-      end = first + pl.seq_rows;
-    } else {
-      u.seq[s] = 0;
-      u.row0[s] = static_cast<int64_t>(tile) * kTile;
-      end = static_cast<int64_t>(p.batch) * pl.seq_rows;
+    const int row0 = (2 * pair + (alternate ? 0 : s)) * kTile;
+    const int rows = min(kTile, p.batch * pl.seq_rows - row0);
+    const int seq0 = pl.by_seq_rows(row0);
+    const int seqs = pl.by_seq_rows(row0 + rows - 1) - seq0 + 1;
+    own[s] = s == 1 && alternate ? own[0] : 0;
+    // (alternate: both slots go by slot 0's tables)
+    for (int k0 = 0; k0 < (s == 1 && alternate ? 0 : seqs); k0 += 32) {
+      const int k = k0 + lane;
+      int keys = 0;
+      if (k < seqs && p.own_max > 0)
+        keys = min(max(__ldg(p.own_len + seq0 + k), 0), p.own_max);
+      const int n = (keys + kTile - 1) / kTile;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      if (k < seqs) {
+        u.keys[s][k] = keys;
+        u.upto[s][k] = own[s] + sum - n;
+      }
+      own[s] += __shfl_sync(0xffffffffu, sum, 31);
     }
-    u.rows[s] = static_cast<int>(min(static_cast<int64_t>(kTile), end - u.row0[s]));
-    u.c[s] = inside && p.own_max > 0 ? min(max(__ldg(p.own_len + u.seq[s]), 0), p.own_max) : 0;
-    u.nc[s] = (u.c[s] + kTile - 1) / kTile;
+    if (lane == 0) {
+      u.row0[s] = row0;
+      u.rows[s] = rows;
+      u.seq0[s] = seq0;
+      u.seqs[s] = seqs;
+      u.own[s] = own[s];
+    }
   }
-  const int64_t total = static_cast<int64_t>(u.np) + u.nc[0] + (u.alternate ? 0 : u.nc[1]);
-  const int n = own ? pl.own_splits : pl.splits;
-  u.m0 = static_cast<int>(total * split / n);
-  u.m1 = static_cast<int>(total * (split + 1) / n);
-  return u;
+  if (lane == 0) {
+    u.valid = 1;
+    u.group = group;
+    u.part = static_cast<int>(blockIdx.x) - pl.share_of(start);
+    u.direct = x0 == 0 && x1 == pl.len;
+    u.alternate = alternate;
+    u.np = np;
+    const int all = own[0] + (alternate ? 0 : own[1]);
+    u.m0 = tiles_before(pl, np, all, x0);
+    u.m1 = tiles_before(pl, np, all, x1);
+    const int p0 = min(u.m0, np), p1 = min(u.m1, np);
+    const int o0 = max(u.m0, np) - np, o1 = max(u.m1, np) - np;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (alternate) {  // places of the list with the slot's parity
+        u.t_pre[s] = p0 + ((p0 ^ s) & 1);
+        u.n_pre[s] = max(0, p1 - u.t_pre[s] + 1) >> 1;
+        u.t_own[s] = o0 + (((np + o0) ^ s) & 1);
+        u.n_own[s] = max(0, o1 - u.t_own[s] + 1) >> 1;
+      } else {
+        u.t_pre[s] = p0;
+        u.n_pre[s] = p1 - p0;
+        u.t_own[s] = u.own_before(s, o0);
+        u.n_own[s] = u.own_before(s, o1) - u.t_own[s];
+      }
+    }
+  }
+  __syncwarp();
 }
+
+// A row of a tile: sequence b, token i, head h.
+struct Row {
+  uint32_t token;
+  int b, i, h;
+};
+__device__ __forceinline__ Row row_at(const PrefixParams& p, int group, uint32_t flat) {
+  Row r;
+  r.token = p.plan.by_gs(flat);
+  r.b = p.plan.by_queries(r.token);
+  r.i = r.token - r.b * p.queries;
+  r.h = group * p.plan.gs + static_cast<int>(flat - r.token * p.plan.gs);
+  return r;
+}
+
+// A warp's 32 Q rows, D / 8 lanes to a row: the lane's 16-byte chunks of them
+// (`mine`: element offset of the lane's own row, -1: none, zeros).
+template <int D>
+struct QRows {
+  static constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  uint4 v[kLanes];
+  __device__ __forceinline__ void load(const PrefixParams& p, int64_t mine) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < kLanes; ++t) {
+      const int64_t src = __shfl_sync(0xffffffffu, mine, t * kAtOnce + lane / kLanes);
+      v[t] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + src) + lane % kLanes)
+                      : make_uint4(0, 0, 0, 0);
+    }
+  }
+  // into the 128-byte-swizzled tile of 64-feature boxes, from row `row0` on
+  __device__ __forceinline__ void store(uint8_t* tile, int row0) const {
+    const int lane = threadIdx.x & 31, chunk = lane % kLanes;
+    uint8_t* dst = tile + (chunk >> 3) * (kTile * 128);
+#pragma unroll
+    for (int t = 0; t < kLanes; ++t)
+      *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + t * kAtOnce + lane / kLanes, chunk & 7)) =
+          v[t];
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -205,64 +388,129 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(smem + Lay::kMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + Lay::kMisc + 4);
   float2* ml = reinterpret_cast<float2*>(smem + Lay::kMl);
+  const auto unit_at = [&](int k) -> Unit& {
+    return *reinterpret_cast<Unit*>(smem + Lay::kUnits + (k & 1) * kUnitBytes);
+  };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const Unit u = unit_of(p);
-  // the kernel that joins the parts may take its place on the GPU; it waits
+  // the kernel that joins the pieces may take its place on the GPU; it waits
   // for this one's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < Lay::kBars; ++i) mbar_init(&bars[i], 1);
-    // arrivals of a slot's warps: all four load Q, those with rows make P
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars[Lay::bQFull + s], 4);
-      mbar_init(&bars[Lay::bPFull + s], (u.rows[s] + 31) / 32);
+  uint32_t reached = p.plan.share(blockIdx.x);
+  const uint32_t share_end = p.plan.share(blockIdx.x + 1);
+  const uint32_t first_job = p.plan.by_len(reached);
+  const int first_group = p.plan.by_pairs(first_job);
+  const int first_pair = first_job - first_group * p.plan.pairs;
+  // Set-up, with the first piece's Q and K/V already on their way: memory takes
+  // a few us to answer all SMs at once.  The two halves of the CTA meet at
+  // barrier 2 when the barriers and TMEM are there.
+  if (warp >= 4) {
+    const int flat = 2 * first_pair * kTile + (static_cast<int>(threadIdx.x) - 128);
+    int64_t mine = -1;
+    if (flat < p.batch * p.plan.seq_rows && reached < share_end) {
+      const Row r = row_at(p, first_group, flat);
+      mine = r.b * p.q_bat + r.i * p.q_tok + static_cast<int64_t>(r.h) * D;
     }
-    mbar_init(&bars[Lay::bMerge], (u.rows[1] + 31) / 32);
-    *abort_flag = 0;
-    fence_mbarrier_init();
+    QRows<D> q;
+    q.load(p, mine);
+    q.store(smem + Lay::kQ + (warp >= 8 ? Lay::kTileBytes : 0), (warp & 3) * 32);
+    fence_proxy_async_smem();
+    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    if (warp == 0 && lane == 0) {
+      prefetch_tmap(&tm_kp);
+      prefetch_tmap(&tm_vp);
+      prefetch_tmap(&tm_ko);
+      prefetch_tmap(&tm_vo);
+      for (int i = 0; i < Lay::kBars; ++i) mbar_init(&bars[i], 1);
+      for (int s = 0; s < 2; ++s) {  // the four warps of a slot
+        mbar_init(&bars[Lay::bQFull + s], 4);
+        mbar_init(&bars[Lay::bPFull + s], 4);
+      }
+      mbar_init(&bars[Lay::bMerge], 4);
+      mbar_init(&bars[Lay::bJoined], 4);
+      // producer, issuer and eight softmax warps
+      mbar_init(&bars[Lay::bUnitEmpty], 10);
+      mbar_init(&bars[Lay::bUnitEmpty + 1], 10);
+      *abort_flag = 0;
+      fence_mbarrier_init();
+    }
+    if (warp == 1) {
+      tmem_alloc(tmem_base_sh, 512);
+      tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_base_sh, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_base_sh;
-  const int kvh = u.group * p.plan.gs / p.G;
+  bool ok = true;
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsLow>();
-    if (warp == 0 && lane == 0 && u.m0 < u.m1) {
+    if (warp == 0 && lane == 0) {
       // ===================== TMA producer
       int nk = 0, nv = 0;  // K / V tiles whose loads were issued
-      bool ok = true;
-      auto load = [&](int buf, int full, const CUtensorMap* map, int st, int tile, int z) {
+      int early = 0;       // of the first piece, before its own lengths are known
+      // Keys that are read once need not push anything else out of L2, this
+      // kernel's own code above all
+      uint64_t policy;
+      if (p.plan.pairs == 1)
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+      else
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+      auto load = [&](int buf, int full, const CUtensorMap* map, int st, int x, int tile, int z) {
         mbar_arrive_expect_tx(&bars[full + st], Lay::kTileBytes);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(smem + buf + st * Lay::kTileBytes + c * Lay::kBoxBytes, map, &bars[full + st],
-                      kvh * D + c * 64, tile * kTile, z);
+          tma_load_3d_hint(smem + buf + st * Lay::kTileBytes + c * Lay::kBoxBytes, map,
+                           &bars[full + st], x + c * 64, tile * kTile, z, policy);
       };
-      for (int m = u.m0; m < u.m1; ++m) {
-        const int j = m - u.m0, st = j % kStages, use = j / kStages;
-        bool prefix, in0, in1;
-        int tile;
-        u.at(m, prefix, tile, in0, in1);
-        const int z = prefix ? 0 : in0 ? u.seq[0] : u.seq[1];
-        if (use > 0)
-          ok = mbar_wait(&bars[Lay::bKEmpty + st], (use - 1) & 1, p.status, abort_flag);
+      if (reached < share_end) {
+        const int np = (p.prefix_len + kTile - 1) / kTile;
+        const uint32_t x0 = reached - first_job * p.plan.len;
+        const int p0 = prefix_before(p.plan, np, x0);
+        const int p1 = prefix_before(p.plan, np, min(share_end - first_job * p.plan.len, p.plan.len));
+        early = min(kStages, p1 - p0);
+        const int x = p.plan.by_per_kv(first_group) * D;
+        for (; nk < early; ++nk, ++nv) {
+          load(Lay::kK, Lay::bKFull, &tm_kp, nk, x, p0 + nk, 0);
+          load(Lay::kV, Lay::bVFull, &tm_vp, nk, x, p0 + nk, 0);
+        }
+      }
+      for (int k = 0; ok; ++k) {
+        ok = mbar_wait(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
         if (!ok) break;
-        load(Lay::kK, Lay::bKFull, prefix ? &tm_kp : &tm_ko, st, tile, z);
-        nk = j + 1;
-        if (use > 0)
-          ok = mbar_wait(&bars[Lay::bVEmpty + st], (use - 1) & 1, p.status, abort_flag);
-        if (!ok) break;
-        load(Lay::kV, Lay::bVFull, prefix ? &tm_vp : &tm_vo, st, tile, z);
-        nv = j + 1;
+        const Unit& u = unit_at(k);
+        if (!u.valid) break;
+        const int x = p.plan.by_per_kv(u.group) * D;
+        const int m1 = u.m1;
+        for (int m = u.m0 + (k == 0 ? early : 0); m < m1; ++m) {
+          const int st = nk % kStages, use = nk / kStages;
+          bool prefix, in0, in1;
+          int tile, z = 0;
+          u.at(m, prefix, tile, in0, in1);
+          if (!prefix) {
+            const int s = u.alternate || in0 ? 0 : 1;
+            const int q = u.sequence(s, tile);
+            tile -= u.upto[s][q];
+            z = u.seq0[s] + q;
+          }
+          if (use > 0)
+            ok = mbar_wait(&bars[Lay::bKEmpty + st], (use - 1) & 1, p.status, abort_flag);
+          if (!ok) break;
+          load(Lay::kK, Lay::bKFull, prefix ? &tm_kp : &tm_ko, st, x, tile, z);
+          ++nk;
+          if (use > 0)
+            ok = mbar_wait(&bars[Lay::bVEmpty + st], (use - 1) & 1, p.status, abort_flag);
+          if (!ok) break;
+          load(Lay::kV, Lay::bVFull, prefix ? &tm_vp : &tm_vo, st, x, tile, z);
+          ++nv;
+        }
+        if (ok) mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
       }
       if (!ok) {
         // drain: wait (ignoring the abort flag) for the loads already issued
@@ -273,21 +521,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(&bars[Lay::bVFull + j % kStages], (j / kStages) & 1, nullptr, nullptr,
                     200000000ull);
       }
-    } else if (warp == 1 && lane == 0 && u.m0 < u.m1) {
+    } else if (warp == 2) {
+      // ===================== pieces of the share, one or two ahead
+      for (int k = 0; ok && (k == 0 || unit_at(k - 1).valid); ++k) {
+        if (k >= 2)
+          ok = mbar_wait_warp(&bars[Lay::bUnitEmpty + (k & 1)], ((k >> 1) - 1) & 1, p.status,
+                              abort_flag);
+        if (!ok) break;
+        make_unit(p, reached, share_end, unit_at(k));
+        if (lane == 0) mbar_arrive(&bars[Lay::bUnitFull + (k & 1)]);
+      }
+    } else if (warp == 1 && lane == 0) {
       // ===================== MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
-      bool ok = true;
-      for (int s = 0; s < (u.alternate ? 1 : 2) && ok; ++s)
-        ok = mbar_wait(&bars[Lay::bQFull + s], 0, p.status, abort_flag);
-      int npv[2] = {0, 0};  // PV issued per slot
-      // S_s = Q_s K^T of ring stage st into slot s's S columns
-      auto issue_s = [&](int s, int st) -> bool {
+      int npv[2] = {0, 0};      // PVs issued per slot
+      int nq0 = 0, nq1 = 0;     // Q tiles taken
+      bool fresh[2] = {};       // no PV of this piece yet: the next one overwrites O
+      // S_s = Q K^T of Q tile sq and ring stage st into slot s's S columns
+      auto issue_s = [&](int s, int st, int sq) -> bool {
         if (npv[s] > 0 &&
             !mbar_wait_spin(&bars[Lay::bPvDone + s], (npv[s] - 1) & 1, p.status, abort_flag))
           return false;  // its last PV still reads the P held there
         tc_fence_after_sync();
-        const int sq = u.alternate ? 0 : s;
         const uint64_t q_desc =
             sdesc_sw128(smem_u32(smem + Lay::kQ + sq * Lay::kTileBytes), 16, 1024);
         const uint64_t k_desc =
@@ -307,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint64_t vb = sdesc_sw128(smem_u32(smem + Lay::kV + st * Lay::kTileBytes),
                                         Lay::kBoxBytes, 1024);  // V, MN-major B
-        const uint32_t acc0 = npv[s] > 0 ? 1u : 0u;
+        const uint32_t acc0 = fresh[s] ? 0u : 1u;
+        fresh[s] = false;
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           umma_bf16_ts(tmem + Lay::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(vb, k * 2048),
@@ -316,55 +573,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++npv[s];
         return true;
       };
-      bool prev0 = false, prev1 = false;
-      int j = 0;
-      for (int m = u.m0; m < u.m1 && ok; ++m, ++j) {
-        const int st = j % kStages, pst = (j + kStages - 1) % kStages;
-        bool prefix, in0, in1;
-        int tile;
-        u.at(m, prefix, tile, in0, in1);
-        auto k_ready = [&] {
-          return mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
-        };
+      int j = 0;  // key tiles so far
+      for (int k = 0; ok; ++k) {
+        ok = mbar_wait(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
+        if (!ok) break;
+        const Unit& u = unit_at(k);
+        if (!u.valid) break;
+        const int m0 = u.m0, m1 = u.m1, np = u.np, own0 = u.own[0], own1 = u.own[1];
+        const int both = 2 * min(own0, own1);
+        const bool alternate = u.alternate;
+        mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
+        if (m0 >= m1) continue;
+        const int q1 = alternate ? 0 : 1;  // Q tile of slot 1
+        ok = mbar_wait(&bars[Lay::bQFull], nq0++ & 1, p.status, abort_flag);
+        if (ok && q1) ok = mbar_wait(&bars[Lay::bQFull + 1], nq1++ & 1, p.status, abort_flag);
+        if (!ok) break;
+        fresh[0] = fresh[1] = true;
+        bool prev0 = false, prev1 = false;
+        int st = 0, pst = 0;
         auto v_ready = [&] {  // of the tile before
           return mbar_wait(&bars[Lay::bVFull + pst], ((j - 1) / kStages) & 1, p.status, abort_flag);
         };
-        if (!((in0 && prev0) || (in1 && prev1))) {
-          // the tile before went to the other slot: this S runs under its softmax
-          ok = k_ready();
-          if (ok && in0) ok = issue_s(0, st);
-          if (ok && in1) ok = issue_s(1, st);
+        // Step m issues S of tile m and PV of tile m - 1; the last one PV only.
+        for (int m = m0; m <= m1; ++m) {
+          const bool more = m < m1;
+          pst = st;
+          st = j % kStages;
+          // as in Unit::at
+          const bool in0 = more && (alternate ? !(m & 1)
+                                    : m < np  ? true
+                                    : m - np < both ? !((m - np) & 1)
+                                                    : own0 > own1);
+          const bool in1 = more && ((!alternate && m < np) || !in0);
+          // A tile that goes to the other slot than the one before (or none):
+          // S_0, S_1, PV_0, PV_1, so that this S runs under the softmax of the
+          // tile before.  Else PV_0, S_0, PV_1, S_1: each slot's softmax runs
+          // under the other's MMAs.
+          const bool apart = !((in0 && prev0) || (in1 && prev1));
+          if (!apart) {
+            ok = v_ready();
+            if (ok && prev0) ok = issue_pv(0, pst);
+          }
+          if (ok && more)
+            ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
+          if (ok && in0) ok = issue_s(0, st, 0);
+          if (!apart) {
+            if (ok && prev1) ok = issue_pv(1, pst);
+            if (!ok) break;
+            umma_commit(&bars[Lay::bVEmpty + pst]);
+          }
+          if (ok && in1) ok = issue_s(1, st, q1);
           if (!ok) break;
-          umma_commit(&bars[Lay::bKEmpty + st]);
-          if (j > 0) {
+          if (more) umma_commit(&bars[Lay::bKEmpty + st]);
+          if (apart && m > m0) {
             ok = v_ready();
             if (ok && prev0) ok = issue_pv(0, pst);
             if (ok && prev1) ok = issue_pv(1, pst);
             if (!ok) break;
             umma_commit(&bars[Lay::bVEmpty + pst]);
           }
-        } else {
-          // PV_0 of the tile before, S_0, PV_1, S_1: each slot's softmax runs
-          // under the other's MMAs
-          ok = v_ready();
-          if (ok && prev0) ok = issue_pv(0, pst);
-          if (ok) ok = k_ready();
-          if (ok && in0) ok = issue_s(0, st);
-          if (ok && prev1) ok = issue_pv(1, pst);
-          if (!ok) break;
-          umma_commit(&bars[Lay::bVEmpty + pst]);
-          if (in1) ok = issue_s(1, st);
-          if (!ok) break;
-          umma_commit(&bars[Lay::bKEmpty + st]);
+          prev0 = in0;
+          prev1 = in1;
+          if (more) ++j;
         }
-        prev0 = in0;
-        prev1 = in1;
-      }
-      if (ok && j > 0) {
-        const int pst = (j - 1) % kStages;
-        ok = mbar_wait(&bars[Lay::bVFull + pst], ((j - 1) / kStages) & 1, p.status, abort_flag);
-        if (ok && prev0) ok = issue_pv(0, pst);
-        if (ok && prev1) ok = issue_pv(1, pst);
       }
       // drain every MMA this thread issued before the CTA may free TMEM
       umma_commit(&bars[Lay::bDrain]);
@@ -378,56 +649,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t colS = s * 128;
     const uint32_t colO = Lay::kColO + s * D;
-    const int rows = s ? u.rows[1] : u.rows[0];
-    const int c_own = s ? u.c[1] : u.c[0];
-    // this thread's row: (sequence b, token i, head h)
-    const bool row_valid = row < rows;
-    const int64_t flat = (s ? u.row0[1] : u.row0[0]) + (row_valid ? row : 0);
-    const int64_t token = flat / p.plan.gs;
-    const int b = static_cast<int>(token / p.queries);
-    const int i = static_cast<int>(token - static_cast<int64_t>(b) * p.queries);
-    const int h = u.group * p.plan.gs + static_cast<int>(flat - token * p.plan.gs);
-    if (s == 0 || !u.alternate) {
-      // Q row into the 128-byte-swizzled tile, zeros below the last row
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.q_bat + i * p.q_tok +
-                                                        static_cast<int64_t>(h) * D);
-      uint8_t* dst = smem + Lay::kQ + s * Lay::kTileBytes;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint4 v = row_valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dst + (k >> 3) * Lay::kBoxBytes + sw128_offset(row, k & 7)) = v;
+    const float sl2 = p.scale_log2;
+    int n_mine = 0, n_other = 0;  // key tiles of this and the other slot so far
+    int j0 = 0;                   // key tiles of the pieces before
+    int n_joined = 0;             // pieces that both slots worked on
+    for (int k = 0; ok; ++k) {
+      ok = mbar_wait_warp(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
+      if (!ok) break;
+      const Unit& u = unit_at(k);  // the next one goes to the other record
+      if (!u.valid) break;
+      const int rows = u.rows[s];
+      const bool has_rows = (warp & 3) * 32 < rows;  // warp-uniform
+      const bool row_valid = row < rows;
+      // own keys this row reads: positions [0, own_hi) of its sequence, the
+      // my_seq-th of the tile
+      const int sl = u.alternate ? 0 : s;  // both slots go by slot 0's tables
+      int my_seq, own_hi;
+      {
+        const Row at = row_at(p, u.group, u.row0[s] + (row_valid ? row : 0));
+        my_seq = at.b - u.seq0[sl];
+        own_hi = u.keys[sl][my_seq];
+        if (p.causal) own_hi = min(own_hi, own_hi - p.queries + at.i + 1);
+        if (u.m0 < u.m1 && (s == 0 || !u.alternate)) {
+          if (k > 0) {  // the first one is there
+            QRows<D> q;
+            q.load(p, row_valid ? at.b * p.q_bat + at.i * p.q_tok + static_cast<int64_t>(at.h) * D
+                                : -1);
+            q.store(smem + Lay::kQ + s * Lay::kTileBytes, (warp & 3) * 32);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::bQFull + s]);
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Lay::bQFull + s]);
-    }
-    if ((warp & 3) * 32 < rows) {  // a warp with rows
-      const float sl2 = p.scale_log2;
-      // own keys this row reads: positions [0, own_hi)
-      const int own_hi = p.causal ? min(c_own, c_own - p.queries + i + 1) : c_own;
+      const int n_pre = u.n_pre[s], n_tiles = n_pre + u.n_own[s];
+      const int step = u.alternate ? 2 : 1;
+      int y = n_pre > 0 ? u.t_pre[s] : u.t_own[s];
       float m_ref = -INFINITY;
       float l = 0.f;
-      int n_tiles = 0;  // of this slot, so far
-      bool ok = true;
-      for (int m = u.m0; m < u.m1; ++m) {
-        bool prefix, in0, in1;
-        int tile;
-        u.at(m, prefix, tile, in0, in1);
-        if (!(s == 0 ? in0 : in1)) continue;
-        if (!mbar_wait_warp(&bars[Lay::bSFull + s], n_tiles & 1, p.status, abort_flag)) {
+      for (int t = 0; t < n_tiles; ++t, y = t == n_pre ? u.t_own[s] : y + step) {
+        const bool prefix = t < n_pre;
+        // this row reads columns [0, hi) of the tile; v_rows of its keys exist
+        int tile = y, v_rows = kTile;
+        int left = p.prefix_len;
+        if (!prefix) {
+          const int q = u.sequence(sl, y);
+          tile -= u.upto[sl][q];
+          v_rows = u.keys[sl][q] - tile * kTile;
+          left = q == my_seq && row_valid ? own_hi : 0;
+        }
+        const int hi = min(left - tile * kTile, kTile);
+        if (!mbar_wait_warp(&bars[Lay::bSFull + s], (n_mine + t) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
+        if (!has_rows) {  // nothing to do, but the MMA counts four warps
+          if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
+          continue;
+        }
         tc_fence_after_sync();
+        const auto clear_v = [&]() -> bool {
+          // the rest of the V tile may hold NaN, and P = 0 would not keep it out
+          const int j = j0 + u.place(s, y) - u.m0, st = j % kStages;
+          if (!mbar_wait_warp(&bars[Lay::bVFull + st], (j / kStages) & 1, p.status, abort_flag))
+            return false;
+          const int warps = (rows + 31) / 32;
+          uint8_t* v = smem + Lay::kV + st * Lay::kTileBytes;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          // 16-byte chunks [v_rows x 8, 128 x 8) of each 64-feature box
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll 1
+            for (int k = v_rows * 8 + (warp & 3) * 32 + lane; k < kTile * 8; k += warps * 32)
+              *reinterpret_cast<uint4*>(v + c * Lay::kBoxBytes + k * 16) = zero;
+          fence_proxy_async_smem();
+          return true;
+        };
+        if (__all_sync(0xffffffffu, hi <= 0)) {  // another sequence's keys: P = 0
+          float zero[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) zero[c] = 0.f;
+          tmem_st32(tmem + lane_base + colS, zero);
+          tmem_st32(tmem + lane_base + colS + 32, zero);
+          if (v_rows < kTile && !clear_v()) {
+            ok = false;
+            break;
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
+          continue;
+        }
         float sv[kTile];
 #pragma unroll
         for (int c = 0; c < kTile / 32; c += 2)
           tmem_ld32x2(tmem + lane_base + colS + c * 32, tmem + lane_base + colS + (c + 1) * 32,
                       sv + c * 32, sv + (c + 1) * 32);
-        // this row reads columns [0, hi) of the tile
-        const int64_t left = static_cast<int64_t>(prefix ? p.prefix_len : own_hi) -
-                             static_cast<int64_t>(tile) * kTile;
-        const int hi = static_cast<int>(min(left, static_cast<int64_t>(kTile)));
         // bit q: no row of this warp reads 32-column chunk q (warp-uniform)
         uint32_t dead = 0;
         if (__any_sync(0xffffffffu, hi < kTile)) {
@@ -456,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scale in one fused multiply-add
         const float m_new = fmaxf(m_ref, mx * sl2);
         const bool need = m_new > m_ref + kRescaleThreshold;  // false while both are -inf
-        if (n_tiles > 0 && __any_sync(0xffffffffu, need)) {
+        if (t > 0 && __any_sync(0xffffffffu, need)) {
           // O holds the PVs so far, scaled by the old reference; the last is
           // complete: the S this tile read was issued after it
           const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
@@ -502,112 +819,147 @@ __global__ void __launch_bounds__(kThreads, 1)
         float rs0, rs1;
         f2_unpack(rs2, rs0, rs1);
         l += rs0 + rs1;
-        const int v_rows = c_own - tile * kTile;  // V rows of this own tile that exist
-        if (!prefix && v_rows < kTile) {
-          // the rest may hold NaN, and P = 0 would not keep it out: clear it
-          const int j = m - u.m0, st = j % kStages;
-          if (!mbar_wait_warp(&bars[Lay::bVFull + st], (j / kStages) & 1, p.status, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int warps = (rows + 31) / 32;
-          uint8_t* v = smem + Lay::kV + st * Lay::kTileBytes;
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          // 16-byte chunks [v_rows x 8, 128 x 8) of each 64-feature box
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            for (int k = v_rows * 8 + (warp & 3) * 32 + lane; k < kTile * 8; k += warps * 32)
-              *reinterpret_cast<uint4*>(v + c * Lay::kBoxBytes + k * 16) = zero;
-          fence_proxy_async_smem();
+        if (v_rows < kTile && !clear_v()) {
+          ok = false;
+          break;
         }
-        ++n_tiles;
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
       }
       // ---- epilogue: wait for the last PV, join the slots, normalise, store
-      if (ok && n_tiles > 0)
-        ok = mbar_wait_warp(&bars[Lay::bPvDone + s], (n_tiles - 1) & 1, p.status, abort_flag);
+      const bool any_mine = n_tiles > 0;
+      n_mine += n_tiles;
+      n_other += u.n_pre[1 - s] + u.n_own[1 - s];
+      j0 += u.m1 - u.m0;
+      if (ok && any_mine)
+        ok = mbar_wait_warp(&bars[Lay::bPvDone + s], (n_mine - 1) & 1, p.status, abort_flag);
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, joined, slot 1's
-      int n_other = 0;
-      if (u.alternate) {
-        if (s == 1) {
-          if (ok) {
-            ml[row] = make_float2(m_ref, l);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[Lay::bMerge]);
-          }
-          ok = false;  // slot 0 stores for both
-        } else {
-          // tiles m0 .. m1 - 1 went to the slots in turn
-          n_other = (u.m1 - u.m0) - n_tiles;
-          ok = ok && mbar_wait_warp(&bars[Lay::bMerge], 0, p.status, abort_flag);
-          if (ok && n_other > 0)
-            ok = mbar_wait_warp(&bars[Lay::bPvDone + 1], (n_other - 1) & 1, p.status, abort_flag);
-          if (ok) {
-            const float2 other = ml[row];
-            const float top = fmaxf(m_ref, other.x);
-            const float safe = (top == -INFINITY) ? 0.f : top;
-            w0 = exp2f(m_ref - safe);
-            w1 = exp2f(other.x - safe);
-            l = l * w0 + other.y * w1;
-            m_ref = top;
-          }
+      const bool join = u.alternate && u.m0 < u.m1;
+      const bool any_other = join && u.n_pre[1 - s] + u.n_own[1 - s] > 0;
+      if (join && s == 1) {
+        if (ok) {
+          ml[row] = make_float2(m_ref, l);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::bMerge]);
+          // its O and `ml` are read by slot 0, which stores for both
+          ok = mbar_wait_warp(&bars[Lay::bJoined], n_joined++ & 1, p.status, abort_flag);
+        }
+      } else if (join) {
+        ok = ok && mbar_wait_warp(&bars[Lay::bMerge], n_joined++ & 1, p.status, abort_flag);
+        if (ok && any_other)
+          ok = mbar_wait_warp(&bars[Lay::bPvDone + 1], (n_other - 1) & 1, p.status, abort_flag);
+        if (ok) {
+          const float2 other = ml[row];
+          const float top = fmaxf(m_ref, other.x);
+          const float safe = (top == -INFINITY) ? 0.f : top;
+          w0 = exp2f(m_ref - safe);
+          w1 = exp2f(other.x - safe);
+          l = l * w0 + other.y * w1;
+          m_ref = top;
         }
       }
-      if (ok) {
+      if (ok && has_rows && !(u.alternate && s == 1)) {
         tc_fence_after_sync();
         const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-        w0 = n_tiles > 0 ? w0 * inv_l : 0.f;
+        w0 = any_mine ? w0 * inv_l : 0.f;
         w1 *= inv_l;
         const float lse = (l > 0.f) ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        const bool direct = p.plan.parts == 1;
-        const int64_t r = token * p.Hq + h;
+        // the row again: kept over the loop above it would cost registers there
+        int own_row = u.row0[s] + (row_valid ? row : 0);
+        asm volatile("" : "+r"(own_row));
+        const Row at = row_at(p, u.group, own_row);
+        const int r = row_valid ? static_cast<int>(at.token) * p.Hq + at.h : -1;
         const int64_t all = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
-        if (direct || __any_sync(0xffffffffu, l > 0.f)) {
+        if (u.direct || __any_sync(0xffffffffu, l > 0.f)) {
+          // The warp's rows, 2 D bytes of each at a time (D / 2 fp32 columns or
+          // all D in bf16), through the Q tile, whose MMAs are complete: D / 8
+          // lanes then store a row's bytes together.  Each warp stays in the
+          // places of its own Q rows: others may be loading the next piece's.
+          constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
+          uint8_t* stage = smem + Lay::kQ + s * Lay::kTileBytes;
+          const int n_rows = min(32, rows - (warp & 3) * 32);
+          const auto place = [&](int rr, int chunk) {
+            return reinterpret_cast<uint4*>(stage + (chunk >> 3) * Lay::kBoxBytes +
+                                            sw128_offset((warp & 3) * 32 + rr, chunk & 7));
+          };
+          const auto put = [&](int chunk, uint4 v) { *place(lane, chunk) = v; };
+          const auto store_rows = [&](uint8_t* out, int64_t pitch) {
+            __syncwarp();
+            const int chunk = lane & (kChunks - 1);
+            constexpr int kBatch = 8;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            if (n_tiles > 0) {
-              tmem_ld32(tmem + lane_base + colO + c * 32, o);
+            for (int r0 = lane / kChunks; r0 - lane / kChunks < n_rows; r0 += kBatch * kAtOnce) {
+              uint4 v[kBatch];
+              int to[kBatch];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= w0;
+              for (int t = 0; t < kBatch; ++t) {
+                to[t] = __shfl_sync(0xffffffffu, r, (r0 + t * kAtOnce) & 31);
+                v[t] = *place((r0 + t * kAtOnce) & 31, chunk);
+              }
+#pragma unroll
+              for (int t = 0; t < kBatch; ++t)
+                if (r0 + t * kAtOnce < n_rows)
+                  *reinterpret_cast<uint4*>(out + to[t] * pitch + chunk * 16) = v[t];
+            }
+            __syncwarp();
+          };
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t col = half * (D / 2);
+            float o[D / 2];
+            const auto load_o = [&](uint32_t from, float* v) {
+              if (D == 128)
+                tmem_ld32x2(tmem + lane_base + from + col, tmem + lane_base + from + col + 32, v,
+                            v + 32);
+              else
+                tmem_ld32(tmem + lane_base + from + col, v);
+            };
+            if (any_mine) {
+              load_o(colO, o);
+#pragma unroll
+              for (int k = 0; k < D / 2; ++k) o[k] *= w0;
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = 0.f;
+              for (int k = 0; k < D / 2; ++k) o[k] = 0.f;
             }
-            if (n_other > 0) {
-              float o1[32];
-              tmem_ld32(tmem + lane_base + Lay::kColO + D + c * 32, o1);
+            if (any_other) {
+              float o1[D / 2];
+              load_o(Lay::kColO + D, o1);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], w1, o[k]);
+              for (int k = 0; k < D / 2; ++k) o[k] = fmaf(o1[k], w1, o[k]);
             }
-            if (row_valid && direct) {
-              __nv_bfloat16* dst = p.o + r * D + c * 32;
+            if (u.direct) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                uint4 v;
-                v.x = pack_bf16x2(o[k], o[k + 1]);
-                v.y = pack_bf16x2(o[k + 2], o[k + 3]);
-                v.z = pack_bf16x2(o[k + 4], o[k + 5]);
-                v.w = pack_bf16x2(o[k + 6], o[k + 7]);
-                *reinterpret_cast<uint4*>(dst + k) = v;
-              }
-            } else if (row_valid) {
-              float* dst = p.part_o + (u.part * all + r) * D + c * 32;
+              for (int k = 0; k < D / 16; ++k)
+                put(half * (D / 16) + k, make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]),
+                                                    pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                                    pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
+                                                    pack_bf16x2(o[8 * k + 6], o[8 * k + 7])));
+              if (half) store_rows(reinterpret_cast<uint8_t*>(p.o), D * 2);
+            } else {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(dst + k) =
-                    make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              for (int k = 0; k < D / 8; ++k)
+                put(k, make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                                  __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3])));
+              store_rows(reinterpret_cast<uint8_t*>(p.part_o + u.part * all * D) + half * (D * 2),
+                         D * 4);
             }
           }
         }
         if (row_valid) {
-          if (direct)
-            p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + i] = lse;
+          if (u.direct)
+            p.lse[(static_cast<int64_t>(at.b) * p.Hq + at.h) * p.queries + at.i] = lse;
           else
             p.part_lse[u.part * all + r] = lse;
         }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (join && s == 0 && ok) mbar_arrive(&bars[Lay::bJoined]);
+        mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
       }
     }
   }
@@ -618,132 +970,157 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the key ranges' partials: `W` warps per (query, head) row, each for
-// every W-th part.  Lanes hold the parts' LSE in turn for the maximum and the
-// weights, then d / 32 features each.  It is launched while the attention
-// kernel still runs and waits for it here, so its own start costs nothing.
-// Few rows have many parts (the GPU was filled by splitting the keys), so a row
-// gets a CTA of its own and its parts are loaded side by side.
+// Joins the pieces' partials: W warps per (query, head) row, each for every
+// W-th piece.  Lanes hold the pieces' LSE in turn for the maximum and the
+// weights, then d / 32 features each, with the loads of kBatch pieces in
+// flight.  It is launched while the attention kernel still runs and waits for
+// its end here, so its own start costs nothing.
 template <int D, int W>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
-  constexpr int kN = D / 32;
-  __shared__ float4 joined[8][32];
+  constexpr int kN = D / 32, kBatch = W == 1 ? 4 : 8;
+  struct alignas(kN * 4) Part {
+    float x[kN];
+  };
+  __shared__ Part joined[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
-  const int64_t r = blockIdx.x * static_cast<int64_t>(8 / W) + warp / W;
+  const int rows = p.batch * p.queries * p.Hq;
+  const int r = blockIdx.x * (8 / W) + warp / W;
+  if (r >= rows) return;
+  // the row's job and its pieces
+  const Plan& pl = p.plan;
+  const uint32_t token = pl.by_heads(r);
+  const uint32_t h = r - token * p.Hq;
+  const uint32_t group = pl.by_gs(h);
+  const uint32_t flat = token * pl.gs + (h - group * pl.gs);
+  const int parts = pl.pieces(group * pl.pairs + flat / (2 * kTile));
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (W == 1 && r >= rows) return;
-  const int parts = p.plan.parts;
-  const float* z = p.part_lse + r;
+  if (parts == 1) return;  // stored already
   float top = -INFINITY;
-  for (int k = lane; k < parts; k += 32) top = fmaxf(top, z[k * rows]);
+  for (int k = lane; k < parts; k += 32)
+    top = fmaxf(top, p.part_lse[static_cast<int64_t>(k) * rows + r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -INFINITY ? 0.f : top;
-  float acc[kN] = {};
+  Part acc{};
   float sum = 0.f;
   for (int k0 = 0; k0 < parts; k0 += 32) {
-    const float zk = k0 + lane < parts ? z[(k0 + lane) * rows] : -INFINITY;
+    const float zk =
+        k0 + lane < parts ? p.part_lse[static_cast<int64_t>(k0 + lane) * rows + r] : -INFINITY;
     const float w = expf(zk - ref);
     sum += w;
     const int n = min(32, parts - k0);
-    for (int k1 = warp % W; k1 < n; k1 += 4 * W) {
-      float v[4][kN];
-      float wk[4];
+    for (int k1 = warp % W; k1 < n; k1 += kBatch * W) {
+      Part v[kBatch];
+      float wk[kBatch];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < kBatch; ++t) {
         const int k = k1 + t * W;
         wk[t] = __shfl_sync(0xffffffffu, w, k & 31);
         if (k >= n) wk[t] = 0.f;
-        // a range without a key of this row left no partial
-        const float* src = p.part_o + ((k0 + k) * rows + r) * D + lane * kN;
-#pragma unroll
-        for (int c = 0; c < kN; c += 2) {
-          const float2 x = wk[t] > 0.f ? *reinterpret_cast<const float2*>(src + c)
-                                       : make_float2(0.f, 0.f);
-          v[t][c] = x.x;
-          v[t][c + 1] = x.y;
-        }
+        // a piece without a key of this row left no partial
+        v[t] = Part{};
+        if (wk[t] > 0.f)
+          v[t] = reinterpret_cast<const Part*>(
+              p.part_o + (static_cast<int64_t>(k0 + k) * rows + r) * D)[lane];
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < kBatch; ++t)
 #pragma unroll
-        for (int c = 0; c < kN; ++c) acc[c] = fmaf(wk[t], v[t][c], acc[c]);
+        for (int c = 0; c < kN; ++c) acc.x[c] = fmaf(wk[t], v[t].x[c], acc.x[c]);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (W > 1) {
-    float* mine = reinterpret_cast<float*>(&joined[warp][lane]);
-#pragma unroll
-    for (int c = 0; c < kN; ++c) mine[c] = acc[c];
-    __syncthreads();
-    if (warp != 0) return;
+    joined[warp][lane] = acc;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(W * 32) : "memory");
+    if (warp % W != 0) return;
 #pragma unroll
     for (int k = 1; k < W; ++k)
 #pragma unroll
-      for (int c = 0; c < kN; ++c) acc[c] += reinterpret_cast<const float*>(&joined[k][lane])[c];
+      for (int c = 0; c < kN; ++c) acc.x[c] += joined[warp + k][lane].x[c];
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t out[kN / 2];
+  struct alignas(kN * 2) Out {
+    uint32_t x[kN / 2];
+  } out;
 #pragma unroll
-  for (int c = 0; c < kN; c += 2) out[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + r * D) + lane * (kN / 2);
-#pragma unroll
-  for (int c = 0; c < kN / 2; ++c) dst[c] = out[c];
+  for (int c = 0; c < kN; c += 2) out.x[c / 2] = pack_bf16x2(acc.x[c] * inv, acc.x[c + 1] * inv);
+  reinterpret_cast<Out*>(p.o + static_cast<int64_t>(r) * D)[lane] = out;
   if (lane == 0) {
-    const int64_t bi = r / p.Hq;
-    const int h = static_cast<int>(r - bi * p.Hq);
-    const int64_t b = bi / p.queries;
-    p.lse[(b * p.Hq + h) * p.queries + (bi - b * p.queries)] =
+    const uint32_t b = pl.by_queries(token);
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + (token - b * p.queries)] =
         sum > 0.f ? top + logf(sum) : -INFINITY;
   }
 }
 
-// How the problem is cut up on a GPU with `sms` SMs.
-Plan make_plan(const csbp_prefix_problem& p, int sms) {
-  Plan pl{};
+// How the problem is cut up on a GPU with `sms` SMs; false if it is too large
+// for 32-bit places in the list.
+bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
   const int G = p.Hq / p.Hkv;
   pl.gs = G;
   while (pl.gs > kTile || G % pl.gs != 0) --pl.gs;  // the largest divisor up to 128
   pl.n_groups = p.Hq / pl.gs;
   pl.seq_rows = p.queries * pl.gs;
-  pl.tiles_seq = static_cast<int32_t>((static_cast<int64_t>(pl.seq_rows) + kTile - 1) / kTile);
-  const int64_t packed = (static_cast<int64_t>(p.batch) * pl.seq_rows + kTile - 1) / kTile;
-  const int64_t inside = static_cast<int64_t>(p.batch) * pl.tiles_seq;
+  const int64_t rows = static_cast<int64_t>(p.batch) * pl.seq_rows;
   const int np = (p.prefix_len + kTile - 1) / kTile;
-  const int own_tiles = (p.own_max + kTile - 1) / kTile;
-  pl.fused = p.prefix_len == 0 || (p.own_max > 0 && inside * 7 <= packed * 8) ? 1 : 0;
-  pl.row_tiles = static_cast<int32_t>(pl.fused ? inside : packed);
+  pl.row_tiles = static_cast<int32_t>((rows + kTile - 1) / kTile);
   pl.pairs = (pl.row_tiles + 1) / 2;
-  const bool own_units = !pl.fused && p.own_max > 0;
-  pl.own_pairs = own_units ? static_cast<int32_t>((inside + 1) / 2) : 0;
-  // Key ranges.  Costs in key-tile times of one CTA: a CTA costs its tiles
-  // and about kOver more to start and store, and the partials of each range
-  // are written and read once at the rate at which K/V stream in.
-  constexpr double kOver = 3.0;
-  const double rows = static_cast<double>(p.batch) * p.queries * p.Hq;
-  const double join = rows * p.d * 8 / (static_cast<double>(sms) * kTile * p.d * 4);
-  auto best = [&](int64_t ctas, int tiles, bool alone) {
-    int pick = 1;
-    double cost = 1e300;
-    for (int n = 1; n <= std::min(std::max(tiles, 1), 2 * sms); ++n) {
-      const double waves = std::ceil(static_cast<double>(ctas * n) / sms);
-      const double c = waves * (std::ceil(static_cast<double>(tiles) / n) + kOver) +
-                       (n > 1 || !alone ? join * n + kOver : 0.0);
-      if (c < cost * 0.999) {
-        cost = c;
-        pick = n;
-      }
-    }
-    return pick;
-  };
-  const int fused_tiles = np + (pl.fused ? own_tiles * 2 : 0);
-  pl.splits = best(static_cast<int64_t>(pl.pairs) * pl.n_groups, fused_tiles, !own_units);
-  pl.own_splits =
-      own_units ? best(static_cast<int64_t>(pl.own_pairs) * pl.n_groups, 2 * own_tiles, false) : 0;
-  pl.parts = pl.splits + pl.own_splits;
-  return pl;
+  const int64_t jobs = static_cast<int64_t>(pl.pairs) * pl.n_groups;
+  // (row tile, sequence) pairs of a head group that share rows: every tile and
+  // every sequence starts one, together where both start
+  int64_t both = kTile;
+  while (pl.seq_rows % both != 0) both /= 2;  // rows between common starts: lcm
+  both = static_cast<int64_t>(pl.seq_rows) * (kTile / both);
+  const int64_t meets = pl.row_tiles + p.batch - (rows + both - 1) / both;
+  // Lengths, in eighths of the time of a key tile read by one slot (1.1 to 1.4
+  // us measured, D = 128): a prefix key tile of two slots takes 13 (1.9 us), the
+  // start and the end of a piece 40.  Own keys count as 5/8 of the room for
+  // them.
+  constexpr int64_t kOne = 8, kTwo = 13, kEnds = 40, kJoin = 36;
+  const int64_t own_mean = (static_cast<int64_t>(p.own_max) * 5 / 8 + kTile - 1) / kTile;
+  int64_t len_prefix = np * (pl.row_tiles == 1 ? kOne : kTwo) + kEnds;
+  int64_t len = len_prefix + (meets * own_mean * kOne + pl.pairs - 1) / pl.pairs;
+  int64_t total = jobs * len;
+  // a share of at least two key tiles
+  pl.ctas = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>(sms, (total - jobs * kEnds) / (2 * kOne))));
+  // Whole jobs, one per CTA, where that ends as soon: a cut costs the joining
+  // of its pieces (5 us, the second kernel).  More CTAs than SMs then start as
+  // others end.
+  const bool whole = (jobs + sms - 1) / sms * len <= total / pl.ctas + kEnds + kJoin;
+  while (total >= int64_t(1) << 30 && len > 1) {  // coarser units: 32-bit places
+    len_prefix = (len_prefix + 1) / 2;
+    len = (len + 1) / 2;
+    total = jobs * len;
+  }
+  if (total >= int64_t(1) << 30) return false;
+  pl.jobs = static_cast<uint32_t>(jobs);
+  pl.len = static_cast<uint32_t>(len);
+  pl.total = static_cast<uint32_t>(total);
+  pl.len_prefix = static_cast<uint32_t>(len_prefix);
+  pl.inv_prefix = 1.f / static_cast<float>(len_prefix);
+  pl.inv_own = len > len_prefix ? 1.f / static_cast<float>(len - len_prefix) : 0.f;
+  if (whole) {
+    pl.ctas = static_cast<int32_t>(jobs);
+    pl.step = static_cast<uint64_t>(len) << 32;
+  } else {
+    pl.step = (static_cast<uint64_t>(total) << 32) / pl.ctas;
+  }
+  pl.by_gs = Divisor::of(pl.gs);
+  pl.by_queries = Divisor::of(p.queries);
+  pl.by_seq_rows = Divisor::of(pl.seq_rows);
+  pl.by_pairs = Divisor::of(pl.pairs);
+  pl.by_len = Divisor::of(pl.len);
+  pl.by_heads = Divisor::of(p.Hq);
+  pl.by_per_kv = Divisor::of(G / pl.gs);  // row groups of a KV head
+  pl.inv_step = static_cast<float>(4294967296.0 / static_cast<double>(pl.step));
+  const int64_t least = std::max<int64_t>(1, total / pl.ctas - 1);
+  pl.parts = pl.ctas == 1 ? 1 : static_cast<int32_t>((len - 1 + least - 1) / least + 1);
+  pl.cut = 0;
+  if (pl.step != static_cast<uint64_t>(len) << 32)
+    for (int c = 1; c < pl.ctas && !pl.cut; ++c) pl.cut = pl.share(c) % pl.len != 0;
+  return true;
 }
 
 bool device_sms(int& sms) {
@@ -757,17 +1134,16 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 size_t part_lse_offset(const csbp_prefix_problem& p, const Plan& pl) {
   const size_t rows = static_cast<size_t>(p.batch) * p.queries * p.Hq;
-  return kStatusBytes + round256(pl.parts > 1 ? pl.parts * rows * p.d * 4 : 0);
+  return kStatusBytes + (pl.cut ? round256(pl.parts * rows * p.d * 4) : 0);
 }
 
 size_t workspace_bytes(const csbp_prefix_problem& p, const Plan& pl) {
   const size_t rows = static_cast<size_t>(p.batch) * p.queries * p.Hq;
-  return part_lse_offset(p, pl) + round256(pl.parts > 1 ? pl.parts * rows * 4 : 0);
+  return part_lse_offset(p, pl) + (pl.cut ? round256(pl.parts * rows * 4) : 0);
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, unsigned grid,
-                   cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, cudaStream_t stream) {
   using Lay = PrefixLayout<D>;
   // the shared-memory limit is a per-device attribute: set it once on each
   // device, and read the kernel's register count there
@@ -791,25 +1167,28 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, unsigned grid
   // allocation: refuse to launch instead
   if (launch_regs[dev] * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
   const int timed = timer_begin(13, stream);
-  prefix_kernel<D><<<grid, kThreads, Lay::kDynSmem, stream>>>(maps[0], maps[1], maps[2], maps[3],
+  prefix_kernel<D><<<p.plan.ctas, kThreads, Lay::kDynSmem, stream>>>(maps[0], maps[1], maps[2], maps[3],
                                                               p);
   e = cudaGetLastError();
   timer_end(timed, stream);
-  if (e != cudaSuccess || p.plan.parts == 1) return e;
+  if (e != cudaSuccess || !p.plan.cut) return e;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
-  const bool wide = rows <= 4096;  // a CTA per row
+  // few rows have many pieces (the keys were split to fill the GPU): more warps
+  // to a row, up to about 32 warps per SM in all
+  const int warps = rows <= 608 ? 8 : rows <= 8192 ? 2 : 1;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 7) / 8));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows * warps + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   const int joined = timer_begin(14, stream);
-  e = wide ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p)
-           : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p);
+  e = warps == 8   ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p)
+      : warps == 2 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 2>, p)
+                   : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p);
   timer_end(joined, stream);
   return e;
 }
@@ -835,8 +1214,8 @@ csbp_status validate(const csbp_prefix_problem* p) {
   if (p->Hq > lim || rows > lim / p->Hq || p->prefix_len > lim / p->Hkv ||
       static_cast<int64_t>(p->batch) * p->own_max > lim / p->Hkv)
     return CSBP_ERR_UNSUPPORTED;
-  // row and tile counts of a head group fit 32 bits
-  if (rows * (p->Hq / p->Hkv) > 0x3fffffff) return CSBP_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits
+  if (rows * p->Hq > 0x3fffffff) return CSBP_ERR_UNSUPPORTED;
   return CSBP_OK;
 }
 
@@ -889,7 +1268,8 @@ extern "C" size_t csbp_prefix_workspace_bytes(const csbp_prefix_problem* problem
   if (validate(problem) != CSBP_OK) return 0;
   int sms = 0;
   if (!device_sms(sms)) sms = 152;  // no GPU: the GB300's count
-  return workspace_bytes(*problem, make_plan(*problem, sms));
+  Plan pl{};
+  return make_plan(*problem, sms, pl) ? workspace_bytes(*problem, pl) : 0;
 }
 
 extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
@@ -905,14 +1285,9 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   const csbp_prefix_problem& p = *problem;
   int sms = 0;
   if (!device_sms(sms)) return CSBP_ERR_CUDA;
-  const Plan pl = make_plan(p, sms);
+  Plan pl{};
+  if (!make_plan(p, sms, pl)) return CSBP_ERR_UNSUPPORTED;
   if (ws_bytes < workspace_bytes(p, pl)) return CSBP_ERR_WORKSPACE;
-  const int64_t grid = static_cast<int64_t>(pl.n_groups) *
-                       (static_cast<int64_t>(pl.pairs) * pl.splits +
-                        static_cast<int64_t>(pl.own_pairs) * pl.own_splits);
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
-  if (grid > 0x7fffffff || rows / 8 >= 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
-
   CUtensorMap maps[4] = {};  // prefix K and V, own K and V
   if (p.prefix_len > 0 && (!kv_map(&maps[0], t, 1, p, p.prefix_len, 1) ||
                            !kv_map(&maps[1], t, 2, p, p.prefix_len, 1)))
@@ -932,7 +1307,6 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.prefix_len = p.prefix_len;
   a.own_max = p.own_max;
   a.Hq = p.Hq;
-  a.G = p.Hq / p.Hkv;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.q = static_cast<const __nv_bfloat16*>(t.t[0]);
@@ -945,7 +1319,7 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.part_lse = reinterpret_cast<float*>(ws + part_lse_offset(p, pl));
   a.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p.d == 128 ? launch<128>(maps, a, static_cast<unsigned>(grid), s)
-                                   : launch<64>(maps, a, static_cast<unsigned>(grid), s);
+  const cudaError_t e = p.d == 128 ? launch<128>(maps, a, s)
+                                   : launch<64>(maps, a, s);
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }
