@@ -268,7 +268,7 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
   const bool alternate = 2 * pair + 1 >= pl.row_tiles;
   const int np = (p.prefix_len + kTile - 1) / kTile;
   int own[2];
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     const int row0 = (2 * pair + (alternate ? 0 : s)) * kTile;
     const int rows = min(kTile, p.batch * pl.seq_rows - row0);
@@ -314,7 +314,7 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
     u.m1 = tiles_before(pl, np, all, x1);
     const int p0 = min(u.m0, np), p1 = min(u.m1, np);
     const int o0 = max(u.m0, np) - np, o1 = max(u.m1, np) - np;
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       if (alternate) {  // places of the list with the slot's parity
         u.t_pre[s] = p0 + ((p0 ^ s) & 1);
@@ -610,28 +610,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           // tile before.  Else PV_0, S_0, PV_1, S_1: each slot's softmax runs
           // under the other's MMAs.
           const bool apart = !((in0 && prev0) || (in1 && prev1));
-          if (!apart) {
-            ok = v_ready();
-            if (ok && prev0) ok = issue_pv(0, pst);
+          // (one copy of each group's code: the kernel's size costs time)
+          const bool pv = m > m0;
+#pragma unroll 1
+          for (int pass = 0; ok && pass < 2; ++pass) {
+            const bool with_pv = pv && (pass == 1) == apart;
+            const bool with_s = more && pass == 0;
+            if (with_pv) {
+              ok = v_ready();
+              if (ok && prev0) ok = issue_pv(0, pst);
+            }
+            if (ok && with_s) {
+              ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
+              if (ok && in0) ok = issue_s(0, st, 0);
+            }
+            if (ok && with_pv) {
+              if (prev1) ok = issue_pv(1, pst);
+              if (ok) umma_commit(&bars[Lay::bVEmpty + pst]);
+            }
+            if (ok && with_s) {
+              if (in1) ok = issue_s(1, st, q1);
+              if (ok) umma_commit(&bars[Lay::bKEmpty + st]);
+            }
+            if (!apart) break;
           }
-          if (ok && more)
-            ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
-          if (ok && in0) ok = issue_s(0, st, 0);
-          if (!apart) {
-            if (ok && prev1) ok = issue_pv(1, pst);
-            if (!ok) break;
-            umma_commit(&bars[Lay::bVEmpty + pst]);
-          }
-          if (ok && in1) ok = issue_s(1, st, q1);
           if (!ok) break;
-          if (more) umma_commit(&bars[Lay::bKEmpty + st]);
-          if (apart && m > m0) {
-            ok = v_ready();
-            if (ok && prev0) ok = issue_pv(0, pst);
-            if (ok && prev1) ok = issue_pv(1, pst);
-            if (!ok) break;
-            umma_commit(&bars[Lay::bVEmpty + pst]);
-          }
           prev0 = in0;
           prev1 = in1;
           if (more) ++j;
@@ -751,11 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kTile / 32; ++q) {
             const int c0 = q * 32;
-            if (__all_sync(0xffffffffu, hi <= c0)) {
-              dead |= 1u << q;
-#pragma unroll
-              for (int c = c0; c < c0 + 32; ++c) sv[c] = -INFINITY;
-            } else if (!__all_sync(0xffffffffu, hi >= c0 + 32)) {
+            if (__all_sync(0xffffffffu, hi <= c0)) dead |= 1u << q;
+            if (!__all_sync(0xffffffffu, hi >= c0 + 32)) {
 #pragma unroll
               for (int c = c0; c < c0 + 32; ++c) sv[c] = c < hi ? sv[c] : -INFINITY;
             }
@@ -996,6 +996,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (parts == 1) return;  // stored already
   float top = -INFINITY;
+#pragma unroll 1
   for (int k = lane; k < parts; k += 32)
     top = fmaxf(top, p.part_lse[static_cast<int64_t>(k) * rows + r]);
 #pragma unroll
@@ -1003,12 +1004,14 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
   const float ref = top == -INFINITY ? 0.f : top;
   Part acc{};
   float sum = 0.f;
+#pragma unroll 1
   for (int k0 = 0; k0 < parts; k0 += 32) {
     const float zk =
         k0 + lane < parts ? p.part_lse[static_cast<int64_t>(k0 + lane) * rows + r] : -INFINITY;
     const float w = expf(zk - ref);
     sum += w;
     const int n = min(32, parts - k0);
+#pragma unroll 1
     for (int k1 = warp % W; k1 < n; k1 += kBatch * W) {
       Part v[kBatch];
       float wk[kBatch];
