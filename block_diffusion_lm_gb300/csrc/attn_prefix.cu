@@ -6,7 +6,7 @@
 // group), flattened in that order; a row tile is 128 consecutive ones, so the
 // prefix K/V pass through the tensor cores once per 128 rows however they
 // divide into sequences, tokens and heads.  The softmax warps copy the tile's
-// rows into shared memory themselves (zeros below the last), which takes any
+// rows into shared memory themselves, which takes any
 // token or batch stride and any group size.
 //
 // Keys.  A row tile reads all prefix key tiles, then the own key tiles of each
@@ -127,7 +127,7 @@ struct PrefixParams {
   int32_t batch, queries, prefix_len, own_max, Hq, causal;
   float scale_log2;
   const __nv_bfloat16* q;
-  int64_t q_tok, q_bat;  // element strides
+  uint32_t q_tok, q_bat;  // strides in 16-byte units
   const int32_t* own_len;
   __nv_bfloat16* o;   // [batch][queries][Hq][d]
   float* lse;         // [batch][Hq][queries]
@@ -346,31 +346,31 @@ __device__ __forceinline__ Row row_at(const PrefixParams& p, int group, uint32_t
   return r;
 }
 
-// A warp's 32 Q rows, D / 8 lanes to a row: the lane's 16-byte chunks of them
-// (`mine`: element offset of the lane's own row, -1: none, zeros).
+// Its place in q, in 16-byte units.
 template <int D>
-struct QRows {
-  static constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+__device__ __forceinline__ uint32_t q_place(const PrefixParams& p, const Row& r) {
+  return r.b * p.q_bat + r.i * p.q_tok + r.h * (D / 8);
+}
+
+// A warp's 32 Q rows into the 128-byte-swizzled tile of 64-feature boxes, from
+// row `row0` on, D / 8 lanes to a row.  `mine`: place of the lane's own row in
+// q, in 16-byte units.
+template <int D>
+__device__ __forceinline__ void copy_q(const PrefixParams& p, uint32_t mine, uint8_t* tile,
+                                       int row0) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  const int lane = threadIdx.x & 31, chunk = lane % kLanes;
+  const uint4* src = reinterpret_cast<const uint4*>(p.q) + chunk;
+  uint8_t* dst = tile + (chunk >> 3) * (kTile * 128);
   uint4 v[kLanes];
-  __device__ __forceinline__ void load(const PrefixParams& p, int64_t mine) {
-    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int t = 0; t < kLanes; ++t) {
-      const int64_t src = __shfl_sync(0xffffffffu, mine, t * kAtOnce + lane / kLanes);
-      v[t] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + src) + lane % kLanes)
-                      : make_uint4(0, 0, 0, 0);
-    }
-  }
-  // into the 128-byte-swizzled tile of 64-feature boxes, from row `row0` on
-  __device__ __forceinline__ void store(uint8_t* tile, int row0) const {
-    const int lane = threadIdx.x & 31, chunk = lane % kLanes;
-    uint8_t* dst = tile + (chunk >> 3) * (kTile * 128);
+  for (int t = 0; t < kLanes; ++t)
+    v[t] = __ldg(src + __shfl_sync(0xffffffffu, mine, t * kAtOnce + lane / kLanes));
 #pragma unroll
-    for (int t = 0; t < kLanes; ++t)
-      *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + t * kAtOnce + lane / kLanes, chunk & 7)) =
-          v[t];
-  }
-};
+  for (int t = 0; t < kLanes; ++t)
+    *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + t * kAtOnce + lane / kLanes, chunk & 7)) =
+        v[t];
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -407,15 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a few us to answer all SMs at once.  The two halves of the CTA meet at
   // barrier 2 when the barriers and TMEM are there.
   if (warp >= 4) {
-    const int flat = 2 * first_pair * kTile + (static_cast<int>(threadIdx.x) - 128);
-    int64_t mine = -1;
-    if (flat < p.batch * p.plan.seq_rows && reached < share_end) {
-      const Row r = row_at(p, first_group, flat);
-      mine = r.b * p.q_bat + r.i * p.q_tok + static_cast<int64_t>(r.h) * D;
-    }
-    QRows<D> q;
-    q.load(p, mine);
-    q.store(smem + Lay::kQ + (warp >= 8 ? Lay::kTileBytes : 0), (warp & 3) * 32);
+    // (rows past the last are copies of it: finite, and never stored)
+    const int flat = min(2 * first_pair * kTile + static_cast<int>(threadIdx.x) - 128,
+                         p.batch * p.plan.seq_rows - 1);
+    copy_q<D>(p, q_place<D>(p, row_at(p, first_group, flat)),
+              smem + Lay::kQ + (warp >= 8 ? Lay::kTileBytes : 0), (warp & 3) * 32);
     fence_proxy_async_smem();
     asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
   } else {
@@ -675,10 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.causal) own_hi = min(own_hi, own_hi - p.queries + at.i + 1);
         if (u.m0 < u.m1 && (s == 0 || !u.alternate)) {
           if (k > 0) {  // the first one is there
-            QRows<D> q;
-            q.load(p, row_valid ? at.b * p.q_bat + at.i * p.q_tok + static_cast<int64_t>(at.h) * D
-                                : -1);
-            q.store(smem + Lay::kQ + s * Lay::kTileBytes, (warp & 3) * 32);
+            copy_q<D>(p, q_place<D>(p, at), smem + Lay::kQ + s * Lay::kTileBytes,
+                      (warp & 3) * 32);
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -885,10 +879,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             sw128_offset((warp & 3) * 32 + rr, chunk & 7));
           };
           const auto put = [&](int chunk, uint4 v) { *place(lane, chunk) = v; };
-          const auto store_rows = [&](uint8_t* out, int64_t pitch) {
+          const auto store_rows = [&](uint8_t* out, int pitch) {
             __syncwarp();
             const int chunk = lane & (kChunks - 1);
-            constexpr int kBatch = 8;
+            out += chunk * 16;
+            constexpr int kBatch = 4;
 #pragma unroll 1
             for (int r0 = lane / kChunks; r0 - lane / kChunks < n_rows; r0 += kBatch * kAtOnce) {
               uint4 v[kBatch];
@@ -901,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int t = 0; t < kBatch; ++t)
                 if (r0 + t * kAtOnce < n_rows)
-                  *reinterpret_cast<uint4*>(out + to[t] * pitch + chunk * 16) = v[t];
+                  *reinterpret_cast<uint4*>(out + static_cast<int64_t>(to[t]) * pitch) = v[t];
             }
             __syncwarp();
           };
@@ -937,15 +932,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
                                                     pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
                                                     pack_bf16x2(o[8 * k + 6], o[8 * k + 7])));
-              if (half) store_rows(reinterpret_cast<uint8_t*>(p.o), D * 2);
+              if (half == 0) continue;  // both halves fill the rows
             } else {
 #pragma unroll
               for (int k = 0; k < D / 8; ++k)
                 put(k, make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
                                   __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3])));
-              store_rows(reinterpret_cast<uint8_t*>(p.part_o + u.part * all * D) + half * (D * 2),
-                         D * 4);
             }
+            store_rows(u.direct ? reinterpret_cast<uint8_t*>(p.o)
+                                : reinterpret_cast<uint8_t*>(p.part_o + u.part * all * D) +
+                                      half * (D * 2),
+                       u.direct ? D * 2 : D * 4);
           }
         }
         if (row_valid) {
@@ -1286,6 +1283,8 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
     return CSBP_ERR_INVALID;
   if (ws_bytes < kStatusBytes) return CSBP_ERR_WORKSPACE;
   const csbp_prefix_problem& p = *problem;
+  // places in q are counted in 32 bits, in units of 16 bytes
+  if (t.bat[0] > (int64_t(1) << 34) / p.batch) return CSBP_ERR_UNSUPPORTED;
   int sms = 0;
   if (!device_sms(sms)) return CSBP_ERR_CUDA;
   Plan pl{};
@@ -1313,8 +1312,8 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.q = static_cast<const __nv_bfloat16*>(t.t[0]);
-  a.q_tok = t.tok[0];
-  a.q_bat = t.bat[0];
+  a.q_tok = static_cast<uint32_t>(t.tok[0] / 8);
+  a.q_bat = static_cast<uint32_t>(t.bat[0] / 8);
   a.own_len = in->own_len;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
