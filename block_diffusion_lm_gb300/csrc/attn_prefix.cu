@@ -80,8 +80,8 @@ struct Divisor {
     r.mul = static_cast<uint32_t>((((uint64_t(1) << r.shift) - d) << 32) / d + 1);
     return r;
   }
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-    return (__umulhi(mul, n) + n) >> shift;
+  __host__ __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (static_cast<uint32_t>((static_cast<uint64_t>(mul) * n) >> 32) + n) >> shift;
   }
 };
 
@@ -96,7 +96,7 @@ struct Plan {
   int32_t ctas;           // shares
   // the list: jobs of equal length in units of time, the first `len_prefix` of
   // each for its prefix tiles and the rest for the own tiles
-  uint32_t jobs, len, len_prefix, total;
+  uint32_t jobs, len, len_prefix, total, snap;
   // share length in 32.32 fixed point, and reciprocals that only guess or cut
   // the same way everywhere
   uint64_t step;
@@ -104,9 +104,13 @@ struct Plan {
   float inv_prefix, inv_own;
   Divisor by_gs, by_queries, by_seq_rows, by_pairs, by_len, by_heads, by_per_kv;
 
-  // start of share c
+  // start of share c; a cut that would leave a piece shorter than `snap` moves to
+  // the end of the job
   __host__ __device__ uint32_t share(uint32_t c) const {
-    return c >= static_cast<uint32_t>(ctas) ? total : static_cast<uint32_t>((c * step) >> 32);
+    if (c >= static_cast<uint32_t>(ctas)) return total;
+    const uint32_t x = static_cast<uint32_t>((c * step) >> 32);
+    const uint32_t start = by_len(x) * len, past = x - start;
+    return past < snap ? start : len - past < snap ? start + len : x;
   }
   // the share that holds place x of the list
   __host__ __device__ int share_of(uint32_t x) const {
@@ -1101,12 +1105,6 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
   pl.len_prefix = static_cast<uint32_t>(len_prefix);
   pl.inv_prefix = 1.f / static_cast<float>(len_prefix);
   pl.inv_own = len > len_prefix ? 1.f / static_cast<float>(len - len_prefix) : 0.f;
-  if (whole) {
-    pl.ctas = static_cast<int32_t>(jobs);
-    pl.step = static_cast<uint64_t>(len) << 32;
-  } else {
-    pl.step = (static_cast<uint64_t>(total) << 32) / pl.ctas;
-  }
   pl.by_gs = Divisor::of(pl.gs);
   pl.by_queries = Divisor::of(p.queries);
   pl.by_seq_rows = Divisor::of(pl.seq_rows);
@@ -1114,12 +1112,30 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
   pl.by_len = Divisor::of(pl.len);
   pl.by_heads = Divisor::of(p.Hq);
   pl.by_per_kv = Divisor::of(G / pl.gs);  // row groups of a KV head
+  pl.snap = 0;
+  if (whole) {
+    pl.ctas = static_cast<int32_t>(jobs);
+    pl.step = static_cast<uint64_t>(len) << 32;
+  } else {
+    // rounded up, so that a share that is a whole number of jobs ends with one
+    pl.step = ((static_cast<uint64_t>(total) << 32) + pl.ctas - 1) / pl.ctas;
+    pl.snap = static_cast<uint32_t>(std::min<int64_t>(kEnds, total / pl.ctas / 3));
+  }
   pl.inv_step = static_cast<float>(4294967296.0 / static_cast<double>(pl.step));
-  const int64_t least = std::max<int64_t>(1, total / pl.ctas - 1);
-  pl.parts = pl.ctas == 1 ? 1 : static_cast<int32_t>((len - 1 + least - 1) / least + 1);
+  // the most cuts inside one job
+  pl.parts = 1;
   pl.cut = 0;
-  if (pl.step != static_cast<uint64_t>(len) << 32)
-    for (int c = 1; c < pl.ctas && !pl.cut; ++c) pl.cut = pl.share(c) % pl.len != 0;
+  uint32_t job = 0;
+  for (int c = 1, parts = 1; !whole && c < pl.ctas; ++c) {
+    const uint32_t x = pl.share(c);
+    if (pl.by_len(x) != job) {
+      job = pl.by_len(x);
+      parts = 1;
+    }
+    if (x == job * pl.len) continue;
+    pl.cut = 1;
+    pl.parts = std::max(pl.parts, ++parts);
+  }
   return true;
 }
 
