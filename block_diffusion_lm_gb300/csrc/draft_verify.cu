@@ -262,12 +262,13 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(VerifyArgs a) {
   if (C > 1) cluster_arrive();
   const int64_t b = blockIdx.x / C;
   const int rank = static_cast<int>(blockIdx.x % C);
-  int n = a.drafts;
-  if (a.length) n = min(max(__ldg(a.length + b), 0), a.drafts);
+  const int32_t* token = a.token + b * a.drafts;
+  const int n = a.length ? min(max(__ldg(a.length + b), 0), a.drafts) : a.drafts;
+  const float r = __ldg(a.r + b);
   if (threadIdx.x == 0) sh.first_bad = n;
   __syncthreads();
-  const int32_t* token = a.token + b * a.drafts;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  // tokens past the n-th are looked up too, so that they do not wait for n
+  for (int i = threadIdx.x; i < a.drafts; i += kThreads) {
     const int x = __ldg(token + i);
     bool ok = false;
     if (x >= 0 && x < a.vocab) {
@@ -275,13 +276,12 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(VerifyArgs a) {
       const double qx = __ldg(a.q + b * a.q_batch + i * a.q_row + x);
       ok = static_cast<double>(__ldg(a.u + b * a.drafts + i)) * qx < px;
     }
-    if (!ok) atomicMin(&sh.first_bad, i);
+    if (!ok && i < n) atomicMin(&sh.first_bad, i);
   }
   __syncthreads();
   const int acc = sh.first_bad;
   const float* p = a.p + b * a.p_batch + acc * a.p_row;
   const float* q = acc < n ? a.q + b * a.q_batch + acc * a.q_row : nullptr;
-  const float r = __ldg(a.r + b);
   int next = draw<C>(p, q, a.vocab, r, rank, sh);
   if (next == kNoWeight && q) {  // p <= q everywhere, the same in all CTAs
     if (C > 1)
@@ -345,9 +345,17 @@ extern "C" csbp_status csbp_draft_verify(const csbp_verify_problem* problem, con
   a.length = length;
   a.accepted = accepted;
   a.out = out;
-  // one CTA reads about as fast as 1/100 of the GPU: a cluster per sequence
-  // once every thread of one CTA would have more than four loads of a row
-  const int ctas = c.vocab > 4 * 4 * kThreads ? kCluster : 1;
+  // A cluster per sequence as large as all sequences' CTAs still run at once
+  // (three to an SM), and with at least four 16-byte loads of a row per thread.
+  // At 96 sequences of a 131,072-token vocabulary 8 CTAs take two waves.
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return CSBP_ERR_CUDA;
+  int ctas = 1;
+  while (ctas < kCluster && static_cast<int64_t>(c.batch) * ctas * 2 <= 3 * sms &&
+         static_cast<int64_t>(c.vocab) >= 2 * ctas * 16 * kThreads)
+    ctas *= 2;
   if (static_cast<int64_t>(c.batch) * ctas > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
   cudaLaunchAttribute together{};
   together.id = cudaLaunchAttributeClusterDimension;
@@ -360,8 +368,10 @@ extern "C" csbp_status csbp_draft_verify(const csbp_verify_problem* problem, con
   cfg.attrs = &together;
   cfg.numAttrs = 1;
   const int timed = timer_begin(15, stream);
-  const cudaError_t e = ctas > 1 ? cudaLaunchKernelEx(&cfg, draft_verify_kernel<kCluster>, a)
-                                 : cudaLaunchKernelEx(&cfg, draft_verify_kernel<1>, a);
+  const cudaError_t e = ctas == 8   ? cudaLaunchKernelEx(&cfg, draft_verify_kernel<8>, a)
+                        : ctas == 4 ? cudaLaunchKernelEx(&cfg, draft_verify_kernel<4>, a)
+                        : ctas == 2 ? cudaLaunchKernelEx(&cfg, draft_verify_kernel<2>, a)
+                                    : cudaLaunchKernelEx(&cfg, draft_verify_kernel<1>, a);
   timer_end(timed, stream);
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }

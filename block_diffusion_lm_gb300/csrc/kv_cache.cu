@@ -152,63 +152,73 @@ __device__ __forceinline__ Codes16 encode16(const Values16& v, int byte) {
 }
 
 // NaN codes in the place of values that are not finite.
-__device__ __noinline__ Codes16 mark16(const Values16& v, Codes16 r) {
+__device__ __forceinline__ Codes16 mark16(const Values16& v, Codes16 r) {
+#pragma unroll
   for (int k = 0; k < 16; ++k)
     if ((v.w[k >> 1] >> (k & 1) * 16 & 0x7f80u) == 0x7f80u) r.w[k >> 2] |= 0x7fu << (k & 3) * 8;
   return r;
 }
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;
 
-// `L` lanes per row (2 .. 32, so that a group of 32 features is 2 lanes of one
-// row), 16 features a lane and step; all loads of K and V of up to kUnroll
-// steps are issued before the first is used: 32 lanes x 32 bytes x 4 in flight
-// per warp.  HBM bounds it: 3 + 1/32 bytes per value at 4 to 5 instructions per
-// value, about half the issue rate (one value at a time took 10 and was bound
-// by them: 154 us where this takes 105, 65,521 x 2 rows of 8 x 128).
-template <int L>
+// Layout of both kernels.  `L` lanes hold a row (2 .. 32, so that a group of 32
+// features is 2 lanes of one row), 16 features a lane and step; K or V by
+// blockIdx.y.  N pieces are in flight per lane, each issued before the first is
+// used: steps of one row where a row takes several (R = 1), else R = N rows, so
+// that short rows do not make short threads.  HBM bounds it: 3 + 1/32 bytes per
+// value, at 4 to 5 instructions per value, about half the issue rate (one value
+// at a time took 10 and was bound by them).
+template <int L, int R>
+struct Shape {
+  static constexpr int kRows = kThreads / L * R;  // of a CTA
+  static constexpr int kPieces = R == 1 ? 2 : R;
+};
+
+template <int L, int R>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
-  constexpr int kRows = kThreads / L;
-  const int lane = threadIdx.x % L;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
-  const Row r = row_of(a, first, threadIdx.x / L);
+  constexpr int N = Shape<L, R>::kPieces;
+  const int lane = threadIdx.x % L, kv = blockIdx.y;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * Shape<L, R>::kRows;
+  Row r[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) r[t] = row_of(a, first, threadIdx.x / L + t * (kThreads / L));
   const int chunks = a.row_values >> 4;  // a multiple of 2
+  const __nv_bfloat16* src = kv ? a.src[1] : a.src[0];
+  const int64_t bat = kv ? a.bat[1] : a.bat[0], tok = kv ? a.tok[1] : a.tok[0];
+  uint8_t* codes = kv ? a.codes[1] : a.codes[0];
+  uint8_t* scales = kv ? a.scales[1] : a.scales[0];
   // the lanes of a row decide alike, those of a warp need not: no early return
   // before the shuffles
-  for (int c0 = 0; c0 < chunks; c0 += L * kUnroll) {
-    Values16 v[2][kUnroll];
+  for (int c0 = lane; c0 - lane < chunks; c0 += R == 1 ? L * N : L) {
+    Values16 v[N];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const __nv_bfloat16* src = a.src[kv] + r.b * a.bat[kv] + r.i * a.tok[kv];
-#pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        const int c = c0 + t * L + lane;
-        v[kv][t] = r.takes_part && c < chunks ? load16(src + c * 16, a.wide) : Values16{};
-      }
+    for (int t = 0; t < N; ++t) {
+      const Row& w = r[R == 1 ? 0 : t];
+      const int c = R == 1 ? c0 + t * L : c0;
+      v[t] = w.takes_part && c < chunks ? load16(src + w.b * bat + w.i * tok + c * 16, a.wide)
+                                        : Values16{};
     }
-    const int64_t slot = r.takes_part ? slot_of(a, r) : -1;
+    int64_t slot[R];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      uint8_t* codes = a.codes[kv] + slot * a.row_values;
-      uint8_t* scales = a.scales[kv] + slot * (a.row_values / kGroup);
+    for (int t = 0; t < R; ++t) slot[t] = r[t].takes_part ? slot_of(a, r[t]) : -1;
 #pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        const int c = c0 + t * L + lane;
-        uint32_t top = top16(v[kv][t]);
-        const bool bad = __any_sync(0xffffffffu, top >= 0x7f80u);
-        const Values16 x = bad ? finite16(v[kv][t]) : v[kv][t];
-        if (bad) top = top16(x);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        // 448 = 1.75 x 2^8: e = exponent - 8, one more above 1.75
-        const int byte = max(0, static_cast<int>((top + 0x1fu) >> 7) - 8);
-        Codes16 out = encode16(x, byte);
-        if (bad) out = mark16(v[kv][t], out);
-        if (slot >= 0 && c < chunks) {
-          *reinterpret_cast<uint4*>(codes + c * 16) =
-              make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]);
-          if ((c & 1) == 0) scales[c >> 1] = static_cast<uint8_t>(byte);
-        }
+    for (int t = 0; t < N; ++t) {
+      const int64_t to = slot[R == 1 ? 0 : t];
+      const int c = R == 1 ? c0 + t * L : c0;
+      uint32_t top = top16(v[t]);
+      const bool bad = __any_sync(0xffffffffu, top >= 0x7f80u);
+      const Values16 x = bad ? finite16(v[t]) : v[t];
+      if (bad) top = top16(x);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      // 448 = 1.75 x 2^8: e = exponent - 8, one more above 1.75
+      const int byte = max(0, static_cast<int>((top + 0x1fu) >> 7) - 8);
+      Codes16 out = encode16(x, byte);
+      if (bad) out = mark16(v[t], out);
+      if (to >= 0 && c < chunks) {
+        *reinterpret_cast<uint4*>(codes + to * a.row_values + c * 16) =
+            make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]);
+        if ((c & 1) == 0)
+          scales[to * (a.row_values / kGroup) + (c >> 1)] = static_cast<uint8_t>(byte);
       }
     }
   }
@@ -232,39 +242,43 @@ __device__ __forceinline__ Values16 decode16(const uint4& codes, uint32_t byte) 
   return r;
 }
 
-// The same lanes and steps as the write.
-template <int L>
+template <int L, int R>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {
-  constexpr int kRows = kThreads / L;
-  const int lane = threadIdx.x % L;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
-  const Row r = row_of(a, first, threadIdx.x / L);
-  if (!r.takes_part) return;
+  constexpr int N = Shape<L, R>::kPieces;
+  const int lane = threadIdx.x % L, kv = blockIdx.y;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * Shape<L, R>::kRows;
+  Row r[R];
+  int64_t slot[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    r[t] = row_of(a, first, threadIdx.x / L + t * (kThreads / L));
+    slot[t] = r[t].takes_part ? slot_of(a, r[t]) : -1;
+  }
   const int chunks = a.row_values >> 4;
-  const int64_t slot = slot_of(a, r);
-  for (int c0 = 0; c0 < chunks; c0 += L * kUnroll) {
-    uint4 v[2][kUnroll];
-    uint32_t sb[2][kUnroll];
+  const uint8_t* codes = kv ? a.codes[1] : a.codes[0];
+  const uint8_t* scales = kv ? a.scales[1] : a.scales[0];
+  __nv_bfloat16* dst = kv ? a.dst[1] : a.dst[0];
+  const int64_t bat = kv ? a.bat[1] : a.bat[0], tok = kv ? a.tok[1] : a.tok[0];
+  for (int c0 = lane; c0 < chunks; c0 += R == 1 ? L * N : L) {
+    uint4 v[N];
+    uint32_t sb[N];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        const int c = c0 + t * L + lane;
-        v[kv][t] = make_uint4(0, 0, 0, 0);
-        sb[kv][t] = 255;  // NaN, for a row that has no place
-        if (slot >= 0 && c < chunks) {
-          v[kv][t] = __ldcs(reinterpret_cast<const uint4*>(a.codes[kv] + slot * a.row_values) + c);
-          sb[kv][t] = __ldg(a.scales[kv] + slot * (a.row_values / kGroup) + (c >> 1));
-        }
+    for (int t = 0; t < N; ++t) {
+      const int64_t from = slot[R == 1 ? 0 : t];
+      const int c = R == 1 ? c0 + t * L : c0;
+      v[t] = make_uint4(0, 0, 0, 0);
+      sb[t] = 255;  // NaN, for a row that has no place
+      if (from >= 0 && c < chunks) {
+        v[t] = __ldcs(reinterpret_cast<const uint4*>(codes + from * a.row_values) + c);
+        sb[t] = __ldg(scales + from * (a.row_values / kGroup) + (c >> 1));
       }
+    }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      __nv_bfloat16* dst = a.dst[kv] + r.b * a.bat[kv] + r.i * a.tok[kv];
-#pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        const int c = c0 + t * L + lane;
-        if (c < chunks) store16(dst + c * 16, decode16(v[kv][t], sb[kv][t]), a.wide);
-      }
+    for (int t = 0; t < N; ++t) {
+      const Row& w = r[R == 1 ? 0 : t];
+      const int c = R == 1 ? c0 + t * L : c0;
+      if (w.takes_part && c < chunks)
+        store16(dst + w.b * bat + w.i * tok + c * 16, decode16(v[t], sb[t]), a.wide);
     }
   }
 }
@@ -320,36 +334,38 @@ csbp_status make_args(const csbp_kv_cache* c, const csbp_cache_rows* r, const vo
   return CSBP_OK;
 }
 
-// One launch over all rows with the fewest lanes per row that cover it in one
-// step (so that short rows share a warp), at most a warp.
-template <bool kWrite>
+template <int L, int R, bool kWrite>
 csbp_status launch(const CacheArgs& a, void* stream) {
-  const int chunks = a.row_values >> 4;
-  const int lanes = chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
-  const int64_t per = kThreads / lanes;
+  constexpr int64_t per = Shape<L, R>::kRows;
   const int64_t grid = (static_cast<int64_t>(a.batch) * a.rows + per - 1) / per;
   if (grid > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid), 2);  // K, V
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned g = static_cast<unsigned>(grid);
   const int timed = timer_begin(kWrite ? 11 : 12, stream);
-  if (lanes == 2)
-    kWrite ? cache_write_kernel<2><<<g, kThreads, 0, s>>>(a)
-           : cache_read_kernel<2><<<g, kThreads, 0, s>>>(a);
-  else if (lanes == 4)
-    kWrite ? cache_write_kernel<4><<<g, kThreads, 0, s>>>(a)
-           : cache_read_kernel<4><<<g, kThreads, 0, s>>>(a);
-  else if (lanes == 8)
-    kWrite ? cache_write_kernel<8><<<g, kThreads, 0, s>>>(a)
-           : cache_read_kernel<8><<<g, kThreads, 0, s>>>(a);
-  else if (lanes == 16)
-    kWrite ? cache_write_kernel<16><<<g, kThreads, 0, s>>>(a)
-           : cache_read_kernel<16><<<g, kThreads, 0, s>>>(a);
+  if (kWrite)
+    cache_write_kernel<L, R><<<g, kThreads, 0, s>>>(a);
   else
-    kWrite ? cache_write_kernel<32><<<g, kThreads, 0, s>>>(a)
-           : cache_read_kernel<32><<<g, kThreads, 0, s>>>(a);
+    cache_read_kernel<L, R><<<g, kThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   timer_end(timed, stream);
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
+}
+
+// The fewest lanes that hold a row in one step (so that short rows share a
+// warp), at most a warp; several rows per lane where one step is all.  Few
+// rows take one row per lane all the same: then latency counts.
+template <bool kWrite>
+csbp_status launch(const CacheArgs& a, void* stream) {
+  constexpr int kRows = kWrite ? 2 : 4;  // (four would hold a write at 95 registers)
+  const int chunks = a.row_values >> 4;
+  const bool few = static_cast<int64_t>(a.batch) * a.rows * chunks < 152 * 4 * kThreads;
+  if (chunks > 32 || (few && chunks > 16)) return launch<32, 1, kWrite>(a, stream);
+  if (few) return launch<16, 1, kWrite>(a, stream);
+  if (chunks <= 2) return launch<2, kRows, kWrite>(a, stream);
+  if (chunks <= 4) return launch<4, kRows, kWrite>(a, stream);
+  if (chunks <= 8) return launch<8, kRows, kWrite>(a, stream);
+  if (chunks <= 16) return launch<16, kRows, kWrite>(a, stream);
+  return launch<32, kRows, kWrite>(a, stream);
 }
 
 }  // namespace
