@@ -651,9 +651,10 @@ def _layout(fn, problem, tensors, check):
     return made
 
 
-def _run(fn, dev, stream, *args):
+def _run(fn, dev, stream, tensors, *args):
     """Call the library on `stream` (default: device `dev`'s current one) with
-    that device current."""
+    that device current.  The memory of `tensors` stays theirs until a stream
+    that was named has done with them."""
     import torch
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
@@ -661,6 +662,9 @@ def _run(fn, dev, stream, *args):
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
         raw = stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     f = getattr(_lib, fn)
     if torch._C._cuda_getDevice() == dev:
         st = f(*args, raw)
@@ -734,7 +738,9 @@ class QuantCache:
         r.start = start.data_ptr()
         if count is not None:
             r.count = count.data_ptr()
-        _run(fn, dev, stream, self._ref, ctypes.byref(r), k.data_ptr(), v.data_ptr())
+        _run(fn, dev, stream, (k, v, table, start, count, self.k, self.v, self.k_scale,
+                               self.v_scale),
+             self._ref, ctypes.byref(r), k.data_ptr(), v.data_ptr())
 
     def write(self, k, v, table, start, count=None, stream=None):
         """Quantise bf16 k, v [batch][rows][Hkv][d] (token and batch strides
@@ -784,7 +790,7 @@ class PrefixAttention:
         if n == 0:
             raise CsbpError("csbp_prefix_workspace_bytes", -1)
         self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
-        self.device = device
+        self.device = self.ws.device
 
     def alloc_outputs(self):
         import torch
@@ -796,7 +802,7 @@ class PrefixAttention:
     def forward(self, q, k_prefix, v_prefix, k_own, v_own, own_len, out=None, stream=None):
         o, lse = out if out is not None else self.alloc_outputs()
         attn_prefix(self.problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, self.ws,
-                    stream)
+                    stream, made_here=out is None)
         return o, lse
 
     def check(self, stream=None):
@@ -808,8 +814,9 @@ def prefix_workspace_bytes(problem: PrefixProblem) -> int:
 
 
 def attn_prefix(problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, workspace,
-                stream=None):
-    import torch
+                stream=None, made_here=False):
+    """csbp_attn_prefix.  `made_here`: o, lse and workspace are this module's own
+    (their layout is known; the device is the workspace's)."""
     p = problem
     if not p.prefix_len:
         k_prefix = v_prefix = None
@@ -817,6 +824,7 @@ def attn_prefix(problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, w
         k_own = v_own = own_len = None
 
     def check():
+        import torch
         c = _Call("csbp_attn_prefix")
         pre = (p.prefix_len, p.Hkv, p.d)
         mine = (p.batch, p.own_max, p.Hkv, p.d)
@@ -837,7 +845,9 @@ def attn_prefix(problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, w
                              tuple(x[2] for x in s)), c.device())
 
     lib()
-    inp, dev = _layout("csbp_attn_prefix", bytes(p),
+    outputs = (workspace.device,) if made_here else ()
+    inp, dev = _layout("csbp_attn_prefix", (bytes(p), outputs),
+                       (q, k_prefix, v_prefix, k_own, v_own, own_len) if made_here else
                        (q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, workspace), check)
     inp = PrefixInputs.from_buffer_copy(inp)
     inp.q = q.data_ptr()
@@ -848,8 +858,10 @@ def attn_prefix(problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, w
         inp.k_own = k_own.data_ptr()
         inp.v_own = v_own.data_ptr()
         inp.own_len = own_len.data_ptr()
-    _run("csbp_attn_prefix", dev, stream, ctypes.byref(p), ctypes.byref(inp), o.data_ptr(),
-         lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _run("csbp_attn_prefix", dev, stream,
+         (q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, workspace),
+         ctypes.byref(p), ctypes.byref(inp), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+         workspace.numel())
 
 
 def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
@@ -908,7 +920,8 @@ def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
     prob, dev = _layout("csbp_draft_verify", None, (p, q, token, u, r, length, accepted, tokens),
                         check)
     if prob is not None:
-        _run("csbp_draft_verify", dev, stream, ctypes.byref(prob), p.data_ptr(),
+        _run("csbp_draft_verify", dev, stream,
+             (p, q, token, u, r, length, accepted, tokens), ctypes.byref(prob), p.data_ptr(),
              q.data_ptr() if K else None, token.data_ptr() if K else None,
              u.data_ptr() if K else None, r.data_ptr(),
              None if length is None else length.data_ptr(), accepted.data_ptr(),
