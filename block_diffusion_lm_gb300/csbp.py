@@ -572,8 +572,8 @@ class VocabCrossEntropy:
 # ----------------------------------------------------------------- generation
 class _Call:
     """Argument checks of the generation operators: dtype, shape and layout of
-    every tensor first, then (in `stream`) that all of them are on one CUDA
-    device, which the call makes current."""
+    every tensor first, then (in `device`) that all of them are on one CUDA
+    device."""
 
     def __init__(self, fn):
         self.fn = fn
@@ -700,6 +700,8 @@ class QuantCache:
         self._tensors = list(zip(("k", "v", "k_scale", "v_scale"), storage))
         ptrs = [c.tensor(n, t, torch.uint8, s)
                 for (n, t), s in zip(self._tensors, (code, code, scale, scale))]
+        if any(t.device != self.k.device for t in storage):
+            raise ValueError("QuantCache: the storage tensors must be on one device")
         self.Hkv, self.d = Hkv, d
         self.struct = KvCache(pages, page_size, Hkv, d, *ptrs)
         self._ref = ctypes.byref(self.struct)

@@ -11,6 +11,7 @@
 
 #include "csbp.h"
 #include "csbp_internal.h"
+#include "generate_internal.h"
 
 namespace csbp {
 
@@ -315,7 +316,7 @@ extern "C" csbp_status csbp_kernel_timing_read(double* fwd_ms, int32_t* n_fwd, d
 }
 
 extern "C" csbp_status csbp_kernel_timing_read_kind(int32_t kind, double* ms, int32_t* n) {
-  if (kind < 0 || kind >= kTimerKinds) return CSBP_ERR_INVALID;
+  if (kind < 0 || kind >= kAllTimerKinds) return CSBP_ERR_INVALID;
   KernelTimer& t = timer();
   std::lock_guard<std::mutex> lk(t.mu);
   double sum = 0.0;

@@ -36,11 +36,10 @@ bool bwd_windowed(const csbp_problem* p);
 // Kernel timing (csbp_kernel_timing): kinds 0 fwd, 1 bwd, 2 CE logits GEMM,
 // 3 CE row kernel, 4 CE dH GEMM, 5 CE dW GEMM, 6 LSE merge, 7 backward
 // preprocess, 8 dQ convert, 9 dK/dV convert (windowed backward), 10 fp8
-// E4M3 input decode, 11 cache write, 12 cache read, 13 prefix attention,
-// 14 prefix partial merge, 15 draft verification.
+// E4M3 input decode.
 // timer_begin returns the pair index to close with timer_end, or -1 when not
 // recording.
-constexpr int kTimerKinds = 16;
+constexpr int kTimerKinds = 11;
 int timer_begin(int kind, void* stream);
 void timer_end(int i, void* stream);
 
@@ -50,10 +49,6 @@ void timer_end(int i, void* stream);
 // if `swizzle128`; out-of-range elements read as zero.
 bool encode_map_2d(void* map, bool f32, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
-// The same for a 3-D bf16 tensor (innermost dimension first): strides[i] is the
-// byte stride of dimension i + 1; box[0] = 64 elements, 128-byte swizzle.
-bool encode_map_3d(void* map, const void* base, const uint64_t dims[3], const uint64_t strides[2],
-                   const uint32_t box[3]);
 int classify_tile(int q_stream, int64_t qt, int k_stream, int64_t kt, int64_t L, int64_t M,
                   int64_t T);
 

@@ -10,6 +10,7 @@
 
 #include <cstdint>
 
+#include "bf16_bits.cuh"
 #include "csbp_generate.h"
 #include "csbp_internal.h"
 
@@ -101,11 +102,6 @@ __device__ __forceinline__ void store16(void* p, const Values16& v, bool wide) {
   }
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
