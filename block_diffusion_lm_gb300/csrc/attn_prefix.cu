@@ -31,7 +31,8 @@
 // when a row's maximum grows by more than 2^8.  Warps without a row of their
 // own take no part.  Own rows past a sequence's end may hold NaN: their scores
 // are masked, and the softmax warps clear their V rows in shared memory before
-// the MMA that would multiply them by P = 0.
+// the MMA that would multiply them by P = 0.  Where another masked V is not
+// finite, the rows it reached are summed again at the end of the piece.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +41,6 @@
 #include <cmath>
 #include <cstdint>
 
-#include "bf16_bits.cuh"
 #include "csbp_generate.h"
 #include "csbp_internal.h"
 #include "device_once.h"
@@ -134,6 +134,8 @@ struct PrefixParams {
   float scale_log2;
   const __nv_bfloat16* q;
   uint32_t q_tok, q_bat;  // strides in 16-byte units
+  const __nv_bfloat16 *k_prefix, *v_prefix, *k_own, *v_own;
+  int64_t tok[4], bat[4];  // element strides of those four
   const int32_t* own_len;
   __nv_bfloat16* o;   // [batch][queries][Hq][d]
   float* lse;         // [batch][Hq][queries]
@@ -160,7 +162,6 @@ struct Unit {
   // n_own own tiles from t_own on, in steps of 1 (alternate: 2)
   int n_pre[2], t_pre[2], n_own[2], t_own[2];
   int keys[2][kTile];       // own keys of each sequence
-  int bad[2][kTile];        // 1: an own V of the sequence is not finite
   int upto[2][kTile + 1];   // own key tiles of the sequences before it
 
   // Which slots read the m-th key tile of the list, and its number among the
@@ -184,6 +185,11 @@ struct Unit {
       t = x < 2 * both ? x >> 1 : x - both;
     }
     in1 = !in0;
+  }
+  // Place in the list of slot s's own tile t.
+  __device__ __forceinline__ int place(int s, int t) const {
+    const int both = min(own[0], own[1]);
+    return np + (alternate ? t : t < both ? 2 * t + s : t + both);
   }
   // Own tiles of slot s among the first x of the list's own tiles.
   __device__ __forceinline__ int own_before(int s, int x) const {
@@ -222,9 +228,7 @@ struct PrefixLayout {
   static constexpr int bKEmpty = bKFull + kStages;
   static constexpr int bVFull = bKEmpty + kStages;
   static constexpr int bVEmpty = bVFull + kStages;
-  static constexpr int bVOwn = bVEmpty + kStages;   // [stage] own tiles: load issued
-  static constexpr int bVClean = bVOwn + kStages;   // [stage] and fit for the MMA
-  static constexpr int bSFull = bVClean + kStages;  // [2] per slot
+  static constexpr int bSFull = bVEmpty + kStages;  // [2] per slot
   static constexpr int bPFull = bSFull + 2;         // [2] (the slot's softmax warps)
   static constexpr int bPvDone = bPFull + 2;        // [2]
   static constexpr int bMerge = bPvDone + 2;        // slot 1's (max, sum) are in shared memory
@@ -294,7 +298,6 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
       }
       if (k < seqs) {
         u.keys[s][k] = keys;
-        u.bad[s][k] = 0;
         u.upto[s][k] = own[s] + sum - n;
       }
       own[s] += __shfl_sync(0xffffffffu, sum, 31);
@@ -377,6 +380,50 @@ __device__ __forceinline__ void copy_q(const PrefixParams& p, uint32_t mine, uin
         v[t];
 }
 
+// acc += sum_j 2^(scale q.k_j - ref) v_j over keys [from, to) of one head, by a
+// whole warp, lane l with features l D / 32 ..; 8 keys in flight.
+template <int D>
+__device__ __forceinline__ void walk_keys(const float (&q)[D / 32], float (&acc)[D / 32],
+                                          const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                          int64_t k_tok, int64_t v_tok, int from, int to,
+                                          float scale, float ref) {
+  constexpr int kN = D / 32, kBatch = 8;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int j0 = from; j0 < to; j0 += kBatch) {
+    float s[kBatch];
+    __nv_bfloat162 vv[kBatch][kN / 2];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const int j = min(j0 + t, to - 1);
+      const __nv_bfloat162* kr = reinterpret_cast<const __nv_bfloat162*>(k + j * k_tok) + lane * (kN / 2);
+      const __nv_bfloat162* vr = reinterpret_cast<const __nv_bfloat162*>(v + j * v_tok) + lane * (kN / 2);
+      s[t] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kN / 2; ++c) {
+        const float2 x = __bfloat1622float2(kr[c]);
+        vv[t][c] = vr[c];
+        s[t] = fmaf(q[2 * c], x.x, fmaf(q[2 * c + 1], x.y, s[t]));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      if (j0 + t >= to) break;
+      const float w = exp2f(fmaf(s[t], scale, -ref));
+#pragma unroll
+      for (int c = 0; c < kN / 2; ++c) {
+        const float2 x = __bfloat1622float2(vv[t][c]);
+        acc[2 * c] = fmaf(w, x.x, acc[2 * c]);
+        acc[2 * c + 1] = fmaf(w, x.y, acc[2 * c + 1]);
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
@@ -432,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(&bars[Lay::bMerge], 4);
       mbar_init(&bars[Lay::bJoined], 4);
-      // producer, issuer, own V's warp and eight softmax warps
-      mbar_init(&bars[Lay::bUnitEmpty], 11);
-      mbar_init(&bars[Lay::bUnitEmpty + 1], 11);
+      // producer, issuer and eight softmax warps
+      mbar_init(&bars[Lay::bUnitEmpty], 10);
+      mbar_init(&bars[Lay::bUnitEmpty + 1], 10);
       *abort_flag = 0;
       fence_mbarrier_init();
     }
@@ -510,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           load(Lay::kV, Lay::bVFull, prefix ? &tm_vp : &tm_vo, st, x, tile, z);
           ++nv;
-          if (!prefix) mbar_arrive(&bars[Lay::bVOwn + st]);
         }
         if (ok) mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
       }
@@ -533,72 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         make_unit(p, reached, share_end, unit_at(k));
         if (lane == 0) mbar_arrive(&bars[Lay::bUnitFull + (k & 1)]);
       }
-    } else if (warp == 3) {
-      // ===================== own V tiles, made fit for the MMA
-      // An MMA multiplies every row's P by every V of the tile, so V must be
-      // finite where P is 0 for being masked: rows past a sequence's end are
-      // cleared, and so is a V that is not finite while other sequences share
-      // the row tile (`bad` then makes its own sequence's rows NaN).
-      int j = 0;             // key tiles so far
-      uint32_t own_uses = 0;  // bit st: parity of the own tiles that stage st held
-      for (int k = 0; ok; ++k) {
-        ok = mbar_wait_warp(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
-        if (!ok) break;
-        Unit& u = unit_at(k);
-        if (!u.valid) break;
-        const int from = max(u.m0, u.np), to = u.m1;
-        for (int m = from; m < to; ++m) {
-          const int jm = j + (m - u.m0), st = jm % kStages;
-          // the load's own barrier only once it is this tile's turn: this warp
-          // skips the prefix tiles, whose phases it would take for its own
-          ok = mbar_wait_warp(&bars[Lay::bVOwn + st], (own_uses >> st) & 1, p.status, abort_flag) &&
-               mbar_wait_warp(&bars[Lay::bVFull + st], (jm / kStages) & 1, p.status, abort_flag);
-          if (!ok) break;
-          own_uses ^= 1u << st;
-          bool prefix, in0, in1;
-          int tile;
-          u.at(m, prefix, tile, in0, in1);
-          const int s = u.alternate || in0 ? 0 : 1;
-          const int q = u.sequence(s, tile);
-          const int v_rows = min(kTile, u.keys[s][q] - (tile - u.upto[s][q]) * kTile);
-          uint4* v = reinterpret_cast<uint4*>(smem + Lay::kV + st * Lay::kTileBytes);
-          // 16-byte chunks of a 64-feature box: row r has 8 r .. 8 r + 7
-          const bool look = u.seqs[s] > 1;
-          uint32_t top = 0;
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c, v += kTile * 8) {
-            if (look)
-#pragma unroll 4
-              for (int i = lane; i < v_rows * 8; i += 32) {
-                const uint4 x = v[i];
-                top = max_u16x2(top, x.x & 0x7fff7fffu);
-                top = max_u16x2(top, x.y & 0x7fff7fffu);
-                top = max_u16x2(top, x.z & 0x7fff7fffu);
-                top = max_u16x2(top, x.w & 0x7fff7fffu);
-              }
-            for (int i = v_rows * 8 + lane; i < kTile * 8; i += 32) v[i] = make_uint4(0, 0, 0, 0);
-          }
-          if (__any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= 0x7f80u)) {
-            uint16_t* x = reinterpret_cast<uint16_t*>(smem + Lay::kV + st * Lay::kTileBytes);
-#pragma unroll 1
-            for (int i = lane; i < kTile * D; i += 32)
-              if ((x[i] & 0x7f80u) == 0x7f80u) x[i] = 0;
-            if (lane == 0) u.bad[s][q] = 1;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[Lay::bVClean + st]);
-        }
-        j += u.m1 - u.m0;
-        if (ok && lane == 0) mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
-      }
     } else if (warp == 1 && lane == 0) {
       // ===================== MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
       int npv[2] = {0, 0};      // PVs issued per slot
       int nq0 = 0, nq1 = 0;     // Q tiles taken
-      uint32_t clean = 0;       // bit st: parity of the own tiles that stage st held
       bool fresh[2] = {};       // no PV of this piece yet: the next one overwrites O
       // S_s = Q K^T of Q tile sq and ring stage st into slot s's S columns
       auto issue_s = [&](int s, int st, int sq) -> bool {
@@ -653,12 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fresh[0] = fresh[1] = true;
         bool prev0 = false, prev1 = false;
         int st = 0, pst = 0;
-        auto v_ready = [&](int m) {  // V of tile m, the one before
-          if (!mbar_wait(&bars[Lay::bVFull + pst], ((j - 1) / kStages) & 1, p.status, abort_flag))
-            return false;
-          if (m < np) return true;
-          clean ^= 1u << pst;  // own tiles only: a phase of its own
-          return mbar_wait(&bars[Lay::bVClean + pst], (~clean >> pst) & 1, p.status, abort_flag);
+        auto v_ready = [&] {  // of the tile before
+          return mbar_wait(&bars[Lay::bVFull + pst], ((j - 1) / kStages) & 1, p.status, abort_flag);
         };
         // Step m issues S of tile m and PV of tile m - 1; the last one PV only.
         for (int m = m0; m <= m1; ++m) {
@@ -683,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool with_pv = pv && (pass == 1) == apart;
             const bool with_s = more && pass == 0;
             if (with_pv) {
-              ok = v_ready(m - 1);
+              ok = v_ready();
               if (ok && prev0) ok = issue_pv(0, pst);
             }
             if (ok && with_s) {
@@ -720,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t colO = Lay::kColO + s * D;
     const float sl2 = p.scale_log2;
     int n_mine = 0, n_other = 0;  // key tiles of this and the other slot so far
+    int j0 = 0;                   // key tiles of the pieces before
     int n_joined = 0;             // pieces that both slots worked on
     for (int k = 0; ok; ++k) {
       ok = mbar_wait_warp(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
@@ -755,12 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       for (int t = 0; t < n_tiles; ++t, y = t == n_pre ? u.t_own[s] : y + step) {
         const bool prefix = t < n_pre;
-        // this row reads columns [0, hi) of the tile
-        int tile = y;
+        // this row reads columns [0, hi) of the tile; v_rows of its keys exist
+        int tile = y, v_rows = kTile;
         int left = p.prefix_len;
         if (!prefix) {
           const int q = u.sequence(sl, y);
           tile -= u.upto[sl][q];
+          v_rows = u.keys[sl][q] - tile * kTile;
           left = q == my_seq && row_valid ? own_hi : 0;
         }
         const int hi = min(left - tile * kTile, kTile);
@@ -773,12 +757,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after_sync();
+        const auto clear_v = [&]() -> bool {
+          // the rest of the V tile may hold NaN, and P = 0 would not keep it out
+          const int j = j0 + u.place(s, y) - u.m0, st = j % kStages;
+          if (!mbar_wait_warp(&bars[Lay::bVFull + st], (j / kStages) & 1, p.status, abort_flag))
+            return false;
+          const int warps = (rows + 31) / 32;
+          uint8_t* v = smem + Lay::kV + st * Lay::kTileBytes;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          // 16-byte chunks [v_rows x 8, 128 x 8) of each 64-feature box
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll 1
+            for (int k = v_rows * 8 + (warp & 3) * 32 + lane; k < kTile * 8; k += warps * 32)
+              *reinterpret_cast<uint4*>(v + c * Lay::kBoxBytes + k * 16) = zero;
+          fence_proxy_async_smem();
+          return true;
+        };
         if (__all_sync(0xffffffffu, hi <= 0)) {  // another sequence's keys: P = 0
           float zero[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) zero[c] = 0.f;
           tmem_st32(tmem + lane_base + colS, zero);
           tmem_st32(tmem + lane_base + colS + 32, zero);
+          if (v_rows < kTile && !clear_v()) {
+            ok = false;
+            break;
+          }
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
@@ -860,6 +865,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float rs0, rs1;
         f2_unpack(rs2, rs0, rs1);
         l += rs0 + rs1;
+        if (v_rows < kTile && !clear_v()) {
+          ok = false;
+          break;
+        }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
@@ -868,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_mine = n_tiles > 0;
       n_mine += n_tiles;
       n_other += u.n_pre[1 - s] + u.n_own[1 - s];
+      j0 += u.m1 - u.m0;
       if (ok && any_mine)
         ok = mbar_wait_warp(&bars[Lay::bPvDone + s], (n_mine - 1) & 1, p.status, abort_flag);
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, joined, slot 1's
@@ -898,17 +908,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && has_rows && !(u.alternate && s == 1)) {
         tc_fence_after_sync();
+        // l is 0 without any key, NaN with a score that is
+        const float inv_l = l == 0.f ? 0.f : 1.f / l;
+        w0 = any_mine ? w0 * inv_l : 0.f;
+        w1 *= inv_l;
+        const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         // the row again: kept over the loop above it would cost registers there
         int own_row = u.row0[s] + (row_valid ? row : 0);
         asm volatile("" : "+r"(own_row));
         const Row at = row_at(p, u.group, own_row);
         const int r = row_valid ? static_cast<int>(at.token) * p.Hq + at.h : -1;
-        // l is 0 without any key, NaN with a score that is
-        float inv_l = l == 0.f ? 0.f : 1.f / l;
-        if (l != 0.f && u.bad[s][at.b - u.seq0[s]]) inv_l = NAN;
-        w0 = any_mine ? w0 * inv_l : 0.f;
-        w1 *= inv_l;
-        const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         const int64_t all = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
         if (u.direct || __any_sync(0xffffffffu, l != 0.f)) {
           // The warp's rows, 2 D bytes of each at a time (D / 2 fp32 columns or
@@ -944,6 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           };
+          float finite = 0.f;  // NaN once an element is not finite
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const uint32_t col = half * (D / 2);
@@ -969,6 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < D / 2; ++k) o[k] = fmaf(o1[k], w1, o[k]);
             }
+#pragma unroll
+            for (int k = 0; k < D / 2; ++k) finite = fmaf(o[k], 0.f, finite);
             if (u.direct) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
@@ -987,6 +999,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 : reinterpret_cast<uint8_t*>(p.part_o + u.part * all * D) +
                                       half * (D * 2),
                        u.direct ? D * 2 : D * 4);
+          }
+          // The MMA multiplies a row's P = 0 by masked keys too, those of other
+          // sequences in its tile and later ones of its own, and 0 times an
+          // infinity or NaN among their V is NaN.  Rows that are not finite where
+          // that can be are summed again over the keys they read alone, the
+          // maximum and sum being right.
+          const int sl = u.alternate ? 0 : s;
+          const bool masked = (u.seqs[sl] > 1 || p.causal) && u.m1 > max(u.m0, u.np);
+          uint32_t again = __ballot_sync(0xffffffffu, masked && row_valid && finite != finite);
+          while (again) {
+            const int rr = __ffs(again) - 1;
+            again &= again - 1;
+            const float top = __shfl_sync(0xffffffffu, m_ref, rr);
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float inv = __shfl_sync(0xffffffffu, inv_l, rr);
+            const int end = __shfl_sync(0xffffffffu, own_hi, rr);
+            const int to = __shfl_sync(0xffffffffu, r, rr);
+            const Row x = row_at(p, u.group, u.row0[s] + (warp & 3) * 32 + rr);
+            constexpr int kN = D / 32;
+            float q[kN], acc[kN];
+            const __nv_bfloat16* qr = p.q + static_cast<int64_t>(q_place<D>(p, x)) * 8 + lane * kN;
+#pragma unroll
+            for (int c = 0; c < kN; ++c) {
+              q[c] = __bfloat162float(qr[c]);
+              acc[c] = 0.f;
+            }
+            const int64_t head = static_cast<int64_t>(p.plan.by_per_kv(u.group)) * D;
+            walk_keys<D>(q, acc, p.k_prefix + head, p.v_prefix + head, p.tok[0], p.tok[1],
+                         min(u.m0, u.np) * kTile,
+                         min(p.prefix_len, min(u.m1, u.np) * kTile), p.scale_log2, ref);
+            // the piece's part of the sequence's own tiles
+            const int sq = x.b - u.seq0[sl], before = u.upto[sl][sq];
+            const int o0 = u.alternate ? max(u.m0, u.np) - u.np : u.t_own[s];
+            const int o1 = u.alternate ? max(u.m1, u.np) - u.np : o0 + u.n_own[s];
+            walk_keys<D>(q, acc, p.k_own + x.b * p.bat[2] + head, p.v_own + x.b * p.bat[3] + head,
+                         p.tok[2], p.tok[3], max(o0 - before, 0) * kTile,
+                         min(end, max(o1 - before, 0) * kTile), p.scale_log2, ref);
+#pragma unroll
+            for (int c = 0; c < kN; ++c) {
+              const int64_t at_c = static_cast<int64_t>(to) * D + lane * kN + c;
+              if (u.direct)
+                p.o[at_c] = __float2bfloat16_rn(acc[c] * inv);
+              else
+                p.part_o[u.part * all * D + at_c] = acc[c] * inv;
+            }
           }
         }
         if (row_valid) {
@@ -1370,6 +1427,12 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.q = static_cast<const __nv_bfloat16*>(t.t[0]);
   a.q_tok = static_cast<uint32_t>(t.tok[0] / 8);
   a.q_bat = static_cast<uint32_t>(t.bat[0] / 8);
+  const __nv_bfloat16** kv[4] = {&a.k_prefix, &a.v_prefix, &a.k_own, &a.v_own};
+  for (int i = 0; i < 4; ++i) {
+    *kv[i] = static_cast<const __nv_bfloat16*>(t.t[i + 1]);
+    a.tok[i] = t.tok[i + 1];
+    a.bat[i] = t.bat[i + 1];
+  }
   a.own_len = in->own_len;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;

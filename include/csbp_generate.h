@@ -98,8 +98,9 @@ csbp_status csbp_cache_read(const csbp_kv_cache* cache, const csbp_cache_rows* r
  *   causal = 1  own keys j <= c - queries + i for query i (the queries are
  *               the last tokens of the c)
  * O = softmax(scale Q K^T) V over those keys and LSE the natural log of the
- * softmax denominator.  A query that reads no key has O = 0, LSE = -inf.
- * Own rows at and past c may hold anything, NaN included.                 */
+ * softmax denominator.  A query that reads no key has O = 0, LSE = -inf.  A key
+ * that a query does not read has no part in its result, whatever it holds (own
+ * rows at and past c, later keys, other sequences' keys), NaN included.     */
 typedef struct {
   int32_t batch, queries;       /* >= 1                                     */
   int32_t prefix_len, own_max;  /* >= 0                                     */
@@ -112,7 +113,8 @@ typedef struct {
  * [prefix_len][Hkv][d] (NULL allowed when prefix_len is 0), k_own and v_own
  * [batch][own_max][Hkv][d] and own_len int32 [batch], 4-byte aligned (all
  * three NULL allowed when own_max is 0).  Strides as in csbp_inputs, in that
- * order; the batch strides of the prefix are not read.                    */
+ * order; the batch strides of the prefix are not read.  batch x the batch
+ * stride of q stays within 2^34 elements, batch x queries x Hq below 2^30.  */
 typedef struct {
   const void *q, *k_prefix, *v_prefix, *k_own, *v_own;
   const int32_t* own_len;

@@ -309,27 +309,42 @@ def test_rows_past_the_end_may_hold_anything(bad, causal):
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("n,causal", [(1, False), (2, True), (40, False)])
 def test_a_sequence_that_is_not_finite_stays_alone(value, n, causal):
-    """K or V of one sequence that are not finite leave every other sequence's
-    rows as they were, to the bit, also where they share row tiles."""
+    """K or V of one sequence that are not finite do not reach any other
+    sequence's rows, also where they share row tiles."""
     B, Lp, S = 9, 150, 200
     lens = [200, 3, 129, 64, 200, 0, 128, 77, 200]
     t = attn_inputs(B, n, Lp, S, 8, 2, 128, 12)
     a = csbp.PrefixAttention(B, n, Lp, S, 8, 2, 128, causal=causal)
-    want = [x.clone() for x in a.forward(**t, own_len=i32(lens))]
     others = [b for b in range(B) if b != 4]
+    rest = {k: x if k.endswith("prefix") else x[others] for k, x in t.items()}
     for name in ("v_own", "k_own"):
         bad = {k: x.clone() for k, x in t.items()}
         bad[name][4, 131, 1, 5] = value
         o, lse = a.forward(**bad, own_len=i32(lens))
         a.check()
-        assert torch.equal(o[others], want[0][others]), name
-        assert torch.equal(lse[others], want[1][others]), name
+        check_attn((o[others], lse[others]), rest, [lens[b] for b in others], causal, 128 ** -0.5)
         # the sequence's own heads of that KV head do not hide it (its last query
         # reads key 131 in every case); an infinite K may give a score of -inf,
         # which weighs nothing
         if name == "v_own" or value != value:
             assert not torch.isfinite(o[4, -1, 4:].float()).all(-1).any(), name
         assert torch.isfinite(o[4, :, :4].float()).all()
+
+
+def test_causal_queries_do_not_see_later_values():
+    """The last key's V is read by the last query only, whatever it holds."""
+    B, n, Lp, S = 3, 6, 300, 140
+    lens = [140, 9, 128]
+    t = attn_inputs(B, n, Lp, S, 4, 2, 64, 13)
+    a = csbp.PrefixAttention(B, n, Lp, S, 4, 2, 64, causal=True)
+    clean = {k: x.clone() for k, x in t.items()}
+    for b, c in enumerate(lens):
+        t["v_own"][b, c - 1] = float("nan")
+        clean["v_own"][b, c - 1] = 0.0
+    o, lse = a.forward(**t, own_len=i32(lens))
+    assert torch.isnan(o[:, -1].float()).all()
+    check_attn((torch.cat([o[:, :-1], a.forward(**clean, own_len=i32(lens))[0][:, -1:]], 1), lse),
+               clean, lens, True, 0.125)
 
 
 def test_attention_strides():
