@@ -31,7 +31,8 @@
 // when a row's maximum grows by more than 2^8.  Warps without a row of their
 // own take no part.  Own rows past a sequence's end may hold NaN: their scores
 // are masked, and the softmax warps clear their V rows in shared memory before
-// the MMA that would multiply them by P = 0.
+// the MMA that would multiply them by P = 0.  Where another masked V is not
+// finite, the rows it reached are summed again at the end of the share.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -39,12 +40,13 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "csbp_generate.h"
 #include "csbp_internal.h"
 #include "device_once.h"
+#include "generate_internal.h"
 #include "mbar_spin.cuh"
-#include "bf16_bits.cuh"
 #include "pair_math.cuh"
 #include "ptx_sm100.cuh"
 
@@ -133,6 +135,8 @@ struct PrefixParams {
   float scale_log2;
   const __nv_bfloat16* q;
   uint32_t q_tok, q_bat;  // strides in 16-byte units
+  const __nv_bfloat16 *k_prefix, *v_prefix, *k_own, *v_own;
+  int64_t tok[4], bat[4];  // element strides of those four
   const int32_t* own_len;
   __nv_bfloat16* o;   // [batch][queries][Hq][d]
   float* lse;         // [batch][Hq][queries]
@@ -159,7 +163,6 @@ struct Unit {
   // n_own own tiles from t_own on, in steps of 1 (alternate: 2)
   int n_pre[2], t_pre[2], n_own[2], t_own[2];
   int keys[2][kTile];       // own keys of each sequence
-  int bad[2][kTile];        // 1: an own V of the sequence is not finite
   int upto[2][kTile + 1];   // own key tiles of the sequences before it
 
   // Which slots read the m-th key tile of the list, and its number among the
@@ -226,8 +229,7 @@ struct PrefixLayout {
   static constexpr int bKEmpty = bKFull + kStages;
   static constexpr int bVFull = bKEmpty + kStages;
   static constexpr int bVEmpty = bVFull + kStages;
-  static constexpr int bVClean = bVEmpty + kStages; // [stage] own tiles: fit for the MMA
-  static constexpr int bSFull = bVClean + kStages;  // [2] per slot
+  static constexpr int bSFull = bVEmpty + kStages;  // [2] per slot
   static constexpr int bPFull = bSFull + 2;         // [2] (the slot's softmax warps)
   static constexpr int bPvDone = bPFull + 2;        // [2]
   static constexpr int bMerge = bPvDone + 2;        // slot 1's (max, sum) are in shared memory
@@ -297,7 +299,6 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
       }
       if (k < seqs) {
         u.keys[s][k] = keys;
-        u.bad[s][k] = 0;
         u.upto[s][k] = own[s] + sum - n;
       }
       own[s] += __shfl_sync(0xffffffffu, sum, 31);
@@ -380,6 +381,146 @@ __device__ __forceinline__ void copy_q(const PrefixParams& p, uint32_t mine, uin
         v[t];
 }
 
+// acc += sum_j 2^(scale q.k_j - ref) v_j over keys [from, to) of one head, for
+// two rows at once: 16 lanes to a row, lane l with features (l % 16) D / 16 .. (k
+// and v point there); 4 keys in flight.  The rows' ranges may differ.
+template <int D>
+__device__ __forceinline__ void walk_keys(const float (&q)[D / 16], float (&acc)[D / 16],
+                                          const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                          int64_t k_tok, int64_t v_tok, int from, int to,
+                                          float scale, float ref) {
+  constexpr int kN = D / 16, kBatch = 4;
+  using Chunk = std::conditional_t<D == 128, uint4, uint2>;
+  int most = to - from;
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+#pragma unroll 1
+  for (int j0 = 0; j0 < most; j0 += kBatch) {
+    float s[kBatch];
+    Chunk vv[kBatch];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      s[t] = 0.f;
+      const int64_t j = max(min(from + j0 + t, to - 1), 0);
+      const Chunk kk = __ldg(reinterpret_cast<const Chunk*>(k + j * k_tok));
+      vv[t] = __ldg(reinterpret_cast<const Chunk*>(v + j * v_tok));
+      const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&kk);
+#pragma unroll
+      for (int e = 0; e < kN / 2; ++e) {
+        const float2 y = __bfloat1622float2(x[e]);
+        s[t] = fmaf(q[2 * e], y.x, fmaf(q[2 * e + 1], y.y, s[t]));
+      }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const float w = exp2f(fmaf(s[t], scale, -ref));
+      if (from + j0 + t >= to) continue;  // a copy of the last key
+      const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&vv[t]);
+#pragma unroll
+      for (int e = 0; e < kN / 2; ++e) {
+        const float2 y = __bfloat1622float2(x[e]);
+        acc[2 * e] = fmaf(w, y.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, y.y, acc[2 * e + 1]);
+      }
+    }
+  }
+}
+
+// Barrier 3: the eight softmax warps.
+__device__ __forceinline__ void softmax_warps_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_warps_and(bool x) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 3, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return all != 0;
+}
+
+// The rows of a share's pieces that came out not finite where masked keys can
+// have done that, summed again over the keys that they read alone; their LSE
+// is right (a score is masked before it is used).  By the softmax warps, when
+// the whole share is done and nobody waits for them.  A wave of pieces whose
+// every row is summed again takes 8 us a key (D = 64); it is there to be right.
+template <int D>
+__device__ __forceinline__ void sum_again(const PrefixParams& p, uint32_t at, uint32_t end, Unit& u) {
+  constexpr int kN = D / 16;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4;
+  const int f0 = (lane & 15) * kN;
+  const int64_t all = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
+  while (true) {
+    if (warp == 0) make_unit(p, at, end, u);
+    softmax_warps_sync();
+    if (!u.valid) return;
+    const int64_t head = static_cast<int64_t>(p.plan.by_per_kv(u.group)) * D + f0;
+#pragma unroll 1
+    for (int i = warp; i < kTile; i += 8) {  // two rows
+      const int s = i >= kTile / 2, row = 2 * i - s * kTile + (lane >> 4);
+      const bool valid = row < u.rows[s] && !(u.alternate && s == 1) &&
+                         (u.seqs[s] > 1 || p.causal) && u.m1 > max(u.m0, u.np);
+      const Row x = row_at(p, u.group, u.row0[s] + min(row, max(u.rows[s] - 1, 0)));
+      const int64_t r = static_cast<int64_t>(x.token) * p.Hq + x.h;
+      const int64_t place = r * D + f0;
+      bool need = false;
+      float lse = 0.f;
+      if (valid) {
+        lse = u.direct ? p.lse[(static_cast<int64_t>(x.b) * p.Hq + x.h) * p.queries + x.i]
+                       : p.part_lse[u.part * all + r];
+        if (lse > -INFINITY) {  // it has keys, and no score is NaN
+          float finite = 0.f;
+#pragma unroll
+          for (int c = 0; c < kN; ++c)
+            finite = fmaf(u.direct ? __bfloat162float(p.o[place + c])
+                                   : p.part_o[u.part * all * D + place + c],
+                          0.f, finite);
+          need = finite != finite;
+        }
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, need);
+      if (found == 0) continue;
+      need = (found >> (lane & 16)) & 0xffffu;
+      float q[kN], acc[kN];
+      const __nv_bfloat16* qr = p.q + static_cast<int64_t>(q_place<D>(p, x)) * 8 + f0;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        q[c] = __bfloat162float(qr[c]);
+        acc[c] = 0.f;
+      }
+      const float ref = lse * 1.4426950408889634f;
+      const int pre0 = min(u.m0, u.np) * kTile;
+      const int pre1 = min(p.prefix_len, min(u.m1, u.np) * kTile);
+      walk_keys<D>(q, acc, p.k_prefix + head, p.v_prefix + head, p.tok[0], p.tok[1], pre0,
+                   need ? pre1 : pre0, p.scale_log2, ref);
+      // the piece's part of the sequence's own tiles
+      const int sq = x.b - u.seq0[s], before = u.upto[s][sq];
+      const int o0 = u.alternate ? max(u.m0, u.np) - u.np : u.t_own[s];
+      const int o1 = u.alternate ? max(u.m1, u.np) - u.np : o0 + u.n_own[s];
+      int hi = u.keys[s][sq];
+      if (p.causal) hi = min(hi, hi - p.queries + x.i + 1);
+      const int own0 = max(o0 - before, 0) * kTile;
+      walk_keys<D>(q, acc, p.k_own + x.b * p.bat[2] + head, p.v_own + x.b * p.bat[3] + head,
+                   p.tok[2], p.tok[3], own0, need ? min(hi, max(o1 - before, 0) * kTile) : own0,
+                   p.scale_log2, ref);
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        if (!need) continue;
+        if (u.direct)
+          p.o[place + c] = __float2bfloat16_rn(acc[c]);
+        else
+          p.part_o[u.part * all * D + place + c] = acc[c];
+      }
+    }
+    softmax_warps_sync();
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
@@ -435,11 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(&bars[Lay::bMerge], 4);
       mbar_init(&bars[Lay::bJoined], 4);
-      // producer, issuer, V's warp and eight softmax warps
-      mbar_init(&bars[Lay::bUnitEmpty], 11);
-      mbar_init(&bars[Lay::bUnitEmpty + 1], 11);
-      // the MMAs that read a V tile and the warp that looked it over
-      for (int st = 0; st < kStages; ++st) mbar_init(&bars[Lay::bVEmpty + st], 2);
+      // producer, issuer and eight softmax warps
+      mbar_init(&bars[Lay::bUnitEmpty], 10);
+      mbar_init(&bars[Lay::bUnitEmpty + 1], 10);
       *abort_flag = 0;
       fence_mbarrier_init();
     }
@@ -458,75 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     setmaxnreg_dec<kRegsLow>();
     if (warp == 0 && lane == 0) {
-      // ===================== TMA producer
-      int nk = 0, nv = 0;  // K / V tiles whose loads were issued
-      int early = 0;       // of the first piece, before its own lengths are known
-      // Keys that are read once need not push anything else out of L2, this
-      // kernel's own code above all
-      uint64_t policy;
-      if (p.plan.pairs == 1)
-        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-      else
-        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-      auto load = [&](int buf, int full, const CUtensorMap* map, int st, int x, int tile, int z) {
-        mbar_arrive_expect_tx(&bars[full + st], Lay::kTileBytes);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d_hint(smem + buf + st * Lay::kTileBytes + c * Lay::kBoxBytes, map,
-                           &bars[full + st], x + c * 64, tile * kTile, z, policy);
-      };
-      if (reached < share_end) {
-        const int np = (p.prefix_len + kTile - 1) / kTile;
-        const uint32_t x0 = reached - first_job * p.plan.len;
-        const int p0 = prefix_before(p.plan, np, x0);
-        const int p1 = prefix_before(p.plan, np, min(share_end - first_job * p.plan.len, p.plan.len));
-        early = min(kStages, p1 - p0);
-        const int x = p.plan.by_per_kv(first_group) * D;
-        for (; nk < early; ++nk, ++nv) {
-          load(Lay::kK, Lay::bKFull, &tm_kp, nk, x, p0 + nk, 0);
-          load(Lay::kV, Lay::bVFull, &tm_vp, nk, x, p0 + nk, 0);
-        }
-      }
-      for (int k = 0; ok; ++k) {
-        ok = mbar_wait(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
-        if (!ok) break;
-        const Unit& u = unit_at(k);
-        if (!u.valid) break;
-        const int x = p.plan.by_per_kv(u.group) * D;
-        const int m1 = u.m1;
-        for (int m = u.m0 + (k == 0 ? early : 0); m < m1; ++m) {
-          const int st = nk % kStages, use = nk / kStages;
-          bool prefix, in0, in1;
-          int tile, z = 0;
-          u.at(m, prefix, tile, in0, in1);
-          if (!prefix) {
-            const int s = u.alternate || in0 ? 0 : 1;
-            const int q = u.sequence(s, tile);
-            tile -= u.upto[s][q];
-            z = u.seq0[s] + q;
-          }
-          if (use > 0)
-            ok = mbar_wait(&bars[Lay::bKEmpty + st], (use - 1) & 1, p.status, abort_flag);
-          if (!ok) break;
-          load(Lay::kK, Lay::bKFull, prefix ? &tm_kp : &tm_ko, st, x, tile, z);
-          ++nk;
-          if (use > 0)
-            ok = mbar_wait(&bars[Lay::bVEmpty + st], (use - 1) & 1, p.status, abort_flag);
-          if (!ok) break;
-          load(Lay::kV, Lay::bVFull, prefix ? &tm_vp : &tm_vo, st, x, tile, z);
-          ++nv;
-        }
-        if (ok) mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
-      }
-      if (!ok) {
-        // drain: wait (ignoring the abort flag) for the loads already issued
-        for (int j = max(0, nk - kStages); j < nk; ++j)
-          mbar_wait(&bars[Lay::bKFull + j % kStages], (j / kStages) & 1, nullptr, nullptr,
-                    200000000ull);
-        for (int j = max(0, nv - kStages); j < nv; ++j)
-          mbar_wait(&bars[Lay::bVFull + j % kStages], (j / kStages) & 1, nullptr, nullptr,
-                    200000000ull);
-      }
     } else if (warp == 2) {
       // ===================== pieces of the share, one or two ahead
       for (int k = 0; ok && (k == 0 || unit_at(k - 1).valid); ++k) {
@@ -537,62 +607,115 @@ __global__ void __launch_bounds__(kThreads, 1)
         make_unit(p, reached, share_end, unit_at(k));
         if (lane == 0) mbar_arrive(&bars[Lay::bUnitFull + (k & 1)]);
       }
-    } else if (warp == 3) {
-      // ===================== own V tiles, made fit for the MMA
-      // An MMA multiplies every row's P by every V of the tile, so V must be
-      // finite where P is 0 for being masked: rows past a sequence's end are
-      // cleared, and so is a V that is not finite while other sequences share
-      // the row tile (`bad` then makes its own sequence's rows NaN).
+    } else if (warp == 1 && lane == 0) {
+      // ===================== MMA issuer
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
+      int npv[2] = {0, 0};      // PVs issued per slot
+      int nq0 = 0, nq1 = 0;     // Q tiles taken
+      bool fresh[2] = {};       // no PV of this piece yet: the next one overwrites O
+      // S_s = Q K^T of Q tile sq and ring stage st into slot s's S columns
+      auto issue_s = [&](int s, int st, int sq) -> bool {
+        if (npv[s] > 0 &&
+            !mbar_wait_spin(&bars[Lay::bPvDone + s], (npv[s] - 1) & 1, p.status, abort_flag))
+          return false;  // its last PV still reads the P held there
+        tc_fence_after_sync();
+        const uint64_t q_desc =
+            sdesc_sw128(smem_u32(smem + Lay::kQ + sq * Lay::kTileBytes), 16, 1024);
+        const uint64_t k_desc =
+            sdesc_sw128(smem_u32(smem + Lay::kK + st * Lay::kTileBytes), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * Lay::kBoxBytes + (k & 3) * 32;
+          umma_bf16_ss(tmem + s * 128, sdesc_step(q_desc, off), sdesc_step(k_desc, off), idesc_s,
+                       k > 0 ? 1u : 0u);
+        }
+        umma_commit(&bars[Lay::bSFull + s]);
+        return true;
+      };
+      // O_s += P_s V of ring stage st, P_s (bf16 pairs) in slot s's S columns
+      auto issue_pv = [&](int s, int st) -> bool {
+        if (!mbar_wait_spin(&bars[Lay::bPFull + s], npv[s] & 1, p.status, abort_flag)) return false;
+        tc_fence_after_sync();
+        const uint64_t vb = sdesc_sw128(smem_u32(smem + Lay::kV + st * Lay::kTileBytes),
+                                        Lay::kBoxBytes, 1024);  // V, MN-major B
+        const uint32_t acc0 = fresh[s] ? 0u : 1u;
+        fresh[s] = false;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_bf16_ts(tmem + Lay::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(vb, k * 2048),
+                       idesc_pv, k > 0 ? 1u : acc0);
+        umma_commit(&bars[Lay::bPvDone + s]);
+        ++npv[s];
+        return true;
+      };
       int j = 0;  // key tiles so far
       for (int k = 0; ok; ++k) {
-        ok = mbar_wait_warp(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
+        ok = mbar_wait(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
         if (!ok) break;
-        Unit& u = unit_at(k);
+        const Unit& u = unit_at(k);
         if (!u.valid) break;
-        for (int m = u.m0; m < u.m1; ++m, ++j) {
-          const int st = j % kStages;
-          ok = mbar_wait_warp(&bars[Lay::bVFull + st], (j / kStages) & 1, p.status, abort_flag);
-          if (!ok) break;
-          if (m >= u.np) {
-            bool prefix, in0, in1;
-            int tile;
-            u.at(m, prefix, tile, in0, in1);
-            const int s = u.alternate || in0 ? 0 : 1;
-            const int q = u.sequence(s, tile);
-            const int v_rows = min(kTile, u.keys[s][q] - (tile - u.upto[s][q]) * kTile);
-            uint4* v = reinterpret_cast<uint4*>(smem + Lay::kV + st * Lay::kTileBytes);
-            // 16-byte chunks of a 64-feature box: row r has 8 r .. 8 r + 7
-            const bool look = u.seqs[s] > 1;
-            uint32_t top = 0;
+        const int m0 = u.m0, m1 = u.m1, np = u.np, own0 = u.own[0], own1 = u.own[1];
+        const int both = 2 * min(own0, own1);
+        const bool alternate = u.alternate;
+        mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
+        if (m0 >= m1) continue;
+        const int q1 = alternate ? 0 : 1;  // Q tile of slot 1
+        ok = mbar_wait(&bars[Lay::bQFull], nq0++ & 1, p.status, abort_flag);
+        if (ok && q1) ok = mbar_wait(&bars[Lay::bQFull + 1], nq1++ & 1, p.status, abort_flag);
+        if (!ok) break;
+        fresh[0] = fresh[1] = true;
+        bool prev0 = false, prev1 = false;
+        int st = 0, pst = 0;
+        auto v_ready = [&] {  // of the tile before
+          return mbar_wait(&bars[Lay::bVFull + pst], ((j - 1) / kStages) & 1, p.status, abort_flag);
+        };
+        // Step m issues S of tile m and PV of tile m - 1; the last one PV only.
+        for (int m = m0; m <= m1; ++m) {
+          const bool more = m < m1;
+          pst = st;
+          st = j % kStages;
+          // as in Unit::at
+          const bool in0 = more && (alternate ? !(m & 1)
+                                    : m < np  ? true
+                                    : m - np < both ? !((m - np) & 1)
+                                                    : own0 > own1);
+          const bool in1 = more && ((!alternate && m < np) || !in0);
+          // A tile that goes to the other slot than the one before (or none):
+          // S_0, S_1, PV_0, PV_1, so that this S runs under the softmax of the
+          // tile before.  Else PV_0, S_0, PV_1, S_1: each slot's softmax runs
+          // under the other's MMAs.
+          const bool apart = !((in0 && prev0) || (in1 && prev1));
+          // (one copy of each group's code: the kernel's size costs time)
+          const bool pv = m > m0;
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c, v += kTile * 8) {
-              if (look)
-#pragma unroll 4
-                for (int i = lane; i < v_rows * 8; i += 32) {
-                  const uint4 x = v[i];
-                  top = max_u16x2(top, x.x & 0x7fff7fffu);
-                  top = max_u16x2(top, x.y & 0x7fff7fffu);
-                  top = max_u16x2(top, x.z & 0x7fff7fffu);
-                  top = max_u16x2(top, x.w & 0x7fff7fffu);
-                }
-              for (int i = v_rows * 8 + lane; i < kTile * 8; i += 32) v[i] = make_uint4(0, 0, 0, 0);
+          for (int pass = 0; ok && pass < 2; ++pass) {
+            const bool with_pv = pv && (pass == 1) == apart;
+            const bool with_s = more && pass == 0;
+            if (with_pv) {
+              ok = v_ready();
+              if (ok && prev0) ok = issue_pv(0, pst);
             }
-            if (__any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= 0x7f80u)) {
-              uint16_t* x = reinterpret_cast<uint16_t*>(smem + Lay::kV + st * Lay::kTileBytes);
-#pragma unroll 1
-              for (int i = lane; i < kTile * D; i += 32)
-                if ((x[i] & 0x7f80u) == 0x7f80u) x[i] = 0;
-              if (lane == 0) u.bad[s][q] = 1;
+            if (ok && with_s) {
+              ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
+              if (ok && in0) ok = issue_s(0, st, 0);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[Lay::bVClean + st]);
+            if (ok && with_pv) {
+              if (prev1) ok = issue_pv(1, pst);
+              if (ok) umma_commit(&bars[Lay::bVEmpty + pst]);
+            }
+            if (ok && with_s) {
+              if (in1) ok = issue_s(1, st, q1);
+              if (ok) umma_commit(&bars[Lay::bKEmpty + st]);
+            }
+            if (!apart) break;
           }
-          if (lane == 0) mbar_arrive(&bars[Lay::bVEmpty + st]);
+          if (!ok) break;
+          prev0 = in0;
+          prev1 = in1;
+          if (more) ++j;
         }
-        if (ok && lane == 0) mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
       }
-    } else if (warp == 1 && lane == 0) {
       // drain every MMA this thread issued before the CTA may free TMEM
       umma_commit(&bars[Lay::bDrain]);
       mbar_wait(&bars[Lay::bDrain], 0, nullptr, nullptr, 500000000ull);
@@ -607,7 +730,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t colO = Lay::kColO + s * D;
     const float sl2 = p.scale_log2;
     int n_mine = 0, n_other = 0;  // key tiles of this and the other slot so far
+    int j0 = 0;                   // key tiles of the pieces before
     int n_joined = 0;             // pieces that both slots worked on
+    bool redo = false;            // a row may have taken in keys that it does not read
     for (int k = 0; ok; ++k) {
       ok = mbar_wait_warp(&bars[Lay::bUnitFull + (k & 1)], (k >> 1) & 1, p.status, abort_flag);
       if (!ok) break;
@@ -642,12 +767,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       for (int t = 0; t < n_tiles; ++t, y = t == n_pre ? u.t_own[s] : y + step) {
         const bool prefix = t < n_pre;
-        // this row reads columns [0, hi) of the tile
-        int tile = y;
+        // this row reads columns [0, hi) of the tile; v_rows of its keys exist
+        int tile = y, v_rows = kTile;
         int left = p.prefix_len;
         if (!prefix) {
           const int q = u.sequence(sl, y);
           tile -= u.upto[sl][q];
+          v_rows = u.keys[sl][q] - tile * kTile;
           left = q == my_seq && row_valid ? own_hi : 0;
         }
         const int hi = min(left - tile * kTile, kTile);
@@ -660,12 +786,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after_sync();
+        const auto clear_v = [&]() -> bool {
+          // the rest of the V tile may hold NaN, and P = 0 would not keep it out
+          const int j = j0 + u.place(s, y) - u.m0, st = j % kStages;
+          if (!mbar_wait_warp(&bars[Lay::bVFull + st], (j / kStages) & 1, p.status, abort_flag))
+            return false;
+          const int warps = (rows + 31) / 32;
+          uint8_t* v = smem + Lay::kV + st * Lay::kTileBytes;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          // 16-byte chunks [v_rows x 8, 128 x 8) of each 64-feature box
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll 1
+            for (int k = v_rows * 8 + (warp & 3) * 32 + lane; k < kTile * 8; k += warps * 32)
+              *reinterpret_cast<uint4*>(v + c * Lay::kBoxBytes + k * 16) = zero;
+          fence_proxy_async_smem();
+          return true;
+        };
         if (__all_sync(0xffffffffu, hi <= 0)) {  // another sequence's keys: P = 0
           float zero[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) zero[c] = 0.f;
           tmem_st32(tmem + lane_base + colS, zero);
           tmem_st32(tmem + lane_base + colS + 32, zero);
+          if (v_rows < kTile && !clear_v()) {
+            ok = false;
+            break;
+          }
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
@@ -747,6 +894,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float rs0, rs1;
         f2_unpack(rs2, rs0, rs1);
         l += rs0 + rs1;
+        if (v_rows < kTile && !clear_v()) {
+          ok = false;
+          break;
+        }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[Lay::bPFull + s]);
@@ -755,6 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_mine = n_tiles > 0;
       n_mine += n_tiles;
       n_other += u.n_pre[1 - s] + u.n_own[1 - s];
+      j0 += u.m1 - u.m0;
       if (ok && any_mine)
         ok = mbar_wait_warp(&bars[Lay::bPvDone + s], (n_mine - 1) & 1, p.status, abort_flag);
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, joined, slot 1's
@@ -785,18 +937,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && has_rows && !(u.alternate && s == 1)) {
         tc_fence_after_sync();
+        // l is 0 without any key, NaN with a score that is
+        const float inv_l = l == 0.f ? 0.f : 1.f / l;
+        w0 = any_mine ? w0 * inv_l : 0.f;
+        w1 *= inv_l;
+        const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         // the row again: kept over the loop above it would cost registers there
         int own_row = u.row0[s] + (row_valid ? row : 0);
         asm volatile("" : "+r"(own_row));
         const Row at = row_at(p, u.group, own_row);
         const int r = row_valid ? static_cast<int>(at.token) * p.Hq + at.h : -1;
-        float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-        if (l > 0.f && u.bad[s][at.b - u.seq0[s]]) inv_l = NAN;
-        w0 = any_mine ? w0 * inv_l : 0.f;
-        w1 *= inv_l;
-        const float lse = (l > 0.f) ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
         const int64_t all = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
-        if (u.direct || __any_sync(0xffffffffu, l > 0.f)) {
+        if (u.direct || __any_sync(0xffffffffu, l != 0.f)) {
           // The warp's rows, 2 D bytes of each at a time (D / 2 fp32 columns or
           // all D in bf16), through the Q tile, whose MMAs are complete: D / 8
           // lanes then store a row's bytes together.  Each warp stays in the
@@ -830,6 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           };
+          float finite = 0.f;  // NaN once an element is not finite
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const uint32_t col = half * (D / 2);
@@ -855,6 +1008,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < D / 2; ++k) o[k] = fmaf(o1[k], w1, o[k]);
             }
+#pragma unroll
+            for (int k = 0; k < D / 2; ++k) finite = fmaf(o[k], 0.f, finite);
             if (u.direct) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
@@ -874,6 +1029,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       half * (D * 2),
                        u.direct ? D * 2 : D * 4);
           }
+          // The MMA multiplies a row's P = 0 by masked keys too, those of other
+          // sequences in its tile and later ones of its own, and 0 times an
+          // infinity or NaN among their V is NaN (see sum_again).
+          redo = redo || ((u.seqs[sl] > 1 || p.causal) && u.m1 > max(u.m0, u.np) && row_valid &&
+                          finite != finite && l == l);
         }
         if (row_valid) {
           if (u.direct)
@@ -889,6 +1049,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
       }
     }
+    // (the K ring is free: every MMA of both slots is complete)
+    if (softmax_warps_and(ok) && !softmax_warps_and(!redo))
+      sum_again<D>(p, reached, share_end, *reinterpret_cast<Unit*>(smem + Lay::kK));
   }
 
   tc_fence_before_sync();
@@ -970,7 +1133,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
 #pragma unroll
       for (int c = 0; c < kN; ++c) acc.x[c] += joined[warp + k][lane].x[c];
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   struct alignas(kN * 2) Out {
     uint32_t x[kN / 2];
   } out;
@@ -980,7 +1143,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
   if (lane == 0) {
     const uint32_t b = pl.by_queries(token);
     p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + (token - b * p.queries)] =
-        sum > 0.f ? top + logf(sum) : -INFINITY;
+        sum == 0.f ? -INFINITY : top + logf(sum);
   }
 }
 
@@ -1256,6 +1419,12 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.q = static_cast<const __nv_bfloat16*>(t.t[0]);
   a.q_tok = static_cast<uint32_t>(t.tok[0] / 8);
   a.q_bat = static_cast<uint32_t>(t.bat[0] / 8);
+  const __nv_bfloat16** kv[4] = {&a.k_prefix, &a.v_prefix, &a.k_own, &a.v_own};
+  for (int i = 0; i < 4; ++i) {
+    *kv[i] = static_cast<const __nv_bfloat16*>(t.t[i + 1]);
+    a.tok[i] = t.tok[i + 1];
+    a.bat[i] = t.bat[i + 1];
+  }
   a.own_len = in->own_len;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;

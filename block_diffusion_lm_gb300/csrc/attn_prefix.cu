@@ -32,7 +32,7 @@
 // own take no part.  Own rows past a sequence's end may hold NaN: their scores
 // are masked, and the softmax warps clear their V rows in shared memory before
 // the MMA that would multiply them by P = 0.  Where another masked V is not
-// finite, the rows it reached are summed again at the end of the piece.
+// finite, the rows it reached are summed again at the end of the share.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "csbp_generate.h"
 #include "csbp_internal.h"
@@ -237,8 +238,8 @@ struct PrefixLayout {
   static constexpr int bUnitEmpty = bUnitFull + 2;  // [2] and used by all roles
   static constexpr int bDrain = bUnitEmpty + 2;
   static constexpr int kBars = bDrain + 1;
-  static constexpr int kMisc = kBar + kBars * 8;    // tmem base, abort flag
-  static constexpr int kMl = (kMisc + 8 + 15) / 16 * 16;  // slot 1's max and sum, 128 rows
+  static constexpr int kMisc = kBar + kBars * 8;    // tmem base, abort flag, redo flag
+  static constexpr int kMl = (kMisc + 12 + 15) / 16 * 16;  // slot 1's max and sum, 128 rows
   static constexpr int kUnits = kMl + kTile * 8;    // ring of two pieces
   static constexpr int kDynSmem = kUnits + 2 * kUnitBytes;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
@@ -380,47 +381,144 @@ __device__ __forceinline__ void copy_q(const PrefixParams& p, uint32_t mine, uin
         v[t];
 }
 
-// acc += sum_j 2^(scale q.k_j - ref) v_j over keys [from, to) of one head, by a
-// whole warp, lane l with features l D / 32 ..; 8 keys in flight.
+// acc += sum_j 2^(scale q.k_j - ref) v_j over keys [from, to) of one head, for
+// two rows at once: 16 lanes to a row, lane l with features (l % 16) D / 16 .. (k
+// and v point there); 4 keys in flight.  The rows' ranges may differ.
 template <int D>
-__device__ __forceinline__ void walk_keys(const float (&q)[D / 32], float (&acc)[D / 32],
+__device__ __forceinline__ void walk_keys(const float (&q)[D / 16], float (&acc)[D / 16],
                                           const __nv_bfloat16* k, const __nv_bfloat16* v,
                                           int64_t k_tok, int64_t v_tok, int from, int to,
                                           float scale, float ref) {
-  constexpr int kN = D / 32, kBatch = 8;
-  const int lane = threadIdx.x & 31;
+  constexpr int kN = D / 16, kBatch = 4;
+  using Chunk = std::conditional_t<D == 128, uint4, uint2>;
+  int most = to - from;
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
 #pragma unroll 1
-  for (int j0 = from; j0 < to; j0 += kBatch) {
+  for (int j0 = 0; j0 < most; j0 += kBatch) {
     float s[kBatch];
-    __nv_bfloat162 vv[kBatch][kN / 2];
+    Chunk vv[kBatch];
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
-      const int j = min(j0 + t, to - 1);
-      const __nv_bfloat162* kr = reinterpret_cast<const __nv_bfloat162*>(k + j * k_tok) + lane * (kN / 2);
-      const __nv_bfloat162* vr = reinterpret_cast<const __nv_bfloat162*>(v + j * v_tok) + lane * (kN / 2);
       s[t] = 0.f;
+      const int64_t j = from + j0 + t < to ? from + j0 + t : 0;  // (in place of no load)
+      const Chunk kk = __ldg(reinterpret_cast<const Chunk*>(k + j * k_tok));
+      vv[t] = __ldg(reinterpret_cast<const Chunk*>(v + j * v_tok));
+      const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&kk);
 #pragma unroll
-      for (int c = 0; c < kN / 2; ++c) {
-        const float2 x = __bfloat1622float2(kr[c]);
-        vv[t][c] = vr[c];
-        s[t] = fmaf(q[2 * c], x.x, fmaf(q[2 * c + 1], x.y, s[t]));
+      for (int e = 0; e < kN / 2; ++e) {
+        const float2 y = __bfloat1622float2(x[e]);
+        s[t] = fmaf(q[2 * e], y.x, fmaf(q[2 * e + 1], y.y, s[t]));
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
       for (int t = 0; t < kBatch; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
-      if (j0 + t >= to) break;
       const float w = exp2f(fmaf(s[t], scale, -ref));
+      if (from + j0 + t >= to) continue;
+      const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&vv[t]);
 #pragma unroll
-      for (int c = 0; c < kN / 2; ++c) {
-        const float2 x = __bfloat1622float2(vv[t][c]);
-        acc[2 * c] = fmaf(w, x.x, acc[2 * c]);
-        acc[2 * c + 1] = fmaf(w, x.y, acc[2 * c + 1]);
+      for (int e = 0; e < kN / 2; ++e) {
+        const float2 y = __bfloat1622float2(x[e]);
+        acc[2 * e] = fmaf(w, y.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, y.y, acc[2 * e + 1]);
       }
     }
+  }
+}
+
+// Barrier 3: the eight softmax warps.
+__device__ __forceinline__ void softmax_warps_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_warps_and(bool x) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 3, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return all != 0;
+}
+
+// The rows of a share's pieces that came out not finite where masked keys can
+// have done that, summed again over the keys that they read alone; their LSE
+// is right (a score is masked before it is used).  By the softmax warps, when
+// the whole share is done: the other roles have ended, so no wait of theirs
+// runs out.  It is there to be right, not fast: 64 sequences of 8 tokens over
+// 65536 keys (32 heads of 64) take 33 ms in place of 0.4 when one own V is NaN.
+template <int D>
+__device__ __forceinline__ void sum_again(const PrefixParams& p, uint32_t at, uint32_t end, Unit& u) {
+  constexpr int kN = D / 16;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4;
+  const int f0 = (lane & 15) * kN;
+  const int64_t all = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
+  while (true) {
+    if (warp == 0) make_unit(p, at, end, u);
+    softmax_warps_sync();
+    if (!u.valid) return;
+    const int64_t head = static_cast<int64_t>(p.plan.by_per_kv(u.group)) * D + f0;
+#pragma unroll 1
+    for (int i = warp; i < kTile; i += 8) {  // two rows
+      const int s = i >= kTile / 2, row = 2 * i - s * kTile + (lane >> 4);
+      const bool valid = row < u.rows[s] && !(u.alternate && s == 1) &&
+                         (u.seqs[s] > 1 || p.causal) && u.m1 > max(u.m0, u.np);
+      const Row x = row_at(p, u.group, u.row0[s] + min(row, max(u.rows[s] - 1, 0)));
+      const int64_t r = static_cast<int64_t>(x.token) * p.Hq + x.h;
+      const int64_t place = r * D + f0;
+      bool need = false;
+      float lse = 0.f;
+      if (valid) {
+        lse = u.direct ? p.lse[(static_cast<int64_t>(x.b) * p.Hq + x.h) * p.queries + x.i]
+                       : p.part_lse[u.part * all + r];
+        if (lse > -INFINITY) {  // it has keys, and no score is NaN
+          float finite = 0.f;
+#pragma unroll
+          for (int c = 0; c < kN; ++c)
+            finite = fmaf(u.direct ? __bfloat162float(p.o[place + c])
+                                   : p.part_o[u.part * all * D + place + c],
+                          0.f, finite);
+          need = finite != finite;
+        }
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, need);
+      if (found == 0) continue;
+      need = (found >> (lane & 16)) & 0xffffu;
+      float q[kN], acc[kN];
+      const __nv_bfloat16* qr = p.q + static_cast<int64_t>(q_place<D>(p, x)) * 8 + f0;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        q[c] = __bfloat162float(qr[c]);
+        acc[c] = 0.f;
+      }
+      const float ref = lse * 1.4426950408889634f;
+      const int pre0 = min(u.m0, u.np) * kTile;
+      const int pre1 = min(p.prefix_len, min(u.m1, u.np) * kTile);
+      walk_keys<D>(q, acc, p.k_prefix + head, p.v_prefix + head, p.tok[0], p.tok[1], pre0,
+                   need ? pre1 : pre0, p.scale_log2, ref);
+      // the piece's part of the sequence's own tiles
+      const int sq = x.b - u.seq0[s], before = u.upto[s][sq];
+      const int o0 = u.alternate ? max(u.m0, u.np) - u.np : u.t_own[s];
+      const int o1 = u.alternate ? max(u.m1, u.np) - u.np : o0 + u.n_own[s];
+      int hi = u.keys[s][sq];
+      if (p.causal) hi = min(hi, hi - p.queries + x.i + 1);
+      const int own0 = max(o0 - before, 0) * kTile;
+      walk_keys<D>(q, acc, p.k_own + x.b * p.bat[2] + head, p.v_own + x.b * p.bat[3] + head,
+                   p.tok[2], p.tok[3], own0, need ? min(hi, max(o1 - before, 0) * kTile) : own0,
+                   p.scale_log2, ref);
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        if (!need) continue;
+        if (u.direct)
+          p.o[place + c] = __float2bfloat16_rn(acc[c]);
+        else
+          p.part_o[u.part * all * D + place + c] = acc[c];
+      }
+    }
+    softmax_warps_sync();
   }
 }
 
@@ -439,6 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
   uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(smem + Lay::kMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + Lay::kMisc + 4);
+  // set when a row may have taken in keys that it does not read
+  volatile int* redo = reinterpret_cast<volatile int*>(smem + Lay::kMisc + 8);
   float2* ml = reinterpret_cast<float2*>(smem + Lay::kMl);
   const auto unit_at = [&](int k) -> Unit& {
     return *reinterpret_cast<Unit*>(smem + Lay::kUnits + (k & 1) * kUnitBytes);
@@ -483,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[Lay::bUnitEmpty], 10);
       mbar_init(&bars[Lay::bUnitEmpty + 1], 10);
       *abort_flag = 0;
+      *redo = 0;
       fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -1002,49 +1103,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // The MMA multiplies a row's P = 0 by masked keys too, those of other
           // sequences in its tile and later ones of its own, and 0 times an
-          // infinity or NaN among their V is NaN.  Rows that are not finite where
-          // that can be are summed again over the keys they read alone, the
-          // maximum and sum being right.
-          const int sl = u.alternate ? 0 : s;
-          const bool masked = (u.seqs[sl] > 1 || p.causal) && u.m1 > max(u.m0, u.np);
-          uint32_t again = __ballot_sync(0xffffffffu, masked && row_valid && finite != finite);
-          while (again) {
-            const int rr = __ffs(again) - 1;
-            again &= again - 1;
-            const float top = __shfl_sync(0xffffffffu, m_ref, rr);
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float inv = __shfl_sync(0xffffffffu, inv_l, rr);
-            const int end = __shfl_sync(0xffffffffu, own_hi, rr);
-            const int to = __shfl_sync(0xffffffffu, r, rr);
-            const Row x = row_at(p, u.group, u.row0[s] + (warp & 3) * 32 + rr);
-            constexpr int kN = D / 32;
-            float q[kN], acc[kN];
-            const __nv_bfloat16* qr = p.q + static_cast<int64_t>(q_place<D>(p, x)) * 8 + lane * kN;
-#pragma unroll
-            for (int c = 0; c < kN; ++c) {
-              q[c] = __bfloat162float(qr[c]);
-              acc[c] = 0.f;
-            }
-            const int64_t head = static_cast<int64_t>(p.plan.by_per_kv(u.group)) * D;
-            walk_keys<D>(q, acc, p.k_prefix + head, p.v_prefix + head, p.tok[0], p.tok[1],
-                         min(u.m0, u.np) * kTile,
-                         min(p.prefix_len, min(u.m1, u.np) * kTile), p.scale_log2, ref);
-            // the piece's part of the sequence's own tiles
-            const int sq = x.b - u.seq0[sl], before = u.upto[sl][sq];
-            const int o0 = u.alternate ? max(u.m0, u.np) - u.np : u.t_own[s];
-            const int o1 = u.alternate ? max(u.m1, u.np) - u.np : o0 + u.n_own[s];
-            walk_keys<D>(q, acc, p.k_own + x.b * p.bat[2] + head, p.v_own + x.b * p.bat[3] + head,
-                         p.tok[2], p.tok[3], max(o0 - before, 0) * kTile,
-                         min(end, max(o1 - before, 0) * kTile), p.scale_log2, ref);
-#pragma unroll
-            for (int c = 0; c < kN; ++c) {
-              const int64_t at_c = static_cast<int64_t>(to) * D + lane * kN + c;
-              if (u.direct)
-                p.o[at_c] = __float2bfloat16_rn(acc[c] * inv);
-              else
-                p.part_o[u.part * all * D + at_c] = acc[c] * inv;
-            }
-          }
+          // infinity or NaN among their V is NaN (see sum_again).
+          if (finite != finite && l == l && (u.seqs[sl] > 1 || p.causal) && u.m1 > max(u.m0, u.np))
+            *redo = 1;
         }
         if (row_valid) {
           if (u.direct)
@@ -1059,6 +1120,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (join && s == 0 && ok) mbar_arrive(&bars[Lay::bJoined]);
         mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
       }
+    }
+    // (the K ring is free: every MMA of both slots is complete)
+    if (softmax_warps_and(ok) && *redo) {
+      uint32_t cta;  // (kept apart from the start's: it would cost registers above)
+      asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
+      sum_again<D>(p, p.plan.share(cta), p.plan.share(cta + 1),
+                   *reinterpret_cast<Unit*>(smem + Lay::kK));
     }
   }
 
