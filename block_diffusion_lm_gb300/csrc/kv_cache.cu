@@ -75,7 +75,9 @@ struct Codes16 {
 };
 
 // 32 bytes: one access, or two of 16 where rows start on 16 only (`wide`, the
-// same for all threads).  Streamed: nobody comes back soon.
+// same for all threads).  Streamed: nobody comes back soon.  8 x 25,000 rows of
+// 128 features are read back in 28.4 us wide, in 31.4 otherwise (writes: 30.0
+// either way).
 __device__ __forceinline__ Values16 load16(const void* p, bool wide) {
   Values16 v;
   if (wide) {
@@ -163,7 +165,9 @@ constexpr int kThreads = 256;
 // used: steps of one row where a row takes several (R = 1), else R = N rows, so
 // that short rows do not make short threads.  HBM bounds it: 3 + 1/32 bytes per
 // value, at 4 to 5 instructions per value, about half the issue rate (one value
-// at a time took 10 and was bound by them).
+// at a time took 10 and was bound by them).  131,072 rows of 8 x 128 features:
+// write 127.6 us, 6.38 TB/s, 0.94 of a plain copy's measured rate; read 122.7
+// us, 6.63 TB/s, 0.98.  A token for each of 8 sequences: 2 to 2.8 us.
 template <int L, int R>
 struct Shape {
   static constexpr int kRows = kThreads / L * R;  // of a CTA
@@ -348,13 +352,17 @@ csbp_status launch(const CacheArgs& a, void* stream) {
 }
 
 // The fewest lanes that hold a row in one step (so that short rows share a
-// warp), at most a warp; several rows per lane where one step is all.  Few
-// rows take one row per lane all the same: then latency counts.
+// warp), at most a warp; two rows per lane where one step is all (25,000 rows of
+// 128 features, 8 sequences: write 30.0 us, read 27.8; four rows per lane 38.2
+// and 28.4, one row and 16 lanes 81.5 and 58.7).  Few rows, up to one CTA of 16
+// per SM, take one row per 16 lanes all the same: then latency counts (8 x 100
+// rows: write 2.5 us, read 2.4, against 2.7 and 3.0; 8 x 500: 3.3 and 3.0
+// against 2.9 and 3.0).
 template <bool kWrite>
 csbp_status launch(const CacheArgs& a, void* stream) {
-  constexpr int kRows = kWrite ? 2 : 4;  // (four would hold a write at 95 registers)
+  constexpr int kRows = 2;
   const int chunks = a.row_values >> 4;
-  const bool few = static_cast<int64_t>(a.batch) * a.rows * chunks < 152 * 4 * kThreads;
+  const bool few = static_cast<int64_t>(a.batch) * a.rows <= 152 * 16;
   if (chunks > 32 || (few && chunks > 16)) return launch<32, 1, kWrite>(a, stream);
   if (few) return launch<16, 1, kWrite>(a, stream);
   if (chunks <= 2) return launch<2, kRows, kWrite>(a, stream);
