@@ -25,14 +25,28 @@
 // second kernel joins them exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
 //
 // Roles (384 threads), as in the training forward: warp 0 lane 0 TMA
-// producer, warp 1 lane 0 MMA issuer, warps 4..7 and 8..11 softmax of slot 0
-// and 1 (thread t = row t = TMEM lane t).  P overwrites the first 64 columns of
-// its S as bf16 pairs and is the TMEM A operand of P V; O is rescaled only
-// when a row's maximum grows by more than 2^8.  Warps without a row of their
-// own take no part.  Own rows past a sequence's end may hold NaN: their scores
-// are masked, and the softmax warps clear their V rows in shared memory before
-// the MMA that would multiply them by P = 0.  Where another masked V is not
-// finite, the rows it reached are summed again at the end of the share.
+// producer, warp 1 lane 0 MMA issuer, warp 2 works out the pieces ahead of the
+// others, warps 4..7 and 8..11 softmax of slot 0 and 1 (thread t = row t = TMEM
+// lane t).  P is the TMEM A operand of P V, as bf16 pairs over the first 64
+// columns of its S (d = 128) or in columns of its own (d = 64); its rounding to
+// bf16 is the one that the tensor cores ask for, maxima and sums stay fp32.  O is
+// rescaled only when a row's maximum grows by more than 2^8.  Warps without a row
+// of their own take no part.  Own rows past a sequence's end may hold NaN: their
+// scores are masked, and the softmax warps clear their V rows in shared memory
+// before the MMA that would multiply them by P = 0.  Where another masked V is
+// not finite, the rows it reached are summed again at the end of the share.
+//
+// Bound.  Long prefixes with enough rows: the chain S -> softmax -> P V of a slot
+// and the issuer's barriers, as in the training forward (tensor pipe 49 % active
+// at d = 128, 30 % at 64; issue slots 33 % and 40 %).  Few rows: HBM.  Small
+// calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
+//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   859 us, 1280 TFLOP/s
+//     (0.66 of the measured bf16 rate); heads of 64       702 us
+//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   186 us
+//   65,536 keys, 8 x 1 queries, 32 / 8 heads   48.4 us, 5.5 TB/s (0.82 of a copy)
+//   8,192 keys, 8 x 1 queries, 32 / 8 heads    18.9 us
+// A kernel without tensor cores took 41,000 us at the second and 7,200 at 8192
+// keys; one job per CTA without cuts 46 us there, 342 at the second.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -165,6 +179,12 @@ struct Unit {
   int keys[2][kTile];       // own keys of each sequence
   int upto[2][kTile + 1];   // own key tiles of the sequences before it
 
+  // Whether slot s's Q tile is read.  One that is not signals nothing: its softmax
+  // could be two pieces ahead of the issuer, where parities say the same again.
+  __device__ __forceinline__ bool q_used(int s) const {
+    return alternate ? s == 0 && m0 < m1 : n_pre[s] + n_own[s] > 0;
+  }
+
   // Which slots read the m-th key tile of the list, and its number among the
   // prefix tiles or the slot's own tiles: prefix tiles first, then the two
   // slots' own tiles in turn.
@@ -243,6 +263,12 @@ struct PrefixLayout {
   static constexpr int kUnits = kMl + kTile * 8;    // ring of two pieces
   static constexpr int kDynSmem = kUnits + 2 * kUnitBytes;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
+  // P of slot s: D = 64 leaves columns for it, where it is not over its S and the
+  // next S need not wait for the PV (a million keys, 16 tokens of 4 sequences and
+  // 32 heads: 778 -> 695 us; 65536 keys, 32 rows a KV head: 44 -> 46 us)
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kColP = kOwnP ? kColO + 2 * D : 0;
+  static constexpr uint32_t kStepP = kOwnP ? kTile / 2 : kTile;
 };
 
 // Key tiles before place x of a job: prefix tiles by place alone (so that
@@ -689,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool fresh[2] = {};       // no PV of this piece yet: the next one overwrites O
       // S_s = Q K^T of Q tile sq and ring stage st into slot s's S columns
       auto issue_s = [&](int s, int st, int sq) -> bool {
-        if (npv[s] > 0 &&
+        if (!Lay::kOwnP && npv[s] > 0 &&
             !mbar_wait_spin(&bars[Lay::bPvDone + s], (npv[s] - 1) & 1, p.status, abort_flag))
           return false;  // its last PV still reads the P held there
         tc_fence_after_sync();
@@ -706,9 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&bars[Lay::bSFull + s]);
         return true;
       };
-      // O_s += P_s V of ring stage st, P_s (bf16 pairs) in slot s's S columns
+      auto p_ready = [&](int s) -> bool {
+        return mbar_wait_spin(&bars[Lay::bPFull + s], npv[s] & 1, p.status, abort_flag);
+      };
+      // O_s += P_s V of ring stage st, P_s as bf16 pairs
       auto issue_pv = [&](int s, int st) -> bool {
-        if (!mbar_wait_spin(&bars[Lay::bPFull + s], npv[s] & 1, p.status, abort_flag)) return false;
+        if (!Lay::kOwnP && !p_ready(s)) return false;
         tc_fence_after_sync();
         const uint64_t vb = sdesc_sw128(smem_u32(smem + Lay::kV + st * Lay::kTileBytes),
                                         Lay::kBoxBytes, 1024);  // V, MN-major B
@@ -716,7 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fresh[s] = false;
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          umma_bf16_ts(tmem + Lay::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(vb, k * 2048),
+          umma_bf16_ts(tmem + Lay::kColO + s * D, tmem + Lay::kColP + s * Lay::kStepP + k * 8,
+                       sdesc_step(vb, k * 2048),
                        idesc_pv, k > 0 ? 1u : acc0);
         umma_commit(&bars[Lay::bPvDone + s]);
         ++npv[s];
@@ -731,11 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m0 = u.m0, m1 = u.m1, np = u.np, own0 = u.own[0], own1 = u.own[1];
         const int both = 2 * min(own0, own1);
         const bool alternate = u.alternate;
+        const bool q0_full = u.q_used(0), q1_full = u.q_used(1);
         mbar_arrive(&bars[Lay::bUnitEmpty + (k & 1)]);
         if (m0 >= m1) continue;
         const int q1 = alternate ? 0 : 1;  // Q tile of slot 1
-        ok = mbar_wait(&bars[Lay::bQFull], nq0++ & 1, p.status, abort_flag);
-        if (ok && q1) ok = mbar_wait(&bars[Lay::bQFull + 1], nq1++ & 1, p.status, abort_flag);
+        if (q0_full) ok = mbar_wait(&bars[Lay::bQFull], nq0++ & 1, p.status, abort_flag);
+        if (ok && q1_full) ok = mbar_wait(&bars[Lay::bQFull + 1], nq1++ & 1, p.status, abort_flag);
         if (!ok) break;
         fresh[0] = fresh[1] = true;
         bool prev0 = false, prev1 = false;
@@ -765,21 +796,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int pass = 0; ok && pass < 2; ++pass) {
             const bool with_pv = pv && (pass == 1) == apart;
             const bool with_s = more && pass == 0;
-            if (with_pv) {
-              ok = v_ready();
-              if (ok && prev0) ok = issue_pv(0, pst);
-            }
-            if (ok && with_s) {
-              ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
-              if (ok && in0) ok = issue_s(0, st, 0);
-            }
-            if (ok && with_pv) {
-              if (prev1) ok = issue_pv(1, pst);
-              if (ok) umma_commit(&bars[Lay::bVEmpty + pst]);
-            }
-            if (ok && with_s) {
-              if (in1) ok = issue_s(1, st, q1);
-              if (ok) umma_commit(&bars[Lay::bKEmpty + st]);
+            if constexpr (Lay::kOwnP) {
+              // S may follow as soon as the S before it is read: before the PV
+              if (with_s)
+                ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
+              if (ok && with_pv) ok = v_ready();
+              if (ok && with_pv && prev0) ok = p_ready(0);
+              if (ok && with_s && in0) ok = issue_s(0, st, 0);
+              if (ok && with_pv && prev0) ok = issue_pv(0, pst);
+              if (ok && with_pv && prev1) ok = p_ready(1);
+              if (ok && with_s && in1) ok = issue_s(1, st, q1);
+              if (ok && with_pv && prev1) ok = issue_pv(1, pst);
+              if (ok && with_pv) umma_commit(&bars[Lay::bVEmpty + pst]);
+              if (ok && with_s) umma_commit(&bars[Lay::bKEmpty + st]);
+            } else {
+              if (with_pv) {
+                ok = v_ready();
+                if (ok && prev0) ok = issue_pv(0, pst);
+              }
+              if (ok && with_s) {
+                ok = mbar_wait(&bars[Lay::bKFull + st], (j / kStages) & 1, p.status, abort_flag);
+                if (ok && in0) ok = issue_s(0, st, 0);
+              }
+              if (ok && with_pv) {
+                if (prev1) ok = issue_pv(1, pst);
+                if (ok) umma_commit(&bars[Lay::bVEmpty + pst]);
+              }
+              if (ok && with_s) {
+                if (in1) ok = issue_s(1, st, q1);
+                if (ok) umma_commit(&bars[Lay::bKEmpty + st]);
+              }
             }
             if (!apart) break;
           }
@@ -800,6 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = threadIdx.x - 128 * (1 + s);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t colS = s * 128;
+    const uint32_t colP = Lay::kColP + s * Lay::kStepP;
     const uint32_t colO = Lay::kColO + s * D;
     const float sl2 = p.scale_log2;
     int n_mine = 0, n_other = 0;  // key tiles of this and the other slot so far
@@ -822,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         my_seq = at.b - u.seq0[sl];
         own_hi = u.keys[sl][my_seq];
         if (p.causal) own_hi = min(own_hi, own_hi - p.queries + at.i + 1);
-        if (u.m0 < u.m1 && (s == 0 || !u.alternate)) {
+        if (u.q_used(s)) {
           if (k > 0) {  // the first one is there
             copy_q<D>(p, q_place<D>(p, at), smem + Lay::kQ + s * Lay::kTileBytes,
                       (warp & 3) * 32);
@@ -849,7 +896,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           left = q == my_seq && row_valid ? own_hi : 0;
         }
         const int hi = min(left - tile * kTile, kTile);
-        if (!mbar_wait_warp(&bars[Lay::bSFull + s], (n_mine + t) & 1, p.status, abort_flag)) {
+        // The last PV read the P columns and wrote O (P over S: this S was
+        // issued after it).
+        const auto pv_done = [&]() -> bool {
+          if (n_mine + t == 0) return true;
+          const bool done =
+              mbar_wait_warp(&bars[Lay::bPvDone + s], (n_mine + t - 1) & 1, p.status, abort_flag);
+          tc_fence_after_sync();
+          return done;
+        };
+        // (a slot that takes every second tile has its S issued after that PV)
+        if (Lay::kOwnP && step == 2) ok = pv_done();
+        if (!ok || !mbar_wait_warp(&bars[Lay::bSFull + s], (n_mine + t) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
@@ -876,11 +934,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         if (__all_sync(0xffffffffu, hi <= 0)) {  // another sequence's keys: P = 0
+          if (Lay::kOwnP && step == 1 && !pv_done()) {
+            ok = false;
+            break;
+          }
           float zero[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) zero[c] = 0.f;
-          tmem_st32(tmem + lane_base + colS, zero);
-          tmem_st32(tmem + lane_base + colS + 32, zero);
+          tmem_st32(tmem + lane_base + colP, zero);
+          tmem_st32(tmem + lane_base + colP + 32, zero);
           if (v_rows < kTile && !clear_v()) {
             ok = false;
             break;
@@ -920,9 +982,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scale in one fused multiply-add
         const float m_new = fmaxf(m_ref, mx * sl2);
         const bool need = m_new > m_ref + kRescaleThreshold;  // false while both are -inf
+        if (Lay::kOwnP && step == 1 && !pv_done()) {
+          ok = false;
+          break;
+        }
         if (t > 0 && __any_sync(0xffffffffu, need)) {
-          // O holds the PVs so far, scaled by the old reference; the last is
-          // complete: the S this tile read was issued after it
+          // O holds the PVs so far, scaled by the old reference
           const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -948,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (((dead >> (2 * half)) & 3u) == 3u) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) packed[c] = 0.f;
-            tmem_st32(tmem + lane_base + colS + half * 32, packed);
+            tmem_st32(tmem + lane_base + colP + half * 32, packed);
             continue;
           }
 #pragma unroll
@@ -961,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs2 = f2_add(rs2, f2_pack(e0, e1));
             packed[c] = __uint_as_float(pack_bf16x2(e0, e1));
           }
-          tmem_st32(tmem + lane_base + colS + half * 32, packed);
+          tmem_st32(tmem + lane_base + colP + half * 32, packed);
         }
         float rs0, rs1;
         f2_unpack(rs2, rs0, rs1);

@@ -347,6 +347,18 @@ def test_causal_queries_do_not_see_later_values():
                clean, lens, True, 0.125)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_row_tiles_without_a_key(d):
+    """Every second row tile, and the last job, reads no key at all."""
+    B, n = 160, 32
+    t = attn_inputs(B, n, 0, 700, 16, 4, d, 17)
+    lens = [0 if b % 2 or b >= 156 else 1 + 37 * b % 700 for b in range(B)]
+    a = csbp.PrefixAttention(B, n, 0, 700, 16, 4, d)
+    out = a.forward(**t, own_len=i32(lens))
+    a.check()
+    check_attn(out, t, lens, False, d ** -0.5)
+
+
 def test_attention_strides():
     """q, k and v as views into packed projections; the prefix as a slice of a
     longer cache."""
