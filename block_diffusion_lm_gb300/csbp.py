@@ -220,7 +220,8 @@ def kernel_timing_read():
 
 def kernel_timing_read_kind(kind: int):
     """(ms, launches) of one timer kind: 0 fwd, 1 bwd, 2 CE logits GEMM,
-    3 CE row kernel, 4 CE dH GEMM, 5 CE dW GEMM."""
+    3 CE row kernel, 4 CE dH GEMM, 5 CE dW GEMM, 11 cache write, 12 cache read,
+    13 prefix attention, 14 the joining of its pieces, 15 draft verification."""
     ms, n = ctypes.c_double(), ctypes.c_int32()
     _check("csbp_kernel_timing_read_kind",
            lib().csbp_kernel_timing_read_kind(kind, ctypes.byref(ms), ctypes.byref(n)))

@@ -50,6 +50,21 @@ def test_struct_layouts_match_the_header(tmp_path):
             assert int(out[f"{name}.{f}"]) == getattr(s, f).offset, (name, f)
 
 
+def test_header_compiles_as_cpp(tmp_path):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    src = tmp_path / "use.cpp"
+    src.write_text('#include "csbp_generate.h"\n'
+                   'static_assert(sizeof(csbp_prefix_problem) > 0, "");\n'
+                   'int main() { return csbp_prefix_workspace_bytes == nullptr; }\n')
+    r = subprocess.run([cxx, "-std=c++11", "-pedantic", "-Wall", "-Wextra", "-Werror", "-c", "-I",
+                        os.path.join(ROOT, "include"), str(src), "-o", str(tmp_path / "use.o"),
+                        "-Wno-address", "-Wno-nonnull-compare"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
 # ------------------------------------------------------------------- C ABI
 def cache(**kw):
     c = csbp.KvCache(10, 16, 4, 64, PTR, PTR, PTR, PTR)
@@ -146,6 +161,14 @@ def test_prefix_outputs_and_workspace_are_checked():
     assert csbp.prefix_workspace_bytes(prefix()) >= 256
 
 
+def test_prefix_sizes_past_the_counters_are_unsupported():
+    """q in 16-byte units within 32 bits, rows within 2^30."""
+    big = prefix_inputs()
+    big.stride_batch[0] = 1 << 33
+    assert attn(prefix(batch=3), big) == UNSUPPORTED
+    assert attn(prefix(batch=1 << 20, queries=1 << 10), prefix_inputs()) == UNSUPPORTED
+
+
 def verify(pr, p=PTR, q=PTR, token=PTR, u=PTR, r=PTR, length=None, acc=PTR, out=PTR):
     return csbp.lib().csbp_draft_verify(ctypes.byref(pr), p, q, token, u, r, length, acc, out,
                                         None)
@@ -199,6 +222,8 @@ def test_cache_binding_checks():
         c.read(i32(3, 2), i32(3), rows=4)
     with pytest.raises(ValueError, match="k_scale must have shape"):
         csbp.QuantCache(6, 16, 2, 64, storage=(c.k, c.v, c.k, c.v_scale))
+    with pytest.raises(ValueError, match="on one device"):
+        csbp.QuantCache(6, 16, 2, 64, storage=(c.k, c.v.to("meta"), c.k_scale, c.v_scale))
     with pytest.raises(ValueError, match="multiple of 32"):
         csbp.QuantCache(6, 16, 2, 48, device="cpu")
     assert c.write(z(0, 5, 2, 64), z(0, 5, 2, 64), i32(0, 2), i32(0)) is None

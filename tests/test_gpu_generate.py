@@ -12,6 +12,8 @@ Tolerances, derived from the arithmetic (half a rounding step is eps / 2):
    2^-24 for each of at most 2^8 sequential additions of a row's sum;
  * verification: exact integers.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -190,6 +192,44 @@ def test_cache_strides():
     assert (dst.cpu()[rest] == 5.0).all()
 
 
+@pytest.mark.parametrize("rows", [5, 1500])
+def test_cache_rows_on_16_bytes(rows):
+    """Rows of the bf16 side that start on 16 bytes but not on 32."""
+    B, H, d = 2, 3, 64
+    g = gen(6)
+    tok = H * d + 8
+
+    def view():
+        flat = normal(g, 8 + B * rows * tok)
+        return flat.as_strided((B, rows, H, d), (rows * tok, tok, d, 1), 8)
+
+    k, v = view(), view()
+    n = -(-(rows + 2) // 16)
+    c = dirty_cache(B * n, 16, H, d, g)
+    before = [t.clone() for t in (c.k, c.v, c.k_scale, c.v_scale)]
+    table = torch.randperm(B * n, generator=g, device="cuda").int().view(B, n)
+    start = i32([0, 2])
+    c.write(k, v, table, start)
+    check_write(c, before, k, v, table, start, None)
+    out = view(), view()
+    c.read(table, start, out=out)
+    check_read(c, out, table, start, None, 0.0)
+
+
+def test_rows_that_share_a_place_leave_bytes_of_either():
+    g = gen(7)
+    k, v = normal(g, 2, 40, 2, 64), normal(g, 2, 40, 2, 64) * 30
+    alone = []
+    for b in range(2):
+        c = csbp.QuantCache(4, 16, 2, 64)
+        c.write(k[b:b + 1], v[b:b + 1], i32([[0, 2, 1]]), i32([3]))
+        alone.append([t.clone() for t in (c.k, c.v, c.k_scale, c.v_scale)])
+    c = csbp.QuantCache(4, 16, 2, 64)
+    c.write(k, v, i32([[0, 2, 1], [0, 2, 1]]), i32([3, 3]))
+    for got, x, y in zip((c.k, c.v, c.k_scale, c.v_scale), *alone):
+        assert ((got == x) | (got == y)).all()
+
+
 def test_cache_beyond_32_bits():
     """Byte offsets past 2^32 in the codes."""
     pages, page = 70000, 64
@@ -331,6 +371,25 @@ def test_a_sequence_that_is_not_finite_stays_alone(value, n, causal):
         assert torch.isfinite(o[4, :, :4].float()).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_not_finite_where_jobs_are_cut(d):
+    """Rows summed again from partial results, with both slots at work."""
+    B, n, Lp, S = 16, 16, 5000, 300
+    lens = [300, 1, 128, 0, 257, 300, 17, 129, 300, 64, 3, 200, 300, 255, 90, 300]
+    t = attn_inputs(B, n, Lp, S, 8, 2, d, 19)
+    t["v_own"][5, 140] = float("nan")
+    t["v_own"][12, 2, 1, 7] = float("inf")
+    a = csbp.PrefixAttention(B, n, Lp, S, 8, 2, d)
+    o, lse = a.forward(**t, own_len=i32(lens))
+    a.check()
+    assert torch.isnan(o[5].float()).all()
+    hit = o[12].float().view(n, 2, 4, d)[:, 1, :, 7]
+    assert torch.isinf(hit).all()
+    rest = [b for b in range(B) if b not in (5, 12)]
+    part = {k: x if "prefix" in k else x[rest] for k, x in t.items()}
+    check_attn((o[rest], lse[rest]), part, [lens[b] for b in rest], False, d ** -0.5)
+
+
 def test_causal_queries_do_not_see_later_values():
     """The last key's V is read by the last query only, whatever it holds."""
     B, n, Lp, S = 3, 6, 300, 140
@@ -440,7 +499,7 @@ def check_verify(got, p, q, x, u, r, length=None):
 
 
 VERIFY = [(1, 1, 2), (1, 0, 7), (5, 3, 100), (3, 4, 1001), (2, 2, 5000), (9, 16, 33),
-          (40, 1, 257), (4, 2, 4099), (2, 1, 20000)]
+          (40, 1, 257), (4, 2, 4099), (2, 1, 20000), (1, 1, 40000), (2, 2, 70001)]
 
 
 @pytest.mark.parametrize("B,K,V", VERIFY)
@@ -623,6 +682,44 @@ def test_other_streams_and_graph_replay_give_the_same():
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def test_cut_attention_in_graphs_and_on_two_streams():
+    """Calls that end with the joining of pieces, captured and at once."""
+    shape = (2, 3, 4096, 130, 8, 2, 128)
+    lens = i32([130, 7])
+    calls, want = [], []
+    for seed in (70, 71):
+        t = attn_inputs(*shape, seed)
+        first = csbp.PrefixAttention(*shape)
+        want.append([x.clone() for x in first.forward(**t, own_len=lens)])
+        calls.append((csbp.PrefixAttention(*shape), t, first.alloc_outputs()))
+        first.check()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs = []
+    for a, t, out in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            a.forward(**t, own_len=lens, out=out)
+            a.forward(**t, own_len=lens, out=out)
+    for _ in range(10):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (a, _, out), w in zip(calls, want):
+        a.check()
+        assert all(torch.equal(x, y) for x, y in zip(out, w))
+        for x in out:
+            x.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (a, t, out), st in zip(calls, streams):
+            a.forward(**t, own_len=lens, out=out, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, out), w in zip(calls, want):
+        assert all(torch.equal(x, y) for x, y in zip(out, w))
+
+
 def test_two_streams_at_once():
     """Calls with workspaces of their own may overlap."""
     a, b = step_state(50), step_state(51)
@@ -635,3 +732,27 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for s, w in zip((a, b), want):
         assert all(torch.equal(x, y) for x, y in zip(w, [*s["o"], *s["acc"], *s["own"]]))
+
+
+def test_each_kernel_kind_is_timed():
+    s = step_state(60)
+    step(s)
+    # (pieces to join: one token over keys that are cut up to fill the GPU)
+    cut = csbp.PrefixAttention(1, 1, 4096, 0, 4, 2, 64)
+    t = attn_inputs(1, 1, 4096, 0, 4, 2, 64, 61)
+    args = t["q"], t["k_prefix"], t["v_prefix"], None, None, None
+    cut.forward(*args)
+    torch.cuda.synchronize()
+    ms, n = ctypes.c_double(), ctypes.c_int32()
+    read = csbp.lib().csbp_kernel_timing_read_kind
+    csbp.kernel_timing(True)
+    try:
+        step(s)
+        cut.forward(*args)
+        torch.cuda.synchronize()
+        for kind in range(11, 16):
+            assert read(kind, ctypes.byref(ms), ctypes.byref(n)) == 0
+            assert n.value >= 1 and 0.0 < ms.value < 1000.0, kind
+        assert read(16, ctypes.byref(ms), ctypes.byref(n)) == -1
+    finally:
+        csbp.kernel_timing(False)
