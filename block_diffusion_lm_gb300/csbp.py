@@ -874,20 +874,14 @@ def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
     Returns int32 (accepted [batch], tokens [batch][drafts + 1]: the accepted
     drafts, the next token, then -1); `out` receives them if given.  q, token
     and u may be None when p has one row per sequence (plain sampling)."""
-    import torch
-    if p is None or p.dim() != 3 or p.shape[1] < 1:
-        raise ValueError("csbp_draft_verify: p must be a [batch][drafts + 1][vocab] tensor")
-    batch, K, V = p.shape[0], p.shape[1] - 1, p.shape[2]
-    if K == 0:
-        q = token = u = None
-    if out is None:
-        accepted = torch.empty((batch,), dtype=torch.int32, device=p.device)
-        tokens = torch.empty((batch, K + 1), dtype=torch.int32, device=p.device)
-    else:
-        accepted, tokens = out
+    accepted, tokens = out if out is not None else (None, None)
 
     def check():
+        import torch
         c = _Call("csbp_draft_verify")
+        if p is None or p.dim() != 3 or p.shape[1] < 1:
+            raise ValueError("csbp_draft_verify: p must be a [batch][drafts + 1][vocab] tensor")
+        batch, K, V = p.shape[0], p.shape[1] - 1, p.shape[2]
 
         def rows(name, t, n):
             """Row and batch stride of fp32 [batch][n][vocab]."""
@@ -915,16 +909,22 @@ def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
         c.tensor("r", r, torch.float32, (batch,))
         if length is not None:
             c.tensor("length", length, torch.int32, (batch,))
-        c.tensor("accepted", accepted, torch.int32, (batch,))
-        c.tensor("tokens", tokens, torch.int32, (batch, K + 1))
-        return (VerifyProblem(batch, K, V, *strides), c.device()) if batch else (None, 0)
+        if out is not None:
+            c.tensor("accepted", accepted, torch.int32, (batch,))
+            c.tensor("tokens", tokens, torch.int32, (batch, K + 1))
+        dev = c.device() if batch else 0
+        return VerifyProblem(batch, K, V, *strides), dev, K, (batch,), (batch, K + 1)
 
     lib()
-    prob, dev = _layout("csbp_draft_verify", None, (p, q, token, u, r, length, accepted, tokens),
-                        check)
-    if prob is not None:
+    prob, dev, K, *shapes = _layout("csbp_draft_verify", out is None,
+                                    (p, q, token, u, r, length, accepted, tokens), check)
+    if out is None:
+        import torch
+        accepted, tokens = (torch.empty(s, dtype=torch.int32, device=p.device) for s in shapes)
+    if prob.batch:
         _run("csbp_draft_verify", dev, stream,
-             (p, q, token, u, r, length, accepted, tokens), ctypes.byref(prob), p.data_ptr(),
+             (p, r, length, accepted, tokens) + ((q, token, u) if K else ()),
+             ctypes.byref(prob), p.data_ptr(),
              q.data_ptr() if K else None, token.data_ptr() if K else None,
              u.data_ptr() if K else None, r.data_ptr(),
              None if length is None else length.data_ptr(), accepted.data_ptr(),
