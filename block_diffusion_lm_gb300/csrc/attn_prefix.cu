@@ -40,9 +40,9 @@
 // and the issuer's barriers, as in the training forward (tensor pipe 49 % active
 // at d = 128, 30 % at 64; issue slots 33 % and 40 %).  Few rows: HBM.  Small
 // calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
-//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   859 us, 1280 TFLOP/s
-//     (0.66 of the measured bf16 rate); heads of 64       702 us
-//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   186 us
+//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   860 us, 1280 TFLOP/s
+//     (0.66 of the measured bf16 rate); heads of 64       696 us
+//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   185 us
 //   65,536 keys, 8 x 1 queries, 32 / 8 heads   48.4 us, 5.5 TB/s (0.82 of a copy)
 //   8,192 keys, 8 x 1 queries, 32 / 8 heads    18.9 us
 // A kernel without tensor cores took 41,000 us at the second and 7,200 at 8192
@@ -277,11 +277,20 @@ __device__ __forceinline__ int prefix_before(const Plan& pl, int np, uint32_t x)
   if (x >= pl.len_prefix) return np;
   return min(np, static_cast<int>(static_cast<float>(x) * pl.inv_prefix * static_cast<float>(np)));
 }
-__device__ __forceinline__ int tiles_before(const Plan& pl, int np, int own, uint32_t x) {
+// An own tile that comes while the other slot has none left takes longer than one
+// that has its turn with the other slot's (4,500 against 2,500 cycles where one
+// warp has rows in it).  64 x 1 queries over up to 2,048 own keys: 92 us with
+// equal counts, 73 counting such a tile 1.25, 66 with 1.4, 66 with 1.5, 70 with
+// 1.75; 24 x 16 over up to 8,192: 76, 71, 72, 73, 76.
+constexpr float kAlone = 1.4f;
+__device__ __forceinline__ int tiles_before(const Plan& pl, int np, int in_turn, int alone,
+                                            uint32_t x) {
   if (x < pl.len_prefix) return prefix_before(pl, np, x);
-  if (x == pl.len) return np + own;
-  return np + min(own, static_cast<int>(static_cast<float>(x - pl.len_prefix) * pl.inv_own *
-                                        static_cast<float>(own)));
+  if (x == pl.len) return np + in_turn + alone;
+  const float both = static_cast<float>(in_turn);
+  const float t = static_cast<float>(x - pl.len_prefix) * pl.inv_own *
+                  (both + kAlone * static_cast<float>(alone));
+  return np + min(in_turn + alone, static_cast<int>(t <= both ? t : both + (t - both) / kAlone));
 }
 
 // The piece at place `at` of the list, in a share that ends at `end`; moves
@@ -344,9 +353,10 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
     u.direct = x0 == 0 && x1 == pl.len;
     u.alternate = alternate;
     u.np = np;
-    const int all = own[0] + (alternate ? 0 : own[1]);
-    u.m0 = tiles_before(pl, np, all, x0);
-    u.m1 = tiles_before(pl, np, all, x1);
+    const int in_turn = alternate ? own[0] : 2 * min(own[0], own[1]);
+    const int alone = alternate ? 0 : abs(own[0] - own[1]);
+    u.m0 = tiles_before(pl, np, in_turn, alone, x0);
+    u.m1 = tiles_before(pl, np, in_turn, alone, x1);
     const int p0 = min(u.m0, np), p1 = min(u.m1, np);
     const int o0 = max(u.m0, np) - np, o1 = max(u.m1, np) - np;
 #pragma unroll 1
@@ -986,7 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        if (t > 0 && __any_sync(0xffffffffu, need)) {
+        // (a row without a key so far has O = 0)
+        if (t > 0 && __any_sync(0xffffffffu, need && m_ref != -INFINITY)) {
           // O holds the PVs so far, scaled by the old reference
           const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
 #pragma unroll 1
