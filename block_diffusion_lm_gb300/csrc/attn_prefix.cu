@@ -24,9 +24,9 @@
 // a normalised fp32 partial and its LSE per piece in the workspace, and a
 // second kernel joins them exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
 //
-// Roles (384 threads), as in the training forward: warp 0 lane 0 TMA
-// producer, warp 1 lane 0 MMA issuer, warp 2 works out the pieces ahead of the
-// others, warps 4..7 and 8..11 softmax of slot 0 and 1 (thread t = row t = TMEM
+// Roles (384 threads), as in the training forward: one thread of warp 0
+// TMA producer, one of warp 1 MMA issuer, warp 2 works out the pieces ahead of
+// the others, warps 4..7 and 8..11 softmax of slot 0 and 1 (thread t = row t = TMEM
 // lane t).  P is the TMEM A operand of P V, as bf16 pairs over the first 64
 // columns of its S (d = 128) or in columns of its own (d = 64); its rounding to
 // bf16 is the one that the tensor cores ask for, maxima and sums stay fp32.  O is
@@ -40,11 +40,11 @@
 // and the issuer's barriers, as in the training forward (tensor pipe 49 % active
 // at d = 128, 30 % at 64; issue slots 33 % and 40 %).  Few rows: HBM.  Small
 // calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
-//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   860 us, 1280 TFLOP/s
-//     (0.66 of the measured bf16 rate); heads of 64       696 us
-//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   185 us
-//   65,536 keys, 8 x 1 queries, 32 / 8 heads   48.4 us, 5.5 TB/s (0.82 of a copy)
-//   8,192 keys, 8 x 1 queries, 32 / 8 heads    18.9 us
+//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   802 us, 1370 TFLOP/s
+//     (0.71 of the measured bf16 rate); heads of 64       623 us
+//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   169 us
+//   65,536 keys, 8 x 1 queries, 32 / 8 heads   46.8 us, 5.7 TB/s (0.85 of a copy)
+//   8,192 keys, 8 x 1 queries, 32 / 8 heads    17.4 us
 // A kernel without tensor cores took 41,000 us at the second and 7,200 at 8192
 // keys; one job per CTA without cuts 46 us there, 342 at the second.
 #include <cuda.h>
@@ -101,6 +101,21 @@ struct Divisor {
     return (static_cast<uint32_t>((static_cast<uint64_t>(mul) * n) >> 32) + n) >> shift;
   }
 };
+
+// True in one thread of a warp (all of it calls this).  With this test, and the
+// warp's number the same in all lanes for the compiler, it keeps what the MMAs and
+// copies of that thread take in uniform registers; `lane == 0` cost 4 to 25 % (a
+// million keys: 861 against 829 us, 8 x 1 queries over 65536 keys with heads of 64
+// 47 against 35).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(yes));
+  return yes != 0;
+}
 
 // How the rows and keys of a problem are cut up (host and device).
 struct Plan {
@@ -580,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return *reinterpret_cast<Unit*>(smem + Lay::kUnits + (k & 1) * kUnitBytes);
   };
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (see elect_one)
   const int lane = threadIdx.x & 31;
   // the kernel that joins the pieces may take its place on the GPU; it waits
   // for this one's end before it reads
@@ -636,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsLow>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
       // ===================== TMA producer
       int nk = 0, nv = 0;  // K / V tiles whose loads were issued
       int early = 0;       // of the first piece, before its own lengths are known
@@ -716,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         make_unit(p, reached, share_end, unit_at(k));
         if (lane == 0) mbar_arrive(&bars[Lay::bUnitFull + (k & 1)]);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
       // ===================== MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
@@ -980,13 +995,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        float mx = -INFINITY;
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (one chain: 829 us, this 803)
 #pragma unroll
         for (int q = 0; q < kTile / 32; ++q) {
           if (dead & (1u << q)) continue;
 #pragma unroll
-          for (int c = q * 32; c < q * 32 + 32; c += 2) mx = fmax3(mx, sv[c], sv[c + 1]);
+          for (int c = q * 32; c < q * 32 + 32; c += 2)
+            mx4[c / 2 % 4] = fmax3(mx4[c / 2 % 4], sv[c], sv[c + 1]);
         }
+        const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
         // scores stay unscaled: the scale is positive, so the row max of the
         // scaled scores is the scaled max, and each exponent below takes the
         // scale in one fused multiply-add
@@ -996,22 +1013,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        // (a row without a key so far has O = 0)
-        if (t > 0 && __any_sync(0xffffffffu, need && m_ref != -INFINITY)) {
-          // O holds the PVs so far, scaled by the old reference
-          const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
+        if (__any_sync(0xffffffffu, need)) {
+          // (a row without a key so far has O = 0)
+          if (t > 0 && __any_sync(0xffffffffu, need && m_ref != -INFINITY)) {
+            // O holds the PVs so far, scaled by the old reference
+            const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld32(tmem + lane_base + colO + c * 32, o);
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(tmem + lane_base + colO + c * 32, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= alpha;
-            tmem_st32(tmem + lane_base + colO + c * 32, o);
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tmem_st32(tmem + lane_base + colO + c * 32, o);
+            }
           }
-        }
-        if (need) {
-          l *= exp2f(m_ref - m_new);  // 0 when m_ref was -inf
-          m_ref = m_new;
+          if (need) {
+            l *= exp2f(m_ref - m_new);  // 0 when m_ref was -inf
+            m_ref = m_new;
+          }
         }
         const float mref_safe = (m_ref == -INFINITY) ? 0.f : m_ref;
         // exponent arguments and the row sum two lanes per instruction

@@ -112,7 +112,10 @@ typedef struct {
 /* bf16 device tensors: q [batch][queries][Hq][d], k_prefix and v_prefix
  * [prefix_len][Hkv][d] (NULL allowed when prefix_len is 0), k_own and v_own
  * [batch][own_max][Hkv][d] and own_len int32 [batch], 4-byte aligned (all
- * three NULL allowed when own_max is 0).  Strides as in csbp_inputs, in that
+ * three NULL allowed when own_max is 0).  The work is cut up as if own_len were
+ * about half of own_max: an own_max near the longest length in use (smaller than
+ * the tensor's rows by its batch stride) is faster than a far larger one.
+ * Strides as in csbp_inputs, in that
  * order; the batch strides of the prefix are not read.  batch x the batch
  * stride of q stays within 2^34 elements, batch x queries x Hq below 2^30.  */
 typedef struct {

@@ -418,6 +418,21 @@ def test_row_tiles_without_a_key(d):
     check_attn(out, t, lens, False, d ** -0.5)
 
 
+@pytest.mark.parametrize("B,n,Lp,S,Hq,Hkv,d", [
+    (16, 1, 1500, 3000, 8, 2, 128), (1, 1, 0, 5000, 2, 2, 64), (40, 3, 700, 1000, 6, 1, 64)])
+@pytest.mark.parametrize("lens", ["none", "few", "one", "all"])
+def test_room_for_more_keys(B, n, Lp, S, Hq, Hkv, d, lens):
+    """Where the own tiles are cut by lengths that only the device knows."""
+    lens = {"none": [0] * B, "few": [b % 7 for b in range(B)],
+            "one": [0] * (B - 1) + [S], "all": [S - b for b in range(B)]}[lens]
+    t = attn_inputs(B, n, Lp, S, Hq, Hkv, d, 23)
+    a = csbp.PrefixAttention(B, n, Lp, S, Hq, Hkv, d)
+    a.ws[256:] = 0x7f          # what a partial holds that nobody wrote
+    out = a.forward(**t, own_len=i32(lens))
+    a.check()
+    check_attn(out, t, lens, False, d ** -0.5)
+
+
 def test_attention_strides():
     """q, k and v as views into packed projections; the prefix as a slice of a
     longer cache."""
