@@ -37,8 +37,8 @@
 // not finite, the rows it reached are summed again at the end of the share.
 //
 // Bound.  Long prefixes with enough rows: the chain S -> softmax -> P V of a slot
-// and the issuer's barriers, as in the training forward (tensor pipe 49 % active
-// at d = 128, 30 % at 64; issue slots 33 % and 40 %).  Few rows: HBM.  Small
+// and the issuer's barriers, as in the training forward (tensor pipe 55 % active
+// at d = 128, 34 % at 64; issue slots 35 % and 44 %).  Few rows: HBM.  Small
 // calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
 //   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   802 us, 1370 TFLOP/s
 //     (0.71 of the measured bf16 rate); heads of 64       623 us
@@ -280,7 +280,7 @@ struct PrefixLayout {
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
   // P of slot s: D = 64 leaves columns for it, where it is not over its S and the
   // next S need not wait for the PV (a million keys, 16 tokens of 4 sequences and
-  // 32 heads: 778 -> 695 us; 65536 keys, 32 rows a KV head: 44 -> 46 us)
+  // 32 heads: 623 us, 685 with P over S)
   static constexpr bool kOwnP = D == 64;
   static constexpr uint32_t kColP = kOwnP ? kColO + 2 * D : 0;
   static constexpr uint32_t kStepP = kOwnP ? kTile / 2 : kTile;
@@ -293,10 +293,9 @@ __device__ __forceinline__ int prefix_before(const Plan& pl, int np, uint32_t x)
   return min(np, static_cast<int>(static_cast<float>(x) * pl.inv_prefix * static_cast<float>(np)));
 }
 // An own tile that comes while the other slot has none left takes longer than one
-// that has its turn with the other slot's (4,500 against 2,500 cycles where one
-// warp has rows in it).  64 x 1 queries over up to 2,048 own keys: 92 us with
-// equal counts, 73 counting such a tile 1.25, 66 with 1.4, 66 with 1.5, 70 with
-// 1.75; 24 x 16 over up to 8,192: 76, 71, 72, 73, 76.
+// that has its turn with the other slot's.  It counts kAlone of one: 64 x 1 queries
+// over up to 2,048 own keys take 78 us with 1, 68 with 1.2, 62 with 1.4, 63 with
+// 1.6; 24 x 16 over up to 8,192 72, 69, 66, 69.
 constexpr float kAlone = 1.4f;
 __device__ __forceinline__ int tiles_before(const Plan& pl, int np, int in_turn, int alone,
                                             uint32_t x) {
@@ -1338,7 +1337,7 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
   both = static_cast<int64_t>(pl.seq_rows) * (kTile / both);
   const int64_t meets = pl.row_tiles + p.batch - (rows + both - 1) / both;
   // Lengths, in eighths of the time of a key tile read by one slot (1.1 to 1.4
-  // us measured, D = 128): a prefix key tile of two slots takes 13 (1.9 us), the
+  // us measured, D = 128): a prefix key tile of two slots takes 13 (1.8 us), the
   // start and the end of a piece 40.  Own keys count as 5/8 of the room for
   // them.
   constexpr int64_t kOne = 8, kTwo = 13, kEnds = 40, kJoin = 36;
