@@ -42,7 +42,7 @@
 // calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
 //   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   802 us, 1370 TFLOP/s
 //     (0.71 of the measured bf16 rate); heads of 64       623 us
-//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   169 us
+//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   166 us
 //   65,536 keys, 8 x 1 queries, 32 / 8 heads   46.8 us, 5.7 TB/s (0.85 of a copy)
 //   8,192 keys, 8 x 1 queries, 32 / 8 heads    17.4 us
 // A kernel without tensor cores took 41,000 us at the second and 7,200 at 8192
@@ -124,7 +124,6 @@ struct Plan {
   int32_t row_tiles;      // per head group
   int32_t pairs;          // jobs per head group
   int32_t parts;          // most pieces of a job
-  int32_t cut;            // 1: some job has more than one piece
   int32_t ctas;           // shares
   // the list: jobs of equal length in units of time, the first `len_prefix` of
   // each for its prefix tiles and the rest for the own tiles
@@ -134,7 +133,7 @@ struct Plan {
   uint64_t step;
   float inv_step;
   float inv_prefix, inv_own;
-  Divisor by_gs, by_queries, by_seq_rows, by_pairs, by_len, by_heads, by_per_kv;
+  Divisor by_gs, by_queries, by_seq_rows, by_pairs, by_len, by_per_kv;
 
   // start of share c; a cut that would leave a piece shorter than `snap` moves to
   // the end of the job
@@ -152,10 +151,14 @@ struct Plan {
     while (share(c + 1) <= x) ++c;
     return c;
   }
-  // pieces that a job is cut into
-  __host__ __device__ int pieces(uint32_t job) const {
-    return share_of(job * len + len - 1) - share_of(job * len) + 1;
-  }
+};
+
+// The jobs that are cut and how many pieces each has; at most one per cut.
+struct CutJobs {
+  static constexpr int kMost = 255;  // as many CTAs, and pieces
+  int32_t n;
+  uint32_t job[kMost];
+  uint8_t parts[kMost];
 };
 
 struct PrefixParams {
@@ -1230,35 +1233,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces' partials: W warps per (query, head) row, each for every
-// W-th piece.  Lanes hold the pieces' LSE in turn for the maximum and the
-// weights, then d / 32 features each, with the loads of kBatch pieces in
-// flight.  It is launched while the attention kernel still runs and waits for
-// its end here, so its own start costs nothing.
+// Joins the pieces' partials: blockIdx.y is a cut job, and W warps work on a
+// (query, head) row of it, each on every W-th piece.  Lanes hold the pieces' LSE in
+// turn for the maximum and the weights, then d / 32 features each, with the loads of
+// kBatch pieces in flight; the first of them are issued before the LSE is there.
+// It is launched while the attention kernel still runs and waits for its end here,
+// so its own start costs nothing.  It adds 9 us to 157 at 16 x 32 queries over
+// 16,384 keys and 10 to 141 at 64 x 64 over 2,048 (12 and 32 with warps for the
+// rows of all jobs, which had to find their pieces), 2 to 3 to the smallest calls.
 template <int D, int W>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
+__global__ void __launch_bounds__(256)
+    prefix_merge_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CutJobs cut) {
   constexpr int kN = D / 32, kBatch = W == 1 ? 4 : 8;
   struct alignas(kN * 4) Part {
     float x[kN];
   };
   __shared__ Part joined[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = p.batch * p.queries * p.Hq;
-  const int r = blockIdx.x * (8 / W) + warp / W;
-  if (r >= rows) return;
-  // the row's job and its pieces
   const Plan& pl = p.plan;
-  const uint32_t token = pl.by_heads(r);
-  const uint32_t h = r - token * p.Hq;
-  const uint32_t group = pl.by_gs(h);
-  const uint32_t flat = token * pl.gs + (h - group * pl.gs);
-  const int parts = pl.pieces(group * pl.pairs + flat / (2 * kTile));
+  const uint32_t job = cut.job[blockIdx.y];
+  const int parts = cut.parts[blockIdx.y];
+  const uint32_t group = pl.by_pairs(job);
+  const int i = blockIdx.x * (8 / W) + warp / W;  // row of the job
+  const int flat = static_cast<int>(job - group * pl.pairs) * (2 * kTile) + i;
+  if (i >= 2 * kTile || flat >= p.batch * pl.seq_rows) return;
+  const uint32_t token = pl.by_gs(flat);
+  const uint32_t h = group * pl.gs + (flat - token * pl.gs);
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
+  const int64_t r = static_cast<int64_t>(token) * p.Hq + h;
+  const Part* part = reinterpret_cast<const Part*>(p.part_o + r * D) + lane;
+  const int64_t step = rows * 32;  // from a piece to the next
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (parts == 1) return;  // stored already
+  Part v[kBatch];
+  const int first = warp % W;
+#pragma unroll
+  for (int t = 0; t < kBatch; ++t)
+    if (first + t * W < min(parts, 32)) v[t] = part[(first + t * W) * step];
   float top = -INFINITY;
 #pragma unroll 1
-  for (int k = lane; k < parts; k += 32)
-    top = fmaxf(top, p.part_lse[static_cast<int64_t>(k) * rows + r]);
+  for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_lse[k * rows + r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -INFINITY ? 0.f : top;
@@ -1266,30 +1279,26 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
   float sum = 0.f;
 #pragma unroll 1
   for (int k0 = 0; k0 < parts; k0 += 32) {
-    const float zk =
-        k0 + lane < parts ? p.part_lse[static_cast<int64_t>(k0 + lane) * rows + r] : -INFINITY;
+    const float zk = k0 + lane < parts ? p.part_lse[(k0 + lane) * rows + r] : -INFINITY;
     const float w = expf(zk - ref);
     sum += w;
     const int n = min(32, parts - k0);
 #pragma unroll 1
-    for (int k1 = warp % W; k1 < n; k1 += kBatch * W) {
-      Part v[kBatch];
-      float wk[kBatch];
+    for (int k1 = first; k1 < n; k1 += kBatch * W) {
+      if (k0 + k1 > first) {
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t)
+          if (k1 + t * W < n) v[t] = part[(k0 + k1 + t * W) * step];
+      }
 #pragma unroll
       for (int t = 0; t < kBatch; ++t) {
         const int k = k1 + t * W;
-        wk[t] = __shfl_sync(0xffffffffu, w, k & 31);
-        if (k >= n) wk[t] = 0.f;
+        const float wk = __shfl_sync(0xffffffffu, w, k & 31);
         // a piece without a key of this row left no partial
-        v[t] = Part{};
-        if (wk[t] > 0.f)
-          v[t] = reinterpret_cast<const Part*>(
-              p.part_o + (static_cast<int64_t>(k0 + k) * rows + r) * D)[lane];
+        if (k >= n || wk == 0.f) continue;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) acc.x[c] = fmaf(wk, v[t].x[c], acc.x[c]);
       }
-#pragma unroll
-      for (int t = 0; t < kBatch; ++t)
-#pragma unroll
-        for (int c = 0; c < kN; ++c) acc.x[c] = fmaf(wk[t], v[t].x[c], acc.x[c]);
     }
   }
 #pragma unroll
@@ -1309,7 +1318,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
   } out;
 #pragma unroll
   for (int c = 0; c < kN; c += 2) out.x[c / 2] = pack_bf16x2(acc.x[c] * inv, acc.x[c + 1] * inv);
-  reinterpret_cast<Out*>(p.o + static_cast<int64_t>(r) * D)[lane] = out;
+  reinterpret_cast<Out*>(p.o + r * D)[lane] = out;
   if (lane == 0) {
     const uint32_t b = pl.by_queries(token);
     p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + (token - b * p.queries)] =
@@ -1319,7 +1328,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
 
 // How the problem is cut up on a GPU with `sms` SMs; false if it is too large
 // for 32-bit places in the list.
-bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
+bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl, CutJobs& cut) {
   const int G = p.Hq / p.Hkv;
   pl.gs = G;
   while (pl.gs > kTile || G % pl.gs != 0) --pl.gs;  // the largest divisor up to 128
@@ -1347,7 +1356,7 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
   int64_t total = jobs * len;
   // a share of at least two key tiles
   pl.ctas = static_cast<int32_t>(std::max<int64_t>(
-      1, std::min<int64_t>(sms, (total - jobs * kEnds) / (2 * kOne))));
+      1, std::min<int64_t>(std::min(sms, CutJobs::kMost), (total - jobs * kEnds) / (2 * kOne))));
   // Whole jobs, one per CTA, where that ends as soon: a cut costs the joining
   // of its pieces (5 us, the second kernel).  More CTAs than SMs then start as
   // others end.
@@ -1369,7 +1378,6 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
   pl.by_seq_rows = Divisor::of(pl.seq_rows);
   pl.by_pairs = Divisor::of(pl.pairs);
   pl.by_len = Divisor::of(pl.len);
-  pl.by_heads = Divisor::of(p.Hq);
   pl.by_per_kv = Divisor::of(G / pl.gs);  // row groups of a KV head
   pl.snap = 0;
   if (whole) {
@@ -1381,19 +1389,17 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl) {
     pl.snap = static_cast<uint32_t>(std::min<int64_t>(kEnds, total / pl.ctas / 3));
   }
   pl.inv_step = static_cast<float>(4294967296.0 / static_cast<double>(pl.step));
-  // the most cuts inside one job
+  // the cuts inside jobs
   pl.parts = 1;
-  pl.cut = 0;
-  uint32_t job = 0;
-  for (int c = 1, parts = 1; !whole && c < pl.ctas; ++c) {
-    const uint32_t x = pl.share(c);
-    if (pl.by_len(x) != job) {
-      job = pl.by_len(x);
-      parts = 1;
-    }
+  cut.n = 0;
+  for (int c = 1; !whole && c < pl.ctas; ++c) {
+    const uint32_t x = pl.share(c), job = pl.by_len(x);
     if (x == job * pl.len) continue;
-    pl.cut = 1;
-    pl.parts = std::max(pl.parts, ++parts);
+    if (cut.n == 0 || cut.job[cut.n - 1] != job) {
+      cut.job[cut.n] = job;
+      cut.parts[cut.n++] = 1;
+    }
+    pl.parts = std::max<int32_t>(pl.parts, ++cut.parts[cut.n - 1]);
   }
   return true;
 }
@@ -1409,16 +1415,17 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 size_t part_lse_offset(const csbp_prefix_problem& p, const Plan& pl) {
   const size_t rows = static_cast<size_t>(p.batch) * p.queries * p.Hq;
-  return kStatusBytes + (pl.cut ? round256(pl.parts * rows * p.d * 4) : 0);
+  return kStatusBytes + (pl.parts > 1 ? round256(pl.parts * rows * p.d * 4) : 0);
 }
 
 size_t workspace_bytes(const csbp_prefix_problem& p, const Plan& pl) {
   const size_t rows = static_cast<size_t>(p.batch) * p.queries * p.Hq;
-  return part_lse_offset(p, pl) + (pl.cut ? round256(pl.parts * rows * 4) : 0);
+  return part_lse_offset(p, pl) + (pl.parts > 1 ? round256(pl.parts * rows * 4) : 0);
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, const CutJobs& cut,
+                   cudaStream_t stream) {
   using Lay = PrefixLayout<D>;
   // the shared-memory limit is a per-device attribute: set it once on each
   // device, and read the kernel's register count there
@@ -1446,8 +1453,9 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, cudaStream_t 
                                                               p);
   e = cudaGetLastError();
   timer_end(timed, stream);
-  if (e != cudaSuccess || !p.plan.cut) return e;
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.queries * p.Hq;
+  if (e != cudaSuccess || cut.n == 0) return e;
+  const int per_job = std::min(2 * kTile, p.batch * p.plan.seq_rows);
+  const int64_t rows = static_cast<int64_t>(cut.n) * per_job;
   // few rows have many pieces (the keys were split to fill the GPU): more warps
   // to a row, up to about 32 warps per SM in all
   const int warps = rows <= 608 ? 8 : rows <= 8192 ? 2 : 1;
@@ -1455,15 +1463,15 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, cudaStream_t 
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows * warps + 7) / 8));
+  cfg.gridDim = dim3(static_cast<unsigned>((per_job * warps + 7) / 8), static_cast<unsigned>(cut.n));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   const int joined = timer_begin(14, stream);
-  e = warps == 8   ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p)
-      : warps == 2 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 2>, p)
-                   : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p);
+  e = warps == 8   ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p, cut)
+      : warps == 2 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 2>, p, cut)
+                   : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p, cut);
   timer_end(joined, stream);
   return e;
 }
@@ -1544,7 +1552,8 @@ extern "C" size_t csbp_prefix_workspace_bytes(const csbp_prefix_problem* problem
   int sms = 0;
   if (!device_sms(sms)) sms = 152;  // no GPU: the GB300's count
   Plan pl{};
-  return make_plan(*problem, sms, pl) ? workspace_bytes(*problem, pl) : 0;
+  CutJobs cut;
+  return make_plan(*problem, sms, pl, cut) ? workspace_bytes(*problem, pl) : 0;
 }
 
 extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
@@ -1563,7 +1572,8 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   int sms = 0;
   if (!device_sms(sms)) return CSBP_ERR_CUDA;
   Plan pl{};
-  if (!make_plan(p, sms, pl)) return CSBP_ERR_UNSUPPORTED;
+  CutJobs cut{};
+  if (!make_plan(p, sms, pl, cut)) return CSBP_ERR_UNSUPPORTED;
   if (ws_bytes < workspace_bytes(p, pl)) return CSBP_ERR_WORKSPACE;
   CUtensorMap maps[4] = {};  // prefix K and V, own K and V
   if (p.prefix_len > 0 && (!kv_map(&maps[0], t, 1, p, p.prefix_len, 1) ||
@@ -1602,7 +1612,7 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.part_lse = reinterpret_cast<float*>(ws + part_lse_offset(p, pl));
   a.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p.d == 128 ? launch<128>(maps, a, s)
-                                   : launch<64>(maps, a, s);
+  const cudaError_t e = p.d == 128 ? launch<128>(maps, a, cut, s)
+                                   : launch<64>(maps, a, cut, s);
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }
