@@ -41,7 +41,7 @@
 // at d = 128, 34 % at 64; issue slots 35 % and 44 %).  Few rows: HBM.  Small
 // calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
 //   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   802 us, 1370 TFLOP/s
-//     (0.71 of the measured bf16 rate); heads of 64       623 us
+//     (0.71 of the measured bf16 rate); heads of 64       604 us
 //   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   166 us
 //   65,536 keys, 8 x 1 queries, 32 / 8 heads   46.8 us, 5.7 TB/s (0.85 of a copy)
 //   8,192 keys, 8 x 1 queries, 32 / 8 heads    17.4 us
@@ -283,7 +283,7 @@ struct PrefixLayout {
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
   // P of slot s: D = 64 leaves columns for it, where it is not over its S and the
   // next S need not wait for the PV (a million keys, 16 tokens of 4 sequences and
-  // 32 heads: 623 us, 685 with P over S)
+  // 32 heads: 604 us; 685 with P over S)
   static constexpr bool kOwnP = D == 64;
   static constexpr uint32_t kColP = kOwnP ? kColO + 2 * D : 0;
   static constexpr uint32_t kStepP = kOwnP ? kTile / 2 : kTile;
@@ -926,15 +926,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The last PV read the P columns and wrote O (P over S: this S was
         // issued after it).
         const auto pv_done = [&]() -> bool {
-          if (n_mine + t == 0) return true;
+          if (!Lay::kOwnP || n_mine + t == 0) return true;
           const bool done =
               mbar_wait_warp(&bars[Lay::bPvDone + s], (n_mine + t - 1) & 1, p.status, abort_flag);
           tc_fence_after_sync();
           return done;
         };
-        // (a slot that takes every second tile has its S issued after that PV)
-        if (Lay::kOwnP && step == 2) ok = pv_done();
-        if (!ok || !mbar_wait_warp(&bars[Lay::bSFull + s], (n_mine + t) & 1, p.status, abort_flag)) {
+        if (!mbar_wait_warp(&bars[Lay::bSFull + s], (n_mine + t) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
@@ -961,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         if (__all_sync(0xffffffffu, hi <= 0)) {  // another sequence's keys: P = 0
-          if (Lay::kOwnP && step == 1 && !pv_done()) {
+          if (!pv_done()) {
             ok = false;
             break;
           }
@@ -1011,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scale in one fused multiply-add
         const float m_new = fmaxf(m_ref, mx * sl2);
         const bool need = m_new > m_ref + kRescaleThreshold;  // false while both are -inf
-        if (Lay::kOwnP && step == 1 && !pv_done()) {
+        if (!pv_done()) {
           ok = false;
           break;
         }
