@@ -1497,6 +1497,9 @@ csbp_status validate(const csbp_prefix_problem* p) {
     return CSBP_ERR_UNSUPPORTED;
   // rows are counted in 32 bits
   if (rows * p->Hq > 0x3fffffff) return CSBP_ERR_UNSUPPORTED;
+  // so are keys, up to the end of their last tile
+  if (p->prefix_len > 0x7fffffff - kTile || p->own_max > 0x7fffffff - kTile)
+    return CSBP_ERR_UNSUPPORTED;
   return CSBP_OK;
 }
 

@@ -103,7 +103,7 @@ csbp_status csbp_cache_read(const csbp_kv_cache* cache, const csbp_cache_rows* r
  * rows at and past c, later keys, other sequences' keys), NaN included.     */
 typedef struct {
   int32_t batch, queries;       /* >= 1                                     */
-  int32_t prefix_len, own_max;  /* >= 0                                     */
+  int32_t prefix_len, own_max;  /* >= 0, below 2^31 - 128                   */
   int32_t Hq, Hkv, d;           /* Hq % Hkv == 0; d 64 or 128               */
   int32_t causal;
   float scale;                  /* > 0, finite                              */

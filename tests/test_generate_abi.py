@@ -162,11 +162,16 @@ def test_prefix_outputs_and_workspace_are_checked():
 
 
 def test_prefix_sizes_past_the_counters_are_unsupported():
-    """q in 16-byte units within 32 bits, rows within 2^30."""
+    """q in 16-byte units within 32 bits, rows within 2^30, keys within 2^31."""
     big = prefix_inputs()
     big.stride_batch[0] = 1 << 33
     assert attn(prefix(batch=3), big) == UNSUPPORTED
     assert attn(prefix(batch=1 << 20, queries=1 << 10), prefix_inputs()) == UNSUPPORTED
+    for kw in (dict(prefix_len=(1 << 31) - 1), dict(own_max=(1 << 31) - 100, batch=1)):
+        p = prefix(Hq=1, Hkv=1, **kw)
+        assert csbp.prefix_workspace_bytes(p) == 0
+        assert attn(p, prefix_inputs()) == UNSUPPORTED
+    assert csbp.prefix_workspace_bytes(prefix(Hq=1, Hkv=1, prefix_len=(1 << 31) - 200)) > 256
 
 
 def verify(pr, p=PTR, q=PTR, token=PTR, u=PTR, r=PTR, length=None, acc=PTR, out=PTR):
