@@ -315,6 +315,23 @@ def _inputs(inputs):
                   (ctypes.c_int64 * 6)(*bat))
 
 
+def _fresh(stream, make):
+    """The tensors that make() allocates (and fills) for a call on `stream`, in a
+    tuple or dict.  They come from the stream that the call runs on: on the
+    current one, where that is another, a fill or an earlier user of the memory
+    could still be waiting and land after the kernel.  The current stream, where
+    the caller goes on, keeps them allocated until it has done with them too."""
+    import torch
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        out = make()
+    for t in out.values() if isinstance(out, dict) else out:
+        if t is not None and t.is_cuda:
+            t.record_stream(torch.cuda.current_stream(t.device))
+    return out
+
+
 def _stream_ptr(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -759,8 +776,9 @@ class QuantCache:
             if rows is None or table is None:
                 raise ValueError("csbp_cache_read: needs `rows` or `out`")
             shape = (table.shape[0], rows, self.Hkv, self.d)
-            out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=self.k.device)
-                        for _ in range(2))
+            out = _fresh(stream, lambda: tuple(
+                torch.zeros(shape, dtype=torch.bfloat16, device=self.k.device)
+                for _ in range(2)))
         self._call("csbp_cache_read", out[0], out[1], table, start, count, stream)
         return out
 
@@ -805,7 +823,7 @@ class PrefixAttention:
                 torch.empty((p.batch, p.Hq, p.queries), dtype=torch.float32, device=self.device))
 
     def forward(self, q, k_prefix, v_prefix, k_own, v_own, own_len, out=None, stream=None):
-        o, lse = out if out is not None else self.alloc_outputs()
+        o, lse = out if out is not None else _fresh(stream, self.alloc_outputs)
         attn_prefix(self.problem, q, k_prefix, v_prefix, k_own, v_own, own_len, o, lse, self.ws,
                     stream, made_here=out is None)
         return o, lse
@@ -922,7 +940,8 @@ def draft_verify(p, q, token, u, r, length=None, out=None, stream=None):
                                     (p, q, token, u, r, length, accepted, tokens), check)
     if out is None:
         import torch
-        accepted, tokens = (torch.empty(s, dtype=torch.int32, device=p.device) for s in shapes)
+        accepted, tokens = _fresh(stream, lambda: tuple(
+            torch.empty(s, dtype=torch.int32, device=p.device) for s in shapes))
     if prob.batch:
         _run("csbp_draft_verify", dev, stream,
              (p, r, length, accepted, tokens) + ((q, token, u) if K else ()),

@@ -1,0 +1,129 @@
+"""Calls on a stream that is named, while the current stream is busy: what the
+binding allocates and fills belongs to the named stream, and what a handle
+filled when it was made is there for any stream.
+
+Every check is bit by bit against the same call on the current stream.  The
+current stream is kept busy with matrix products, long enough (tens of
+milliseconds) that a fill behind them would land after the kernel.
+"""
+import pytest
+import torch
+
+from block_diffusion_lm_gb300 import csbp
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from block_diffusion_lm_gb300 import build
+    build.build()
+
+
+@pytest.fixture(scope="module")
+def busy():
+    """Keeps the current stream busy for some tens of milliseconds."""
+    x = torch.zeros((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+
+    def run():
+        for _ in range(50):
+            torch.mm(x, x, out=y)
+
+    run()
+    torch.cuda.synchronize()
+    return run
+
+
+def normal(seed, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def pending_blocks(like, busy):
+    """Free memory of the sizes of `like` whose last user, a fill, waits behind
+    the current stream's work."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = [torch.empty_like(t) for t in like]
+    busy()
+    for t in old:
+        t.fill_(7)
+
+
+def flat(x):
+    """The tensors of an output (tuples, dicts, None)."""
+    if x is None:
+        return []
+    if isinstance(x, dict):
+        return [t for k in sorted(x) for t in flat(x[k])]
+    return [x] if isinstance(x, torch.Tensor) else [t for y in x for t in flat(y)]
+
+
+def on_a_named_stream(call, busy):
+    """`call(stream)` allocates its outputs; compared with `call(None)`."""
+    want = [t.clone() for t in flat(call(None))]
+    pending_blocks(want, busy)
+    side = torch.cuda.Stream()
+    got = flat(call(side))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got, strict=True):
+        assert torch.equal(a, b)
+    # and the memory stays with the reader on the current stream
+    got = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    busy()
+    seen = [t.clone() for t in flat(got)]
+    shapes = [t.shape for t in flat(got)]
+    types = [t.dtype for t in flat(got)]
+    del got
+    with torch.cuda.stream(side):
+        for s, d in zip(shapes, types):
+            torch.empty(s, dtype=d, device="cuda").fill_(9)
+    torch.cuda.synchronize()
+    for a, b in zip(want, seen, strict=True):
+        assert torch.equal(a, b)
+
+
+# ------------------------------------------------------ generation operators
+def filled_cache(B, rows, page, Hkv, d, seed):
+    n = -(-rows // page)
+    c = csbp.QuantCache(B * n, page, Hkv, d)
+    table = torch.arange(B * n, device="cuda").int().view(B, n)
+    c.write(normal(seed, B, rows, Hkv, d), normal(seed + 1, B, rows, Hkv, d), table, i32([0] * B))
+    return c, table
+
+
+@pytest.mark.parametrize("B,rows", [(3, 40), (2, 5000)])
+def test_cache_read(B, rows, busy):
+    c, table = filled_cache(B, rows, 16, 4, 128, 1)
+    start, count = i32([0] * B), i32([rows - 3 * b for b in range(B)])
+    on_a_named_stream(lambda st: c.read(table, start, count, rows=rows, stream=st), busy)
+
+
+@pytest.mark.parametrize("B,n", [(2, 3), (16, 64)])
+def test_prefix_attention(B, n, busy):
+    Lp, S, Hq, Hkv, d = 2000, 100, 8, 2, 128
+    a = csbp.PrefixAttention(B, n, Lp, S, Hq, Hkv, d)
+    args = (normal(3, B, n, Hq, d), normal(4, Lp, Hkv, d), normal(5, Lp, Hkv, d),
+            normal(6, B, S, Hkv, d), normal(7, B, S, Hkv, d), i32([S - b for b in range(B)]))
+    on_a_named_stream(lambda st: a.forward(*args, stream=st), busy)
+
+
+@pytest.mark.parametrize("B,K", [(3, 4), (700, 900)])
+def test_draft_verify(B, K, busy):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    V = 33
+    p = torch.rand((B, K + 1, V), generator=g, device="cuda")
+    q = torch.rand((B, K, V), generator=g, device="cuda")
+    x = torch.randint(0, V, (B, K), generator=g, device="cuda").int()
+    u, r = (torch.rand(s, generator=g, device="cuda") for s in ((B, K), (B,)))
+    on_a_named_stream(lambda st: csbp.draft_verify(p, q, x, u, r, stream=st), busy)
