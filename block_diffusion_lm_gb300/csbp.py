@@ -332,6 +332,18 @@ def _fresh(stream, make):
     return out
 
 
+def _zeros(shape, device):
+    """Zeroed bytes that a handle keeps, ready for any stream: the host waits
+    for the fill, once per handle.  (Under capture the fill is part of the graph.)"""
+    import torch
+    t = torch.zeros(shape, dtype=torch.uint8, device=device)
+    if t.is_cuda:
+        with torch.cuda.device(t.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+    return t
+
+
 def _stream_ptr(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -711,8 +723,7 @@ class QuantCache:
         code = (pages, page_size, Hkv, d)
         scale = (pages, page_size, Hkv, d // 32)
         if storage is None:
-            storage = [torch.zeros(s, dtype=torch.uint8, device=device)
-                       for s in (code, code, scale, scale)]
+            storage = [_zeros(s, device) for s in (code, code, scale, scale)]
         self.k, self.v, self.k_scale, self.v_scale = storage
         c = _Call("QuantCache")
         self._tensors = list(zip(("k", "v", "k_scale", "v_scale"), storage))
@@ -812,7 +823,7 @@ class PrefixAttention:
             n = prefix_workspace_bytes(self.problem)
         if n == 0:
             raise CsbpError("csbp_prefix_workspace_bytes", -1)
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.ws = _zeros(n, device)
         self.device = self.ws.device
 
     def alloc_outputs(self):

@@ -127,3 +127,55 @@ def test_draft_verify(B, K, busy):
     x = torch.randint(0, V, (B, K), generator=g, device="cuda").int()
     u, r = (torch.rand(s, generator=g, device="cuda") for s in ((B, K), (B,)))
     on_a_named_stream(lambda st: csbp.draft_verify(p, q, x, u, r, stream=st), busy)
+
+
+# ------------------------------------------------- handles made while busy
+def test_a_new_cache_is_ready_for_another_stream(busy):
+    k, v = normal(10, 2, 40, 2, 64), normal(11, 2, 40, 2, 64)
+    table, start = torch.arange(6, device="cuda").int().view(2, 3), i32([0, 0])
+    old = csbp.QuantCache(6, 16, 2, 64)
+    old.write(k, v, table, start)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    new = csbp.QuantCache(6, 16, 2, 64)
+    new.write(k, v, table, start, stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip((old.k, old.v, old.k_scale, old.v_scale),
+                    (new.k, new.v, new.k_scale, new.v_scale)):
+        assert torch.equal(a, b)
+
+
+def test_a_new_workspace_is_ready_for_another_stream(busy):
+    """Its status word above all: the memory held something else before."""
+    shape = (2, 3, 4096, 130, 8, 2, 128)
+    args = (normal(12, 2, 3, 8, 128), normal(13, 4096, 2, 128), normal(14, 4096, 2, 128),
+            normal(15, 2, 130, 2, 128), normal(16, 2, 130, 2, 128), i32([130, 7]))
+    first = csbp.PrefixAttention(*shape)
+    want = first.forward(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # (not the default stream: the status word is read behind its work anyway)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        before = torch.full_like(first.ws, 1)
+        torch.cuda.synchronize()
+        del before
+        busy()
+        a = csbp.PrefixAttention(*shape)
+        out = a.forward(*args, stream=side)
+        a.check(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, out))
+
+
+def test_a_handle_can_be_made_under_capture():
+    q, k, v = normal(17, 1, 2, 2, 64), normal(18, 300, 2, 64), normal(19, 300, 2, 64)
+    want = csbp.PrefixAttention(1, 2, 300, 0, 2, 2, 64).forward(q, k, v, None, None, None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = csbp.PrefixAttention(1, 2, 300, 0, 2, 2, 64)
+        got = a.forward(q, k, v, None, None, None)
+    graph.replay()
+    a.check()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
