@@ -429,7 +429,8 @@ def e4m3_to_bf16(x, scale: float, out=None, stream=None):
     if not x.is_contiguous():
         raise ValueError("csbp_e4m3_to_bf16: x must be contiguous")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out, = _fresh(stream, lambda: (
+            torch.empty(x.shape, dtype=torch.bfloat16, device=x.device),))
     c.tensor("out", out, torch.bfloat16, tuple(x.shape))
     c.seen.append(("x", x))
     c.done()
@@ -488,8 +489,8 @@ class BlockDiffusionAttention:
         self.block_owner, self.chunk_owner, self.info = bo, co, info
         self.work_host = words
         self.work_dev = torch.from_numpy(words).to(device)
-        self.ws_fwd = torch.zeros(workspace_bytes(self.problem, 0), dtype=torch.uint8, device=device)
-        self.ws_bwd = torch.zeros(workspace_bytes(self.problem, 1), dtype=torch.uint8, device=device)
+        self.ws_fwd = _zeros(workspace_bytes(self.problem, 0), device)
+        self.ws_bwd = _zeros(workspace_bytes(self.problem, 1), device)
         self.device = device
         self.shape = (batch, L, Hq, d)
         self.kv_shape = (batch, L, Hkv, d)
@@ -513,14 +514,14 @@ class BlockDiffusionAttention:
         return g
 
     def forward(self, t, out=None, stream=None):
-        o_clean, o_corr, lse = out if out is not None else self.alloc_outputs()
+        o_clean, o_corr, lse = out if out is not None else _fresh(stream, self.alloc_outputs)
         attn_fwd(self.problem, t, self.work_dev, self.info, o_clean, o_corr, lse, self.ws_fwd,
                  stream)
         return o_clean, o_corr, lse
 
     def backward(self, t, fwd_out, grads=None, stream=None):
         o_clean, o_corr, lse = fwd_out
-        g = grads if grads is not None else self.alloc_grads()
+        g = grads if grads is not None else _fresh(stream, self.alloc_grads)
         attn_bwd(self.problem, t, self.work_dev, self.info, o_clean, o_corr, lse,
                  t.get("do_clean"), t["do_corr"], g, self.ws_bwd, stream)
         return g
@@ -572,12 +573,11 @@ class VocabCrossEntropy:
 
     def __init__(self, rows, d_model, vocab, chunk_rows=0, head_grad=True, grad_scale=1.0,
                  device="cuda"):
-        import torch
         self.problem = make_ce_problem(rows, d_model, vocab, chunk_rows, head_grad, grad_scale)
         n = ce_workspace_bytes(self.problem)
         if n == 0:
             raise CsbpError("csbp_ce_workspace_bytes", -1)
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.ws = _zeros(n, device)
         self.device = device
 
     def alloc_outputs(self):
@@ -591,7 +591,7 @@ class VocabCrossEntropy:
         return loss, lse, dh, dw
 
     def __call__(self, h, w, target, out=None, stream=None):
-        loss, lse, dh, dw = out if out is not None else self.alloc_outputs()
+        loss, lse, dh, dw = out if out is not None else _fresh(stream, self.alloc_outputs)
         vocab_ce(self.problem, h, w, target, loss, lse, dh, dw, self.ws, stream)
         return loss, lse, dh, dw
 

@@ -179,3 +179,55 @@ def test_a_handle_can_be_made_under_capture():
     graph.replay()
     a.check()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+# ------------------------------------------------------- training operators
+@pytest.fixture(scope="module")
+def training():
+    """One tile per copy: at most two addends per gradient, so results repeat."""
+    shape = (1, 128, 64, 128)
+    names = ("q_clean", "k_clean", "v_clean", "q_corr", "k_corr", "v_corr", "do_clean", "do_corr")
+    t = {n: normal(30 + i, *shape) for i, n in enumerate(names)}
+    return csbp.BlockDiffusionAttention(1, 128, 16, 64, 64, 128), t
+
+
+def test_training_forward(training, busy):
+    a, t = training
+    on_a_named_stream(lambda st: a.forward(t, stream=st), busy)
+
+
+def test_training_backward(training, busy):
+    a, t = training
+    out = a.forward(t)
+    on_a_named_stream(lambda st: a.backward(t, out, stream=st), busy)
+
+
+def test_vocab_cross_entropy(busy):
+    N, Dm, V = 256, 256, 8192
+    ce = csbp.VocabCrossEntropy(N, Dm, V)
+    h, w = normal(40, N, Dm), normal(41, V, Dm)
+    target = torch.arange(N, device="cuda").int() * 31
+    on_a_named_stream(lambda st: ce(h, w, target, stream=st), busy)
+
+
+def test_e4m3_decode(busy):
+    x = (torch.arange(1 << 21, device="cuda") % 120).to(torch.uint8)
+    on_a_named_stream(lambda st: csbp.e4m3_to_bf16(x, 0.5, stream=st), busy)
+
+
+def test_a_new_training_workspace_is_ready_for_another_stream(training, busy):
+    _, t = training
+    want = training[0].forward(t)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        before = [torch.full_like(w, 1) for w in (training[0].ws_fwd, training[0].ws_bwd)]
+        torch.cuda.synchronize()
+        del before
+        busy()
+        a = csbp.BlockDiffusionAttention(1, 128, 16, 64, 64, 128)
+        out = a.forward(t, stream=side)
+        a.check(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(flat(want), flat(out), strict=True))
