@@ -1175,6 +1175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < D / 2; ++k) o[k] = fmaf(o1[k], w1, o[k]);
             }
+            // without a key O is 0, not 0 times what masked keys left in it
+#pragma unroll
+            for (int k = 0; k < D / 2; ++k) o[k] = l == 0.f ? 0.f : o[k];
 #pragma unroll
             for (int k = 0; k < D / 2; ++k) finite = fmaf(o[k], 0.f, finite);
             if (u.direct) {

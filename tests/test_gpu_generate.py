@@ -771,3 +771,40 @@ def test_each_kernel_kind_is_timed():
         assert read(16, ctypes.byref(ms), ctypes.byref(n)) == -1
     finally:
         csbp.kernel_timing(False)
+
+
+# ------------------------------------- rows without a key, keys not finite
+@pytest.mark.parametrize("name", ["v_own", "k_own"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,n,S,Hq,Hkv,causal,lens,where", [
+    (1, 4, 9, 2, 1, True, [2], (0, 0)),                     # queries before the first key
+    (2, 3, 9, 4, 2, False, [0, 9], (1, 4)),                 # beside a neighbour of the tile
+    (5, 40, 140, 4, 2, True, [30, 140, 0, 7, 0], (0, 0)),   # several row tiles
+    (5, 40, 140, 4, 2, True, [30, 140, 0, 7, 0], (1, 139)),
+    (3, 50, 300, 2, 1, False, [0, 300, 0], (1, 290)),       # the last row tile alone
+    (1, 1000, 5000, 1, 1, True, [400], (0, 3)),             # far more room than keys
+])
+def test_rows_without_a_key_beside_keys_that_are_not_finite(B, n, S, Hq, Hkv, causal, lens, where,
+                                                            d, value, name):
+    """No prefix, so that some rows read no key at all: O = 0 and LSE = -inf
+    whatever the keys of the tile hold, and other rows that do not read the key
+    that is not finite come out as without it."""
+    t = attn_inputs(B, n, 0, S, Hq, Hkv, d, 90)
+    a = csbp.PrefixAttention(B, n, 0, S, Hq, Hkv, d, causal=causal)
+    clean = [x.clone() for x in a.forward(**t, own_len=i32(lens))]
+    check_attn(clean, t, lens, causal, d ** -0.5)
+    b, j = where
+    bad = dict(t)
+    bad[name] = t[name].clone()
+    bad[name][b, j] = value
+    o, lse = a.forward(**bad, own_len=i32(lens))
+    a.check()
+    reads = torch.zeros((B, n), dtype=torch.bool, device="cuda")
+    reads[b] = j <= lens[b] - n + torch.arange(n, device="cuda") if causal else True
+    assert not reads.all() and reads.any()
+    assert not torch.isfinite(o[reads].float()).all() or name == "k_own"
+    o, lse = o.clone(), lse.clone()
+    o[reads] = clean[0][reads]
+    lse = torch.where(reads[:, None], clean[1], lse)
+    check_attn((o, lse), t, lens, causal, d ** -0.5)
