@@ -3,12 +3,14 @@
 
 #include <cstdint>
 
+#include "csbp_internal.h"
+
 namespace csbp {
 
 // Timer kinds (csbp_kernel_timing) after those of csbp_internal.h: 11 cache
 // write, 12 cache read, 13 prefix attention, 14 the joining of its pieces, 15
 // draft verification.
-constexpr int kAllTimerKinds = 16;
+constexpr int kAllTimerKinds = kTimerKinds + 5;
 
 // Encode a 3-D TMA descriptor (a CUtensorMap at `map`) over a bf16 tensor,
 // innermost dimension first: strides[i] is the byte stride of dimension i + 1;
