@@ -4,17 +4,18 @@
 //
 // The answers are whole numbers, so the arithmetic must not depend on the
 // order of summation: u q and p are compared as exact products in 64 bits,
-// and the sums carry about 2^-46 of their value.  64-bit adds run at 1/64 of
-// the 32-bit rate here, so the pass over the vocabulary keeps each lane's sum
-// as an unevaluated pair of fp32 numbers (error-free additions) and only the
-// joining of lanes, and the search inside the one segment that holds the
-// answer, are 64-bit.
+// and the sums are kept to 2^-42 of their value at worst.  64-bit adds run at
+// 1/64 of the 32-bit rate here, so the pass over the vocabulary keeps sums as
+// unevaluated fp32 numbers (error-free additions, Knuth's two-sum) and only the
+// joining of warps, and the search inside the one segment that holds the answer,
+// are 64-bit.
 //
 // A sequence reads two rows of the vocabulary (p and q where its first draft
 // was refused) or one, and answers with a few integers: HBM bounds a full batch
-// (96 sequences of 131,072 tokens 21.6 us, 4.6 TB/s), the chain of three passes,
-// each a load and a joining of warps, a small one (3 of 32,768 tokens 8.1 us).
-// 64-bit sums throughout took 74 us at the first, one CTA per sequence 38.
+// (96 sequences of 131,072 tokens 22.0 us, 4.6 TB/s), the chain of three passes,
+// each a load and a joining of warps, a small one (3 of 32,768 tokens 8.0 us).
+// 64-bit sums throughout took 74 us at the first, one CTA per sequence 38, one
+// running pair per lane, which is less exact, 21.4.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -37,40 +38,60 @@ struct VerifyArgs {
   int32_t *accepted, *out;
 };
 
-// Unevaluated sum hi + lo, |lo| small against hi.
+// Sums of weights w >= 0 are unevaluated: hi + lo in a tree, h + m + l over all
+// of a lane's trees.  How far off they can be, with u = 2^-24 (half a step) and
+// S the sum in question: a leaf has |lo| <= u S, a node of level k
+// |lo| <= (k + 1) u S, and its two roundings of lo lose (2 k + 1) u^2 S at most.
+// So 16 weights lose (3 + 5 + 7 + 9) u^2 S, however many trees follow (the third
+// word keeps them to u^3), the step back to a pair u^2 S, and the five levels of
+// a warp (3 + 5 + 7 + 9 + 11) u^2 S: 60 u^2 = 2^-42.1 in all, for any vocabulary;
+// with roundings of either sign about 2^-47.  (One running pair per lane, whose lo
+// collects the roundings of all its additions, is off by 2^-45 after 256 of them
+// and by 2^-38 after 8,192.)
 struct Pair {
   float hi, lo;
 };
+struct Sum {
+  float h, m, l;
+};
 
-// s += x + e, where e is a rounding remainder of x
-__device__ __forceinline__ void add(Pair& s, float x, float e) {
-  const float t = s.hi + x;
-  const float b = t - s.hi;
-  s.lo += ((s.hi - (t - b)) + (x - b)) + e;
-  s.hi = t;
-}
-
-// The weight max(p - q, 0) as d + e exactly (e the remainder of the rounded
-// difference d); 0 for a NaN.
-__device__ __forceinline__ void add_residual(Pair& s, float p, float q) {
-  const float d = p - q;
-  const float b = d - p;
-  const float e = (p - (d - b)) - (q + b);
-  if (d > 0.f) add(s, d, e);
-}
-
-template <bool kResidual>
-__device__ __forceinline__ void add_weight(Pair& s, float p, float q) {
-  if (kResidual)
-    add_residual(s, p, q);
-  else if (p > 0.f)
-    add(s, p, 0.f);
+// a + b exactly
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float t = a + b;
+  const float x = t - a;
+  return {t, (a - (t - x)) + (b - x)};
 }
 
 // a + b of two such sums
 __device__ __forceinline__ Pair join(Pair a, Pair b) {
-  add(a, b.hi, b.lo);
-  return a;
+  Pair s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;
+}
+
+__device__ __forceinline__ Pair join(const Pair (&a)[4]) {
+  return join(join(a[0], a[1]), join(a[2], a[3]));
+}
+
+// s += x, with |m| <= u h and |l| <= u m kept
+__device__ __forceinline__ void add(Sum& s, Pair x) {
+  const Pair h = two_sum(s.h, x.hi), m = two_sum(s.m, x.lo), e = two_sum(m.hi, h.lo);
+  const float l = s.l + (m.lo + e.lo);
+  s.h = h.hi + e.hi;
+  const float r = e.hi - (s.h - h.hi);
+  s.m = r + l;
+  s.l = l - (s.m - r);
+}
+
+// The weight exactly: p, or max(p - q, 0) as the rounded difference and its
+// remainder.  0 for a NaN.
+template <bool kResidual>
+__device__ __forceinline__ Pair weight(float p, float q) {
+  if (!kResidual) return {p > 0.f ? p : 0.f, 0.f};
+  const float d = p - q;
+  const float x = d - p;
+  const float e = (p - (d - x)) - (q + x);
+  return d > 0.f ? Pair{d, e} : Pair{0.f, 0.f};
 }
 
 // Sum over the warp, in lane 0 (other lanes have partial sums).
@@ -88,33 +109,50 @@ __device__ __forceinline__ double warp_sum(Pair s) {
 template <bool kResidual>
 __device__ __forceinline__ Pair lane_sum(const float* p, const float* q, int64_t v0, int64_t v1,
                                          int lane) {
-  Pair s{0.f, 0.f};
+  Sum s{0.f, 0.f, 0.f};
   const uintptr_t low = reinterpret_cast<uintptr_t>(p + v0) |
                         (kResidual ? reinterpret_cast<uintptr_t>(q + v0) : 0);
-  int64_t v = v0;
+  constexpr int kN = 4;
+  int left = static_cast<int>(v1 - v0);
+  p += v0;
+  q += kResidual ? v0 : 0;
   if ((low & 15u) == 0) {
-    constexpr int kUnroll = 4;
-    for (; v + 128 * kUnroll <= v1; v += 128 * kUnroll) {
-      float4 x[kUnroll], y[kUnroll];
+#pragma unroll 1
+    for (; left >= 128 * kN; left -= 128 * kN, p += 128 * kN, q += kResidual ? 128 * kN : 0) {
+      float4 x[kN], y[kN];
 #pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        x[t] = __ldg(reinterpret_cast<const float4*>(p + v + t * 128) + lane);
-        if (kResidual) y[t] = __ldg(reinterpret_cast<const float4*>(q + v + t * 128) + lane);
+      for (int t = 0; t < kN; ++t) {
+        x[t] = __ldg(reinterpret_cast<const float4*>(p + t * 128) + lane);
+        y[t] = kResidual ? __ldg(reinterpret_cast<const float4*>(q + t * 128) + lane)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      Pair w[kN];
 #pragma unroll
-      for (int t = 0; t < kUnroll; ++t) {
-        if (!kResidual) y[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-        add_weight<kResidual>(s, x[t].x, y[t].x);
-        add_weight<kResidual>(s, x[t].y, y[t].y);
-        add_weight<kResidual>(s, x[t].z, y[t].z);
-        add_weight<kResidual>(s, x[t].w, y[t].w);
+      for (int t = 0; t < kN; ++t) {
+        const Pair four[4] = {weight<kResidual>(x[t].x, y[t].x), weight<kResidual>(x[t].y, y[t].y),
+                              weight<kResidual>(x[t].z, y[t].z), weight<kResidual>(x[t].w, y[t].w)};
+        w[t] = join(four);
       }
+      add(s, join(w));
     }
   }
-#pragma unroll 4
-  for (v += lane; v < v1; v += 32)
-    add_weight<kResidual>(s, __ldg(p + v), kResidual ? __ldg(q + v) : 0.f);
-  return s;
+#pragma unroll 1
+  for (; left >= 32 * kN; left -= 32 * kN, p += 32 * kN, q += kResidual ? 32 * kN : 0) {
+    float x[kN], y[kN];
+#pragma unroll
+    for (int t = 0; t < kN; ++t) {
+      x[t] = __ldg(p + t * 32 + lane);
+      y[t] = kResidual ? __ldg(q + t * 32 + lane) : 0.f;
+    }
+    Pair w[kN];
+#pragma unroll
+    for (int t = 0; t < kN; ++t) w[t] = weight<kResidual>(x[t], y[t]);
+    add(s, join(w));
+  }
+#pragma unroll 1
+  for (int k = lane; k < left; k += 32)
+    add(s, weight<kResidual>(__ldg(p + k), kResidual ? __ldg(q + k) : 0.f));
+  return {s.h, s.m + s.l};
 }
 
 __device__ __forceinline__ Pair lane_sum(const float* p, const float* q, int64_t v0, int64_t v1,
@@ -261,9 +299,9 @@ __device__ int draw(const float* p, const float* q, int V, float r, int rank, Sh
 }
 
 // C CTAs (a cluster) per sequence, each for a part of the vocabulary; all of
-// them judge the drafts.
+// them judge the drafts.  Three CTAs to an SM take 40 registers a thread.
 template <int C>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) draft_verify_kernel(VerifyArgs a) {
   __shared__ Shared sh;
   if (C > 1) cluster_arrive();
   const int64_t b = blockIdx.x / C;

@@ -144,8 +144,8 @@ csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem, const csbp_pref
  * The next token comes from w_v = max(p_a(v) - q_a(v), 0) when a < n (from
  * p_a when that is 0 everywhere), from p_n when a = n: the smallest v with
  * w_0 + .. + w_v > r (w_0 + .. + w_V-1).
- * The products and comparisons are exact and the sums are kept to about 2^-46
- * of their value.  A negative weight or NaN counts as 0; without any positive
+ * The products and comparisons are exact and the sums are kept to 2^-42 of
+ * their value (2^-47 as a rule), for any vocabulary.  A negative weight or NaN counts as 0; without any positive
  * finite weight, or with sums that are not finite, the next token is -1.  A
  * draft outside [0, vocab) is not accepted.                               */
 typedef struct {

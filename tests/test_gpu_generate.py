@@ -808,3 +808,35 @@ def test_rows_without_a_key_beside_keys_that_are_not_finite(B, n, S, Hq, Hkv, ca
     o[reads] = clean[0][reads]
     lse = torch.where(reads[:, None], clean[1], lse)
     check_attn((o, lse), t, lens, causal, d ** -0.5)
+
+
+# ------------------------------------------------- sums of long vocabularies
+@pytest.mark.parametrize("V", [131072, 1 << 27])
+def test_verify_sums_beside_a_border(V):
+    """r = 1/2 and w_0 + w_1 a little more or less than the rest R, so that token
+    1 or 2 is next.  Two sums are compared: each may be off by 2^-42 of its
+    value (see the kernel's comment), half of w_0 + w_1 + R and w_0 + w_1 by
+    2^-42 R each, and half the gap has to be more: a gap of 2^-40 R does.  All
+    weight lies where few threads read it, so that one thread adds thousands."""
+    rng = np.random.default_rng(5)
+    at = np.arange(max(512, V // 4096))
+    at = (at // 4) * 128 + at % 4
+    p, want = torch.zeros((6, 1, V), device="cuda"), []
+    for b in range(6):
+        w = np.exp(rng.standard_normal(len(at)) * 2).astype(np.float32)
+        w = np.maximum(w, np.float32(2.0 ** -20))
+        unit = 80                                      # exact sums in units of 2^-80
+        R = sum(int(np.ldexp(float(x), 50)) for x in w[2:]) << (unit - 50)
+        gap = R >> 40
+        T = R + gap if b % 2 else R - gap
+        hi = np.float32(T / 2.0 ** unit)
+        hi = np.nextafter(np.nextafter(hi, np.float32(0)), np.float32(0))
+        lo = np.float32((T - (int(np.ldexp(float(hi), 40)) << (unit - 40))) / 2.0 ** unit)
+        w[0], w[1] = hi, lo
+        T = sum(int(np.ldexp(float(x), 50)) for x in (hi, lo)) << (unit - 50)
+        assert 0.9 * gap < abs(T - R) < 1.1 * gap
+        p[b, 0, torch.from_numpy(at).cuda()] = torch.from_numpy(w).cuda()
+        want.append(1 if T > R else int(at[2]))
+    r = torch.full((6,), 0.5, device="cuda")
+    acc, out = csbp.draft_verify(p, None, None, None, r)
+    assert (acc == 0).all() and out[:, 0].tolist() == want
