@@ -231,10 +231,10 @@ __device__ int draw(const float* p, const float* q, int V, float r, int rank, Sh
     const double x = __shfl_sync(0xffffffffu, all, kWarps - 1);
     if (C == 1) {
       if (lane == 0) sh.cta[0] = x;
-      __syncwarp();
     } else if (lane < C) {
       store_cluster(&sh.cta[rank], lane, x);
     }
+    __syncwarp();  // the barrier wants whole warps
   }
   if (C > 1) {
     cluster_arrive();
