@@ -1425,7 +1425,7 @@ size_t workspace_bytes(const csbp_prefix_problem& p, const Plan& pl) {
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, const CutJobs& cut,
+cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, const CutJobs& cut, int sms,
                    cudaStream_t stream) {
   using Lay = PrefixLayout<D>;
   // the shared-memory limit is a per-device attribute: set it once on each
@@ -1459,7 +1459,7 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, const CutJobs
   const int64_t rows = static_cast<int64_t>(cut.n) * per_job;
   // few rows have many pieces (the keys were split to fill the GPU): more warps
   // to a row, up to about 32 warps per SM in all
-  const int warps = rows <= 608 ? 8 : rows <= 8192 ? 2 : 1;
+  const int warps = rows <= 4 * sms ? 8 : rows <= 8192 ? 2 : 1;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -1616,7 +1616,7 @@ extern "C" csbp_status csbp_attn_prefix(const csbp_prefix_problem* problem,
   a.part_lse = reinterpret_cast<float*>(ws + part_lse_offset(p, pl));
   a.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p.d == 128 ? launch<128>(maps, a, cut, s)
-                                   : launch<64>(maps, a, cut, s);
+  const cudaError_t e = p.d == 128 ? launch<128>(maps, a, cut, sms, s)
+                                   : launch<64>(maps, a, cut, sms, s);
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }

@@ -362,7 +362,11 @@ template <bool kWrite>
 csbp_status launch(const CacheArgs& a, void* stream) {
   constexpr int kRows = 2;
   const int chunks = a.row_values >> 4;
-  const bool few = static_cast<int64_t>(a.batch) * a.rows <= 152 * 16;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return CSBP_ERR_CUDA;
+  const bool few = static_cast<int64_t>(a.batch) * a.rows <= 16 * sms;
   if (chunks > 32 || (few && chunks > 16)) return launch<32, 1, kWrite>(a, stream);
   if (few) return launch<16, 1, kWrite>(a, stream);
   if (chunks <= 2) return launch<2, kRows, kWrite>(a, stream);
