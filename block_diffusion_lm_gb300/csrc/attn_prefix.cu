@@ -24,6 +24,14 @@
 // a normalised fp32 partial and its LSE per piece in the workspace, and a
 // second kernel joins them exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
 //
+// Runs.  The tensor cores' accumulator drops what is below its last place, a
+// little in each of a tile's eight steps and always towards zero: O over T key
+// tiles came out small by T 2^-21 of itself (V = 1: 0.5 % over a million keys,
+// 18 % over 40 million, and nothing is added any more from 2^26 equal weights on).
+// So a row reads about 2,048 tiles in a piece, 2^-10, and never more than twice as
+// many: where an equal share could hold more, every job is cut into `runs` of one
+// length, each with a partial of its own.
+//
 // Roles (384 threads), as in the training forward: one thread of warp 0
 // TMA producer, one of warp 1 MMA issuer, warp 2 works out the pieces ahead of
 // the others, warps 4..7 and 8..11 softmax of slot 0 and 1 (thread t = row t = TMEM
@@ -125,18 +133,20 @@ struct Plan {
   int32_t pairs;          // jobs per head group
   int32_t parts;          // most pieces of a job
   int32_t ctas;           // shares
-  // the list: jobs of equal length in units of time, the first `len_prefix` of
-  // each for its prefix tiles and the rest for the own tiles
-  uint32_t jobs, len, len_prefix, total, snap;
+  int32_t runs;           // of a job; 1: jobs are cut where shares end
+  // the list: jobs of equal length `full` in units of time, the first
+  // `len_prefix` of each for its prefix tiles and the rest for the own tiles.
+  // Its entries are runs, of length `len`.
+  uint32_t len, full, len_prefix, total, snap;
   // share length in 32.32 fixed point, and reciprocals that only guess or cut
   // the same way everywhere
   uint64_t step;
   float inv_step;
   float inv_prefix, inv_own;
-  Divisor by_gs, by_queries, by_seq_rows, by_pairs, by_len, by_per_kv;
+  Divisor by_gs, by_queries, by_seq_rows, by_pairs, by_len, by_runs, by_per_kv;
 
   // start of share c; a cut that would leave a piece shorter than `snap` moves to
-  // the end of the job
+  // the end of the job (of the run before it, where there are runs)
   __host__ __device__ uint32_t share(uint32_t c) const {
     if (c >= static_cast<uint32_t>(ctas)) return total;
     const uint32_t x = static_cast<uint32_t>((c * step) >> 32);
@@ -151,9 +161,25 @@ struct Plan {
     while (share(c + 1) <= x) ++c;
     return c;
   }
+
+  // The piece at place `at` of a share that ends at `end`: its job and run, and
+  // the range of the job's places.
+  struct Piece {
+    uint32_t job, run, x0, x1;
+  };
+  __host__ __device__ Piece piece(uint32_t at, uint32_t end) const {
+    const uint32_t entry = by_len(at), start = entry * len;
+    Piece r;
+    r.job = by_runs(entry);
+    r.run = entry - r.job * runs;
+    r.x0 = at - start + r.run * len;
+    r.x1 = (end - start < len ? end - start : len) + r.run * len;
+    return r;
+  }
 };
 
-// The jobs that are cut and how many pieces each has; at most one per cut.
+// The jobs that are cut and how many pieces each has; at most one per cut.  (With
+// runs all jobs are, each into its runs, and the list is empty.)
 struct CutJobs {
   static constexpr int kMost = 255;  // as many CTAs, and pieces
   int32_t n;
@@ -303,7 +329,7 @@ constexpr float kAlone = 1.4f;
 __device__ __forceinline__ int tiles_before(const Plan& pl, int np, int in_turn, int alone,
                                             uint32_t x) {
   if (x < pl.len_prefix) return prefix_before(pl, np, x);
-  if (x == pl.len) return np + in_turn + alone;
+  if (x == pl.full) return np + in_turn + alone;
   const float both = static_cast<float>(in_turn);
   const float t = static_cast<float>(x - pl.len_prefix) * pl.inv_own *
                   (both + kAlone * static_cast<float>(alone));
@@ -321,11 +347,11 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
     __syncwarp();
     return;
   }
-  const uint32_t job = pl.by_len(at), start = job * pl.len;
-  const uint32_t x0 = at - start, x1 = min(end - start, pl.len);
-  at = start + x1;
-  const int group = pl.by_pairs(job);
-  const int pair = job - group * pl.pairs;
+  const Plan::Piece piece = pl.piece(at, end);
+  const uint32_t start = at - piece.x0;  // of the job, where shares cut it
+  at += piece.x1 - piece.x0;
+  const int group = pl.by_pairs(piece.job);
+  const int pair = piece.job - group * pl.pairs;
   const bool alternate = 2 * pair + 1 >= pl.row_tiles;
   const int np = (p.prefix_len + kTile - 1) / kTile;
   int own[2];
@@ -366,14 +392,14 @@ __device__ __forceinline__ void make_unit(const PrefixParams& p, uint32_t& at, u
   if (lane == 0) {
     u.valid = 1;
     u.group = group;
-    u.part = static_cast<int>(blockIdx.x) - pl.share_of(start);
-    u.direct = x0 == 0 && x1 == pl.len;
+    u.part = pl.runs > 1 ? piece.run : static_cast<int>(blockIdx.x) - pl.share_of(start);
+    u.direct = piece.x0 == 0 && piece.x1 == pl.full;
     u.alternate = alternate;
     u.np = np;
     const int in_turn = alternate ? own[0] : 2 * min(own[0], own[1]);
     const int alone = alternate ? 0 : abs(own[0] - own[1]);
-    u.m0 = tiles_before(pl, np, in_turn, alone, x0);
-    u.m1 = tiles_before(pl, np, in_turn, alone, x1);
+    u.m0 = tiles_before(pl, np, in_turn, alone, piece.x0);
+    u.m1 = tiles_before(pl, np, in_turn, alone, piece.x1);
     const int p0 = min(u.m0, np), p1 = min(u.m1, np);
     const int o0 = max(u.m0, np) - np, o1 = max(u.m1, np) - np;
 #pragma unroll 1
@@ -605,9 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   uint32_t reached = p.plan.share(blockIdx.x);
   const uint32_t share_end = p.plan.share(blockIdx.x + 1);
-  const uint32_t first_job = p.plan.by_len(reached);
-  const int first_group = p.plan.by_pairs(first_job);
-  const int first_pair = first_job - first_group * p.plan.pairs;
+  const Plan::Piece first = p.plan.piece(reached, share_end);
+  const int first_group = p.plan.by_pairs(first.job);
+  const int first_pair = first.job - first_group * p.plan.pairs;
   // Set-up, with the first piece's Q and K/V already on their way: memory takes
   // a few us to answer all SMs at once.  The two halves of the CTA meet at
   // barrier 2 when the barriers and TMEM are there.
@@ -673,9 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (reached < share_end) {
         const int np = (p.prefix_len + kTile - 1) / kTile;
-        const uint32_t x0 = reached - first_job * p.plan.len;
-        const int p0 = prefix_before(p.plan, np, x0);
-        const int p1 = prefix_before(p.plan, np, min(share_end - first_job * p.plan.len, p.plan.len));
+        const int p0 = prefix_before(p.plan, np, first.x0);
+        const int p1 = prefix_before(p.plan, np, first.x1);
         early = min(kStages, p1 - p0);
         const int x = p.plan.by_per_kv(first_group) * D;
         for (; nk < early; ++nk, ++nv) {
@@ -1234,8 +1259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces' partials: blockIdx.y is a cut job, and W warps work on a
-// (query, head) row of it, each on every W-th piece.  Lanes hold the pieces' LSE in
+// Joins the pieces' partials: `blocks` CTAs for each cut job, and W warps work on
+// a (query, head) row of it, each on every W-th piece.  Lanes hold the pieces' LSE in
 // turn for the maximum and the weights, then d / 32 features each, with the loads of
 // kBatch pieces in flight; the first of them are issued before the LSE is there.
 // It is launched while the attention kernel still runs and waits for its end here,
@@ -1244,7 +1269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows of all jobs, which had to find their pieces), 2 to 3 to the smallest calls.
 template <int D, int W>
 __global__ void __launch_bounds__(256)
-    prefix_merge_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CutJobs cut) {
+    prefix_merge_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CutJobs cut,
+                        int blocks) {
   constexpr int kN = D / 32, kBatch = W == 1 ? 4 : 8;
   struct alignas(kN * 4) Part {
     float x[kN];
@@ -1252,10 +1278,11 @@ __global__ void __launch_bounds__(256)
   __shared__ Part joined[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Plan& pl = p.plan;
-  const uint32_t job = cut.job[blockIdx.y];
-  const int parts = cut.parts[blockIdx.y];
+  const int n = static_cast<int>(blockIdx.x) / blocks;
+  const uint32_t job = pl.runs > 1 ? n : cut.job[n];
+  const int parts = pl.runs > 1 ? pl.runs : cut.parts[n];
   const uint32_t group = pl.by_pairs(job);
-  const int i = blockIdx.x * (8 / W) + warp / W;  // row of the job
+  const int i = (static_cast<int>(blockIdx.x) - n * blocks) * (8 / W) + warp / W;  // row of the job
   const int flat = static_cast<int>(job - group * pl.pairs) * (2 * kTile) + i;
   if (i >= 2 * kTile || flat >= p.batch * pl.seq_rows) return;
   const uint32_t token = pl.by_gs(flat);
@@ -1351,6 +1378,7 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl, CutJobs& cut) {
   // start and the end of a piece 40.  Own keys count as 5/8 of the room for
   // them.
   constexpr int64_t kOne = 8, kTwo = 13, kEnds = 40, kJoin = 36;
+  constexpr int64_t kMostTiles = 2048;  // that a row reads in a piece (see Runs above)
   const int64_t own_mean = (static_cast<int64_t>(p.own_max) * 5 / 8 + kTile - 1) / kTile;
   int64_t len_prefix = np * (pl.row_tiles == 1 ? kOne : kTwo) + kEnds;
   int64_t len = len_prefix + (meets * own_mean * kOne + pl.pairs - 1) / pl.pairs;
@@ -1362,38 +1390,67 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl, CutJobs& cut) {
   // of its pieces (5 us, the second kernel).  More CTAs than SMs then start as
   // others end.
   const bool whole = (jobs + sms - 1) / sms * len <= total / pl.ctas + kEnds + kJoin;
+  // Runs, where a row could read more than kMostTiles in one piece: of all numbers
+  // up to about twice the least, the one with which the CTA with most runs ends
+  // first.  (A row reads the prefix and its own sequence's keys; long sequences of
+  // one job may all be as long as their room.)
+  const int64_t own_most = (static_cast<int64_t>(p.own_max) + kTile - 1) / kTile;
+  int64_t runs = 1, longest = len;
+  if (own_most > kMostTiles) {
+    const int64_t seqs = std::min<int64_t>(p.batch, (kTile + pl.seq_rows - 2) / pl.seq_rows + 1);
+    longest = len_prefix + 2 * seqs * own_most * kOne;
+  }
+  const double cut_to = whole ? 1.0 : static_cast<double>(total / pl.ctas) / static_cast<double>(len);
+  if (np + own_most > kMostTiles &&
+      static_cast<double>(longest) * std::min(cut_to, 1.0) > kMostTiles * kTwo) {
+    const int64_t least = (longest + kMostTiles * kTwo - 1) / (kMostTiles * kTwo);
+    int64_t best = INT64_MAX;
+    for (int64_t r = least; r <= 2 * least + 16; ++r) {
+      const int64_t time = (jobs * r + sms - 1) / sms * ((len + r - 1) / r + kEnds);
+      if (time < best) {
+        best = time;
+        runs = r;
+      }
+    }
+    len = (len + runs - 1) / runs;
+    pl.ctas = static_cast<int32_t>(std::min<int64_t>(sms, jobs * runs));
+    total = jobs * runs * len;
+  }
   while (total >= int64_t(1) << 30 && len > 1) {  // coarser units: 32-bit places
     len_prefix = (len_prefix + 1) / 2;
     len = (len + 1) / 2;
-    total = jobs * len;
+    total = jobs * runs * len;
   }
   if (total >= int64_t(1) << 30) return false;
-  pl.jobs = static_cast<uint32_t>(jobs);
+  pl.runs = static_cast<int32_t>(runs);
   pl.len = static_cast<uint32_t>(len);
+  pl.full = static_cast<uint32_t>(len * runs);
   pl.total = static_cast<uint32_t>(total);
   pl.len_prefix = static_cast<uint32_t>(len_prefix);
   pl.inv_prefix = 1.f / static_cast<float>(len_prefix);
-  pl.inv_own = len > len_prefix ? 1.f / static_cast<float>(len - len_prefix) : 0.f;
+  pl.inv_own = pl.full > len_prefix ? 1.f / static_cast<float>(pl.full - len_prefix) : 0.f;
   pl.by_gs = Divisor::of(pl.gs);
   pl.by_queries = Divisor::of(p.queries);
   pl.by_seq_rows = Divisor::of(pl.seq_rows);
   pl.by_pairs = Divisor::of(pl.pairs);
   pl.by_len = Divisor::of(pl.len);
+  pl.by_runs = Divisor::of(pl.runs);
   pl.by_per_kv = Divisor::of(G / pl.gs);  // row groups of a KV head
   pl.snap = 0;
-  if (whole) {
+  if (whole && runs == 1) {
     pl.ctas = static_cast<int32_t>(jobs);
     pl.step = static_cast<uint64_t>(len) << 32;
   } else {
     // rounded up, so that a share that is a whole number of jobs ends with one
     pl.step = ((static_cast<uint64_t>(total) << 32) + pl.ctas - 1) / pl.ctas;
-    pl.snap = static_cast<uint32_t>(std::min<int64_t>(kEnds, total / pl.ctas / 3));
+    pl.snap = runs > 1 ? pl.len  // every cut moves to the end of a run
+                       : static_cast<uint32_t>(std::min<int64_t>(kEnds, total / pl.ctas / 3));
   }
   pl.inv_step = static_cast<float>(4294967296.0 / static_cast<double>(pl.step));
   // the cuts inside jobs
-  pl.parts = 1;
+  pl.parts = pl.runs;
   cut.n = 0;
-  for (int c = 1; !whole && c < pl.ctas; ++c) {
+  for (int c = 1; !whole && runs == 1 && c < pl.ctas; ++c) {
     const uint32_t x = pl.share(c), job = pl.by_len(x);
     if (x == job * pl.len) continue;
     if (cut.n == 0 || cut.job[cut.n - 1] != job) {
@@ -1454,9 +1511,10 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, const CutJobs
                                                               p);
   e = cudaGetLastError();
   timer_end(timed, stream);
-  if (e != cudaSuccess || cut.n == 0) return e;
+  const int jobs = p.plan.runs > 1 ? p.plan.pairs * p.plan.n_groups : cut.n;
+  if (e != cudaSuccess || jobs == 0) return e;
   const int per_job = std::min(2 * kTile, p.batch * p.plan.seq_rows);
-  const int64_t rows = static_cast<int64_t>(cut.n) * per_job;
+  const int64_t rows = static_cast<int64_t>(jobs) * per_job;
   // few rows have many pieces (the keys were split to fill the GPU): more warps
   // to a row, up to about 32 warps per SM in all
   const int warps = rows <= 4 * sms ? 8 : rows <= 8192 ? 2 : 1;
@@ -1464,15 +1522,16 @@ cudaError_t launch(const CUtensorMap* maps, const PrefixParams& p, const CutJobs
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((per_job * warps + 7) / 8), static_cast<unsigned>(cut.n));
+  const int blocks = (per_job * warps + 7) / 8;
+  cfg.gridDim = dim3(static_cast<unsigned>(jobs) * blocks);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   const int joined = timer_begin(14, stream);
-  e = warps == 8   ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p, cut)
-      : warps == 2 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 2>, p, cut)
-                   : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p, cut);
+  e = warps == 8   ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 8>, p, cut, blocks)
+      : warps == 2 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 2>, p, cut, blocks)
+                   : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, 1>, p, cut, blocks);
   timer_end(joined, stream);
   return e;
 }

@@ -840,3 +840,86 @@ def test_verify_sums_beside_a_border(V):
     r = torch.full((6,), 0.5, device="cuda")
     acc, out = csbp.draft_verify(p, None, None, None, r)
     assert (acc == 0).all() and out[:, 0].tolist() == want
+
+
+# --------------------------------------------------------- long key ranges
+@pytest.mark.parametrize("d,Lp", [(64, 4_000_000), (128, 1_500_000)])
+def test_sums_over_millions_of_keys(d, Lp):
+    """Many rows and a long prefix, with values that all keys share: O is those
+    values, whatever the weights.  Off by 2^-8 (P rounded to bf16), 2^-8 (O
+    rounded) and 2^-9 at most for what the accumulator drops."""
+    n, Hq = 912, 64
+    g = gen(92)
+    k = torch.empty((Lp, 1, d), dtype=torch.bfloat16, device="cuda")
+    for x in k.split(1 << 20):
+        x.copy_(normal(g, *x.shape) * 0.3)
+    row = torch.linspace(0.25, 2.0, d, device="cuda").to(torch.bfloat16)
+    row[1::2] *= -1
+    v = row.expand(Lp, 1, d).contiguous()
+    q = normal(g, 1, n, Hq, d)
+    a = csbp.PrefixAttention(1, n, Lp, 0, Hq, 1, d)
+    o, lse = a.forward(q, k, v, None, None, None)
+    a.check()
+    assert ((o.double() / row.double() - 1).abs() <= 2.0 ** -7 + 2.0 ** -9).all()
+    for i, h in ((0, 0), (511, 63), (911, 7)):
+        z = torch.logsumexp((k[:, 0].double() @ q[0, i, h].double()) * d ** -0.5, 0)
+        assert abs(float(lse[0, h, i]) - float(z)) <= 2.0 ** -13
+
+
+def row_by_row(t, got, own_len, causal, samples, scale):
+    """Sampled rows against the definition in 64 bits, on the GPU."""
+    o, lse = got
+    n, Hq = t["q"].shape[1:3]
+    G = Hq // t["k_prefix"].shape[1]
+    d = o.shape[-1]
+    for b, i, h in samples:
+        c = min(max(own_len[b], 0), t["k_own"].shape[1])
+        c = max(min(c, c - n + i + 1), 0) if causal else c
+        k, v = (torch.cat([t[x + "_prefix"][:, h // G], t[x + "_own"][b, :c, h // G]]).double()
+                for x in "kv")
+        q = t["q"][b, i, h].double()
+        s = (k @ q) * scale
+        z = torch.logsumexp(s, 0)
+        p = torch.exp(s - z)
+        A, want = p @ v.abs(), p @ v
+        T = float((k.abs() @ q.abs()).max()) * scale
+        tol = (2.0 ** -8 + 2.0 ** -9 + 2.0 ** -12 + 2 * d * 2.0 ** -24 * T) * A + 2.0 ** -8 * want.abs()
+        assert ((o[b, i, h].double() - want).abs() <= tol).all(), (b, i, h)
+        ztol = d * 2.0 ** -24 * T + 2.0 ** -15 + 2.0 ** -22 * abs(float(z))
+        assert abs(float(lse[b, h, i]) - float(z)) <= ztol, (b, i, h)
+
+
+@pytest.mark.parametrize("d,S,Lp", [(64, 700, 300_000), (128, 700, 300_000), (64, 300_000, 700)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_jobs_cut_into_runs(d, S, Lp, causal):
+    """So many rows that jobs would stay whole, over so many keys that each is cut
+    into runs; the last row tile is alone; one V is not finite."""
+    B, n, Hq = 17, 127, 16
+    if S > Lp:
+        B, n = 4, 600
+    t = attn_inputs(B, n, Lp, S, Hq, 1, d, 93)
+    lens = [(S - 61 * b) if b % 5 else 3 * b for b in range(B)]
+    a = csbp.PrefixAttention(B, n, Lp, S, Hq, 1, d, causal=causal)
+    rows = B * n * Hq
+    assert a.ws.numel() >= 2 * rows * d * 4             # partials
+    got = a.forward(**t, own_len=i32(lens))
+    a.check()
+    rng = np.random.default_rng(94)
+    some = [(0, 0, 0), (B - 1, n - 1, Hq - 1), (1, 5, 3)] + [
+        tuple(int(x) for x in rng.integers(0, (B, n, Hq))) for _ in range(12)]
+    row_by_row(t, got, lens, causal, some, d ** -0.5)
+    again = a.forward(**t, own_len=i32(lens))
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    want = [x.clone() for x in got]
+    b, j = 1, lens[1] - 2                               # read by its sequence's last queries
+    t["v_own"][b, j] = float("nan")
+    o, lse = a.forward(**t, own_len=i32(lens))
+    a.check()
+    reads = torch.zeros((B, n), dtype=torch.bool, device="cuda")
+    reads[b] = j <= lens[b] - n + torch.arange(n, device="cuda") if causal else True
+    assert torch.isnan(o[reads].float()).all() and torch.equal(lse, want[1])
+    assert torch.isfinite(o[~reads].float()).all()
+    # rows beside it in a row tile are summed again
+    other = ((o != want[0]).flatten(2).any(-1) & ~reads).nonzero().tolist()
+    row_by_row(t, (o, lse), lens, causal, [(b, i, h) for b, i in other[::37] for h in (0, 9)],
+               d ** -0.5)
