@@ -169,11 +169,13 @@ struct Plan {
   };
   __host__ __device__ Piece piece(uint32_t at, uint32_t end) const {
     const uint32_t entry = by_len(at), start = entry * len;
-    Piece r;
-    r.job = by_runs(entry);
-    r.run = entry - r.job * runs;
-    r.x0 = at - start + r.run * len;
-    r.x1 = (end - start < len ? end - start : len) + r.run * len;
+    Piece r{entry, 0, at - start, end - start < len ? end - start : len};
+    if (runs > 1) {
+      r.job = by_runs(entry);
+      r.run = entry - r.job * runs;
+      r.x0 += r.run * len;
+      r.x1 += r.run * len;
+    }
     return r;
   }
 };
