@@ -600,6 +600,10 @@ class VocabCrossEntropy:
 
 
 # ----------------------------------------------------------------- generation
+# Each call takes `stream` (default: the current one).  The caller orders a stream
+# that is named after what its inputs come from, and its results before their use.
+
+
 class _Call:
     """Argument checks of the generation operators: dtype, shape and layout of
     every tensor first, then (in `device`) that all of them are on one CUDA
@@ -806,8 +810,10 @@ class PrefixAttention:
     queries are the last tokens of own_len and read own keys up to themselves;
     otherwise (a block being denoised) they read all own_len keys.  The prefix
     (own) tensors may be None when prefix_len (own_max) is 0.  The work is cut up
-    for lengths of about half of own_max: views k[:, :m] of a larger room, with
+    for lengths of five eighths of own_max: views k[:, :m] of a larger room, with
     an own_max = m near the lengths in use, are faster than the whole room.
+    Calls that can overlap (two streams, two captured graphs) need handles of
+    their own: they share this one's workspace.
     """
 
     def __init__(self, batch, queries, prefix_len, own_max, Hq, Hkv, d, causal=False,

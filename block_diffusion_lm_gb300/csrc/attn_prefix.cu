@@ -48,11 +48,12 @@
 // and the issuer's barriers, as in the training forward (tensor pipe 55 % active
 // at d = 128, 34 % at 64; issue slots 35 % and 44 %).  Few rows: HBM.  Small
 // calls: a start of about 4 us, an end of 3.5, and the second kernel.  Measured:
-//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   802 us, 1370 TFLOP/s
-//     (0.71 of the measured bf16 rate); heads of 64       604 us
-//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   166 us
-//   65,536 keys, 8 x 1 queries, 32 / 8 heads   46.8 us, 5.7 TB/s (0.85 of a copy)
-//   8,192 keys, 8 x 1 queries, 32 / 8 heads    17.4 us
+//   1,048,576 keys, 4 x 16 queries, 32 / 8 heads of 128   790 us, 1390 TFLOP/s
+//     (0.72 of the measured bf16 rate), 869 us and 1265 call after call, where the
+//     power cap lowers the clocks; heads of 64            606 us
+//   16,384 keys, 16 x 32 queries of 40 / 8 heads, own keys up to 1024   167 us
+//   65,536 keys, 8 x 1 queries, 32 / 8 heads   48.8 us, 5.5 TB/s (0.81 of a copy)
+//   8,192 keys, 8 x 1 queries, 32 / 8 heads    18.4 us
 // A kernel without tensor cores took 41,000 us at the second and 7,200 at 8192
 // keys; one job per CTA without cuts 46 us there, 342 at the second.
 #include <cuda.h>

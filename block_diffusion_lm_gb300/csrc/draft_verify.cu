@@ -392,9 +392,9 @@ extern "C" csbp_status csbp_draft_verify(const csbp_verify_problem* problem, con
   // A cluster per sequence as large as all sequences' CTAs still run at once
   // (three to an SM), and with at least four 16-byte loads of a row per thread.
   // Measured, us, with 1, 2, 4 and 8 CTAs at a 131,072-token vocabulary:
-  // 1 sequence 20.4, 16.1, 10.4, 9.0; 48 sequences 33.0, 20.3, 15.1, 14.2; 96
-  // sequences 38.5, 27.7, 21.7, 26.5; 200 sequences 50.9, 43.0, 45.6, 50.7.  At
-  // 8,000 tokens (3 sequences) 7.3, 7.9, 7.9, 7.9.
+  // 1 sequence 21.4, 15.0, 10.6, 9.7; 48 sequences 30.9, 19.1, 15.4, 14.0; 96
+  // sequences 37.7, 27.1, 20.9, 24.3; 200 sequences 51.1, 40.0, 42.5, 49.0.  At
+  // 8,000 tokens (3 sequences) 7.7, 8.1, 7.9, 7.9.
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -313,7 +313,8 @@ csbp_status csbp_check_status(void* workspace, void* stream);
  * current device and clears the record; while it is on, every csbp_attn_fwd
  * and csbp_attn_bwd call records an event pair on its stream around its main
  * kernel (fwd_kernel / bwd_kernel) and its HBM-bound launches, and
- * csbp_vocab_ce one around each of its launches, up to 4096 pairs in all
+ * csbp_vocab_ce and the calls of csbp_generate.h one around each of their
+ * launches, up to 4096 pairs in all
  * (later launches are not timed).
  * csbp_kernel_timing(0) stops recording and keeps the record.
  * csbp_kernel_timing_read synchronises the recorded events and returns the

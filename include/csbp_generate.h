@@ -45,7 +45,8 @@ extern "C" {
 /* ------------------------------------------------------- quantised cache
  * One layer's K and V, each as
  *   codes   uint8 [pages][page_size][Hkv][d]       E4M3 (csbp_e4m3_to_bf16)
- *   scales  uint8 [pages][page_size][Hkv][d / 32]  byte s stands for 2^(s-127)
+ *   scales  uint8 [pages][page_size][Hkv][d / 32]  byte s stands for 2^(s-127),
+ *           255 for NaN
  * d: a multiple of 32, 32 .. 1024.  A value is code x scale, so reading back
  * is exact in bf16 (wherever 2^(s-127) x code is a bf16 number; smaller ones
  * round to nearest even).                                                 */
@@ -80,7 +81,8 @@ typedef struct {
  * NaN and infinities are stored as NaN (E4M3 has no infinities).  A row whose
  * position is negative or past the table, or whose page is outside
  * [0, pages), is not written.  Rows that land on the same place of the same
- * page leave it with bytes of either.  Nothing else of the cache changes.  */
+ * page leave each byte of it as one of them writes it: codes and scales may
+ * come from different rows.  Nothing else of the cache changes.            */
 csbp_status csbp_cache_write(const csbp_kv_cache* cache, const csbp_cache_rows* rows,
                              const void* k, const void* v, void* stream);
 
@@ -100,7 +102,13 @@ csbp_status csbp_cache_read(const csbp_kv_cache* cache, const csbp_cache_rows* r
  * O = softmax(scale Q K^T) V over those keys and LSE the natural log of the
  * softmax denominator.  A query that reads no key has O = 0, LSE = -inf.  A key
  * that a query does not read has no part in its result, whatever it holds (own
- * rows at and past c, later keys, other sequences' keys), NaN included.     */
+ * rows at and past c, later keys, other sequences' keys), NaN included.
+ * O is summed in fp32 on the tensor cores, which drop what is below the last
+ * place: a row reads about 262,144 keys (twice as many at most) into one sum,
+ * which costs it 2^-10 (2^-9) of its value where all values share a sign.
+ * causal = 1 is made for a few queries (drafted tokens, a block): all c own
+ * keys pass by every query, so a chunk of thousands of queries does up to twice
+ * the work that its own keys need.                                          */
 typedef struct {
   int32_t batch, queries;       /* >= 1                                     */
   int32_t prefix_len, own_max;  /* >= 0, below 2^31 - 128                   */
@@ -113,7 +121,7 @@ typedef struct {
  * [prefix_len][Hkv][d] (NULL allowed when prefix_len is 0), k_own and v_own
  * [batch][own_max][Hkv][d] and own_len int32 [batch], 4-byte aligned (all
  * three NULL allowed when own_max is 0).  The work is cut up as if own_len were
- * about half of own_max: an own_max near the longest length in use (smaller than
+ * five eighths of own_max: an own_max near the longest length in use (smaller than
  * the tensor's rows by its batch stride) is faster than a far larger one.
  * Strides as in csbp_inputs, in that
  * order; the batch strides of the prefix are not read.  batch x the batch
@@ -126,8 +134,10 @@ typedef struct {
 } csbp_prefix_inputs;
 
 /* Workspace bytes of csbp_attn_prefix on the current device: the status word
- * and the fp32 partial results of the key ranges that a query's keys are cut
- * into.  0 for an invalid problem. */
+ * and the fp32 partial results (d + 1 numbers per query and head) of the key
+ * ranges that a query's keys are cut into: as many as share its keys among the
+ * SMs or, with many queries, one to two per 262,144 keys.  0 for an invalid
+ * problem. */
 size_t csbp_prefix_workspace_bytes(const csbp_prefix_problem* problem);
 
 /*  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]
