@@ -1395,18 +1395,20 @@ bool make_plan(const csbp_prefix_problem& p, int sms, Plan& pl, CutJobs& cut) {
   const bool whole = (jobs + sms - 1) / sms * len <= total / pl.ctas + kEnds + kJoin;
   // Runs, where a row could read more than kMostTiles in one piece: of all numbers
   // up to about twice the least, the one with which the CTA with most runs ends
-  // first.  (A row reads the prefix and its own sequence's keys; long sequences of
-  // one job may all be as long as their room.)
+  // first.  (A row reads the prefix and its own sequence's keys.  Where those alone
+  // can be too many, all sequences of a job may be as long as their room, which
+  // puts `dense` times as many own tiles into a unit as the list assumes.)
   const int64_t own_most = (static_cast<int64_t>(p.own_max) + kTile - 1) / kTile;
-  int64_t runs = 1, longest = len;
+  double dense = 1.0;
   if (own_most > kMostTiles) {
     const int64_t seqs = std::min<int64_t>(p.batch, (kTile + pl.seq_rows - 2) / pl.seq_rows + 1);
-    longest = len_prefix + 2 * seqs * own_most * kOne;
+    dense = std::max(1.0, static_cast<double>(2 * seqs * own_most * kOne) /
+                              static_cast<double>(len - len_prefix));
   }
-  const double cut_to = whole ? 1.0 : static_cast<double>(total / pl.ctas) / static_cast<double>(len);
-  if (np + own_most > kMostTiles &&
-      static_cast<double>(longest) * std::min(cut_to, 1.0) > kMostTiles * kTwo) {
-    const int64_t least = (longest + kMostTiles * kTwo - 1) / (kMostTiles * kTwo);
+  int64_t runs = 1;
+  const int64_t longest = static_cast<int64_t>(kMostTiles * kTwo / dense);  // of a piece
+  if (np + own_most > kMostTiles && (whole ? len : std::min(len, total / pl.ctas)) > longest) {
+    const int64_t least = (len + longest - 1) / longest;
     int64_t best = INT64_MAX;
     for (int64_t r = least; r <= 2 * least + 16; ++r) {
       const int64_t time = (jobs * r + sms - 1) / sms * ((len + r - 1) / r + kEnds);
