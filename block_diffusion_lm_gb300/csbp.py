@@ -74,6 +74,28 @@ class CacheRows(ctypes.Structure):
                 ("stride_tok", ctypes.c_int64 * 2), ("stride_batch", ctypes.c_int64 * 2)]
 
 
+class RotaryStruct(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("turns", ctypes.c_void_p)]
+
+
+class AppendQueries(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("stride_tok", ctypes.c_int64 * 2), ("stride_batch", ctypes.c_int64 * 2)]
+
+
+class PagedProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "queries", "table_pages", "Hq", "causal", "window", "sinks")] + [
+                    ("scale", ctypes.c_float)]
+
+
+class PagedInputs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("stride_tok", ctypes.c_int64),
+                ("stride_batch", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("length", ctypes.c_void_p)]
+
+
 class PrefixProblem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("batch", "queries", "prefix_len", "own_max", "Hq", "Hkv", "d", "causal")] + [
@@ -143,11 +165,19 @@ def lib():
         L.csbp_vocab_ce.argtypes = [P(CeProblem), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.csbp_cache_write.argtypes = [P(KvCache), P(CacheRows), vp, vp, vp]
         L.csbp_cache_read.argtypes = [P(KvCache), P(CacheRows), vp, vp, vp]
+        L.csbp_rotary_turns.argtypes = [P(ctypes.c_double), i32, P(ctypes.c_uint64)]
+        L.csbp_cache_append.argtypes = [P(KvCache), P(CacheRows), P(RotaryStruct), vp, vp,
+                                        P(AppendQueries), vp]
+        L.csbp_paged_workspace_bytes.argtypes = [P(PagedProblem), P(KvCache)]
+        L.csbp_paged_workspace_bytes.restype = sz
+        L.csbp_attn_paged.argtypes = [P(PagedProblem), P(KvCache), P(PagedInputs), vp, vp, vp,
+                                      sz, vp]
         L.csbp_prefix_workspace_bytes.argtypes = [P(PrefixProblem)]
         L.csbp_prefix_workspace_bytes.restype = sz
         L.csbp_attn_prefix.argtypes = [P(PrefixProblem), P(PrefixInputs), vp, vp, vp, sz, vp]
         L.csbp_draft_verify.argtypes = [P(VerifyProblem)] + [vp] * 9
-        for fn in ("csbp_cache_write", "csbp_cache_read", "csbp_attn_prefix",
+        for fn in ("csbp_cache_write", "csbp_cache_read", "csbp_rotary_turns",
+                   "csbp_cache_append", "csbp_attn_paged", "csbp_attn_prefix",
                    "csbp_draft_verify", "csbp_block_schedule", "csbp_attn_fwd", "csbp_attn_bwd", "csbp_lse_merge",
                    "csbp_check_status", "csbp_kernel_timing", "csbp_kernel_timing_read",
                    "csbp_kernel_timing_read_kind", "csbp_vocab_ce", "csbp_wait_selftest"):
@@ -220,8 +250,9 @@ def kernel_timing_read():
 
 def kernel_timing_read_kind(kind: int):
     """(ms, launches) of one timer kind: 0 fwd, 1 bwd, 2 CE logits GEMM,
-    3 CE row kernel, 4 CE dH GEMM, 5 CE dW GEMM, 11 cache write, 12 cache read,
-    13 prefix attention, 14 the joining of its pieces, 15 draft verification."""
+    3 CE row kernel, 4 CE dH GEMM, 5 CE dW GEMM, 11 cache write and append, 12
+    cache read, 13 prefix and paged attention, 14 the joining of the former's
+    pieces, 15 draft verification."""
     ms, n = ctypes.c_double(), ctypes.c_int32()
     _check("csbp_kernel_timing_read_kind",
            lib().csbp_kernel_timing_read_kind(kind, ctypes.byref(ms), ctypes.byref(n)))
@@ -709,9 +740,34 @@ def _run(fn, dev, stream, tensors, *args):
         raise CsbpError(fn, st)
 
 
+class Rotary:
+    """Rotary positions of a model: `frequencies` are dim / 2 numbers in radians
+    per position (theta ** (-2 i / dim) as a rule, scaled as the model has it),
+    for the pairs (x_i, x_{i + dim/2}) of a head's first dim features, or
+    (x_2i, x_2i+1) if `interleaved`.  dim is a multiple of 16.  Keeps them on the
+    device in a form that is exact at any position."""
+
+    def __init__(self, frequencies, interleaved=False, device="cuda"):
+        import torch
+        n = len(frequencies)
+        if n < 8 or n % 8:
+            raise ValueError(f"Rotary: the number of frequencies, dim / 2, must be a multiple of "
+                             f"8, got {n}")
+        turns = (ctypes.c_uint64 * n)()
+        st = lib().csbp_rotary_turns((ctypes.c_double * n)(*[float(f) for f in frequencies]), n,
+                                     turns)
+        _check("csbp_rotary_turns", st)
+        host = torch.frombuffer(turns, dtype=torch.int64).clone()
+        self.turns = host.to(device)  # (pageable: the host waits for the copy)
+        self.dim = 2 * n
+        self.struct = RotaryStruct(self.dim, 1 if interleaved else 0, self.turns.data_ptr())
+        self._ref = ctypes.byref(self.struct)
+
+
 class QuantCache:
     """One layer's paged K/V cache in E4M3 with a power-of-two scale per 32
-    features of a head (csbp_cache_write / csbp_cache_read).
+    features of a head (csbp_cache_write / csbp_cache_append / csbp_cache_read;
+    PagedAttention reads it where it lies).
 
     Owns (or, with `storage`, wraps) the uint8 tensors k, v [pages][page_size]
     [Hkv][d] and k_scale, v_scale [pages][page_size][Hkv][d / 32].  Which pages
@@ -740,8 +796,9 @@ class QuantCache:
         self._ref = ctypes.byref(self.struct)
         self._key = (Hkv, d, str(self.k.device))
 
-    def _check(self, fn, k, v, table, start, count):
-        """(CacheRows without pointers, rows, device index)."""
+    def _check(self, fn, k, v, table, start, count, more=None):
+        """(CacheRows without pointers or None, device index); `more(call)` checks
+        what else the call takes."""
         import torch
         c = _Call(fn)
         if k is None or k.dim() != 4:
@@ -757,6 +814,8 @@ class QuantCache:
         if count is not None:
             c.tensor("count", count, torch.int32, (batch,))
         c.seen += self._tensors
+        if more is not None:
+            more(c)
         if batch * rows == 0:
             return None, 0
         r = CacheRows(batch, rows, table.shape[1], None, None, None, (kt, vt), (kb, vb))
@@ -796,6 +855,150 @@ class QuantCache:
                 for _ in range(2)))
         self._call("csbp_cache_read", out[0], out[1], table, start, count, stream)
         return out
+
+
+    def append(self, k, v, table, start, count=None, *, rotary, q=None, out=None, stream=None):
+        """`write` of k, rotated by its positions start[b] + i, and of v; q
+        [batch][rows][Hq][d], if given, is rotated along.  Returns the rotated
+        q: `out` (which may be q; rows i >= count[b] keep what they hold), or a
+        tensor made here (zero there), or None without q."""
+        import torch
+        fn = "csbp_cache_append"
+        lib()
+
+        qs = AppendQueries()
+
+        def more(c):
+            nonlocal qs
+            if not isinstance(rotary, Rotary):
+                raise ValueError(f"{fn}: rotary must be a Rotary")
+            if rotary.dim > self.d:
+                raise ValueError(f"{fn}: rotary has {rotary.dim} features, a head {self.d}")
+            c.seen.append(("rotary", rotary.turns))
+            if q is None:
+                if out is not None:
+                    raise ValueError(f"{fn}: out without q")
+                return
+            if q.dim() != 4:
+                raise ValueError(f"{fn}: q must be a [batch][rows][Hq][d] tensor")
+            shape = (*k.shape[:2], q.shape[2], self.d)
+            _, qt, qb = c.strided("q", q, shape)
+            ot = ob = 0
+            if out is not None:
+                _, ot, ob = c.strided("out", out, shape)
+            qs = AppendQueries(q.shape[2], None, None, (qt, ot), (qb, ob))
+
+        def check():
+            return (*self._check(fn, k, v, table, start, count, more), qs)
+
+        turns = rotary.turns if isinstance(rotary, Rotary) else None
+        r, dev, qs = _layout(fn, self._key, (k, v, table, start, count, q, out, turns), check)
+        if q is not None and out is None:
+            make = torch.zeros if count is not None else torch.empty
+            out, = _fresh(stream, lambda: (make(q.shape, dtype=q.dtype, device=q.device),))
+        if r is None:
+            return out
+        r = CacheRows.from_buffer_copy(r)
+        r.table = table.data_ptr()
+        r.start = start.data_ptr()
+        if count is not None:
+            r.count = count.data_ptr()
+        if q is not None:
+            qs = AppendQueries.from_buffer_copy(qs)
+            qs.q = q.data_ptr()
+            qs.out = out.data_ptr()
+        _run(fn, dev, stream, (k, v, table, start, count, q, out, turns, self.k, self.v,
+                               self.k_scale, self.v_scale),
+             self._ref, ctypes.byref(r), rotary._ref, k.data_ptr(), v.data_ptr(),
+             ctypes.byref(qs))
+        return out
+
+
+class PagedAttention:
+    """Attention of `queries` new tokens of each of `batch` sequences over the
+    pages of a QuantCache (csbp_attn_paged).  Owns the workspace of one shape,
+    for all caches (layers) of that shape.
+
+    forward(q, cache, table, length) takes bf16 q [batch][queries][Hq][d], the
+    cache with the new tokens' own keys in it, int32 table [batch][table_pages]
+    and int32 length [batch] (keys, the new ones included), and returns (o, lse):
+    bf16 [batch][queries][Hq][d] and fp32 [batch][Hq][queries].  causal: the
+    queries are the last tokens of `length` and read keys up to themselves;
+    otherwise (a block being denoised) they read all of them.  window: only the
+    last `window` keys up to a query's position count, and the first `sinks`.
+    Calls that can overlap (two streams, two captured graphs) need handles of
+    their own: they share this one's workspace.
+    """
+
+    def __init__(self, batch, queries, table_pages, page_size, Hq, Hkv, d, causal=False, window=0,
+                 sinks=0, scale=None, device="cuda"):
+        import torch
+        self.problem = PagedProblem(batch, queries, table_pages, Hq, 1 if causal else 0, window,
+                                    sinks, float(scale if scale is not None else d ** -0.5))
+        self._cache = KvCache(1, page_size, Hkv, d)
+        if torch.device(device).type == "cuda":
+            with torch.cuda.device(device):
+                n = paged_workspace_bytes(self.problem, self._cache)
+        else:
+            n = paged_workspace_bytes(self.problem, self._cache)
+        if n == 0:
+            raise CsbpError("csbp_paged_workspace_bytes", -1)
+        self.ws = _zeros(n, device)
+        self.device = self.ws.device
+        self._key = (bytes(self.problem), page_size, Hkv, d, str(self.device))
+
+    def alloc_outputs(self):
+        import torch
+        p = self.problem
+        return (torch.empty((p.batch, p.queries, p.Hq, self._cache.d), dtype=torch.bfloat16,
+                            device=self.device),
+                torch.empty((p.batch, p.Hq, p.queries), dtype=torch.float32, device=self.device))
+
+    def forward(self, q, cache, table, length, out=None, stream=None):
+        fn = "csbp_attn_paged"
+        p, mine = self.problem, self._cache
+        if not isinstance(cache, QuantCache):
+            raise ValueError(f"{fn}: cache must be a QuantCache")
+        lib()
+        o, lse = out if out is not None else (None, None)
+
+        def check():
+            import torch
+            c = _Call(fn)
+            got = cache.struct.page_size, cache.Hkv, cache.d
+            want = mine.page_size, mine.Hkv, mine.d
+            if got != want:
+                raise ValueError(f"{fn}: the cache has (page_size, Hkv, d) = {got}, this handle "
+                                 f"{want}")
+            _, tok, bat = c.strided("q", q, (p.batch, p.queries, p.Hq, mine.d))
+            c.tensor("table", table, torch.int32, (p.batch, p.table_pages))
+            c.tensor("length", length, torch.int32, (p.batch,))
+            if out is not None:
+                c.tensor("o", o, torch.bfloat16, (p.batch, p.queries, p.Hq, mine.d))
+                c.tensor("lse", lse, torch.float32, (p.batch, p.Hq, p.queries))
+            c.seen += [("workspace", self.ws), *cache._tensors]
+            return PagedInputs(None, tok, bat), c.device()
+
+        inp, dev = _layout(fn, (self._key, cache._key, cache.struct.page_size),
+                           (q, table, length, o, lse), check)
+        if out is None:
+            o, lse = _fresh(stream, self.alloc_outputs)
+        inp = PagedInputs.from_buffer_copy(inp)
+        inp.q = q.data_ptr()
+        inp.table = table.data_ptr()
+        inp.length = length.data_ptr()
+        _run(fn, dev, stream, (q, table, length, o, lse, self.ws, cache.k, cache.v, cache.k_scale,
+                               cache.v_scale),
+             ctypes.byref(p), cache._ref, ctypes.byref(inp), o.data_ptr(), lse.data_ptr(),
+             self.ws.data_ptr(), self.ws.numel())
+        return o, lse
+
+    def check(self, stream=None):
+        check_status(self.ws, stream)
+
+
+def paged_workspace_bytes(problem: PagedProblem, cache: KvCache) -> int:
+    return int(lib().csbp_paged_workspace_bytes(ctypes.byref(problem), ctypes.byref(cache)))
 
 
 class PrefixAttention:

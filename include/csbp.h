@@ -330,9 +330,10 @@ csbp_status csbp_kernel_timing_read(double* fwd_ms, int32_t* n_fwd, double* bwd_
  * of the attention calls: 6 the LSE merge (one per query stream and batch
  * entry), 7 the backward preprocess and 8 the dQ convert (one per query
  * stream), 9 the dK/dV converts of a windowed backward (one pair per key
- * stream); 10 csbp_e4m3_to_bf16; and (csbp_generate.h) 11 csbp_cache_write,
- * 12 csbp_cache_read, 13 the attention kernel of csbp_attn_prefix and 14 the
- * joining of its key ranges, 15 csbp_draft_verify.  One event pair per launch.
+ * stream); 10 csbp_e4m3_to_bf16; and (csbp_generate.h) 11 csbp_cache_write and
+ * csbp_cache_append, 12 csbp_cache_read, 13 the attention kernel of
+ * csbp_attn_prefix or csbp_attn_paged and 14 the joining of the former's key
+ * ranges, 15 csbp_draft_verify.  One event pair per launch.
  * CSBP_ERR_INVALID for another kind. */
 csbp_status csbp_kernel_timing_read_kind(int32_t kind, double* ms, int32_t* n);
 

@@ -6,6 +6,11 @@
  *   csbp_cache_write / csbp_cache_read   a paged K/V cache kept in E4M3 with
  *                     one power-of-two scale per 32 features, written from
  *                     bf16 and read back to bf16
+ *   csbp_cache_append the same write with the position rotation on the way,
+ *                     of the queries too
+ *   csbp_attn_paged   attention of a few new tokens per sequence over that
+ *                     cache where it lies, optionally with a sliding window and
+ *                     first tokens that stay visible
  *   csbp_attn_prefix  attention of a batch of sequences that share one long
  *                     prefix: the prefix keys are read once for all of them
  *   csbp_draft_verify verification of drafted tokens against the target's
@@ -91,6 +96,84 @@ csbp_status csbp_cache_write(const csbp_kv_cache* cache, const csbp_cache_rows* 
  * out of range (as above) reads as NaN.                                   */
 csbp_status csbp_cache_read(const csbp_kv_cache* cache, const csbp_cache_rows* rows, void* k,
                             void* v, void* stream);
+
+/* --------------------------------------------- append with position rotation
+ * Rotary positions: of the first `dim` features of each K and Q head, the pairs
+ * (x_i, x_{i + dim/2}), or (x_2i, x_2i+1) if `interleaved`, i < dim / 2, become
+ *   (a cos t - b sin t, a sin t + b cos t),  t = position x freq_i,
+ * in fp32, with t exact modulo a whole turn at any position (`turns`).       */
+typedef struct {
+  int32_t dim;            /* a multiple of 16, 16 .. d                      */
+  int32_t interleaved;    /* 0 or 1                                         */
+  const uint64_t* turns;  /* device [dim / 2], 8-byte aligned               */
+} csbp_rotary;
+
+/* turns[i] = freq[i] / 2 pi modulo 1, in units of 2^-64, for n frequencies in
+ * radians per position.  Host memory, no CUDA call; the caller copies the
+ * result to the device.  CSBP_ERR_INVALID for a frequency above 2^20 or NaN.  */
+csbp_status csbp_rotary_turns(const double* freq, int32_t n, uint64_t* turns);
+
+/* Queries that a csbp_cache_append rotates along: bf16 [batch][rows][Hq][d],
+ * stride_tok / stride_batch of q (0) and out (1) as in csbp_inputs.  out may be
+ * q itself (with the same strides).                                        */
+typedef struct {
+  int32_t Hq;  /* 0: none */
+  const void* q;
+  void* out;
+  int64_t stride_tok[2], stride_batch[2];
+} csbp_append_queries;
+
+/* csbp_cache_write of the rotated k and of v, and the rotated queries rounded to
+ * bf16, in one call: row i of sequence b is at position start[b] + i.  Scales
+ * and codes are those of the rotated values themselves, without a rounding to
+ * bf16 in between; a pair with a NaN or an infinity in it, or a value past
+ * fp32's range, is stored as NaN.  Queries of the rows that take part (i <
+ * count[b]) are rotated whatever their position or page; others keep what they
+ * hold in `out`.  d is at most 512.  `queries` may be NULL.                 */
+csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_cache_rows* rows,
+                              const csbp_rotary* rotary, const void* k, const void* v,
+                              const csbp_append_queries* queries, void* stream);
+
+/* ------------------------------------------------ attention over the pages
+ * `queries` new tokens of each of `batch` sequences over the keys that a
+ * csbp_kv_cache holds for them (their own included: they are appended first).
+ * With c = min(max(length[b], 0), table_pages x page_size), query i stands at
+ * position t = c - queries + i and reads the keys j < c with
+ *   causal   j <= t           (otherwise the tokens read one another, too)
+ *   window   t - j < window  or  j < sinks   (window 0: all)
+ * A key whose page is outside [0, pages) is not read.  O = softmax(scale Q K^T) V
+ * and LSE as in csbp_attn_prefix (whose results they can be merged with); a
+ * query that reads no key has O = 0, LSE = -inf, and a key that a query does not
+ * read has no part in its result, whatever it holds.                       */
+typedef struct {
+  int32_t batch, queries;  /* >= 1                                          */
+  int32_t table_pages;     /* >= 1; x page_size below 2^31 - 1024           */
+  int32_t Hq;              /* a multiple of the cache's Hkv                 */
+  int32_t causal;
+  int32_t window, sinks;   /* >= 0; sinks only count with a window          */
+  float scale;             /* > 0, finite                                   */
+} csbp_paged_problem;
+
+/*  q       bf16 [batch][queries][Hq][d], strides as in csbp_inputs
+ *  table   device int32 [batch][table_pages], 4-byte aligned
+ *  length  device int32 [batch]: keys of each sequence, the new ones included */
+typedef struct {
+  const void* q;
+  int64_t stride_tok, stride_batch;
+  const int32_t *table, *length;
+} csbp_paged_inputs;
+
+/* Workspace bytes on the current device: the status word and partial results of
+ * the key ranges that sequences are cut into.  Only sizes are read of `cache`
+ * (Hkv, d, page_size).  0 for an invalid problem.                          */
+size_t csbp_paged_workspace_bytes(const csbp_paged_problem* problem, const csbp_kv_cache* cache);
+
+/* The cache's d is 64 or 128.  workspace: zeroed once by the caller, as in
+ * csbp_attn_fwd; calls that can overlap need workspaces of their own.
+ *  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]       */
+csbp_status csbp_attn_paged(const csbp_paged_problem* problem, const csbp_kv_cache* cache,
+                            const csbp_paged_inputs* in, void* o, float* lse, void* workspace,
+                            size_t ws_bytes, void* stream);
 
 /* --------------------------------------------------- shared-prefix attention
  * `batch` sequences of `queries` tokens each.  Every query reads all

@@ -120,3 +120,96 @@ def draft_verify(p, q, token, u, r, length):
         nxt = draw(pa)
     nxt = -1 if nxt is None else nxt
     return a, [int(t) for t in token[:a]] + [nxt] + [-1] * (K - a)
+
+
+# ------------------------------------------------------------ rotary positions
+def _pi(digits):
+    """pi x 10^digits, by Machin's formula in integers."""
+    one = 10 ** (digits + 10)
+
+    def arccot(x):
+        total = term = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+
+    return 4 * (4 * arccot(5) - arccot(239)) // 10 ** 10
+
+
+_TWO_PI = 2 * _pi(60)      # x 10^60
+
+
+def angles(pos, freq):
+    """pos x freq modulo 2 pi, [len(pos)][len(freq)]: the product is exact."""
+    out = np.empty((len(pos), len(freq)))
+    for f, x in enumerate(freq):
+        n, d = float(x).as_integer_ratio()
+        for i, p in enumerate(pos):
+            t = int(p) * n * 10 ** 60 // d % _TWO_PI
+            out[i, f] = t / 10 ** 60
+    return out
+
+
+def rotate(x, angle, interleaved):
+    """x float64 [rows][heads][d], angle [rows][dim / 2]."""
+    half = angle.shape[-1]
+    y = x.copy()
+    a, b = ((slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else
+            (slice(0, half), slice(half, 2 * half)))
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    with np.errstate(invalid="ignore"):
+        y[..., a] = x[..., a] * c - x[..., b] * s
+        y[..., b] = x[..., a] * s + x[..., b] * c
+    return y
+
+
+def pair_size(x, half, interleaved):
+    """|a| + |b| of the pair that each feature is in, |x| beyond the pairs."""
+    n = np.abs(x)
+    a, b = ((slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else
+            (slice(0, half), slice(half, 2 * half)))
+    both = n[..., a] + n[..., b]
+    n[..., a] = n[..., b] = both
+    return n
+
+
+# --------------------------------------------------- attention over the pages
+def paged_attention(q, k, v, table, length, page_size, causal, window, sinks, scale):
+    """q [B][n][Hq][d]; k, v [pages][page_size][Hkv][d], the values that the
+    cache stands for.  Returns (O, LSE [B][Hq][n], A = sum_j p_j |v_j|, Smax
+    [B][Hq][n], the largest scale * sum_c |q_c k_c| of a row's keys)."""
+    B, n, Hq, d = q.shape
+    pages, _, Hkv = k.shape[:3]
+    G = Hq // Hkv
+    O, A = np.zeros(q.shape), np.zeros(q.shape)
+    Z = np.full((B, Hq, n), -np.inf)
+    T = np.zeros((B, Hq, n))
+    for b in range(B):
+        c = min(max(int(length[b]), 0), table.shape[1] * page_size)
+        j = np.arange(c)
+        page = table[b, j // page_size].astype(np.int64)
+        there = (page >= 0) & (page < pages)
+        j, page = j[there], page[there]
+        kb, vb = k[page, j % page_size], v[page, j % page_size]
+        for i in range(n):
+            t = c - n + i
+            ok = np.ones(len(j), bool)
+            if causal:
+                ok &= j <= t
+            if window:
+                ok &= (t - j < window) | (j < sinks)
+            if not ok.any():
+                continue
+            for h in range(Hq):
+                x = kb[ok, h // G] @ q[b, i, h] * scale
+                m = x.max()
+                w = np.exp(x - m)
+                vv = vb[ok, h // G]
+                O[b, i, h] = w @ vv / w.sum()
+                A[b, i, h] = w @ np.abs(vv) / w.sum()
+                Z[b, h, i] = m + np.log(w.sum())
+                T[b, h, i] = (np.abs(kb[ok, h // G]) @ np.abs(q[b, i, h])).max() * scale
+    return O, Z, A, T

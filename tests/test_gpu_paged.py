@@ -1,0 +1,633 @@
+"""GPU parity of serving from the quantised paged cache (append with rotation,
+attention over the pages, window and sinks) with the float64 oracle.
+
+Tolerances, derived from the arithmetic (half a rounding step is eps / 2):
+ * append: scale bytes are equal; a code stands for the rotated value to half a
+   step of E4M3, plus the rotation's fp32 error, below 2^-20 (|a| + |b|) for a pair
+   (two products and a sum at 2^-24 each, sine and cosine within 2^-22 with their
+   argument's rounding); a rotated query to 2^-8 |y| (bf16) plus the same;
+ * attention: with A = sum_j p_j |v_j|, an O element is off by at most 2^-8 A
+   (P rounded to bf16 or finer) + 2^-8 |O| (O rounded to bf16) + 2^-12 A (the
+   exponential's 2^-21 and the sums' 2^-24 per step), and an exponent argument x
+   carries 2 d 2^-24 T from its dot product on the tensor cores, which truncate
+   (T the largest scale sum |q k| of the row), so 4 d 2^-24 T A more.  LSE: 2 d
+   2^-24 T + 2^-21 + 2^-22 |LSE|, and 2^-24 for each of at most 2^8 sequential
+   additions of a row's sum.  P below 2^-30 of a row's maximum may be held with an
+   absolute error of 2^-40 of the largest |v|: 2^-40 Vmax for each key.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from block_diffusion_lm_gb300 import csbp
+from oracle import generate_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from block_diffusion_lm_gb300 import build
+    build.build()
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def same(a, b):
+    """Bit by bit (NaN included)."""
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b,
+                                                                                     strict=True))
+
+
+# ------------------------------------------------------------------- append
+def dirty_cache(pages, page, Hkv, d, g):
+    c = csbp.QuantCache(pages, page, Hkv, d)
+    for t in (c.k, c.v, c.k_scale, c.v_scale):
+        t.copy_(torch.randint(0, 120, t.shape, generator=g, device="cuda"))
+    return c
+
+
+def slots(table, start, count, rows, page, pages):
+    """(b, i, slot) of every row that takes part; slot -1 when out of range."""
+    out = []
+    for b in range(table.shape[0]):
+        for i in range(rows if count is None else min(rows, max(0, int(count[b])))):
+            pos = int(start[b]) + i
+            ok = 0 <= pos < table.shape[1] * page
+            pg = int(table[b, pos // page]) if ok else -1
+            out.append((b, i, pg * page + pos % page if 0 <= pg < pages else -1))
+    return out
+
+
+def half_step(x, e):
+    """Half an E4M3 step at x under the scale 2^e."""
+    a = np.maximum(np.abs(x) / np.exp2(e), 2.0 ** -6)
+    return np.exp2(np.floor(np.log2(a)) - 4 + e)
+
+
+def check_append(c, before, q, out, k, v, table, start, count, freq, interleaved):
+    """The cache and the rotated queries against the oracle; `before`: what the
+    cache held, and `out` in rows that take no part."""
+    pages, page, Hkv, d = c.k.shape
+    B, rows = k.shape[:2]
+    at = slots(table, start, count, rows, page, pages)
+    half = len(freq)
+    pos = np.array([[int(start[b]) + i for i in range(rows)] for b in range(B)]).reshape(-1)
+    uniq, inv = np.unique(pos, return_inverse=True)
+    angle = O.angles(uniq, freq)[inv]
+    for x, codes, scales, old, old_s in ((k, c.k, c.k_scale, before[0], before[2]),
+                                         (v, c.v, c.v_scale, before[1], before[3])):
+        raw = f64(x).reshape(B * rows, Hkv, d)
+        y, size = raw, np.zeros(raw.shape)
+        if x is k:
+            y = O.rotate(raw, angle, interleaved)
+            size = O.pair_size(raw, half, interleaved)
+            size[..., 2 * half:] = 0
+        _, sb = O.quantise(y)
+        want = O.dequantise(old.cpu().numpy(), old_s.cpu().numpy()).reshape(-1, Hkv, d)
+        want_s = old_s.cpu().numpy().reshape(-1, Hkv, d // 32).copy()
+        tol = np.zeros(want.shape)
+        for b, i, s in at:
+            if s >= 0:
+                r = b * rows + i
+                want[s], want_s[s] = np.where(np.isfinite(y[r]), y[r], np.nan), sb[r]
+                e = np.repeat(sb[r].astype(int) - 127, 32, -1)
+                tol[s] = half_step(y[r], e) * (1 + 1e-9) + 2.0 ** -20 * size[r]
+        np.testing.assert_array_equal(scales.cpu().numpy().reshape(want_s.shape), want_s)
+        got = O.dequantise(codes.cpu().numpy(), scales.cpu().numpy()).reshape(want.shape)
+        np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+        fine = ~np.isnan(want)
+        assert (np.abs(got - want)[fine] <= tol[fine]).all()
+    if q is None:
+        return
+    raw = f64(q).reshape(B * rows, *q.shape[2:])
+    y = O.rotate(raw, angle, interleaved).reshape(q.shape)
+    size = O.pair_size(raw, half, interleaved)
+    size[..., 2 * half:] = 0
+    tol = 2.0 ** -8 * np.abs(y) + 2.0 ** -20 * size.reshape(q.shape)
+    got = f64(out)
+    part = np.zeros((B, rows), bool)
+    for b, i, _ in at:
+        part[b, i] = True
+    assert (np.abs(got - y)[part] <= tol[part]).all()
+    if (~part).any():
+        np.testing.assert_array_equal(got[~part], before[4][~part])
+
+
+def freqs(rot, theta=1e4):
+    return [theta ** (-2 * i / rot) for i in range(rot // 2)]
+
+
+def stored(c):
+    return [t.clone() for t in (c.k, c.v, c.k_scale, c.v_scale)]
+
+
+APPENDS = [  # batch, rows, page, table entries, Hkv, d, Hq, rotary dim
+    (1, 1, 1, 1, 1, 32, 1, 32), (3, 5, 16, 2, 2, 64, 14, 64), (2, 60, 64, 5, 3, 96, 0, 96),
+    (4, 33, 7, 8, 8, 128, 40, 128), (1, 100, 128, 2, 1, 512, 3, 512), (65, 1, 16, 3, 4, 128, 5, 16),
+    (2, 300, 48, 9, 2, 64, 4, 32), (3, 9, 4, 5, 2, 160, 2, 112), (2, 7, 16, 2, 8, 128, 32, 64),
+    (700, 6, 16, 2, 1, 128, 1, 128)]
+
+
+@pytest.mark.parametrize("B,rows,page,n,Hkv,d,Hq,rot", APPENDS)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_append(B, rows, page, n, Hkv, d, Hq, rot, interleaved, ragged):
+    g = gen(B * 1000 + rows)
+    pages = B * n + 2
+    c = dirty_cache(pages, page, Hkv, d, g)
+    before = stored(c)
+    k, v = normal(g, B, rows, Hkv, d), normal(g, B, rows, Hkv, d) * 1e-3
+    q = normal(g, B, rows, Hq, d) if Hq else None
+    table = torch.randperm(pages, generator=g, device="cuda")[:B * n].view(B, n).int()
+    start = torch.randint(0, n * page - rows + 1, (B,), generator=g, device="cuda").int()
+    count = None
+    if ragged:
+        count = torch.randint(-1, rows + 2, (B,), generator=g, device="cuda").int()
+    f = freqs(rot)
+    out = c.append(k, v, table, start, count, rotary=csbp.Rotary(f, interleaved), q=q)
+    assert (out is None) == (q is None)
+    if q is not None:
+        before.append(np.zeros(q.shape))
+    check_append(c, before, q, out, k, v, table, start, count, f, interleaved)
+
+
+def test_append_at_far_positions():
+    """Up to the last position of 31 bits: page 2^16, 2^15 - 1 entries."""
+    g = gen(3)
+    c = dirty_cache(2, 65536, 1, 64, g)
+    n = 32767
+    table = torch.full((3, n), -1, dtype=torch.int32, device="cuda")
+    table[0, -1], table[1, n // 3], table[2, 15] = 0, 1, 1
+    start = i32([n * 65536 - 9, n // 3 * 65536 + 77, 15 * 65536 + 5000])
+    k, v, q = (normal(g, 3, 9, h, 64) for h in (1, 1, 3))
+    before = [*stored(c), None]
+    f = freqs(64, 1e6)
+    out = c.append(k, v, table, start, rotary=csbp.Rotary(f), q=q)
+    check_append(c, before, q, out, k, v, table, start, None, f, False)
+
+
+def test_append_rows_without_a_place():
+    """Positions and pages out of range: nothing is written, queries are rotated
+    all the same (from negative positions on)."""
+    g = gen(4)
+    c = dirty_cache(3, 8, 2, 64, g)
+    table = i32([[0, 7], [-1, 1], [2, 5]])
+    start = i32([5, 2, -3])
+    k, v, q = (normal(g, 3, 8, h, 64) for h in (2, 2, 4))
+    before = [*stored(c), None]
+    f = freqs(48)
+    out = c.append(k, v, table, start, rotary=csbp.Rotary(f), q=q)
+    check_append(c, before, q, out, k, v, table, start, None, f, False)
+
+
+def test_append_scales_next_to_where_they_change():
+    """Groups whose largest rotated magnitude is 448 x 2^e but for a 10^-9th,
+    above and below: the scale is that of the rotation itself."""
+    d, n = 64, 32
+    c = csbp.QuantCache(1, n, 1, d)
+    x = torch.zeros((1, n, 1, d), dtype=torch.bfloat16, device="cuda")
+    x[..., 0] = 2.0        # pairs (2, 0): cos t is 0.875 next to the border
+    x[..., 5] = 1e-3
+    want = []
+    for sign in (-1, 1):
+        # position p turns by p f: one frequency for each test of both sides
+        f = [(np.arccos(0.875) + sign * 1e-9)] + [0.0] * 31
+        c.append(x[:, :2], x[:, :2], i32([[0]]), i32([0]), rotary=csbp.Rotary(f))
+        want.append(O.quantise(O.rotate(f64(x[0, :2]), O.angles([0, 1], f), False))[1])
+        np.testing.assert_array_equal(c.k_scale.cpu().numpy()[0, :2], want[-1])
+    assert want[0][1, 0, 0] != want[1][1, 0, 0]      # the two sides differ
+    # and many random angles, near the border by chance
+    g = gen(8)
+    k = normal(g, 1, n, 1, d)
+    k[..., ::2] *= 1e-2
+    f = freqs(64, 1e6)
+    before = [*stored(c)]
+    v = k.clone()
+    c.append(k, v, i32([[0]]), i32([0]), rotary=csbp.Rotary(f, True))
+    check_append(c, before, None, None, k, v, i32([[0]]), i32([0]), None, f, True)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_append_values_that_are_not_finite(value):
+    """Both of a pair are stored as NaN, the group's scale is the others'."""
+    g = gen(5)
+    c = dirty_cache(2, 16, 2, 96, g)
+    k, v = normal(g, 1, 20, 2, 96), normal(g, 1, 20, 2, 96)
+    k[0, 3, 1, 7] = k[0, 4, 0, 90] = v[0, 5, 0, 95] = value
+    k[0, 6] = value
+    before = stored(c)
+    f = freqs(64)
+    start = i32([0])        # position 0 of the cache is row 0; angle 0 among them
+    c.append(k, v, i32([[1, 0]]), start, rotary=csbp.Rotary(f))
+    y = O.rotate(f64(k)[0], O.angles(range(20), f), False)
+    assert not np.isfinite(y[3, 1, [7, 39]]).any()
+    check_append(c, before, None, None, k, v, i32([[1, 0]]), start, None, f, False)
+
+
+def test_append_strides_and_in_place():
+    """Views into a packed projection, queries rotated where they lie; and an
+    `out` of its own strides."""
+    g = gen(6)
+    B, rows, Hq, Hkv, d = 3, 7, 6, 2, 64
+    packed = normal(g, B, rows + 2, Hq + 2 * Hkv + 1, d)[:, :rows]
+    q, k, v = packed[:, :, :Hq], packed[:, :, Hq:Hq + Hkv], packed[:, :, Hq + Hkv:-1]
+    table, start, count = i32([[0, 1]] * 3) + 2 * torch.arange(3, device="cuda").int()[:, None], i32(
+        [0, 3, 8]), i32([7, 0, 5])
+    f, ro = freqs(64), csbp.Rotary(freqs(64))
+    c = dirty_cache(6, 8, Hkv, d, g)
+    before = stored(c)
+    room = torch.full((B, rows, Hq + 3, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = c.append(k, v, table, start, count, rotary=ro, q=q, out=room[:, :, :Hq])
+    assert out.data_ptr() == room.data_ptr()
+    check_append(c, [*before, np.full(q.shape, 7.0)], q, out, k, v, table, start, count, f, False)
+    assert (room[:, :, Hq:] == 7).all()
+    want, kept = out.clone(), packed.clone()
+    old = q.clone()
+    c.append(k, v, table, start, count, rotary=ro, q=q, out=q)
+    part = torch.arange(rows, device="cuda")[None] < count[:, None]
+    assert torch.equal(q[part], want[part]) and torch.equal(q[~part], old[~part])
+    assert torch.equal(packed[:, :, Hq:], kept[:, :, Hq:])
+
+
+def test_append_without_rotation_is_write():
+    g = gen(7)
+    a, b = (csbp.QuantCache(9, 16, 3, 128) for _ in range(2))
+    k, v = normal(g, 2, 50, 3, 128) * 3, normal(g, 2, 50, 3, 128)
+    table, start = torch.randperm(9, generator=g, device="cuda")[:8].view(2, 4).int(), i32([0, 13])
+    a.write(k, v, table, start)
+    b.append(k, v, table, start, rotary=csbp.Rotary([0.0] * 64))
+    assert same(stored(a), stored(b))
+
+
+# ---------------------------------------------------------------- attention
+def filled(pages, page, Hkv, d, g):
+    """A cache full of keys and values, and what they stand for."""
+    c = csbp.QuantCache(pages, page, Hkv, d)
+    x = [normal(g, pages, page, Hkv, d) for _ in range(2)]
+    table, zero = torch.arange(pages, device="cuda").int()[:, None], i32([0] * pages)
+    c.write(*x, table, zero)
+    return c
+
+
+def values(c):
+    return [O.dequantise(t.cpu().numpy(), s.cpu().numpy())
+            for t, s in ((c.k, c.k_scale), (c.v, c.v_scale))]
+
+
+def check_attn(out, q, c, table, length, causal, window, sinks, scale, rows=None):
+    k, v = values(c)
+    want, lse, A, T = O.paged_attention(f64(q), k, v, table.cpu().numpy(), length.tolist(),
+                                        c.k.shape[1], causal, window, sinks, scale)
+    d = q.shape[-1]
+    Tr = T.transpose(0, 2, 1)[..., None]
+    tiny = 2.0 ** -40 * np.nanmax(np.abs(np.where(np.isfinite(v), v, 0))) * max(length.tolist())
+    tol = (2.0 ** -8 + 2.0 ** -12 + 4 * d * 2.0 ** -24 * Tr) * A + 2.0 ** -8 * np.abs(want) + tiny
+    got = f64(out[0])
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / np.maximum(tol, 1e-30))
+    z = f64(out[1])
+    none = lse == -np.inf
+    np.testing.assert_array_equal(z == -np.inf, none)
+    assert (got.transpose(0, 2, 1, 3)[none] == 0).all()
+    tol = 2 * d * 2.0 ** -24 * T + 2.0 ** -21 + 2.0 ** -22 * np.abs(np.where(none, 0, lse)) + 2.0 ** -16
+    assert (np.abs(z[~none] - lse[~none]) <= tol[~none]).all()
+
+
+def attn_case(B, n, per, page, Hq, Hkv, d, seed, lens=None):
+    g = gen(seed)
+    pages = B * per + 2
+    c = filled(pages, page, Hkv, d, g)
+    table = torch.randperm(pages, generator=g, device="cuda")[:B * per].view(B, per).int()
+    if lens is None:
+        lens = torch.randint(0, per * page + 1, (B,), generator=g, device="cuda").tolist()
+    return c, normal(g, B, n, Hq, d), table, i32(lens)
+
+
+SHAPES = [  # batch, queries, table entries, page, Hq, Hkv, d, lengths
+    (1, 1, 1, 1, 1, 1, 64, [1]), (1, 1, 1, 1, 1, 1, 128, [0]),
+    (3, 1, 5, 16, 2, 2, 64, [80, 1, 17]), (2, 1, 9, 64, 32, 8, 128, [576, 129]),
+    (4, 1, 40, 16, 8, 1, 128, [640, 0, 333, 16]), (2, 1, 3, 100, 32, 4, 128, None),
+    (3, 1, 70, 7, 12, 4, 64, None), (2, 1, 11, 48, 14, 2, 64, [528, 47]),
+    (2, 1, 20, 16, 9, 3, 128, None), (2, 1, 6, 16, 40, 5, 64, None),
+    (1, 1, 4, 16, 24, 24, 64, [55]), (1, 1, 3, 32, 33, 11, 128, [90]),
+    (2, 1, 4, 16, 64, 1, 128, None), (2, 1, 4, 16, 34, 2, 64, None),
+    (5, 3, 6, 16, 8, 2, 64, [2, 96, 0, 1, 40]), (3, 9, 4, 64, 40, 8, 128, None),
+    (2, 16, 8, 32, 14, 2, 64, [256, 5]), (2, 32, 5, 64, 40, 8, 128, [320, 100]),
+    (1, 130, 3, 64, 4, 4, 128, [192]), (2, 70, 20, 16, 16, 2, 64, [300, 31]),
+    (1, 200, 5, 64, 5, 1, 64, [260]), (17, 2, 3, 8, 3, 1, 128, None),
+    (200, 1, 2, 16, 4, 2, 64, None), (1, 1, 1000, 1, 4, 1, 64, [777]),
+]
+MASKS = [(False, 0, 0), (True, 0, 0), (True, 37, 4), (False, 20, 0), (True, 1, 0), (False, 64, 70),
+         (True, 10000, 3)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("causal,window,sinks", MASKS)
+def test_attention(shape, causal, window, sinks):
+    B, n, per, page, Hq, Hkv, d, lens = shape
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 11, lens)
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window, sinks=sinks)
+    out = a.forward(q, c, table, length)
+    check_attn(out, q, c, table, length, causal, window, sinks, d ** -0.5)
+    # the same again, bit by bit
+    assert same(a.forward(q, c, table, length), out)
+    a.check()
+
+
+@pytest.mark.parametrize("B,n,per,page,Hq,Hkv,d,causal,window,sinks", [
+    (2, 1, 300, 64, 8, 2, 128, True, 0, 0),         # cut into many pieces
+    (1, 1, 2000, 16, 4, 1, 64, False, 0, 0),
+    (3, 1, 100, 64, 8, 8, 64, True, 5000, 130),
+    (2, 4, 150, 64, 8, 2, 128, True, 0, 0),
+    (1, 20, 200, 64, 10, 2, 64, False, 3000, 4),
+    (1, 300, 60, 64, 4, 1, 128, True, 1000, 4),     # a chunk
+])
+def test_attention_over_long_texts(B, n, per, page, Hq, Hkv, d, causal, window, sinks):
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 12,
+                                    [per * page - 7 * b - 3 for b in range(B)])
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window, sinks=sinks)
+    out = a.forward(q * 3, c, table, length)
+    check_attn(out, q * 3, c, table, length, causal, window, sinks, d ** -0.5)
+
+
+def test_attention_of_equal_weights_over_a_long_text():
+    """q = 0 and V = 1: O is 1 and the LSE ln of the number of keys, however many
+    are added up."""
+    B, per, page, Hkv, d = 2, 16384, 64, 2, 64
+    c = csbp.QuantCache(64, page, Hkv, d)
+    one = torch.ones((64, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    c.write(one, one, torch.arange(64, device="cuda").int()[:, None], i32([0] * 64))
+    table = torch.randint(0, 64, (B, per), device="cuda").int()
+    length = i32([per * page, per * page - 12345])
+    for n, Hq in ((1, 4), (40, 4)):
+        q = torch.zeros((B, n, Hq, d), dtype=torch.bfloat16, device="cuda")
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d)
+        o, lse = a.forward(q, c, table, length)
+        # sums of up to 2^20 terms that lose 2^-23 each in a run of at most 2^13 steps
+        assert (o.float() - 1).abs().max() <= 2.0 ** -8
+        want = torch.log(length.double())[:, None, None]
+        assert (lse.double() - want).abs().max() <= 2.0 ** -9
+
+
+def test_attention_strides_and_pages():
+    """Queries in a packed projection; pages out of range are not read; the same
+    page twice."""
+    B, n, per, page, Hq, Hkv, d = 3, 2, 6, 16, 8, 2, 128
+    c, _, table, _ = attn_case(B, n, per, page, Hq, Hkv, d, 13)
+    g = gen(14)
+    q = normal(g, B, n + 1, Hq + 3, d)[:, :n, :Hq]
+    table[0, 2], table[1, 0], table[2, :] = -1, 1 << 30, -(1 << 31)
+    table[1, 3] = table[1, 1]
+    length = i32([90, 96, 50])
+    for causal, window, sinks in MASKS:
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window,
+                                sinks=sinks, scale=0.3)
+        check_attn(a.forward(q, c, table, length), q, c, table, length, causal, window, sinks, 0.3)
+    # lengths past the table, and below zero
+    length = i32([1 << 30, -5, 97])
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d)
+    check_attn(a.forward(q, c, table, length), q, c, table, i32([96, 0, 96]), False, 0, 0, d ** -0.5)
+
+
+def test_attention_reads_pages_past_32_bits():
+    pages, page, Hkv, d = 70000, 64, 8, 128      # 4.6e9 codes
+    c = csbp.QuantCache(pages, page, Hkv, d)
+    g = gen(15)
+    ids = [69999, 3, 65536, 69998]
+    x = [normal(g, 4, page, Hkv, d) for _ in range(2)]
+    c.append(*x, i32(ids)[:, None], i32([0] * 4), rotary=csbp.Rotary([0.0] * 64))
+    small = csbp.QuantCache(4, page, Hkv, d)
+    small.write(*x, i32([[0], [1], [2], [3]]), i32([0] * 4))
+    for n in (1, 40):
+        q = normal(g, 1, n, 16, d)
+        a = csbp.PagedAttention(1, n, 4, page, 16, Hkv, d)
+        got = a.forward(q, c, i32([ids]), i32([250]))
+        assert same(got, a.forward(q, small, i32([[0, 1, 2, 3]]), i32([250])))
+
+
+# ------------------------------------- keys that are not read, not finite
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("kind", ["code", "scale"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,n,Hq,Hkv,causal,window,sinks,lens,where", [
+    (2, 1, 4, 2, True, 0, 0, [60, 33], (1, 33)),         # just past the end
+    (2, 1, 4, 2, True, 8, 4, [60, 33], (0, 30)),         # before the window
+    (2, 5, 4, 2, True, 0, 0, [60, 33], (0, 58)),         # later than some queries
+    (2, 5, 4, 2, True, 9, 2, [60, 33], (1, 21)),         # out of some queries' windows
+    (2, 40, 4, 2, True, 0, 0, [60, 45], (0, 40)),        # the same, many rows
+    (1, 40, 8, 1, True, 16, 3, [90], (0, 50)),
+    (1, 40, 8, 1, False, 16, 3, [90], (0, 40)),
+])
+def test_keys_that_are_not_read_do_not_matter(B, n, Hq, Hkv, causal, window, sinks, lens, where, d,
+                                              kind, name):
+    """NaN in a key: rows that do not read it come out as without it, bit by bit;
+    rows that do are NaN."""
+    page, per = 16, 6
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 16, lens)
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window, sinks=sinks)
+    clean = [x.clone() for x in a.forward(q, c, table, length)]
+    check_attn(clean, q, c, table, length, causal, window, sinks, d ** -0.5)
+    b, j = where
+    pg = int(table[b, j // page])
+    if kind == "code":
+        getattr(c, name)[pg, j % page, 0, 5] = 0x7f
+        getattr(c, name)[pg, j % page, Hkv - 1, d - 1] = 0xff
+    else:
+        getattr(c, name + "_scale")[pg, j % page, :, d // 32 - 1] = 255
+    o, lse = a.forward(q, c, table, length)
+    t = lens[b] - n + np.arange(n)
+    reads = np.full(n, j < lens[b])
+    if causal:
+        reads &= j <= t
+    if window:
+        reads &= (t - j < window) | (j < sinks)
+    G = Hq // Hkv
+    for bb in range(B):
+        for i in range(n):
+            for h in range(Hq):
+                bad = bb == b and reads[i] and (kind == "scale" or h // G in (0, Hkv - 1))
+                x, want = o[bb, i, h], clean[0][bb, i, h]
+                zx, zw = lse[bb, h, i], clean[1][bb, h, i]
+                if not bad:
+                    assert torch.equal(x, want) and torch.equal(zx, zw), (bb, i, h)
+                elif name == "k":
+                    assert x.isnan().all() and zx.isnan()
+                else:
+                    hit = [f for f in (5, d - 1) if kind == "code"
+                           and h // G == (0 if f == 5 else Hkv - 1)]
+                    hit = hit or list(range(d - 32, d))
+                    nan = x.isnan().cpu().numpy()
+                    assert nan[hit].all() and nan.sum() == len(hit)
+                    assert torch.equal(zx, zw)
+
+
+def test_values_far_apart():
+    """Scales from 2^-100 to 2^100 beside one another."""
+    B, n, per, page, Hq, Hkv, d = 1, 1, 8, 16, 4, 1, 64
+    for n in (1, 40):
+        c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 17, [128])
+        g = gen(18)
+        c.v_scale.copy_(torch.randint(27, 228, c.v_scale.shape, generator=g, device="cuda"))
+        c.k_scale.copy_(torch.randint(100, 125, c.k_scale.shape, generator=g, device="cuda"))
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+        check_attn(a.forward(q, c, table, length), q, c, table, length, True, 0, 0, d ** -0.5)
+
+
+def test_queries_far_apart():
+    """Rows of very large and very small queries."""
+    B, n, per, page, Hq, Hkv, d = 1, 8, 4, 16, 4, 2, 128
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 19, [64])
+    q = q * torch.exp2(torch.arange(-100, 28, 4, device="cuda").float()).view(1, n, Hq, 1)
+    q = q.bfloat16()
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, scale=2.0 ** -20)
+    check_attn(a.forward(q, c, table, length), q, c, table, length, False, 0, 0, 2.0 ** -20)
+    c.k_scale.sub_(60)
+    q2 = (q.float() * 2.0 ** 60).bfloat16()
+    check_attn(a.forward(q2, c, table, length), q2, c, table, length, False, 0, 0, 2.0 ** -20)
+
+
+# --------------------------------------------------------------- as one runs
+def step_state(seed, B=3, n=4, Hq=8, Hkv=2, d=64, page=16, per=8, layers=2):
+    g = gen(seed)
+    s = dict(ro=csbp.Rotary(freqs(d)), q=normal(g, B, n, Hq, d), k=normal(g, B, n, Hkv, d),
+             v=normal(g, B, n, Hkv, d),
+             caches=[filled(B * per, page, Hkv, d, g) for _ in range(layers)],
+             table=torch.randperm(B * per, generator=g, device="cuda").view(B, per).int(),
+             start=i32([60, 0, 33][:B]), a=csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, True),
+             o=torch.empty((B, n, Hq, d), dtype=torch.bfloat16, device="cuda"),
+             lse=torch.empty((B, Hq, n), device="cuda"), rq=normal(g, B, n, Hq, d))
+    s["length"] = s["start"] + n
+    return s
+
+
+def step(s, stream=None):
+    """Each layer appends its tokens and reads its cache; returns what came out."""
+    for c in s["caches"]:
+        c.append(s["k"], s["v"], s["table"], s["start"], rotary=s["ro"], q=s["q"], out=s["rq"],
+                 stream=stream)
+        s["a"].forward(s["rq"], c, s["table"], s["length"], out=(s["o"], s["lse"]), stream=stream)
+    return s["rq"], s["o"], s["lse"]
+
+
+def test_step_against_read_and_prefix_attention():
+    """append + paged attention = the write, read back and attention of the prefix
+    operator, to the difference of their roundings."""
+    s = step_state(20)
+    rq, o, lse = step(s)
+    c = s["caches"][-1]
+    B, n, Hq, d = s["q"].shape
+    rows = int(s["length"].max())
+    ko, vo = c.read(s["table"], i32([0] * B), rows=rows)
+    pre = csbp.PrefixAttention(B, n, 0, rows, Hq, c.Hkv, d, causal=True)
+    o2, lse2 = pre.forward(rq, None, None, ko, vo, s["length"])
+    A = vo.abs().float().max()
+    assert (o.float() - o2.float()).abs().max() <= 2 * (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -12) * A
+    assert (lse - lse2).abs().max() <= 2.0 ** -14
+    check_attn((o, lse), rq, c, s["table"], s["length"], True, 0, 0, d ** -0.5)
+
+
+def test_captured_step_follows_its_inputs():
+    """One graph of both operators in two layers, replayed with other values and
+    other lengths."""
+    s, t = step_state(21), step_state(22)
+    want = []
+    for x in (s, t):
+        before = [stored(c) for c in x["caches"]]
+        want.append([y.clone() for y in step(x)] + [y for c in x["caches"] for y in stored(c)])
+        for c, old in zip(x["caches"], before):
+            for dst, src in zip((c.k, c.v, c.k_scale, c.v_scale), old):
+                dst.copy_(src)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    keep = [stored(c) for c in s["caches"]]
+    with torch.cuda.graph(graph):
+        step(s)
+    for x, w in ((s, want[0]), (t, want[1]), (s, None)):
+        if w is None:
+            break
+        for name in ("q", "k", "v", "table", "start", "length"):
+            s[name].copy_(x[name])
+        for c, src in zip(s["caches"], keep if x is s else [stored(c) for c in t["caches"]]):
+            for dst, y in zip((c.k, c.v, c.k_scale, c.v_scale), src):
+                dst.copy_(y)
+        s["o"].fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [s["rq"], s["o"], s["lse"]] + [y for c in s["caches"] for y in stored(c)]
+        assert same(got, w)
+
+
+def test_two_streams_at_once():
+    a, b = step_state(23), step_state(24)
+    want = [[x.clone() for x in step(s)] for s in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for s, st in zip((a, b), streams):
+            step(s, stream=st)
+    torch.cuda.synchronize()
+    for s, w in zip((a, b), want):
+        assert same([s["rq"], s["o"], s["lse"]], w)
+
+
+def test_one_handle_many_calls_in_a_row():
+    """Pieces of one call are not mistaken for those of another: lengths change
+    from call to call on one workspace."""
+    c, q, table, _ = attn_case(4, 1, 200, 16, 8, 2, 128, 25)
+    a = csbp.PagedAttention(4, 1, 200, 16, 8, 2, 128, causal=True)
+    lens = [[3200, 1, 0, 50], [16, 3000, 2900, 2800], [0, 0, 0, 0], [3200] * 4, [1, 2, 3, 4]]
+    outs = [a.forward(q, c, table, i32(x)) for x in lens * 3]
+    torch.cuda.synchronize()
+    for k, x in enumerate(lens):
+        check_attn(outs[k], q, c, table, i32(x), True, 0, 0, 128 ** -0.5)
+        assert same(outs[k], outs[k + 5]) and same(outs[k], outs[k + 10])
+
+
+def test_rows_of_outputs_and_cache_behind_stay():
+    """Outputs are written whole and nothing else is; the cache is only read."""
+    c, q, table, length = attn_case(2, 3, 4, 16, 4, 2, 64, 26, [30, 64])
+    before = stored(c)
+    a = csbp.PagedAttention(2, 3, 4, 16, 4, 2, 64, True)
+    o = torch.full((4, 3, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, 4, 3), 7.0, device="cuda")
+    want = a.forward(q, c, table, length)
+    a.forward(q, c, table, length, out=(o[1:3], lse[1:3]))
+    assert same(want, (o[1:3], lse[1:3]))
+    assert (o[::3] == 7).all() and (lse[::3] == 7).all() and same(before, stored(c))
+
+
+def test_kernels_are_timed():
+    s = step_state(27)
+    step(s)
+    torch.cuda.synchronize()
+    ms, n = ctypes.c_double(), ctypes.c_int32()
+    csbp.kernel_timing(True)
+    try:
+        step(s)
+        torch.cuda.synchronize()
+        for kind in (11, 13):
+            assert csbp.lib().csbp_kernel_timing_read_kind(kind, ctypes.byref(ms),
+                                                           ctypes.byref(n)) == 0
+            assert n.value == 2 and 0.0 < ms.value < 1000.0
+    finally:
+        csbp.kernel_timing(False)
