@@ -68,6 +68,7 @@
 #include "csbp_generate.h"
 #include "csbp_internal.h"
 #include "device_once.h"
+#include "divisor.cuh"
 #include "generate_internal.h"
 #include "mbar_spin.cuh"
 #include "pair_math.cuh"
@@ -95,21 +96,6 @@ __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const void* tma
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
-
-// Division of 0 <= n < 2^31 by an invariant d >= 1 (Granlund and Montgomery,
-// "Division by invariant integers using multiplication").
-struct Divisor {
-  uint32_t mul, shift;
-  static Divisor of(uint32_t d) {
-    Divisor r{0, 0};
-    while ((uint64_t(1) << r.shift) < d) ++r.shift;
-    r.mul = static_cast<uint32_t>((((uint64_t(1) << r.shift) - d) << 32) / d + 1);
-    return r;
-  }
-  __host__ __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-    return (static_cast<uint32_t>((static_cast<uint64_t>(mul) * n) >> 32) + n) >> shift;
-  }
-};
 
 // True in one thread of a warp (all of it calls this).  With this test, and the
 // warp's number the same in all lanes for the compiler, it keeps what the MMAs and

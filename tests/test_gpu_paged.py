@@ -304,13 +304,15 @@ def check_attn(out, q, c, table, length, causal, window, sinks, scale, rows=None
     tiny = 2.0 ** -40 * np.nanmax(np.abs(np.where(np.isfinite(v), v, 0))) * max(length.tolist())
     tol = (2.0 ** -8 + 2.0 ** -12 + 4 * d * 2.0 ** -24 * Tr) * A + 2.0 ** -8 * np.abs(want) + tiny
     got = f64(out[0])
-    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / np.maximum(tol, 1e-30))
+    worst = float(np.max(np.abs(got - want) / np.maximum(tol, 1e-300)))
+    assert worst <= 1, worst
     z = f64(out[1])
     none = lse == -np.inf
     np.testing.assert_array_equal(z == -np.inf, none)
     assert (got.transpose(0, 2, 1, 3)[none] == 0).all()
     tol = 2 * d * 2.0 ** -24 * T + 2.0 ** -21 + 2.0 ** -22 * np.abs(np.where(none, 0, lse)) + 2.0 ** -16
-    assert (np.abs(z[~none] - lse[~none]) <= tol[~none]).all()
+    worst = float(np.max(np.abs(z[~none] - lse[~none]) / tol[~none], initial=0))
+    assert worst <= 1, worst
 
 
 def attn_case(B, n, per, page, Hq, Hkv, d, seed, lens=None):
