@@ -3,12 +3,11 @@
 // they lie, once, in E4M3.
 //
 // Rows and keys.  The query rows of one KV head of a sequence are (token, head of
-// the group), flattened; a row tile is up to 16 of them (8 where that is all: then
-// half of the softmax is left out).  A row tile reads the keys that any of its rows
-// reads, sinks first, then the window (or all), in steps of 16 keys per warp.  A
-// warp takes one KV head and every S-th step of 16 keys; the CTA's warps are H heads
-// x S such slices, so that the scale bytes of a token's heads, which share a 32-byte
-// sector, are read by one CTA at one time.
+// the group), flattened; a row tile is 8, 16 or 32 of them.  A row tile reads the
+// keys that any of its rows reads, sinks first, then the window (or all), in steps
+// of 16 keys per warp.  A warp takes one KV head and every S-th step of 16 keys; the
+// CTA's warps are H heads x S such slices, so that the scale bytes of a token's
+// heads, which share a 32-byte sector, are read by one CTA at one time.
 //
 // Work.  The steps of all sequences and row tiles, end to end, form one list that
 // is cut into equal shares, one per SM: every CTA adds the lengths up and finds its
@@ -16,22 +15,24 @@
 // leaves normalised fp32 partials with their LSE in the workspace, which a second
 // kernel joins exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
 //
-// Matrix products.  With at most 16 rows the tensor-memory path would write every K
-// and V value to shared memory once more, as bf16, and that alone would bound it:
-// the products are m16n8k16 warp MMAs, whose operands go from the codes to registers
-// with one conversion per two values (E4M3 to f16 is exact).  Which feature or key
-// is which k of an MMA is free as long as both operands agree, so a lane takes
-// what lies side by side.
-//   S = Q K^T  per group of 32 features in its own accumulator, which is then
-//              scaled by the key's 2^e in fp32; Q is held in f16 with a power of
-//              two per row (8 bits of mantissa, exact for elements down to 2^-23
-//              of the row's largest).
-//   O = P V    P is held in f16, as p 2^14 2^(e - E), with V's scale 2^e of the
-//              key and group and E the largest so far: its rounding is 2^-12 of
-//              p, or 2^-39 of the largest p v below f16's normal range.
+// Matrix products.  With so few rows the tensor-memory path would write every K and
+// V value to shared memory once more, as bf16, and that alone would bound it: the
+// products are m16n8k16 warp MMAs, whose operands go from the codes to registers
+// with one conversion per two values (E4M3 to f16 is exact).  Keys or features are
+// the 16 and query rows the 8, so that 8 rows waste nothing:
+//   S^T = K Q^T  per group of 32 features in its own accumulator, which is then
+//                scaled by the key's 2^e in fp32; Q is held in f16 with a power
+//                of two per row (8 bits of mantissa, exact for elements down to
+//                2^-23 of the row's largest).
+//   O^T = V^T P^T  P is held in f16, as p 2^14 2^(e - E), with V's scale 2^e of the
+//                key and group and E the largest so far: its rounding is 2^-11 of
+//                p, or 2^-39 of the largest p v below f16's normal range.
+// ldmatrix brings K's codes as four features of a key and, transposed, V's as four
+// keys of a feature; which of the 16 keys is which row of the first product is
+// chosen so that P^T needs one transposition of 8 x 8 for the second.
 // Maxima, sums, O and everything that is scaled are fp32.  The tensor cores'
 // accumulator drops what is below its last place at every step of 16 keys: after
-// 2,048 of them (2^-13) O is added to a second sum in shared memory.
+// 2,048 of them (2^-13) O is put aside in the workspace and a new sum begun.
 //
 // Keys that a row does not read.  Steps at the edge of a row's range are masked;
 // there, NaN codes of V are taken out of the product and put back into the rows
@@ -43,6 +44,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "csbp_generate.h"
 #include "csbp_internal.h"
@@ -55,8 +57,8 @@ namespace csbp {
 namespace {
 
 constexpr size_t kStatusBytes = 256;
-constexpr int kMaxWarps = 8;  // of a CTA: two per scheduler, for the registers
-constexpr int kStages = 4;
+constexpr int kMostWarps = 16;
+constexpr int kStages = 3;
 constexpr int kKeys = 16;     // of a warp's step
 constexpr int kFlush = 2048;  // steps that one accumulator takes in
 constexpr float kShift = 14.f;  // p is held as p 2^14; a row's maximum may lag by 2^1
@@ -79,18 +81,16 @@ struct PagedParams {
   float* part_o;  // [2 x CTAs][heads][tile rows][d]
   float* part_z;  // [2 x CTAs][heads][tile rows]
   int2* pieces;   // per sequence, row tile and head block: first CTA, number of them
+  float* aside_o;  // [CTAs x warps][tile rows][d]: sums put aside
+  float* aside_z;  // [CTAs x warps][tile rows]
 };
 
 // ----------------------------------------------------------- instructions
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  const int n = there ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
-  const int n = there ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -110,19 +110,19 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-// Two E4M3 codes (the low 16 bits) as f16, exact, NaN as NaN.
-__device__ __forceinline__ uint32_t f16_of(uint32_t two) {
+// Two E4M3 codes (of the low or the high half of a word) as f16, exact, NaN as NaN.
+__device__ __forceinline__ uint32_t f16_low(uint32_t w) {
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n}"
       : "=r"(r)
-      : "r"(two));
+      : "r"(w));
   return r;
 }
-__device__ __forceinline__ uint32_t f16_of_high(uint32_t two) {
+__device__ __forceinline__ uint32_t f16_high(uint32_t w) {
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n}"
       : "=r"(r)
-      : "r"(two));
+      : "r"(w));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -135,12 +135,34 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// 8 x 8 f16 numbers, row g in lanes 4g .. 4g + 3: transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+// Four 8 x 16-byte matrices: lane 4g + t gets bytes 4t .. of row g of each.
+__device__ __forceinline__ void load_rows(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// Two 16 x 16-byte matrices transposed: lane 4g + t gets rows 4t .. 4t + 3 of columns
+// g and g + 8 of each.
+__device__ __forceinline__ void load_columns(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // ------------------------------------------------------------ the work list
@@ -167,23 +189,44 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile,
   return r;
 }
 
-// A place in the list: entry (sequence, row tile), block of heads, step.
+// A place in the list: entry (sequence, row tile), block of heads, and the step, as
+// the warp's keys from j on, of which those below `end` count; `left` steps follow
+// in this stretch (the sinks, or the rest).
 struct Cursor {
-  int entry, block, step;
-  int b, tile;
+  int entry, block, b, tile;
+  int j, end, left;
+  bool front;
   Range r;
+  __device__ __forceinline__ void seek(const PagedParams& p, int slice, int step) {
+    front = step < r.n_first;
+    const int k = front ? step : step - r.n_first;
+    j = (front ? 0 : r.lo) + (k * p.slices + slice) * kKeys;
+    end = front ? r.first : r.hi;
+    left = (front ? r.n_first : r.n - r.n_first) - 1 - k;
+  }
   __device__ __forceinline__ void load(const PagedParams& p, int tile_rows) {
     b = p.by_row_tiles(entry);
     tile = entry - b * p.row_tiles;
     if (b < p.batch) r = range_of(p, b, tile, tile_rows);
   }
-  __device__ __forceinline__ void next(const PagedParams& p, int tile_rows) {
-    if (++step < r.n) return;
-    step = 0;
-    if (++block < p.head_blocks) return;
-    block = 0;
-    ++entry;
-    load(p, tile_rows);
+  __device__ __forceinline__ bool last() const {
+    return left == 0 && (!front || r.n == r.n_first);
+  }
+  __device__ __forceinline__ void next(const PagedParams& p, int tile_rows, int slice) {
+    if (left > 0) {
+      --left;
+      j += p.slices * kKeys;
+      return;
+    }
+    int step = 0;
+    if (front && r.n > r.n_first) {
+      step = r.n_first;
+    } else if (++block == p.head_blocks) {
+      block = 0;
+      ++entry;
+      load(p, tile_rows);
+    }
+    seek(p, slice, step);
   }
 };
 
@@ -191,9 +234,9 @@ struct Share {
   uint64_t total, per, begin, end;  // steps
 };
 
-// Adds all steps up and finds the CTA's share: (entry, block, step) of its begin.
+// Adds all steps up and finds the CTA's share, and the cursor of its begin.
 __device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows, uint64_t* room,
-                                            Cursor& cur) {
+                                            int slice, Cursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int entries = p.batch * p.row_tiles;
   Share s{0, 0, 0, 0};
@@ -233,8 +276,8 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows,
         const uint64_t from = before + sum - mine;
         if (s.begin >= from && s.begin < from + mine) {
           const uint32_t in = static_cast<uint32_t>(s.begin - from);
-          room[kMaxWarps] = static_cast<uint64_t>(e);
-          room[kMaxWarps + 1] = static_cast<uint64_t>(in / n) << 32 | in % n;
+          room[kMostWarps] = static_cast<uint64_t>(e);
+          room[kMostWarps + 1] = static_cast<uint64_t>(in / n) << 32 | in % n;
         }
       }
       before += all;
@@ -244,50 +287,56 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows,
   }
   __syncthreads();
   if (s.begin < s.end) {
-    cur.entry = static_cast<int>(room[kMaxWarps]);
-    cur.block = static_cast<int>(room[kMaxWarps + 1] >> 32);
-    cur.step = static_cast<int>(room[kMaxWarps + 1]);
+    cur.entry = static_cast<int>(room[kMostWarps]);
+    cur.block = static_cast<int>(room[kMostWarps + 1] >> 32);
     cur.load(p, tile_rows);
+    cur.seek(p, slice, static_cast<int>(room[kMostWarps + 1]));
   }
   return s;
 }
 
+// Warps of a CTA, by its registers: 32 sums and 16 words of Q per lane and 8 rows.
+__host__ __device__ constexpr int most_warps(int tiles) { return tiles == 1 ? 16 : tiles == 2 ? 12 : 8; }
+
 // ------------------------------------------------------------ shared memory
-template <int D, bool kHalf>
+template <int D, int NT>
 struct Rows {
-  static constexpr int kRows = kHalf ? 8 : 16;  // of a tile
+  static constexpr int kRows = 8 * NT;  // of a tile
   static constexpr int kGroups = D / 32;
-  // a warp's ring stage: K codes, V codes, scale words (K, V), which keys are there
+  // a warp's ring stage: K codes, V codes, scale words (K, V), which keys are there;
+  // a step that has been worked on leaves it to 8 rows of the result [row][D + 4]
+  // and their LSE (log2)
   static constexpr int kCodes = kKeys * D;
   static constexpr int kWords = 2 * kCodes;
   static constexpr int kThere = kWords + 2 * kKeys * 4;
-  static constexpr int kStage = kThere + 16;
-  // the step's scales: fp32 of K [key][group], f16 of V [key][group]
+  static constexpr int kSumRow = D + 4;
+  static constexpr int kSumZ = 8 * kSumRow * 4;
+  static constexpr int kStage = (kThere + 16 > kSumZ + 32 ? kThere + 16 : kSumZ + 32) / 128 * 128 + 128;
+  // the step's scales: fp32 of K [key][group], f16 of V [group][key]
   static constexpr int kScales = kStages * kStage;
-  static constexpr int kScaleBytes = kKeys * kGroups * 6;
-  // second sum: normalised O [row][D] and LSE (log2)
-  static constexpr int kSum = kScales + kScaleBytes;
-  static constexpr int kSumRow = D;
-  static constexpr int kSumZ = kSum + kRows * kSumRow * 4;
-  static constexpr int kWarpBytes = (kSumZ + kRows * 4 + 127) / 128 * 128;
-  static constexpr int kRoom = 128;  // find_share, in front
+  static constexpr int kWarpBytes = kScales + kKeys * kGroups * 6;
+  static constexpr int kRoom = 256;  // find_share, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
 
-  // Place of 32-byte group `g` of key row `r`: rows that are read together lie in
-  // different banks (K: a lane quarter reads rows r .. r + 3; V: rows r, r + 2, ..)
-  static __device__ __forceinline__ uint32_t k_at(int r, int g) {
-    return r * D + (D == 128 ? (g ^ (r & 3)) : (g ^ ((r >> 1) & 1))) * 32;
+  // Place of a row's 16-byte chunks: chunk c lies at c ^ this.  The rows that an
+  // ldmatrix takes at once (K: 0, 1, 4, 5, .. or 2, 3, 6, 7, ..; V: 0 .. 7) lie in
+  // different banks.
+  static __device__ __forceinline__ int k_swizzle(int r) {
+    return D == 128 ? (r & 1) | (r >> 1 & 6) : r >> 2 & 3;
   }
-  static __device__ __forceinline__ uint32_t v_at(int r, int g) {
-    const int q = ((r >> 1) & 7) | (r & 1) << 3;
-    return q * D + (D == 128 ? (g ^ (q & 3)) : (g ^ ((q >> 1) & 1))) * 32;
-  }
+  static __device__ __forceinline__ int v_swizzle(int r) { return D == 128 ? r & 7 : r >> 1 & 3; }
 };
-static_assert(Rows<128, false>::smem(kMaxWarps) <= 232448, "shared memory of a CTA");
+static_assert(Rows<128, 1>::smem(most_warps(1)) <= 232448 &&
+                  Rows<128, 2>::smem(most_warps(2)) <= 232448,
+              "shared memory of a CTA");
+static_assert(Rows<128, 1>::kWarpBytes % 128 == 0 && Rows<64, 1>::kWarpBytes % 64 == 0,
+              "swizzled rows");
 
-// Where key row r of a step stands among the scales: the four that lane quarter t
-// works with (2t, 2t + 1, 2t + 8, 2t + 9) side by side.
-__device__ __forceinline__ int scale_place(int r) { return (r & 6) << 1 | (r & 1) | (r >> 3) << 1; }
+// Key of row m of the first product: rows 2t, 2t + 1 and 2t + 8, 2t + 9 are the keys
+// 4t .. 4t + 3 that lane quarter t has of V.
+__device__ __forceinline__ int key_of(int m) { return (m & 6) << 1 | (m & 1) | (m >> 3) << 1; }
+// and the row of a key
+__device__ __forceinline__ int row_of_key(int r) { return (r >> 1 & 6) | (r & 1) | (r & 2) << 2; }
 
 // Byte-wise larger of two words.
 __device__ __forceinline__ uint32_t max_u8x4(uint32_t a, uint32_t b) { return __vmaxu4(a, b); }
@@ -300,80 +349,75 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return (m >> 7) * 0xffu;
 }
 
-// The keys of one step ahead: what the lane looked up for key row (lane & 15).
+// What a lane looked up for key row (lane & 15) of a step ahead.
 struct Ahead {
   int page, place, block;
 };
 
-template <int D, bool kHalf>
+template <int D, int NT>
 struct Kernel {
-  using L = Rows<D, kHalf>;
+  using L = Rows<D, NT>;
   static constexpr int kG = L::kGroups;
 
   const PagedParams& p;
   const int lane, g, t, slice, head_in;
   const uint32_t mem;  // the warp's shared memory
-  float* const sum;    // second sum
-  float* const sum_z;
 
-  // rows g and g + 8
-  uint32_t q[kG][2][4];
-  float acc[D / 8][4];
-  float m[2], l[2], row_scale[2];
-  int row_lo[2], row_hi[2];  // [lo, hi) of a row, besides the sinks
-  int all_lo, all_hi;        // of the rows of the tile alike
-  uint32_t top;              // E of each group, a byte each
-  bool summed;               // the second sum holds something
+  // rows 8n + 2t and 8n + 2t + 1 at 2n and 2n + 1
+  float acc[NT][D / 16][4];  // O^T: features 16f + g and + 8 of the two rows
+  uint32_t q[NT][D / 16][2];
+  float m[2 * NT], l[2 * NT], row_scale[2 * NT];
+  int row_lo[2 * NT], row_hi[2 * NT];  // [lo, hi) of a row, besides the sinks
+  int all_lo, all_hi;                  // of the rows of the tile alike
+  uint32_t top;                        // E of each group, a byte each
+  bool aside;                          // a sum has been put aside
 
-  __device__ __forceinline__ Kernel(const PagedParams& p, uint8_t* smem)
+  __device__ __forceinline__ Kernel(const PagedParams& p, const uint8_t* smem)
       : p(p), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3),
         slice(static_cast<int>(threadIdx.x >> 5) / p.heads),
         head_in(static_cast<int>(threadIdx.x >> 5) % p.heads),
-        mem(smem_u32(smem)), sum(reinterpret_cast<float*>(smem + L::kSum)),
-        sum_z(reinterpret_cast<float*>(smem + L::kSumZ)) {}
+        mem(smem_u32(smem)) {}
 
   __device__ __forceinline__ Ahead look(Cursor& cur) const {
-    const bool front = cur.step < cur.r.n_first;
-    const int step = front ? cur.step : cur.step - cur.r.n_first;
-    const int j = (front ? 0 : cur.r.lo) + (step * p.slices + slice) * kKeys + (lane & 15);
+    const int j = cur.j + (lane & 15);
     Ahead a;
     const int entry = p.by_page(j);
     a.place = j - entry * p.page_size;
     a.block = cur.block;
     a.page = -1;
-    if (j < (front ? cur.r.first : cur.r.hi))
+    if (j < cur.end)
       a.page = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
-    cur.next(p, L::kRows);
+    cur.next(p, L::kRows, slice);
     return a;
   }
 
-  // Starts the copies of a step into a stage of the ring.
+  // Starts the copies of a step into a stage of the ring.  A key that is not there
+  // is a copy of the cache's first row; its score is masked.
   __device__ __forceinline__ void issue(const Ahead& a, int stage, uint32_t& pending) const {
     const uint32_t at = mem + stage * L::kStage;
     const int head = a.block * p.heads + head_in;
-    const bool there = a.page >= 0 && a.page < p.pages && head < p.Hkv;
-    const int slot = there ? a.page * p.page_size + a.place : -1;
+    const bool there = static_cast<uint32_t>(a.page) < static_cast<uint32_t>(p.pages) && head < p.Hkv;
+    const uint32_t row =
+        there ? static_cast<uint32_t>(a.page * p.page_size + a.place) * p.Hkv + head : 0;
     constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
-    const int chunk = lane % kChunks;
+    const int chunk = lane % kChunks, r0 = lane / kChunks;
+    const uint8_t *k = p.k + chunk * 16, *v = p.v + chunk * 16;
 #pragma unroll
     for (int i = 0; i < kKeys / kAtOnce; ++i) {
-      const int r = i * kAtOnce + lane / kChunks;
-      const int from = __shfl_sync(0xffffffffu, slot, r);
-      const int64_t row = (static_cast<int64_t>(max(from, 0)) * p.Hkv + head) * D + chunk * 16;
-      const bool ok = from >= 0;
-      copy16(at + L::k_at(r, chunk >> 1) + (chunk & 1) * 16, p.k + (ok ? row : 0), ok);
-      copy16(at + L::kCodes + L::v_at(r, chunk >> 1) + (chunk & 1) * 16, p.v + (ok ? row : 0), ok);
+      const int r = i * kAtOnce + r0;
+      const uint64_t from = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * D;
+      copy16(at + r * D + (chunk ^ L::k_swizzle(r)) * 16, k + from);
+      copy16(at + L::kCodes + r * D + (chunk ^ L::v_swizzle(r)) * 16, v + from);
     }
-    // scale bytes of K (lanes 0 .. 15) and V; a key that is not there has 0
+    // scale bytes of K (lanes 0 .. 15) and V
     const uint8_t* scales = lane < 16 ? p.k_scale : p.v_scale;
-    const int64_t place = there ? (static_cast<int64_t>(slot) * p.Hkv + head) * kG : 0;
+    const uint64_t place = static_cast<uint64_t>(row) * kG;
     if (p.wide_scales) {
-      copy4(at + L::kWords + lane * 4, scales + (place & ~int64_t(3)), there);
+      copy4(at + L::kWords + lane * 4, scales + (place & ~uint64_t(3)));
     } else {
       uint32_t w = 0;
-      if (there)
 #pragma unroll
-        for (int e = 0; e < kG; ++e) w |= static_cast<uint32_t>(__ldg(scales + place + e)) << 8 * e;
+      for (int e = 0; e < kG; ++e) w |= static_cast<uint32_t>(__ldg(scales + place + e)) << 8 * e;
       pending = w;  // stored when the next step is issued, so that nobody waits here
     }
     const uint32_t is = __ballot_sync(0xffffffffu, there);
@@ -384,65 +428,67 @@ struct Kernel {
     if (!p.wide_scales) sts32(mem + stage * L::kStage + L::kWords + lane * 4, pending);
   }
 
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[n][f][k] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x) {
+      l[x] = 0.f;
+      // (not -inf: a difference with a masked score has to stay a number)
+      m[x] = -3e38f;
+    }
+    top = 0;
+  }
+
   // Rows of a tile: queries to registers, and what each row reads.
   __device__ __forceinline__ void begin(const Cursor& cur) {
-    const int head = cur.block * p.heads + head_in;
+    const int head = min(cur.block * p.heads + head_in, p.Hkv - 1);
     const int rows = p.queries * p.G, row0 = cur.tile * L::kRows;
 #pragma unroll
-    for (int x = 0; x < (kHalf ? 1 : 2); ++x) {
-      const int r = row0 + g + 8 * x;
-      const int i = p.by_G(min(r, rows - 1)), gi = min(r, rows - 1) - i * p.G;
-      uint4 raw[kG];
-      const __nv_bfloat16* src =
-          p.q + cur.b * p.q_bat + i * p.q_tok +
-          (static_cast<int64_t>(min(head, p.Hkv - 1)) * p.G + gi) * D + t * 8;
+    for (int n = 0; n < NT; ++n) {
+      const int r = min(row0 + 8 * n + g, rows - 1);
+      const int i = p.by_G(r), gi = r - i * p.G;
+      const __nv_bfloat16* src = p.q + cur.b * p.q_bat + i * p.q_tok +
+                                 (static_cast<int64_t>(head) * p.G + gi) * D + t * 4;
+      uint2 raw[D / 16];
 #pragma unroll
-      for (int e = 0; e < kG; ++e) raw[e] = __ldg(reinterpret_cast<const uint4*>(src + e * 32));
+      for (int f = 0; f < D / 16; ++f) raw[f] = __ldg(reinterpret_cast<const uint2*>(src + f * 16));
       uint32_t most = 0;
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        const uint32_t w[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) most = max(most, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
-      }
+      for (int f = 0; f < D / 16; ++f)
+        most = max(max(most, max(raw[f].x & 0x7fffu, raw[f].x >> 16 & 0x7fffu)),
+                   max(raw[f].y & 0x7fffu, raw[f].y >> 16 & 0x7fffu));
       most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
       // the largest element becomes 2^7 .. 2^8
       const int ex = max(static_cast<int>(most >> 7) - 127, -110);
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-      row_scale[x] = p.scale_log2 * ldexpf(1.f, ex - 7);
+      const float scale = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
+      const float back = p.scale_log2 * ldexpf(1.f, ex - 7);
+      row_scale[2 * n] = __shfl_sync(0xffffffffu, back, 8 * t);
+      row_scale[2 * n + 1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        const uint32_t w[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          h[k] = pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-        q[e][0][x] = h[0];
-        q[e][0][x + 2] = h[1];
-        q[e][1][x] = h[2];
-        q[e][1][x + 2] = h[3];
+      for (int f = 0; f < D / 16; ++f) {
+        q[n][f][0] = pack_f16(__uint_as_float(raw[f].x << 16) * scale,
+                              __uint_as_float(raw[f].x & 0xffff0000u) * scale);
+        q[n][f][1] = pack_f16(__uint_as_float(raw[f].y << 16) * scale,
+                              __uint_as_float(raw[f].y & 0xffff0000u) * scale);
       }
-      const int at = cur.r.c - p.queries + i;
-      row_hi[x] = p.causal ? at + 1 : cur.r.c;
-      row_lo[x] = p.window ? at - p.window + 1 : 0;
-    }
-    if (kHalf) {
 #pragma unroll
-      for (int e = 0; e < kG; ++e) q[e][0][1] = q[e][0][3] = q[e][1][1] = q[e][1][3] = 0;
+      for (int x = 0; x < 2; ++x) {
+        const int at = cur.r.c - p.queries + static_cast<int>(p.by_G(min(row0 + 8 * n + 2 * t + x, rows - 1)));
+        row_hi[2 * n + x] = p.causal ? at + 1 : cur.r.c;
+        row_lo[2 * n + x] = p.window ? at - p.window + 1 : 0;
+      }
     }
     const int i0 = p.by_G(row0), i1 = p.by_G(min(row0 + L::kRows, rows) - 1);
     all_hi = p.causal ? cur.r.c - p.queries + i0 + 1 : cur.r.c;
     all_lo = p.window ? cur.r.c - p.queries + i1 - p.window + 1 : 0;
-#pragma unroll
-    for (int e = 0; e < D / 8; ++e)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
-    // (not -inf: a difference with a masked score has to stay a number)
-    m[0] = m[1] = -3e38f;
-    l[0] = l[1] = 0.f;
-    top = 0;
-    summed = false;
+    aside = false;
+    clear();
   }
 
   __device__ __forceinline__ bool reads(int x, int j) const {
@@ -459,9 +505,11 @@ struct Kernel {
       const int by = static_cast<int>((now >> 8 * e & 255) - (top >> 8 * e & 255));
       const float f = by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[4 * e + k][c] *= f;
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[n][2 * e + k][c] *= f;
     }
     top = now;
   }
@@ -476,382 +524,403 @@ struct Kernel {
       const int head = cur.block * p.heads + head_in;
       word = head & 1 ? word >> 16 : word & 0xffffu;
     }
-    const bool odd_scale = any_byte_255(word);
-    const uint32_t v_word =
-        lane < 16 ? 0 : odd_scale ? word & ~(__vcmpeq4(word, 0xffffffffu)) : word;
-    if (__any_sync(0xffffffffu, max_u8x4(top, v_word) != top)) raise_top(v_word);
     const bool is_there = there >> (lane & 15) & 1;
+    const bool odd_scale = any_byte_255(word);
+    uint32_t v_word = lane >= 16 && is_there ? word : 0;
+    if (odd_scale) v_word &= ~__vcmpeq4(word, 0xffffffffu);
+    if (__any_sync(0xffffffffu, max_u8x4(top, v_word) != top)) raise_top(v_word);
     // byte by byte, nothing is borrowed
-    const uint32_t delta = is_there ? top - v_word : 0;
-    // f16 holds 2^-delta to delta = 14 (bytes of 4 (15 - delta)); more goes another way
-    bool special = lane >= 16 && (odd_scale || ((delta + 0x71717171u) & 0x80808080u) != 0 ||
-                                  (delta & 0x80808080u) != 0);
-    if (D == 64) special = lane >= 16 && (odd_scale || ((delta + 0x00007171u) & 0x8080u) != 0 ||
-                                          (delta & 0x8080u) != 0);
-    special = __any_sync(0xffffffffu, special && is_there);
+    const uint32_t delta = lane >= 16 && is_there ? top - v_word : 0;
+    // f16 holds 2^-delta to delta = 14; more, and NaN, goes another way
+    const bool special = __any_sync(
+        0xffffffffu, (delta + 0x71717171u * (kG == 4) + 0x7171u * (kG == 2) | delta) & 0x80808080u ||
+                         (lane >= 16 && is_there && odd_scale));
     __syncwarp();  // (the scales of the step before have been read)
-    {
-      const int place = scale_place(lane & 15);
-      if (lane < 16) {
-        float f[kG];
+    const int key = lane & 15;
+    if (lane < 16) {
+      float f[kG];
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          const uint32_t b = word >> 8 * e & 255;
-          f[e] = __uint_as_float(b == 255 ? 0x7fffffffu : max(b << 23, 0x00400000u));
-        }
-        if constexpr (kG == 4)
-          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(scales + place * 16), "f"(f[0]),
-                       "f"(f[1]), "f"(f[2]), "f"(f[3])
-                       : "memory");
-        else
-          asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(scales + place * 8), "f"(f[0]),
-                       "f"(f[1])
-                       : "memory");
-      } else {
-        // upper bytes of the f16 numbers 2^-delta
-        const uint32_t h = 0x3c3c3c3cu - (delta << 2 & 0xfcfcfcfcu);
-        if constexpr (kG == 4)
-          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(v_scales + place * 8),
-                       "r"(__byte_perm(h, 0, 0x1404)), "r"(__byte_perm(h, 0, 0x3424))
-                       : "memory");
-        else
-          sts32(v_scales + place * 4, __byte_perm(h, 0, 0x1404));
+      for (int e = 0; e < kG; ++e) {
+        const uint32_t b = word >> 8 * e & 255;
+        f[e] = __uint_as_float(b == 255 ? 0x7fffffffu : max(b << 23, 0x00400000u));
+      }
+      const uint32_t to = scales + row_of_key(key) * kG * 4;
+      if constexpr (kG == 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to), "f"(f[0]), "f"(f[1]),
+                     "f"(f[2]), "f"(f[3])
+                     : "memory");
+      else
+        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(f[0]), "f"(f[1]) : "memory");
+    } else {
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {  // 2^-delta
+        const uint32_t h = 0x3c00u - ((delta >> 8 * e & 255) << 10);
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_scales + e * (2 * kKeys) + key * 2),
+                     "h"(static_cast<uint16_t>(h))
+                     : "memory");
       }
     }
     __syncwarp();
 
-    // ------- S = Q K^T
-    float s[2][4];
+    // ------- S^T = K Q^T, keys of rows g and g + 8
+    float s[NT][4];
     {
-      float ks[4][kG];  // of keys 2t, 2t + 1, 2t + 8, 2t + 9
+      float ks[2][kG];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t from = scales + (8 * k + g) * kG * 4;
         if constexpr (kG == 4)
           asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                        : "=f"(ks[k][0]), "=f"(ks[k][1]), "=f"(ks[k][2]), "=f"(ks[k][3])
-                       : "r"(scales + (4 * t + k) * 16)
+                       : "r"(from)
                        : "memory");
         else
           asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
                        : "=f"(ks[k][0]), "=f"(ks[k][1])
-                       : "r"(scales + (4 * t + k) * 8)
+                       : "r"(from)
                        : "memory");
       }
+      const int r = key_of(lane & 15);
+      const uint32_t k0 = at + r * D + (((lane >> 4) ^ L::k_swizzle(r)) << 4);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int e = 0; e < kG; ++e) {
+        uint32_t w[4];
+        load_rows(w, k0 ^ (e << 5));
+        uint32_t a[8];
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          const uint2 w = lds64(at + L::k_at(8 * x + g, e) + 8 * t);
+        for (int k = 0; k < 4; ++k) {
+          a[k] = f16_low(w[k]);
+          a[4 + k] = f16_high(w[k]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(c, q[e][0], f16_of(w.x), f16_of_high(w.x));
-          mma(c, q[e][1], f16_of(w.y), f16_of_high(w.y));
-          if (e == 0) {
-            s[x][0] = c[0] * ks[2 * x][0];
-            s[x][1] = c[1] * ks[2 * x + 1][0];
-            s[x][2] = c[2] * ks[2 * x][0];
-            s[x][3] = c[3] * ks[2 * x + 1][0];
-          } else {
-            s[x][0] = fmaf(c[0], ks[2 * x][e], s[x][0]);
-            s[x][1] = fmaf(c[1], ks[2 * x + 1][e], s[x][1]);
-            s[x][2] = fmaf(c[2], ks[2 * x][e], s[x][2]);
-            s[x][3] = fmaf(c[3], ks[2 * x + 1][e], s[x][3]);
-          }
+          mma(c, a[0], a[1], a[4], a[5], q[n][2 * e][0], q[n][2 * e][1]);
+          mma(c, a[2], a[3], a[6], a[7], q[n][2 * e + 1][0], q[n][2 * e + 1][1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            s[n][k] = e == 0 ? c[k] * ks[k >> 1][0] : fmaf(c[k], ks[k >> 1][e], s[n][k]);
         }
       }
     }
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < (kHalf ? 2 : 4); ++k) s[x][k] *= row_scale[k >> 1];
+      for (int k = 0; k < 4; ++k) s[n][k] *= row_scale[2 * n + (k & 1)];
 
     // ------- mask
-    const bool front = cur.step < cur.r.n_first;
-    const int j0 = (front ? 0 : cur.r.lo) +
-                   ((front ? cur.step : cur.step - cur.r.n_first) * p.slices + slice) * kKeys;
-    const bool inside = there == 0xffffu && j0 + kKeys <= all_hi &&
-                        (j0 >= all_lo || j0 + kKeys <= p.sinks);
+    const bool inside = there == 0xffffu && cur.j + kKeys <= all_hi &&
+                        (cur.j >= all_lo || cur.j + kKeys <= p.sinks);
     if (!inside) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int k = 0; k < 2; ++k) {
+        const int r = key_of(8 * k + g);
+        const bool here = there >> r & 1;
 #pragma unroll
-        for (int k = 0; k < (kHalf ? 2 : 4); ++k) {
-          const int r = 8 * x + 2 * t + (k & 1);
-          if (!(there >> r & 1) || !reads(k >> 1, j0 + r)) s[x][k] = -INFINITY;
-        }
+        for (int x = 0; x < 2 * NT; ++x)
+          if (!here || !reads(x, cur.j + r)) s[x >> 1][2 * k + (x & 1)] = -INFINITY;
+      }
     }
 
     // ------- softmax
-    const float most0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    const float most1 = kHalf ? 0.f : fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-    if (__any_sync(0xffffffffu, most0 > m[0] + 1.f || (!kHalf && most1 > m[1] + 1.f))) {
+    bool grows = false;
 #pragma unroll
-      for (int x = 0; x < (kHalf ? 1 : 2); ++x) {
-        float most = x ? most1 : most0;
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    for (int x = 0; x < 2 * NT; ++x)
+      grows |= fmaxf(s[x >> 1][x & 1], s[x >> 1][2 + (x & 1)]) > m[x] + 1.f;
+    if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+      for (int x = 0; x < 2 * NT; ++x) {
+        float most = fmaxf(s[x >> 1][x & 1], s[x >> 1][2 + (x & 1)]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
         const float now = fmaxf(m[x], most), f = ex2_approx(m[x] - now);
         m[x] = now;
         l[x] *= f;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          acc[e][2 * x] *= f;
-          acc[e][2 * x + 1] *= f;
+        for (int e = 0; e < D / 16; ++e) {
+          acc[x >> 1][e][x & 1] *= f;
+          acc[x >> 1][e][2 + (x & 1)] *= f;
         }
       }
     }
-    float pr[2][4];
+    float pr[NT][4];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < (kHalf ? 2 : 4); ++k) pr[x][k] = ex2_approx(s[x][k] - (m[k >> 1] - kShift));
-    l[0] += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
-    if (!kHalf) l[1] += (pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]);
+      for (int k = 0; k < 4; ++k) pr[n][k] = ex2_approx(s[n][k] - (m[2 * n + (k & 1)] - kShift));
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x) l[x] += pr[x >> 1][x & 1] + pr[x >> 1][2 + (x & 1)];
 
-    // ------- P under V's scales, a set for each group
-    uint32_t a[kG][4];
+    // ------- P^T: row g, keys 4t .. 4t + 3, under V's scales of each group
+    uint32_t b[NT][kG][2];
     if (!special) {
-      uint32_t pa[4];
-      pa[0] = pack_f16(pr[0][0], pr[0][1]);
-      pa[2] = pack_f16(pr[1][0], pr[1][1]);
-      if (!kHalf) {
-        pa[1] = pack_f16(pr[0][2], pr[0][3]);
-        pa[3] = pack_f16(pr[1][2], pr[1][3]);
-      }
-      uint32_t vs[4][kG / 2];
+      uint2 vs[kG];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (kG == 4) {
-          const uint2 w = lds64(v_scales + (4 * t + k) * 8);
-          vs[k][0] = w.x;
-          vs[k][1] = w.y;
-        } else {
-          vs[k][0] = lds32(v_scales + (4 * t + k) * 4);
+      for (int e = 0; e < kG; ++e) vs[e] = lds64(v_scales + e * (2 * kKeys) + 8 * t);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t b0 = transpose8(pack_f16(pr[n][0], pr[n][1]));
+        const uint32_t b1 = transpose8(pack_f16(pr[n][2], pr[n][3]));
+#pragma unroll
+        for (int e = 0; e < kG; ++e) {
+          b[n][e][0] = mul_f16x2(b0, vs[e].x);
+          b[n][e][1] = mul_f16x2(b1, vs[e].y);
         }
-      }
-#pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        const int which = e & 1 ? 0x7632 : 0x5410;
-        const uint32_t s01 = __byte_perm(vs[0][e >> 1], vs[1][e >> 1], which);
-        const uint32_t s23 = __byte_perm(vs[2][e >> 1], vs[3][e >> 1], which);
-        a[e][0] = mul_f16x2(pa[0], s01);
-        a[e][2] = mul_f16x2(pa[2], s23);
-        a[e][1] = kHalf ? 0 : mul_f16x2(pa[1], s01);
-        a[e][3] = kHalf ? 0 : mul_f16x2(pa[3], s23);
       }
     } else {
       // in fp32: scales far below the largest, or NaN (in the rows that read the key)
+      uint32_t w[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t w[2];
+      for (int k = 0; k < 2; ++k) {
+        w[k] = lds32(at + L::kWords + (16 + key_of(8 * k + g)) * 4);
+        if (D == 64 && p.wide_scales && ((cur.block * p.heads + head_in) & 1)) w[k] >>= 16;
+      }
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        float f[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int r = 8 * x + 2 * t + k;
-          w[k] = lds32(at + L::kWords + (16 + r) * 4);
-          if (D == 64 && p.wide_scales && ((cur.block * p.heads + head_in) & 1)) w[k] >>= 16;
+          const int byte = static_cast<int>(w[k] >> 8 * e & 255);
+          const int by = static_cast<int>(top >> 8 * e & 255) - byte;
+          f[k] = byte == 255 ? NAN
+                 : by >= 0 && by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23)
+                                       : 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          float f[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NT; ++n) {
+          float x[4];
 #pragma unroll
-          for (int k = 0; k < (kHalf ? 2 : 4); ++k) {
-            const int b = static_cast<int>(w[k & 1] >> 8 * e & 255);
-            const int by = static_cast<int>(top >> 8 * e & 255) - b;
-            const float scale = b == 255 ? NAN : by < 127 ? __uint_as_float((127u - by) << 23) : 0.f;
-            if (s[x][k] != -INFINITY) f[k] = pr[x][k] * scale;
-          }
-          a[e][2 * x] = pack_f16(f[0], f[1]);
-          a[e][2 * x + 1] = pack_f16(f[2], f[3]);
+          for (int k = 0; k < 4; ++k) x[k] = s[n][k] == -INFINITY ? 0.f : pr[n][k] * f[k >> 1];
+          b[n][e][0] = transpose8(pack_f16(x[0], x[1]));
+          b[n][e][1] = transpose8(pack_f16(x[2], x[3]));
         }
       }
     }
 
-    // ------- O += P V
-    const uint32_t v = at + L::kCodes + 4 * g;
+    // ------- O^T += V^T P^T
+    const int r = lane & 15;
+    const uint32_t v0 = at + L::kCodes + r * D + (((lane >> 4) ^ L::v_swizzle(r)) << 4);
     bool bad = false;
     if (!inside) {
 #pragma unroll
-      for (int e = 0; e < kG; ++e)
+      for (int e = 0; e < kG; ++e) {
+        uint32_t w[4];
+        load_columns(w, v0 ^ (e << 5));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          bad |= nan_codes(lds32(v + L::v_at(2 * t + (k & 1) + (k >> 1) * 8, e))) != 0;
+        for (int k = 0; k < 4; ++k) bad |= nan_codes(w[k]) != 0;
+      }
       bad = __any_sync(0xffffffffu, bad);
     }
     if (!bad) {
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
         uint32_t w[4];
+        load_columns(w, v0 ^ (e << 5));
+        uint32_t a[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = lds32(v + L::v_at(2 * t + (k & 1) + (k >> 1) * 8, e));
+        for (int k = 0; k < 4; ++k) {
+          a[k] = f16_low(w[k]);
+          a[4 + k] = f16_high(w[k]);
+        }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t lo = __byte_perm(w[0], w[1], k ? 0x7362 : 0x5140);
-          const uint32_t hi = __byte_perm(w[2], w[3], k ? 0x7362 : 0x5140);
-          mma(acc[4 * e + 2 * k], a[e], f16_of(lo), f16_of(hi));
-          mma(acc[4 * e + 2 * k + 1], a[e], f16_of_high(lo), f16_of_high(hi));
+        for (int n = 0; n < NT; ++n) {
+          mma(acc[n][2 * e], a[0], a[1], a[4], a[5], b[n][e][0], b[n][e][1]);
+          mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], b[n][e][0], b[n][e][1]);
         }
       }
     } else {
       // NaN codes as 0 in the product, then NaN wherever a row reads one of them
-      uint32_t sees[4] = {0, 0, 0, 0};
+      uint32_t sees[NT][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        sees[2 * x] = pack_f16(s[x][0] != -INFINITY, s[x][1] != -INFINITY);
-        if (!kHalf) sees[2 * x + 1] = pack_f16(s[x][2] != -INFINITY, s[x][3] != -INFINITY);
-      }
-#pragma unroll 1
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          sees[n][k] = transpose8(
+              pack_f16(s[n][2 * k] != -INFINITY, s[n][2 * k + 1] != -INFINITY));
+#pragma unroll
       for (int e = 0; e < kG; ++e) {
-        uint32_t w[4], is[4], ae[4] = {0, 0, 0, 0};
+        uint32_t w[4], is[4];
+        load_columns(w, v0 ^ (e << 5));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          w[k] = lds32(v + L::v_at(2 * t + (k & 1) + (k >> 1) * 8, e));
           is[k] = nan_codes(w[k]);
           w[k] &= ~is[k];
           is[k] &= 0x38383838u;  // 1
         }
 #pragma unroll
-        for (int c = 0; c < kG; ++c)
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ae[k] = c == e ? a[c][k] : ae[k];
+          for (int n = 0; n < NT; ++n) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma(acc[n][2 * e + f], f16_low(w[2 * f]), f16_low(w[2 * f + 1]), f16_high(w[2 * f]),
+                f16_high(w[2 * f + 1]), b[n][e][0], b[n][e][1]);
+            mma(c, f16_low(is[2 * f]), f16_low(is[2 * f + 1]), f16_high(is[2 * f]),
+                f16_high(is[2 * f + 1]), sees[n][0], sees[n][1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t pick = k & 2 ? 0x7362 : 0x5140;
-          const uint32_t lo = __byte_perm(w[0], w[1], pick), hi = __byte_perm(w[2], w[3], pick);
-          const uint32_t nlo = __byte_perm(is[0], is[1], pick), nhi = __byte_perm(is[2], is[3], pick);
-          float add[4] = {0.f, 0.f, 0.f, 0.f}, n[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(add, ae, k & 1 ? f16_of_high(lo) : f16_of(lo), k & 1 ? f16_of_high(hi) : f16_of(hi));
-          mma(n, sees, k & 1 ? f16_of_high(nlo) : f16_of(nlo), k & 1 ? f16_of_high(nhi) : f16_of(nhi));
-#pragma unroll
-          for (int c = 0; c < kG; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (c == e) acc[4 * c + k][i] += n[i] > 0.f ? NAN : add[i];
-        }
+            for (int k = 0; k < 4; ++k)
+              if (c[k] > 0.f) acc[n][2 * e + f][k] = NAN;
+          }
       }
     }
   }
 
-  // Adds what the registers hold to the second sum (normalised, with its LSE) and
-  // starts anew.
-  __device__ __forceinline__ void store_sum() {
+  // What the registers hold as a normalised O and its LSE, joined with what was put
+  // aside: O stays in `acc`, z[x] is the LSE (log2) of row x.
+  __device__ __forceinline__ void normalise(float (&z)[2 * NT]) {
+    const int64_t at =
+        (static_cast<int64_t>(blockIdx.x) * (p.heads * p.slices) + (threadIdx.x >> 5)) * L::kRows;
 #pragma unroll
-    for (int x = 0; x < (kHalf ? 1 : 2); ++x) {
-      float z = l[x];
-      z += __shfl_xor_sync(0xffffffffu, z, 1);
-      z += __shfl_xor_sync(0xffffffffu, z, 2);
-      const int row = g + 8 * x;
-      const float inv = z == 0.f ? 0.f : 1.f / z;
-      const float lse = z == 0.f ? -INFINITY : m[x] - kShift + log2f(z);
-      float mine = 1.f, old = 0.f, all = lse;
-      if (summed) {
-        const float before = sum_z[row], most = fmaxf(before, lse);
+    for (int x = 0; x < 2 * NT; ++x) {
+      const int n = x >> 1, row = 8 * n + 2 * t + (x & 1);
+      float sum = l[x];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      z[x] = sum == 0.f ? -INFINITY : m[x] - kShift + log2f(sum);
+      float mine = 1.f, old = 0.f;
+      if (aside) {
+        const float before = p.aside_z[at + row], most = fmaxf(before, z[x]);
         const float ref = most == -INFINITY ? 0.f : most;
         old = exp2f(before - ref);
-        mine = exp2f(lse - ref);
-        const float both = old + mine;
-        all = both == 0.f ? -INFINITY : ref + log2f(both);
-        const float f = both == 0.f ? 0.f : 1.f / both;
+        mine = exp2f(z[x] - ref);
+        const float both = old + mine, f = both == 0.f ? 0.f : 1.f / both;
+        z[x] = both == 0.f ? -INFINITY : ref + log2f(both);
         old *= f;
         mine *= f;
       }
-      __syncwarp();
-      if (t == 0) sum_z[row] = all;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        // 2^(E - 127), in two steps: the first may lie below fp32's range alone
-        const int ex = static_cast<int>(top >> 8 * e & 255);
+      for (int f = 0; f < D / 16; ++f) {
+        // 2^(E - 127), in two steps: one could lie below fp32's range
+        const int ex = static_cast<int>(top >> 8 * (f / 2) & 255);
         const float f0 = __uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23);
         const float f1 = __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63) << 23);
-        float* to = sum + row * L::kSumRow + 32 * e + 8 * t;
-        float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = acc[4 * e + k][2 * x] * inv * f0 * f1;
-          v[4 + k] = acc[4 * e + k][2 * x + 1] * inv * f0 * f1;
+        for (int k = 0; k < 2; ++k) {
+          float& o = acc[n][f][2 * k + (x & 1)];
+          o = o * inv * f0 * f1;
+          if (aside) o = o * mine + p.aside_o[(at + row) * D + 16 * f + 8 * k + g] * old;
         }
-        if (summed) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = to[k] * old + v[k] * mine;
-        }
-        reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
-      l[x] = 0.f;
     }
-#pragma unroll
-    for (int e = 0; e < D / 8; ++e)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
-    summed = true;
-    __syncwarp();
   }
 
-  // The rows of a piece, joined over the slices: to the outputs where the piece is
-  // the whole of a row's keys (`part` < 0), else to a place among the partials.
-  __device__ __forceinline__ void finish(const Cursor& cur, int part, const uint8_t* warps) const {
+  // Puts the sum aside and begins another.
+  __device__ __forceinline__ void put_aside() {
+    float z[2 * NT];
+    normalise(z);
+    const int64_t at =
+        (static_cast<int64_t>(blockIdx.x) * (p.heads * p.slices) + (threadIdx.x >> 5)) * L::kRows;
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x) {
+      const int n = x >> 1, row = 8 * n + 2 * t + (x & 1);
+      if (g == 0) p.aside_z[at + row] = z[x];
+#pragma unroll
+      for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          p.aside_o[(at + row) * D + 16 * f + 8 * k + g] = acc[n][f][2 * k + (x & 1)];
+    }
+    __syncwarp();
+    aside = true;
+    clear();
+  }
+
+  // The rows of a piece, joined over the slices, 8 rows at a time by way of the stage
+  // that was last worked on: to the outputs where the piece is the whole of a row's
+  // keys (`part` < 0), else to a place among the partials.
+  __device__ __forceinline__ void finish(const Cursor& cur, int part, uint8_t* warps, int stage) {
     const int head = cur.block * p.heads + head_in;
-    if (head >= p.Hkv) return;
     const int rows = min(L::kRows, p.queries * p.G - cur.tile * L::kRows);
-    const uint8_t* first = warps + head_in * L::kWarpBytes;  // slice 0 of the head
+    const auto sync = [&] {
+      if (p.slices > 1)
+        __syncthreads();
+      else
+        __syncwarp();
+    };
+    float z[2 * NT];
+    normalise(z);
+    uint8_t* mine = warps + (threadIdx.x >> 5) * L::kWarpBytes + stage * L::kStage;
+    const uint8_t* first = warps + head_in * L::kWarpBytes + stage * L::kStage;  // slice 0
     const int64_t stride = static_cast<int64_t>(p.heads) * L::kWarpBytes;
-    constexpr int kLanes = D / 4;
-    for (int x = slice * 32 + lane; x < rows * kLanes; x += p.slices * 32) {
-      const int row = x / kLanes, f = x % kLanes * 4;
-      float most = -INFINITY;
-      for (int s = 0; s < p.slices; ++s)
-        most = fmaxf(most, reinterpret_cast<const float*>(first + s * stride + L::kSumZ)[row]);
-      const float ref = most == -INFINITY ? 0.f : most;
-      float both = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < p.slices; ++s) {
-        const float z = reinterpret_cast<const float*>(first + s * stride + L::kSumZ)[row];
-        if (z == -INFINITY) continue;  // it has read nothing
-        const float w = exp2f(z - ref);
-        const float4 v = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(first + s * stride + L::kSum) + row * L::kSumRow + f);
-        both += w;
-        o.x = fmaf(w, v.x, o.x);
-        o.y = fmaf(w, v.y, o.y);
-        o.z = fmaf(w, v.z, o.z);
-        o.w = fmaf(w, v.w, o.w);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (8 * n >= rows) break;
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float* to = reinterpret_cast<float*>(mine) + (2 * t + x) * L::kSumRow + g;
+#pragma unroll
+        for (int f = 0; f < D / 16; ++f) {
+          to[16 * f] = acc[n][f][x];
+          to[16 * f + 8] = acc[n][f][2 + x];
+        }
+        if (g == 0) reinterpret_cast<float*>(mine + L::kSumZ)[2 * t + x] = z[2 * n + x];
       }
-      const float inv = both == 0.f ? 0.f : 1.f / both;
-      const float z = both == 0.f ? -INFINITY : ref + log2f(both);
-      o.x *= inv;
-      o.y *= inv;
-      o.z *= inv;
-      o.w *= inv;
-      if (part < 0) {
-        const int r = cur.tile * L::kRows + row, i = p.by_G(r), h = head * p.G + r - i * p.G;
-        const int64_t token = static_cast<int64_t>(cur.b) * p.queries + i;
-        *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
-            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-        if (f == 0)
-          p.lse[(static_cast<int64_t>(cur.b) * p.Hq + h) * p.queries + i] = z * 0.6931471805599453f;
-      } else {
-        const int64_t at = (static_cast<int64_t>(part) * p.heads + head_in) * L::kRows + row;
-        *reinterpret_cast<float4*>(p.part_o + at * D + f) = o;
-        if (f == 0) p.part_z[at] = z;
+      sync();
+      constexpr int kLanes = D / 4;
+      for (int y = slice * 32 + lane; y < 8 * kLanes; y += p.slices * 32) {
+        const int row = y / kLanes, f = y % kLanes * 4;
+        if (head >= p.Hkv || 8 * n + row >= rows) continue;
+        float most = -INFINITY;
+        for (int s = 0; s < p.slices; ++s)
+          most = fmaxf(most, reinterpret_cast<const float*>(first + s * stride + L::kSumZ)[row]);
+        const float ref = most == -INFINITY ? 0.f : most;
+        float both = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < p.slices; ++s) {
+          const float zs = reinterpret_cast<const float*>(first + s * stride + L::kSumZ)[row];
+          if (zs == -INFINITY) continue;  // it has read nothing
+          const float w = exp2f(zs - ref);
+          const float4 v = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(first + s * stride) + row * L::kSumRow + f);
+          both += w;
+          o.x = fmaf(w, v.x, o.x);
+          o.y = fmaf(w, v.y, o.y);
+          o.z = fmaf(w, v.z, o.z);
+          o.w = fmaf(w, v.w, o.w);
+        }
+        const float inv = both == 0.f ? 0.f : 1.f / both;
+        const float lse = both == 0.f ? -INFINITY : ref + log2f(both);
+        o.x *= inv;
+        o.y *= inv;
+        o.z *= inv;
+        o.w *= inv;
+        if (part < 0) {
+          const int q_row = cur.tile * L::kRows + 8 * n + row, i = p.by_G(q_row);
+          const int h = head * p.G + q_row - i * p.G;
+          const int64_t token = static_cast<int64_t>(cur.b) * p.queries + i;
+          *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
+              make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+          if (f == 0)
+            p.lse[(static_cast<int64_t>(cur.b) * p.Hq + h) * p.queries + i] =
+                lse * 0.6931471805599453f;
+        } else {
+          const int64_t at =
+              (static_cast<int64_t>(part) * p.heads + head_in) * L::kRows + 8 * n + row;
+          *reinterpret_cast<float4*>(p.part_o + at * D + f) = o;
+          if (f == 0) p.part_z[at] = lse;
+        }
       }
+      sync();
     }
   }
 };
 
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(most_warps(NT) * 32, 1)
     paged_rows_kernel(const __grid_constant__ PagedParams p) {
-  using L = Rows<D, kHalf>;
+  using L = Rows<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5;
-  Cursor ahead{};
-  const Share share = find_share(p, L::kRows, reinterpret_cast<uint64_t*>(smem), ahead);
-  if (share.begin >= share.end) return;
   uint8_t* warps = smem + L::kRoom;
-  Kernel<D, kHalf> k(p, warps + warp * L::kWarpBytes);
+  Kernel<D, NT> k(p, warps + (threadIdx.x >> 5) * L::kWarpBytes);
+  Cursor ahead{};
+  const Share share = find_share(p, L::kRows, reinterpret_cast<uint64_t*>(smem), k.slice, ahead);
+  if (share.begin >= share.end) return;
   Cursor cur = ahead;
   const uint32_t steps = static_cast<uint32_t>(share.end - share.begin);
   uint32_t pending = 0;
-  uint32_t issued = 0;
   // the first steps' tables are looked up together: one wait for all
   {
     Ahead a[kStages - 1];
@@ -865,17 +934,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (i < static_cast<int>(steps)) {
         k.issue(a[i], i, pending);
         k.store_pending(i, pending);
-        ++issued;
       } else {
         copies_commit();
       }
     }
   }
+  uint32_t issued = min(steps, static_cast<uint32_t>(kStages - 1));
   Ahead next{-1, 0, 0};
   if (issued < steps) next = k.look(ahead);
-  int pending_stage = -1;
+  int stage = 0, into = kStages - 1;  // of step i, and of the step to be issued
+  bool waits = false;                 // a pending scale word, for the stage before `into`
   bool fresh = true;
   int in_sum = 0;
+  // the list's place of the item's first step
+  uint64_t item = share.begin - (cur.r.n - 1 - (cur.left + (cur.front ? cur.r.n - cur.r.n_first : 0)));
   for (uint32_t i = 0; i < steps; ++i) {
     if (fresh) {
       k.begin(cur);
@@ -883,49 +955,47 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       in_sum = 0;
     }
     copies_wait<kStages - 2>();
-    if (pending_stage >= 0) k.store_pending(pending_stage, pending);
-    pending_stage = -1;
+    if (waits) k.store_pending(into == 0 ? kStages - 1 : into - 1, pending);
+    waits = false;
     __syncwarp();
     if (issued < steps) {
-      pending_stage = issued % kStages;
-      k.issue(next, pending_stage, pending);
+      k.issue(next, into, pending);
+      waits = true;
       if (++issued < steps) next = k.look(ahead);
     } else {
       copies_commit();
     }
-    k.step(cur, i % kStages);
-    const bool ends = cur.step + 1 == cur.r.n || i + 1 == steps;
-    if (++in_sum == kFlush || ends) {
-      k.store_sum();
-      in_sum = 0;
-    }
+    k.step(cur, stage);
+    const bool ends = cur.last() || i + 1 == steps;
     if (ends) {
-      // the item's first and last step in the list, and the CTAs that these are in
-      const uint64_t first = share.begin + i - cur.step;
-      const uint32_t from = static_cast<uint32_t>(first / share.per);
-      const uint32_t pieces = static_cast<uint32_t>((first + cur.r.n - 1) / share.per) - from + 1;
+      // the CTAs that the item's first and last step are in
+      const uint32_t from = static_cast<uint32_t>(item / share.per);
+      const uint32_t pieces = static_cast<uint32_t>((item + cur.r.n - 1) / share.per) - from + 1;
       const bool starts = from == blockIdx.x;
       if (starts && threadIdx.x == 0)
         p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
             make_int2(static_cast<int>(from), static_cast<int>(pieces));
       // a CTA leaves at most two partials: where an item ends or goes through (0)
       // and where one begins (1)
-      const int part = pieces == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-      if (p.slices > 1) __syncthreads();
-      k.finish(cur, part, warps);
-      if (p.slices > 1) __syncthreads();
-      else __syncwarp();
+      k.finish(cur, pieces == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0), warps,
+               stage);
       fresh = true;
+      item += cur.r.n;
+    } else if (++in_sum == kFlush) {
+      k.put_aside();
+      in_sum = 0;
     }
-    cur.next(p, L::kRows);
+    cur.next(p, L::kRows, k.slice);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    into = into + 1 == kStages ? 0 : into + 1;
   }
   copies_wait<0>();
 }
 
 // Joins the partials of a row tile that was cut; a CTA per head of it.
-template <int D, bool kHalf>
+template <int D, int NT>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int kRows = Rows<D, kHalf>::kRows, kLanes = D / 4;
+  constexpr int kRows = Rows<D, NT>::kRows, kLanes = D / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int item = blockIdx.x, head_in = blockIdx.y;
   const int2 piece = p.pieces[item];
@@ -978,9 +1048,13 @@ struct Cut {
 
 Cut cut_of(const csbp_paged_problem& p, const csbp_kv_cache& c) {
   Cut r{};
+  const int64_t rows = static_cast<int64_t>(p.queries) * (p.Hq / c.Hkv);
+  r.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  r.row_tiles = static_cast<int>((rows + r.tile_rows - 1) / r.tile_rows);
+  const int most = most_warps(r.tile_rows / 8);
   double best = 0;
-  for (int h = 1; h <= std::min(kMaxWarps, c.Hkv); ++h) {
-    const int blocks = (c.Hkv + h - 1) / h, s = kMaxWarps / h;
+  for (int h = 1; h <= std::min(most, c.Hkv); ++h) {
+    const int blocks = (c.Hkv + h - 1) / h, s = most / h;
     const double busy = static_cast<double>(h) * s * c.Hkv / (static_cast<double>(blocks) * h);
     if (busy >= best) {
       best = busy;
@@ -989,9 +1063,6 @@ Cut cut_of(const csbp_paged_problem& p, const csbp_kv_cache& c) {
       r.head_blocks = blocks;
     }
   }
-  const int64_t rows = static_cast<int64_t>(p.queries) * (p.Hq / c.Hkv);
-  r.tile_rows = rows <= 8 ? 8 : 16;
-  r.row_tiles = static_cast<int>((rows + r.tile_rows - 1) / r.tile_rows);
   r.items = static_cast<int64_t>(p.batch) * r.row_tiles * r.head_blocks;
   return r;
 }
@@ -1024,33 +1095,37 @@ bool device_sms(int& sms) {
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Places {
-  size_t part_z, pieces, bytes;
+  size_t part_z, aside_o, aside_z, pieces, bytes;
 };
 Places places(const Cut& cut, int d, int sms) {
   const size_t rows = static_cast<size_t>(2) * sms * cut.heads * cut.tile_rows;
   Places r;
   r.part_z = kStatusBytes + round256(rows * d * 4);
-  r.pieces = r.part_z + round256(rows * 4);
+  const size_t sums = static_cast<size_t>(sms) * cut.heads * cut.slices * cut.tile_rows;
+  r.aside_o = r.part_z + round256(rows * 4);
+  r.aside_z = r.aside_o + round256(sums * d * 4);
+  r.pieces = r.aside_z + round256(sums * 4);
   r.bytes = r.pieces + round256(static_cast<size_t>(cut.items) * sizeof(int2));
   return r;
 }
 
-template <int D, bool kHalf>
+template <int D, int NT>
 cudaError_t launch(const PagedParams& p, const Cut& cut, int sms, cudaStream_t stream) {
-  using L = Rows<D, kHalf>;
+  using L = Rows<D, NT>;
   static PerDeviceOnce configured;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!configured.run(dev, [&](int) {
-        e = cudaFuncSetAttribute(paged_rows_kernel<D, kHalf>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kMaxWarps));
+        e = cudaFuncSetAttribute(paged_rows_kernel<D, NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 L::smem(most_warps(NT)));
         return e == cudaSuccess;
       }))
     return e != cudaSuccess ? e : cudaErrorInvalidDevice;
   const int warps = cut.heads * cut.slices;
   const int timed = timer_begin(13, stream);
-  paged_rows_kernel<D, kHalf><<<sms, warps * 32, L::smem(warps), stream>>>(p);
+  paged_rows_kernel<D, NT><<<sms, warps * 32, L::smem(warps), stream>>>(p);
   e = cudaGetLastError();
   timer_end(timed, stream);
   if (e != cudaSuccess) return e;
@@ -1064,7 +1139,7 @@ cudaError_t launch(const PagedParams& p, const Cut& cut, int sms, cudaStream_t s
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   const int joined = timer_begin(14, stream);
-  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHalf>, p);
+  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT>, p);
   timer_end(joined, stream);
   return e;
 }
@@ -1146,11 +1221,17 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + kStatusBytes);
   a.part_z = reinterpret_cast<float*>(ws + at.part_z);
+  a.aside_o = reinterpret_cast<float*>(ws + at.aside_o);
+  a.aside_z = reinterpret_cast<float*>(ws + at.aside_z);
   a.pieces = reinterpret_cast<int2*>(ws + at.pieces);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool half = cut.tile_rows == 8;
-  const cudaError_t e = cache->d == 128
-                            ? (half ? launch<128, true>(a, cut, sms, s) : launch<128, false>(a, cut, sms, s))
-                            : (half ? launch<64, true>(a, cut, sms, s) : launch<64, false>(a, cut, sms, s));
+  const auto run = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return cut.tile_rows == 8    ? launch<D, 1>(a, cut, sms, s)
+           : cut.tile_rows == 16 ? launch<D, 2>(a, cut, sms, s)
+                                 : launch<D, 4>(a, cut, sms, s);
+  };
+  const cudaError_t e = cache->d == 128 ? run(std::integral_constant<int, 128>())
+                                        : run(std::integral_constant<int, 64>());
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }
