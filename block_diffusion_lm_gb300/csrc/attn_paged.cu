@@ -5,7 +5,7 @@
 // Rows and keys.  The query rows of one KV head of a sequence are (token, head of
 // the group), flattened; a row tile is 8, 16 or 32 of them.  A row tile reads the
 // keys that any of its rows reads, sinks first, then the window (or all), in steps
-// of 16 keys per warp.  A warp takes one KV head and every S-th step of 16 keys; the
+// of 32 keys per warp.  A warp takes one KV head and every S-th step of 32 keys; the
 // CTA's warps are H heads x S such slices, so that the scale bytes of a token's
 // heads, which share a 32-byte sector, are read by one CTA at one time.
 //
@@ -31,7 +31,7 @@
 // keys of a feature; which of the 16 keys is which row of the first product is
 // chosen so that P^T needs one transposition of 8 x 8 for the second.
 // Maxima, sums, O and everything that is scaled are fp32.  The tensor cores'
-// accumulator drops what is below its last place at every step of 16 keys: after
+// accumulator drops what is below its last place at every MMA of 16 keys: after
 // 2,048 of them (2^-13) O is put aside in the workspace and a new sum begun.
 //
 // Keys that a row does not read.  Steps at the edge of a row's range are masked;
@@ -57,10 +57,10 @@ namespace csbp {
 namespace {
 
 constexpr size_t kStatusBytes = 256;
-constexpr int kMostWarps = 16;
-constexpr int kStages = 3;
-constexpr int kKeys = 16;     // of a warp's step
-constexpr int kFlush = 2048;  // steps that one accumulator takes in
+constexpr int kMostWarps = 12;
+constexpr int kStages = 2;
+constexpr int kKeys = 32;     // of a warp's step, two MMAs
+constexpr int kFlush = 1024;  // steps that one accumulator takes in
 constexpr float kShift = 14.f;  // p is held as p 2^14; a row's maximum may lag by 2^1
 
 struct PagedParams {
@@ -296,7 +296,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows,
 }
 
 // Warps of a CTA, by its registers: 32 sums and 16 words of Q per lane and 8 rows.
-__host__ __device__ constexpr int most_warps(int tiles) { return tiles == 1 ? 16 : tiles == 2 ? 12 : 8; }
+__host__ __device__ constexpr int most_warps(int tiles) { return tiles == 1 ? 12 : 8; }
 
 // ------------------------------------------------------------ shared memory
 template <int D, int NT>
@@ -311,14 +311,15 @@ struct Rows {
   static constexpr int kThere = kWords + 2 * kKeys * 4;
   static constexpr int kSumRow = D + 4;
   static constexpr int kSumZ = 8 * kSumRow * 4;
-  static constexpr int kStage = (kThere + 16 > kSumZ + 32 ? kThere + 16 : kSumZ + 32) / 128 * 128 + 128;
+  static constexpr int kStage = kThere + 128;
+  static_assert(kSumZ + 32 <= kStage, "a worked-on stage holds 8 rows");
   // the step's scales: fp32 of K [key][group], f16 of V [group][key]
   static constexpr int kScales = kStages * kStage;
   static constexpr int kWarpBytes = kScales + kKeys * kGroups * 6;
   static constexpr int kRoom = 256;  // find_share, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
 
-  // Place of a row's 16-byte chunks: chunk c lies at c ^ this.  The rows that an
+  // Place of a key's 16-byte chunks: chunk c lies at c ^ this.  The rows that an
   // ldmatrix takes at once (K: 0, 1, 4, 5, .. or 2, 3, 6, 7, ..; V: 0 .. 7) lie in
   // different banks.
   static __device__ __forceinline__ int k_swizzle(int r) {
@@ -332,16 +333,28 @@ static_assert(Rows<128, 1>::smem(most_warps(1)) <= 232448 &&
 static_assert(Rows<128, 1>::kWarpBytes % 128 == 0 && Rows<64, 1>::kWarpBytes % 64 == 0,
               "swizzled rows");
 
-// Key of row m of the first product: rows 2t, 2t + 1 and 2t + 8, 2t + 9 are the keys
-// 4t .. 4t + 3 that lane quarter t has of V.
+// Key (of 16) of row m of the first product: rows 2t, 2t + 1 and 2t + 8, 2t + 9 are
+// the keys 4t .. 4t + 3 that lane quarter t has of V.
 __device__ __forceinline__ int key_of(int m) { return (m & 6) << 1 | (m & 1) | (m >> 3) << 1; }
 // and the row of a key
 __device__ __forceinline__ int row_of_key(int r) { return (r >> 1 & 6) | (r & 1) | (r & 2) << 2; }
 
-// Byte-wise larger of two words.
-__device__ __forceinline__ uint32_t max_u8x4(uint32_t a, uint32_t b) { return __vmaxu4(a, b); }
+// Sign bits of the bytes of a that are not below those of b.
+__device__ __forceinline__ uint32_t at_least_u8x4(uint32_t a, uint32_t b) {
+  const uint32_t t = (a | 0x80808080u) - (b & 0x7f7f7f7fu);
+  return ((a & ~b) | (~(a ^ b) & t)) & 0x80808080u;
+}
 __device__ __forceinline__ bool any_byte_255(uint32_t w) {
   return ((~w - 0x01010101u) & w & 0x80808080u) != 0;
+}
+// Two scale bytes as fp32: 2^(byte - 127), 255 as NaN.
+__device__ __forceinline__ void two_scales(uint32_t w, float& lo, float& hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n}"
+      : "=r"(r)
+      : "r"(w));
+  lo = __uint_as_float(r << 16);
+  hi = __uint_as_float(r & 0xffff0000u);
 }
 // Bytes of E4M3 NaN codes in a word, as 0xff.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
@@ -349,7 +362,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return (m >> 7) * 0xffu;
 }
 
-// What a lane looked up for key row (lane & 15) of a step ahead.
+// What a lane looked up for its key of a step ahead.
 struct Ahead {
   int page, place, block;
 };
@@ -379,7 +392,7 @@ struct Kernel {
         mem(smem_u32(smem)) {}
 
   __device__ __forceinline__ Ahead look(Cursor& cur) const {
-    const int j = cur.j + (lane & 15);
+    const int j = cur.j + lane;
     Ahead a;
     const int entry = p.by_page(j);
     a.place = j - entry * p.page_size;
@@ -393,7 +406,7 @@ struct Kernel {
 
   // Starts the copies of a step into a stage of the ring.  A key that is not there
   // is a copy of the cache's first row; its score is masked.
-  __device__ __forceinline__ void issue(const Ahead& a, int stage, uint32_t& pending) const {
+  __device__ __forceinline__ void issue(const Ahead& a, int stage, uint2& pending) const {
     const uint32_t at = mem + stage * L::kStage;
     const int head = a.block * p.heads + head_in;
     const bool there = static_cast<uint32_t>(a.page) < static_cast<uint32_t>(p.pages) && head < p.Hkv;
@@ -409,23 +422,28 @@ struct Kernel {
       copy16(at + r * D + (chunk ^ L::k_swizzle(r)) * 16, k + from);
       copy16(at + L::kCodes + r * D + (chunk ^ L::v_swizzle(r)) * 16, v + from);
     }
-    // scale bytes of K (lanes 0 .. 15) and V
-    const uint8_t* scales = lane < 16 ? p.k_scale : p.v_scale;
+    // scale bytes
     const uint64_t place = static_cast<uint64_t>(row) * kG;
     if (p.wide_scales) {
-      copy4(at + L::kWords + lane * 4, scales + (place & ~uint64_t(3)));
+      copy4(at + L::kWords + lane * 4, p.k_scale + (place & ~uint64_t(3)));
+      copy4(at + L::kWords + (kKeys + lane) * 4, p.v_scale + (place & ~uint64_t(3)));
     } else {
-      uint32_t w = 0;
+      uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < kG; ++e) w |= static_cast<uint32_t>(__ldg(scales + place + e)) << 8 * e;
-      pending = w;  // stored when the next step is issued, so that nobody waits here
+      for (int e = 0; e < kG; ++e) {
+        w[0] |= static_cast<uint32_t>(__ldg(p.k_scale + place + e)) << 8 * e;
+        w[1] |= static_cast<uint32_t>(__ldg(p.v_scale + place + e)) << 8 * e;
+      }
+      pending = make_uint2(w[0], w[1]);  // stored a step later, so that nobody waits here
     }
     const uint32_t is = __ballot_sync(0xffffffffu, there);
     if (lane == 0) sts32(at + L::kThere, is);
     copies_commit();
   }
-  __device__ __forceinline__ void store_pending(int stage, uint32_t pending) const {
-    if (!p.wide_scales) sts32(mem + stage * L::kStage + L::kWords + lane * 4, pending);
+  __device__ __forceinline__ void store_pending(int stage, uint2 pending) const {
+    if (p.wide_scales) return;
+    sts32(mem + stage * L::kStage + L::kWords + lane * 4, pending.x);
+    sts32(mem + stage * L::kStage + L::kWords + (kKeys + lane) * 4, pending.y);
   }
 
   __device__ __forceinline__ void clear() {
@@ -467,7 +485,8 @@ struct Kernel {
       // the largest element becomes 2^7 .. 2^8
       const int ex = max(static_cast<int>(most >> 7) - 127, -110);
       const float scale = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-      const float back = p.scale_log2 * ldexpf(1.f, ex - 7);
+      // (not 0: a masked score times it has to stay -inf)
+      const float back = fmaxf(p.scale_log2 * ldexpf(1.f, ex - 7), 1e-37f);
       row_scale[2 * n] = __shfl_sync(0xffffffffu, back, 8 * t);
       row_scale[2 * n + 1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
@@ -495,11 +514,16 @@ struct Kernel {
     return j < row_hi[x] && (j >= row_lo[x] || j < p.sinks);
   }
 
-  // E grows: what was summed under the old one is scaled.
-  __device__ __forceinline__ void raise_top(uint32_t w) {
+  // Scales that are above E, far below it or NaN: E becomes the largest so far, and
+  // what was summed under the old one is scaled.  Whether P's scales do not fit f16.
+  __device__ __forceinline__ bool odd_scales(uint32_t word, bool is_there, uint32_t& delta) {
+    const bool nan = is_there && any_byte_255(word);
+    uint32_t now = is_there ? word : 0;
+    if (nan) now &= ~__vcmpeq4(word, 0xffffffffu);
+    const uint32_t mine = now;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w = max_u8x4(w, __shfl_xor_sync(0xffffffffu, w, o));
-    const uint32_t now = max_u8x4(top, w);
+    for (int o = 16; o > 0; o >>= 1) now = __vmaxu4(now, __shfl_xor_sync(0xffffffffu, now, o));
+    now = __vmaxu4(now, top);
 #pragma unroll
     for (int e = 0; e < kG; ++e) {
       const int by = static_cast<int>((now >> 8 * e & 255) - (top >> 8 * e & 255));
@@ -512,63 +536,64 @@ struct Kernel {
           for (int c = 0; c < 4; ++c) acc[n][2 * e + k][c] *= f;
     }
     top = now;
+    delta = is_there ? top - mine : 0;  // byte by byte, nothing is borrowed
+    return __any_sync(0xffffffffu, nan || !fits(delta));
+  }
+  // f16 holds 2^-delta to delta = 14.
+  static __device__ __forceinline__ bool fits(uint32_t delta) {
+    return ((delta + (kG == 4 ? 0x71717171u : 0x7171u) | delta) & 0x80808080u) == 0;
   }
 
   __device__ __forceinline__ void step(const Cursor& cur, int stage) {
     const uint32_t at = mem + stage * L::kStage;
     const uint32_t scales = mem + L::kScales, v_scales = scales + kKeys * kG * 4;
-    // ------- the step's scales
-    uint32_t word = lds32(at + L::kWords + lane * 4);
-    const uint32_t there = lds32(at + L::kThere) & 0xffffu;
+    // ------- the step's scales, a key per lane
+    uint32_t k_word = lds32(at + L::kWords + lane * 4);
+    uint32_t v_word = lds32(at + L::kWords + (kKeys + lane) * 4);
+    const uint32_t there = lds32(at + L::kThere);
+    const bool upper = D == 64 && p.wide_scales && ((cur.block * p.heads + head_in) & 1);
     if (D == 64 && p.wide_scales) {  // its half of the word
-      const int head = cur.block * p.heads + head_in;
-      word = head & 1 ? word >> 16 : word & 0xffffu;
+      k_word = upper ? k_word >> 16 : k_word & 0xffffu;
+      v_word = upper ? v_word >> 16 : v_word & 0xffffu;
     }
-    const bool is_there = there >> (lane & 15) & 1;
-    const bool odd_scale = any_byte_255(word);
-    uint32_t v_word = lane >= 16 && is_there ? word : 0;
-    if (odd_scale) v_word &= ~__vcmpeq4(word, 0xffffffffu);
-    if (__any_sync(0xffffffffu, max_u8x4(top, v_word) != top)) raise_top(v_word);
-    // byte by byte, nothing is borrowed
-    const uint32_t delta = lane >= 16 && is_there ? top - v_word : 0;
-    // f16 holds 2^-delta to delta = 14; more, and NaN, goes another way
-    const bool special = __any_sync(
-        0xffffffffu, (delta + 0x71717171u * (kG == 4) + 0x7171u * (kG == 2) | delta) & 0x80808080u ||
-                         (lane >= 16 && is_there && odd_scale));
-    __syncwarp();  // (the scales of the step before have been read)
-    const int key = lane & 15;
-    if (lane < 16) {
-      float f[kG];
-#pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        const uint32_t b = word >> 8 * e & 255;
-        f[e] = __uint_as_float(b == 255 ? 0x7fffffffu : max(b << 23, 0x00400000u));
-      }
-      const uint32_t to = scales + row_of_key(key) * kG * 4;
-      if constexpr (kG == 4)
+    const bool is_there = there >> lane & 1;
+    uint32_t delta = is_there ? top - v_word : 0;
+    bool special = is_there && (at_least_u8x4(top, v_word) != 0x80808080u || any_byte_255(v_word) ||
+                                !fits(delta));
+    special = __any_sync(0xffffffffu, special);
+    if (special) special = odd_scales(v_word, is_there, delta);
+    {
+      float f[4];
+      two_scales(k_word, f[0], f[1]);
+      const uint32_t to = scales + ((lane & 16) + row_of_key(lane & 15)) * kG * 4;
+      if constexpr (kG == 4) {
+        two_scales(k_word >> 16, f[2], f[3]);
         asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to), "f"(f[0]), "f"(f[1]),
                      "f"(f[2]), "f"(f[3])
                      : "memory");
-      else
+      } else {
         asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(f[0]), "f"(f[1]) : "memory");
-    } else {
-#pragma unroll
-      for (int e = 0; e < kG; ++e) {  // 2^-delta
-        const uint32_t h = 0x3c00u - ((delta >> 8 * e & 255) << 10);
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_scales + e * (2 * kKeys) + key * 2),
-                     "h"(static_cast<uint16_t>(h))
-                     : "memory");
       }
+      // 2^-delta in f16: only the upper byte, 4 (15 - delta)
+      const uint32_t h = 0x3c3c3c3cu - 4 * delta;
+#pragma unroll
+      for (int e = 0; e < kG; ++e)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_scales + e * (2 * kKeys) + lane * 2),
+                     "h"(static_cast<uint16_t>(__byte_perm(h, 0, 0x0004 | e << 4)))
+                     : "memory");
     }
     __syncwarp();
 
-    // ------- S^T = K Q^T, keys of rows g and g + 8
-    float s[NT][4];
-    {
+    // ------- S^T = K Q^T: of each 16 keys those of rows g and g + 8
+    float s[2][NT][4];
+    const int r_k = key_of(lane & 15);
+    const uint32_t k0 = at + r_k * D + (((lane >> 4) ^ L::k_swizzle(r_k)) << 4);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       float ks[2][kG];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint32_t from = scales + (8 * k + g) * kG * 4;
+        const uint32_t from = scales + (16 * u + 8 * k + g) * kG * 4;
         if constexpr (kG == 4)
           asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                        : "=f"(ks[k][0]), "=f"(ks[k][1]), "=f"(ks[k][2]), "=f"(ks[k][3])
@@ -580,12 +605,10 @@ struct Kernel {
                        : "r"(from)
                        : "memory");
       }
-      const int r = key_of(lane & 15);
-      const uint32_t k0 = at + r * D + (((lane >> 4) ^ L::k_swizzle(r)) << 4);
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
         uint32_t w[4];
-        load_rows(w, k0 ^ (e << 5));
+        load_rows(w, (k0 ^ (e << 5)) + 16 * u * D);
         uint32_t a[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -599,41 +622,42 @@ struct Kernel {
           mma(c, a[2], a[3], a[6], a[7], q[n][2 * e + 1][0], q[n][2 * e + 1][1]);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            s[n][k] = e == 0 ? c[k] * ks[k >> 1][0] : fmaf(c[k], ks[k >> 1][e], s[n][k]);
+            s[u][n][k] = e == 0 ? c[k] * ks[k >> 1][0] : fmaf(c[k], ks[k >> 1][e], s[u][n][k]);
         }
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][k] *= row_scale[2 * n + (k & 1)];
 
     // ------- mask
-    const bool inside = there == 0xffffu && cur.j + kKeys <= all_hi &&
+    const bool inside = there == 0xffffffffu && cur.j + kKeys <= all_hi &&
                         (cur.j >= all_lo || cur.j + kKeys <= p.sinks);
     if (!inside) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = key_of(8 * k + g);
+      for (int k = 0; k < 4; ++k) {
+        const int r = 16 * (k >> 1) + key_of(8 * (k & 1) + g);
         const bool here = there >> r & 1;
 #pragma unroll
         for (int x = 0; x < 2 * NT; ++x)
-          if (!here || !reads(x, cur.j + r)) s[x >> 1][2 * k + (x & 1)] = -INFINITY;
+          if (!here || !reads(x, cur.j + r)) s[k >> 1][x >> 1][2 * (k & 1) + (x & 1)] = -INFINITY;
       }
     }
 
-    // ------- softmax
+    // ------- softmax (scores before the row's scale, which is positive)
+    float most[2 * NT];
     bool grows = false;
 #pragma unroll
-    for (int x = 0; x < 2 * NT; ++x)
-      grows |= fmaxf(s[x >> 1][x & 1], s[x >> 1][2 + (x & 1)]) > m[x] + 1.f;
+    for (int x = 0; x < 2 * NT; ++x) {
+      const int n = x >> 1, k = x & 1;
+      most[x] = fmaxf(fmaxf(s[0][n][k], s[0][n][2 + k]), fmaxf(s[1][n][k], s[1][n][2 + k])) *
+                row_scale[x];
+      grows |= most[x] > m[x] + 1.f;
+    }
     if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
       for (int x = 0; x < 2 * NT; ++x) {
-        float most = fmaxf(s[x >> 1][x & 1], s[x >> 1][2 + (x & 1)]);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const float now = fmaxf(m[x], most), f = ex2_approx(m[x] - now);
+        for (int o = 4; o < 32; o <<= 1)
+          most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], o));
+        const float now = fmaxf(m[x], most[x]), f = ex2_approx(m[x] - now);
         m[x] = now;
         l[x] *= f;
 #pragma unroll
@@ -643,125 +667,137 @@ struct Kernel {
         }
       }
     }
-    float pr[NT][4];
+    float pr[2][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pr[n][k] = ex2_approx(s[n][k] - (m[2 * n + (k & 1)] - kShift));
+      for (int k = 0; k < 4; ++k) {
+        const int x = 2 * n + (k & 1);
 #pragma unroll
-    for (int x = 0; x < 2 * NT; ++x) l[x] += pr[x >> 1][x & 1] + pr[x >> 1][2 + (x & 1)];
-
-    // ------- P^T: row g, keys 4t .. 4t + 3, under V's scales of each group
-    uint32_t b[NT][kG][2];
-    if (!special) {
-      uint2 vs[kG];
-#pragma unroll
-      for (int e = 0; e < kG; ++e) vs[e] = lds64(v_scales + e * (2 * kKeys) + 8 * t);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t b0 = transpose8(pack_f16(pr[n][0], pr[n][1]));
-        const uint32_t b1 = transpose8(pack_f16(pr[n][2], pr[n][3]));
-#pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          b[n][e][0] = mul_f16x2(b0, vs[e].x);
-          b[n][e][1] = mul_f16x2(b1, vs[e].y);
-        }
-      }
-    } else {
-      // in fp32: scales far below the largest, or NaN (in the rows that read the key)
-      uint32_t w[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        w[k] = lds32(at + L::kWords + (16 + key_of(8 * k + g)) * 4);
-        if (D == 64 && p.wide_scales && ((cur.block * p.heads + head_in) & 1)) w[k] >>= 16;
+        for (int u = 0; u < 2; ++u)
+          pr[u][n][k] = ex2_approx(fmaf(s[u][n][k], row_scale[x], kShift - m[x]));
       }
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        float f[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int byte = static_cast<int>(w[k] >> 8 * e & 255);
-          const int by = static_cast<int>(top >> 8 * e & 255) - byte;
-          f[k] = byte == 255 ? NAN
-                 : by >= 0 && by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23)
-                                       : 0.f;
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = s[n][k] == -INFINITY ? 0.f : pr[n][k] * f[k >> 1];
-          b[n][e][0] = transpose8(pack_f16(x[0], x[1]));
-          b[n][e][1] = transpose8(pack_f16(x[2], x[3]));
-        }
-      }
+      for (int k = 0; k < 2; ++k)
+        l[2 * n + k] += (pr[0][n][k] + pr[0][n][2 + k]) + (pr[1][n][k] + pr[1][n][2 + k]);
     }
 
-    // ------- O^T += V^T P^T
-    const int r = lane & 15;
-    const uint32_t v0 = at + L::kCodes + r * D + (((lane >> 4) ^ L::v_swizzle(r)) << 4);
+    // ------- P^T: row g, keys 4t .. 4t + 3 of each 16, under V's scales of each group,
+    // and O^T += V^T P^T
+    const int r_v = lane & 15;
+    const uint32_t v0 = at + L::kCodes + r_v * D + (((lane >> 4) ^ L::v_swizzle(r_v)) << 4);
     bool bad = false;
     if (!inside) {
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        uint32_t w[4];
-        load_columns(w, v0 ^ (e << 5));
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) bad |= nan_codes(w[k]) != 0;
-      }
+        for (int e = 0; e < kG; ++e) {
+          uint32_t w[4];
+          load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) bad |= nan_codes(w[k]) != 0;
+        }
       bad = __any_sync(0xffffffffu, bad);
     }
-    if (!bad) {
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        uint32_t w[4];
-        load_columns(w, v0 ^ (e << 5));
-        uint32_t a[8];
+    for (int u = 0; u < 2; ++u) {
+      uint32_t b[NT][kG][2];
+      if (!special) {
+        uint2 vs[kG];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[k] = f16_low(w[k]);
-          a[4 + k] = f16_high(w[k]);
-        }
+        for (int e = 0; e < kG; ++e) vs[e] = lds64(v_scales + e * (2 * kKeys) + 32 * u + 8 * t);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma(acc[n][2 * e], a[0], a[1], a[4], a[5], b[n][e][0], b[n][e][1]);
-          mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], b[n][e][0], b[n][e][1]);
-        }
-      }
-    } else {
-      // NaN codes as 0 in the product, then NaN wherever a row reads one of them
-      uint32_t sees[NT][2];
+          const uint32_t b0 = transpose8(pack_f16(pr[u][n][0], pr[u][n][1]));
+          const uint32_t b1 = transpose8(pack_f16(pr[u][n][2], pr[u][n][3]));
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int e = 0; e < kG; ++e) {
+            b[n][e][0] = mul_f16x2(b0, vs[e].x);
+            b[n][e][1] = mul_f16x2(b1, vs[e].y);
+          }
+        }
+      } else {
+        // in fp32: scales far below the largest, or NaN (in the rows that read the key)
+        uint32_t w[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          sees[n][k] = transpose8(
-              pack_f16(s[n][2 * k] != -INFINITY, s[n][2 * k + 1] != -INFINITY));
+          w[k] = lds32(at + L::kWords + (kKeys + 16 * u + key_of(8 * k + g)) * 4) >>
+                 (upper ? 16 : 0);
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        uint32_t w[4], is[4];
-        load_columns(w, v0 ^ (e << 5));
+        for (int e = 0; e < kG; ++e) {
+          float f[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          is[k] = nan_codes(w[k]);
-          w[k] &= ~is[k];
-          is[k] &= 0x38383838u;  // 1
-        }
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
+          for (int k = 0; k < 2; ++k) {
+            const int byte = static_cast<int>(w[k] >> 8 * e & 255);
+            const int by = static_cast<int>(top >> 8 * e & 255) - byte;
+            f[k] = byte == 255 ? NAN
+                   : by >= 0 && by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23)
+                                         : 0.f;
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma(acc[n][2 * e + f], f16_low(w[2 * f]), f16_low(w[2 * f + 1]), f16_high(w[2 * f]),
-                f16_high(w[2 * f + 1]), b[n][e][0], b[n][e][1]);
-            mma(c, f16_low(is[2 * f]), f16_low(is[2 * f + 1]), f16_high(is[2 * f]),
-                f16_high(is[2 * f + 1]), sees[n][0], sees[n][1]);
+            float x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (c[k] > 0.f) acc[n][2 * e + f][k] = NAN;
+              x[k] = s[u][n][k] == -INFINITY ? 0.f : pr[u][n][k] * f[k >> 1];
+            b[n][e][0] = transpose8(pack_f16(x[0], x[1]));
+            b[n][e][1] = transpose8(pack_f16(x[2], x[3]));
           }
+        }
+      }
+      if (!bad) {
+#pragma unroll
+        for (int e = 0; e < kG; ++e) {
+          uint32_t w[4];
+          load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
+          uint32_t a[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a[k] = f16_low(w[k]);
+            a[4 + k] = f16_high(w[k]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma(acc[n][2 * e], a[0], a[1], a[4], a[5], b[n][e][0], b[n][e][1]);
+            mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], b[n][e][0], b[n][e][1]);
+          }
+        }
+      } else {
+        // NaN codes as 0 in the product, then NaN wherever a row reads one of them
+        uint32_t sees[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            sees[n][k] = transpose8(
+                pack_f16(s[u][n][2 * k] != -INFINITY, s[u][n][2 * k + 1] != -INFINITY));
+#pragma unroll
+        for (int e = 0; e < kG; ++e) {
+          uint32_t w[4], is[4];
+          load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            is[k] = nan_codes(w[k]);
+            w[k] &= ~is[k];
+            is[k] &= 0x38383838u;  // 1
+          }
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              mma(acc[n][2 * e + f], f16_low(w[2 * f]), f16_low(w[2 * f + 1]), f16_high(w[2 * f]),
+                  f16_high(w[2 * f + 1]), b[n][e][0], b[n][e][1]);
+              mma(c, f16_low(is[2 * f]), f16_low(is[2 * f + 1]), f16_high(is[2 * f]),
+                  f16_high(is[2 * f + 1]), sees[n][0], sees[n][1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (c[k] > 0.f) acc[n][2 * e + f][k] = NAN;
+            }
+        }
       }
     }
+    __syncwarp();  // the stage and the scales have been read
   }
 
   // What the registers hold as a normalised O and its LSE, joined with what was put
@@ -920,17 +956,17 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   if (share.begin >= share.end) return;
   Cursor cur = ahead;
   const uint32_t steps = static_cast<uint32_t>(share.end - share.begin);
-  uint32_t pending = 0;
+  uint2 pending = make_uint2(0, 0);
   // the first steps' tables are looked up together: one wait for all
   {
-    Ahead a[kStages - 1];
+    Ahead a[kStages];
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       a[i] = Ahead{-1, 0, 0};
       if (i < static_cast<int>(steps)) a[i] = k.look(ahead);
     }
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       if (i < static_cast<int>(steps)) {
         k.issue(a[i], i, pending);
         k.store_pending(i, pending);
@@ -939,32 +975,21 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
       }
     }
   }
-  uint32_t issued = min(steps, static_cast<uint32_t>(kStages - 1));
+  uint32_t issued = min(steps, static_cast<uint32_t>(kStages));
   Ahead next{-1, 0, 0};
   if (issued < steps) next = k.look(ahead);
-  int stage = 0, into = kStages - 1;  // of step i, and of the step to be issued
-  bool waits = false;                 // a pending scale word, for the stage before `into`
   bool fresh = true;
-  int in_sum = 0;
+  int in_sum = 0, stage = 0;
   // the list's place of the item's first step
   uint64_t item = share.begin - (cur.r.n - 1 - (cur.left + (cur.front ? cur.r.n - cur.r.n_first : 0)));
-  for (uint32_t i = 0; i < steps; ++i) {
+  for (uint32_t i = 0; i < steps; ++i, stage ^= 1) {
     if (fresh) {
       k.begin(cur);
       fresh = false;
       in_sum = 0;
     }
-    copies_wait<kStages - 2>();
-    if (waits) k.store_pending(into == 0 ? kStages - 1 : into - 1, pending);
-    waits = false;
+    copies_wait<kStages - 1>();
     __syncwarp();
-    if (issued < steps) {
-      k.issue(next, into, pending);
-      waits = true;
-      if (++issued < steps) next = k.look(ahead);
-    } else {
-      copies_commit();
-    }
     k.step(cur, stage);
     const bool ends = cur.last() || i + 1 == steps;
     if (ends) {
@@ -985,9 +1010,15 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
       k.put_aside();
       in_sum = 0;
     }
+    // (the last issue's scale words; one is always a step old)
+    if (i > 0 && issued > kStages) k.store_pending(stage ^ 1, pending);
+    if (issued < steps) {
+      k.issue(next, stage, pending);
+      if (++issued < steps) next = k.look(ahead);
+    } else {
+      copies_commit();
+    }
     cur.next(p, L::kRows, k.slice);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    into = into + 1 == kStages ? 0 : into + 1;
   }
   copies_wait<0>();
 }
