@@ -3,7 +3,7 @@
 // they lie, once, in E4M3.
 //
 // Rows and keys.  The query rows of one KV head of a sequence are (token, head of
-// the group), flattened; a row tile is 8, 16 or 32 of them.  A row tile reads the
+// the group), flattened; a row tile is 8 or 16 of them.  A row tile reads the
 // keys that any of its rows reads, sinks first, then the window (or all), in steps
 // of 32 keys per warp.  A warp takes one KV head and every S-th step of 32 keys; the
 // CTA's warps are H heads x S such slices, so that the scale bytes of a token's
@@ -77,7 +77,7 @@ struct PagedParams {
   int32_t heads, slices, head_blocks;  // KV heads and slices of a CTA, CTAs' worth of heads
   int32_t row_tiles;
   int32_t wide_scales;  // scale bytes of a token are loaded in 4-byte words
-  Divisor by_page, by_G, by_row_tiles;
+  Divisor by_page, by_G, by_row_tiles, by_step;  // (a step: the CTA's keys)
   float* part_o;  // [2 x CTAs][heads][tile rows][d]
   float* part_z;  // [2 x CTAs][heads][tile rows]
   int2* pieces;   // per sequence, row tile and head block: first CTA, number of them
@@ -135,6 +135,11 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ float lg2_approx(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // 8 x 8 f16 numbers, row g in lanes 4g .. 4g + 3: transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t r;
@@ -183,74 +188,47 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile,
   r.lo = p.window ? max(t0 - p.window + 1, 0) : 0;
   r.lo = min(r.lo, r.hi);
   r.first = p.window ? min(p.sinks, r.lo) : 0;
-  const int per = kKeys * p.slices;
-  r.n_first = (r.first + per - 1) / per;
-  r.n = max(r.n_first + (r.hi - r.lo + per - 1) / per, 1);
+  const int more = kKeys * p.slices - 1;
+  r.n_first = p.by_step(r.first + more);
+  r.n = max(r.n_first + static_cast<int>(p.by_step(r.hi - r.lo + more)), 1);
   return r;
 }
 
-// A place in the list: entry (sequence, row tile), block of heads, and the step, as
-// the warp's keys from j on, of which those below `end` count; `left` steps follow
-// in this stretch (the sinks, or the rest).
+// A place in the list: entry (sequence, row tile), block of heads, step of it.
 struct Cursor {
-  int entry, block, b, tile;
-  int j, end, left;
-  bool front;
+  int entry, block, step, b;
   Range r;
-  __device__ __forceinline__ void seek(const PagedParams& p, int slice, int step) {
-    front = step < r.n_first;
-    const int k = front ? step : step - r.n_first;
-    j = (front ? 0 : r.lo) + (k * p.slices + slice) * kKeys;
-    end = front ? r.first : r.hi;
-    left = (front ? r.n_first : r.n - r.n_first) - 1 - k;
-  }
   __device__ __forceinline__ void load(const PagedParams& p, int tile_rows) {
     b = p.by_row_tiles(entry);
-    tile = entry - b * p.row_tiles;
-    if (b < p.batch) r = range_of(p, b, tile, tile_rows);
-  }
-  __device__ __forceinline__ bool last() const {
-    return left == 0 && (!front || r.n == r.n_first);
-  }
-  __device__ __forceinline__ void next(const PagedParams& p, int tile_rows, int slice) {
-    if (left > 0) {
-      --left;
-      j += p.slices * kKeys;
-      return;
-    }
-    int step = 0;
-    if (front && r.n > r.n_first) {
-      step = r.n_first;
-    } else if (++block == p.head_blocks) {
-      block = 0;
-      ++entry;
-      load(p, tile_rows);
-    }
-    seek(p, slice, step);
+    if (b < p.batch) r = range_of(p, b, entry - b * p.row_tiles, tile_rows);
   }
 };
 
 struct Share {
-  uint64_t total, per, begin, end;  // steps
+  uint64_t begin, end;  // steps of the list
+  uint32_t per;         // steps of a share, 2^31 at most
 };
 
 // Adds all steps up and finds the CTA's share, and the cursor of its begin.
-__device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows, uint64_t* room,
-                                            int slice, Cursor& cur) {
+template <int R>
+__device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room, Cursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int entries = p.batch * p.row_tiles;
-  Share s{0, 0, 0, 0};
-  // pass 0 finds the total; the begin is found in the same pass where one sweep
-  // takes in all entries
-  for (int pass = 0; pass < 2; ++pass) {
+  Share s{0, 0, 0};
+  uint64_t total = 0;
+  // the total, then the begin; both at once where one sweep takes in all entries
+  const bool one_sweep = entries <= static_cast<int>(blockDim.x);
+#pragma unroll 1
+  for (int pass = one_sweep ? 1 : 0; pass < 2; ++pass) {
     uint64_t before = 0;
+#pragma unroll 1
     for (int e0 = 0; e0 < entries; e0 += blockDim.x) {
       const int e = e0 + tid;
       uint64_t mine = 0;
-      int n = 0;
+      int n = 1;
       if (e < entries) {
         const int b = p.by_row_tiles(e);
-        n = range_of(p, b, e - b * p.row_tiles, tile_rows).n;
+        n = range_of(p, b, e - b * p.row_tiles, R).n;
         mine = static_cast<uint64_t>(n) * p.head_blocks;
       }
       uint64_t sum = mine;
@@ -263,16 +241,17 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows,
       if (lane == 31) room[warp] = sum;
       __syncthreads();
       uint64_t all = 0;
+#pragma unroll 1
       for (int w = 0; w < warps; ++w) {
         if (w < warp) sum += room[w];
         all += room[w];
       }
-      const bool one_sweep = entries <= static_cast<int>(blockDim.x);
-      if (pass == 0 && one_sweep) s.total = all;
-      if (pass == 1 || one_sweep) {
-        s.per = (s.total + gridDim.x - 1) / gridDim.x;
-        s.begin = min(s.per * blockIdx.x, s.total);
-        s.end = min(s.begin + s.per, s.total);
+      if (one_sweep) total = all;
+      if (pass == 1) {
+        const uint64_t per = (total + gridDim.x - 1) / gridDim.x;
+        s.per = static_cast<uint32_t>(min(per, uint64_t(1) << 31));
+        s.begin = min(per * blockIdx.x, total);
+        s.end = min(s.begin + per, total);
         const uint64_t from = before + sum - mine;
         if (s.begin >= from && s.begin < from + mine) {
           const uint32_t in = static_cast<uint32_t>(s.begin - from);
@@ -282,15 +261,14 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, int tile_rows,
       }
       before += all;
     }
-    if (pass == 0) s.total = before;
-    if (entries <= static_cast<int>(blockDim.x)) break;
+    total = before;
   }
   __syncthreads();
   if (s.begin < s.end) {
     cur.entry = static_cast<int>(room[kMostWarps]);
     cur.block = static_cast<int>(room[kMostWarps + 1] >> 32);
-    cur.load(p, tile_rows);
-    cur.seek(p, slice, static_cast<int>(room[kMostWarps + 1]));
+    cur.step = static_cast<int>(room[kMostWarps + 1]);
+    cur.load(p, R);
   }
   return s;
 }
@@ -303,19 +281,19 @@ template <int D, int NT>
 struct Rows {
   static constexpr int kRows = 8 * NT;  // of a tile
   static constexpr int kGroups = D / 32;
-  // a warp's ring stage: K codes, V codes, scale words (K, V), which keys are there;
+  // a warp's ring stage: K codes, V codes, scale words (K, V), the step's record;
   // a step that has been worked on leaves it to 8 rows of the result [row][D + 4]
   // and their LSE (log2)
   static constexpr int kCodes = kKeys * D;
   static constexpr int kWords = 2 * kCodes;
-  static constexpr int kThere = kWords + 2 * kKeys * 4;
+  static constexpr int kRecord = kWords + 2 * kKeys * 4;
   static constexpr int kSumRow = D + 4;
   static constexpr int kSumZ = 8 * kSumRow * 4;
-  static constexpr int kStage = kThere + 128;
+  static constexpr int kStage = kRecord + 128;
   static_assert(kSumZ + 32 <= kStage, "a worked-on stage holds 8 rows");
-  // the step's scales: fp32 of K [key][group], f16 of V [group][key]
+  // the step's scales: fp32 of K [key][group], f16 of V [group][key] in two factors
   static constexpr int kScales = kStages * kStage;
-  static constexpr int kWarpBytes = kScales + kKeys * kGroups * 6;
+  static constexpr int kWarpBytes = kScales + kKeys * kGroups * 8;
   static constexpr int kRoom = 256;  // find_share, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
 
@@ -362,9 +340,20 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return (m >> 7) * 0xffu;
 }
 
-// What a lane looked up for its key of a step ahead.
+// What a step is about, as the ring carries it.
+struct Record {
+  uint32_t there;    // which of its keys are there
+  int j;             // the first of them
+  int entry, block;  // (see Cursor)
+  int step, n;       // of the entry's n
+  int c;             // keys of the sequence
+  int pad;
+};
+
+// A step ahead: its record, and what the lane looked up for its key.
 struct Ahead {
-  int page, place, block;
+  Record r;
+  int page, place;
 };
 
 template <int D, int NT>
@@ -391,24 +380,33 @@ struct Kernel {
         head_in(static_cast<int>(threadIdx.x >> 5) % p.heads),
         mem(smem_u32(smem)) {}
 
-  __device__ __forceinline__ Ahead look(Cursor& cur) const {
-    const int j = cur.j + lane;
-    Ahead a;
-    const int entry = p.by_page(j);
+  __device__ __forceinline__ void look(Cursor& cur, Ahead& a) const {
+    const bool front = cur.step < cur.r.n_first;
+    a.r.j = (front ? 0 : cur.r.lo) +
+            ((front ? cur.step : cur.step - cur.r.n_first) * p.slices + slice) * kKeys;
+    const int j = a.r.j + lane, entry = p.by_page(j);
     a.place = j - entry * p.page_size;
-    a.block = cur.block;
     a.page = -1;
-    if (j < cur.end)
+    if (j < (front ? cur.r.first : cur.r.hi))
       a.page = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
-    cur.next(p, L::kRows, slice);
-    return a;
+    a.r.entry = cur.entry;
+    a.r.block = cur.block;
+    a.r.step = cur.step;
+    a.r.n = cur.r.n;
+    a.r.c = cur.r.c;
+    if (++cur.step < cur.r.n) return;
+    cur.step = 0;
+    if (++cur.block < p.head_blocks) return;
+    cur.block = 0;
+    ++cur.entry;
+    cur.load(p, L::kRows);
   }
 
   // Starts the copies of a step into a stage of the ring.  A key that is not there
   // is a copy of the cache's first row; its score is masked.
   __device__ __forceinline__ void issue(const Ahead& a, int stage, uint2& pending) const {
     const uint32_t at = mem + stage * L::kStage;
-    const int head = a.block * p.heads + head_in;
+    const int head = a.r.block * p.heads + head_in;
     const bool there = static_cast<uint32_t>(a.page) < static_cast<uint32_t>(p.pages) && head < p.Hkv;
     const uint32_t row =
         there ? static_cast<uint32_t>(a.page * p.page_size + a.place) * p.Hkv + head : 0;
@@ -437,8 +435,14 @@ struct Kernel {
       pending = make_uint2(w[0], w[1]);  // stored a step later, so that nobody waits here
     }
     const uint32_t is = __ballot_sync(0xffffffffu, there);
-    if (lane == 0) sts32(at + L::kThere, is);
-    copies_commit();
+    if (lane == 0) {
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kRecord), "r"(is),
+                   "r"(a.r.j), "r"(a.r.entry), "r"(a.r.block)
+                   : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kRecord + 16),
+                   "r"(a.r.step), "r"(a.r.n), "r"(a.r.c), "r"(0)
+                   : "memory");
+    }
   }
   __device__ __forceinline__ void store_pending(int stage, uint2 pending) const {
     if (p.wide_scales) return;
@@ -463,14 +467,15 @@ struct Kernel {
   }
 
   // Rows of a tile: queries to registers, and what each row reads.
-  __device__ __forceinline__ void begin(const Cursor& cur) {
+  __device__ __forceinline__ void begin(const Record& cur) {
     const int head = min(cur.block * p.heads + head_in, p.Hkv - 1);
-    const int rows = p.queries * p.G, row0 = cur.tile * L::kRows;
+    const int b = p.by_row_tiles(cur.entry);
+    const int rows = p.queries * p.G, row0 = (cur.entry - b * p.row_tiles) * L::kRows;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = min(row0 + 8 * n + g, rows - 1);
       const int i = p.by_G(r), gi = r - i * p.G;
-      const __nv_bfloat16* src = p.q + cur.b * p.q_bat + i * p.q_tok +
+      const __nv_bfloat16* src = p.q + b * p.q_bat + i * p.q_tok +
                                  (static_cast<int64_t>(head) * p.G + gi) * D + t * 4;
       uint2 raw[D / 16];
 #pragma unroll
@@ -498,14 +503,14 @@ struct Kernel {
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int at = cur.r.c - p.queries + static_cast<int>(p.by_G(min(row0 + 8 * n + 2 * t + x, rows - 1)));
-        row_hi[2 * n + x] = p.causal ? at + 1 : cur.r.c;
+        const int at = cur.c - p.queries + static_cast<int>(p.by_G(min(row0 + 8 * n + 2 * t + x, rows - 1)));
+        row_hi[2 * n + x] = p.causal ? at + 1 : cur.c;
         row_lo[2 * n + x] = p.window ? at - p.window + 1 : 0;
       }
     }
     const int i0 = p.by_G(row0), i1 = p.by_G(min(row0 + L::kRows, rows) - 1);
-    all_hi = p.causal ? cur.r.c - p.queries + i0 + 1 : cur.r.c;
-    all_lo = p.window ? cur.r.c - p.queries + i1 - p.window + 1 : 0;
+    all_hi = p.causal ? cur.c - p.queries + i0 + 1 : cur.c;
+    all_lo = p.window ? cur.c - p.queries + i1 - p.window + 1 : 0;
     aside = false;
     clear();
   }
@@ -515,12 +520,11 @@ struct Kernel {
   }
 
   // Scales that are above E, far below it or NaN: E becomes the largest so far, and
-  // what was summed under the old one is scaled.  Whether P's scales do not fit f16.
+  // what was summed under the old one is scaled.  What is left of E - e beyond what
+  // one f16 factor holds goes to a second; whether there is any.
   __device__ __forceinline__ bool odd_scales(uint32_t word, bool is_there, uint32_t& delta) {
-    const bool nan = is_there && any_byte_255(word);
-    uint32_t now = is_there ? word : 0;
-    if (nan) now &= ~__vcmpeq4(word, 0xffffffffu);
-    const uint32_t mine = now;
+    uint32_t now = is_there ? word & ~__vcmpeq4(word, 0xffffffffu) : 0;
+    delta = now;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) now = __vmaxu4(now, __shfl_xor_sync(0xffffffffu, now, o));
     now = __vmaxu4(now, top);
@@ -536,21 +540,63 @@ struct Kernel {
           for (int c = 0; c < 4; ++c) acc[n][2 * e + k][c] *= f;
     }
     top = now;
-    delta = is_there ? top - mine : 0;  // byte by byte, nothing is borrowed
-    return __any_sync(0xffffffffu, nan || !fits(delta));
-  }
-  // f16 holds 2^-delta to delta = 14.
-  static __device__ __forceinline__ bool fits(uint32_t delta) {
-    return ((delta + (kG == 4 ? 0x71717171u : 0x7171u) | delta) & 0x80808080u) == 0;
+    const uint32_t all = is_there ? top - delta : 0;  // byte by byte, nothing is borrowed
+    delta = __vminu4(all, 0x0e0e0e0eu);
+    const bool more = __any_sync(0xffffffffu, all != delta);
+    if (more) {
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {  // 2^-rest, down to f16's last 2^-24, else 0
+        const int rest = static_cast<int>((all - delta) >> 8 * e & 255);
+        const uint32_t h = rest <= 14 ? 0x3c00u - (rest << 10) : rest <= 24 ? 1u << (24 - rest) : 0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(mem + L::kScales + kKeys * kG * 6 +
+                                                     e * (2 * kKeys) + lane * 2),
+                     "h"(static_cast<uint16_t>(h))
+                     : "memory");
+      }
+    }
+    return more;
   }
 
-  __device__ __forceinline__ void step(const Cursor& cur, int stage) {
+  // NaN in V (codes, or `v_word`'s scales): NaN in the sums of the rows that read the
+  // key, and 0 in the place of the codes, for the rows that do not.
+  __device__ __forceinline__ void mark_nan(const Record& cur, uint32_t v, uint32_t v_word) {
+#pragma unroll 1
+    for (int r = 0; r < kKeys; ++r) {
+      const uint32_t scale = __shfl_sync(0xffffffffu, v_word, r);
+      if (!(cur.there >> r & 1)) continue;
+      const uint32_t row = v + r * D;
+#pragma unroll
+      for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // feature 16f + 8k + g
+          uint32_t code;
+          asm volatile("ld.shared.u8 %0, [%1];"
+                       : "=r"(code)
+                       : "r"(row + (((f ^ L::v_swizzle(r)) << 4) | 8 * k | g))
+                       : "memory");
+          if ((code & 0x7f) != 0x7f && (scale >> 8 * (f / 2) & 255) != 255) continue;
+#pragma unroll
+          for (int x = 0; x < 2 * NT; ++x)
+            if (reads(x, cur.j + r)) acc[x >> 1][f][2 * k + (x & 1)] = NAN;
+        }
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane * 4; i < kKeys * D; i += 128) {
+      const uint32_t w = lds32(v + i);
+      if (nan_codes(w)) sts32(v + i, w & ~nan_codes(w));
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void step(const Record& cur, int stage) {
     const uint32_t at = mem + stage * L::kStage;
     const uint32_t scales = mem + L::kScales, v_scales = scales + kKeys * kG * 4;
     // ------- the step's scales, a key per lane
     uint32_t k_word = lds32(at + L::kWords + lane * 4);
     uint32_t v_word = lds32(at + L::kWords + (kKeys + lane) * 4);
-    const uint32_t there = lds32(at + L::kThere);
+    const uint32_t there = cur.there;
     const bool upper = D == 64 && p.wide_scales && ((cur.block * p.heads + head_in) & 1);
     if (D == 64 && p.wide_scales) {  // its half of the word
       k_word = upper ? k_word >> 16 : k_word & 0xffffu;
@@ -558,10 +604,16 @@ struct Kernel {
     }
     const bool is_there = there >> lane & 1;
     uint32_t delta = is_there ? top - v_word : 0;
-    bool special = is_there && (at_least_u8x4(top, v_word) != 0x80808080u || any_byte_255(v_word) ||
-                                !fits(delta));
-    special = __any_sync(0xffffffffu, special);
-    if (special) special = odd_scales(v_word, is_there, delta);
+    // f16 holds 2^-delta to delta = 14; two factors beyond
+    const uint32_t odd = (delta + (kG == 4 ? 0x71717171u : 0x7171u)) | delta;
+    bool two = is_there && ((odd | ~at_least_u8x4(top, v_word)) & 0x80808080u) != 0;
+    bool bad = false;
+    if (__any_sync(0xffffffffu, two)) {
+      two = odd_scales(v_word, is_there, delta);
+      bad = __any_sync(0xffffffffu, is_there && any_byte_255(v_word));
+    } else {
+      two = false;
+    }
     {
       float f[4];
       two_scales(k_word, f[0], f[1]);
@@ -682,118 +734,63 @@ struct Kernel {
         l[2 * n + k] += (pr[0][n][k] + pr[0][n][2 + k]) + (pr[1][n][k] + pr[1][n][2 + k]);
     }
 
+    // ------- NaN in V where some row does not read the key
+    const uint32_t v_codes = at + L::kCodes;
+    if (!inside) {
+      uint32_t found = 0;
+#pragma unroll
+      for (int i = 0; i < kKeys * D / 512; ++i) {
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(v_codes + i * 512 + lane * 16)
+                     : "memory");
+        found |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+      }
+      bad |= __any_sync(0xffffffffu, found != 0);
+    }
+    if (bad) mark_nan(cur, v_codes, v_word);
+
     // ------- P^T: row g, keys 4t .. 4t + 3 of each 16, under V's scales of each group,
     // and O^T += V^T P^T
     const int r_v = lane & 15;
-    const uint32_t v0 = at + L::kCodes + r_v * D + (((lane >> 4) ^ L::v_swizzle(r_v)) << 4);
-    bool bad = false;
-    if (!inside) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          uint32_t w[4];
-          load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) bad |= nan_codes(w[k]) != 0;
-        }
-      bad = __any_sync(0xffffffffu, bad);
-    }
+    const uint32_t v0 = v_codes + r_v * D + (((lane >> 4) ^ L::v_swizzle(r_v)) << 4);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      uint32_t b[NT][kG][2];
-      if (!special) {
-        uint2 vs[kG];
+      uint32_t b0[NT], b1[NT];
 #pragma unroll
-        for (int e = 0; e < kG; ++e) vs[e] = lds64(v_scales + e * (2 * kKeys) + 32 * u + 8 * t);
+      for (int n = 0; n < NT; ++n) {
+        b0[n] = transpose8(pack_f16(pr[u][n][0], pr[u][n][1]));
+        b1[n] = transpose8(pack_f16(pr[u][n][2], pr[u][n][3]));
+      }
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        const uint2 vs = lds64(v_scales + e * (2 * kKeys) + 32 * u + 8 * t);
+        uint32_t c0[NT], c1[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint32_t b0 = transpose8(pack_f16(pr[u][n][0], pr[u][n][1]));
-          const uint32_t b1 = transpose8(pack_f16(pr[u][n][2], pr[u][n][3]));
-#pragma unroll
-          for (int e = 0; e < kG; ++e) {
-            b[n][e][0] = mul_f16x2(b0, vs[e].x);
-            b[n][e][1] = mul_f16x2(b1, vs[e].y);
-          }
+          c0[n] = mul_f16x2(b0[n], vs.x);
+          c1[n] = mul_f16x2(b1[n], vs.y);
         }
-      } else {
-        // in fp32: scales far below the largest, or NaN (in the rows that read the key)
-        uint32_t w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          w[k] = lds32(at + L::kWords + (kKeys + 16 * u + key_of(8 * k + g)) * 4) >>
-                 (upper ? 16 : 0);
-#pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          float f[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int byte = static_cast<int>(w[k] >> 8 * e & 255);
-            const int by = static_cast<int>(top >> 8 * e & 255) - byte;
-            f[k] = byte == 255 ? NAN
-                   : by >= 0 && by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23)
-                                         : 0.f;
-          }
+        if (two) {
+          const uint2 more = lds64(v_scales + kKeys * kG * 2 + e * (2 * kKeys) + 32 * u + 8 * t);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[k] = s[u][n][k] == -INFINITY ? 0.f : pr[u][n][k] * f[k >> 1];
-            b[n][e][0] = transpose8(pack_f16(x[0], x[1]));
-            b[n][e][1] = transpose8(pack_f16(x[2], x[3]));
+            c0[n] = mul_f16x2(c0[n], more.x);
+            c1[n] = mul_f16x2(c1[n], more.y);
           }
         }
-      }
-      if (!bad) {
+        uint32_t w[4], a[8];
+        load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
 #pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          uint32_t w[4];
-          load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
-          uint32_t a[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k] = f16_low(w[k]);
-            a[4 + k] = f16_high(w[k]);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma(acc[n][2 * e], a[0], a[1], a[4], a[5], b[n][e][0], b[n][e][1]);
-            mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], b[n][e][0], b[n][e][1]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          a[k] = f16_low(w[k]);
+          a[4 + k] = f16_high(w[k]);
         }
-      } else {
-        // NaN codes as 0 in the product, then NaN wherever a row reads one of them
-        uint32_t sees[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            sees[n][k] = transpose8(
-                pack_f16(s[u][n][2 * k] != -INFINITY, s[u][n][2 * k + 1] != -INFINITY));
-#pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          uint32_t w[4], is[4];
-          load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            is[k] = nan_codes(w[k]);
-            w[k] &= ~is[k];
-            is[k] &= 0x38383838u;  // 1
-          }
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-              mma(acc[n][2 * e + f], f16_low(w[2 * f]), f16_low(w[2 * f + 1]), f16_high(w[2 * f]),
-                  f16_high(w[2 * f + 1]), b[n][e][0], b[n][e][1]);
-              mma(c, f16_low(is[2 * f]), f16_low(is[2 * f + 1]), f16_high(is[2 * f]),
-                  f16_high(is[2 * f + 1]), sees[n][0], sees[n][1]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (c[k] > 0.f) acc[n][2 * e + f][k] = NAN;
-            }
+        for (int n = 0; n < NT; ++n) {
+          mma(acc[n][2 * e], a[0], a[1], a[4], a[5], c0[n], c1[n]);
+          mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], c0[n], c1[n]);
         }
       }
     }
@@ -811,15 +808,15 @@ struct Kernel {
       float sum = l[x];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      z[x] = sum == 0.f ? -INFINITY : m[x] - kShift + log2f(sum);
+      z[x] = sum == 0.f ? -INFINITY : m[x] - kShift + lg2_approx(sum);
       float mine = 1.f, old = 0.f;
       if (aside) {
         const float before = p.aside_z[at + row], most = fmaxf(before, z[x]);
         const float ref = most == -INFINITY ? 0.f : most;
-        old = exp2f(before - ref);
-        mine = exp2f(z[x] - ref);
+        old = ex2_approx(before - ref);
+        mine = ex2_approx(z[x] - ref);
         const float both = old + mine, f = both == 0.f ? 0.f : 1.f / both;
-        z[x] = both == 0.f ? -INFINITY : ref + log2f(both);
+        z[x] = both == 0.f ? -INFINITY : ref + lg2_approx(both);
         old *= f;
         mine *= f;
       }
@@ -840,10 +837,8 @@ struct Kernel {
     }
   }
 
-  // Puts the sum aside and begins another.
-  __device__ __forceinline__ void put_aside() {
-    float z[2 * NT];
-    normalise(z);
+  // Puts a normalised sum aside and begins another.
+  __device__ __forceinline__ void put_aside(const float (&z)[2 * NT]) {
     const int64_t at =
         (static_cast<int64_t>(blockIdx.x) * (p.heads * p.slices) + (threadIdx.x >> 5)) * L::kRows;
     __syncwarp();
@@ -865,17 +860,17 @@ struct Kernel {
   // The rows of a piece, joined over the slices, 8 rows at a time by way of the stage
   // that was last worked on: to the outputs where the piece is the whole of a row's
   // keys (`part` < 0), else to a place among the partials.
-  __device__ __forceinline__ void finish(const Cursor& cur, int part, uint8_t* warps, int stage) {
+  __device__ __forceinline__ void finish(const Record& cur, int part, const float (&z)[2 * NT],
+                                         uint8_t* warps, int stage) {
     const int head = cur.block * p.heads + head_in;
-    const int rows = min(L::kRows, p.queries * p.G - cur.tile * L::kRows);
+    const int b = p.by_row_tiles(cur.entry), row0 = (cur.entry - b * p.row_tiles) * L::kRows;
+    const int rows = min(L::kRows, p.queries * p.G - row0);
     const auto sync = [&] {
       if (p.slices > 1)
         __syncthreads();
       else
         __syncwarp();
     };
-    float z[2 * NT];
-    normalise(z);
     uint8_t* mine = warps + (threadIdx.x >> 5) * L::kWarpBytes + stage * L::kStage;
     const uint8_t* first = warps + head_in * L::kWarpBytes + stage * L::kStage;  // slice 0
     const int64_t stride = static_cast<int64_t>(p.heads) * L::kWarpBytes;
@@ -895,19 +890,22 @@ struct Kernel {
       }
       sync();
       constexpr int kLanes = D / 4;
+#pragma unroll 1
       for (int y = slice * 32 + lane; y < 8 * kLanes; y += p.slices * 32) {
         const int row = y / kLanes, f = y % kLanes * 4;
         if (head >= p.Hkv || 8 * n + row >= rows) continue;
         float most = -INFINITY;
+#pragma unroll 1
         for (int s = 0; s < p.slices; ++s)
           most = fmaxf(most, reinterpret_cast<const float*>(first + s * stride + L::kSumZ)[row]);
         const float ref = most == -INFINITY ? 0.f : most;
         float both = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int s = 0; s < p.slices; ++s) {
           const float zs = reinterpret_cast<const float*>(first + s * stride + L::kSumZ)[row];
           if (zs == -INFINITY) continue;  // it has read nothing
-          const float w = exp2f(zs - ref);
+          const float w = ex2_approx(zs - ref);
           const float4 v = *reinterpret_cast<const float4*>(
               reinterpret_cast<const float*>(first + s * stride) + row * L::kSumRow + f);
           both += w;
@@ -917,19 +915,19 @@ struct Kernel {
           o.w = fmaf(w, v.w, o.w);
         }
         const float inv = both == 0.f ? 0.f : 1.f / both;
-        const float lse = both == 0.f ? -INFINITY : ref + log2f(both);
+        const float lse = both == 0.f ? -INFINITY : ref + lg2_approx(both);
         o.x *= inv;
         o.y *= inv;
         o.z *= inv;
         o.w *= inv;
         if (part < 0) {
-          const int q_row = cur.tile * L::kRows + 8 * n + row, i = p.by_G(q_row);
+          const int q_row = row0 + 8 * n + row, i = p.by_G(q_row);
           const int h = head * p.G + q_row - i * p.G;
-          const int64_t token = static_cast<int64_t>(cur.b) * p.queries + i;
+          const int64_t token = static_cast<int64_t>(b) * p.queries + i;
           *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
               make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
           if (f == 0)
-            p.lse[(static_cast<int64_t>(cur.b) * p.Hq + h) * p.queries + i] =
+            p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + i] =
                 lse * 0.6931471805599453f;
         } else {
           const int64_t at =
@@ -951,74 +949,63 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint8_t* warps = smem + L::kRoom;
   Kernel<D, NT> k(p, warps + (threadIdx.x >> 5) * L::kWarpBytes);
-  Cursor ahead{};
-  const Share share = find_share(p, L::kRows, reinterpret_cast<uint64_t*>(smem), k.slice, ahead);
+  Cursor cursor{};
+  const Share share =
+      find_share<L::kRows>(p, reinterpret_cast<uint64_t*>(smem), cursor);
   if (share.begin >= share.end) return;
-  Cursor cur = ahead;
-  const uint32_t steps = static_cast<uint32_t>(share.end - share.begin);
+  const int steps = static_cast<int>(share.end - share.begin);
+  Ahead next;
+  k.look(cursor, next);
   uint2 pending = make_uint2(0, 0);
-  // the first steps' tables are looked up together: one wait for all
-  {
-    Ahead a[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-      a[i] = Ahead{-1, 0, 0};
-      if (i < static_cast<int>(steps)) a[i] = k.look(ahead);
-    }
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-      if (i < static_cast<int>(steps)) {
-        k.issue(a[i], i, pending);
-        k.store_pending(i, pending);
-      } else {
-        copies_commit();
+  int in_sum = 0, stage = 0;
+  // two rounds that only start copies, then one for each step
+#pragma unroll 1
+  for (int i = -kStages; i < steps; ++i, stage ^= 1) {
+    if (i >= 0) {
+      copies_wait<kStages - 1>();
+      __syncwarp();
+      Record r;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(r.there), "=r"(r.j), "=r"(r.entry), "=r"(r.block)
+                   : "r"(k.mem + stage * L::kStage + L::kRecord)
+                   : "memory");
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(r.step), "=r"(r.n), "=r"(r.c), "=r"(r.pad)
+                   : "r"(k.mem + stage * L::kStage + L::kRecord + 16)
+                   : "memory");
+      if (i == 0 || r.step == 0) {
+        k.begin(r);
+        in_sum = 0;
+      }
+      k.step(r, stage);
+      const bool ends = r.step + 1 == r.n || i + 1 == steps;
+      if (ends || ++in_sum == kFlush) {
+        float z[2 * NT];
+        k.normalise(z);
+        if (!ends) {
+          k.put_aside(z);
+          in_sum = 0;
+        } else {
+          // a CTA leaves at most two partials: where an item ends or goes through (0)
+          // and where one begins (1); the latter knows how many there are
+          const bool starts = r.step <= i;
+          const int left = r.n - 1 - r.step;  // steps of the item in later shares
+          if (starts && threadIdx.x == 0)
+            p.pieces[static_cast<int64_t>(r.entry) * p.head_blocks + r.block] = make_int2(
+                static_cast<int>(blockIdx.x),
+                1 + static_cast<int>((static_cast<uint32_t>(left) + share.per - 1) / share.per));
+          k.finish(r, starts && left == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0),
+                   z, warps, stage);
+        }
       }
     }
-  }
-  uint32_t issued = min(steps, static_cast<uint32_t>(kStages));
-  Ahead next{-1, 0, 0};
-  if (issued < steps) next = k.look(ahead);
-  bool fresh = true;
-  int in_sum = 0, stage = 0;
-  // the list's place of the item's first step
-  uint64_t item = share.begin - (cur.r.n - 1 - (cur.left + (cur.front ? cur.r.n - cur.r.n_first : 0)));
-  for (uint32_t i = 0; i < steps; ++i, stage ^= 1) {
-    if (fresh) {
-      k.begin(cur);
-      fresh = false;
-      in_sum = 0;
-    }
-    copies_wait<kStages - 1>();
-    __syncwarp();
-    k.step(cur, stage);
-    const bool ends = cur.last() || i + 1 == steps;
-    if (ends) {
-      // the CTAs that the item's first and last step are in
-      const uint32_t from = static_cast<uint32_t>(item / share.per);
-      const uint32_t pieces = static_cast<uint32_t>((item + cur.r.n - 1) / share.per) - from + 1;
-      const bool starts = from == blockIdx.x;
-      if (starts && threadIdx.x == 0)
-        p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
-            make_int2(static_cast<int>(from), static_cast<int>(pieces));
-      // a CTA leaves at most two partials: where an item ends or goes through (0)
-      // and where one begins (1)
-      k.finish(cur, pieces == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0), warps,
-               stage);
-      fresh = true;
-      item += cur.r.n;
-    } else if (++in_sum == kFlush) {
-      k.put_aside();
-      in_sum = 0;
-    }
-    // (the last issue's scale words; one is always a step old)
-    if (i > 0 && issued > kStages) k.store_pending(stage ^ 1, pending);
-    if (issued < steps) {
+    // (scale words of the step before: nobody waits for them)
+    if (i > -kStages) k.store_pending(stage ^ 1, pending);
+    if (i + kStages < steps) {
       k.issue(next, stage, pending);
-      if (++issued < steps) next = k.look(ahead);
-    } else {
-      copies_commit();
+      if (i + kStages + 1 < steps) k.look(cursor, next);
     }
-    cur.next(p, L::kRows, k.slice);
+    copies_commit();
   }
   copies_wait<0>();
 }
@@ -1049,7 +1036,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const float ref = most == -INFINITY ? 0.f : most;
 #pragma unroll 4
     for (int k = 0; k < piece.y; ++k) {
-      const float z = p.part_z[place(k)], w = exp2f(z - ref);
+      const float z = p.part_z[place(k)], w = ex2_approx(z - ref);
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + place(k) * D + f);
       if (z == -INFINITY) continue;  // it has read nothing
       both += w;
@@ -1059,7 +1046,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       o.w = fmaf(w, v.w, o.w);
     }
     const float inv = both == 0.f ? 0.f : 1.f / both;
-    const float z = both == 0.f ? -INFINITY : ref + log2f(both);
+    const float z = both == 0.f ? -INFINITY : ref + lg2_approx(both);
     const int r = tile * kRows + row, i = p.by_G(r), h = head * p.G + r - i * p.G;
     const int64_t token = static_cast<int64_t>(b) * p.queries + i;
     *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
@@ -1080,7 +1067,7 @@ struct Cut {
 Cut cut_of(const csbp_paged_problem& p, const csbp_kv_cache& c) {
   Cut r{};
   const int64_t rows = static_cast<int64_t>(p.queries) * (p.Hq / c.Hkv);
-  r.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  r.tile_rows = rows <= 8 ? 8 : 16;
   r.row_tiles = static_cast<int>((rows + r.tile_rows - 1) / r.tile_rows);
   const int most = most_warps(r.tile_rows / 8);
   double best = 0;
@@ -1249,6 +1236,7 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.by_page = Divisor::of(static_cast<uint32_t>(cache->page_size));
   a.by_G = Divisor::of(static_cast<uint32_t>(a.G));
   a.by_row_tiles = Divisor::of(static_cast<uint32_t>(cut.row_tiles));
+  a.by_step = Divisor::of(static_cast<uint32_t>(kKeys * cut.slices));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + kStatusBytes);
   a.part_z = reinterpret_cast<float*>(ws + at.part_z);
@@ -1258,9 +1246,7 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const auto run = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    return cut.tile_rows == 8    ? launch<D, 1>(a, cut, sms, s)
-           : cut.tile_rows == 16 ? launch<D, 2>(a, cut, sms, s)
-                                 : launch<D, 4>(a, cut, sms, s);
+    return cut.tile_rows == 8 ? launch<D, 1>(a, cut, sms, s) : launch<D, 2>(a, cut, sms, s);
   };
   const cudaError_t e = cache->d == 128 ? run(std::integral_constant<int, 128>())
                                         : run(std::integral_constant<int, 64>());
