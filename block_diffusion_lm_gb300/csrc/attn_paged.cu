@@ -86,11 +86,14 @@ struct PagedParams {
 };
 
 // ----------------------------------------------------------- instructions
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copies of `n` bytes (16 or 4), or as many zeros (n = 0: nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -210,6 +213,7 @@ struct Share {
 };
 
 // Adds all steps up and finds the CTA's share, and the cursor of its begin.
+// `room`: a number per warp, and at kMostWarps the cursor.
 template <int R>
 __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room, Cursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -225,11 +229,10 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room
     for (int e0 = 0; e0 < entries; e0 += blockDim.x) {
       const int e = e0 + tid;
       uint64_t mine = 0;
-      int n = 1;
+      Cursor here{e, 0, 0, 0, {}};
       if (e < entries) {
-        const int b = p.by_row_tiles(e);
-        n = range_of(p, b, e - b * p.row_tiles, R).n;
-        mine = static_cast<uint64_t>(n) * p.head_blocks;
+        here.load(p, R);
+        mine = static_cast<uint64_t>(here.r.n) * p.head_blocks;
       }
       uint64_t sum = mine;
 #pragma unroll
@@ -248,15 +251,17 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room
       }
       if (one_sweep) total = all;
       if (pass == 1) {
-        const uint64_t per = (total + gridDim.x - 1) / gridDim.x;
+        const uint64_t per = total >> 32 ? (total + gridDim.x - 1) / gridDim.x
+                                         : (static_cast<uint32_t>(total) - 1) / gridDim.x + 1;
         s.per = static_cast<uint32_t>(min(per, uint64_t(1) << 31));
         s.begin = min(per * blockIdx.x, total);
         s.end = min(s.begin + per, total);
         const uint64_t from = before + sum - mine;
         if (s.begin >= from && s.begin < from + mine) {
           const uint32_t in = static_cast<uint32_t>(s.begin - from);
-          room[kMostWarps] = static_cast<uint64_t>(e);
-          room[kMostWarps + 1] = static_cast<uint64_t>(in / n) << 32 | in % n;
+          here.block = in / here.r.n;
+          here.step = in - here.block * here.r.n;
+          *reinterpret_cast<Cursor*>(room + kMostWarps) = here;
         }
       }
       before += all;
@@ -264,12 +269,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room
     total = before;
   }
   __syncthreads();
-  if (s.begin < s.end) {
-    cur.entry = static_cast<int>(room[kMostWarps]);
-    cur.block = static_cast<int>(room[kMostWarps + 1] >> 32);
-    cur.step = static_cast<int>(room[kMostWarps + 1]);
-    cur.load(p, R);
-  }
+  if (s.begin < s.end) cur = *reinterpret_cast<const Cursor*>(room + kMostWarps);
   return s;
 }
 
@@ -403,13 +403,15 @@ struct Kernel {
   }
 
   // Starts the copies of a step into a stage of the ring.  A key that is not there
-  // is a copy of the cache's first row; its score is masked.
+  // is zeros (copies of one row of the cache would make it a hot spot: 61 x 1 queries
+  // with a window of 92 keys took 24 us).
   __device__ __forceinline__ void issue(const Ahead& a, int stage, uint2& pending) const {
     const uint32_t at = mem + stage * L::kStage;
     const int head = a.r.block * p.heads + head_in;
     const bool there = static_cast<uint32_t>(a.page) < static_cast<uint32_t>(p.pages) && head < p.Hkv;
     const uint32_t row =
         there ? static_cast<uint32_t>(a.page * p.page_size + a.place) * p.Hkv + head : 0;
+    const uint32_t is = __ballot_sync(0xffffffffu, there);
     constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
     const int chunk = lane % kChunks, r0 = lane / kChunks;
     const uint8_t *k = p.k + chunk * 16, *v = p.v + chunk * 16;
@@ -417,24 +419,26 @@ struct Kernel {
     for (int i = 0; i < kKeys / kAtOnce; ++i) {
       const int r = i * kAtOnce + r0;
       const uint64_t from = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * D;
-      copy16(at + r * D + (chunk ^ L::k_swizzle(r)) * 16, k + from);
-      copy16(at + L::kCodes + r * D + (chunk ^ L::v_swizzle(r)) * 16, v + from);
+      const int n = is >> r & 1 ? 16 : 0;
+      copy16(at + r * D + (chunk ^ L::k_swizzle(r)) * 16, k + from, n);
+      copy16(at + L::kCodes + r * D + (chunk ^ L::v_swizzle(r)) * 16, v + from, n);
     }
     // scale bytes
     const uint64_t place = static_cast<uint64_t>(row) * kG;
     if (p.wide_scales) {
-      copy4(at + L::kWords + lane * 4, p.k_scale + (place & ~uint64_t(3)));
-      copy4(at + L::kWords + (kKeys + lane) * 4, p.v_scale + (place & ~uint64_t(3)));
+      copy4(at + L::kWords + lane * 4, p.k_scale + (place & ~uint64_t(3)), there ? 4 : 0);
+      copy4(at + L::kWords + (kKeys + lane) * 4, p.v_scale + (place & ~uint64_t(3)),
+            there ? 4 : 0);
     } else {
       uint32_t w[2] = {0, 0};
+      if (there)
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        w[0] |= static_cast<uint32_t>(__ldg(p.k_scale + place + e)) << 8 * e;
-        w[1] |= static_cast<uint32_t>(__ldg(p.v_scale + place + e)) << 8 * e;
-      }
+        for (int e = 0; e < kG; ++e) {
+          w[0] |= static_cast<uint32_t>(__ldg(p.k_scale + place + e)) << 8 * e;
+          w[1] |= static_cast<uint32_t>(__ldg(p.v_scale + place + e)) << 8 * e;
+        }
       pending = make_uint2(w[0], w[1]);  // stored a step later, so that nobody waits here
     }
-    const uint32_t is = __ballot_sync(0xffffffffu, there);
     if (lane == 0) {
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kRecord), "r"(is),
                    "r"(a.r.j), "r"(a.r.entry), "r"(a.r.block)
@@ -962,7 +966,6 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
 #pragma unroll 1
   for (int i = -kStages; i < steps; ++i, stage ^= 1) {
     if (i >= 0) {
-      copies_wait<kStages - 1>();
       __syncwarp();
       Record r;
       asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -977,6 +980,8 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
         k.begin(r);
         in_sum = 0;
       }
+      copies_wait<kStages - 1>();
+      __syncwarp();
       k.step(r, stage);
       const bool ends = r.step + 1 == r.n || i + 1 == steps;
       if (ends || ++in_sum == kFlush) {
