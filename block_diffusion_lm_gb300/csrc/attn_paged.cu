@@ -10,7 +10,9 @@
 // heads, which share a 32-byte sector, are read by one CTA at one time.
 //
 // Work.  The steps of all sequences and row tiles, end to end, form one list that
-// is cut into equal shares, one per SM: every CTA adds the lengths up and finds its
+// is cut into equal shares, one per SM (or, where a token's heads take several CTAs,
+// as many per group of SMs: the CTAs of a group read the same tokens at the same
+// time, and sectors of scale bytes that they share come from DRAM once): every CTA adds the lengths up and finds its
 // share itself, so that lengths never come to the host.  A row tile that is cut
 // leaves normalised fp32 partials with their LSE in the workspace, which a second
 // kernel joins exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
@@ -76,6 +78,7 @@ struct PagedParams {
   // how rows and heads are cut up
   int32_t heads, slices, head_blocks;  // KV heads and slices of a CTA, CTAs' worth of heads
   int32_t row_tiles;
+  int32_t lanes, lane_ctas;  // of the list: CTA c has share c / lanes of lane c % lanes
   int32_t wide_scales;  // scale bytes of a token are loaded in 4-byte words
   Divisor by_page, by_G, by_row_tiles, by_step;  // (a step: the CTA's keys)
   float* part_o;  // [2 x CTAs][heads][tile rows][d]
@@ -232,7 +235,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room
       Cursor here{e, 0, 0, 0, {}};
       if (e < entries) {
         here.load(p, R);
-        mine = static_cast<uint64_t>(here.r.n) * p.head_blocks;
+        mine = static_cast<uint64_t>(here.r.n) * (p.head_blocks / p.lanes);
       }
       uint64_t sum = mine;
 #pragma unroll
@@ -251,16 +254,19 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room
       }
       if (one_sweep) total = all;
       if (pass == 1) {
-        const uint64_t per = total >> 32 ? (total + gridDim.x - 1) / gridDim.x
-                                         : (static_cast<uint32_t>(total) - 1) / gridDim.x + 1;
+        const uint32_t ctas = p.lane_ctas;
+        const uint64_t per = total >> 32 ? (total + ctas - 1) / ctas
+                                         : (static_cast<uint32_t>(total) - 1) / ctas + 1;
         s.per = static_cast<uint32_t>(min(per, uint64_t(1) << 31));
-        s.begin = min(per * blockIdx.x, total);
+        const uint32_t mine_is = blockIdx.x / p.lanes;
+        s.begin = min(per * mine_is, total);
         s.end = min(s.begin + per, total);
         const uint64_t from = before + sum - mine;
         if (s.begin >= from && s.begin < from + mine) {
           const uint32_t in = static_cast<uint32_t>(s.begin - from);
-          here.block = in / here.r.n;
-          here.step = in - here.block * here.r.n;
+          const int before_me = in / here.r.n;
+          here.step = in - before_me * here.r.n;
+          here.block = before_me * p.lanes + blockIdx.x % p.lanes;
           *reinterpret_cast<Cursor*>(room + kMostWarps) = here;
         }
       }
@@ -396,8 +402,9 @@ struct Kernel {
     a.r.c = cur.r.c;
     if (++cur.step < cur.r.n) return;
     cur.step = 0;
-    if (++cur.block < p.head_blocks) return;
-    cur.block = 0;
+    cur.block += p.lanes;
+    if (cur.block < p.head_blocks) return;
+    cur.block %= p.lanes;
     ++cur.entry;
     cur.load(p, L::kRows);
   }
@@ -761,29 +768,35 @@ struct Kernel {
     const uint32_t v0 = v_codes + r_v * D + (((lane >> 4) ^ L::v_swizzle(r_v)) << 4);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      uint32_t b0[NT], b1[NT];
+      uint32_t b[NT][kG][2];
+      {
+        uint2 vs[kG];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        b0[n] = transpose8(pack_f16(pr[u][n][0], pr[u][n][1]));
-        b1[n] = transpose8(pack_f16(pr[u][n][2], pr[u][n][3]));
-      }
-#pragma unroll
-      for (int e = 0; e < kG; ++e) {
-        const uint2 vs = lds64(v_scales + e * (2 * kKeys) + 32 * u + 8 * t);
-        uint32_t c0[NT], c1[NT];
+        for (int e = 0; e < kG; ++e) vs[e] = lds64(v_scales + e * (2 * kKeys) + 32 * u + 8 * t);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          c0[n] = mul_f16x2(b0[n], vs.x);
-          c1[n] = mul_f16x2(b1[n], vs.y);
+          const uint32_t b0 = transpose8(pack_f16(pr[u][n][0], pr[u][n][1]));
+          const uint32_t b1 = transpose8(pack_f16(pr[u][n][2], pr[u][n][3]));
+#pragma unroll
+          for (int e = 0; e < kG; ++e) {
+            b[n][e][0] = mul_f16x2(b0, vs[e].x);
+            b[n][e][1] = mul_f16x2(b1, vs[e].y);
+          }
         }
-        if (two) {
+      }
+      if (two) {
+#pragma unroll
+        for (int e = 0; e < kG; ++e) {
           const uint2 more = lds64(v_scales + kKeys * kG * 2 + e * (2 * kKeys) + 32 * u + 8 * t);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            c0[n] = mul_f16x2(c0[n], more.x);
-            c1[n] = mul_f16x2(c1[n], more.y);
+            b[n][e][0] = mul_f16x2(b[n][e][0], more.x);
+            b[n][e][1] = mul_f16x2(b[n][e][1], more.y);
           }
         }
+      }
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
         uint32_t w[4], a[8];
         load_columns(w, (v0 ^ (e << 5)) + 16 * u * D);
 #pragma unroll
@@ -793,8 +806,8 @@ struct Kernel {
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma(acc[n][2 * e], a[0], a[1], a[4], a[5], c0[n], c1[n]);
-          mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], c0[n], c1[n]);
+          mma(acc[n][2 * e], a[0], a[1], a[4], a[5], b[n][e][0], b[n][e][1]);
+          mma(acc[n][2 * e + 1], a[2], a[3], a[6], a[7], b[n][e][0], b[n][e][1]);
         }
       }
     }
@@ -819,12 +832,12 @@ struct Kernel {
         const float ref = most == -INFINITY ? 0.f : most;
         old = ex2_approx(before - ref);
         mine = ex2_approx(z[x] - ref);
-        const float both = old + mine, f = both == 0.f ? 0.f : 1.f / both;
+        const float both = old + mine, f = both == 0.f ? 0.f : __fdividef(1.f, both);
         z[x] = both == 0.f ? -INFINITY : ref + lg2_approx(both);
         old *= f;
         mine *= f;
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
 #pragma unroll
       for (int f = 0; f < D / 16; ++f) {
         // 2^(E - 127), in two steps: one could lie below fp32's range
@@ -895,9 +908,9 @@ struct Kernel {
       sync();
       constexpr int kLanes = D / 4;
 #pragma unroll 1
-      for (int y = slice * 32 + lane; y < 8 * kLanes; y += p.slices * 32) {
+      for (int y = slice * 32 + lane; y < min(8, rows - 8 * n) * kLanes; y += p.slices * 32) {
         const int row = y / kLanes, f = y % kLanes * 4;
-        if (head >= p.Hkv || 8 * n + row >= rows) continue;
+        if (head >= p.Hkv) break;
         float most = -INFINITY;
 #pragma unroll 1
         for (int s = 0; s < p.slices; ++s)
@@ -918,7 +931,7 @@ struct Kernel {
           o.z = fmaf(w, v.z, o.z);
           o.w = fmaf(w, v.w, o.w);
         }
-        const float inv = both == 0.f ? 0.f : 1.f / both;
+        const float inv = both == 0.f ? 0.f : __fdividef(1.f, both);
         const float lse = both == 0.f ? -INFINITY : ref + lg2_approx(both);
         o.x *= inv;
         o.y *= inv;
@@ -1034,7 +1047,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // the first piece is where the item begins, the others are their CTAs' first
     const auto place = [&](int k) {
-      return (static_cast<int64_t>(2 * (piece.x + k) + (k == 0)) * p.heads + head_in) * kRows + row;
+      return (static_cast<int64_t>(2 * (piece.x + k * p.lanes) + (k == 0)) * p.heads + head_in) * kRows + row;
     };
 #pragma unroll 4
     for (int k = 0; k < piece.y; ++k) most = fmaxf(most, p.part_z[place(k)]);
@@ -1050,7 +1063,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       o.z = fmaf(w, v.z, o.z);
       o.w = fmaf(w, v.w, o.w);
     }
-    const float inv = both == 0.f ? 0.f : 1.f / both;
+    const float inv = both == 0.f ? 0.f : __fdividef(1.f, both);
     const float z = both == 0.f ? -INFINITY : ref + lg2_approx(both);
     const int r = tile * kRows + row, i = p.by_G(r), h = head * p.G + r - i * p.G;
     const int64_t token = static_cast<int64_t>(b) * p.queries + i;
@@ -1148,7 +1161,7 @@ cudaError_t launch(const PagedParams& p, const Cut& cut, int sms, cudaStream_t s
     return e != cudaSuccess ? e : cudaErrorInvalidDevice;
   const int warps = cut.heads * cut.slices;
   const int timed = timer_begin(13, stream);
-  paged_rows_kernel<D, NT><<<sms, warps * 32, L::smem(warps), stream>>>(p);
+  paged_rows_kernel<D, NT><<<p.lanes * p.lane_ctas, warps * 32, L::smem(warps), stream>>>(p);
   e = cudaGetLastError();
   timer_end(timed, stream);
   if (e != cudaSuccess) return e;
@@ -1236,6 +1249,8 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.slices = cut.slices;
   a.head_blocks = cut.head_blocks;
   a.row_tiles = cut.row_tiles;
+  a.lanes = cut.head_blocks <= sms / 8 ? cut.head_blocks : 1;
+  a.lane_ctas = sms / a.lanes;
   a.wide_scales = aligned(cache->k_scale, 4) && aligned(cache->v_scale, 4) &&
                   cache->Hkv * (cache->d / kGroup) % 4 == 0;
   a.by_page = Divisor::of(static_cast<uint32_t>(cache->page_size));
