@@ -78,9 +78,11 @@ struct PagedParams {
   // how rows and heads are cut up
   int32_t heads, slices, head_blocks;  // KV heads and slices of a CTA, CTAs' worth of heads
   int32_t row_tiles;
-  int32_t lanes, lane_ctas;  // of the list: CTA c has share c / lanes of lane c % lanes
+  // of the list: CTA c has share c / lanes of lane c % lanes, which takes every
+  // lanes-th block of heads
+  int32_t lanes, lane_ctas, lane_blocks;
   int32_t wide_scales;  // scale bytes of a token are loaded in 4-byte words
-  Divisor by_page, by_G, by_row_tiles, by_step;  // (a step: the CTA's keys)
+  Divisor by_page, by_G, by_row_tiles, by_lanes, by_step;  // (a step: the CTA's keys)
   float* part_o;  // [2 x CTAs][heads][tile rows][d]
   float* part_z;  // [2 x CTAs][heads][tile rows]
   int2* pieces;   // per sequence, row tile and head block: first CTA, number of them
@@ -211,42 +213,40 @@ struct Cursor {
 };
 
 struct Share {
-  uint64_t begin, end;  // steps of the list
-  uint32_t per;         // steps of a share, 2^31 at most
+  uint32_t begin, end, per;  // steps of the list (the host keeps it below 2^31)
 };
 
 // Adds all steps up and finds the CTA's share, and the cursor of its begin.
 // `room`: a number per warp, and at kMostWarps the cursor.
 template <int R>
-__device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room, Cursor& cur) {
+__device__ __forceinline__ Share find_share(const PagedParams& p, uint32_t* room, Cursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int entries = p.batch * p.row_tiles;
   Share s{0, 0, 0};
-  uint64_t total = 0;
+  uint32_t total = 0;
   // the total, then the begin; both at once where one sweep takes in all entries
   const bool one_sweep = entries <= static_cast<int>(blockDim.x);
 #pragma unroll 1
   for (int pass = one_sweep ? 1 : 0; pass < 2; ++pass) {
-    uint64_t before = 0;
+    uint32_t before = 0;
 #pragma unroll 1
     for (int e0 = 0; e0 < entries; e0 += blockDim.x) {
-      const int e = e0 + tid;
-      uint64_t mine = 0;
-      Cursor here{e, 0, 0, 0, {}};
-      if (e < entries) {
+      Cursor here{e0 + tid, 0, 0, 0, {}};
+      uint32_t mine = 0;
+      if (here.entry < entries) {
         here.load(p, R);
-        mine = static_cast<uint64_t>(here.r.n) * (p.head_blocks / p.lanes);
+        mine = static_cast<uint32_t>(here.r.n) * p.lane_blocks;
       }
-      uint64_t sum = mine;
+      uint32_t sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
       }
-      __syncthreads();
+      if (!one_sweep) __syncthreads();
       if (lane == 31) room[warp] = sum;
       __syncthreads();
-      uint64_t all = 0;
+      uint32_t all = 0;
 #pragma unroll 1
       for (int w = 0; w < warps; ++w) {
         if (w < warp) sum += room[w];
@@ -254,19 +254,14 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint64_t* room
       }
       if (one_sweep) total = all;
       if (pass == 1) {
-        const uint32_t ctas = p.lane_ctas;
-        const uint64_t per = total >> 32 ? (total + ctas - 1) / ctas
-                                         : (static_cast<uint32_t>(total) - 1) / ctas + 1;
-        s.per = static_cast<uint32_t>(min(per, uint64_t(1) << 31));
-        const uint32_t mine_is = blockIdx.x / p.lanes;
-        s.begin = min(per * mine_is, total);
-        s.end = min(s.begin + per, total);
-        const uint64_t from = before + sum - mine;
+        s.per = (total - 1) / p.lane_ctas + 1;
+        s.begin = min(s.per * p.by_lanes(blockIdx.x), total);
+        s.end = min(s.begin + s.per, total);
+        const uint32_t from = before + sum - mine;
         if (s.begin >= from && s.begin < from + mine) {
-          const uint32_t in = static_cast<uint32_t>(s.begin - from);
-          const int before_me = in / here.r.n;
-          here.step = in - before_me * here.r.n;
-          here.block = before_me * p.lanes + blockIdx.x % p.lanes;
+          const int passed = (s.begin - from) / here.r.n;
+          here.step = s.begin - from - passed * here.r.n;
+          here.block = passed * p.lanes + blockIdx.x - p.by_lanes(blockIdx.x) * p.lanes;
           *reinterpret_cast<Cursor*>(room + kMostWarps) = here;
         }
       }
@@ -287,19 +282,20 @@ template <int D, int NT>
 struct Rows {
   static constexpr int kRows = 8 * NT;  // of a tile
   static constexpr int kGroups = D / 32;
-  // a warp's ring stage: K codes, V codes, scale words (K, V), the step's record;
-  // a step that has been worked on leaves it to 8 rows of the result [row][D + 4]
-  // and their LSE (log2)
+  // a warp's ring stage: K codes, V codes, scale words (K, V), the step's record
   static constexpr int kCodes = kKeys * D;
   static constexpr int kWords = 2 * kCodes;
   static constexpr int kRecord = kWords + 2 * kKeys * 4;
-  static constexpr int kSumRow = D + 4;
-  static constexpr int kSumZ = 8 * kSumRow * 4;
   static constexpr int kStage = kRecord + 128;
-  static_assert(kSumZ + 32 <= kStage, "a worked-on stage holds 8 rows");
   // the step's scales: fp32 of K [key][group], f16 of V [group][key] in two factors
   static constexpr int kScales = kStages * kStage;
-  static constexpr int kWarpBytes = kScales + kKeys * kGroups * 8;
+  // and when an item ends, in their place, 4 rows of the result [row][D + 4] and their
+  // LSE (log2)
+  static constexpr int kSum = kScales;
+  static constexpr int kSumRow = D + 4;
+  static constexpr int kSumZ = kSum + 4 * kSumRow * 4;
+  static constexpr int kWarpBytes = (kSumZ + 16 + 127) / 128 * 128;
+  static_assert(kScales + kKeys * kGroups * 8 <= kSumZ, "shared memory of a warp");
   static constexpr int kRoom = 256;  // find_share, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
 
@@ -404,7 +400,7 @@ struct Kernel {
     cur.step = 0;
     cur.block += p.lanes;
     if (cur.block < p.head_blocks) return;
-    cur.block %= p.lanes;
+    cur.block -= p.lanes * p.lane_blocks;
     ++cur.entry;
     cur.load(p, L::kRows);
   }
@@ -874,11 +870,11 @@ struct Kernel {
     clear();
   }
 
-  // The rows of a piece, joined over the slices, 8 rows at a time by way of the stage
-  // that was last worked on: to the outputs where the piece is the whole of a row's
-  // keys (`part` < 0), else to a place among the partials.
+  // The rows of a piece, joined over the slices, 4 rows at a time by way of shared
+  // memory: to the outputs where the piece is the whole of a row's keys (`part` < 0),
+  // else to a place among the partials.
   __device__ __forceinline__ void finish(const Record& cur, int part, const float (&z)[2 * NT],
-                                         uint8_t* warps, int stage) {
+                                         uint8_t* warps) {
     const int head = cur.block * p.heads + head_in;
     const int b = p.by_row_tiles(cur.entry), row0 = (cur.entry - b * p.row_tiles) * L::kRows;
     const int rows = min(L::kRows, p.queries * p.G - row0);
@@ -888,29 +884,31 @@ struct Kernel {
       else
         __syncwarp();
     };
-    uint8_t* mine = warps + (threadIdx.x >> 5) * L::kWarpBytes + stage * L::kStage;
-    const uint8_t* first = warps + head_in * L::kWarpBytes + stage * L::kStage;  // slice 0
-    const int64_t stride = static_cast<int64_t>(p.heads) * L::kWarpBytes;
+    uint8_t* mine = warps + (threadIdx.x >> 5) * L::kWarpBytes;
+    const uint8_t* first = warps + head_in * L::kWarpBytes;  // slice 0
+    const int stride = p.heads * L::kWarpBytes;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (8 * n >= rows) break;
-      __syncwarp();
+    for (int n = 0; n < 2 * NT; ++n) {  // rows 4n .. 4n + 3: those of the lanes t / 2 = n % 2
+      if (4 * n >= rows) break;
+      if (t >> 1 == (n & 1)) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float* to = reinterpret_cast<float*>(mine) + (2 * t + x) * L::kSumRow + g;
+        for (int x = 0; x < 2; ++x) {
+          const int row = 2 * (t & 1) + x;
+          float* to = reinterpret_cast<float*>(mine + L::kSum) + row * L::kSumRow + g;
 #pragma unroll
-        for (int f = 0; f < D / 16; ++f) {
-          to[16 * f] = acc[n][f][x];
-          to[16 * f + 8] = acc[n][f][2 + x];
+          for (int f = 0; f < D / 16; ++f) {
+            to[16 * f] = acc[n / 2][f][x];
+            to[16 * f + 8] = acc[n / 2][f][2 + x];
+          }
+          if (g == 0) reinterpret_cast<float*>(mine + L::kSumZ)[row] = z[n / 2 * 2 + x];
         }
-        if (g == 0) reinterpret_cast<float*>(mine + L::kSumZ)[2 * t + x] = z[2 * n + x];
       }
       sync();
       constexpr int kLanes = D / 4;
 #pragma unroll 1
-      for (int y = slice * 32 + lane; y < min(8, rows - 8 * n) * kLanes; y += p.slices * 32) {
-        const int row = y / kLanes, f = y % kLanes * 4;
+      for (int y = slice * 32 + lane; y < min(4, rows - 4 * n) * kLanes; y += p.slices * 32) {
         if (head >= p.Hkv) break;
+        const int row = y / kLanes, f = y % kLanes * 4;
         float most = -INFINITY;
 #pragma unroll 1
         for (int s = 0; s < p.slices; ++s)
@@ -924,7 +922,7 @@ struct Kernel {
           if (zs == -INFINITY) continue;  // it has read nothing
           const float w = ex2_approx(zs - ref);
           const float4 v = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(first + s * stride) + row * L::kSumRow + f);
+              reinterpret_cast<const float*>(first + s * stride + L::kSum) + row * L::kSumRow + f);
           both += w;
           o.x = fmaf(w, v.x, o.x);
           o.y = fmaf(w, v.y, o.y);
@@ -938,17 +936,16 @@ struct Kernel {
         o.z *= inv;
         o.w *= inv;
         if (part < 0) {
-          const int q_row = row0 + 8 * n + row, i = p.by_G(q_row);
+          const int q_row = row0 + 4 * n + row, i = p.by_G(q_row);
           const int h = head * p.G + q_row - i * p.G;
           const int64_t token = static_cast<int64_t>(b) * p.queries + i;
           *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
               make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
           if (f == 0)
-            p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + i] =
-                lse * 0.6931471805599453f;
+            p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + i] = lse * 0.6931471805599453f;
         } else {
           const int64_t at =
-              (static_cast<int64_t>(part) * p.heads + head_in) * L::kRows + 8 * n + row;
+              (static_cast<int64_t>(part) * p.heads + head_in) * L::kRows + 4 * n + row;
           *reinterpret_cast<float4*>(p.part_o + at * D + f) = o;
           if (f == 0) p.part_z[at] = lse;
         }
@@ -968,7 +965,7 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   Kernel<D, NT> k(p, warps + (threadIdx.x >> 5) * L::kWarpBytes);
   Cursor cursor{};
   const Share share =
-      find_share<L::kRows>(p, reinterpret_cast<uint64_t*>(smem), cursor);
+      find_share<L::kRows>(p, reinterpret_cast<uint32_t*>(smem), cursor);
   if (share.begin >= share.end) return;
   const int steps = static_cast<int>(share.end - share.begin);
   Ahead next;
@@ -978,9 +975,9 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   // two rounds that only start copies, then one for each step
 #pragma unroll 1
   for (int i = -kStages; i < steps; ++i, stage ^= 1) {
+    Record r;
     if (i >= 0) {
       __syncwarp();
-      Record r;
       asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(r.there), "=r"(r.j), "=r"(r.entry), "=r"(r.block)
                    : "r"(k.mem + stage * L::kStage + L::kRecord)
@@ -996,26 +993,28 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
       copies_wait<kStages - 1>();
       __syncwarp();
       k.step(r, stage);
-      const bool ends = r.step + 1 == r.n || i + 1 == steps;
-      if (ends || ++in_sum == kFlush) {
-        float z[2 * NT];
-        k.normalise(z);
-        if (!ends) {
-          k.put_aside(z);
-          in_sum = 0;
-        } else {
-          // a CTA leaves at most two partials: where an item ends or goes through (0)
-          // and where one begins (1); the latter knows how many there are
-          const bool starts = r.step <= i;
-          const int left = r.n - 1 - r.step;  // steps of the item in later shares
-          if (starts && threadIdx.x == 0)
-            p.pieces[static_cast<int64_t>(r.entry) * p.head_blocks + r.block] = make_int2(
-                static_cast<int>(blockIdx.x),
-                1 + static_cast<int>((static_cast<uint32_t>(left) + share.per - 1) / share.per));
-          k.finish(r, starts && left == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0),
-                   z, warps, stage);
-        }
+    }
+    if (i >= 0) {
+    const bool ends = r.step + 1 == r.n || i + 1 == steps;
+    if (ends || ++in_sum == kFlush) {
+      float z[2 * NT];
+      k.normalise(z);
+      if (!ends) {
+        k.put_aside(z);
+        in_sum = 0;
+      } else {
+        // a CTA leaves at most two partials: where an item ends or goes through (0)
+        // and where one begins (1); the latter knows how many there are
+        const bool starts = r.step <= i;
+        const int left = r.n - 1 - r.step;  // steps of the item in later shares
+        if (starts && threadIdx.x == 0)
+          p.pieces[static_cast<int64_t>(r.entry) * p.head_blocks + r.block] =
+              make_int2(static_cast<int>(blockIdx.x),
+                        1 + static_cast<int>((left + share.per - 1) / share.per));
+        k.finish(r, starts && left == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0),
+                 z, warps);
       }
+    }
     }
     // (scale words of the step before: nobody waits for them)
     if (i > -kStages) k.store_pending(stage ^ 1, pending);
@@ -1117,6 +1116,10 @@ csbp_status validate(const csbp_paged_problem* p, const csbp_kv_cache* c) {
   if (static_cast<int64_t>(p->table_pages) * c->page_size > 0x7fffffff - 1024)
     return CSBP_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(p->batch) * p->queries > 0x3fffffff / p->Hq)
+    return CSBP_ERR_UNSUPPORTED;
+  const int64_t keys = static_cast<int64_t>(p->table_pages) * c->page_size;
+  const Cut cut = cut_of(*p, *c);
+  if ((keys / (kKeys * cut.slices) + 3) * cut.head_blocks > 0x7fffffff / (cut.items / cut.head_blocks))
     return CSBP_ERR_UNSUPPORTED;
   return CSBP_OK;
 }
@@ -1251,6 +1254,8 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.row_tiles = cut.row_tiles;
   a.lanes = cut.head_blocks <= sms / 8 ? cut.head_blocks : 1;
   a.lane_ctas = sms / a.lanes;
+  a.lane_blocks = cut.head_blocks / a.lanes;
+  a.by_lanes = Divisor::of(static_cast<uint32_t>(a.lanes));
   a.wide_scales = aligned(cache->k_scale, 4) && aligned(cache->v_scale, 4) &&
                   cache->Hkv * (cache->d / kGroup) % 4 == 0;
   a.by_page = Divisor::of(static_cast<uint32_t>(cache->page_size));
