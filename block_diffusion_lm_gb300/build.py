@@ -25,7 +25,7 @@ LIB_DEBUG = os.path.join(PKG, "libcsbp_debug.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["schedule.cpp", "csbp_api.cu", "attn_fwd.cu", "attn_bwd.cu", "elementwise.cu",
            "noalloc.cu", "vocab_ce.cu", "kv_cache.cu", "cache_append.cu", "attn_paged.cu",
-           "attn_prefix.cu", "draft_verify.cu", "selftest.cu"]
+           "attn_paged_tiles.cu", "attn_prefix.cu", "draft_verify.cu", "selftest.cu"]
 
 
 def nvcc() -> str:

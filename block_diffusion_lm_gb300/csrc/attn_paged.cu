@@ -51,103 +51,23 @@
 #include "csbp_generate.h"
 #include "csbp_internal.h"
 #include "device_once.h"
-#include "divisor.cuh"
 #include "kv_cache.cuh"
+#include "paged_work.cuh"
 #include "ptx_sm100.cuh"
 
 namespace csbp {
 namespace {
 
+using namespace paged;
+
 constexpr size_t kStatusBytes = 256;
 constexpr int kMostWarps = 12;
 constexpr int kStages = 2;
 constexpr int kKeys = 32;     // of a warp's step, two MMAs
+constexpr int kMostRows = 16;  // of a head and sequence; more go to whole tiles
 constexpr int kFlush = 1024;  // steps that one accumulator takes in
 constexpr float kShift = 14.f;  // p is held as p 2^14; a row's maximum may lag by 2^1
 
-struct PagedParams {
-  int32_t pages, page_size, Hkv, table_pages;
-  const uint8_t *k, *v, *k_scale, *v_scale;
-  int32_t batch, queries, Hq, G, causal, window, sinks;
-  float scale_log2;
-  const __nv_bfloat16* q;
-  int64_t q_tok, q_bat;
-  const int32_t *table, *length;
-  __nv_bfloat16* o;
-  float* lse;
-  // how rows and heads are cut up
-  int32_t heads, slices, head_blocks;  // KV heads and slices of a CTA, CTAs' worth of heads
-  int32_t row_tiles;
-  // of the list: CTA c has share c / lanes of lane c % lanes, which takes every
-  // lanes-th block of heads
-  int32_t lanes, lane_ctas, lane_blocks;
-  int32_t wide_scales;  // scale bytes of a token are loaded in 4-byte words
-  Divisor by_page, by_G, by_row_tiles, by_lanes, by_step;  // (a step: the CTA's keys)
-  float* part_o;  // [2 x CTAs][heads][tile rows][d]
-  float* part_z;  // [2 x CTAs][heads][tile rows]
-  int2* pieces;   // per sequence, row tile and head block: first CTA, number of them
-  float* aside_o;  // [CTAs x warps][tile rows][d]: sums put aside
-  float* aside_z;  // [CTAs x warps][tile rows]
-};
-
-// ----------------------------------------------------------- instructions
-// Copies of `n` bytes (16 or 4), or as many zeros (n = 0: nothing is read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-// Two E4M3 codes (of the low or the high half of a word) as f16, exact, NaN as NaN.
-__device__ __forceinline__ uint32_t f16_low(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t f16_high(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // 8 x 8 f16 numbers, row g in lanes 4g .. 4g + 3: transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t r;
@@ -176,102 +96,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// ------------------------------------------------------------ the work list
-// The keys that a row tile reads: [0, first) and [lo, hi), in steps.
-struct Range {
-  int c;           // keys of the sequence
-  int first, lo, hi;
-  int n_first, n;  // steps: of [0, first), and all (at least one)
-};
-
-__device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile, int tile_rows) {
-  Range r;
-  r.c = min(max(__ldg(p.length + b), 0), p.table_pages * p.page_size);
-  const int i0 = p.by_G(tile * tile_rows);
-  const int i1 = p.by_G(min((tile + 1) * tile_rows, p.queries * p.G) - 1);
-  const int t0 = r.c - p.queries + i0, t1 = r.c - p.queries + i1;
-  r.hi = p.causal ? max(t1 + 1, 0) : r.c;
-  r.lo = p.window ? max(t0 - p.window + 1, 0) : 0;
-  r.lo = min(r.lo, r.hi);
-  r.first = p.window ? min(p.sinks, r.lo) : 0;
-  const int more = kKeys * p.slices - 1;
-  r.n_first = p.by_step(r.first + more);
-  r.n = max(r.n_first + static_cast<int>(p.by_step(r.hi - r.lo + more)), 1);
-  return r;
-}
-
-// A place in the list: entry (sequence, row tile), block of heads, step of it.
-struct Cursor {
-  int entry, block, step, b;
-  Range r;
-  __device__ __forceinline__ void load(const PagedParams& p, int tile_rows) {
-    b = p.by_row_tiles(entry);
-    if (b < p.batch) r = range_of(p, b, entry - b * p.row_tiles, tile_rows);
-  }
-};
-
-struct Share {
-  uint32_t begin, end, per;  // steps of the list (the host keeps it below 2^31)
-};
-
-// Adds all steps up and finds the CTA's share, and the cursor of its begin.
-// `room`: a number per warp, and at kMostWarps the cursor.
-template <int R>
-__device__ __forceinline__ Share find_share(const PagedParams& p, uint32_t* room, Cursor& cur) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int entries = p.batch * p.row_tiles;
-  Share s{0, 0, 0};
-  uint32_t total = 0;
-  // the total, then the begin; both at once where one sweep takes in all entries
-  const bool one_sweep = entries <= static_cast<int>(blockDim.x);
-#pragma unroll 1
-  for (int pass = one_sweep ? 1 : 0; pass < 2; ++pass) {
-    uint32_t before = 0;
-#pragma unroll 1
-    for (int e0 = 0; e0 < entries; e0 += blockDim.x) {
-      Cursor here{e0 + tid, 0, 0, 0, {}};
-      uint32_t mine = 0;
-      if (here.entry < entries) {
-        here.load(p, R);
-        mine = static_cast<uint32_t>(here.r.n) * p.lane_blocks;
-      }
-      uint32_t sum = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      if (!one_sweep) __syncthreads();
-      if (lane == 31) room[warp] = sum;
-      __syncthreads();
-      uint32_t all = 0;
-#pragma unroll 1
-      for (int w = 0; w < warps; ++w) {
-        if (w < warp) sum += room[w];
-        all += room[w];
-      }
-      if (one_sweep) total = all;
-      if (pass == 1) {
-        s.per = (total - 1) / p.lane_ctas + 1;
-        s.begin = min(s.per * p.by_lanes(blockIdx.x), total);
-        s.end = min(s.begin + s.per, total);
-        const uint32_t from = before + sum - mine;
-        if (s.begin >= from && s.begin < from + mine) {
-          const int passed = (s.begin - from) / here.r.n;
-          here.step = s.begin - from - passed * here.r.n;
-          here.block = passed * p.lanes + blockIdx.x - p.by_lanes(blockIdx.x) * p.lanes;
-          *reinterpret_cast<Cursor*>(room + kMostWarps) = here;
-        }
-      }
-      before += all;
-    }
-    total = before;
-  }
-  __syncthreads();
-  if (s.begin < s.end) cur = *reinterpret_cast<const Cursor*>(room + kMostWarps);
-  return s;
 }
 
 // Warps of a CTA, by its registers: 32 sums and 16 words of Q per lane and 8 rows.
@@ -319,14 +143,6 @@ __device__ __forceinline__ int key_of(int m) { return (m & 6) << 1 | (m & 1) | (
 // and the row of a key
 __device__ __forceinline__ int row_of_key(int r) { return (r >> 1 & 6) | (r & 1) | (r & 2) << 2; }
 
-// Sign bits of the bytes of a that are not below those of b.
-__device__ __forceinline__ uint32_t at_least_u8x4(uint32_t a, uint32_t b) {
-  const uint32_t t = (a | 0x80808080u) - (b & 0x7f7f7f7fu);
-  return ((a & ~b) | (~(a ^ b) & t)) & 0x80808080u;
-}
-__device__ __forceinline__ bool any_byte_255(uint32_t w) {
-  return ((~w - 0x01010101u) & w & 0x80808080u) != 0;
-}
 // Two scale bytes as fp32: 2^(byte - 127), 255 as NaN.
 __device__ __forceinline__ void two_scales(uint32_t w, float& lo, float& hi) {
   uint32_t r;
@@ -336,12 +152,6 @@ __device__ __forceinline__ void two_scales(uint32_t w, float& lo, float& hi) {
   lo = __uint_as_float(r << 16);
   hi = __uint_as_float(r & 0xffff0000u);
 }
-// Bytes of E4M3 NaN codes in a word, as 0xff.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return (m >> 7) * 0xffu;
-}
-
 // What a step is about, as the ring carries it.
 struct Record {
   uint32_t there;    // which of its keys are there
@@ -965,7 +775,7 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   Kernel<D, NT> k(p, warps + (threadIdx.x >> 5) * L::kWarpBytes);
   Cursor cursor{};
   const Share share =
-      find_share<L::kRows>(p, reinterpret_cast<uint32_t*>(smem), cursor);
+      find_share<L::kRows, kMostWarps>(p, reinterpret_cast<uint32_t*>(smem), cursor);
   if (share.begin >= share.end) return;
   const int steps = static_cast<int>(share.end - share.begin);
   Ahead next;
@@ -1027,26 +837,28 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   copies_wait<0>();
 }
 
-// Joins the partials of a row tile that was cut; a CTA per head of it.
-template <int D, int NT>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int kRows = Rows<D, NT>::kRows, kLanes = D / 4;
+// Joins the partials of a row tile that was cut; a CTA per head and 16 rows of it.
+template <int D>
+__global__ void __launch_bounds__(128)
+    paged_join_kernel(const __grid_constant__ PagedParams p, int tile_rows) {
+  constexpr int kLanes = D / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int item = blockIdx.x, head_in = blockIdx.y;
+  const int item = blockIdx.x, chunks = (tile_rows + 15) / 16;
+  const int head_in = blockIdx.y / chunks, from = (blockIdx.y - head_in * chunks) * 16;
   const int2 piece = p.pieces[item];
   if (piece.y <= 1) return;
   const int entry = item / p.head_blocks, block = item - entry * p.head_blocks;
   const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
   const int head = block * p.heads + head_in;
   if (head >= p.Hkv) return;
-  const int rows = min(kRows, p.queries * p.G - tile * kRows);
+  const int rows = min(min(tile_rows, from + 16), p.queries * p.G - tile * tile_rows) - from;
   for (int x = threadIdx.x; x < rows * kLanes; x += 128) {
-    const int row = x / kLanes, f = x % kLanes * 4;
+    const int row = from + x / kLanes, f = x % kLanes * 4;
     float most = -INFINITY, both = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // the first piece is where the item begins, the others are their CTAs' first
     const auto place = [&](int k) {
-      return (static_cast<int64_t>(2 * (piece.x + k * p.lanes) + (k == 0)) * p.heads + head_in) * kRows + row;
+      return (static_cast<int64_t>(2 * (piece.x + k * p.lanes) + (k == 0)) * p.heads + head_in) * tile_rows + row;
     };
 #pragma unroll 4
     for (int k = 0; k < piece.y; ++k) most = fmaxf(most, p.part_z[place(k)]);
@@ -1064,7 +876,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     }
     const float inv = both == 0.f ? 0.f : __fdividef(1.f, both);
     const float z = both == 0.f ? -INFINITY : ref + lg2_approx(both);
-    const int r = tile * kRows + row, i = p.by_G(r), h = head * p.G + r - i * p.G;
+    const int r = tile * tile_rows + row, i = p.by_G(r), h = head * p.G + r - i * p.G;
     const int64_t token = static_cast<int64_t>(b) * p.queries + i;
     *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -1077,15 +889,22 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 // How the heads and rows of a problem are cut up: H x S warps to a CTA, as many
 // as can be with as few heads of the last CTA missing.
 struct Cut {
-  int heads, slices, head_blocks, row_tiles, tile_rows;
+  int heads, slices, head_blocks, row_tiles, tile_rows, step_keys;
   int64_t items;
+  bool tiles;  // whole row tiles
 };
 
 Cut cut_of(const csbp_paged_problem& p, const csbp_kv_cache& c) {
   Cut r{};
   const int64_t rows = static_cast<int64_t>(p.queries) * (p.Hq / c.Hkv);
-  r.tile_rows = rows <= 8 ? 8 : 16;
+  r.tiles = rows > kMostRows;
+  r.tile_rows = r.tiles ? kPairRows : rows <= 8 ? 8 : 16;
   r.row_tiles = static_cast<int>((rows + r.tile_rows - 1) / r.tile_rows);
+  r.items = static_cast<int64_t>(p.batch) * r.row_tiles * c.Hkv;
+  r.heads = r.slices = 1;
+  r.head_blocks = c.Hkv;
+  r.step_keys = kTileKeys;
+  if (r.tiles) return r;
   const int most = most_warps(r.tile_rows / 8);
   double best = 0;
   for (int h = 1; h <= std::min(most, c.Hkv); ++h) {
@@ -1099,6 +918,7 @@ Cut cut_of(const csbp_paged_problem& p, const csbp_kv_cache& c) {
     }
   }
   r.items = static_cast<int64_t>(p.batch) * r.row_tiles * r.head_blocks;
+  r.step_keys = kKeys * r.slices;
   return r;
 }
 
@@ -1119,7 +939,7 @@ csbp_status validate(const csbp_paged_problem* p, const csbp_kv_cache* c) {
     return CSBP_ERR_UNSUPPORTED;
   const int64_t keys = static_cast<int64_t>(p->table_pages) * c->page_size;
   const Cut cut = cut_of(*p, *c);
-  if ((keys / (kKeys * cut.slices) + 3) * cut.head_blocks > 0x7fffffff / (cut.items / cut.head_blocks))
+  if ((keys / cut.step_keys + 3) * cut.head_blocks > 0x7fffffff / (cut.items / cut.head_blocks))
     return CSBP_ERR_UNSUPPORTED;
   return CSBP_OK;
 }
@@ -1149,7 +969,7 @@ Places places(const Cut& cut, int d, int sms) {
 }
 
 template <int D, int NT>
-cudaError_t launch(const PagedParams& p, const Cut& cut, int sms, cudaStream_t stream) {
+cudaError_t launch(const PagedParams& p, const Cut& cut, cudaStream_t stream) {
   using L = Rows<D, NT>;
   static PerDeviceOnce configured;
   int dev = 0;
@@ -1163,24 +983,23 @@ cudaError_t launch(const PagedParams& p, const Cut& cut, int sms, cudaStream_t s
       }))
     return e != cudaSuccess ? e : cudaErrorInvalidDevice;
   const int warps = cut.heads * cut.slices;
-  const int timed = timer_begin(13, stream);
   paged_rows_kernel<D, NT><<<p.lanes * p.lane_ctas, warps * 32, L::smem(warps), stream>>>(p);
-  e = cudaGetLastError();
-  timer_end(timed, stream);
-  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t join(const PagedParams& p, const Cut& cut, int d, cudaStream_t stream) {
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(cut.items), static_cast<unsigned>(cut.heads));
+  cfg.gridDim = dim3(static_cast<unsigned>(cut.items),
+                     static_cast<unsigned>(cut.heads * ((cut.tile_rows + 15) / 16)));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  const int joined = timer_begin(14, stream);
-  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT>, p);
-  timer_end(joined, stream);
-  return e;
+  return d == 128 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<128>, p, cut.tile_rows)
+                  : cudaLaunchKernelEx(&cfg, paged_join_kernel<64>, p, cut.tile_rows);
 }
 
 }  // namespace
@@ -1261,7 +1080,9 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.by_page = Divisor::of(static_cast<uint32_t>(cache->page_size));
   a.by_G = Divisor::of(static_cast<uint32_t>(a.G));
   a.by_row_tiles = Divisor::of(static_cast<uint32_t>(cut.row_tiles));
-  a.by_step = Divisor::of(static_cast<uint32_t>(kKeys * cut.slices));
+  a.step_keys = cut.step_keys;
+  a.by_step = Divisor::of(static_cast<uint32_t>(cut.step_keys));
+  a.status = static_cast<int*>(workspace);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + kStatusBytes);
   a.part_z = reinterpret_cast<float*>(ws + at.part_z);
@@ -1271,9 +1092,16 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const auto run = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    return cut.tile_rows == 8 ? launch<D, 1>(a, cut, sms, s) : launch<D, 2>(a, cut, sms, s);
+    return cut.tile_rows == 8 ? launch<D, 1>(a, cut, s) : launch<D, 2>(a, cut, s);
   };
-  const cudaError_t e = cache->d == 128 ? run(std::integral_constant<int, 128>())
-                                        : run(std::integral_constant<int, 64>());
+  const int timed = timer_begin(13, stream);
+  cudaError_t e = cut.tiles         ? launch_tiles(a, cache->d, s)
+                  : cache->d == 128 ? run(std::integral_constant<int, 128>())
+                                    : run(std::integral_constant<int, 64>());
+  timer_end(timed, stream);
+  if (e != cudaSuccess) return CSBP_ERR_CUDA;
+  const int joined = timer_begin(14, stream);
+  e = join(a, cut, cache->d, s);
+  timer_end(joined, stream);
   return e == cudaSuccess ? CSBP_OK : CSBP_ERR_CUDA;
 }

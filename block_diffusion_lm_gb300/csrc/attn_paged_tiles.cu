@@ -1,0 +1,885 @@
+// Attention over the quantised paged K/V cache for more query rows than the warp
+// MMAs of attn_paged.cu carry (csbp_generate.h): blocks that are denoised, drafts of
+// wide groups, chunks of prompts; on tcgen05 with its accumulators in TMEM.
+//
+// Rows.  The query rows of one KV head of a sequence, (token, head of the group)
+// flattened, in row tiles of 128; a CTA works on two of them ("slots") against the
+// keys that any of their rows reads, in tiles of 128 keys.  A last single row tile
+// goes to both slots, which take the key tiles in turn and are joined at the end
+// (`alternate`).  The list of steps (a pair of row tiles, a key tile, a KV head) is
+// cut as in attn_paged.cu (paged_work.cuh), with as many partials and the same
+// joining kernel.
+//
+// Operands.  K, V and Q are f16 in shared memory, P f16 in TMEM, all under powers of
+// two that fp32 takes back: E4M3 codes are exact in f16, and so are their group
+// scales 2^(e - E) down to 2^-24, with E the largest scale byte of the K tile, and of
+// V the largest so far in the feature group (O is rescaled when it grows, as it is
+// when a row's maximum does).  An operand below 2^-31 of the largest beside it becomes
+// 0.  P is p 2^11, rounded to 2^-11 of itself (2^-36 of the row's largest at least).
+//
+// Keys.  Three converter warps look the pages up, copy codes and scale bytes to a
+// ring of five half tiles (cp.async, about 66 KB ahead) and write K and V as f16 into
+// the one 128-byte-swizzled tile that each has: S(t) of both slots is done long before
+// K(t + 1) is wanted, and P V(t) before V(t + 1).  One thread issues the MMAs, two
+// warpgroups do the softmax, a row per thread, as in the training forward.
+//
+// Keys that a row does not read are masked.  Where some row of the pair does not read
+// a key of a tile, NaN in V is written as 0 and remembered: the rows that read it are
+// marked when they are stored.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "csbp_internal.h"
+#include "device_once.h"
+#include "mbar_spin.cuh"
+#include "paged_work.cuh"
+#include "pair_math.cuh"
+#include "ptx_sm100.cuh"
+
+namespace csbp {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kConverters = 96;
+constexpr float kThreshold = 4.f;  // log2: a row's maximum may lag by that
+constexpr float kShift = 11.f;     // P = p 2^11
+constexpr int kHeadroom = 6;       // K and V operands: codes times up to 2^6
+constexpr int kFlush = 512;        // key tiles that one accumulator takes in
+constexpr int kHalves = 5;         // of the ring
+constexpr int kInfos = 8;
+
+template <int D>
+struct Tiles {
+  static constexpr int kTileBytes = kTile * D * 2;  // Q, K or V tile (f16)
+  static constexpr int kBoxBytes = kTile * 128;     // its 64-feature boxes
+  static constexpr int kHalf = kTile * D;           // codes
+  static constexpr int kQ = 0;                      // 2 slots
+  static constexpr int kK = kQ + 2 * kTileBytes;
+  static constexpr int kV = kK + kTileBytes;
+  static constexpr int kRing = kV + kTileBytes;
+  static constexpr int kWords = kRing + kHalves * kHalf;  // [3 tiles][K, V][key] scale words
+  static constexpr int kInfo = kWords + 3 * 2 * kTile * 4;
+  static constexpr int kBar = kInfo + kInfos * 64;
+  static constexpr int bQFull = 0;                  // [2] per slot
+  static constexpr int bKFull = 2, bKEmpty = 3, bVFull = 4, bVEmpty = 5;
+  static constexpr int bSFull = 6, bPFull = 8, bPvDone = 10;  // [2]
+  static constexpr int bDrain = 12, kBars = 13;
+  static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
+  static constexpr int kRedo = kMisc + 8;           // [kInfos] by item
+  static constexpr int kTop = kRedo + kInfos * 4;   // [3 warps][K, V] largest scale bytes
+  static constexpr int kSmem = kTop + 24;
+  static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
+};
+static_assert(Tiles<128>::kSmem <= 232448, "shared memory of a CTA");
+
+// What the converters leave about a tile, in shared memory.
+struct Info {
+  float k_factor;     // of S
+  uint32_t top;       // E of V
+  int j0;             // first key
+  int edge;           // some row does not read some key
+  uint32_t there[6];  // keys of warps 0 .. 2: 32 and 11 (10) each
+  uint32_t pad[6];
+};
+static_assert(sizeof(Info) == 64, "");
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4)                                   // D: f32; A and B: f16
+         | (static_cast<uint32_t>(b_mn_major) << 16)  // B major-ness
+         | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// True in one thread of a warp; keeps what it passes to MMAs in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+__device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+
+// A CTA's part of one item.
+struct Piece {
+  int b, head, tile;  // sequence, KV head, pair of row tiles
+  int k0, count, n;   // its steps, of the item's n
+  int rows;           // of the pair
+  bool alternate;
+};
+
+__device__ __forceinline__ Piece piece_of(const PagedParams& p, const Cursor& cur, int left) {
+  Piece x;
+  x.b = cur.b;
+  x.head = cur.block;
+  x.tile = cur.entry - cur.b * p.row_tiles;
+  x.k0 = cur.step;
+  x.n = cur.r.n;
+  x.count = min(cur.r.n - cur.step, left);
+  x.rows = min(kPairRows, p.queries * p.G - x.tile * kPairRows);
+  x.alternate = x.rows <= kTile;
+  return x;
+}
+__device__ __forceinline__ void next_item(const PagedParams& p, Cursor& cur) {
+  cur.step = 0;
+  cur.block += p.lanes;
+  if (cur.block < p.head_blocks) return;
+  cur.block -= p.lanes * p.lane_blocks;
+  ++cur.entry;
+  cur.load(p, kPairRows);
+}
+
+// First key of step k.
+__device__ __forceinline__ int key_of(const Range& r, int k) {
+  return k < r.n_first ? k * kTileKeys : r.lo + (k - r.n_first) * kTileKeys;
+}
+// Whether all rows of a pair read all of the keys j0 .. j0 + 127.
+__device__ __forceinline__ bool all_read(const PagedParams& p, const Range& r, int tile, int rows,
+                                         int j0) {
+  const int i0 = p.by_G(tile * kPairRows), i1 = p.by_G(tile * kPairRows + rows - 1);
+  const int hi = p.causal ? r.c - p.queries + i0 + 1 : r.c;
+  const int lo = p.window ? r.c - p.queries + i1 - p.window + 1 : 0;
+  return j0 + kTileKeys <= hi && (j0 >= lo || j0 + kTileKeys <= p.sinks);
+}
+
+// 2^(kHeadroom - delta) in f16, both halves; 0 below 2^-24, NaN for a byte of 255.
+__device__ __forceinline__ uint32_t operand_scale(int top, int byte) {
+  const int delta = top - byte;
+  const uint32_t h = byte == 255 ? 0x7fffu
+                     : delta <= kHeadroom + 14 ? static_cast<uint32_t>(kHeadroom + 15 - delta) << 10
+                     : delta <= kHeadroom + 24 ? 1u << (kHeadroom + 24 - delta)
+                                               : 0u;
+  return h | h << 16;
+}
+
+// ---------------------------------------------------------------- converters
+template <int D>
+struct Converter {
+  using L = Tiles<D>;
+  const PagedParams& p;
+  uint8_t* const smem;
+  const uint32_t mem;
+  const int warp, lane, tid;  // of the converters
+  const int first, count;     // key rows of the warp
+  // rows lane and lane + 32 of the tile that is being copied, and of the next
+  uint32_t row[2];
+  bool there[2];
+  int page[2], place[2];
+
+  __device__ __forceinline__ Converter(const PagedParams& p, uint8_t* smem)
+      : p(p), smem(smem), mem(smem_u32(smem)), warp(static_cast<int>(threadIdx.x >> 5) - 1),
+        lane(threadIdx.x & 31), tid(static_cast<int>(threadIdx.x) - 32), first(43 * warp),
+        count(warp < 2 ? 43 : 42) {}
+
+  __device__ __forceinline__ void look(const Cursor& cur) {
+    const int j0 = key_of(cur.r, cur.step);
+    const int end = cur.step < cur.r.n_first ? cur.r.first : cur.r.hi;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int m = lane + 32 * x, j = j0 + first + m, entry = p.by_page(j);
+      place[x] = j - entry * p.page_size;
+      page[x] = -1;
+      if (m < count && j < end)
+        page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
+    }
+  }
+
+  // Takes what was looked up for the tile at `cur`, and leaves a record of it.
+  __device__ __forceinline__ void take(const Cursor& cur, int t) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      there[x] = static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(p.pages);
+      row[x] = there[x] ? static_cast<uint32_t>(page[x] * p.page_size + place[x]) * p.Hkv + cur.block
+                        : 0;
+    }
+    const uint32_t w0 = __ballot_sync(0xffffffffu, there[0]);
+    const uint32_t w1 = __ballot_sync(0xffffffffu, there[1]);
+    Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
+    if (lane == 0) {
+      info.there[2 * warp] = w0;
+      info.there[2 * warp + 1] = w1;
+      if (warp == 0) {
+        const int j0 = key_of(cur.r, cur.step), tile = cur.entry - cur.b * p.row_tiles;
+        info.j0 = j0;
+        info.edge = !all_read(p, cur.r, tile, min(kPairRows, p.queries * p.G - tile * kPairRows), j0);
+      }
+    }
+    // scale bytes, with K's codes
+    const uint32_t words = mem + L::kWords + (t % 3) * (2 * kTile * 4);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int m = lane + 32 * x;
+      if (m >= count) continue;
+      const uint32_t to = words + (first + m) * 4;
+      const uint64_t at = static_cast<uint64_t>(row[x]) * (D / 32);
+      if (p.wide_scales) {
+        const int n = there[x] ? 4 : 0;
+        copy4(to, p.k_scale + (at & ~uint64_t(3)), n);
+        copy4(to + kTile * 4, p.v_scale + (at & ~uint64_t(3)), n);
+      } else {
+        uint32_t k = 0, v = 0;
+        if (there[x])
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            k |= static_cast<uint32_t>(__ldg(p.k_scale + at + e)) << 8 * e;
+            v |= static_cast<uint32_t>(__ldg(p.v_scale + at + e)) << 8 * e;
+          }
+        sts32(to, k);
+        sts32(to + kTile * 4, v);
+      }
+    }
+  }
+
+  // Starts the copies of K's or V's codes of the tile taken last.
+  __device__ __forceinline__ void copy(const uint8_t* codes, int half) const {
+    constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
+    const int chunk = lane % kChunks, r0 = lane / kChunks;
+    const uint8_t* src = codes + chunk * 16;
+    const uint32_t at = mem + L::kRing + half * L::kHalf;
+    const uint32_t is[2] = {__ballot_sync(0xffffffffu, there[0]),
+                            __ballot_sync(0xffffffffu, there[1])};
+#pragma unroll
+    for (int i = 0; i < (43 + kAtOnce - 1) / kAtOnce; ++i) {
+      const int m = i * kAtOnce + r0, x = i * kAtOnce / 32;
+      const uint64_t from = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row[x], m & 31)) * D;
+      if (m >= count) continue;
+      const int r = first + m;
+      copy16(at + r * D + (D == 128 ? chunk ^ (r & 1) << 2 : chunk) * 16, src + from,
+             is[x] >> (m & 31) & 1 ? 16 : 0);
+    }
+  }
+
+  // The scale bytes of a key (D = 64: its head's half of a word).
+  __device__ __forceinline__ uint32_t word(int t, int kv, int key, bool upper) const {
+    const uint32_t w = lds32(mem + L::kWords + ((t % 3) * 2 + kv) * (kTile * 4) + key * 4);
+    return D == 128 ? w : upper ? w >> 16 : w & 0xffffu;
+  }
+
+  // Largest scale bytes of a tile, a byte per group: K, V.
+  __device__ __forceinline__ uint2 largest(int t, bool upper) const {
+    uint32_t k = 0, v = 0;
+    for (int key = tid; key < kTile; key += kConverters) {
+      uint32_t a = word(t, 0, key, upper), b = word(t, 1, key, upper);
+      if (any_byte_255(a) || any_byte_255(b)) {
+        a &= ~__vcmpeq4(a, 0xffffffffu);
+        b &= ~__vcmpeq4(b, 0xffffffffu);
+      }
+      k = __vmaxu4(k, a);
+      v = __vmaxu4(v, b);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      k = __vmaxu4(k, __shfl_xor_sync(0xffffffffu, k, o));
+      v = __vmaxu4(v, __shfl_xor_sync(0xffffffffu, v, o));
+    }
+    uint2* all = reinterpret_cast<uint2*>(smem + L::kTop);
+    if (lane == 0) all[warp] = make_uint2(k, v);
+    converters_sync();
+    k = __vmaxu4(__vmaxu4(all[0].x, all[1].x), all[2].x);
+    v = __vmaxu4(__vmaxu4(all[0].y, all[1].y), all[2].y);
+    return make_uint2(k, v);
+  }
+
+  // Codes of half tile `half` to f16 in the operand tile at `tile`, under E `top`.
+  // `edge`: NaN is written as 0; whether there was any.
+  __device__ __forceinline__ bool convert(int half, int t, int kv, bool upper, uint32_t top,
+                                          uint32_t tile, bool edge) const {
+    const uint32_t from = mem + L::kRing + half * L::kHalf;
+    const uint32_t bytes = mem + L::kWords + ((t % 3) * 2 + kv) * (kTile * 4) + (upper ? 2 : 0);
+    constexpr int kAtOnce = D == 128 ? 4 : 8;
+    const int c = D == 128 ? (lane & 3) | lane >> 4 << 2 : lane & 3;
+    const int r0 = D == 128 ? lane >> 2 & 3 : lane >> 2;
+    const int e = static_cast<int>(top >> 8 * (c >> 1) & 255);
+    bool found = false;
+#pragma unroll 2
+    for (int q = warp; q < kTile / kAtOnce; q += 3) {
+      const int r = q * kAtOnce + r0;
+      uint32_t w[4], byte;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(from + r * D + (D == 128 ? c ^ (r & 1) << 2 : c) * 16)
+                   : "memory");
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(bytes + r * 4 + (c >> 1)) : "memory");
+      if (edge) {
+        const uint32_t bad[4] = {nan_codes(w[0]), nan_codes(w[1]), nan_codes(w[2]), nan_codes(w[3])};
+        if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0 || byte == 255) {
+          found = true;
+          if (byte == 255) byte = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] &= ~bad[k];
+        }
+      }
+      const uint32_t s = operand_scale(e, static_cast<int>(byte));
+      uint32_t h[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[2 * k] = mul_f16x2(f16_low(w[k]), s);
+        h[2 * k + 1] = mul_f16x2(f16_high(w[k]), s);
+      }
+      const uint32_t to = tile + (c >> 2) * L::kBoxBytes + sw128_offset(r, 2 * (c & 3));
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                   "r"(h[3])
+                   : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(h[4]), "r"(h[5]),
+                   "r"(h[6]), "r"(h[7])
+                   : "memory");
+    }
+    return found;
+  }
+
+  // All tiles of the share.  A wait that gives up is passed over: the other waits
+  // give up too, and the results are void.
+  __device__ __forceinline__ void run(Cursor cur, int steps, uint64_t* bars, int* abort_flag) {
+    // `ahead` is the tile whose copies start, `cur` the one that is converted
+    Cursor ahead = cur, taken = cur;
+    int left = steps, head = cur.block, item = 0;
+    bool fresh = true;
+    const auto go_on = [&](Cursor& c) {
+      if (++c.step == c.r.n) next_item(p, c);
+    };
+    look(ahead);
+    uint32_t top = 0;
+    volatile int* redo = reinterpret_cast<volatile int*>(smem + L::kRedo);
+    int issued = 0;  // half tiles
+    const auto issue = [&] {
+      if (issued < 2 * steps) {
+        const int t = issued >> 1;
+        if ((issued & 1) == 0) {
+          taken = ahead;
+          take(taken, t);
+          copy(p.k, issued % kHalves);
+        } else {
+          copy(p.v, issued % kHalves);
+          if (t + 1 < steps) {
+            go_on(ahead);
+            look(ahead);
+          }
+        }
+      }
+      ++issued;
+      copies_commit();
+    };
+#pragma unroll 1
+    for (int h = 0; h < kHalves - 1; ++h) issue();
+#pragma unroll 1
+    for (int t = 0; left > 0; ++t, --left) {
+      const bool upper = D == 64 && p.wide_scales && (head & 1);
+      // ------- K
+      copies_wait<kHalves - 2>();
+      converters_sync();
+      issue();
+      const uint2 most = largest(t, upper);
+      uint32_t k_top = __vmaxu4(most.x, most.x >> 16);
+      k_top = max(k_top & 255, k_top >> 8 & 255);
+      top = fresh ? most.y : __vmaxu4(top, most.y);
+      Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
+      if (tid == 0) {
+        // 2^(E - 127 - headroom); (not 0: a masked score times it has to stay -inf)
+        info.k_factor = ldexpf(1.f, static_cast<int>(k_top) - 127 - kHeadroom);
+        info.top = top;
+        if (fresh) redo[item % kInfos] = 0;
+      }
+      if (t > 0) mbar_wait_warp(&bars[L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
+      convert((2 * t) % kHalves, t, 0, upper, k_top * 0x01010101u, mem + L::kK, false);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::bKFull]);
+      // ------- V
+      copies_wait<kHalves - 2>();
+      converters_sync();
+      const bool edge = info.edge || info.there[0] != ~0u || info.there[2] != ~0u ||
+                        info.there[4] != ~0u || info.there[1] != 0x7ffu ||
+                        info.there[3] != 0x7ffu || info.there[5] != 0x3ffu;
+      issue();
+      if (t > 0) mbar_wait_warp(&bars[L::bVEmpty], (t - 1) & 1, p.status, abort_flag);
+      if (convert((2 * t + 1) % kHalves, t, 1, upper, top, mem + L::kV, edge))
+        redo[item % kInfos] = 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::bVFull]);
+      // ------- on
+      fresh = cur.step + 1 == cur.r.n;
+      go_on(cur);
+      if (fresh) ++item;
+      head = cur.block;
+    }
+    copies_wait<0>();
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tiles_kernel(const __grid_constant__ PagedParams p) {
+  using L = Tiles<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need a 1024-aligned window
+    if (threadIdx.x == 0) atomicExch(p.status, DEV_MISALIGNED);
+    return;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
+
+  Cursor cur{};
+  const Share share =
+      find_share<kPairRows, kThreads / 32>(p, reinterpret_cast<uint32_t*>(smem), cur);
+  if (share.begin >= share.end) return;
+  const int steps = static_cast<int>(share.end - share.begin);
+  if (threadIdx.x == 0) {
+    // arrivals: converter warps, a slot's softmax warps, else one commit
+    for (int i = 0; i < L::kBars; ++i) {
+      const bool softmax = (i >= L::bQFull && i < L::bQFull + 2) || (i >= L::bPFull && i < L::bPFull + 2);
+      mbar_init(&bars[i], softmax ? 4 : i == L::bKFull || i == L::bVFull ? 3 : 1);
+    }
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_base_sh, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_base_sh;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      // ===================== MMA issuer
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
+      bool ok = true;
+      int npv[2] = {0, 0}, nq[2] = {0, 0};  // P V issued and Q tiles taken per slot
+      int in_sum[2] = {0, 0};               // key tiles in the accumulator
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kV), L::kBoxBytes, 1024);  // MN-major
+      // S_s = Q K^T of Q tile sq
+      auto issue_s = [&](int s, int sq) -> bool {
+        if (npv[s] > 0 &&
+            !mbar_wait_spin(&bars[L::bPvDone + s], (npv[s] - 1) & 1, p.status, abort_flag))
+          return false;  // its last P V still reads the P held there
+        tc_fence_after_sync();
+        const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQ + sq * L::kTileBytes), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
+          umma_bf16_ss(tmem + s * 128, sdesc_step(q_desc, off), sdesc_step(k_desc, off), idesc_s,
+                       k > 0 ? 1u : 0u);
+        }
+        umma_commit(&bars[L::bSFull + s]);
+        return true;
+      };
+      // O_s += P_s V
+      auto issue_pv = [&](int s) -> bool {
+        if (!mbar_wait_spin(&bars[L::bPFull + s], npv[s] & 1, p.status, abort_flag)) return false;
+        tc_fence_after_sync();
+        const uint32_t acc0 = in_sum[s] > 0 ? 1u : 0u;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_bf16_ts(tmem + L::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(v_desc, k * 2048),
+                       idesc_pv, k > 0 ? 1u : acc0);
+        umma_commit(&bars[L::bPvDone + s]);
+        ++npv[s];
+        if (++in_sum[s] == kFlush) in_sum[s] = 0;
+        return true;
+      };
+      int t = 0;  // key tiles so far
+      for (int left = steps; ok && left > 0;) {
+        const Piece x = piece_of(p, cur, left);
+        ok = mbar_wait(&bars[L::bQFull], nq[0]++ & 1, p.status, abort_flag);
+        if (ok && !x.alternate)
+          ok = mbar_wait(&bars[L::bQFull + 1], nq[1]++ & 1, p.status, abort_flag);
+        in_sum[0] = in_sum[1] = 0;
+        for (int m = 0; ok && m <= x.count; ++m) {
+          const bool more = m < x.count;
+          if (x.alternate) {
+            // S runs under the softmax of the tile before
+            const int s = m & 1;
+            if (more) {
+              ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag) &&
+                   issue_s(s, 0);
+              if (ok) umma_commit(&bars[L::bKEmpty]);
+            }
+            if (ok && m > 0) {
+              ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag) &&
+                   issue_pv(1 - s);
+              if (ok) umma_commit(&bars[L::bVEmpty]);
+            }
+          } else {
+            // each slot's softmax runs under the other's MMAs
+            if (m > 0)
+              ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag) &&
+                   issue_pv(0);
+            if (ok && more)
+              ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag) &&
+                   issue_s(0, 0);
+            if (ok && m > 0) {
+              ok = issue_pv(1);
+              if (ok) umma_commit(&bars[L::bVEmpty]);
+            }
+            if (ok && more) {
+              ok = issue_s(1, 1);
+              if (ok) umma_commit(&bars[L::bKEmpty]);
+            }
+          }
+        }
+        t += x.count;
+        left -= x.count;
+        if (left > 0) next_item(p, cur);
+      }
+      // drain every MMA this thread issued before the CTA may free TMEM
+      umma_commit(&bars[L::bDrain]);
+      mbar_wait(&bars[L::bDrain], 0, nullptr, nullptr, 500000000ull);
+    }
+  } else if (warp < 4) {
+    Converter<D>(p, smem).run(cur, steps, bars, abort_flag);
+  } else {
+    // ===================== softmax warpgroup of slot s
+    const int s = (warp - 4) >> 2;
+    const int row = threadIdx.x - 128 * (1 + s);
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t colS = s * 128, colO = L::kColO + s * D;
+    bool ok = true;
+    int n_s = 0;  // key tiles of this slot so far
+    int t0 = 0;   // key tiles so far
+    int item = 0;
+    float* const aside_o = p.aside_o + static_cast<int64_t>(blockIdx.x) * kPairRows * D;
+    float* const aside_z = p.aside_z + static_cast<int64_t>(blockIdx.x) * kPairRows;
+    for (int left = steps; left > 0; ++item) {
+      const Piece x = piece_of(p, cur, left);
+      const int total = p.queries * p.G;
+      const int row0 = x.tile * kPairRows + (x.alternate ? 0 : s * kTile);
+      const bool has_rows = row0 + (warp & 3) * 32 < total;  // warp-uniform
+      const bool row_valid = row0 + row < total;
+      const int r = min(row0 + row, total - 1);
+      const int qi = p.by_G(r), h = x.head * p.G + r - qi * p.G;
+      const int at = cur.r.c - p.queries + qi;
+      const int row_hi = p.causal ? at + 1 : cur.r.c, row_lo = p.window ? at - p.window + 1 : 0;
+      // ------- the row of Q, its largest element as 2^7 .. 2^8
+      float row_scale = 0.f;
+      if (has_rows) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(p.q + x.b * p.q_bat + qi * p.q_tok + static_cast<int64_t>(h) * D);
+        uint4 raw[D / 8];
+        uint32_t most = 0;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) raw[k] = __ldg(src + k);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+        }
+        const int ex = max(static_cast<int>(most >> 7) - 127, -110);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
+        row_scale = p.scale_log2 * ldexpf(1.f, ex - 7);
+        if (s == 0 || !x.alternate) {
+          uint8_t* q = smem + L::kQ + s * L::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+            *reinterpret_cast<uint4*>(q + (k >> 3) * L::kBoxBytes + sw128_offset(row, k & 7)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          fence_proxy_async_smem();
+        }
+      }
+      if (s == 0 || !x.alternate) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      uint32_t top = 0;
+      int in_sum = 0;
+      bool aside = false;
+
+      // What has been summed as normalised O and LSE (log2), joined with what was put
+      // aside (`with`: rows of that buffer); `use(c, o)` gets 32 features at a time.
+      // Whole warps.
+      const auto read_sum = [&](bool own, bool other, auto use) -> float {
+        tc_fence_after_sync();
+        float z = in_sum == 0 || l == 0.f ? -INFINITY : m_ref - kShift + log2f(l);
+        const float z_own = own ? aside_z[s * kTile + row] : -INFINITY;
+        const float z_other = other ? aside_z[kTile + row] : -INFINITY;
+        const float most = fmaxf(z, fmaxf(z_own, z_other)), ref = most == -INFINITY ? 0.f : most;
+        float w = exp2f(z - ref), w_own = exp2f(z_own - ref), w_other = exp2f(z_other - ref);
+        const float all = w + w_own + w_other, inv = all == 0.f ? 0.f : 1.f / all;
+        const float inv_l = in_sum == 0 || l == 0.f ? 0.f : 1.f / l;
+        w *= inv;
+        w_own *= inv;
+        w_other *= inv;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          if (in_sum > 0) tmem_ld32(tmem + lane_base + colO + c * 32, o);
+          // 2^(E - 127 - headroom), in two steps: one could lie below fp32's range
+          const int ex = static_cast<int>(top >> 8 * c & 255);
+          const float f0 = __uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23) * inv_l;
+          const float f1 =
+              __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63 - kHeadroom) << 23);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            o[i] = in_sum > 0 && z != -INFINITY ? o[i] * f0 * f1 : 0.f;
+            if (own || other) o[i] = z != -INFINITY ? o[i] * w : 0.f;
+          }
+          if (own && z_own != -INFINITY) {
+            const float4* v = reinterpret_cast<const float4*>(aside_o + (s * kTile + row) * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = v[i];
+              o[4 * i] = fmaf(y.x, w_own, o[4 * i]);
+              o[4 * i + 1] = fmaf(y.y, w_own, o[4 * i + 1]);
+              o[4 * i + 2] = fmaf(y.z, w_own, o[4 * i + 2]);
+              o[4 * i + 3] = fmaf(y.w, w_own, o[4 * i + 3]);
+            }
+          }
+          if (other && z_other != -INFINITY) {
+            const float4* v = reinterpret_cast<const float4*>(aside_o + (kTile + row) * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = v[i];
+              o[4 * i] = fmaf(y.x, w_other, o[4 * i]);
+              o[4 * i + 1] = fmaf(y.y, w_other, o[4 * i + 1]);
+              o[4 * i + 2] = fmaf(y.z, w_other, o[4 * i + 2]);
+              o[4 * i + 3] = fmaf(y.w, w_other, o[4 * i + 3]);
+            }
+          }
+          use(c, o);
+        }
+        return all == 0.f ? -INFINITY : ref + log2f(all);
+      };
+      const auto put_aside = [&](bool own) {
+        const float z = read_sum(own, false, [&](int c, const float (&o)[32]) {
+          float4* to = reinterpret_cast<float4*>(aside_o + (s * kTile + row) * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        });
+        aside_z[s * kTile + row] = z;
+      };
+      // the last P V of this slot
+      const auto last_done = [&] {
+        if (n_s > 0 && ok)
+          ok = mbar_wait_warp(&bars[L::bPvDone + s], (n_s - 1) & 1, p.status, abort_flag);
+      };
+
+#pragma unroll 1
+      for (int m = x.alternate ? s : 0; ok && m < x.count; m += x.alternate ? 2 : 1) {
+        if (in_sum == kFlush) {
+          last_done();
+          if (!ok) break;
+          if (has_rows) put_aside(aside);
+          tc_fence_before_sync();
+          aside = true;
+          in_sum = 0;
+          m_ref = -INFINITY;
+          l = 0.f;
+        }
+        if (!mbar_wait_warp(&bars[L::bSFull + s], n_s & 1, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++n_s;
+        if (!has_rows) {  // nothing to do, but the MMA counts four warps
+          ++in_sum;
+          if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
+          continue;
+        }
+        tc_fence_after_sync();
+        const Info& info = reinterpret_cast<const Info*>(smem + L::kInfo)[(t0 + m) % kInfos];
+        // (not 0: a masked score times it has to stay -inf)
+        const float mult = fmaxf(row_scale * info.k_factor, 1e-37f);
+        float sv[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile / 32; c += 2)
+          tmem_ld32x2(tmem + lane_base + colS + c * 32, tmem + lane_base + colS + (c + 1) * 32,
+                      sv + c * 32, sv + (c + 1) * 32);
+        const uint32_t a0 = info.there[0], b0 = info.there[1], a1 = info.there[2],
+                       b1 = info.there[3], a2 = info.there[4], b2 = info.there[5];
+        if (info.edge || (a0 & a1 & a2) != ~0u || b0 != 0x7ffu || b1 != 0x7ffu || b2 != 0x3ffu) {
+          const uint32_t there[4] = {a0, b0 | a1 << 11, a1 >> 21 | b1 << 11 | a2 << 22,
+                                     a2 >> 10 | b2 << 22};
+          const auto below = [&](int j, int q) -> uint32_t {  // keys of word q before j
+            const int n = min(max(j - info.j0 - 32 * q, 0), 32);
+            return n == 32 ? ~0u : (1u << n) - 1;
+          };
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t reads =
+                there[q] & below(row_hi, q) & (~below(row_lo, q) | (p.window ? below(p.sinks, q) : 0u));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              sv[32 * q + c] = reads >> c & 1 ? sv[32 * q + c] : -INFINITY;
+          }
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 2) mx4[c / 2 % 4] = fmax3(mx4[c / 2 % 4], sv[c], sv[c + 1]);
+        const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
+        const float m_new = fmaxf(m_ref, mx * mult);
+        const bool need = m_new > m_ref + kThreshold;  // false while both are -inf
+        const uint32_t now = info.top;
+        if (in_sum > 0 && (now != top || __any_sync(0xffffffffu, need))) {
+          // O holds the P V so far, under the old maximum and E (its last P V is done:
+          // this S was issued after it)
+          const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            const int by = static_cast<int>((now >> 8 * c & 255) - (top >> 8 * c & 255));
+            const float f =
+                alpha * (by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23) : 0.f);
+            float o[32];
+            tmem_ld32(tmem + lane_base + colO + c * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(tmem + lane_base + colO + c * 32, o);
+          }
+        }
+        top = now;
+        if (need) {
+          l *= exp2f(m_ref - m_new);  // 0 when m_ref was -inf
+          m_ref = m_new;
+        }
+        const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - kShift;
+        const uint64_t mult2 = f2_pack(mult, mult), neg = f2_pack(-ref, -ref);
+        uint64_t rs2 = f2_pack(0.f, 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float packed[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(sv[half * 64 + 2 * c], sv[half * 64 + 2 * c + 1]), mult2, neg),
+                      x0, x1);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+            rs2 = f2_add(rs2, f2_pack(e0, e1));
+            packed[c] = __uint_as_float(pack_f16(e0, e1));
+          }
+          tmem_st32(tmem + lane_base + colS + half * 32, packed);
+        }
+        float rs0, rs1;
+        f2_unpack(rs2, rs0, rs1);
+        l += rs0 + rs1;
+        ++in_sum;
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
+      }
+      last_done();
+      // ------- the piece's end
+      const int later = x.n - x.k0 - x.count;  // steps of the item in later shares
+      const bool starts = x.k0 == 0;
+      if (starts && threadIdx.x == 128)
+        p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
+            make_int2(static_cast<int>(blockIdx.x),
+                      1 + static_cast<int>((later + share.per - 1) / share.per));
+      if (x.alternate && s == 1 && ok && has_rows) {
+        put_aside(aside);
+        __threadfence_block();
+      }
+      if (x.alternate) softmax_sync();
+      if (ok && has_rows && (s == 0 || !x.alternate)) {
+        const int part = starts && later == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+        const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
+        // NaN in V that was kept out of the products
+        const auto nan_at = [&](int c) -> uint32_t {  // features of chunk c, a bit each
+          uint32_t bad = 0;
+          for (int k = x.k0; k < x.k0 + x.count; ++k) {
+            const int j0 = key_of(cur.r, k), end = k < cur.r.n_first ? cur.r.first : cur.r.hi;
+            for (int j = j0; j < min(j0 + kTileKeys, end); ++j) {
+              if (!(j < row_hi && (j >= row_lo || j < p.sinks))) continue;
+              const int entry = p.by_page(j);
+              const int pg = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_pages + entry);
+              if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) continue;
+              const uint64_t slot = static_cast<uint32_t>(pg * p.page_size + j - entry * p.page_size);
+              const uint64_t place = slot * p.Hkv + x.head;
+              if (__ldg(p.v_scale + place * (D / 32) + c) == 255) bad = ~0u;
+              for (int i = 0; i < 32; ++i)
+                if ((__ldg(p.v + place * D + c * 32 + i) & 0x7f) == 0x7f) bad |= 1u << i;
+            }
+          }
+          return bad;
+        };
+        const int64_t token = static_cast<int64_t>(x.b) * p.queries + qi;
+        const int64_t place = static_cast<int64_t>(part) * kPairRows + (x.alternate ? 0 : s * kTile) + row;
+        const float z = read_sum(aside, x.alternate, [&](int c, float (&o)[32]) {
+          if (redo) {
+            const uint32_t bad = row_valid ? nan_at(c) : 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (bad >> i & 1) o[i] = NAN;
+          }
+          if (!row_valid) return;
+          if (part < 0) {
+            uint4* to = reinterpret_cast<uint4*>(p.o + (token * p.Hq + h) * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                 pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                 pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                 pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          } else {
+            float4* to = reinterpret_cast<float4*>(p.part_o + place * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        });
+        if (row_valid) {
+          if (part < 0)
+            p.lse[(static_cast<int64_t>(x.b) * p.Hq + h) * p.queries + qi] = z * 0.6931471805599453f;
+          else
+            p.part_z[place] = z;
+        }
+      }
+      tc_fence_before_sync();
+      if (x.alternate) softmax_sync();  // slot 1's sum has been read
+      t0 += x.count;
+      left -= x.count;
+      if (left > 0) next_item(p, cur);
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
+  static PerDeviceOnce configured;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!configured.run(dev, [&](int) {
+        e = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Tiles<D>::kSmem);
+        return e == cudaSuccess;
+      }))
+    return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  paged_tiles_kernel<D><<<p.lanes * p.lane_ctas, kThreads, Tiles<D>::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tiles(const PagedParams& p, int d, cudaStream_t stream) {
+  return d == 128 ? launch<128>(p, stream) : launch<64>(p, stream);
+}
+
+}  // namespace paged
+}  // namespace csbp
