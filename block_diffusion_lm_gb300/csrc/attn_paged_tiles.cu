@@ -50,6 +50,11 @@ constexpr int kHeadroom = 6;       // K and V operands: codes times up to 2^6
 constexpr int kFlush = 512;        // key tiles that one accumulator takes in
 constexpr int kHalves = 5;         // of the ring
 constexpr int kInfos = 8;
+// Per-warpgroup register budgets (setmaxnreg): issuer and converters, softmax.  Their
+// sum must not exceed the launch allocation (checked on the host).
+constexpr uint32_t kRegsLow = 112;
+constexpr uint32_t kRegsSoftmax = 192;
+constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsSoftmax;
 
 template <int D>
 struct Tiles {
@@ -70,7 +75,8 @@ struct Tiles {
   static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
   static constexpr int kRedo = kMisc + 8;           // [kInfos] by item
   static constexpr int kTop = kRedo + kInfos * 4;   // [3 warps][K, V] largest scale bytes
-  static constexpr int kSmem = kTop + 24;
+  static constexpr int kCursor = (kTop + 24 + 15) / 16 * 16;  // of each softmax warp
+  static constexpr int kSmem = kCursor + 8 * 48;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
 };
 static_assert(Tiles<128>::kSmem <= 232448, "shared memory of a CTA");
@@ -82,7 +88,9 @@ struct Info {
   int j0;             // first key
   int edge;           // some row does not read some key
   uint32_t there[6];  // keys of warps 0 .. 2: 32 and 11 (10) each
-  uint32_t pad[6];
+  int upper;          // scale bytes are the upper half of their words
+  int first;          // of a piece
+  uint32_t pad[4];
 };
 static_assert(sizeof(Info) == 64, "");
 
@@ -101,6 +109,24 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(yes));
   return yes != 0;
+}
+
+// 8 consecutive fp32 TMEM columns of this thread's lane, times f.
+__device__ __forceinline__ void tmem_scale8(uint32_t at, float f) {
+  float r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] *= f;
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+      "tcgen05.wait::st.sync.aligned;\n" ::"r"(at),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+      : "memory");
 }
 
 __device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
@@ -133,6 +159,37 @@ __device__ __forceinline__ void next_item(const PagedParams& p, Cursor& cur) {
   cur.block -= p.lanes * p.lane_blocks;
   ++cur.entry;
   cur.load(p, kPairRows);
+}
+
+// A warp's cursor while its registers hold scores.
+__device__ __forceinline__ void keep_cursor(uint32_t at, const Cursor& c) {
+  if ((threadIdx.x & 31) == 0) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(c.entry), "r"(c.block),
+                 "r"(c.step), "r"(c.b)
+                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + 16), "r"(c.r.c), "r"(c.r.first),
+                 "r"(c.r.lo), "r"(c.r.hi)
+                 : "memory");
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at + 32), "r"(c.r.n_first), "r"(c.r.n)
+                 : "memory");
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ Cursor kept_cursor(uint32_t at) {
+  Cursor c;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(c.entry), "=r"(c.block), "=r"(c.step), "=r"(c.b)
+               : "r"(at)
+               : "memory");
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(c.r.c), "=r"(c.r.first), "=r"(c.r.lo), "=r"(c.r.hi)
+               : "r"(at + 16)
+               : "memory");
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+               : "=r"(c.r.n_first), "=r"(c.r.n)
+               : "r"(at + 32)
+               : "memory");
+  return c;
 }
 
 // First key of step k.
@@ -191,7 +248,7 @@ struct Converter {
   }
 
   // Takes what was looked up for the tile at `cur`, and leaves a record of it.
-  __device__ __forceinline__ void take(const Cursor& cur, int t) {
+  __device__ __forceinline__ void take(const Cursor& cur, int t, bool piece_begins) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       there[x] = static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(p.pages);
@@ -207,6 +264,8 @@ struct Converter {
       if (warp == 0) {
         const int j0 = key_of(cur.r, cur.step), tile = cur.entry - cur.b * p.row_tiles;
         info.j0 = j0;
+        info.upper = D == 64 && p.wide_scales && (cur.block & 1);
+        info.first = piece_begins;
         info.edge = !all_read(p, cur.r, tile, min(kPairRows, p.queries * p.G - tile * kPairRows), j0);
       }
     }
@@ -297,7 +356,7 @@ struct Converter {
     const int r0 = D == 128 ? lane >> 2 & 3 : lane >> 2;
     const int e = static_cast<int>(top >> 8 * (c >> 1) & 255);
     bool found = false;
-#pragma unroll 2
+#pragma unroll 4
     for (int q = warp; q < kTile / kAtOnce; q += 3) {
       const int r = q * kAtOnce + r0;
       uint32_t w[4], byte;
@@ -333,85 +392,232 @@ struct Converter {
     return found;
   }
 
-  // All tiles of the share.  A wait that gives up is passed over: the other waits
-  // give up too, and the results are void.
-  __device__ __forceinline__ void run(Cursor cur, int steps, uint64_t* bars, int* abort_flag) {
-    // `ahead` is the tile whose copies start, `cur` the one that is converted
-    Cursor ahead = cur, taken = cur;
-    int left = steps, head = cur.block, item = 0;
-    bool fresh = true;
-    const auto go_on = [&](Cursor& c) {
-      if (++c.step == c.r.n) next_item(p, c);
-    };
-    look(ahead);
-    uint32_t top = 0;
+  // All tiles of the share, K and V of each in turn.  A wait that gives up is passed
+  // over: the other waits give up too, and the results are void.
+  __device__ __forceinline__ void run(Cursor& ahead, int steps, uint64_t* bars, int* abort_flag) {
     volatile int* redo = reinterpret_cast<volatile int*>(smem + L::kRedo);
-    int issued = 0;  // half tiles
-    const auto issue = [&] {
-      if (issued < 2 * steps) {
-        const int t = issued >> 1;
-        if ((issued & 1) == 0) {
-          taken = ahead;
-          take(taken, t);
-          copy(p.k, issued % kHalves);
-        } else {
-          copy(p.v, issued % kHalves);
-          if (t + 1 < steps) {
-            go_on(ahead);
-            look(ahead);
-          }
+    uint32_t top = 0, k_top = 0;
+    int item = -1, ring = 0, into = 0;  // half tiles that are converted and copied next
+    bool begins = true;
+    look(ahead);
+#pragma unroll 1
+    for (int h = 1 - kHalves; h < 2 * steps; ++h) {
+      if (h >= 0) {
+        copies_wait<kHalves - 2>();
+        converters_sync();
+      }
+      // ------- copies, four half tiles ahead
+      const int i = h + kHalves - 1;
+      if (i < 2 * steps) {
+        if ((i & 1) == 0) take(ahead, i >> 1, begins);
+        copy(i & 1 ? p.v : p.k, into);
+        if ((i & 1) && i + 1 < 2 * steps) {
+          begins = ++ahead.step == ahead.r.n;
+          if (begins) next_item(p, ahead);
+          look(ahead);
         }
       }
-      ++issued;
       copies_commit();
-    };
-#pragma unroll 1
-    for (int h = 0; h < kHalves - 1; ++h) issue();
-#pragma unroll 1
-    for (int t = 0; left > 0; ++t, --left) {
-      const bool upper = D == 64 && p.wide_scales && (head & 1);
-      // ------- K
-      copies_wait<kHalves - 2>();
-      converters_sync();
-      issue();
-      const uint2 most = largest(t, upper);
-      uint32_t k_top = __vmaxu4(most.x, most.x >> 16);
-      k_top = max(k_top & 255, k_top >> 8 & 255);
-      top = fresh ? most.y : __vmaxu4(top, most.y);
+      into = into + 1 == kHalves ? 0 : into + 1;
+      if (h < 0) continue;
+      // ------- conversion
+      const int t = h >> 1, kv = h & 1;
       Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
-      if (tid == 0) {
-        // 2^(E - 127 - headroom); (not 0: a masked score times it has to stay -inf)
-        info.k_factor = ldexpf(1.f, static_cast<int>(k_top) - 127 - kHeadroom);
-        info.top = top;
-        if (fresh) redo[item % kInfos] = 0;
+      const bool upper = D == 64 && info.upper;
+      if (kv == 0) {
+        const uint2 most = largest(t, upper);
+        k_top = __vmaxu4(most.x, most.x >> 16);
+        k_top = max(k_top & 255, k_top >> 8 & 255);
+        top = info.first ? most.y : __vmaxu4(top, most.y);
+        item += info.first;
+        if (tid == 0) {
+          // 2^(E - 127 - headroom)
+          info.k_factor = ldexpf(1.f, static_cast<int>(k_top) - 127 - kHeadroom);
+          info.top = top;
+          if (info.first) redo[item % kInfos] = 0;
+        }
       }
-      if (t > 0) mbar_wait_warp(&bars[L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
-      convert((2 * t) % kHalves, t, 0, upper, k_top * 0x01010101u, mem + L::kK, false);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::bKFull]);
-      // ------- V
-      copies_wait<kHalves - 2>();
-      converters_sync();
-      const bool edge = info.edge || info.there[0] != ~0u || info.there[2] != ~0u ||
-                        info.there[4] != ~0u || info.there[1] != 0x7ffu ||
-                        info.there[3] != 0x7ffu || info.there[5] != 0x3ffu;
-      issue();
-      if (t > 0) mbar_wait_warp(&bars[L::bVEmpty], (t - 1) & 1, p.status, abort_flag);
-      if (convert((2 * t + 1) % kHalves, t, 1, upper, top, mem + L::kV, edge))
+      const bool edge =
+          kv && (info.edge || (info.there[0] & info.there[2] & info.there[4]) != ~0u ||
+                 info.there[1] != 0x7ffu || info.there[3] != 0x7ffu || info.there[5] != 0x3ffu);
+      if (t > 0)
+        mbar_wait_warp(&bars[kv ? L::bVEmpty : L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
+      if (convert(ring, t, kv, upper, kv ? top : k_top * 0x01010101u, mem + (kv ? L::kV : L::kK), edge))
         redo[item % kInfos] = 1;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::bVFull]);
-      // ------- on
-      fresh = cur.step + 1 == cur.r.n;
-      go_on(cur);
-      if (fresh) ++item;
-      head = cur.block;
+      if (lane == 0) mbar_arrive(&bars[kv ? L::bVFull : L::bKFull]);
+      ring = ring + 1 == kHalves ? 0 : ring + 1;
     }
     copies_wait<0>();
   }
 };
+
+// ------------------------------------------------------------- softmax rows
+// What a softmax thread's row is.
+struct RowAt {
+  int i, h;    // query and head
+  int lo, hi;  // keys [lo, hi) of it, besides the sinks
+};
+__device__ __forceinline__ RowAt row_at(const PagedParams& p, const Piece& x, int c, int row) {
+  const int r = min(x.tile * kPairRows + row, p.queries * p.G - 1);
+  RowAt a;
+  a.i = p.by_G(r);
+  a.h = x.head * p.G + r - a.i * p.G;
+  const int at = c - p.queries + a.i;
+  a.hi = p.causal ? at + 1 : c;
+  a.lo = p.window ? at - p.window + 1 : 0;
+  return a;
+}
+
+// The row of Q as f16 with its largest element as 2^7 .. 2^8, to row `to` of the tile
+// at `tile` (if any); returns what its scores are to be multiplied by.
+template <int D>
+__device__ __noinline__ float load_query(const PagedParams& p, const Piece x, const RowAt a,
+                                         uint8_t* tile, int to) {
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + x.b * p.q_bat + a.i * p.q_tok +
+                                                    static_cast<int64_t>(a.h) * D);
+  uint4 raw[D / 8];
+  uint32_t most = 0;
+#pragma unroll
+  for (int k = 0; k < D / 8; ++k) raw[k] = __ldg(src + k);
+#pragma unroll
+  for (int k = 0; k < D / 8; ++k) {
+    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+  }
+  const int ex = max(static_cast<int>(most >> 7) - 127, -110);
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
+  if (tile) {
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k) {
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+      *reinterpret_cast<uint4*>(tile + (k >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to, k & 7)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  return p.scale_log2 * ldexpf(1.f, ex - 7);
+}
+
+// Features (of chunk c, a bit each) that are NaN in some key of the piece that the row
+// reads.
+template <int D>
+__device__ __noinline__ uint32_t nan_features(const PagedParams& p, const Piece x, const Range r,
+                                              const RowAt a, int c) {
+  uint32_t bad = 0;
+  for (int k = x.k0; k < x.k0 + x.count; ++k) {
+    const int j0 = key_of(r, k), end = k < r.n_first ? r.first : r.hi;
+    for (int j = j0; j < min(j0 + kTileKeys, end); ++j) {
+      if (!(j < a.hi && (j >= a.lo || j < p.sinks))) continue;
+      const int entry = p.by_page(j);
+      const int pg = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_pages + entry);
+      if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) continue;
+      const uint64_t slot = static_cast<uint32_t>(pg * p.page_size + j - entry * p.page_size);
+      const uint64_t place = slot * p.Hkv + x.head;
+      if (__ldg(p.v_scale + place * (D / 32) + c) == 255) bad = ~0u;
+      for (int i = 0; i < 32; ++i)
+        if ((__ldg(p.v + place * D + c * 32 + i) & 0x7f) == 0x7f) bad |= 1u << i;
+    }
+  }
+  return bad;
+}
+
+// What a row has summed.
+struct Sum {
+  float m, l;    // largest score (log2) and sum of P under it
+  uint32_t top;  // E of each feature group
+  int tiles;     // key tiles in the accumulator
+  bool aside;    // and earlier ones in `aside_o`, `aside_z`
+};
+
+// Stores a row's normalised O and its LSE, joined with what was put aside and, of an
+// alternate piece, with what slot 1 has left there.  To the outputs (`part` = -1), a
+// place among the partials, or aside (kAside).  Whole warps; `o_at` is the warp's O.
+constexpr int kAside = -2;
+template <int D>
+__device__ __noinline__ void store_sum(const PagedParams& p, const Piece x, const Range r,
+                                       const RowAt a, const Sum sum, uint32_t o_at, int s, int row,
+                                       int part, bool redo) {
+  tc_fence_after_sync();
+  float* const aside_o = p.aside_o + static_cast<int64_t>(blockIdx.x) * kPairRows * D;
+  float* const aside_z = p.aside_z + static_cast<int64_t>(blockIdx.x) * kPairRows;
+  const bool other = x.alternate && s == 0 && part != kAside, here = sum.tiles > 0;
+  const int mine = s * kTile + row, others = kTile + row;
+  const float z = here && sum.l != 0.f ? sum.m - kShift + log2f(sum.l) : -INFINITY;
+  const float z_mine = sum.aside ? aside_z[mine] : -INFINITY;
+  const float z_other = other ? aside_z[others] : -INFINITY;
+  const float most = fmaxf(z, fmaxf(z_mine, z_other)), ref = most == -INFINITY ? 0.f : most;
+  float w = exp2f(z - ref), w_mine = exp2f(z_mine - ref), w_other = exp2f(z_other - ref);
+  const float all = w + w_mine + w_other, inv = all == 0.f ? 0.f : 1.f / all;
+  // (NaN in the sum goes on to all of the row)
+  w = z == -INFINITY ? 0.f : w * inv / sum.l;
+  w_mine *= inv;
+  w_other *= inv;
+  const float lse = all == 0.f ? -INFINITY : ref + log2f(all);
+  const bool valid = x.tile * kPairRows + (x.alternate ? 0 : s * kTile) + row < p.queries * p.G;
+  const int64_t token = static_cast<int64_t>(x.b) * p.queries + a.i;
+  const int64_t place = static_cast<int64_t>(part) * kPairRows + (x.alternate ? 0 : s * kTile) + row;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    if (here) tmem_ld32(o_at + c * 32, o);
+    // 2^(E - 127 - headroom), in two steps: one could lie below fp32's range
+    const int ex = static_cast<int>(sum.top >> 8 * c & 255);
+    const float f0 = __uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23);
+    const float f1 = __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63 - kHeadroom) << 23);
+    const bool some = here && z != -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * w * f0 * f1 : 0.f;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      if (k == 0 ? z_mine == -INFINITY : z_other == -INFINITY) continue;
+      const float f = k == 0 ? w_mine : w_other;
+      const float4* v =
+          reinterpret_cast<const float4*>(aside_o + (k == 0 ? mine : others) * D + c * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 y = v[i];
+        o[4 * i] = fmaf(y.x, f, o[4 * i]);
+        o[4 * i + 1] = fmaf(y.y, f, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(y.z, f, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(y.w, f, o[4 * i + 3]);
+      }
+    }
+    if (redo) {
+      const uint32_t bad = valid ? nan_features<D>(p, x, r, a, c) : 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (bad >> i & 1) o[i] = NAN;
+    }
+    if (part == -1) {
+      if (!valid) continue;
+      uint4* to = reinterpret_cast<uint4*>(p.o + (token * p.Hq + a.h) * D + c * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                           pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                           pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+    } else {
+      float4* to = reinterpret_cast<float4*>(part == kAside ? aside_o + mine * D + c * 32
+                                                            : p.part_o + place * D + c * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+  }
+  if (part == kAside)
+    aside_z[mine] = lse;
+  else if (part >= 0)
+    p.part_z[place] = lse;
+  else if (valid)
+    p.lse[(static_cast<int64_t>(x.b) * p.Hq + a.h) * p.queries + a.i] = lse * 0.6931471805599453f;
+  tc_fence_before_sync();
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -452,6 +658,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_base_sh;
 
+  if (warp < 4)
+    setmaxnreg_dec<kRegsLow>();
+  else
+    setmaxnreg_inc<kRegsSoftmax>();
   if (warp == 0) {
     if (elect_one()) {
       // ===================== MMA issuer
@@ -552,124 +762,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_s = 0;  // key tiles of this slot so far
     int t0 = 0;   // key tiles so far
     int item = 0;
-    float* const aside_o = p.aside_o + static_cast<int64_t>(blockIdx.x) * kPairRows * D;
-    float* const aside_z = p.aside_z + static_cast<int64_t>(blockIdx.x) * kPairRows;
+    const uint32_t kept = smem_u32(smem + L::kCursor + (warp - 4) * 48);
+    keep_cursor(kept, cur);
+    const uint32_t s_at = tmem + lane_base + colS, o_at = tmem + lane_base + colO;
     for (int left = steps; left > 0; ++item) {
-      const Piece x = piece_of(p, cur, left);
-      const int total = p.queries * p.G;
-      const int row0 = x.tile * kPairRows + (x.alternate ? 0 : s * kTile);
-      const bool has_rows = row0 + (warp & 3) * 32 < total;  // warp-uniform
-      const bool row_valid = row0 + row < total;
-      const int r = min(row0 + row, total - 1);
-      const int qi = p.by_G(r), h = x.head * p.G + r - qi * p.G;
-      const int at = cur.r.c - p.queries + qi;
-      const int row_hi = p.causal ? at + 1 : cur.r.c, row_lo = p.window ? at - p.window + 1 : 0;
-      // ------- the row of Q, its largest element as 2^7 .. 2^8
+      int count, stride, hi, lo;
       float row_scale = 0.f;
+      bool has_rows;
+      {
+      const Cursor cur = kept_cursor(kept);
+      const Piece x = piece_of(p, cur, left);
+      const int first_row = x.alternate ? 0 : s * kTile;
+      has_rows = first_row + (warp & 3) * 32 < x.rows;  // warp-uniform
+      const RowAt a = row_at(p, x, cur.r.c, first_row + row);
       if (has_rows) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(p.q + x.b * p.q_bat + qi * p.q_tok + static_cast<int64_t>(h) * D);
-        uint4 raw[D / 8];
-        uint32_t most = 0;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) raw[k] = __ldg(src + k);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
-        }
-        const int ex = max(static_cast<int>(most >> 7) - 127, -110);
-        const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-        row_scale = p.scale_log2 * ldexpf(1.f, ex - 7);
-        if (s == 0 || !x.alternate) {
-          uint8_t* q = smem + L::kQ + s * L::kTileBytes;
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-            *reinterpret_cast<uint4*>(q + (k >> 3) * L::kBoxBytes + sw128_offset(row, k & 7)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          fence_proxy_async_smem();
-        }
+        row_scale = load_query<D>(p, x, a, s == 0 || !x.alternate ? smem + L::kQ + s * L::kTileBytes : nullptr,
+                                  row);
+        fence_proxy_async_smem();
       }
       if (s == 0 || !x.alternate) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
       }
-      float m_ref = -INFINITY, l = 0.f;
-      uint32_t top = 0;
-      int in_sum = 0;
-      bool aside = false;
-
-      // What has been summed as normalised O and LSE (log2), joined with what was put
-      // aside (`with`: rows of that buffer); `use(c, o)` gets 32 features at a time.
-      // Whole warps.
-      const auto read_sum = [&](bool own, bool other, auto use) -> float {
-        tc_fence_after_sync();
-        float z = in_sum == 0 || l == 0.f ? -INFINITY : m_ref - kShift + log2f(l);
-        const float z_own = own ? aside_z[s * kTile + row] : -INFINITY;
-        const float z_other = other ? aside_z[kTile + row] : -INFINITY;
-        const float most = fmaxf(z, fmaxf(z_own, z_other)), ref = most == -INFINITY ? 0.f : most;
-        float w = exp2f(z - ref), w_own = exp2f(z_own - ref), w_other = exp2f(z_other - ref);
-        const float all = w + w_own + w_other, inv = all == 0.f ? 0.f : 1.f / all;
-        const float inv_l = in_sum == 0 || l == 0.f ? 0.f : 1.f / l;
-        w *= inv;
-        w_own *= inv;
-        w_other *= inv;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          if (in_sum > 0) tmem_ld32(tmem + lane_base + colO + c * 32, o);
-          // 2^(E - 127 - headroom), in two steps: one could lie below fp32's range
-          const int ex = static_cast<int>(top >> 8 * c & 255);
-          const float f0 = __uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23) * inv_l;
-          const float f1 =
-              __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63 - kHeadroom) << 23);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o[i] = in_sum > 0 && z != -INFINITY ? o[i] * f0 * f1 : 0.f;
-            if (own || other) o[i] = z != -INFINITY ? o[i] * w : 0.f;
-          }
-          if (own && z_own != -INFINITY) {
-            const float4* v = reinterpret_cast<const float4*>(aside_o + (s * kTile + row) * D + c * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 y = v[i];
-              o[4 * i] = fmaf(y.x, w_own, o[4 * i]);
-              o[4 * i + 1] = fmaf(y.y, w_own, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(y.z, w_own, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(y.w, w_own, o[4 * i + 3]);
-            }
-          }
-          if (other && z_other != -INFINITY) {
-            const float4* v = reinterpret_cast<const float4*>(aside_o + (kTile + row) * D + c * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 y = v[i];
-              o[4 * i] = fmaf(y.x, w_other, o[4 * i]);
-              o[4 * i + 1] = fmaf(y.y, w_other, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(y.z, w_other, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(y.w, w_other, o[4 * i + 3]);
-            }
-          }
-          use(c, o);
-        }
-        return all == 0.f ? -INFINITY : ref + log2f(all);
-      };
-      const auto put_aside = [&](bool own) {
-        const float z = read_sum(own, false, [&](int c, const float (&o)[32]) {
-          float4* to = reinterpret_cast<float4*>(aside_o + (s * kTile + row) * D + c * 32);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        });
-        aside_z[s * kTile + row] = z;
-      };
+      hi = a.hi;
+      lo = a.lo;
+      count = x.count;
+      stride = x.alternate ? 2 : 1;
+      }
+      Sum sum{-INFINITY, 0.f, 0, 0, false};
       // the last P V of this slot
       const auto last_done = [&] {
         if (n_s > 0 && ok)
@@ -677,16 +797,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 
 #pragma unroll 1
-      for (int m = x.alternate ? s : 0; ok && m < x.count; m += x.alternate ? 2 : 1) {
-        if (in_sum == kFlush) {
+      for (int m = stride == 2 ? s : 0; ok && m < count; m += stride) {
+        if (sum.tiles == kFlush) {
           last_done();
           if (!ok) break;
-          if (has_rows) put_aside(aside);
-          tc_fence_before_sync();
-          aside = true;
-          in_sum = 0;
-          m_ref = -INFINITY;
-          l = 0.f;
+          if (has_rows) {
+            const Cursor cur = kept_cursor(kept);
+            const Piece x = piece_of(p, cur, left);
+            store_sum<D>(p, x, cur.r, row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row), sum, o_at, s, row, kAside, false);
+          }
+          sum = Sum{-INFINITY, 0.f, 0, 0, true};
         }
         if (!mbar_wait_warp(&bars[L::bSFull + s], n_s & 1, p.status, abort_flag)) {
           ok = false;
@@ -694,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_s;
         if (!has_rows) {  // nothing to do, but the MMA counts four warps
-          ++in_sum;
+          ++sum.tiles;
           if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
           continue;
         }
@@ -705,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sv[kTile];
 #pragma unroll
         for (int c = 0; c < kTile / 32; c += 2)
-          tmem_ld32x2(tmem + lane_base + colS + c * 32, tmem + lane_base + colS + (c + 1) * 32,
+          tmem_ld32x2(s_at + c * 32, s_at + (c + 1) * 32,
                       sv + c * 32, sv + (c + 1) * 32);
         const uint32_t a0 = info.there[0], b0 = info.there[1], a1 = info.there[2],
                        b1 = info.there[3], a2 = info.there[4], b2 = info.there[5];
@@ -719,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t reads =
-                there[q] & below(row_hi, q) & (~below(row_lo, q) | (p.window ? below(p.sinks, q) : 0u));
+                there[q] & below(hi, q) & (~below(lo, q) | (p.window ? below(p.sinks, q) : 0u));
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               sv[32 * q + c] = reads >> c & 1 ? sv[32 * q + c] : -INFINITY;
@@ -729,31 +849,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kTile; c += 2) mx4[c / 2 % 4] = fmax3(mx4[c / 2 % 4], sv[c], sv[c + 1]);
         const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
-        const float m_new = fmaxf(m_ref, mx * mult);
-        const bool need = m_new > m_ref + kThreshold;  // false while both are -inf
+        const float m_new = fmaxf(sum.m, mx * mult);
+        const bool need = m_new > sum.m + kThreshold;  // false while both are -inf
         const uint32_t now = info.top;
-        if (in_sum > 0 && (now != top || __any_sync(0xffffffffu, need))) {
+        if (sum.tiles > 0 && (now != sum.top || __any_sync(0xffffffffu, need))) {
           // O holds the P V so far, under the old maximum and E (its last P V is done:
           // this S was issued after it)
-          const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
+          const float alpha = need ? exp2f(sum.m - m_new) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            const int by = static_cast<int>((now >> 8 * c & 255) - (top >> 8 * c & 255));
-            const float f =
-                alpha * (by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23) : 0.f);
-            float o[32];
-            tmem_ld32(tmem + lane_base + colO + c * 32, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(tmem + lane_base + colO + c * 32, o);
+          for (int c = 0; c < D / 8; ++c) {  // (8 at a time: the scores are in registers)
+            const int by = static_cast<int>((now >> 8 * (c / 4) & 255) - (sum.top >> 8 * (c / 4) & 255));
+            tmem_scale8(o_at + c * 8,
+                        alpha * (by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23) : 0.f));
           }
         }
-        top = now;
+        sum.top = now;
         if (need) {
-          l *= exp2f(m_ref - m_new);  // 0 when m_ref was -inf
-          m_ref = m_new;
+          sum.l *= exp2f(sum.m - m_new);  // 0 when sum.m was -inf
+          sum.m = m_new;
         }
-        const float ref = (m_ref == -INFINITY ? 0.f : m_ref) - kShift;
+        const float ref = (sum.m == -INFINITY ? 0.f : sum.m) - kShift;
         const uint64_t mult2 = f2_pack(mult, mult), neg = f2_pack(-ref, -ref);
         uint64_t rs2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -768,88 +883,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs2 = f2_add(rs2, f2_pack(e0, e1));
             packed[c] = __uint_as_float(pack_f16(e0, e1));
           }
-          tmem_st32(tmem + lane_base + colS + half * 32, packed);
+          tmem_st32(s_at + half * 32, packed);
         }
         float rs0, rs1;
         f2_unpack(rs2, rs0, rs1);
-        l += rs0 + rs1;
-        ++in_sum;
+        sum.l += rs0 + rs1;
+        ++sum.tiles;
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
       }
       last_done();
       // ------- the piece's end
+      Cursor cur = kept_cursor(kept);
+      const Piece x = piece_of(p, cur, left);
+      const RowAt a = row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row);
       const int later = x.n - x.k0 - x.count;  // steps of the item in later shares
       const bool starts = x.k0 == 0;
       if (starts && threadIdx.x == 128)
         p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
             make_int2(static_cast<int>(blockIdx.x),
                       1 + static_cast<int>((later + share.per - 1) / share.per));
-      if (x.alternate && s == 1 && ok && has_rows) {
-        put_aside(aside);
-        __threadfence_block();
-      }
-      if (x.alternate) softmax_sync();
-      if (ok && has_rows && (s == 0 || !x.alternate)) {
-        const int part = starts && later == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-        const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
-        // NaN in V that was kept out of the products
-        const auto nan_at = [&](int c) -> uint32_t {  // features of chunk c, a bit each
-          uint32_t bad = 0;
-          for (int k = x.k0; k < x.k0 + x.count; ++k) {
-            const int j0 = key_of(cur.r, k), end = k < cur.r.n_first ? cur.r.first : cur.r.hi;
-            for (int j = j0; j < min(j0 + kTileKeys, end); ++j) {
-              if (!(j < row_hi && (j >= row_lo || j < p.sinks))) continue;
-              const int entry = p.by_page(j);
-              const int pg = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_pages + entry);
-              if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) continue;
-              const uint64_t slot = static_cast<uint32_t>(pg * p.page_size + j - entry * p.page_size);
-              const uint64_t place = slot * p.Hkv + x.head;
-              if (__ldg(p.v_scale + place * (D / 32) + c) == 255) bad = ~0u;
-              for (int i = 0; i < 32; ++i)
-                if ((__ldg(p.v + place * D + c * 32 + i) & 0x7f) == 0x7f) bad |= 1u << i;
-            }
-          }
-          return bad;
-        };
-        const int64_t token = static_cast<int64_t>(x.b) * p.queries + qi;
-        const int64_t place = static_cast<int64_t>(part) * kPairRows + (x.alternate ? 0 : s * kTile) + row;
-        const float z = read_sum(aside, x.alternate, [&](int c, float (&o)[32]) {
-          if (redo) {
-            const uint32_t bad = row_valid ? nan_at(c) : 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (bad >> i & 1) o[i] = NAN;
-          }
-          if (!row_valid) return;
-          if (part < 0) {
-            uint4* to = reinterpret_cast<uint4*>(p.o + (token * p.Hq + h) * D + c * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
-                                 pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                 pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                                 pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-          } else {
-            float4* to = reinterpret_cast<float4*>(p.part_o + place * D + c * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-        });
-        if (row_valid) {
-          if (part < 0)
-            p.lse[(static_cast<int64_t>(x.b) * p.Hq + h) * p.queries + qi] = z * 0.6931471805599453f;
-          else
-            p.part_z[place] = z;
+      const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
+      const int part =
+          starts && later == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+      // (slot 1 of an alternate piece leaves its sum aside for slot 0)
+#pragma unroll 1
+      for (int turn = x.alternate ? 1 : s; turn >= (x.alternate ? 0 : s); --turn) {
+        if (turn == s && ok && has_rows)
+          store_sum<D>(p, x, cur.r, a, sum, o_at, s, row,
+                       x.alternate && s == 1 ? kAside : part, redo && !(x.alternate && s == 1));
+        if (x.alternate && turn == 1) {
+          __threadfence_block();
+          softmax_sync();
         }
       }
       tc_fence_before_sync();
       if (x.alternate) softmax_sync();  // slot 1's sum has been read
       t0 += x.count;
       left -= x.count;
-      if (left > 0) next_item(p, cur);
+      if (left > 0) {
+        next_item(p, cur);
+        __syncwarp();
+        keep_cursor(kept, cur);
+      }
     }
   }
 
@@ -862,15 +939,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
   static PerDeviceOnce configured;
+  static int launch_regs[PerDeviceOnce::kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (!configured.run(dev, [&](int) {
+  if (!configured.run(dev, [&](int device) {
         e = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Tiles<D>::kSmem);
-        return e == cudaSuccess;
+        if (e != cudaSuccess) return false;
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, paged_tiles_kernel<D>);
+        if (e != cudaSuccess) return false;
+        launch_regs[device] = fa.numRegs;
+        return true;
       }))
     return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  // setmaxnreg.inc would wait forever if the budgets exceeded the launch allocation
+  if (launch_regs[dev] * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
   paged_tiles_kernel<D><<<p.lanes * p.lane_ctas, kThreads, Tiles<D>::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
