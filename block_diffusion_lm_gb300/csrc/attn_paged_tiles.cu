@@ -17,11 +17,12 @@
 // when a row's maximum does).  An operand below 2^-31 of the largest beside it becomes
 // 0.  P is p 2^11, rounded to 2^-11 of itself (2^-36 of the row's largest at least).
 //
-// Keys.  Three converter warps look the pages up, copy codes and scale bytes to a
-// ring of five half tiles (cp.async, about 66 KB ahead) and write K and V as f16 into
-// the one 128-byte-swizzled tile that each has: S(t) of both slots is done long before
-// K(t + 1) is wanted, and P V(t) before V(t + 1).  One thread issues the MMAs, two
-// warpgroups do the softmax, a row per thread, as in the training forward.
+// Keys.  One warp looks the pages up and starts the copies of K's codes and the scale
+// bytes into a ring of five half tiles, about 66 KB ahead, another those of V's (cp.async:
+// one bulk copy per key takes 58 clocks of the issuing warp each); five warps write K and V as f16 into the one 128-byte-swizzled tile that each has: S(t) of both
+// slots is done long before K(t + 1) is wanted, and P V(t) before V(t + 1).  One thread
+// issues the MMAs, two warpgroups do the softmax, a row per thread, as in the training
+// forward.
 //
 // Keys that a row does not read are masked.  Where some row of the pair does not read
 // a key of a tile, NaN in V is written as 0 and remembered: the rows that read it are
@@ -42,19 +43,19 @@ namespace csbp {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kConverters = 96;
+constexpr int kThreads = 512;
+constexpr int kWarps = 5;  // converters
 constexpr float kThreshold = 4.f;  // log2: a row's maximum may lag by that
 constexpr float kShift = 11.f;     // P = p 2^11
 constexpr int kHeadroom = 6;       // K and V operands: codes times up to 2^6
 constexpr int kFlush = 512;        // key tiles that one accumulator takes in
 constexpr int kHalves = 5;         // of the ring
 constexpr int kInfos = 8;
-// Per-warpgroup register budgets (setmaxnreg): issuer and converters, softmax.  Their
+// Per-warpgroup register budgets (setmaxnreg): issuer, copies and converters, softmax.  Their
 // sum must not exceed the launch allocation (checked on the host).
-constexpr uint32_t kRegsLow = 112;
+constexpr uint32_t kRegsLow = 64;
 constexpr uint32_t kRegsSoftmax = 192;
-constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsSoftmax;
+constexpr int kRegsNeeded = 256 * kRegsLow + 256 * kRegsSoftmax;
 
 template <int D>
 struct Tiles {
@@ -67,32 +68,45 @@ struct Tiles {
   static constexpr int kRing = kV + kTileBytes;
   static constexpr int kWords = kRing + kHalves * kHalf;  // [3 tiles][K, V][key] scale words
   static constexpr int kInfo = kWords + 3 * 2 * kTile * 4;
-  static constexpr int kBar = kInfo + kInfos * 64;
+  static constexpr int kRows = kInfo + kInfos * 64;  // [3 tiles][key] place in the cache
+  static constexpr int kBar = kRows + 3 * kTile * 4;
   static constexpr int bQFull = 0;                  // [2] per slot
   static constexpr int bKFull = 2, bKEmpty = 3, bVFull = 4, bVEmpty = 5;
   static constexpr int bSFull = 6, bPFull = 8, bPvDone = 10;  // [2]
-  static constexpr int bDrain = 12, kBars = 13;
+  static constexpr int bDrain = 12;
+  static constexpr int bInfo = 13;                  // [2] by tile
+  static constexpr int bRows = 15;                  // [2] by tile: places of its keys
+  static constexpr int bFull = 17;                  // [kHalves] codes are there
+  static constexpr int bFree = bFull + kHalves;     // and have been converted
+  static constexpr int kBars = bFree + kHalves;
   static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
   static constexpr int kRedo = kMisc + 8;           // [kInfos] by item
-  static constexpr int kTop = kRedo + kInfos * 4;   // [3 warps][K, V] largest scale bytes
-  static constexpr int kCursor = (kTop + 24 + 15) / 16 * 16;  // of each softmax warp
+  static constexpr int kCursor = (kRedo + kInfos * 4 + 15) / 16 * 16;  // of each softmax warp
   static constexpr int kSmem = kCursor + 8 * 48;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
 };
 static_assert(Tiles<128>::kSmem <= 232448, "shared memory of a CTA");
 
-// What the converters leave about a tile, in shared memory.
+// What is known about a tile, in shared memory.
 struct Info {
+  uint32_t there[4];  // which keys are there
   float k_factor;     // of S
-  uint32_t top;       // E of V
+  uint32_t k_top;     // E of K
+  uint32_t top;       // E of V, a byte per group
   int j0;             // first key
   int edge;           // some row does not read some key
-  uint32_t there[6];  // keys of warps 0 .. 2: 32 and 11 (10) each
-  int upper;          // scale bytes are the upper half of their words
+  int upper;          // the scale bytes are the upper half of their words
+  int item;           // the CTA's pieces so far
   int first;          // of a piece
-  uint32_t pad[4];
+  int pad[4];
 };
 static_assert(sizeof(Info) == 64, "");
+
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// One arrival when the lane's cp.async copies so far are done.
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
   return (1u << 4)                                   // D: f32; A and B: f16
@@ -129,7 +143,6 @@ __device__ __forceinline__ void tmem_scale8(uint32_t at, float f) {
       : "memory");
 }
 
-__device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // A CTA's part of one item.
@@ -196,15 +209,6 @@ __device__ __forceinline__ Cursor kept_cursor(uint32_t at) {
 __device__ __forceinline__ int key_of(const Range& r, int k) {
   return k < r.n_first ? k * kTileKeys : r.lo + (k - r.n_first) * kTileKeys;
 }
-// Whether all rows of a pair read all of the keys j0 .. j0 + 127.
-__device__ __forceinline__ bool all_read(const PagedParams& p, const Range& r, int tile, int rows,
-                                         int j0) {
-  const int i0 = p.by_G(tile * kPairRows), i1 = p.by_G(tile * kPairRows + rows - 1);
-  const int hi = p.causal ? r.c - p.queries + i0 + 1 : r.c;
-  const int lo = p.window ? r.c - p.queries + i1 - p.window + 1 : 0;
-  return j0 + kTileKeys <= hi && (j0 >= lo || j0 + kTileKeys <= p.sinks);
-}
-
 // 2^(kHeadroom - delta) in f16, both halves; 0 below 2^-24, NaN for a byte of 255.
 __device__ __forceinline__ uint32_t operand_scale(int top, int byte) {
   const int delta = top - byte;
@@ -215,102 +219,123 @@ __device__ __forceinline__ uint32_t operand_scale(int top, int byte) {
   return h | h << 16;
 }
 
-// ---------------------------------------------------------------- converters
+// -------------------------------------------------------------------- copies
+// Two warps: one looks keys up and copies K and the scale bytes, one copies V and works
+// the scales' maxima out once they are there.
 template <int D>
-struct Converter {
+struct Copier {
   using L = Tiles<D>;
   const PagedParams& p;
   uint8_t* const smem;
   const uint32_t mem;
-  const int warp, lane, tid;  // of the converters
-  const int first, count;     // key rows of the warp
-  // rows lane and lane + 32 of the tile that is being copied, and of the next
-  uint32_t row[2];
-  bool there[2];
-  int page[2], place[2];
+  const int lane;
+  uint64_t* const bars;
+  int* const abort_flag;
 
-  __device__ __forceinline__ Converter(const PagedParams& p, uint8_t* smem)
-      : p(p), smem(smem), mem(smem_u32(smem)), warp(static_cast<int>(threadIdx.x >> 5) - 1),
-        lane(threadIdx.x & 31), tid(static_cast<int>(threadIdx.x) - 32), first(43 * warp),
-        count(warp < 2 ? 43 : 42) {}
+  __device__ __forceinline__ Copier(const PagedParams& p, uint8_t* smem, uint64_t* bars,
+                                    int* abort_flag)
+      : p(p), smem(smem), mem(smem_u32(smem)), lane(threadIdx.x & 31), bars(bars),
+        abort_flag(abort_flag) {}
 
-  __device__ __forceinline__ void look(const Cursor& cur) {
-    const int j0 = key_of(cur.r, cur.step);
-    const int end = cur.step < cur.r.n_first ? cur.r.first : cur.r.hi;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int m = lane + 32 * x, j = j0 + first + m, entry = p.by_page(j);
-      place[x] = j - entry * p.page_size;
-      page[x] = -1;
-      if (m < count && j < end)
-        page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
-    }
+  __device__ __forceinline__ bool wait(int bar, int parity) const {
+    return mbar_wait_warp(&bars[bar], parity & 1, p.status, abort_flag);
   }
 
-  // Takes what was looked up for the tile at `cur`, and leaves a record of it.
-  __device__ __forceinline__ void take(const Cursor& cur, int t, bool piece_begins) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      there[x] = static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(p.pages);
-      row[x] = there[x] ? static_cast<uint32_t>(page[x] * p.page_size + place[x]) * p.Hkv + cur.block
-                        : 0;
-    }
-    const uint32_t w0 = __ballot_sync(0xffffffffu, there[0]);
-    const uint32_t w1 = __ballot_sync(0xffffffffu, there[1]);
-    Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
-    if (lane == 0) {
-      info.there[2 * warp] = w0;
-      info.there[2 * warp + 1] = w1;
-      if (warp == 0) {
-        const int j0 = key_of(cur.r, cur.step), tile = cur.entry - cur.b * p.row_tiles;
-        info.j0 = j0;
-        info.upper = D == 64 && p.wide_scales && (cur.block & 1);
-        info.first = piece_begins;
-        info.edge = !all_read(p, cur.r, tile, min(kPairRows, p.queries * p.G - tile * kPairRows), j0);
-      }
-    }
-    // scale bytes, with K's codes
-    const uint32_t words = mem + L::kWords + (t % 3) * (2 * kTile * 4);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int m = lane + 32 * x;
-      if (m >= count) continue;
-      const uint32_t to = words + (first + m) * 4;
-      const uint64_t at = static_cast<uint64_t>(row[x]) * (D / 32);
-      if (p.wide_scales) {
-        const int n = there[x] ? 4 : 0;
-        copy4(to, p.k_scale + (at & ~uint64_t(3)), n);
-        copy4(to + kTile * 4, p.v_scale + (at & ~uint64_t(3)), n);
-      } else {
-        uint32_t k = 0, v = 0;
-        if (there[x])
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            k |= static_cast<uint32_t>(__ldg(p.k_scale + at + e)) << 8 * e;
-            v |= static_cast<uint32_t>(__ldg(p.v_scale + at + e)) << 8 * e;
-          }
-        sts32(to, k);
-        sts32(to + kTile * 4, v);
-      }
-    }
-  }
-
-  // Starts the copies of K's or V's codes of the tile taken last.
-  __device__ __forceinline__ void copy(const uint8_t* codes, int half) const {
+  // Starts the copies of K's or V's codes of tile t.
+  __device__ __forceinline__ void copy(const uint8_t* codes, int t, int half,
+                                       const uint32_t (&there)[4]) const {
     constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
     const int chunk = lane % kChunks, r0 = lane / kChunks;
     const uint8_t* src = codes + chunk * 16;
-    const uint32_t at = mem + L::kRing + half * L::kHalf;
-    const uint32_t is[2] = {__ballot_sync(0xffffffffu, there[0]),
-                            __ballot_sync(0xffffffffu, there[1])};
+    const uint32_t to = mem + L::kRing + half * L::kHalf + r0 * D + chunk * 16;
+    const uint32_t rows = mem + L::kRows + (t % 3) * (kTile * 4) + r0 * 4;
+#pragma unroll 8
+    for (int i = 0; i < kTile / kAtOnce; ++i) {
+      const int r = i * kAtOnce;
+      const uint64_t from = static_cast<uint64_t>(lds32(rows + r * 4)) * D;
+      copy16(to + r * D, src + from, there[r / 32] >> (r % 32 + r0) & 1 ? 16 : 0);
+    }
+    arrive_after_copies(smem_u32(&bars[L::bFull + half]));
+  }
+
+  __device__ __forceinline__ void run_k(Cursor& cur, int steps) {
+    int page[4], place[4];  // of keys lane + 32 x of the next tile
+    const auto look = [&] {
+      const int end = cur.step < cur.r.n_first ? cur.r.first : cur.r.hi;
+      const int j0 = key_of(cur.r, cur.step) + lane;
 #pragma unroll
-    for (int i = 0; i < (43 + kAtOnce - 1) / kAtOnce; ++i) {
-      const int m = i * kAtOnce + r0, x = i * kAtOnce / 32;
-      const uint64_t from = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row[x], m & 31)) * D;
-      if (m >= count) continue;
-      const int r = first + m;
-      copy16(at + r * D + (D == 128 ? chunk ^ (r & 1) << 2 : chunk) * 16, src + from,
-             is[x] >> (m & 31) & 1 ? 16 : 0);
+      for (int x = 0; x < 4; ++x) {
+        const int j = j0 + 32 * x, entry = p.by_page(j);
+        place[x] = j - entry * p.page_size;
+        page[x] = -1;
+        if (j < end) page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
+      }
+    };
+    int item = 0, hi = 0, lo = 0;
+    bool begins = true;
+    look();
+#pragma unroll 1
+    for (int t = 0; t < steps; ++t) {
+      // (the places and scale words of tile t - 3 have been used: V(t - 3) is converted,
+      // and K's half tile is free)
+      const int h = 2 * t;
+      if (t >= 3 && !wait(L::bFree + (h - 5) % kHalves, (h - 5) / kHalves)) return;
+      Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
+      if (begins) {  // keys that all rows of the pair read
+        const int first = (cur.entry - cur.b * p.row_tiles) * kPairRows;
+        const int last = min(first + kPairRows, p.queries * p.G) - 1;
+        hi = p.causal ? cur.r.c - p.queries + static_cast<int>(p.by_G(first)) + 1 : cur.r.c;
+        lo = p.window ? cur.r.c - p.queries + static_cast<int>(p.by_G(last)) - p.window + 1 : 0;
+      }
+      const int j0 = key_of(cur.r, cur.step);
+      bool edge = !(j0 + kTileKeys <= hi && (j0 >= lo || j0 + kTileKeys <= p.sinks));
+      uint32_t rows = mem + L::kRows + (t % 3) * (kTile * 4) + lane * 4;
+      uint32_t words = mem + L::kWords + (t % 3) * (2 * kTile * 4) + lane * 4;
+      uint32_t there[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x, rows += 128, words += 128) {
+        const bool is = static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(p.pages);
+        const uint32_t row =
+            is ? static_cast<uint32_t>(page[x] * p.page_size + place[x]) * p.Hkv + cur.block : 0;
+        there[x] = __ballot_sync(0xffffffffu, is);
+        edge |= there[x] != ~0u;
+        sts32(rows, row);
+        const uint64_t at = static_cast<uint64_t>(row) * (D / 32);
+        if (p.wide_scales) {
+          copy4(words, p.k_scale + (at & ~uint64_t(3)), is ? 4 : 0);
+          copy4(words + kTile * 4, p.v_scale + (at & ~uint64_t(3)), is ? 4 : 0);
+        } else {
+          uint32_t k = 0, v = 0;
+          if (is)
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+              k |= static_cast<uint32_t>(__ldg(p.k_scale + at + e)) << 8 * e;
+              v |= static_cast<uint32_t>(__ldg(p.v_scale + at + e)) << 8 * e;
+            }
+          sts32(words, k);
+          sts32(words + kTile * 4, v);
+        }
+      }
+      if (lane == 0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) info.there[x] = there[x];
+        info.j0 = j0;
+        info.edge = edge;
+        info.upper = D == 64 && p.wide_scales && (cur.block & 1);
+        info.item = item;
+        info.first = begins;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::bRows + (t & 1)]);
+      copy(p.k, t, h % kHalves, there);
+      if (t + 1 < steps) {
+        begins = ++cur.step == cur.r.n;
+        if (begins) {
+          next_item(p, cur);
+          ++item;
+        }
+        look();
+      }
     }
   }
 
@@ -320,136 +345,161 @@ struct Converter {
     return D == 128 ? w : upper ? w >> 16 : w & 0xffffu;
   }
 
-  // Largest scale bytes of a tile, a byte per group: K, V.
-  __device__ __forceinline__ uint2 largest(int t, bool upper) const {
-    uint32_t k = 0, v = 0;
-    for (int key = tid; key < kTile; key += kConverters) {
-      uint32_t a = word(t, 0, key, upper), b = word(t, 1, key, upper);
-      if (any_byte_255(a) || any_byte_255(b)) {
-        a &= ~__vcmpeq4(a, 0xffffffffu);
-        b &= ~__vcmpeq4(b, 0xffffffffu);
+  __device__ __forceinline__ void run_v(int steps) {
+    uint32_t top = 0;
+#pragma unroll 1
+    for (int t = 0; t <= steps; ++t) {
+      if (t < steps) {
+        const int h = 2 * t + 1;
+        if (!wait(L::bRows + (t & 1), t >> 1)) return;
+        if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
+        const Info& info = reinterpret_cast<const Info*>(smem + L::kInfo)[t % kInfos];
+        const uint32_t there[4] = {info.there[0], info.there[1], info.there[2], info.there[3]};
+        copy(p.v, t, h % kHalves, there);
       }
-      k = __vmaxu4(k, a);
-      v = __vmaxu4(v, b);
-    }
+      if (t == 0) continue;
+      // the scales of the tile before: they have had a tile's time to come
+      const int u = t - 1;
+      if (!wait(L::bFull + 2 * u % kHalves, 2 * u / kHalves)) return;
+      Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[u % kInfos];
+      const bool upper = D == 64 && info.upper, begins = info.first;
+      uint32_t k = 0, v = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      k = __vmaxu4(k, __shfl_xor_sync(0xffffffffu, k, o));
-      v = __vmaxu4(v, __shfl_xor_sync(0xffffffffu, v, o));
+      for (int x = 0; x < 4; ++x) {
+        uint32_t a = word(u, 0, lane + 32 * x, upper), b = word(u, 1, lane + 32 * x, upper);
+        if (any_byte_255(a) || any_byte_255(b)) {
+          a &= ~__vcmpeq4(a, 0xffffffffu);
+          b &= ~__vcmpeq4(b, 0xffffffffu);
+        }
+        k = __vmaxu4(k, a);
+        v = __vmaxu4(v, b);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v = __vmaxu4(v, __shfl_xor_sync(0xffffffffu, v, o));
+      k = max(max(k & 255, k >> 8 & 255), max(k >> 16 & 255, k >> 24));
+      k = __reduce_max_sync(0xffffffffu, k);
+      top = begins ? v : __vmaxu4(top, v);
+      if (lane == 0) {
+        info.k_factor = ldexpf(1.f, static_cast<int>(k) - 127 - kHeadroom);
+        info.k_top = k;
+        info.top = top;
+        if (begins) reinterpret_cast<volatile int*>(smem + L::kRedo)[info.item % kInfos] = 0;
+        mbar_arrive(&bars[L::bInfo + (u & 1)]);
+      }
+      __syncwarp();
     }
-    uint2* all = reinterpret_cast<uint2*>(smem + L::kTop);
-    if (lane == 0) all[warp] = make_uint2(k, v);
-    converters_sync();
-    k = __vmaxu4(__vmaxu4(all[0].x, all[1].x), all[2].x);
-    v = __vmaxu4(__vmaxu4(all[0].y, all[1].y), all[2].y);
-    return make_uint2(k, v);
   }
+};
+
+// ---------------------------------------------------------------- converters
+template <int D>
+struct Converter {
+  using L = Tiles<D>;
+  const PagedParams& p;
+  uint8_t* const smem;
+  const uint32_t mem;
+  const int warp, lane;
+
+  __device__ __forceinline__ Converter(const PagedParams& p, uint8_t* smem)
+      : p(p), smem(smem), mem(smem_u32(smem)), warp(static_cast<int>(threadIdx.x >> 5) - 3),
+        lane(threadIdx.x & 31) {}
 
   // Codes of half tile `half` to f16 in the operand tile at `tile`, under E `top`.
-  // `edge`: NaN is written as 0; whether there was any.
-  __device__ __forceinline__ bool convert(int half, int t, int kv, bool upper, uint32_t top,
-                                          uint32_t tile, bool edge) const {
-    const uint32_t from = mem + L::kRing + half * L::kHalf;
-    const uint32_t bytes = mem + L::kWords + ((t % 3) * 2 + kv) * (kTile * 4) + (upper ? 2 : 0);
+  // kEdge: NaN is written as 0; whether there was any.
+  template <bool kEdge>
+  __device__ __forceinline__ bool convert(uint32_t from, uint32_t bytes, uint32_t top,
+                                          uint32_t tile) const {
+    // 4 rows of 8 pieces of 16 codes (D = 64: 8 of 4) at a time, so that 8 lanes read
+    // and write different banks
     constexpr int kAtOnce = D == 128 ? 4 : 8;
-    const int c = D == 128 ? (lane & 3) | lane >> 4 << 2 : lane & 3;
-    const int r0 = D == 128 ? lane >> 2 & 3 : lane >> 2;
+    const int r0 = D == 128 ? (lane >> 4) * 2 + (lane >> 2 & 1) : lane >> 2;
+    const int c = D == 128 ? (lane & 3) + 4 * ((lane >> 2 ^ lane >> 3) & 1) : lane & 3;
     const int e = static_cast<int>(top >> 8 * (c >> 1) & 255);
+    from += c * 16;
+    bytes += c >> 1;
+    tile += (c >> 2) * L::kBoxBytes;
     bool found = false;
-#pragma unroll 4
-    for (int q = warp; q < kTile / kAtOnce; q += 3) {
-      const int r = q * kAtOnce + r0;
-      uint32_t w[4], byte;
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(from + r * D + (D == 128 ? c ^ (r & 1) << 2 : c) * 16)
-                   : "memory");
-      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(bytes + r * 4 + (c >> 1)) : "memory");
-      if (edge) {
-        const uint32_t bad[4] = {nan_codes(w[0]), nan_codes(w[1]), nan_codes(w[2]), nan_codes(w[3])};
-        if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0 || byte == 255) {
-          found = true;
-          if (byte == 255) byte = 0;
+    constexpr int kBatch = 3;  // loaded together
+#pragma unroll 1
+    for (int q0 = warp; q0 < kTile / kAtOnce; q0 += kBatch * kWarps) {
+      uint32_t w[kBatch][4], byte[kBatch];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] &= ~bad[k];
+      for (int x = 0; x < kBatch; ++x) {
+        const int r = min(q0 + x * kWarps, kTile / kAtOnce - 1) * kAtOnce + r0;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[x][0]), "=r"(w[x][1]), "=r"(w[x][2]), "=r"(w[x][3])
+                     : "r"(from + r * D)
+                     : "memory");
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte[x]) : "r"(bytes + r * 4) : "memory");
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (x > 0 && q0 + x * kWarps >= kTile / kAtOnce) break;  // (the same for the warp)
+        const int r = (q0 + x * kWarps) * kAtOnce + r0;
+        if (kEdge) {
+          uint32_t bad = byte[x] == 255;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) bad |= nan_codes(w[x][k]);
+          if (bad) {
+            found = true;
+            if (byte[x] == 255) byte[x] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[x][k] &= ~nan_codes(w[x][k]);
+          }
         }
+        // 2^(headroom - (E - e)) in f16, the normal ones at once
+        const int field = kHeadroom + 15 - e + static_cast<int>(byte[x]);
+        uint32_t s = static_cast<uint32_t>(field) * 0x04000400u;
+        if (field <= 0 || byte[x] == 255) s = operand_scale(e, static_cast<int>(byte[x]));
+        const uint32_t to = tile + sw128_offset(r, 2 * (c & 3));
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to),
+                     "r"(mul_f16x2(f16_low(w[x][0]), s)), "r"(mul_f16x2(f16_high(w[x][0]), s)),
+                     "r"(mul_f16x2(f16_low(w[x][1]), s)), "r"(mul_f16x2(f16_high(w[x][1]), s))
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16),
+                     "r"(mul_f16x2(f16_low(w[x][2]), s)), "r"(mul_f16x2(f16_high(w[x][2]), s)),
+                     "r"(mul_f16x2(f16_low(w[x][3]), s)), "r"(mul_f16x2(f16_high(w[x][3]), s))
+                     : "memory");
       }
-      const uint32_t s = operand_scale(e, static_cast<int>(byte));
-      uint32_t h[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[2 * k] = mul_f16x2(f16_low(w[k]), s);
-        h[2 * k + 1] = mul_f16x2(f16_high(w[k]), s);
-      }
-      const uint32_t to = tile + (c >> 2) * L::kBoxBytes + sw128_offset(r, 2 * (c & 3));
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-                   "r"(h[3])
-                   : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(h[4]), "r"(h[5]),
-                   "r"(h[6]), "r"(h[7])
-                   : "memory");
     }
     return found;
   }
 
-  // All tiles of the share, K and V of each in turn.  A wait that gives up is passed
-  // over: the other waits give up too, and the results are void.
-  __device__ __forceinline__ void run(Cursor& ahead, int steps, uint64_t* bars, int* abort_flag) {
-    volatile int* redo = reinterpret_cast<volatile int*>(smem + L::kRedo);
-    uint32_t top = 0, k_top = 0;
-    int item = -1, ring = 0, into = 0;  // half tiles that are converted and copied next
-    bool begins = true;
-    look(ahead);
+  __device__ __forceinline__ void run(int steps, uint64_t* bars, int* abort_flag) {
+    int half = 0, use = 0;
+    bool ok = true;
 #pragma unroll 1
-    for (int h = 1 - kHalves; h < 2 * steps; ++h) {
-      if (h >= 0) {
-        copies_wait<kHalves - 2>();
-        converters_sync();
-      }
-      // ------- copies, four half tiles ahead
-      const int i = h + kHalves - 1;
-      if (i < 2 * steps) {
-        if ((i & 1) == 0) take(ahead, i >> 1, begins);
-        copy(i & 1 ? p.v : p.k, into);
-        if ((i & 1) && i + 1 < 2 * steps) {
-          begins = ++ahead.step == ahead.r.n;
-          if (begins) next_item(p, ahead);
-          look(ahead);
-        }
-      }
-      copies_commit();
-      into = into + 1 == kHalves ? 0 : into + 1;
-      if (h < 0) continue;
-      // ------- conversion
+    for (int h = 0; ok && h < 2 * steps; ++h) {
       const int t = h >> 1, kv = h & 1;
-      Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
-      const bool upper = D == 64 && info.upper;
-      if (kv == 0) {
-        const uint2 most = largest(t, upper);
-        k_top = __vmaxu4(most.x, most.x >> 16);
-        k_top = max(k_top & 255, k_top >> 8 & 255);
-        top = info.first ? most.y : __vmaxu4(top, most.y);
-        item += info.first;
-        if (tid == 0) {
-          // 2^(E - 127 - headroom)
-          info.k_factor = ldexpf(1.f, static_cast<int>(k_top) - 127 - kHeadroom);
-          info.top = top;
-          if (info.first) redo[item % kInfos] = 0;
-        }
+      const Info& info = reinterpret_cast<const Info*>(smem + L::kInfo)[t % kInfos];
+      if (kv == 0)
+        ok = mbar_wait_warp(&bars[L::bInfo + (t & 1)], (t >> 1) & 1, p.status, abort_flag);
+      ok = ok && mbar_wait_warp(&bars[L::bFull + half], use & 1, p.status, abort_flag);
+      if (ok && t > 0)
+        ok = mbar_wait_warp(&bars[kv ? L::bVEmpty : L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
+      if (!ok) break;
+      const uint32_t from = mem + L::kRing + half * L::kHalf;
+      const uint32_t bytes = mem + L::kWords + ((t % 3) * 2 + kv) * (kTile * 4) +
+                             (D == 64 && info.upper ? 2 : 0);
+      const uint32_t top = kv ? info.top : info.k_top * 0x01010101u;
+      const uint32_t tile = mem + (kv ? L::kV : L::kK);
+      if (kv && info.edge) {
+        if (convert<true>(from, bytes, top, tile))
+          reinterpret_cast<volatile int*>(smem + L::kRedo)[info.item % kInfos] = 1;
+      } else {
+        convert<false>(from, bytes, top, tile);
       }
-      const bool edge =
-          kv && (info.edge || (info.there[0] & info.there[2] & info.there[4]) != ~0u ||
-                 info.there[1] != 0x7ffu || info.there[3] != 0x7ffu || info.there[5] != 0x3ffu);
-      if (t > 0)
-        mbar_wait_warp(&bars[kv ? L::bVEmpty : L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
-      if (convert(ring, t, kv, upper, kv ? top : k_top * 0x01010101u, mem + (kv ? L::kV : L::kK), edge))
-        redo[item % kInfos] = 1;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kv ? L::bVFull : L::bKFull]);
-      ring = ring + 1 == kHalves ? 0 : ring + 1;
+      if (lane == 0) {
+        mbar_arrive(&bars[kv ? L::bVFull : L::bKFull]);
+        mbar_arrive(&bars[L::bFree + half]);
+      }
+      if (++half == kHalves) {
+        half = 0;
+        ++use;
+      }
     }
-    copies_wait<0>();
   }
 };
 
@@ -641,10 +691,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (share.begin >= share.end) return;
   const int steps = static_cast<int>(share.end - share.begin);
   if (threadIdx.x == 0) {
-    // arrivals: converter warps, a slot's softmax warps, else one commit
+    // arrivals: converter warps, a slot's softmax warps, the copying lanes,
+    // else one arrival or commit
     for (int i = 0; i < L::kBars; ++i) {
       const bool softmax = (i >= L::bQFull && i < L::bQFull + 2) || (i >= L::bPFull && i < L::bPFull + 2);
-      mbar_init(&bars[i], softmax ? 4 : i == L::bKFull || i == L::bVFull ? 3 : 1);
+      mbar_init(&bars[i], softmax                                             ? 4
+                          : i == L::bKFull || i == L::bVFull || i >= L::bFree ? kWarps
+                          : i >= L::bFull                                     ? 32
+                                                                              : 1);
     }
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -658,12 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_base_sh;
 
-  if (warp < 4)
+  if (warp < 8) {
     setmaxnreg_dec<kRegsLow>();
-  else
-    setmaxnreg_inc<kRegsSoftmax>();
-  if (warp == 0) {
-    if (elect_one()) {
+    if (warp == 0 && elect_one()) {
       // ===================== MMA issuer
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
@@ -711,34 +762,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         in_sum[0] = in_sum[1] = 0;
         for (int m = 0; ok && m <= x.count; ++m) {
           const bool more = m < x.count;
-          if (x.alternate) {
-            // S runs under the softmax of the tile before
-            const int s = m & 1;
-            if (more) {
-              ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag) &&
-                   issue_s(s, 0);
-              if (ok) umma_commit(&bars[L::bKEmpty]);
-            }
-            if (ok && m > 0) {
-              ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag) &&
-                   issue_pv(1 - s);
-              if (ok) umma_commit(&bars[L::bVEmpty]);
-            }
-          } else {
-            // each slot's softmax runs under the other's MMAs
-            if (m > 0)
-              ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag) &&
-                   issue_pv(0);
-            if (ok && more)
-              ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag) &&
-                   issue_s(0, 0);
-            if (ok && m > 0) {
-              ok = issue_pv(1);
-              if (ok) umma_commit(&bars[L::bVEmpty]);
-            }
-            if (ok && more) {
-              ok = issue_s(1, 1);
-              if (ok) umma_commit(&bars[L::bKEmpty]);
+          // Both slots: P V_0, S_0, P V_1, S_1, each slot's softmax under the other's MMAs.
+          // Alternate: S of this tile, under the softmax of the one before, then its P V.
+          // (one copy of each group's code: the kernel's size costs time)
+#pragma unroll 1
+          for (int i = 0; ok && i < (x.alternate ? 2 : 4); ++i) {
+            const bool pv = (i & 1) == (x.alternate ? 1 : 0);
+            const int s = x.alternate ? (m ^ i) & 1 : i >> 1;
+            if (pv && m > 0) {
+              if (s == 0 || x.alternate)
+                ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag);
+              ok = ok && issue_pv(s);
+              if (ok && (s == 1 || x.alternate)) umma_commit(&bars[L::bVEmpty]);
+            } else if (!pv && more) {
+              if (s == 0 || x.alternate)
+                ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag);
+              ok = ok && issue_s(s, x.alternate ? 0 : s);
+              if (ok && (s == 1 || x.alternate)) umma_commit(&bars[L::bKEmpty]);
             }
           }
         }
@@ -749,20 +789,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain every MMA this thread issued before the CTA may free TMEM
       umma_commit(&bars[L::bDrain]);
       mbar_wait(&bars[L::bDrain], 0, nullptr, nullptr, 500000000ull);
+    } else if (warp == 1) {
+      Copier<D>(p, smem, bars, abort_flag).run_k(cur, steps);
+      copies_wait_all();
+    } else if (warp == 2) {
+      Copier<D>(p, smem, bars, abort_flag).run_v(steps);
+      copies_wait_all();
+    } else if (warp >= 3) {
+      Converter<D>(p, smem).run(steps, bars, abort_flag);
     }
-  } else if (warp < 4) {
-    Converter<D>(p, smem).run(cur, steps, bars, abort_flag);
   } else {
+    setmaxnreg_inc<kRegsSoftmax>();
     // ===================== softmax warpgroup of slot s
-    const int s = (warp - 4) >> 2;
-    const int row = threadIdx.x - 128 * (1 + s);
+    const int s = (warp - 8) >> 2;
+    const int row = threadIdx.x - 128 * (2 + s);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t colS = s * 128, colO = L::kColO + s * D;
     bool ok = true;
     int n_s = 0;  // key tiles of this slot so far
     int t0 = 0;   // key tiles so far
     int item = 0;
-    const uint32_t kept = smem_u32(smem + L::kCursor + (warp - 4) * 48);
+    const uint32_t kept = smem_u32(smem + L::kCursor + (warp - 8) * 48);
     keep_cursor(kept, cur);
     const uint32_t s_at = tmem + lane_base + colS, o_at = tmem + lane_base + colO;
     for (int left = steps; left > 0; ++item) {
@@ -827,11 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kTile / 32; c += 2)
           tmem_ld32x2(s_at + c * 32, s_at + (c + 1) * 32,
                       sv + c * 32, sv + (c + 1) * 32);
-        const uint32_t a0 = info.there[0], b0 = info.there[1], a1 = info.there[2],
-                       b1 = info.there[3], a2 = info.there[4], b2 = info.there[5];
-        if (info.edge || (a0 & a1 & a2) != ~0u || b0 != 0x7ffu || b1 != 0x7ffu || b2 != 0x3ffu) {
-          const uint32_t there[4] = {a0, b0 | a1 << 11, a1 >> 21 | b1 << 11 | a2 << 22,
-                                     a2 >> 10 | b2 << 22};
+        if (info.edge) {
+          const uint32_t there[4] = {info.there[0], info.there[1], info.there[2], info.there[3]};
           const auto below = [&](int j, int q) -> uint32_t {  // keys of word q before j
             const int n = min(max(j - info.j0 - 32 * q, 0), 32);
             return n == 32 ? ~0u : (1u << n) - 1;
@@ -900,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowAt a = row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row);
       const int later = x.n - x.k0 - x.count;  // steps of the item in later shares
       const bool starts = x.k0 == 0;
-      if (starts && threadIdx.x == 128)
+      if (starts && threadIdx.x == 256)
         p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
             make_int2(static_cast<int>(blockIdx.x),
                       1 + static_cast<int>((later + share.per - 1) / share.per));
