@@ -241,19 +241,26 @@ struct Copier {
     return mbar_wait_warp(&bars[bar], parity & 1, p.status, abort_flag);
   }
 
-  // Starts the copies of K's or V's codes of tile t.
-  __device__ __forceinline__ void copy(const uint8_t* codes, int t, int half,
-                                       const uint32_t (&there)[4]) const {
-    constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
+  // Starts the copies of K's or V's codes of tile t.  (One copy of the code for both
+  // warps, and a loop: what the roles of this kernel run per tile has to fit the
+  // instruction cache together.)
+  __device__ __noinline__ void copy(const uint8_t* codes, int t, int half) const {
+    constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks, kBatch = 32 / kAtOnce;
     const int chunk = lane % kChunks, r0 = lane / kChunks;
     const uint8_t* src = codes + chunk * 16;
-    const uint32_t to = mem + L::kRing + half * L::kHalf + r0 * D + chunk * 16;
-    const uint32_t rows = mem + L::kRows + (t % 3) * (kTile * 4) + r0 * 4;
-#pragma unroll 8
-    for (int i = 0; i < kTile / kAtOnce; ++i) {
-      const int r = i * kAtOnce;
-      const uint64_t from = static_cast<uint64_t>(lds32(rows + r * 4)) * D;
-      copy16(to + r * D, src + from, there[r / 32] >> (r % 32 + r0) & 1 ? 16 : 0);
+    uint32_t to = mem + L::kRing + half * L::kHalf + r0 * D + chunk * 16;
+    uint32_t rows = mem + L::kRows + (t % 3) * (kTile * 4) + r0 * 4;
+    uint32_t word = mem + L::kInfo + (t % kInfos) * 64;
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x, to += 32 * D, rows += 128, word += 4) {  // 32 keys
+      uint32_t row[kBatch];
+      const uint32_t there = lds32(word) >> r0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) row[i] = lds32(rows + i * kAtOnce * 4);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        copy16(to + i * kAtOnce * D, src + static_cast<uint64_t>(row[i]) * D,
+               there >> i * kAtOnce & 1 ? 16 : 0);
     }
     arrive_after_copies(smem_u32(&bars[L::bFull + half]));
   }
@@ -327,7 +334,7 @@ struct Copier {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::bRows + (t & 1)]);
-      copy(p.k, t, h % kHalves, there);
+      copy(p.k, t, h % kHalves);
       if (t + 1 < steps) {
         begins = ++cur.step == cur.r.n;
         if (begins) {
@@ -349,16 +356,9 @@ struct Copier {
     uint32_t top = 0;
 #pragma unroll 1
     for (int t = 0; t <= steps; ++t) {
-      if (t < steps) {
-        const int h = 2 * t + 1;
-        if (!wait(L::bRows + (t & 1), t >> 1)) return;
-        if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
-        const Info& info = reinterpret_cast<const Info*>(smem + L::kInfo)[t % kInfos];
-        const uint32_t there[4] = {info.there[0], info.there[1], info.there[2], info.there[3]};
-        copy(p.v, t, h % kHalves, there);
-      }
-      if (t == 0) continue;
+      if (t < steps && !wait(L::bRows + (t & 1), t >> 1)) return;
       // the scales of the tile before: they have had a tile's time to come
+      if (t > 0) {
       const int u = t - 1;
       if (!wait(L::bFull + 2 * u % kHalves, 2 * u / kHalves)) return;
       Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[u % kInfos];
@@ -387,6 +387,12 @@ struct Copier {
         mbar_arrive(&bars[L::bInfo + (u & 1)]);
       }
       __syncwarp();
+      }
+      if (t < steps) {
+        const int h = 2 * t + 1;
+        if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
+        copy(p.v, t, h % kHalves);
+      }
     }
   }
 };
@@ -719,17 +725,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
       bool ok = true;
-      int npv[2] = {0, 0}, nq[2] = {0, 0};  // P V issued and Q tiles taken per slot
-      int in_sum[2] = {0, 0};               // key tiles in the accumulator
-      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kK), 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kV), L::kBoxBytes, 1024);  // MN-major
-      // S_s = Q K^T of Q tile sq
-      auto issue_s = [&](int s, int sq) -> bool {
-        if (npv[s] > 0 &&
-            !mbar_wait_spin(&bars[L::bPvDone + s], (npv[s] - 1) & 1, p.status, abort_flag))
-          return false;  // its last P V still reads the P held there
+      int npv0 = 0, npv1 = 0, nq0 = 0, nq1 = 0;  // P V issued and Q tiles taken per slot
+      int sum0 = 0, sum1 = 0;                    // key tiles in the accumulators
+      // (descriptors are made where they are used: 64 registers hold few of them)
+      const uint32_t base = smem_u32(smem);
+      const auto desc_of = [&](uint32_t at, uint32_t lead) {
+        asm volatile("" : "+r"(at));
+        return sdesc_sw128(at, lead, 1024);
+      };
+      // S_s = Q K^T of Q tile sq; `done`: the slot's P V so far, the last of which still
+      // reads the P held there
+      auto issue_s = [&](int s, int sq, int done) {
+        if (done > 0)
+          ok = mbar_wait_spin(&bars[L::bPvDone + s], (done - 1) & 1, p.status, abort_flag);
+        if (!ok) return;
         tc_fence_after_sync();
-        const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQ + sq * L::kTileBytes), 16, 1024);
+        const uint64_t q_desc = desc_of(base + L::kQ + sq * L::kTileBytes, 16);
+        const uint64_t k_desc = desc_of(base + L::kK, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
@@ -737,49 +749,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                        k > 0 ? 1u : 0u);
         }
         umma_commit(&bars[L::bSFull + s]);
-        return true;
       };
       // O_s += P_s V
-      auto issue_pv = [&](int s) -> bool {
-        if (!mbar_wait_spin(&bars[L::bPFull + s], npv[s] & 1, p.status, abort_flag)) return false;
+      auto issue_pv = [&](int s, int& done, int& sum) {
+        ok = mbar_wait_spin(&bars[L::bPFull + s], done & 1, p.status, abort_flag);
+        if (!ok) return;
         tc_fence_after_sync();
-        const uint32_t acc0 = in_sum[s] > 0 ? 1u : 0u;
+        const uint32_t acc0 = sum > 0 ? 1u : 0u;
+        const uint64_t v_desc = desc_of(base + L::kV, L::kBoxBytes);  // MN-major
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           umma_bf16_ts(tmem + L::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(v_desc, k * 2048),
                        idesc_pv, k > 0 ? 1u : acc0);
         umma_commit(&bars[L::bPvDone + s]);
-        ++npv[s];
-        if (++in_sum[s] == kFlush) in_sum[s] = 0;
-        return true;
+        ++done;
+        if (++sum == kFlush) sum = 0;
       };
       int t = 0;  // key tiles so far
       for (int left = steps; ok && left > 0;) {
         const Piece x = piece_of(p, cur, left);
-        ok = mbar_wait(&bars[L::bQFull], nq[0]++ & 1, p.status, abort_flag);
-        if (ok && !x.alternate)
-          ok = mbar_wait(&bars[L::bQFull + 1], nq[1]++ & 1, p.status, abort_flag);
-        in_sum[0] = in_sum[1] = 0;
-        for (int m = 0; ok && m <= x.count; ++m) {
-          const bool more = m < x.count;
-          // Both slots: P V_0, S_0, P V_1, S_1, each slot's softmax under the other's MMAs.
-          // Alternate: S of this tile, under the softmax of the one before, then its P V.
-          // (one copy of each group's code: the kernel's size costs time)
+        const bool both = !x.alternate;
+        const int count = x.count;
+        ok = mbar_wait(&bars[L::bQFull], nq0++ & 1, p.status, abort_flag);
+        if (ok && both) ok = mbar_wait(&bars[L::bQFull + 1], nq1++ & 1, p.status, abort_flag);
+        sum0 = sum1 = 0;
+        // Both slots: P V_0, S_0, P V_1, S_1, each slot's softmax under the other's MMAs.
+        // Alternate: S of this tile, under the softmax of the one before, then its P V.
 #pragma unroll 1
-          for (int i = 0; ok && i < (x.alternate ? 2 : 4); ++i) {
-            const bool pv = (i & 1) == (x.alternate ? 1 : 0);
-            const int s = x.alternate ? (m ^ i) & 1 : i >> 1;
-            if (pv && m > 0) {
-              if (s == 0 || x.alternate)
-                ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag);
-              ok = ok && issue_pv(s);
-              if (ok && (s == 1 || x.alternate)) umma_commit(&bars[L::bVEmpty]);
-            } else if (!pv && more) {
-              if (s == 0 || x.alternate)
-                ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag);
-              ok = ok && issue_s(s, x.alternate ? 0 : s);
-              if (ok && (s == 1 || x.alternate)) umma_commit(&bars[L::bKEmpty]);
-            }
+        for (int m = 0; ok && m <= count; ++m) {
+          const bool more = m < count, even = !(m & 1);
+          const auto k_full = [&] {
+            ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag);
+          };
+          const auto v_full = [&] {
+            ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag);
+          };
+          if (both && m > 0) {
+            v_full();
+            if (ok) issue_pv(0, npv0, sum0);
+          }
+          if (ok && more && (both || even)) {
+            k_full();
+            if (ok) issue_s(0, 0, npv0);
+            if (ok && !both) umma_commit(&bars[L::bKEmpty]);
+          }
+          if (ok && m > 0 && (both || even)) {
+            if (!both) v_full();
+            if (ok) issue_pv(1, npv1, sum1);
+            if (ok) umma_commit(&bars[L::bVEmpty]);
+          }
+          if (ok && more && (both || !even)) {
+            if (!both) k_full();
+            if (ok) issue_s(1, both ? 1 : 0, npv1);
+            if (ok) umma_commit(&bars[L::bKEmpty]);
+          }
+          if (ok && !both && !even) {
+            v_full();
+            if (ok) issue_pv(0, npv0, sum0);
+            if (ok) umma_commit(&bars[L::bVEmpty]);
           }
         }
         t += x.count;
