@@ -478,9 +478,9 @@ struct Converter {
     for (int h = 0; ok && h < 2 * steps; ++h) {
       const int t = h >> 1, kv = h & 1;
       const Info& info = reinterpret_cast<const Info*>(smem + L::kInfo)[t % kInfos];
-      if (kv == 0)
-        ok = mbar_wait_warp(&bars[L::bInfo + (t & 1)], (t >> 1) & 1, p.status, abort_flag);
-      ok = ok && mbar_wait_warp(&bars[L::bFull + half], use & 1, p.status, abort_flag);
+      // (what is known of a tile is known when its K is there)
+      ok = kv == 0 ? mbar_wait_warp(&bars[L::bInfo + (t & 1)], (t >> 1) & 1, p.status, abort_flag)
+                   : mbar_wait_warp(&bars[L::bFull + half], use & 1, p.status, abort_flag);
       if (ok && t > 0)
         ok = mbar_wait_warp(&bars[kv ? L::bVEmpty : L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
       if (!ok) break;
@@ -733,12 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("" : "+r"(at));
         return sdesc_sw128(at, lead, 1024);
       };
-      // S_s = Q K^T of Q tile sq; `done`: the slot's P V so far, the last of which still
-      // reads the P held there
-      auto issue_s = [&](int s, int sq, int done) {
-        if (done > 0)
-          ok = mbar_wait_spin(&bars[L::bPvDone + s], (done - 1) & 1, p.status, abort_flag);
-        if (!ok) return;
+      // S_s = Q K^T of Q tile sq
+      auto issue_s = [&](int s, int sq) {
         tc_fence_after_sync();
         const uint64_t q_desc = desc_of(base + L::kQ + sq * L::kTileBytes, 16);
         const uint64_t k_desc = desc_of(base + L::kK, 16);
@@ -751,19 +747,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&bars[L::bSFull + s]);
       };
       // O_s += P_s V
-      auto issue_pv = [&](int s, int& done, int& sum) {
-        ok = mbar_wait_spin(&bars[L::bPFull + s], done & 1, p.status, abort_flag);
-        if (!ok) return;
+      auto issue_pv = [&](int s, uint32_t acc0) {
         tc_fence_after_sync();
-        const uint32_t acc0 = sum > 0 ? 1u : 0u;
         const uint64_t v_desc = desc_of(base + L::kV, L::kBoxBytes);  // MN-major
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           umma_bf16_ts(tmem + L::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(v_desc, k * 2048),
                        idesc_pv, k > 0 ? 1u : acc0);
         umma_commit(&bars[L::bPvDone + s]);
-        ++done;
-        if (++sum == kFlush) sum = 0;
       };
       int t = 0;  // key tiles so far
       for (int left = steps; ok && left > 0;) {
@@ -773,40 +764,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(&bars[L::bQFull], nq0++ & 1, p.status, abort_flag);
         if (ok && both) ok = mbar_wait(&bars[L::bQFull + 1], nq1++ & 1, p.status, abort_flag);
         sum0 = sum1 = 0;
-        // Both slots: P V_0, S_0, P V_1, S_1, each slot's softmax under the other's MMAs.
-        // Alternate: S of this tile, under the softmax of the one before, then its P V.
+        // S of tile m and P V of tile m - 1, of the slots that work on them, each as soon
+        // as what it reads is there (a slot's S after its P V, which reads the P there):
+        // the conversion of K and V, of which there is one tile each, waits for them
+        // (P V_0, S_0, P V_1, S_1 in this order: 6,700 clocks a tile against FIXME)
 #pragma unroll 1
         for (int m = 0; ok && m <= count; ++m) {
-          const bool more = m < count, even = !(m & 1);
-          const auto k_full = [&] {
-            ok = mbar_wait_spin(&bars[L::bKFull], (t + m) & 1, p.status, abort_flag);
-          };
-          const auto v_full = [&] {
-            ok = mbar_wait_spin(&bars[L::bVFull], (t + m - 1) & 1, p.status, abort_flag);
-          };
-          if (both && m > 0) {
-            v_full();
-            if (ok) issue_pv(0, npv0, sum0);
-          }
-          if (ok && more && (both || even)) {
-            k_full();
-            if (ok) issue_s(0, 0, npv0);
-            if (ok && !both) umma_commit(&bars[L::bKEmpty]);
-          }
-          if (ok && m > 0 && (both || even)) {
-            if (!both) v_full();
-            if (ok) issue_pv(1, npv1, sum1);
-            if (ok) umma_commit(&bars[L::bVEmpty]);
-          }
-          if (ok && more && (both || !even)) {
-            if (!both) k_full();
-            if (ok) issue_s(1, both ? 1 : 0, npv1);
-            if (ok) umma_commit(&bars[L::bKEmpty]);
-          }
-          if (ok && !both && !even) {
-            v_full();
-            if (ok) issue_pv(0, npv0, sum0);
-            if (ok) umma_commit(&bars[L::bVEmpty]);
+          // bits 0, 1: S of the slots to be issued, 2, 3: P V
+          uint32_t todo = both ? (m < count ? 3u : 0u) | (m > 0 ? 12u : 0u)
+                               : (m < count ? 1u << (m & 1) : 0u) | (m > 0 ? 8u >> (m & 1) : 0u);
+          bool k_full = false, v_full = false;
+          uint64_t t0 = 0;
+          int idle = 0;
+          while (todo) {
+            bool some = false;
+            if (!v_full && (todo & 12)) v_full = mbar_test_wait(&bars[L::bVFull], (t + m - 1) & 1);
+            if (!k_full && (todo & 3)) k_full = mbar_test_wait(&bars[L::bKFull], (t + m) & 1);
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+              const int npv = s ? npv1 : npv0;
+              if ((todo >> s & 4) && v_full && mbar_test_wait(&bars[L::bPFull + s], npv & 1)) {
+                int sum = s ? sum1 : sum0;
+                issue_pv(s, sum > 0 ? 1u : 0u);
+                if (++sum == kFlush) sum = 0;
+                if (s) {
+                  ++npv1;
+                  sum1 = sum;
+                } else {
+                  ++npv0;
+                  sum0 = sum;
+                }
+                todo &= ~(4u << s);
+                if (!(todo & 12)) umma_commit(&bars[L::bVEmpty]);
+                some = true;
+              } else if ((todo >> s & 1) && !(todo >> s & 4) && k_full &&
+                         (npv == 0 || mbar_test_wait(&bars[L::bPvDone + s], (npv - 1) & 1))) {
+                issue_s(s, both ? s : 0);
+                todo &= ~(1u << s);
+                if (!(todo & 3)) umma_commit(&bars[L::bKEmpty]);
+                some = true;
+              }
+            }
+            // bounded, as every wait
+            if (some) {
+              idle = 0;
+            } else if ((++idle & 63) == 0) {
+              const uint64_t now = globaltimer_ns();
+              if (idle == 64) t0 = now;
+              if (*reinterpret_cast<volatile int*>(abort_flag) || now - t0 > 2000000000ull) {
+                if (now - t0 > 2000000000ull) {
+                  atomicExch(p.status, DEV_TIMEOUT);
+                  *reinterpret_cast<volatile int*>(abort_flag) = 1;
+                }
+                ok = false;
+                break;
+              }
+            }
           }
         }
         t += x.count;
