@@ -18,11 +18,14 @@
 // 0.  P is p 2^11, rounded to 2^-11 of itself (2^-36 of the row's largest at least).
 //
 // Keys.  One warp looks the pages up and starts the copies of K's codes and the scale
-// bytes into a ring of five half tiles, about 66 KB ahead, another those of V's (cp.async:
-// one bulk copy per key takes 58 clocks of the issuing warp each); five warps write K and V as f16 into the one 128-byte-swizzled tile that each has: S(t) of both
-// slots is done long before K(t + 1) is wanted, and P V(t) before V(t + 1).  One thread
-// issues the MMAs, two warpgroups do the softmax, a row per thread, as in the training
-// forward.
+// bytes into a ring of three half tiles, another those of V's (cp.async: one bulk copy
+// per key takes 58 clocks of the issuing warp each); five warps write K and V as f16
+// into 128-byte-swizzled tiles: one for K (S(t) of both slots is done long before
+// K(t + 1) is wanted) and two for V.  An alternate piece, which has one Q tile, puts
+// every other K in the place of the second.  A handover between warps takes 300 to 400
+// clocks, and with one V tile the round P V, conversion, P V was the longest chain.
+// One thread issues the MMAs, two warpgroups do the softmax, a row per thread, as in
+// the training forward.
 //
 // Keys that a row does not read are masked.  Where some row of the pair does not read
 // a key of a tile, NaN in V is written as 0 and remembered: the rows that read it are
@@ -49,7 +52,7 @@ constexpr float kThreshold = 4.f;  // log2: a row's maximum may lag by that
 constexpr float kShift = 11.f;     // P = p 2^11
 constexpr int kHeadroom = 6;       // K and V operands: codes times up to 2^6
 constexpr int kFlush = 512;        // key tiles that one accumulator takes in
-constexpr int kHalves = 5;         // of the ring
+constexpr int kHalves = 3;         // of the ring
 constexpr int kInfos = 8;
 // Per-warpgroup register budgets (setmaxnreg): issuer, copies and converters, softmax.  Their
 // sum must not exceed the launch allocation (checked on the host).
@@ -65,18 +68,19 @@ struct Tiles {
   static constexpr int kQ = 0;                      // 2 slots
   static constexpr int kK = kQ + 2 * kTileBytes;
   static constexpr int kV = kK + kTileBytes;
-  static constexpr int kRing = kV + kTileBytes;
+  static constexpr int kRing = kV + 2 * kTileBytes;
   static constexpr int kWords = kRing + kHalves * kHalf;  // [3 tiles][K, V][key] scale words
   static constexpr int kInfo = kWords + 3 * 2 * kTile * 4;
   static constexpr int kRows = kInfo + kInfos * 64;  // [3 tiles][key] place in the cache
   static constexpr int kBar = kRows + 3 * kTile * 4;
+  // barriers; those of K and V are [2] by tile
   static constexpr int bQFull = 0;                  // [2] per slot
-  static constexpr int bKFull = 2, bKEmpty = 3, bVFull = 4, bVEmpty = 5;
-  static constexpr int bSFull = 6, bPFull = 8, bPvDone = 10;  // [2]
-  static constexpr int bDrain = 12;
-  static constexpr int bInfo = 13;                  // [2] by tile
-  static constexpr int bRows = 15;                  // [2] by tile: places of its keys
-  static constexpr int bFull = 17;                  // [kHalves] codes are there
+  static constexpr int bKFull = 2, bKEmpty = 4, bVFull = 6, bVEmpty = 8;
+  static constexpr int bSFull = 10, bPFull = 12, bPvDone = 14;  // [2] per slot
+  static constexpr int bDrain = 16;
+  static constexpr int bInfo = 17;                  // [2] by tile
+  static constexpr int bRows = 19;                  // [2] by tile: places of its keys
+  static constexpr int bFull = 21;                  // [kHalves] codes are there
   static constexpr int bFree = bFull + kHalves;     // and have been converted
   static constexpr int kBars = bFree + kHalves;
   static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
@@ -98,7 +102,9 @@ struct Info {
   int upper;          // the scale bytes are the upper half of their words
   int item;           // the CTA's pieces so far
   int first;          // of a piece
-  int pad[4];
+  int k_at;           // where K goes
+  int k_after;        // the tile whose S has to be done by then
+  int pad[2];
 };
 static_assert(sizeof(Info) == 64, "");
 
@@ -278,19 +284,21 @@ struct Copier {
         if (j < end) page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
       }
     };
-    int item = 0, hi = 0, lo = 0;
-    bool begins = true;
+    int item = 0, hi = 0, lo = 0, m = 0;
+    bool begins = true, alternate = false;
     look();
 #pragma unroll 1
     for (int t = 0; t < steps; ++t) {
-      // (the places and scale words of tile t - 3 have been used: V(t - 3) is converted,
-      // and K's half tile is free)
+      // (V(t - 2), which had K's half tile, has been converted: so the places and scale
+      // words of tile t - 3 are free too)
       const int h = 2 * t;
-      if (t >= 3 && !wait(L::bFree + (h - 5) % kHalves, (h - 5) / kHalves)) return;
+      if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
       Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
       if (begins) {  // keys that all rows of the pair read
         const int first = (cur.entry - cur.b * p.row_tiles) * kPairRows;
         const int last = min(first + kPairRows, p.queries * p.G) - 1;
+        alternate = last - first < kTile;
+        m = 0;
         hi = p.causal ? cur.r.c - p.queries + static_cast<int>(p.by_G(first)) + 1 : cur.r.c;
         lo = p.window ? cur.r.c - p.queries + static_cast<int>(p.by_G(last)) - p.window + 1 : 0;
       }
@@ -331,7 +339,12 @@ struct Copier {
         info.upper = D == 64 && p.wide_scales && (cur.block & 1);
         info.item = item;
         info.first = begins;
+        // (the second Q tile is free when the piece before is done, and its MMAs are
+        // when the first S of this piece is)
+        info.k_at = alternate && (m & 1) ? L::kQ + L::kTileBytes : L::kK;
+        info.k_after = alternate && m > 1 ? t - 2 : t - 1;
       }
+      ++m;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::bRows + (t & 1)]);
       copy(p.k, t, h % kHalves);
@@ -355,18 +368,19 @@ struct Copier {
   __device__ __forceinline__ void run_v(int steps) {
     uint32_t top = 0;
 #pragma unroll 1
-    for (int t = 0; t <= steps; ++t) {
-      if (t < steps && !wait(L::bRows + (t & 1), t >> 1)) return;
-      // the scales of the tile before: they have had a tile's time to come
-      if (t > 0) {
-      const int u = t - 1;
-      if (!wait(L::bFull + 2 * u % kHalves, 2 * u / kHalves)) return;
-      Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[u % kInfos];
+    for (int t = 0; t < steps; ++t) {
+      const int h = 2 * t + 1;
+      if (!wait(L::bRows + (t & 1), t >> 1)) return;
+      if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
+      copy(p.v, t, h % kHalves);
+      // the scales
+      if (!wait(L::bFull + (h - 1) % kHalves, (h - 1) / kHalves)) return;
+      Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
       const bool upper = D == 64 && info.upper, begins = info.first;
       uint32_t k = 0, v = 0;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        uint32_t a = word(u, 0, lane + 32 * x, upper), b = word(u, 1, lane + 32 * x, upper);
+        uint32_t a = word(t, 0, lane + 32 * x, upper), b = word(t, 1, lane + 32 * x, upper);
         if (any_byte_255(a) || any_byte_255(b)) {
           a &= ~__vcmpeq4(a, 0xffffffffu);
           b &= ~__vcmpeq4(b, 0xffffffffu);
@@ -384,15 +398,9 @@ struct Copier {
         info.k_top = k;
         info.top = top;
         if (begins) reinterpret_cast<volatile int*>(smem + L::kRedo)[info.item % kInfos] = 0;
-        mbar_arrive(&bars[L::bInfo + (u & 1)]);
+        mbar_arrive(&bars[L::bInfo + (t & 1)]);
       }
       __syncwarp();
-      }
-      if (t < steps) {
-        const int h = 2 * t + 1;
-        if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
-        copy(p.v, t, h % kHalves);
-      }
     }
   }
 };
@@ -481,14 +489,16 @@ struct Converter {
       // (what is known of a tile is known when its K is there)
       ok = kv == 0 ? mbar_wait_warp(&bars[L::bInfo + (t & 1)], (t >> 1) & 1, p.status, abort_flag)
                    : mbar_wait_warp(&bars[L::bFull + half], use & 1, p.status, abort_flag);
-      if (ok && t > 0)
-        ok = mbar_wait_warp(&bars[kv ? L::bVEmpty : L::bKEmpty], (t - 1) & 1, p.status, abort_flag);
+      const int after = kv ? t - 2 : info.k_after;
+      if (ok && after >= 0)
+        ok = mbar_wait_warp(&bars[(kv ? L::bVEmpty : L::bKEmpty) + (after & 1)], after >> 1 & 1,
+                            p.status, abort_flag);
       if (!ok) break;
       const uint32_t from = mem + L::kRing + half * L::kHalf;
       const uint32_t bytes = mem + L::kWords + ((t % 3) * 2 + kv) * (kTile * 4) +
                              (D == 64 && info.upper ? 2 : 0);
       const uint32_t top = kv ? info.top : info.k_top * 0x01010101u;
-      const uint32_t tile = mem + (kv ? L::kV : L::kK);
+      const uint32_t tile = mem + (kv ? L::kV + (t & 1) * L::kTileBytes : info.k_at);
       if (kv && info.edge) {
         if (convert<true>(from, bytes, top, tile))
           reinterpret_cast<volatile int*>(smem + L::kRedo)[info.item % kInfos] = 1;
@@ -498,7 +508,7 @@ struct Converter {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&bars[kv ? L::bVFull : L::bKFull]);
+        mbar_arrive(&bars[(kv ? L::bVFull : L::bKFull) + (t & 1)]);
         mbar_arrive(&bars[L::bFree + half]);
       }
       if (++half == kHalves) {
@@ -697,14 +707,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (share.begin >= share.end) return;
   const int steps = static_cast<int>(share.end - share.begin);
   if (threadIdx.x == 0) {
-    // arrivals: converter warps, a slot's softmax warps, the copying lanes,
-    // else one arrival or commit
+    // arrivals: converter warps, a slot's softmax warps, the copying lanes, else one
+    // arrival or commit
     for (int i = 0; i < L::kBars; ++i) {
-      const bool softmax = (i >= L::bQFull && i < L::bQFull + 2) || (i >= L::bPFull && i < L::bPFull + 2);
-      mbar_init(&bars[i], softmax                                             ? 4
-                          : i == L::bKFull || i == L::bVFull || i >= L::bFree ? kWarps
-                          : i >= L::bFull                                     ? 32
-                                                                              : 1);
+      const auto is = [&](int bar) { return i == bar || i == bar + 1; };
+      mbar_init(&bars[i], is(L::bQFull) || is(L::bPFull)                   ? 4
+                          : is(L::bKFull) || is(L::bVFull) || i >= L::bFree ? kWarps
+                          : i >= L::bFull                                   ? 32
+                                                                            : 1);
     }
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -734,10 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return sdesc_sw128(at, lead, 1024);
       };
       // S_s = Q K^T of Q tile sq
-      auto issue_s = [&](int s, int sq) {
+      auto issue_s = [&](int s, int sq, int k_at) {
         tc_fence_after_sync();
         const uint64_t q_desc = desc_of(base + L::kQ + sq * L::kTileBytes, 16);
-        const uint64_t k_desc = desc_of(base + L::kK, 16);
+        const uint64_t k_desc = desc_of(base + k_at, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
@@ -747,9 +757,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&bars[L::bSFull + s]);
       };
       // O_s += P_s V
-      auto issue_pv = [&](int s, uint32_t acc0) {
+      auto issue_pv = [&](int s, int v_at, uint32_t acc0) {
         tc_fence_after_sync();
-        const uint64_t v_desc = desc_of(base + L::kV, L::kBoxBytes);  // MN-major
+        const uint64_t v_desc = desc_of(base + v_at, L::kBoxBytes);  // MN-major
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           umma_bf16_ts(tmem + L::kColO + s * D, tmem + s * 128 + k * 8, sdesc_step(v_desc, k * 2048),
@@ -766,8 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum0 = sum1 = 0;
         // S of tile m and P V of tile m - 1, of the slots that work on them, each as soon
         // as what it reads is there (a slot's S after its P V, which reads the P there):
-        // the conversion of K and V, of which there is one tile each, waits for them
-        // (P V_0, S_0, P V_1, S_1 in this order: 6,700 clocks a tile against FIXME)
+        // the conversion of K and V waits for them
 #pragma unroll 1
         for (int m = 0; ok && m <= count; ++m) {
           // bits 0, 1: S of the slots to be issued, 2, 3: P V
@@ -778,14 +787,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           int idle = 0;
           while (todo) {
             bool some = false;
-            if (!v_full && (todo & 12)) v_full = mbar_test_wait(&bars[L::bVFull], (t + m - 1) & 1);
-            if (!k_full && (todo & 3)) k_full = mbar_test_wait(&bars[L::bKFull], (t + m) & 1);
+            const int tk = t + m, tv = t + m - 1;  // K's and V's tile
+            if (!v_full && (todo & 12))
+              v_full = mbar_test_wait(&bars[L::bVFull + (tv & 1)], tv >> 1 & 1);
+            if (!k_full && (todo & 3))
+              k_full = mbar_test_wait(&bars[L::bKFull + (tk & 1)], tk >> 1 & 1);
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
               const int npv = s ? npv1 : npv0;
               if ((todo >> s & 4) && v_full && mbar_test_wait(&bars[L::bPFull + s], npv & 1)) {
                 int sum = s ? sum1 : sum0;
-                issue_pv(s, sum > 0 ? 1u : 0u);
+                issue_pv(s, L::kV + (tv & 1) * L::kTileBytes, sum > 0 ? 1u : 0u);
                 if (++sum == kFlush) sum = 0;
                 if (s) {
                   ++npv1;
@@ -795,13 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   sum0 = sum;
                 }
                 todo &= ~(4u << s);
-                if (!(todo & 12)) umma_commit(&bars[L::bVEmpty]);
+                if (!(todo & 12)) umma_commit(&bars[L::bVEmpty + (tv & 1)]);
                 some = true;
               } else if ((todo >> s & 1) && !(todo >> s & 4) && k_full &&
                          (npv == 0 || mbar_test_wait(&bars[L::bPvDone + s], (npv - 1) & 1))) {
-                issue_s(s, both ? s : 0);
+                issue_s(s, both ? s : 0, !both && (m & 1) ? L::kQ + L::kTileBytes : L::kK);
                 todo &= ~(1u << s);
-                if (!(todo & 3)) umma_commit(&bars[L::bKEmpty]);
+                if (!(todo & 3)) umma_commit(&bars[L::bKEmpty + (tk & 1)]);
                 some = true;
               }
             }
