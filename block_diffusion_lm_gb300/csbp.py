@@ -80,7 +80,8 @@ class RotaryStruct(ctypes.Structure):
 
 
 class AppendQueries(ctypes.Structure):
-    _fields_ = [("Hq", ctypes.c_int32), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    _fields_ = [("Hq", ctypes.c_int32), ("clear", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("out", ctypes.c_void_p),
                 ("stride_tok", ctypes.c_int64 * 2), ("stride_batch", ctypes.c_int64 * 2)]
 
 
@@ -886,7 +887,7 @@ class QuantCache:
             ot = ob = 0
             if out is not None:
                 _, ot, ob = c.strided("out", out, shape)
-            qs = AppendQueries(q.shape[2], None, None, (qt, ot), (qb, ob))
+            qs = AppendQueries(q.shape[2], 1 if out is None else 0, None, None, (qt, ot), (qb, ob))
 
         def check():
             return (*self._check(fn, k, v, table, start, count, more), qs)
@@ -894,8 +895,8 @@ class QuantCache:
         turns = rotary.turns if isinstance(rotary, Rotary) else None
         r, dev, qs = _layout(fn, self._key, (k, v, table, start, count, q, out, turns), check)
         if q is not None and out is None:
-            make = torch.zeros if count is not None else torch.empty
-            out, = _fresh(stream, lambda: (make(q.shape, dtype=q.dtype, device=q.device),))
+            out, = _fresh(stream, lambda: (
+                torch.empty(q.shape, dtype=q.dtype, device=q.device),))
         if r is None:
             return out
         r = CacheRows.from_buffer_copy(r)

@@ -46,8 +46,9 @@ struct AppendArgs {
   __nv_bfloat16* q_out;
   int64_t q_tok[2], q_bat[2];
   int32_t lanes;             // of a head: d / 16, up to the next power of two
-  int32_t kv_steps, steps;   // steps of a warp for K (and for V), and for all
-  int32_t parts;             // warps that share a token's steps
+  int32_t kv_steps, q_steps;  // steps of a warp for K (and for V), and for Q
+  int32_t parts;              // warps that share a token's steps
+  int32_t clear;              // rows of q_out that take no part become zeros
 };
 
 // 2 x 8 bf16 values of a lane as they lie in memory.
@@ -106,16 +107,21 @@ __device__ __forceinline__ void rotate(T* lo, T* hi, const T* c, const T* s, boo
   }
 }
 
+struct Encoded {
+  int byte[2];
+  uint2 code[2];
+};
+
 // The lane's 16 rotated K values in 64 bits, their groups' scale bytes and the
 // codes.  The whole warp calls it; `top` is the warp's room for the largest
 // magnitude of each chunk of 8 features.
-__device__ __noinline__ void encode_exact(const uint64_t* turns, int64_t pos, bool turned,
-                                          bool interleaved, const Raw* raw, int c0, int c1,
-                                          double* top, int* byte, uint2* code) {
+__device__ __noinline__ Encoded encode_exact(const uint64_t* turns, int64_t pos, bool turned,
+                                             bool interleaved, Raw raw, int c0, int c1,
+                                             double* top) {
   double lo[8], hi[8];
   for (int e = 0; e < 8; ++e) {
-    lo[e] = value(raw->lo, e);
-    hi[e] = value(raw->hi, e);
+    lo[e] = value(raw.lo, e);
+    hi[e] = value(raw.hi, e);
   }
   if (turned) {
     double c[8], s[8];
@@ -135,6 +141,7 @@ __device__ __noinline__ void encode_exact(const uint64_t* turns, int64_t pos, bo
     if (f0[e] == f0[e]) m0 = fmax(m0, fabs(lo[e]));
     if (f1[e] == f1[e]) m1 = fmax(m1, fabs(hi[e]));
   }
+  __syncwarp();
   top[c0] = m0;
   top[c1] = m1;
   __syncwarp();
@@ -143,15 +150,27 @@ __device__ __noinline__ void encode_exact(const uint64_t* turns, int64_t pos, bo
     m1 = fmax(m1, top[c1 ^ e]);
   }
   __syncwarp();
-  byte[0] = scale_byte(m0);
-  byte[1] = scale_byte(m1);
-  code[0] = encode8(f0, byte[0]);
-  code[1] = encode8(f1, byte[1]);
+  Encoded r;
+  r.byte[0] = scale_byte(m0);
+  r.byte[1] = scale_byte(m1);
+  r.code[0] = encode8(f0, r.byte[0]);
+  r.code[1] = encode8(f1, r.byte[1]);
+  return r;
 }
 
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
-  // per chunk of 8 features of the heads in a step: 16 lanes' worth each of
-  // magnitude and pair size (or of 64-bit magnitudes)
+// A lane's two chunks of a head.
+__device__ __forceinline__ Raw load(const __nv_bfloat16* row, int x0, int x1, bool has) {
+  Raw r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (has) {
+    r.lo = reinterpret_cast<const uint4*>(row)[x0];
+    r.hi = reinterpret_cast<const uint4*>(row)[x1];
+  }
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+  // per chunk of 8 features of the heads in a step: magnitude and pair size (or a
+  // 64-bit magnitude)
   __shared__ __align__(16) float2 room[kWarps][64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -162,49 +181,92 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
   r.b = static_cast<int>(b);
   r.i = static_cast<int>(token - b * a.c.rows);
   // the same for the whole warp
-  if (b >= a.c.batch || (a.c.count && r.i >= __ldg(a.c.count + r.b))) return;
+  if (b >= a.c.batch) return;
+  r.takes_part = !a.c.count || r.i < __ldg(a.c.count + r.b);
+  const int at_once = 32 / a.lanes;
+  const int l = lane & (a.lanes - 1), head0 = lane / a.lanes;
+  const bool here = l < a.d / 16, turned = l < a.turned;
+  // chunks of 8 features that the lane holds: a chunk and the one that it is rotated
+  // with, or neighbours
+  const bool split = turned && !a.interleaved;
+  const int c0 = split ? l : 2 * l, c1 = split ? l + a.turned : 2 * l + 1;
+  __nv_bfloat16* const out = a.q_out + r.b * a.q_bat[1] + r.i * a.q_tok[1];
+  if (!r.takes_part) {
+    if (a.clear)
+      for (int step = part; step < a.q_steps; step += a.parts) {
+        const int head = step * at_once + head0;
+        if (!here || head >= a.Hq) continue;
+        uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(head) * a.d);
+        dst[c0] = dst[c1] = make_uint4(0, 0, 0, 0);
+      }
+    return;
+  }
   const int64_t slot = slot_of(a.c, r);
   const int64_t pos = static_cast<int64_t>(__ldg(a.c.start + r.b)) + r.i;
 
-  const int l = lane & (a.lanes - 1), head0 = lane / a.lanes, at_once = 32 / a.lanes;
-  const bool here = l < a.d / 16, turned = l < a.turned;
-  // chunks of 8 features that the lane holds
-  const bool split = turned && !a.interleaved;
-  const int c0 = split ? l : 2 * l, c1 = split ? l + a.turned : 2 * l + 1;
   const uint64_t* turns = a.turns + 8 * l;
   float cosine[8], sine[8];
-  bool angles = false;
-
-  const int chunks = 2 * a.lanes;  // of a head, in `room`
-  float2* mine = room[warp] + head0 * chunks;
-  for (int step = part; step < a.steps; step += a.parts) {
-    const int kind = step < a.kv_steps ? 0 : step < 2 * a.kv_steps ? 1 : 2;  // K, V, Q
-    const int head = (step - kind * a.kv_steps) * at_once + head0;
-    if (kind < 2 && slot < 0) continue;
-    const bool has = here && head < (kind == 2 ? a.Hq : a.Hkv);
-    const bool turn = kind != 1 && turned;
-    const int x0 = kind == 1 ? 2 * l : c0, x1 = kind == 1 ? 2 * l + 1 : c1;
-    Raw raw{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (has) {
-      const __nv_bfloat16* src =
-          (kind == 2 ? a.q + r.b * a.q_bat[0] + r.i * a.q_tok[0]
-                     : (kind ? a.c.src[1] + r.b * a.c.bat[1] + r.i * a.c.tok[1]
-                             : a.c.src[0] + r.b * a.c.bat[0] + r.i * a.c.tok[0])) +
-          static_cast<int64_t>(head) * a.d;
-      raw.lo = reinterpret_cast<const uint4*>(src)[x0];
-      raw.hi = reinterpret_cast<const uint4*>(src)[x1];
-    }
-    if (!angles && kind != 1) {
-      angles = true;
-      if (turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(turns + e);
-          sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sine[e],
-                    &cosine[e]);
-        }
-      }
+  for (int e = 0; e < 8; ++e) {
+    cosine[e] = 1.f;
+    sine[e] = 0.f;
+    if (turned) {
+      const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(turns + e);
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sine[e],
+                &cosine[e]);
     }
+  }
+
+  // ------- Q, two heads of a lane at a time
+  const __nv_bfloat16* q = a.q + r.b * a.q_bat[0] + r.i * a.q_tok[0];
+#pragma unroll 1
+  for (int step = part; step < a.q_steps; step += 2 * a.parts) {
+    Raw raw[2];
+    bool has[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int head = (step + k * a.parts) * at_once + head0;
+      has[k] = here && head < a.Hq;
+      raw[k] = load(q + static_cast<int64_t>(head) * a.d, c0, c1, has[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!has[k]) continue;
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = value(raw[k].lo, e);
+        hi[e] = value(raw[k].hi, e);
+      }
+      if (turned) rotate(lo, hi, cosine, sine, a.interleaved != 0);
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(lo[2 * e], lo[2 * e + 1]);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(hi[2 * e], hi[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&x);
+        w[4 + e] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(
+          out + static_cast<int64_t>((step + k * a.parts) * at_once + head0) * a.d);
+      dst[c0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[c1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+  if (slot < 0) return;  // the same for the whole warp
+
+  // ------- K and V
+  float2* mine = room[warp] + head0 * 2 * a.lanes;
+#pragma unroll 1
+  for (int step = part; step < 2 * a.kv_steps; step += a.parts) {
+    const bool v = step >= a.kv_steps, turn = !v && turned;
+    const int head = (v ? step - a.kv_steps : step) * at_once + head0;
+    const bool has = here && head < a.Hkv;
+    const int x0 = v ? 2 * l : c0, x1 = v ? 2 * l + 1 : c1;
+    const __nv_bfloat16* src = (v ? a.c.src[1] + r.b * a.c.bat[1] + r.i * a.c.tok[1]
+                                  : a.c.src[0] + r.b * a.c.bat[0] + r.i * a.c.tok[0]) +
+                               static_cast<int64_t>(head) * a.d;
+    const Raw raw = load(src, x0, x1, has);
     float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -225,23 +287,6 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
         n1 = n0;
       }
       rotate(lo, hi, cosine, sine, a.interleaved != 0);
-    }
-    if (kind == 2) {
-      if (has) {
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 x = __floats2bfloat162_rn(lo[2 * e], lo[2 * e + 1]);
-          const __nv_bfloat162 y = __floats2bfloat162_rn(hi[2 * e], hi[2 * e + 1]);
-          w[e] = *reinterpret_cast<const uint32_t*>(&x);
-          w[4 + e] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(a.q_out + r.b * a.q_bat[1] + r.i * a.q_tok[1] +
-                                              static_cast<int64_t>(head) * a.d);
-        dst[x0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[x1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
-      continue;
     }
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -264,31 +309,28 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       m1 = fmaxf(m1, y.x);
       n1 = fmaxf(n1, y.y);
     }
-    int byte[2] = {scale_byte(m0), scale_byte(m1)};
-    uint2 code[2];
-    bool near = false;
-    if (kind == 0) {  // twice the bound on the error of a rotated value
-      n0 *= 0x1p-20f;
-      n1 *= 0x1p-20f;
-      near = scale_byte(m0 + n0) != scale_byte(fmaxf(m0 - n0, 0.f)) ||
-             scale_byte(m1 + n1) != scale_byte(fmaxf(m1 - n1, 0.f));
-    }
+    Encoded r;
+    r.byte[0] = scale_byte(m0);
+    r.byte[1] = scale_byte(m1);
+    n0 *= 0x1p-20f;  // twice the bound on the error of a rotated value; 0 for V
+    n1 *= 0x1p-20f;
+    const bool near = scale_byte(m0 + n0) != scale_byte(fmaxf(m0 - n0, 0.f)) ||
+                      scale_byte(m1 + n1) != scale_byte(fmaxf(m1 - n1, 0.f));
     if (__any_sync(0xffffffffu, near)) {
-      __syncwarp();
-      encode_exact(turns, pos, turn, a.interleaved != 0, &raw, x0, x1,
-                   reinterpret_cast<double*>(mine), byte, code);
+      r = encode_exact(turns, pos, turn, a.interleaved != 0, raw, x0, x1,
+                       reinterpret_cast<double*>(mine));
     } else {
-      code[0] = encode8(lo, byte[0]);
-      code[1] = encode8(hi, byte[1]);
+      r.code[0] = encode8(lo, r.byte[0]);
+      r.code[1] = encode8(hi, r.byte[1]);
     }
     if (!has) continue;
     const int64_t row = slot * a.Hkv + head;
-    uint8_t* codes = (kind ? a.c.codes[1] : a.c.codes[0]) + row * a.d;
-    uint8_t* scales = (kind ? a.c.scales[1] : a.c.scales[0]) + row * (a.d / kGroup);
-    reinterpret_cast<uint2*>(codes)[x0] = code[0];
-    reinterpret_cast<uint2*>(codes)[x1] = code[1];
-    if ((x0 & 3) == 0) scales[x0 >> 2] = static_cast<uint8_t>(byte[0]);
-    if ((x1 & 3) == 0) scales[x1 >> 2] = static_cast<uint8_t>(byte[1]);
+    uint8_t* codes = (v ? a.c.codes[1] : a.c.codes[0]) + row * a.d;
+    uint8_t* scales = (v ? a.c.scales[1] : a.c.scales[0]) + row * (a.d / kGroup);
+    reinterpret_cast<uint2*>(codes)[x0] = r.code[0];
+    reinterpret_cast<uint2*>(codes)[x1] = r.code[1];
+    if ((x0 & 3) == 0) scales[x0 >> 2] = static_cast<uint8_t>(r.byte[0]);
+    if ((x1 & 3) == 0) scales[x1 >> 2] = static_cast<uint8_t>(r.byte[1]);
   }
 }
 
@@ -328,7 +370,8 @@ extern "C" csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_
       rotary->interleaved < 0 || rotary->interleaved > 1 || !rotary->turns ||
       !aligned(rotary->turns, 8))
     return CSBP_ERR_INVALID;
-  if (queries && queries->Hq < 0) return CSBP_ERR_INVALID;
+  if (queries && (queries->Hq < 0 || queries->clear < 0 || queries->clear > 1))
+    return CSBP_ERR_INVALID;
   if (a.c.batch == 0) return CSBP_OK;
   if (cache->d > kMaxD) return CSBP_ERR_UNSUPPORTED;
   a.c.src[0] = static_cast<const __nv_bfloat16*>(k);
@@ -343,6 +386,7 @@ extern "C" csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_
       return CSBP_ERR_INVALID;
     if (queries->Hq > 65536) return CSBP_ERR_UNSUPPORTED;
     a.Hq = queries->Hq;
+    a.clear = queries->clear;
     a.q = static_cast<const __nv_bfloat16*>(queries->q);
     a.q_out = static_cast<__nv_bfloat16*>(queries->out);
     const int64_t row = static_cast<int64_t>(a.Hq) * a.d;
@@ -364,7 +408,7 @@ extern "C" csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_
   while (a.lanes * 16 < a.d) a.lanes *= 2;
   const int at_once = 32 / a.lanes;
   a.kv_steps = (a.Hkv + at_once - 1) / at_once;
-  a.steps = 2 * a.kv_steps + (a.Hq + at_once - 1) / at_once;
+  a.q_steps = (a.Hq + at_once - 1) / at_once;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -372,7 +416,7 @@ extern "C" csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_
   // few tokens are shared among warps, up to 16 per SM: then latency counts
   const int64_t tokens = static_cast<int64_t>(a.c.batch) * a.c.rows;
   a.parts = static_cast<int32_t>(
-      std::max<int64_t>(1, std::min<int64_t>(a.steps, 16 * sms / tokens)));
+      std::max<int64_t>(1, std::min<int64_t>(2 * a.kv_steps + a.q_steps, 16 * sms / tokens)));
   const int64_t grid = (tokens * a.parts + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
   const int timed = timer_begin(11, stream);

@@ -117,7 +117,8 @@ csbp_status csbp_rotary_turns(const double* freq, int32_t n, uint64_t* turns);
  * stride_tok / stride_batch of q (0) and out (1) as in csbp_inputs.  out may be
  * q itself (with the same strides).                                        */
 typedef struct {
-  int32_t Hq;  /* 0: none */
+  int32_t Hq;     /* 0: none */
+  int32_t clear;  /* 1: rows of out that take no part become zeros */
   const void* q;
   void* out;
   int64_t stride_tok[2], stride_batch[2];
@@ -129,7 +130,7 @@ typedef struct {
  * bf16 in between; a pair with a NaN or an infinity in it, or a value past
  * fp32's range, is stored as NaN.  Queries of the rows that take part (i <
  * count[b]) are rotated whatever their position or page; others keep what they
- * hold in `out`.  d is at most 512.  `queries` may be NULL.                 */
+ * hold in `out` (or become zeros: `clear`).  d is at most 512.  `queries` may be NULL.                 */
 csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_cache_rows* rows,
                               const csbp_rotary* rotary, const void* k, const void* v,
                               const csbp_append_queries* queries, void* stream);
