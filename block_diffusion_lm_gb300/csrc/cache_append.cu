@@ -11,12 +11,14 @@
 // Scales.  A rotated value has an error of up to 2^-21 (|a| + |b|) in fp32, which
 // is nothing to its code, but could decide a scale where the group's largest
 // magnitude lies next to 448 x 2^e.  Such groups (one in 10^5) are worked out
-// again in 64 bits, so that the scale is that of the rotation itself.
+// again in 64 bits, so that the scale is that of the rotation itself; after the
+// others, as a call among them cost the loop 50 registers.
 //
 // HBM bounds it: 3 + 1/32 bytes per value of K and V, 4 of Q.  A warp holds one
 // token and goes through its heads, so that an angle's sine and cosine are worked
 // out once for all heads that the warp takes; d / 16 lanes hold a head, each 8
-// features and the 8 that they are rotated with.
+// features and the 8 that they are rotated with.  131,042 tokens of 48 heads of
+// 128: 408 us, 5.4 TB/s; 2,048 of 56 heads: 13.3 us; one token's 8 heads of each: 4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -168,6 +170,18 @@ __device__ __forceinline__ Raw load(const __nv_bfloat16* row, int x0, int x1, bo
   return r;
 }
 
+// Codes and scale bytes of a lane's two chunks.
+__device__ __forceinline__ void store(const AppendArgs& a, bool v, int64_t slot, int head, int x0,
+                                      int x1, const Encoded& x) {
+  const int64_t row = slot * a.Hkv + head;
+  uint8_t* codes = (v ? a.c.codes[1] : a.c.codes[0]) + row * a.d;
+  uint8_t* scales = (v ? a.c.scales[1] : a.c.scales[0]) + row * (a.d / kGroup);
+  reinterpret_cast<uint2*>(codes)[x0] = x.code[0];
+  reinterpret_cast<uint2*>(codes)[x1] = x.code[1];
+  if ((x0 & 3) == 0) scales[x0 >> 2] = static_cast<uint8_t>(x.byte[0]);
+  if ((x1 & 3) == 0) scales[x1 >> 2] = static_cast<uint8_t>(x.byte[1]);
+}
+
 __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_constant__ AppendArgs a) {
   // per chunk of 8 features of the heads in a step: magnitude and pair size (or a
   // 64-bit magnitude)
@@ -256,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_
   if (slot < 0) return;  // the same for the whole warp
 
   // ------- K and V
+  // steps that have a scale to be worked out in 64 bits, one bit for every 32nd
+  uint32_t again = 0;
   float2* mine = room[warp] + head0 * 2 * a.lanes;
 #pragma unroll 1
   for (int step = part; step < 2 * a.kv_steps; step += a.parts) {
@@ -309,28 +325,33 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_
       m1 = fmaxf(m1, y.x);
       n1 = fmaxf(n1, y.y);
     }
-    Encoded r;
-    r.byte[0] = scale_byte(m0);
-    r.byte[1] = scale_byte(m1);
+    Encoded x;
+    x.byte[0] = scale_byte(m0);
+    x.byte[1] = scale_byte(m1);
     n0 *= 0x1p-20f;  // twice the bound on the error of a rotated value; 0 for V
     n1 *= 0x1p-20f;
     const bool near = scale_byte(m0 + n0) != scale_byte(fmaxf(m0 - n0, 0.f)) ||
                       scale_byte(m1 + n1) != scale_byte(fmaxf(m1 - n1, 0.f));
-    if (__any_sync(0xffffffffu, near)) {
-      r = encode_exact(turns, pos, turn, a.interleaved != 0, raw, x0, x1,
-                       reinterpret_cast<double*>(mine));
-    } else {
-      r.code[0] = encode8(lo, r.byte[0]);
-      r.code[1] = encode8(hi, r.byte[1]);
-    }
+    again |= static_cast<uint32_t>(near) << ((step / a.parts) & 31);
+    x.code[0] = encode8(lo, x.byte[0]);
+    x.code[1] = encode8(hi, x.byte[1]);
     if (!has) continue;
-    const int64_t row = slot * a.Hkv + head;
-    uint8_t* codes = (v ? a.c.codes[1] : a.c.codes[0]) + row * a.d;
-    uint8_t* scales = (v ? a.c.scales[1] : a.c.scales[0]) + row * (a.d / kGroup);
-    reinterpret_cast<uint2*>(codes)[x0] = r.code[0];
-    reinterpret_cast<uint2*>(codes)[x1] = r.code[1];
-    if ((x0 & 3) == 0) scales[x0 >> 2] = static_cast<uint8_t>(r.byte[0]);
-    if ((x1 & 3) == 0) scales[x1 >> 2] = static_cast<uint8_t>(r.byte[1]);
+    store(a, v, slot, head, x0, x1, x);
+  }
+
+  // ------- scales next to a border, and their codes, once more
+  again = __reduce_or_sync(0xffffffffu, again);
+  if (again == 0) return;
+#pragma unroll 1
+  for (int step = part; step < a.kv_steps; step += a.parts) {
+    if (!(again >> ((step / a.parts) & 31) & 1)) continue;
+    const int head = step * at_once + head0;
+    const bool has = here && head < a.Hkv;
+    const __nv_bfloat16* src =
+        a.c.src[0] + r.b * a.c.bat[0] + r.i * a.c.tok[0] + static_cast<int64_t>(head) * a.d;
+    const Encoded x = encode_exact(turns, pos, turned, a.interleaved != 0, load(src, c0, c1, has),
+                                   c0, c1, reinterpret_cast<double*>(mine));
+    if (has) store(a, false, slot, head, c0, c1, x);
   }
 }
 
@@ -413,10 +434,12 @@ extern "C" csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return CSBP_ERR_CUDA;
-  // few tokens are shared among warps, up to 16 per SM: then latency counts
+  // few tokens are shared among warps, up to 32 per SM: then latency counts, and
+  // the sines and cosines that each of them works out do not (2,048 tokens of 56
+  // heads: 16 per SM 17.7 us, 24 16.2, 32 13.3, 64 16.9)
   const int64_t tokens = static_cast<int64_t>(a.c.batch) * a.c.rows;
   a.parts = static_cast<int32_t>(
-      std::max<int64_t>(1, std::min<int64_t>(2 * a.kv_steps + a.q_steps, 16 * sms / tokens)));
+      std::max<int64_t>(1, std::min<int64_t>(2 * a.kv_steps + a.q_steps, 32 * sms / tokens)));
   const int64_t grid = (tokens * a.parts + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
   const int timed = timer_begin(11, stream);

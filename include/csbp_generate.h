@@ -130,7 +130,8 @@ typedef struct {
  * bf16 in between; a pair with a NaN or an infinity in it, or a value past
  * fp32's range, is stored as NaN.  Queries of the rows that take part (i <
  * count[b]) are rotated whatever their position or page; others keep what they
- * hold in `out` (or become zeros: `clear`).  d is at most 512.  `queries` may be NULL.                 */
+ * hold in `out` (or become zeros: `clear`).  d is at most 512.  `queries` may
+ * be NULL.                                                                  */
 csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_cache_rows* rows,
                               const csbp_rotary* rotary, const void* k, const void* v,
                               const csbp_append_queries* queries, void* stream);

@@ -129,7 +129,8 @@ def test_bad_appends_are_refused():
     for kw in (dict(dim=0), dict(dim=8), dict(dim=24), dict(dim=80), dict(dim=-16),
                dict(interleaved=2), dict(turns=None), dict(turns=PTR + 4)):
         assert append(ro=rotary(**kw)) == INVALID
-    for kw in (dict(Hq=-1), dict(clear=2), dict(clear=-1), dict(q=None), dict(out=None), dict(q=PTR + 8), dict(out=PTR + 4),
+    for kw in (dict(Hq=-1), dict(clear=2), dict(clear=-1), dict(q=None), dict(out=None),
+               dict(q=PTR + 8), dict(out=PTR + 4),
                dict(tok=(504, 0)), dict(tok=(0, 516)), dict(bat=(4088, 0)), dict(bat=(0, 4100)),
                dict(tok=(-512, 0)), dict(bat=(0, 1 << 60)), dict(tok=(1 << 60, 0))):
         assert append(q=queries(**kw)) == INVALID
