@@ -857,7 +857,6 @@ class QuantCache:
         self._call("csbp_cache_read", out[0], out[1], table, start, count, stream)
         return out
 
-
     def append(self, k, v, table, start, count=None, *, rotary, q=None, out=None, stream=None):
         """`write` of k, rotated by its positions start[b] + i, and of v; q
         [batch][rows][Hq][d], if given, is rotated along.  Returns the rotated
@@ -866,7 +865,6 @@ class QuantCache:
         import torch
         fn = "csbp_cache_append"
         lib()
-
         qs = AppendQueries()
 
         def more(c):

@@ -64,7 +64,12 @@ constexpr size_t kStatusBytes = 256;
 constexpr int kMostWarps = 12;
 constexpr int kStages = 2;
 constexpr int kKeys = 32;     // of a warp's step, two MMAs
-constexpr int kMostRows = 16;  // of a head and sequence; more go to whole tiles
+// Rows of a head and sequence that go to row tiles of 16, which read the keys again
+// each (from L2); more go to whole tiles (attn_paged_tiles.cu).  16 sequences of 16,000
+// keys, 8 heads of 128: 20 / 40 / 45 / 60 rows take 165 / 227 / 228 / 289 us here and
+// 275 / 280 / 282 / 282 there; 24 sequences with a window of 1,000, 2 heads of 64: 28 / 56
+// rows 18.2 / 26.9 and 24.1 / 24.7.
+constexpr int kMostRows = 48;
 constexpr int kFlush = 1024;  // steps that one accumulator takes in
 constexpr float kShift = 14.f;  // p is held as p 2^14; a row's maximum may lag by 2^1
 
@@ -837,21 +842,21 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   copies_wait<0>();
 }
 
-// Joins the partials of a row tile that was cut; a CTA per head and 16 rows of it.
+// Joins the partials of a row tile that was cut; a CTA per head and 8 rows of it.
 template <int D>
 __global__ void __launch_bounds__(128)
     paged_join_kernel(const __grid_constant__ PagedParams p, int tile_rows) {
   constexpr int kLanes = D / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int item = blockIdx.x, chunks = (tile_rows + 15) / 16;
-  const int head_in = blockIdx.y / chunks, from = (blockIdx.y - head_in * chunks) * 16;
+  const int item = blockIdx.x, chunks = (tile_rows + 7) / 8;
+  const int head_in = blockIdx.y / chunks, from = (blockIdx.y - head_in * chunks) * 8;
   const int2 piece = p.pieces[item];
   if (piece.y <= 1) return;
   const int entry = item / p.head_blocks, block = item - entry * p.head_blocks;
   const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
   const int head = block * p.heads + head_in;
   if (head >= p.Hkv) return;
-  const int rows = min(min(tile_rows, from + 16), p.queries * p.G - tile * tile_rows) - from;
+  const int rows = min(min(tile_rows, from + 8), p.queries * p.G - tile * tile_rows) - from;
   for (int x = threadIdx.x; x < rows * kLanes; x += 128) {
     const int row = from + x / kLanes, f = x % kLanes * 4;
     float most = -INFINITY, both = 0.f;
@@ -993,7 +998,7 @@ cudaError_t join(const PagedParams& p, const Cut& cut, int d, cudaStream_t strea
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(cut.items),
-                     static_cast<unsigned>(cut.heads * ((cut.tile_rows + 15) / 16)));
+                     static_cast<unsigned>(cut.heads * ((cut.tile_rows + 7) / 8)));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = &early;

@@ -338,6 +338,9 @@ SHAPES = [  # batch, queries, table entries, page, Hq, Hkv, d, lengths
     (1, 130, 3, 64, 4, 4, 128, [192]), (2, 70, 20, 16, 16, 2, 64, [300, 31]),
     (1, 200, 5, 64, 5, 1, 64, [260]), (17, 2, 3, 8, 3, 1, 128, None),
     (200, 1, 2, 16, 4, 2, 64, None), (1, 1, 1000, 1, 4, 1, 64, [777]),
+    (900, 1, 2, 16, 4, 2, 64, None), (700, 30, 2, 16, 2, 1, 64, None),  # more than threads
+    (2, 12, 4, 64, 4, 1, 128, [200, 77]), (1, 49, 4, 16, 3, 3, 64, [64]),
+    (2, 129, 4, 64, 2, 1, 128, [256, 3]), (1, 257, 3, 64, 2, 2, 64, [150]),
 ]
 MASKS = [(False, 0, 0), (True, 0, 0), (True, 37, 4), (False, 20, 0), (True, 1, 0), (False, 64, 70),
          (True, 10000, 3)]
@@ -389,6 +392,53 @@ def test_attention_of_equal_weights_over_a_long_text():
         assert (o.float() - 1).abs().max() <= 2.0 ** -8
         want = torch.log(length.double())[:, None, None]
         assert (lse.double() - want).abs().max() <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("n,Hq", [(1, 4), (6, 4), (40, 2)])
+def test_accumulators_that_are_put_aside(n, Hq):
+    """Texts that one CTA reads for itself, past what one accumulator takes in:
+    with q = 0, O is the mean of V.  Half a rounding of O, 2^-8 of it; 2^-12 for
+    sums of up to 2^11 MMAs that drop 2^-23 each.  LSE: 2^-13 for up to 2^11
+    additions at 2^-24, and its own rounding."""
+    B, page, per, d, n_pages = 304, 64, 10000, 64, 60
+    g = gen(31)
+    c = csbp.QuantCache(n_pages, page, 1, d)
+    x = (torch.rand((n_pages, page, 1, d), generator=g, device="cuda") + 0.5).bfloat16()
+    c.write(x, x, torch.arange(n_pages, device="cuda").int()[:, None], i32([0] * n_pages))
+    table = torch.randint(0, n_pages, (B, per), generator=g, device="cuda").int()
+    table[:, :per // 2] %= 7             # the first half has another mean
+    length = i32([per * page - 1000 * b for b in range(B)])
+    v = torch.from_numpy(values(c)[1]).cuda()[:, :, 0]       # [pages][page][d]
+    a = csbp.PagedAttention(B, n, per, page, Hq, 1, d)
+    q = torch.zeros((B, n, Hq, d), dtype=torch.bfloat16, device="cuda")
+    o, lse = a.forward(q, c, table, length)
+    a.check()
+    whole = v.sum(1)
+    for b in range(0, B, 19):
+        m = int(length[b])
+        want = whole[table[b, :m // page].long()].sum(0)
+        want = (want + v[table[b, m // page].long(), :m % page].sum(0)) / m if m % page else want / m
+        assert ((o[b].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want).all()
+        z = float(np.log(m))
+        assert (lse[b].double() - z).abs().max() <= 2.0 ** -12 + 2.0 ** -22 * z
+
+
+def test_scale_bytes_at_odd_addresses():
+    """A cache in storage of its user's whose scale bytes start anywhere."""
+    for Hkv, n in ((4, 1), (4, 40)):
+        c, q, table, length = attn_case(2, n, 5, 16, 8, Hkv, 128, 32, [80, 33])
+        want = csbp.PagedAttention(2, n, 5, 16, 8, Hkv, 128).forward(q, c, table, length)
+        room = [torch.zeros(t.numel() + 8, dtype=torch.uint8, device="cuda")
+                for t in (c.k_scale, c.v_scale)]
+        views = [r[x:x + t.numel()].view(t.shape).copy_(t)
+                 for r, t, x in zip(room, (c.k_scale, c.v_scale), (1, 3))]
+        odd = csbp.QuantCache(*c.k.shape, storage=(c.k, c.v, *views))
+        a = csbp.PagedAttention(2, n, 5, 16, 8, Hkv, 128)
+        assert same(a.forward(q, odd, table, length), want)
+        k = normal(gen(33), 2, 3, Hkv, 128)
+        for x in (c, odd):
+            x.append(k, k, table, i32([7, 30]), rotary=csbp.Rotary(freqs(128)))
+        assert same(stored(c)[2:], stored(odd)[2:])
 
 
 def test_attention_strides_and_pages():
@@ -503,6 +553,11 @@ def test_queries_far_apart():
     q = q.bfloat16()
     a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, scale=2.0 ** -20)
     check_attn(a.forward(q, c, table, length), q, c, table, length, False, 0, 0, 2.0 ** -20)
+    n = 30                               # 60 rows, on the tiles
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 19, [64])
+    q = (q * torch.exp2(torch.arange(-100, 20, 1, device="cuda").float()).view(1, n, Hq, 1)).bfloat16()
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, scale=2.0 ** -20)
+    check_attn(a.forward(q, c, table, length), q, c, table, length, False, 0, 0, 2.0 ** -20)
     c.k_scale.sub_(60)
     q2 = (q.float() * 2.0 ** 60).bfloat16()
     check_attn(a.forward(q2, c, table, length), q2, c, table, length, False, 0, 0, 2.0 ** -20)
@@ -531,10 +586,11 @@ def step(s, stream=None):
     return s["rq"], s["o"], s["lse"]
 
 
-def test_step_against_read_and_prefix_attention():
+@pytest.mark.parametrize("n", [4, 20])
+def test_step_against_read_and_prefix_attention(n):
     """append + paged attention = the write, read back and attention of the prefix
     operator, to the difference of their roundings."""
-    s = step_state(20)
+    s = step_state(20, n=n)
     rq, o, lse = step(s)
     c = s["caches"][-1]
     B, n, Hq, d = s["q"].shape
@@ -548,10 +604,11 @@ def test_step_against_read_and_prefix_attention():
     check_attn((o, lse), rq, c, s["table"], s["length"], True, 0, 0, d ** -0.5)
 
 
-def test_captured_step_follows_its_inputs():
+@pytest.mark.parametrize("n", [4, 20])
+def test_captured_step_follows_its_inputs(n):
     """One graph of both operators in two layers, replayed with other values and
     other lengths."""
-    s, t = step_state(21), step_state(22)
+    s, t = step_state(21, n=n), step_state(22, n=n)
     want = []
     for x in (s, t):
         before = [stored(c) for c in x["caches"]]
@@ -579,8 +636,9 @@ def test_captured_step_follows_its_inputs():
         assert same(got, w)
 
 
-def test_two_streams_at_once():
-    a, b = step_state(23), step_state(24)
+@pytest.mark.parametrize("n", [4, 20])
+def test_two_streams_at_once(n):
+    a, b = step_state(23, n=n), step_state(24, n=n)
     want = [[x.clone() for x in step(s)] for s in (a, b)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -592,11 +650,12 @@ def test_two_streams_at_once():
         assert same([s["rq"], s["o"], s["lse"]], w)
 
 
-def test_one_handle_many_calls_in_a_row():
+@pytest.mark.parametrize("n", [1, 10, 30])
+def test_one_handle_many_calls_in_a_row(n):
     """Pieces of one call are not mistaken for those of another: lengths change
     from call to call on one workspace."""
-    c, q, table, _ = attn_case(4, 1, 200, 16, 8, 2, 128, 25)
-    a = csbp.PagedAttention(4, 1, 200, 16, 8, 2, 128, causal=True)
+    c, q, table, _ = attn_case(4, n, 200, 16, 8, 2, 128, 25)
+    a = csbp.PagedAttention(4, n, 200, 16, 8, 2, 128, causal=True)
     lens = [[3200, 1, 0, 50], [16, 3000, 2900, 2800], [0, 0, 0, 0], [3200] * 4, [1, 2, 3, 4]]
     outs = [a.forward(q, c, table, i32(x)) for x in lens * 3]
     torch.cuda.synchronize()
@@ -605,17 +664,47 @@ def test_one_handle_many_calls_in_a_row():
         assert same(outs[k], outs[k + 5]) and same(outs[k], outs[k + 10])
 
 
-def test_rows_of_outputs_and_cache_behind_stay():
+@pytest.mark.parametrize("n", [3, 9, 50])
+def test_rows_of_outputs_and_cache_behind_stay(n):
     """Outputs are written whole and nothing else is; the cache is only read."""
-    c, q, table, length = attn_case(2, 3, 4, 16, 4, 2, 64, 26, [30, 64])
+    c, q, table, length = attn_case(2, n, 4, 16, 4, 2, 64, 26, [30, 64])
     before = stored(c)
-    a = csbp.PagedAttention(2, 3, 4, 16, 4, 2, 64, True)
-    o = torch.full((4, 3, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
-    lse = torch.full((4, 4, 3), 7.0, device="cuda")
+    a = csbp.PagedAttention(2, n, 4, 16, 4, 2, 64, True)
+    o = torch.full((4, n, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, 4, n), 7.0, device="cuda")
     want = a.forward(q, c, table, length)
     a.forward(q, c, table, length, out=(o[1:3], lse[1:3]))
     assert same(want, (o[1:3], lse[1:3]))
     assert (o[::3] == 7).all() and (lse[::3] == 7).all() and same(before, stored(c))
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_on_a_named_stream(n):
+    """Outputs made in a call on a named stream are there whatever the current one
+    is busy with, zeros of rows that take no part among them."""
+    s = step_state(28, n=n)
+    x = torch.zeros((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    count = i32([n, 0, n - 1])
+
+    def call(stream):
+        rq = s["caches"][0].append(s["k"], s["v"], s["table"], s["start"], count, rotary=s["ro"],
+                                   q=s["q"], stream=stream)
+        return rq, *s["a"].forward(rq, s["caches"][0], s["table"], s["length"], stream=stream)
+
+    want = [t.clone() for t in call(None)]
+    assert (want[0][1] == 0).all()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = [torch.empty_like(t) for t in want]
+    for _ in range(50):
+        torch.mm(x, x)
+    for t in old:
+        t.fill_(7)
+    del old, t
+    side = torch.cuda.Stream()
+    got = call(side)
+    torch.cuda.synchronize()
+    assert same(got, want)
 
 
 def test_kernels_are_timed():
