@@ -13,9 +13,9 @@
 // Operands.  K, V and Q are f16 in shared memory, P f16 in TMEM, all under powers of
 // two that fp32 takes back: E4M3 codes are exact in f16, and so are their group
 // scales 2^(e - E) down to 2^-24, with E the largest scale byte of the K tile, and of
-// V the largest so far in the feature group (O is rescaled when it grows, as it is
-// when a row's maximum does).  An operand below 2^-31 of the largest beside it becomes
-// 0.  P is p 2^11, rounded to 2^-11 of itself (2^-36 of the row's largest at least).
+// V twice the largest so far in the feature group (O is rescaled when one grows past
+// that, and when a row's maximum has grown by 2^5.9, for all of the warp's rows).  An operand below 2^-31 of the largest beside it becomes
+// 0.  P is p 2^10, rounded to 2^-11 of itself (2^-35 of the row's largest at least).
 //
 // Keys.  One warp looks the pages up and starts the copies of K's codes and the scale
 // bytes into a ring of three half tiles, another those of V's (cp.async: one bulk copy
@@ -48,9 +48,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = 5;  // converters
-constexpr float kThreshold = 4.f;  // log2: a row's maximum may lag by that
-constexpr float kShift = 11.f;     // P = p 2^11
-constexpr int kHeadroom = 6;       // K and V operands: codes times up to 2^6
+constexpr float kThreshold = 5.9f;  // log2: a row's maximum may lag by that
+constexpr float kShift = 10.f;     // P = p 2^10 (2^15.9 at most)
+constexpr int kHeadroom = 7;       // K and V operands: codes times up to 2^7
 constexpr int kFlush = 512;        // key tiles that one accumulator takes in
 constexpr int kHalves = 3;         // of the ring
 constexpr int kInfos = 8;
@@ -392,7 +392,8 @@ struct Copier {
       for (int o = 16; o > 0; o >>= 1) v = __vmaxu4(v, __shfl_xor_sync(0xffffffffu, v, o));
       k = max(max(k & 255, k >> 8 & 255), max(k >> 16 & 255, k >> 24));
       k = __reduce_max_sync(0xffffffffu, k);
-      top = begins ? v : __vmaxu4(top, v);
+      // (twice as much as now, so that a little growth does not rescale O)
+      if (begins || __vmaxu4(top, v) != top) top = __vmaxu4(begins ? 0 : top, __vaddus4(v, 0x01010101u));
       if (lane == 0) {
         info.k_factor = ldexpf(1.f, static_cast<int>(k) - 127 - kHeadroom);
         info.k_top = k;
@@ -936,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) {
             const uint32_t reads =
                 there[q] & below(hi, q) & (~below(lo, q) | (p.window ? below(p.sinks, q) : 0u));
+            if (!__all_sync(0xffffffffu, reads == ~0u))
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               sv[32 * q + c] = reads >> c & 1 ? sv[32 * q + c] : -INFINITY;
@@ -946,12 +948,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kTile; c += 2) mx4[c / 2 % 4] = fmax3(mx4[c / 2 % 4], sv[c], sv[c + 1]);
         const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
         const float m_new = fmaxf(sum.m, mx * mult);
-        const bool need = m_new > sum.m + kThreshold;  // false while both are -inf
+        // where a row's maximum has grown by too much (never while both are -inf), that of
+        // all of the warp's rows is brought up to date: O is rescaled for all of them
+        const bool need = __any_sync(0xffffffffu, m_new > sum.m + kThreshold);
         const uint32_t now = info.top;
-        if (sum.tiles > 0 && (now != sum.top || __any_sync(0xffffffffu, need))) {
+        if (sum.tiles > 0 && (now != sum.top || need)) {
           // O holds the P V so far, under the old maximum and E (its last P V is done:
           // this S was issued after it)
-          const float alpha = need ? exp2f(sum.m - m_new) : 1.f;
+          const float alpha = need && m_new != sum.m ? exp2f(sum.m - m_new) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D / 8; ++c) {  // (8 at a time: the scores are in registers)
             const int by = static_cast<int>((now >> 8 * (c / 4) & 255) - (sum.top >> 8 * (c / 4) & 255));
@@ -960,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         sum.top = now;
-        if (need) {
+        if (need && m_new != sum.m) {
           sum.l *= exp2f(sum.m - m_new);  // 0 when sum.m was -inf
           sum.m = m_new;
         }
