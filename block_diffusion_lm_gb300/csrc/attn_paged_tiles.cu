@@ -85,8 +85,9 @@ struct Tiles {
   static constexpr int kBars = bFree + kHalves;
   static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
   static constexpr int kRedo = kMisc + 8;           // [kInfos] by item
-  static constexpr int kCursor = (kRedo + kInfos * 4 + 15) / 16 * 16;  // of each softmax warp
-  static constexpr int kSmem = kCursor + 8 * 48;
+  static constexpr int kCursor = (kRedo + kInfos * 4 + 15) / 16 * 16;  // [2] of each softmax warp
+  static constexpr int kScale = kCursor + 8 * 2 * 48;  // [2 slots][row] of Q
+  static constexpr int kSmem = kScale + 2 * kTile * 4;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
 };
 static_assert(Tiles<128>::kSmem <= 232448, "shared memory of a CTA");
@@ -149,6 +150,24 @@ __device__ __forceinline__ void tmem_scale8(uint32_t at, float f) {
       : "memory");
 }
 
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t* r) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// 16 columns of the thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15])
+      : "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // A CTA's part of one item.
@@ -537,37 +556,51 @@ __device__ __forceinline__ RowAt row_at(const PagedParams& p, const Piece& x, in
   return a;
 }
 
-// The row of Q as f16 with its largest element as 2^7 .. 2^8, to row `to` of the tile
-// at `tile` (if any); returns what its scores are to be multiplied by.
+// Starts the copies of the warp's 32 rows of Q, from `row0` of the pair on, to rows
+// `to0` .. of the tile at `tile`.
 template <int D>
-__device__ __noinline__ float load_query(const PagedParams& p, const Piece x, const RowAt a,
-                                         uint8_t* tile, int to) {
-  const uint4* src = reinterpret_cast<const uint4*>(p.q + x.b * p.q_bat + a.i * p.q_tok +
-                                                    static_cast<int64_t>(a.h) * D);
-  uint4 raw[D / 8];
+__device__ __noinline__ void copy_query(const PagedParams& p, const Piece x, int row0,
+                                        uint32_t tile, int to0) {
+  constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
+  const int lane = threadIdx.x & 31, c = lane % kChunks;
+#pragma unroll 4
+  for (int r = lane / kChunks; r < 32; r += kAtOnce) {
+    const RowAt a = row_at(p, x, 0, row0 + r);
+    copy16(tile + (c >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to0 + r, c & 7),
+           p.q + x.b * p.q_bat + a.i * p.q_tok + static_cast<int64_t>(a.h) * D + c * 8, 16);
+  }
+}
+
+// That row `to` of the tile as f16 with its largest element as 2^7 .. 2^8 (and the
+// copies of the warp waited for); returns what its scores are to be multiplied by.
+template <int D>
+__device__ __noinline__ float convert_query(const PagedParams& p, uint32_t tile, int to) {
+  copies_wait_all();
+  __syncwarp();
   uint32_t most = 0;
-#pragma unroll
-  for (int k = 0; k < D / 8; ++k) raw[k] = __ldg(src + k);
-#pragma unroll
+#pragma unroll 4
   for (int k = 0; k < D / 8; ++k) {
-    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    uint32_t w[4];
+    lds128(tile + (k >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to, k & 7), w);
 #pragma unroll
     for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
   }
   const int ex = max(static_cast<int>(most >> 7) - 127, -110);
   const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-  if (tile) {
+#pragma unroll 4
+  for (int k = 0; k < D / 8; ++k) {
+    const uint32_t at = tile + (k >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to, k & 7);
+    uint32_t w[4];
+    lds128(at, w);
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k) {
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-      *reinterpret_cast<uint4*>(tile + (k >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to, k & 7)) =
-          make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
   }
+  fence_proxy_async_smem();
+  __syncwarp();
   return p.scale_log2 * ldexpf(1.f, ex - 7);
 }
 
@@ -629,25 +662,27 @@ __device__ __noinline__ void store_sum(const PagedParams& p, const Piece x, cons
   const bool valid = x.tile * kPairRows + (x.alternate ? 0 : s * kTile) + row < p.queries * p.G;
   const int64_t token = static_cast<int64_t>(x.b) * p.queries + a.i;
   const int64_t place = static_cast<int64_t>(part) * kPairRows + (x.alternate ? 0 : s * kTile) + row;
+  uint32_t bad = 0;
+  // (few columns at a time: code that runs once per piece has to come from L2 first)
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
-    float o[32];
-    if (here) tmem_ld32(o_at + c * 32, o);
+  for (int c = 0; c < D; c += 16) {
+    float o[16];
+    if (here) tmem_ld16(o_at + c, o);
     // 2^(E - 127 - headroom), in two steps: one could lie below fp32's range
-    const int ex = static_cast<int>(sum.top >> 8 * c & 255);
+    const int ex = static_cast<int>(sum.top >> (c / 32 * 8) & 255);
     const float f0 = __uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23);
     const float f1 = __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63 - kHeadroom) << 23);
     const bool some = here && z != -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * w * f0 * f1 : 0.f;
+    for (int i = 0; i < 16; ++i) o[i] = some ? o[i] * w * f0 * f1 : 0.f;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       if (k == 0 ? z_mine == -INFINITY : z_other == -INFINITY) continue;
       const float f = k == 0 ? w_mine : w_other;
       const float4* v =
-          reinterpret_cast<const float4*>(aside_o + (k == 0 ? mine : others) * D + c * 32);
+          reinterpret_cast<const float4*>(aside_o + (k == 0 ? mine : others) * D + c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const float4 y = v[i];
         o[4 * i] = fmaf(y.x, f, o[4 * i]);
         o[4 * i + 1] = fmaf(y.y, f, o[4 * i + 1]);
@@ -656,24 +691,24 @@ __device__ __noinline__ void store_sum(const PagedParams& p, const Piece x, cons
       }
     }
     if (redo) {
-      const uint32_t bad = valid ? nan_features<D>(p, x, r, a, c) : 0;
+      bad = c & 16 ? bad >> 16 : valid ? nan_features<D>(p, x, r, a, c / 32) : 0;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 16; ++i)
         if (bad >> i & 1) o[i] = NAN;
     }
     if (part == -1) {
       if (!valid) continue;
-      uint4* to = reinterpret_cast<uint4*>(p.o + (token * p.Hq + a.h) * D + c * 32);
+      uint4* to = reinterpret_cast<uint4*>(p.o + (token * p.Hq + a.h) * D + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
         to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
                            pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
                            pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
     } else {
-      float4* to = reinterpret_cast<float4*>(part == kAside ? aside_o + mine * D + c * 32
-                                                            : p.part_o + place * D + c * 32);
+      float4* to = reinterpret_cast<float4*>(part == kAside ? aside_o + mine * D + c
+                                                            : p.part_o + place * D + c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i)
         to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     }
   }
@@ -862,33 +897,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_s = 0;  // key tiles of this slot so far
     int t0 = 0;   // key tiles so far
     int item = 0;
-    const uint32_t kept = smem_u32(smem + L::kCursor + (warp - 8) * 48);
+    uint32_t kept = smem_u32(smem + L::kCursor + (warp - 8) * 96), kept_next = kept + 48;
     keep_cursor(kept, cur);
     const uint32_t s_at = tmem + lane_base + colS, o_at = tmem + lane_base + colO;
+    const uint32_t q_tile = smem_u32(smem + L::kQ + s * L::kTileBytes);
+    float* const q_scale = reinterpret_cast<float*>(smem + L::kScale) + s * kTile;
+    // Q of a piece, if the slot has one: its copies begun, then the rest
+    const auto begin_query = [&](const Piece& x) {
+      const int first = (x.alternate ? 0 : s * kTile) + (warp & 3) * 32;
+      if ((s == 0 || !x.alternate) && first < x.rows) copy_query<D>(p, x, first, q_tile, (warp & 3) * 32);
+    };
+    const auto finish_query = [&](const Piece& x) {
+      if (s == 1 && x.alternate) return;
+      if ((warp & 3) * 32 + s * kTile < x.rows) q_scale[row] = convert_query<D>(p, q_tile, row);
+      if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
+    };
+    bool has_query = false;
     for (int left = steps; left > 0; ++item) {
       int count, stride, hi, lo;
-      float row_scale = 0.f;
       bool has_rows;
       {
-      const Cursor cur = kept_cursor(kept);
-      const Piece x = piece_of(p, cur, left);
-      const int first_row = x.alternate ? 0 : s * kTile;
-      has_rows = first_row + (warp & 3) * 32 < x.rows;  // warp-uniform
-      const RowAt a = row_at(p, x, cur.r.c, first_row + row);
-      if (has_rows) {
-        row_scale = load_query<D>(p, x, a, s == 0 || !x.alternate ? smem + L::kQ + s * L::kTileBytes : nullptr,
-                                  row);
-        fence_proxy_async_smem();
+        const Cursor cur = kept_cursor(kept);
+        const Piece x = piece_of(p, cur, left);
+        const int first_row = x.alternate ? 0 : s * kTile;
+        has_rows = first_row + (warp & 3) * 32 < x.rows;  // warp-uniform
+        const RowAt a = row_at(p, x, cur.r.c, first_row + row);
+        if (!has_query) {
+          begin_query(x);
+          finish_query(x);
+        }
+        hi = a.hi;
+        lo = a.lo;
+        count = x.count;
+        stride = x.alternate ? 2 : 1;
       }
-      if (s == 0 || !x.alternate) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
-      }
-      hi = a.hi;
-      lo = a.lo;
-      count = x.count;
-      stride = x.alternate ? 2 : 1;
-      }
+      float row_scale = q_scale[row];
       Sum sum{-INFINITY, 0.f, 0, 0, false};
       // the last P V of this slot
       const auto last_done = [&] {
@@ -918,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
           continue;
         }
+        if (stride == 2 && m == 1) row_scale = q_scale[row - s * kTile];  // slot 0's Q
         tc_fence_after_sync();
         const Info& info = reinterpret_cast<const Info*>(smem + L::kInfo)[(t0 + m) % kInfos];
         // (not 0: a masked score times it has to stay -inf)
@@ -993,9 +1037,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
       }
-      last_done();
       // ------- the piece's end
-      Cursor cur = kept_cursor(kept);
+      // The next one's Q goes to the place of this one's, whose last scores are there, and
+      // its first scores come while this one's sum is stored.  (Both slots of an
+      // alternate piece read the one Q tile.)
+      const bool more = left > count;
+      has_query = ok && more && stride == 1;
+      if (more) {
+        Cursor cur = kept_cursor(kept);
+        next_item(p, cur);
+        keep_cursor(kept_next, cur);
+        if (has_query) begin_query(piece_of(p, cur, left - count));
+      }
+      last_done();
+      if (has_query) finish_query(piece_of(p, kept_cursor(kept_next), left - count));
+      const Cursor cur = kept_cursor(kept);
       const Piece x = piece_of(p, cur, left);
       const RowAt a = row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row);
       const int later = x.n - x.k0 - x.count;  // steps of the item in later shares
@@ -1022,11 +1078,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x.alternate) softmax_sync();  // slot 1's sum has been read
       t0 += x.count;
       left -= x.count;
-      if (left > 0) {
-        next_item(p, cur);
-        __syncwarp();
-        keep_cursor(kept, cur);
-      }
+      const uint32_t next = kept_next;
+      kept_next = kept;
+      kept = next;
     }
   }
 
