@@ -85,9 +85,10 @@ struct Tiles {
   static constexpr int kBars = bFree + kHalves;
   static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
   static constexpr int kRedo = kMisc + 8;           // [kInfos] by item
-  static constexpr int kCursor = (kRedo + kInfos * 4 + 15) / 16 * 16;  // [2] of each softmax warp
-  static constexpr int kScale = kCursor + 8 * 2 * 48;  // [2 slots][row] of Q
-  static constexpr int kSmem = kScale + 2 * kTile * 4;
+  static constexpr int kCursor = (kRedo + kInfos * 4 + 15) / 16 * 16;  // of each softmax warp
+  static constexpr int kScale = kCursor + 8 * 48;  // [2 slots][row] of Q
+  static constexpr int kJoin = kScale + 2 * kTile * 4;  // [row] of an alternate piece's slot 1
+  static constexpr int kSmem = kJoin + kTile * 16;
   static constexpr uint32_t kColO = 256;            // O of slot s at kColO + D s
 };
 static_assert(Tiles<128>::kSmem <= 232448, "shared memory of a CTA");
@@ -556,18 +557,19 @@ __device__ __forceinline__ RowAt row_at(const PagedParams& p, const Piece& x, in
   return a;
 }
 
-// Starts the copies of the warp's 32 rows of Q, from `row0` of the pair on, to rows
-// `to0` .. of the tile at `tile`.
+// Starts the copies of the warp's 32 rows of Q to rows `to0` .. of the tile at `tile`;
+// `a` is the lane's row.
 template <int D>
-__device__ __noinline__ void copy_query(const PagedParams& p, const Piece x, int row0,
+__device__ __noinline__ void copy_query(const PagedParams& p, const Piece x, const RowAt a,
                                         uint32_t tile, int to0) {
   constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
   const int lane = threadIdx.x & 31, c = lane % kChunks;
+  const int64_t mine = x.b * p.q_bat + a.i * p.q_tok + static_cast<int64_t>(a.h) * D;
+  tile += (c >> 3) * Tiles<D>::kBoxBytes;
 #pragma unroll 4
   for (int r = lane / kChunks; r < 32; r += kAtOnce) {
-    const RowAt a = row_at(p, x, 0, row0 + r);
-    copy16(tile + (c >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to0 + r, c & 7),
-           p.q + x.b * p.q_bat + a.i * p.q_tok + static_cast<int64_t>(a.h) * D + c * 8, 16);
+    const int64_t from = __shfl_sync(0xffffffffu, mine, r);
+    copy16(tile + sw128_offset(to0 + r, c & 7), p.q + from + c * 8, 16);
   }
 }
 
@@ -583,8 +585,9 @@ __device__ __noinline__ float convert_query(const PagedParams& p, uint32_t tile,
     uint32_t w[4];
     lds128(tile + (k >> 3) * Tiles<D>::kBoxBytes + sw128_offset(to, k & 7), w);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+    for (int e = 0; e < 4; ++e) most = __vmaxu2(most, w[e] & 0x7fff7fffu);
   }
+  most = max(most & 0xffffu, most >> 16);
   const int ex = max(static_cast<int>(most >> 7) - 127, -110);
   const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
 #pragma unroll 4
@@ -635,82 +638,150 @@ struct Sum {
   bool aside;    // and earlier ones in `aside_o`, `aside_z`
 };
 
+// ... and the LSE of it (log2).
+__device__ __forceinline__ float lse_of(const Sum& sum) {
+  return sum.tiles > 0 && sum.l != 0.f ? sum.m - kShift + log2f(sum.l) : -INFINITY;
+}
+
+// What slot 1 of an alternate piece leaves for slot 0, beside its O.
+struct Join {
+  float z, inv;  // LSE, 1 / l
+  uint32_t top;
+  int what;      // bit 0: it has summed something, bit 1: it has put something aside
+};
+
+// 2^(E - 127 - headroom) of feature group g in two factors: one could lie below fp32's
+// range.
+__device__ __forceinline__ float2 unit_of(uint32_t top, int g) {
+  const int ex = static_cast<int>(top >> 8 * g & 255);
+  return make_float2(__uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23),
+                     __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63 - kHeadroom) << 23));
+}
+
 // Stores a row's normalised O and its LSE, joined with what was put aside and, of an
-// alternate piece, with what slot 1 has left there.  To the outputs (`part` = -1), a
-// place among the partials, or aside (kAside).  Whole warps; `o_at` is the warp's O.
+// alternate piece (`other`), with slot 1's.  To the outputs (`part` = -1), a place among
+// the partials, or aside (kAside).  Whole warps; `o_at` is the warp's O.  On their way
+// to outputs and partials the rows pass through the Q tile at `tile`, so that they are
+// written as wholes: 32 rows' 16 bytes at a time took 1,500 clocks per 16 columns.  (What
+// is put aside, in the middle of a piece, does not.)
 constexpr int kAside = -2;
 template <int D>
 __device__ __noinline__ void store_sum(const PagedParams& p, const Piece x, const Range r,
                                        const RowAt a, const Sum sum, uint32_t o_at, int s, int row,
-                                       int part, bool redo) {
+                                       int part, bool redo, uint32_t tile, const Join* other) {
   tc_fence_after_sync();
   float* const aside_o = p.aside_o + static_cast<int64_t>(blockIdx.x) * kPairRows * D;
   float* const aside_z = p.aside_z + static_cast<int64_t>(blockIdx.x) * kPairRows;
-  const bool other = x.alternate && s == 0 && part != kAside, here = sum.tiles > 0;
   const int mine = s * kTile + row, others = kTile + row;
-  const float z = here && sum.l != 0.f ? sum.m - kShift + log2f(sum.l) : -INFINITY;
+  const bool here = sum.tiles > 0;
+  Join o1{-INFINITY, 0.f, 0, 0};
+  if (other) o1 = other[row];
+  const float z = lse_of(sum);
   const float z_mine = sum.aside ? aside_z[mine] : -INFINITY;
-  const float z_other = other ? aside_z[others] : -INFINITY;
-  const float most = fmaxf(z, fmaxf(z_mine, z_other)), ref = most == -INFINITY ? 0.f : most;
-  float w = exp2f(z - ref), w_mine = exp2f(z_mine - ref), w_other = exp2f(z_other - ref);
-  const float all = w + w_mine + w_other, inv = all == 0.f ? 0.f : 1.f / all;
-  // (NaN in the sum goes on to all of the row)
+  const float z_other = o1.what & 2 ? aside_z[others] : -INFINITY;
+  const float most = fmaxf(fmaxf(z, o1.z), fmaxf(z_mine, z_other));
+  const float ref = most == -INFINITY ? 0.f : most;
+  float w = exp2f(z - ref), w1 = exp2f(o1.z - ref);
+  float w_mine = exp2f(z_mine - ref), w_other = exp2f(z_other - ref);
+  const float all = w + w1 + w_mine + w_other, inv = all == 0.f ? 0.f : 1.f / all;
+  // (NaN in a sum goes on to all of the row)
   w = z == -INFINITY ? 0.f : w * inv / sum.l;
+  w1 = o1.z == -INFINITY ? 0.f : w1 * inv * o1.inv;
   w_mine *= inv;
   w_other *= inv;
   const float lse = all == 0.f ? -INFINITY : ref + log2f(all);
   const bool valid = x.tile * kPairRows + (x.alternate ? 0 : s * kTile) + row < p.queries * p.G;
   const int64_t token = static_cast<int64_t>(x.b) * p.queries + a.i;
   const int64_t place = static_cast<int64_t>(part) * kPairRows + (x.alternate ? 0 : s * kTile) + row;
-  uint32_t bad = 0;
-  // (few columns at a time: code that runs once per piece has to come from L2 first)
+  // where the row goes, in bytes
+  uint8_t* const base = reinterpret_cast<uint8_t*>(part == -1 ? static_cast<void*>(p.o) : p.part_o);
+  const int64_t row_at = part != -1 ? place * D * 4 : valid ? (token * p.Hq + a.h) * D * 2 : -1;
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int c = 0; c < D; c += 16) {
-    float o[16];
-    if (here) tmem_ld16(o_at + c, o);
-    // 2^(E - 127 - headroom), in two steps: one could lie below fp32's range
-    const int ex = static_cast<int>(sum.top >> (c / 32 * 8) & 255);
-    const float f0 = __uint_as_float(static_cast<uint32_t>(ex / 2 + 64) << 23);
-    const float f1 = __uint_as_float(static_cast<uint32_t>(ex - ex / 2 + 63 - kHeadroom) << 23);
-    const bool some = here && z != -INFINITY;
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = some ? o[i] * w * f0 * f1 : 0.f;
+    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+    if (here) {
+      tmem_ld32(o_at + c, o);
+      const float2 u = unit_of(sum.top, c / 32);
+      const float f = w * u.x;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = o[i] * f * u.y;
+    }
+    if (o1.what & 1) {
+      const float2 u = unit_of(o1.top, c / 32);
+      const float f = w1 * u.x;
+#pragma unroll
+      for (int k = 0; k < 32; k += 16) {
+        float y[16];
+        tmem_ld16(o_at + D + c + k, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[k + i] = fmaf(y[i] * f, u.y, o[k + i]);
+      }
+    }
+    if (sum.aside || (o1.what & 2)) {
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      if (k == 0 ? z_mine == -INFINITY : z_other == -INFINITY) continue;
-      const float f = k == 0 ? w_mine : w_other;
-      const float4* v =
-          reinterpret_cast<const float4*>(aside_o + (k == 0 ? mine : others) * D + c);
+      for (int k = 0; k < 2; ++k) {
+        if (k == 0 ? z_mine == -INFINITY : z_other == -INFINITY) continue;
+        const float f = k == 0 ? w_mine : w_other;
+        const float4* v =
+            reinterpret_cast<const float4*>(aside_o + (k == 0 ? mine : others) * D + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 y = v[i];
-        o[4 * i] = fmaf(y.x, f, o[4 * i]);
-        o[4 * i + 1] = fmaf(y.y, f, o[4 * i + 1]);
-        o[4 * i + 2] = fmaf(y.z, f, o[4 * i + 2]);
-        o[4 * i + 3] = fmaf(y.w, f, o[4 * i + 3]);
+        for (int i = 0; i < 8; ++i) {
+          const float4 y = v[i];
+          o[4 * i] = fmaf(y.x, f, o[4 * i]);
+          o[4 * i + 1] = fmaf(y.y, f, o[4 * i + 1]);
+          o[4 * i + 2] = fmaf(y.z, f, o[4 * i + 2]);
+          o[4 * i + 3] = fmaf(y.w, f, o[4 * i + 3]);
+        }
       }
     }
     if (redo) {
-      bad = c & 16 ? bad >> 16 : valid ? nan_features<D>(p, x, r, a, c / 32) : 0;
+      const uint32_t bad = valid ? nan_features<D>(p, x, r, a, c / 32) : 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 32; ++i)
         if (bad >> i & 1) o[i] = NAN;
     }
-    if (part == -1) {
-      if (!valid) continue;
-      uint4* to = reinterpret_cast<uint4*>(p.o + (token * p.Hq + a.h) * D + c);
+    if (part == kAside) {
+      float4* to = reinterpret_cast<float4*>(aside_o + mine * D + c);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        to[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                           pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                           pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-    } else {
-      float4* to = reinterpret_cast<float4*>(part == kAside ? aside_o + mine * D + c
-                                                            : p.part_o + place * D + c);
+      for (int i = 0; i < 8; ++i)
+        to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      continue;
+    }
+    const auto put = [&](int chunk, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                       tile + (chunk >> 3) * Tiles<D>::kBoxBytes + sw128_offset(row, chunk & 7)),
+                   "r"(w0), "r"(w1), "r"(w2), "r"(w3)
+                   : "memory");
+    };
+    if (part == -1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        put(c / 8 + i, pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+            pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        put(c % (D / 2) / 4 + i, __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+            __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
     }
+    // the tile's rows have 2 D bytes: the whole row, or half of the fp32
+    const int width = part == -1 ? D : D / 2;
+    if ((c + 32) % width != 0) continue;
+    constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
+    const int k = lane % kChunks;
+    uint8_t* const to = base + (part == -1 ? 0 : (c + 32 - width) * 4) + k * 16;
+    __syncwarp();
+#pragma unroll 4
+    for (int y = lane / kChunks; y < 32; y += kAtOnce) {
+      const int64_t at = __shfl_sync(0xffffffffu, row_at, y);
+      uint32_t v[4];
+      lds128(tile + (k >> 3) * Tiles<D>::kBoxBytes + sw128_offset((row & ~31) + y, k & 7), v);
+      if (at >= 0) *reinterpret_cast<uint4*>(to + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    __syncwarp();
   }
   if (part == kAside)
     aside_z[mine] = lse;
@@ -897,22 +968,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_s = 0;  // key tiles of this slot so far
     int t0 = 0;   // key tiles so far
     int item = 0;
-    uint32_t kept = smem_u32(smem + L::kCursor + (warp - 8) * 96), kept_next = kept + 48;
+    const uint32_t kept = smem_u32(smem + L::kCursor + (warp - 8) * 48);
     keep_cursor(kept, cur);
     const uint32_t s_at = tmem + lane_base + colS, o_at = tmem + lane_base + colO;
     const uint32_t q_tile = smem_u32(smem + L::kQ + s * L::kTileBytes);
     float* const q_scale = reinterpret_cast<float*>(smem + L::kScale) + s * kTile;
-    // Q of a piece, if the slot has one: its copies begun, then the rest
-    const auto begin_query = [&](const Piece& x) {
-      const int first = (x.alternate ? 0 : s * kTile) + (warp & 3) * 32;
-      if ((s == 0 || !x.alternate) && first < x.rows) copy_query<D>(p, x, first, q_tile, (warp & 3) * 32);
-    };
-    const auto finish_query = [&](const Piece& x) {
-      if (s == 1 && x.alternate) return;
-      if ((warp & 3) * 32 + s * kTile < x.rows) q_scale[row] = convert_query<D>(p, q_tile, row);
-      if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
-    };
-    bool has_query = false;
     for (int left = steps; left > 0; ++item) {
       int count, stride, hi, lo;
       bool has_rows;
@@ -922,9 +982,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first_row = x.alternate ? 0 : s * kTile;
         has_rows = first_row + (warp & 3) * 32 < x.rows;  // warp-uniform
         const RowAt a = row_at(p, x, cur.r.c, first_row + row);
-        if (!has_query) {
-          begin_query(x);
-          finish_query(x);
+        if (s == 0 || !x.alternate) {
+          if (has_rows) {
+            copy_query<D>(p, x, a, q_tile, row & ~31);
+            q_scale[row] = convert_query<D>(p, q_tile, row);
+          }
+          if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
         }
         hi = a.hi;
         lo = a.lo;
@@ -947,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (has_rows) {
             const Cursor cur = kept_cursor(kept);
             const Piece x = piece_of(p, cur, left);
-            store_sum<D>(p, x, cur.r, row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row), sum, o_at, s, row, kAside, false);
+            store_sum<D>(p, x, cur.r, row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row), sum, o_at, s, row, kAside, false, 0, nullptr);
           }
           sum = Sum{-INFINITY, 0.f, 0, 0, true};
         }
@@ -1038,20 +1101,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars[L::bPFull + s]);
       }
       // ------- the piece's end
-      // The next one's Q goes to the place of this one's, whose last scores are there, and
-      // its first scores come while this one's sum is stored.  (Both slots of an
-      // alternate piece read the one Q tile.)
-      const bool more = left > count;
-      has_query = ok && more && stride == 1;
-      if (more) {
-        Cursor cur = kept_cursor(kept);
-        next_item(p, cur);
-        keep_cursor(kept_next, cur);
-        if (has_query) begin_query(piece_of(p, cur, left - count));
-      }
       last_done();
-      if (has_query) finish_query(piece_of(p, kept_cursor(kept_next), left - count));
-      const Cursor cur = kept_cursor(kept);
+      Cursor cur = kept_cursor(kept);
       const Piece x = piece_of(p, cur, left);
       const RowAt a = row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row);
       const int later = x.n - x.k0 - x.count;  // steps of the item in later shares
@@ -1063,24 +1114,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
       const int part =
           starts && later == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-      // (slot 1 of an alternate piece leaves its sum aside for slot 0)
-#pragma unroll 1
-      for (int turn = x.alternate ? 1 : s; turn >= (x.alternate ? 0 : s); --turn) {
-        if (turn == s && ok && has_rows)
-          store_sum<D>(p, x, cur.r, a, sum, o_at, s, row,
-                       x.alternate && s == 1 ? kAside : part, redo && !(x.alternate && s == 1));
-        if (x.alternate && turn == 1) {
-          __threadfence_block();
-          softmax_sync();
-        }
+      Join* const other = reinterpret_cast<Join*>(smem + L::kJoin);
+      if (x.alternate) {  // slot 0 stores for both
+        if (s == 1)
+          other[row] = Join{lse_of(sum), 1.f / sum.l, sum.top,
+                            (sum.tiles > 0 ? 1 : 0) | (sum.aside ? 2 : 0)};
+        tc_fence_before_sync();
+        if (s == 1 && sum.aside) __threadfence_block();
+        softmax_sync();
       }
+      if (ok && has_rows && !(x.alternate && s == 1))
+        store_sum<D>(p, x, cur.r, a, sum, o_at, s, row, part, redo, q_tile,
+                     x.alternate ? other : nullptr);
       tc_fence_before_sync();
-      if (x.alternate) softmax_sync();  // slot 1's sum has been read
+      if (x.alternate) softmax_sync();  // what slot 1 has summed has been read
       t0 += x.count;
       left -= x.count;
-      const uint32_t next = kept_next;
-      kept_next = kept;
-      kept = next;
+      if (left > 0) {
+        next_item(p, cur);
+        keep_cursor(kept, cur);
+      }
     }
   }
 
