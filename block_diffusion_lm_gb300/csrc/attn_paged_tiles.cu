@@ -5,27 +5,34 @@
 // Rows.  The query rows of one KV head of a sequence, (token, head of the group)
 // flattened, in row tiles of 128; a CTA works on two of them ("slots") against the
 // keys that any of their rows reads, in tiles of 128 keys.  A last single row tile
-// goes to both slots, which take the key tiles in turn and are joined at the end
-// (`alternate`).  The list of steps (a pair of row tiles, a key tile, a KV head) is
-// cut as in attn_paged.cu (paged_work.cuh), with as many partials and the same
+// goes to both slots, which take the key tiles in turn; slot 0 joins the two sums at
+// the end (`alternate`).  The list of steps (a pair of row tiles, a key tile, a KV
+// head) is cut as in attn_paged.cu (paged_work.cuh), with as many partials and the same
 // joining kernel.
 //
 // Operands.  K, V and Q are f16 in shared memory, P f16 in TMEM, all under powers of
 // two that fp32 takes back: E4M3 codes are exact in f16, and so are their group
 // scales 2^(e - E) down to 2^-24, with E the largest scale byte of the K tile, and of
 // V twice the largest so far in the feature group (O is rescaled when one grows past
-// that, and when a row's maximum has grown by 2^5.9, for all of the warp's rows).  An operand below 2^-31 of the largest beside it becomes
-// 0.  P is p 2^10, rounded to 2^-11 of itself (2^-35 of the row's largest at least).
+// that, and when a row's maximum has grown by 2^5.9, for all of the warp's rows).  An
+// operand below 2^-31 of the largest beside it becomes 0.  P is p 2^10, rounded to
+// 2^-11 of itself (2^-35 of the row's largest at least).
 //
 // Keys.  One warp looks the pages up and starts the copies of K's codes and the scale
 // bytes into a ring of three half tiles, another those of V's (cp.async: one bulk copy
 // per key takes 58 clocks of the issuing warp each); five warps write K and V as f16
 // into 128-byte-swizzled tiles: one for K (S(t) of both slots is done long before
 // K(t + 1) is wanted) and two for V.  An alternate piece, which has one Q tile, puts
-// every other K in the place of the second.  A handover between warps takes 300 to 400
-// clocks, and with one V tile the round P V, conversion, P V was the longest chain.
-// One thread issues the MMAs, two warpgroups do the softmax, a row per thread, as in
-// the training forward.
+// every other K in the place of the second.  One thread issues the MMAs, two warpgroups
+// do the softmax, a row per thread, as in the training forward.
+//
+// What bounds it.  16 sequences of 16,384 keys, 8 heads of 128, 160 rows: 258 us, where
+// the bytes take 66 and the MMAs 141 (of 2 x 128 rows); a chunk of 2,000 tokens in a
+// window of 1,024: 203 us, MMAs 60.  A pair of row tiles takes a key tile in 4,600
+// clocks: two softmax rows of 128 scores per thread (1,800 clocks alone, 3,700 both at
+// once), P V, and the next S, with a handover of 300 to 400 clocks between them, and
+// beside that the conversion of K and V (3,500).  An item of a window costs 12,000 more
+// for its result and the next Q.
 //
 // Keys that a row does not read are masked.  Where some row of the pair does not read
 // a key of a tile, NaN in V is written as 0 and remembered: the rows that read it are
@@ -309,10 +316,9 @@ struct Copier {
     look();
 #pragma unroll 1
     for (int t = 0; t < steps; ++t) {
-      // (V(t - 2), which had K's half tile, has been converted: so the places and scale
-      // words of tile t - 3 are free too)
+      // (the places and scale words of tile t - 3 are free: V(t - 3) had been converted
+      // when the codes of K(t - 1) were copied)
       const int h = 2 * t;
-      if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
       Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
       if (begins) {  // keys that all rows of the pair read
         const int first = (cur.entry - cur.b * p.row_tiles) * kPairRows;
@@ -365,6 +371,8 @@ struct Copier {
         info.k_after = alternate && m > 1 ? t - 2 : t - 1;
       }
       ++m;
+      // V(t - 2) had the half tile (and all that waited for bRows of t - 2 are past it)
+      if (h >= kHalves && !wait(L::bFree + h % kHalves, h / kHalves - 1)) return;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::bRows + (t & 1)]);
       copy(p.k, t, h % kHalves);
