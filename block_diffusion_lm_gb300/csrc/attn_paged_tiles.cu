@@ -106,14 +106,14 @@ struct Info {
   float k_factor;     // of S
   uint32_t k_top;     // E of K
   uint32_t top;       // E of V, a byte per group
-  int j0;             // first key
+  int at, cut, j0;    // its first place in the list; the first [0, cut) of its keys are
+                      // sinks (at ..), the others keys j0 + their place in the tile
   int edge;           // some row does not read some key
   int upper;          // the scale bytes are the upper half of their words
   int item;           // the CTA's pieces so far
   int first;          // of a piece
   int k_at;           // where K goes
   int k_after;        // the tile whose S has to be done by then
-  int pad[2];
 };
 static_assert(sizeof(Info) == 64, "");
 
@@ -238,10 +238,6 @@ __device__ __forceinline__ Cursor kept_cursor(uint32_t at) {
   return c;
 }
 
-// First key of step k.
-__device__ __forceinline__ int key_of(const Range& r, int k) {
-  return k < r.n_first ? k * kTileKeys : r.lo + (k - r.n_first) * kTileKeys;
-}
 // 2^(kHeadroom - delta) in f16, both halves; 0 below 2^-24, NaN for a byte of 255.
 __device__ __forceinline__ uint32_t operand_scale(int top, int byte) {
   const int delta = top - byte;
@@ -301,14 +297,13 @@ struct Copier {
   __device__ __forceinline__ void run_k(Cursor& cur, int steps) {
     int page[4], place[4];  // of keys lane + 32 x of the next tile
     const auto look = [&] {
-      const int end = cur.step < cur.r.n_first ? cur.r.first : cur.r.hi;
-      const int j0 = key_of(cur.r, cur.step) + lane;
+      const int i0 = cur.step * kTileKeys + lane, end = cur.r.keys();
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int j = j0 + 32 * x, entry = p.by_page(j);
+        const int j = cur.r.key(i0 + 32 * x), entry = p.by_page(j);
         place[x] = j - entry * p.page_size;
         page[x] = -1;
-        if (j < end) page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
+        if (i0 + 32 * x < end) page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
       }
     };
     int item = 0, hi = 0, lo = 0, m = 0;
@@ -328,8 +323,11 @@ struct Copier {
         hi = p.causal ? cur.r.c - p.queries + static_cast<int>(p.by_G(first)) + 1 : cur.r.c;
         lo = p.window ? cur.r.c - p.queries + static_cast<int>(p.by_G(last)) - p.window + 1 : 0;
       }
-      const int j0 = key_of(cur.r, cur.step);
-      bool edge = !(j0 + kTileKeys <= hi && (j0 >= lo || j0 + kTileKeys <= p.sinks));
+      const int at = cur.step * kTileKeys, cut = min(max(cur.r.first - at, 0), kTileKeys);
+      const int j0 = at - cur.r.first + cur.r.lo;  // (of a key that is no sink)
+      // (the first sinks are read by all rows)
+      bool edge = cut < kTileKeys && !(j0 + kTileKeys <= hi &&
+                                       (j0 + cut >= lo || j0 + kTileKeys <= p.sinks));
       uint32_t rows = mem + L::kRows + (t % 3) * (kTile * 4) + lane * 4;
       uint32_t words = mem + L::kWords + (t % 3) * (2 * kTile * 4) + lane * 4;
       uint32_t there[4];
@@ -360,6 +358,8 @@ struct Copier {
       if (lane == 0) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) info.there[x] = there[x];
+        info.at = at;
+        info.cut = cut;
         info.j0 = j0;
         info.edge = edge;
         info.upper = D == 64 && p.wide_scales && (cur.block & 1);
@@ -622,8 +622,8 @@ __device__ __noinline__ uint32_t nan_features(const PagedParams& p, const Piece 
                                               const RowAt a, int c) {
   uint32_t bad = 0;
   for (int k = x.k0; k < x.k0 + x.count; ++k) {
-    const int j0 = key_of(r, k), end = k < r.n_first ? r.first : r.hi;
-    for (int j = j0; j < min(j0 + kTileKeys, end); ++j) {
+    for (int i = k * kTileKeys; i < min((k + 1) * kTileKeys, r.keys()); ++i) {
+      const int j = r.key(i);
       if (!(j < a.hi && (j >= a.lo || j < p.sinks))) continue;
       const int entry = p.by_page(j);
       const int pg = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_pages + entry);
@@ -1044,14 +1044,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                       sv + c * 32, sv + (c + 1) * 32);
         if (info.edge) {
           const uint32_t there[4] = {info.there[0], info.there[1], info.there[2], info.there[3]};
-          const auto below = [&](int j, int q) -> uint32_t {  // keys of word q before j
-            const int n = min(max(j - info.j0 - 32 * q, 0), 32);
+          const auto first = [&](int n, int q) -> uint32_t {  // those of word q among the first n
+            n = min(max(n - 32 * q, 0), 32);
             return n == 32 ? ~0u : (1u << n) - 1;
           };
+          const int cut = info.cut, at = info.at, j0 = info.j0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            const uint32_t sinks = first(cut, q);
             const uint32_t reads =
-                there[q] & below(hi, q) & (~below(lo, q) | (p.window ? below(p.sinks, q) : 0u));
+                there[q] &
+                ((sinks & first(hi - at, q)) |
+                 (~sinks & first(hi - j0, q) &
+                  (~first(lo - j0, q) | (p.window ? first(p.sinks - j0, q) : 0u))));
             if (!__all_sync(0xffffffffu, reads == ~0u))
 #pragma unroll
             for (int c = 0; c < 32; ++c)

@@ -112,12 +112,21 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return (m >> 7) * 0xffu;
 }
 
+// Whole row tiles, on the tensor-memory path (attn_paged_tiles.cu); its steps are tiles
+// of 128 keys of one KV head.
+constexpr int kPairRows = 256;
+constexpr int kTileKeys = 128;
+
 // ------------------------------------------------------------ the work list
 // The keys that a row tile reads: [0, first) and [lo, hi), in steps.
 struct Range {
   int c;           // keys of the sequence
   int first, lo, hi;
   int n_first, n;  // steps: of [0, first), and all (at least one)
+  // Where both parts are one list (whole tiles: a step of a few sinks alone cost a tenth
+  // of a window of 1,024), the key at place i of it, and its length.
+  __device__ __forceinline__ int key(int i) const { return i < first ? i : i - first + lo; }
+  __device__ __forceinline__ int keys() const { return first + hi - lo; }
 };
 
 __device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile, int tile_rows) {
@@ -131,8 +140,9 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile,
   r.lo = min(r.lo, r.hi);
   r.first = p.window ? min(p.sinks, r.lo) : 0;
   const int more = p.step_keys - 1;
-  r.n_first = p.by_step(r.first + more);
-  r.n = max(r.n_first + static_cast<int>(p.by_step(r.hi - r.lo + more)), 1);
+  r.n_first = tile_rows == kPairRows ? 0 : p.by_step(r.first + more);
+  const int others = tile_rows == kPairRows ? r.keys() : r.hi - r.lo;
+  r.n = max(r.n_first + static_cast<int>(p.by_step(others + more)), 1);
   return r;
 }
 
@@ -208,10 +218,6 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, uint32_t* room
   return s;
 }
 
-// Whole row tiles of 256 on the tensor-memory path (attn_paged_tiles.cu); its steps
-// are tiles of 128 keys of one KV head.
-constexpr int kPairRows = 256;
-constexpr int kTileKeys = 128;
 cudaError_t launch_tiles(const PagedParams& p, int d, cudaStream_t stream);
 
 }  // namespace paged

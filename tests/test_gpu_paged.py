@@ -366,6 +366,9 @@ def test_attention(shape, causal, window, sinks):
     (2, 4, 150, 64, 8, 2, 128, True, 0, 0),
     (1, 20, 200, 64, 10, 2, 64, False, 3000, 4),
     (1, 300, 60, 64, 4, 1, 128, True, 1000, 4),     # a chunk
+    (1, 300, 60, 64, 4, 1, 128, True, 1000, 200),   # sinks end inside a tile
+    (2, 100, 40, 48, 3, 1, 64, False, 300, 128),
+    (2, 100, 40, 48, 3, 1, 64, True, 129, 127),
 ])
 def test_attention_over_long_texts(B, n, per, page, Hq, Hkv, d, causal, window, sinks):
     c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 12,
