@@ -14,8 +14,8 @@
 // as many per group of SMs: the CTAs of a group read the same tokens at the same
 // time, and sectors of scale bytes that they share come from DRAM once): every CTA adds the lengths up and finds its
 // share itself, so that lengths never come to the host.  A row tile that is cut
-// leaves normalised fp32 partials with their LSE in the workspace, which a second
-// kernel joins exactly ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
+// leaves normalised fp32 partials with their LSE in the workspace, which are joined
+// exactly, by the last CTA that leaves one or by a second kernel ([Blog] "在线 softmax 合并：为什么分两段算仍是同一个注意力").
 //
 // Matrix products.  With so few rows the tensor-memory path would write every K and
 // V value to shared memory once more, as bf16, and that alone would bound it: the
@@ -106,6 +106,19 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 // Warps of a CTA, by its registers: 32 sums and 16 words of Q per lane and 8 rows.
 __host__ __device__ constexpr int most_warps(int tiles) { return tiles == 1 ? 12 : 8; }
 
+// Whether the CTAs join what was cut.  One query of 32 heads: 64 x 8,192 keys take 140 us
+// so and 145 with a kernel of its own, 4 x 1,048,576 484 and 513, a window of 1,024 37.5
+// either way, 3 x 1,000 keys of 2 heads 8.9 and 9.4; but with 16 rows to a tile, which one
+// CTA joins, 16 sequences of 10 rows and 8 heads take 120 and 98.
+__host__ __device__ constexpr bool joins_itself(int tile_rows) { return tile_rows == 8; }
+
+// Pieces of cut items that a CTA has left, two at most, in shared memory.
+struct Pieces {
+  int entry[2], block[2];
+  int first[2], n[2];  // CTAs first, first + lanes, .. have its n pieces
+  int count, last;
+};
+
 // ------------------------------------------------------------ shared memory
 template <int D, int NT>
 struct Rows {
@@ -124,8 +137,10 @@ struct Rows {
   static constexpr int kSumRow = D + 4;
   static constexpr int kSumZ = kSum + 4 * kSumRow * 4;
   static constexpr int kWarpBytes = (kSumZ + 16 + 127) / 128 * 128;
+  static_assert((kMostWarps * 4 + sizeof(Cursor)) <= 192, "find_share beside Pieces");
   static_assert(kScales + kKeys * kGroups * 8 <= kSumZ, "shared memory of a warp");
-  static constexpr int kRoom = 256;  // find_share, in front
+  static constexpr int kPieces = 192;
+  static constexpr int kRoom = 256;  // find_share and Pieces, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
 
   // Place of a key's 16-byte chunks: chunk c lies at c ^ this.  The rows that an
@@ -770,13 +785,124 @@ struct Kernel {
   }
 };
 
+// 4 features (f ..) of U rows that were cut into n pieces, of which piece k lies at
+// at[u] + k step (+ begin for the first) among the partials; (b, q_row, head)[u] is what
+// they are, b < 0 for none.  (From L2: other CTAs wrote them, perhaps in this launch.)
+struct JoinedRow {
+  int b, q_row, head;
+};
+template <int D, int U>
+__device__ __forceinline__ void join_rows(const PagedParams& p, int n, const int64_t (&at)[U],
+                                          int64_t step, int64_t begin,
+                                          const JoinedRow (&row)[U], int f) {
+  float m[U], both[U];
+  float4 o[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    m[u] = -INFINITY;
+    both[u] = 0.f;
+    o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    float z[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t x = at[u] + k * step + (k == 0 ? begin : 0);
+      z[u] = __ldcg(p.part_z + x);
+      v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + x * D + f));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // (a piece that has read nothing is O = 0, LSE = -inf)
+      const float most = fmaxf(m[u], z[u]), ref = most == -INFINITY ? 0.f : most;
+      const float old = ex2_approx(m[u] - ref), w = ex2_approx(z[u] - ref);
+      m[u] = most;
+      both[u] = fmaf(both[u], old, w);
+      o[u].x = fmaf(w, v[u].x, o[u].x * old);
+      o[u].y = fmaf(w, v[u].y, o[u].y * old);
+      o[u].z = fmaf(w, v[u].z, o[u].z * old);
+      o[u].w = fmaf(w, v[u].w, o[u].w * old);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (row[u].b < 0) continue;
+    const float inv = both[u] == 0.f ? 0.f : __fdividef(1.f, both[u]);
+    const float z = both[u] == 0.f ? -INFINITY : m[u] + lg2_approx(both[u]);
+    const int i = p.by_G(row[u].q_row), h = row[u].head * p.G + row[u].q_row - i * p.G;
+    const int64_t token = static_cast<int64_t>(row[u].b) * p.queries + i;
+    *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) = make_uint2(
+        pack_bf16x2(o[u].x * inv, o[u].y * inv), pack_bf16x2(o[u].z * inv, o[u].w * inv));
+    if (f == 0)
+      p.lse[(static_cast<int64_t>(row[u].b) * p.Hq + h) * p.queries + i] = z * 0.6931471805599453f;
+  }
+}
+
+// Joins the pieces of an item.  The whole CTA calls it.
+template <int D, int R>
+__device__ __forceinline__ void join_item(const PagedParams& p, int entry, int block, int first,
+                                          int n) {
+  constexpr int kLanes = D / 4;
+  const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
+  const int rows = min(R, p.queries * p.G - tile * R);
+  // the first piece is where the item begins, the others are their CTAs' first
+  const int64_t piece = static_cast<int64_t>(p.heads) * R;
+  constexpr int U = 2;
+  const int stride = blockDim.x / kLanes, all = p.heads * rows;
+  for (int x0 = threadIdx.x / kLanes; x0 < all; x0 += U * stride) {
+    int64_t at[U];
+    JoinedRow row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = min(x0 + u * stride, all - 1);
+      const int head_in = x / rows, r = x - head_in * rows, head = block * p.heads + head_in;
+      at[u] = 2 * first * piece + head_in * R + r;
+      row[u] = JoinedRow{x0 + u * stride < all && head < p.Hkv ? b : -1, tile * R + r, head};
+    }
+    join_rows<D, U>(p, n, at, 2 * p.lanes * piece, piece, row, threadIdx.x % kLanes * 4);
+  }
+}
+
+// The last CTA to have left a piece of an item joins them, in their order.  At the end,
+// where the CTA has its registers for that.
+template <int D, int R>
+__device__ __forceinline__ void join_pieces(const PagedParams& p, Pieces& cut) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int last = 0;
+    for (int x = 0; x < cut.count; ++x) {
+      int* arrived = p.arrived + static_cast<int64_t>(cut.entry[x]) * p.head_blocks + cut.block[x];
+      int before;  // (releases the CTA's pieces, acquires the others')
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                   : "=r"(before)
+                   : "l"(arrived)
+                   : "memory");
+      if (before == cut.n[x] - 1) {
+        *arrived = 0;  // for the next launch
+        last |= 1 << x;
+      }
+    }
+    cut.last = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int x = 0; x < 2; ++x)
+    if (cut.last >> x & 1)
+      join_item<D, R>(p, cut.entry[x], cut.block[x], cut.first[x], cut.n[x]);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
     paged_rows_kernel(const __grid_constant__ PagedParams p) {
   using L = Rows<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr bool kFused = joins_itself(L::kRows);
+  if (!kFused) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint8_t* warps = smem + L::kRoom;
+  Pieces& cut = *reinterpret_cast<Pieces*>(smem + L::kPieces);
+  if (threadIdx.x == 0) cut.count = 0;
   Kernel<D, NT> k(p, warps + (threadIdx.x >> 5) * L::kWarpBytes);
   Cursor cursor{};
   const Share share =
@@ -821,13 +947,20 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
         // a CTA leaves at most two partials: where an item ends or goes through (0)
         // and where one begins (1); the latter knows how many there are
         const bool starts = r.step <= i;
-        const int left = r.n - 1 - r.step;  // steps of the item in later shares
-        if (starts && threadIdx.x == 0)
+        const bool whole = starts && r.step + 1 == r.n;
+        k.finish(r, whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0), z, warps);
+        if (!kFused && starts && threadIdx.x == 0)
           p.pieces[static_cast<int64_t>(r.entry) * p.head_blocks + r.block] =
               make_int2(static_cast<int>(blockIdx.x),
-                        1 + static_cast<int>((left + share.per - 1) / share.per));
-        k.finish(r, starts && left == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0),
-                 z, warps);
+                        1 + static_cast<int>((r.n - 1 - r.step + share.per - 1) / share.per));
+        if (kFused && !whole && threadIdx.x == 0) {
+          const uint32_t first = share.begin + i - r.step, last = first + r.n - 1;
+          const int x = cut.count++, c = first / share.per;  // (of the lane's CTAs)
+          cut.entry[x] = r.entry;
+          cut.block[x] = r.block;
+          cut.first[x] = c * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
+          cut.n[x] = static_cast<int>(last / share.per) - c + 1;
+        }
       }
     }
     }
@@ -840,54 +973,35 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
     copies_commit();
   }
   copies_wait<0>();
+  if (kFused) join_pieces<D, L::kRows>(p, cut);
 }
 
-// Joins the partials of a row tile that was cut; a CTA per head and 8 rows of it.
+// Joins the pieces where a launch does not do so itself; a CTA per head and 8 rows.
 template <int D>
 __global__ void __launch_bounds__(128)
     paged_join_kernel(const __grid_constant__ PagedParams p, int tile_rows) {
   constexpr int kLanes = D / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int item = blockIdx.x, chunks = (tile_rows + 7) / 8;
+  const int item = blockIdx.x, chunks = tile_rows / 8;
   const int head_in = blockIdx.y / chunks, from = (blockIdx.y - head_in * chunks) * 8;
   const int2 piece = p.pieces[item];
   if (piece.y <= 1) return;
   const int entry = item / p.head_blocks, block = item - entry * p.head_blocks;
   const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
   const int head = block * p.heads + head_in;
-  if (head >= p.Hkv) return;
-  const int rows = min(min(tile_rows, from + 8), p.queries * p.G - tile * tile_rows) - from;
-  for (int x = threadIdx.x; x < rows * kLanes; x += 128) {
-    const int row = from + x / kLanes, f = x % kLanes * 4;
-    float most = -INFINITY, both = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the first piece is where the item begins, the others are their CTAs' first
-    const auto place = [&](int k) {
-      return (static_cast<int64_t>(2 * (piece.x + k * p.lanes) + (k == 0)) * p.heads + head_in) * tile_rows + row;
-    };
-#pragma unroll 4
-    for (int k = 0; k < piece.y; ++k) most = fmaxf(most, p.part_z[place(k)]);
-    const float ref = most == -INFINITY ? 0.f : most;
-#pragma unroll 4
-    for (int k = 0; k < piece.y; ++k) {
-      const float z = p.part_z[place(k)], w = ex2_approx(z - ref);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + place(k) * D + f);
-      if (z == -INFINITY) continue;  // it has read nothing
-      both += w;
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
-    }
-    const float inv = both == 0.f ? 0.f : __fdividef(1.f, both);
-    const float z = both == 0.f ? -INFINITY : ref + lg2_approx(both);
-    const int r = tile * tile_rows + row, i = p.by_G(r), h = head * p.G + r - i * p.G;
-    const int64_t token = static_cast<int64_t>(b) * p.queries + i;
-    *reinterpret_cast<uint2*>(p.o + (token * p.Hq + h) * D + f) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (f == 0)
-      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.queries + i] = z * 0.6931471805599453f;
+  const int rows = min(8, p.queries * p.G - tile * tile_rows - from);
+  if (rows <= 0 || head >= p.Hkv) return;
+  constexpr int U = 8 * kLanes / 128;
+  const int64_t size = static_cast<int64_t>(p.heads) * tile_rows;  // of a piece
+  int64_t at[U];
+  JoinedRow row[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = threadIdx.x / kLanes + u * (128 / kLanes);
+    at[u] = 2 * piece.x * size + head_in * tile_rows + from + min(r, rows - 1);
+    row[u] = JoinedRow{r < rows ? b : -1, tile * tile_rows + from + r, head};
   }
+  join_rows<D, U>(p, piece.y, at, 2 * p.lanes * size, size, row, threadIdx.x % kLanes * 4);
 }
 
 // ------------------------------------------------------------------- host
@@ -998,7 +1112,7 @@ cudaError_t join(const PagedParams& p, const Cut& cut, int d, cudaStream_t strea
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(cut.items),
-                     static_cast<unsigned>(cut.heads * ((cut.tile_rows + 7) / 8)));
+                     static_cast<unsigned>(cut.heads * (cut.tile_rows / 8)));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = &early;
@@ -1094,6 +1208,7 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.aside_o = reinterpret_cast<float*>(ws + at.aside_o);
   a.aside_z = reinterpret_cast<float*>(ws + at.aside_z);
   a.pieces = reinterpret_cast<int2*>(ws + at.pieces);
+  a.arrived = reinterpret_cast<int*>(ws + at.pieces);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const auto run = [&](auto d) {
     constexpr int D = decltype(d)::value;
@@ -1105,6 +1220,7 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
                                     : run(std::integral_constant<int, 64>());
   timer_end(timed, stream);
   if (e != cudaSuccess) return CSBP_ERR_CUDA;
+  if (joins_itself(cut.tile_rows)) return CSBP_OK;
   const int joined = timer_begin(14, stream);
   e = join(a, cut, cache->d, s);
   timer_end(joined, stream);

@@ -34,6 +34,8 @@ struct PagedParams {
   float* part_o;  // [2 x CTAs][heads][tile rows][d]
   float* part_z;  // [2 x CTAs][heads][tile rows]
   int2* pieces;   // per sequence, row tile and head block: first CTA, number of them
+  int* arrived;   // in their place where the CTAs join them: how many are there, 0
+                  // between launches
   // sums put aside: [CTAs x warps][tile rows][d], or [CTAs][tile rows][d] where a CTA
   // works on whole tiles, and their LSE
   float *aside_o, *aside_z;

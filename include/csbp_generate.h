@@ -170,9 +170,11 @@ typedef struct {
  * (Hkv, d, page_size).  0 for an invalid problem.                          */
 size_t csbp_paged_workspace_bytes(const csbp_paged_problem* problem, const csbp_kv_cache* cache);
 
-/* The cache's d is 64 or 128.  workspace: zeroed once by the caller, as in
- * csbp_attn_fwd; calls that can overlap need workspaces of their own.
- *  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]       */
+/* The cache's d is 64 or 128; its pages x page_size places are counted in 31 bits.
+ * workspace: zeroed whole by the caller before its first call; its later calls are
+ * of the same problem, and calls that can overlap need workspaces of their own.
+ *  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]
+ * CSBP_ERR_UNSUPPORTED: another d; tokens x heads, keys or steps past 31 bits.  */
 csbp_status csbp_attn_paged(const csbp_paged_problem* problem, const csbp_kv_cache* cache,
                             const csbp_paged_inputs* in, void* o, float* lse, void* workspace,
                             size_t ws_bytes, void* stream);
