@@ -335,7 +335,7 @@ extern "C" csbp_status csbp_kernel_timing_read_kind(int32_t kind, double* ms, in
   return CSBP_OK;
 }
 
-extern "C" int32_t csbp_version(void) { return 500; }  // 0.5.0: generation operators
+extern "C" int32_t csbp_version(void) { return 600; }  // 0.6.0: append and paged attention
 
 extern "C" const char* csbp_status_string(csbp_status s) {
   switch (s) {

@@ -9,7 +9,7 @@ namespace csbp {
 
 // Timer kinds (csbp_kernel_timing) after those of csbp_internal.h: 11 cache
 // write and append, 12 cache read, 13 prefix and paged attention, 14 the joining
-// of the former's pieces, 15 draft verification.
+// of their pieces in a kernel of its own, 15 draft verification.
 constexpr int kAllTimerKinds = kTimerKinds + 5;
 
 // Encode a 3-D TMA descriptor (a CUtensorMap at `map`) over a bf16 tensor,

@@ -332,8 +332,8 @@ csbp_status csbp_kernel_timing_read(double* fwd_ms, int32_t* n_fwd, double* bwd_
  * stream), 9 the dK/dV converts of a windowed backward (one pair per key
  * stream); 10 csbp_e4m3_to_bf16; and (csbp_generate.h) 11 csbp_cache_write and
  * csbp_cache_append, 12 csbp_cache_read, 13 the attention kernel of
- * csbp_attn_prefix or csbp_attn_paged and 14 the joining of the former's key
- * ranges, 15 csbp_draft_verify.  One event pair per launch.
+ * csbp_attn_prefix or csbp_attn_paged and 14 the joining of their key ranges
+ * (where a kernel of its own does that), 15 csbp_draft_verify.  One event pair per launch.
  * CSBP_ERR_INVALID for another kind. */
 csbp_status csbp_kernel_timing_read_kind(int32_t kind, double* ms, int32_t* n);
 
@@ -356,7 +356,8 @@ const char* csbp_status_string(csbp_status status);
  * 0.3.0 (300) added the token and batch strides of csbp_inputs and
  * csbp_schedule_info.problem_key.  0.4.0 (400) added csbp_problem.per_rank
  * and rank (one CSBP rank's query rows) and csbp_attn_bwd_noalloc_status.
- * 0.5.0 (500) added csbp_generate.h. */
+ * 0.5.0 (500) added csbp_generate.h.  0.6.0 (600) added csbp_rotary_turns,
+ * csbp_cache_append, csbp_paged_workspace_bytes and csbp_attn_paged. */
 int32_t csbp_version(void);
 
 #ifdef __cplusplus
