@@ -14,7 +14,7 @@
 // two that fp32 takes back: E4M3 codes are exact in f16, and so are their group
 // scales 2^(e - E) down to 2^-24, with E the largest scale byte of the K tile, and of
 // V twice the largest so far in the feature group (O is rescaled when one grows past
-// that, and when a row's maximum has grown by 2^5.9, for all of the warp's rows).  An
+// that, and when the maximum of a row has grown by 2^5.9).  An
 // operand below 2^-31 of the largest beside it becomes 0.  P is p 2^10, rounded to
 // 2^-11 of itself (2^-35 of the row's largest at least).
 //
@@ -1068,14 +1068,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kTile; c += 2) mx4[c / 2 % 4] = fmax3(mx4[c / 2 % 4], sv[c], sv[c + 1]);
         const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
         const float m_new = fmaxf(sum.m, mx * mult);
-        // where a row's maximum has grown by too much (never while both are -inf), that of
-        // all of the warp's rows is brought up to date: O is rescaled for all of them
-        const bool need = __any_sync(0xffffffffu, m_new > sum.m + kThreshold);
+        // A row's maximum is brought up to date where it has grown by too much itself: what
+        // other rows of the warp read does not say when.  (false while both are -inf)
+        const bool need = m_new > sum.m + kThreshold;
         const uint32_t now = info.top;
-        if (sum.tiles > 0 && (now != sum.top || need)) {
+        if (sum.tiles > 0 && (now != sum.top || __any_sync(0xffffffffu, need))) {
           // O holds the P V so far, under the old maximum and E (its last P V is done:
           // this S was issued after it)
-          const float alpha = need && m_new != sum.m ? exp2f(sum.m - m_new) : 1.f;
+          const float alpha = need ? exp2f(sum.m - m_new) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D / 8; ++c) {  // (8 at a time: the scores are in registers)
             const int by = static_cast<int>((now >> 8 * (c / 4) & 255) - (sum.top >> 8 * (c / 4) & 255));
@@ -1084,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         sum.top = now;
-        if (need && m_new != sum.m) {
+        if (need) {
           sum.l *= exp2f(sum.m - m_new);  // 0 when sum.m was -inf
           sum.m = m_new;
         }

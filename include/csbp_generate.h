@@ -174,6 +174,10 @@ size_t csbp_paged_workspace_bytes(const csbp_paged_problem* problem, const csbp_
  * workspace: zeroed whole by the caller before its first call; its later calls are
  * of the same problem, and calls that can overlap need workspaces of their own.
  *  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]
+ * Operands are held with 8 (q) and 4 (k, v) bits of significand under powers of
+ * two; with more than 48 query rows per KV head and sequence, a value below 2^-31
+ * of the largest scale beside it counts as 0 (k: among 128 keys; v: in its group
+ * of features among the keys read so far).
  * CSBP_ERR_UNSUPPORTED: another d; tokens x heads, keys or steps past 31 bits.  */
 csbp_status csbp_attn_paged(const csbp_paged_problem* problem, const csbp_kv_cache* cache,
                             const csbp_paged_inputs* in, void* o, float* lse, void* workspace,

@@ -536,6 +536,34 @@ def test_keys_that_are_not_read_do_not_matter(B, n, Hq, Hkv, causal, window, sin
                     assert torch.equal(zx, zw)
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,d", [(2, 4, 2, 64), (12, 4, 2, 128), (60, 4, 2, 128),
+                                        (200, 2, 1, 64)])
+def test_rows_do_not_depend_on_other_rows(n, Hq, Hkv, d):
+    """Another query, or a key that only later queries read, changes nothing for a
+    row, bit by bit: also where it changes the other rows' maxima by much."""
+    B, page, per = 2, 16, 40
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 34, [per * page, 500])
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+    q[:, :, :, 3] = 1
+    want = [x.clone() for x in a.forward(q, c, table, length)]
+    for i, factor in ((1, 100.0), (n // 2, float("nan")), (n - 1, -7.0)):
+        q2 = q.clone()
+        q2[:, i] *= factor
+        o, lse = a.forward(q2, c, table, length)
+        others = [x for x in range(n) if x != i]
+        assert same((o[:, others], lse[:, :, others]), (want[0][:, others], want[1][:, :, others]))
+    later = 1 if n == 2 else n // 2       # a key of that query's own place
+    for b in range(B):
+        j = int(length[b]) - n + later
+        pg = int(table[b, j // page])
+        c.k_scale[pg, j % page] += 8
+        c.k[pg, j % page, :, 3] = 0x7e    # 448 x the scale, where all queries are 1
+        c.v_scale[pg, j % page] += 5
+    o, lse = a.forward(q, c, table, length)
+    assert same((o[:, :later], lse[:, :, :later]), (want[0][:, :later], want[1][:, :, :later]))
+    assert not torch.equal(lse[:, :, later:], want[1][:, :, later:])
+
+
 def test_values_far_apart():
     """Scales from 2^-100 to 2^100 beside one another."""
     B, n, per, page, Hq, Hkv, d = 1, 1, 8, 16, 4, 1, 64
