@@ -1164,8 +1164,10 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.q_bat = (p.batch > 1 && in->stride_batch != 0) ? in->stride_batch : span;
   if (a.q_bat < span || a.q_bat % 8 != 0 || a.q_bat >= kMaxElems) return CSBP_ERR_INVALID;
   if (ws_bytes < kStatusBytes) return CSBP_ERR_WORKSPACE;
-  // places in the cache are counted in 32 bits
-  if (cache->pages * cache->page_size > 0x7fffffff) return CSBP_ERR_UNSUPPORTED;
+  // places in the cache are counted in 31 bits, heads of them in 32
+  if (cache->pages * cache->page_size >
+      std::min<int64_t>(0x7fffffff, 0xffffffffll / cache->Hkv))
+    return CSBP_ERR_UNSUPPORTED;
   int sms = 0;
   if (!device_sms(sms)) sms = 152;
   const Cut cut = cut_of(p, *cache);

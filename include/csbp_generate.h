@@ -170,7 +170,8 @@ typedef struct {
  * (Hkv, d, page_size).  0 for an invalid problem.                          */
 size_t csbp_paged_workspace_bytes(const csbp_paged_problem* problem, const csbp_kv_cache* cache);
 
-/* The cache's d is 64 or 128; its pages x page_size places are counted in 31 bits.
+/* The cache's d is 64 or 128; its pages x page_size places are counted in 31
+ * bits, and their heads in 32.
  * workspace: zeroed whole by the caller before its first call; its later calls are
  * of the same problem, and calls that can overlap need workspaces of their own.
  *  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]

@@ -185,6 +185,9 @@ def test_bad_paged_calls_are_refused():
                      (dict(Hkv=3), INVALID), (dict(page_size=0), INVALID)):
         assert attn(c=cache(**kw)) == want
         assert csbp.paged_workspace_bytes(problem(), cache(**kw)) == 0
+    for kw in (dict(pages=1 << 27), dict(pages=1 << 26, page_size=16, Hkv=4)):
+        assert attn(c=cache(**kw)) == UNSUPPORTED
+    assert attn(c=cache(pages=(1 << 26) - 1, page_size=16, Hkv=4), n=256) == WORKSPACE
     for kw in (dict(pages=0), dict(pages=1 << 31), dict(k=None), dict(v_scale=None),
                dict(v=PTR + 8)):
         assert attn(c=cache(**kw)) == INVALID
