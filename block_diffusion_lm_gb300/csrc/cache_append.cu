@@ -18,7 +18,10 @@
 // token and goes through its heads, so that an angle's sine and cosine are worked
 // out once for all heads that the warp takes; d / 16 lanes hold a head, each 8
 // features and the 8 that they are rotated with.  131,042 tokens of 48 heads of
-// 128: 408 us, 5.4 TB/s; 2,048 of 56 heads: 13.3 us; one token's 8 heads of each: 4.
+// 128: 380 us, 5.8 TB/s; 2,048 of 56 heads: 12.7 us; 8 tokens of 48 heads: 3.4.
+// What counts for many tokens is how many loads are in flight: 24 warps per SM in CTAs of
+// 4 (of 8 warps: 392 us), the next step's K or V loaded while one is encoded (406), sines
+// and cosines in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,11 +33,12 @@
 #include "csbp_generate.h"
 #include "csbp_internal.h"
 #include "kv_cache.cuh"
+#include "ptx_sm100.cuh"
 
 namespace csbp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 512;  // d / 16 lanes of one warp
 
@@ -107,6 +111,13 @@ __device__ __forceinline__ void rotate(T* lo, T* hi, const T* c, const T* s, boo
       hi[e] = a * s[e] + b * c[e];
     }
   }
+}
+
+__device__ __forceinline__ void lds_f4(uint32_t a, float* r) {
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+               : "r"(a)
+               : "memory");
 }
 
 struct Encoded {
@@ -182,10 +193,11 @@ __device__ __forceinline__ void store(const AppendArgs& a, bool v, int64_t slot,
   if ((x1 & 3) == 0) scales[x1 >> 2] = static_cast<uint8_t>(x.byte[1]);
 }
 
-__global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) cache_append_kernel(const __grid_constant__ AppendArgs a) {
   // per chunk of 8 features of the heads in a step: magnitude and pair size (or a
   // 64-bit magnitude)
   __shared__ __align__(16) float2 room[kWarps][64];
+  __shared__ float4 angle[4][kThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t token = item / a.parts;
@@ -219,17 +231,29 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_
   const int64_t pos = static_cast<int64_t>(__ldg(a.c.start + r.b)) + r.i;
 
   const uint64_t* turns = a.turns + 8 * l;
-  float cosine[8], sine[8];
+  if (turned) {
+    float cosine[8], sine[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cosine[e] = 1.f;
-    sine[e] = 0.f;
-    if (turned) {
+    for (int e = 0; e < 8; ++e) {
       const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(turns + e);
       sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sine[e],
                 &cosine[e]);
     }
+    angle[0][threadIdx.x] = make_float4(cosine[0], cosine[1], cosine[2], cosine[3]);
+    angle[1][threadIdx.x] = make_float4(cosine[4], cosine[5], cosine[6], cosine[7]);
+    angle[2][threadIdx.x] = make_float4(sine[0], sine[1], sine[2], sine[3]);
+    angle[3][threadIdx.x] = make_float4(sine[4], sine[5], sine[6], sine[7]);
   }
+  // (from shared memory each time: the registers hold a step's loads instead)
+  const uint32_t angles = smem_u32(&angle[0][threadIdx.x]);
+  const auto turn_pairs = [&](float* lo, float* hi) {
+    float c[8], s[8];
+    lds_f4(angles, c);
+    lds_f4(angles + kThreads * 16, c + 4);
+    lds_f4(angles + 2 * kThreads * 16, s);
+    lds_f4(angles + 3 * kThreads * 16, s + 4);
+    rotate(lo, hi, c, s, a.interleaved != 0);
+  };
 
   // ------- Q, two heads of a lane at a time
   const __nv_bfloat16* q = a.q + r.b * a.q_bat[0] + r.i * a.q_tok[0];
@@ -252,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_
         lo[e] = value(raw[k].lo, e);
         hi[e] = value(raw[k].hi, e);
       }
-      if (turned) rotate(lo, hi, cosine, sine, a.interleaved != 0);
+      if (turned) turn_pairs(lo, hi);
       uint32_t w[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -273,16 +297,24 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_
   // steps that have a scale to be worked out in 64 bits, one bit for every 32nd
   uint32_t again = 0;
   float2* mine = room[warp] + head0 * 2 * a.lanes;
+  const auto fetch = [&](int step) {
+    const bool v = step >= a.kv_steps;
+    const int head = (v ? step - a.kv_steps : step) * at_once + head0;
+    const __nv_bfloat16* src = (v ? a.c.src[1] + r.b * a.c.bat[1] + r.i * a.c.tok[1]
+                                  : a.c.src[0] + r.b * a.c.bat[0] + r.i * a.c.tok[0]) +
+                               static_cast<int64_t>(head) * a.d;
+    return load(src, v ? 2 * l : c0, v ? 2 * l + 1 : c1,
+                here && head < a.Hkv && step < 2 * a.kv_steps);
+  };
+  Raw next = fetch(part);
 #pragma unroll 1
   for (int step = part; step < 2 * a.kv_steps; step += a.parts) {
     const bool v = step >= a.kv_steps, turn = !v && turned;
     const int head = (v ? step - a.kv_steps : step) * at_once + head0;
     const bool has = here && head < a.Hkv;
     const int x0 = v ? 2 * l : c0, x1 = v ? 2 * l + 1 : c1;
-    const __nv_bfloat16* src = (v ? a.c.src[1] + r.b * a.c.bat[1] + r.i * a.c.tok[1]
-                                  : a.c.src[0] + r.b * a.c.bat[0] + r.i * a.c.tok[0]) +
-                               static_cast<int64_t>(head) * a.d;
-    const Raw raw = load(src, x0, x1, has);
+    const Raw raw = next;
+    next = fetch(step + a.parts);
     float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -302,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_append_kernel(const __grid_
         for (int e = 0; e < 8; ++e) n0 = fmaxf(n0, fabsf(lo[e]) + fabsf(hi[e]));
         n1 = n0;
       }
-      rotate(lo, hi, cosine, sine, a.interleaved != 0);
+      turn_pairs(lo, hi);
     }
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -436,7 +468,7 @@ extern "C" csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_
     return CSBP_ERR_CUDA;
   // few tokens are shared among warps, up to 32 per SM: then latency counts, and
   // the sines and cosines that each of them works out do not (2,048 tokens of 56
-  // heads: 16 per SM 17.7 us, 24 16.2, 32 13.3, 64 16.9)
+  // heads: 24 per SM 14.8 us, 32 12.7, 48 15.4)
   const int64_t tokens = static_cast<int64_t>(a.c.batch) * a.c.rows;
   a.parts = static_cast<int32_t>(
       std::max<int64_t>(1, std::min<int64_t>(2 * a.kv_steps + a.q_steps, 32 * sms / tokens)));
