@@ -555,7 +555,9 @@ struct Kernel {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
           most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], o));
-        const float now = fmaxf(m[x], most[x]), f = ex2_approx(m[x] - now);
+        // (a row's own maximum says when it is brought up to date, not the others')
+        const float now = most[x] > m[x] + 1.f ? most[x] : m[x];
+        const float f = now == m[x] ? 1.f : ex2_approx(m[x] - now);
         m[x] = now;
         l[x] *= f;
 #pragma unroll

@@ -536,13 +536,13 @@ def test_keys_that_are_not_read_do_not_matter(B, n, Hq, Hkv, causal, window, sin
                     assert torch.equal(zx, zw)
 
 
-@pytest.mark.parametrize("n,Hq,Hkv,d", [(2, 4, 2, 64), (12, 4, 2, 128), (60, 4, 2, 128),
-                                        (200, 2, 1, 64)])
+@pytest.mark.parametrize("n,Hq,Hkv,d", [(2, 8, 4, 64), (12, 8, 4, 128), (60, 8, 4, 128),
+                                        (200, 4, 4, 64)])
 def test_rows_do_not_depend_on_other_rows(n, Hq, Hkv, d):
     """Another query, or a key that only later queries read, changes nothing for a
     row, bit by bit: also where it changes the other rows' maxima by much."""
-    B, page, per = 2, 16, 40
-    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 34, [per * page, 500])
+    B, page, per = 8, 64, 64              # several steps in a row for every CTA
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 34, [per * page] * 7 + [2000])
     a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
     q[:, :, :, 3] = 1
     want = [x.clone() for x in a.forward(q, c, table, length)]
