@@ -995,6 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             copy_query<D>(p, x, a, q_tile, row & ~31);
             q_scale[row] = convert_query<D>(p, q_tile, row);
           }
+          __syncwarp();  // (the other slot may read what all lanes have written)
           if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
         }
         hi = a.hi;

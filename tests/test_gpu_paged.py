@@ -594,6 +594,21 @@ def test_queries_far_apart():
     check_attn(a.forward(q2, c, table, length), q2, c, table, length, False, 0, 0, 2.0 ** -20)
 
 
+# ------------------------------------------ pieces of several tiles of keys
+@pytest.mark.parametrize("n,Hq,Hkv,d", [(32, 16, 8, 64), (30, 16, 4, 128)])
+def test_queries_of_other_sizes_in_tiles_taken_in_turn(n, Hq, Hkv, d):
+    """64 and 120 rows per KV head, whose tiles of keys go to two halves of a CTA in
+    turn, four and more to a CTA: each row under its own power of two."""
+    B, page, per = 8, 64, 16
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 41,
+                                    [1024, 1000, 900, 1, 129, 128, 513, 1023])
+    q = q * torch.exp2((torch.arange(n * Hq, device="cuda") % 11 - 8.0)).view(1, n, Hq, 1).bfloat16()
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+    out = a.forward(q, c, table, length)
+    check_attn(out, q, c, table, length, True, 0, 0, d ** -0.5)
+    assert same(a.forward(q, c, table, length), out)
+
+
 # --------------------------------------------------------------- as one runs
 def step_state(seed, B=3, n=4, Hq=8, Hkv=2, d=64, page=16, per=8, layers=2):
     g = gen(seed)
