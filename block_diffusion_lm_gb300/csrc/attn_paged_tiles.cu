@@ -81,7 +81,7 @@ struct Tiles {
   static constexpr int kRows = kInfo + kInfos * 64;  // [3 tiles][key] place in the cache
   static constexpr int kBar = kRows + 3 * kTile * 4;
   // barriers; those of K and V are [2] by tile
-  static constexpr int bQFull = 0;                  // [2] per slot
+  static constexpr int bQFull = 0;                  // [2] per slot: it begins a piece
   static constexpr int bKFull = 2, bKEmpty = 4, bVFull = 6, bVEmpty = 8;
   static constexpr int bSFull = 10, bPFull = 12, bPvDone = 14;  // [2] per slot
   static constexpr int bDrain = 16;
@@ -365,8 +365,9 @@ struct Copier {
         info.upper = D == 64 && p.wide_scales && (cur.block & 1);
         info.item = item;
         info.first = begins;
-        // (the second Q tile is free when the piece before is done, and its MMAs are
-        // when the first S of this piece is)
+        // (the second Q tile is free when slot 1 has stored the piece before, which passes
+        // through it, and the MMAs before are done: so it is when the first S of this piece
+        // is, which waits for slot 1's arrival on its bQFull, in every piece)
         info.k_at = alternate && (m & 1) ? L::kQ + L::kTileBytes : L::kK;
         info.k_after = alternate && m > 1 ? t - 2 : t - 1;
       }
@@ -850,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
       bool ok = true;
-      int npv0 = 0, npv1 = 0, nq0 = 0, nq1 = 0;  // P V issued and Q tiles taken per slot
+      int npv0 = 0, npv1 = 0, pieces = 0;        // P V issued per slot, pieces so far
       int sum0 = 0, sum1 = 0;                    // key tiles in the accumulators
       // (descriptors are made where they are used: 64 registers hold few of them)
       const uint32_t base = smem_u32(smem);
@@ -886,8 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece x = piece_of(p, cur, left);
         const bool both = !x.alternate;
         const int count = x.count;
-        ok = mbar_wait(&bars[L::bQFull], nq0++ & 1, p.status, abort_flag);
-        if (ok && both) ok = mbar_wait(&bars[L::bQFull + 1], nq1++ & 1, p.status, abort_flag);
+        ok = mbar_wait(&bars[L::bQFull], pieces & 1, p.status, abort_flag) &&
+             mbar_wait(&bars[L::bQFull + 1], pieces & 1, p.status, abort_flag);
+        ++pieces;
         sum0 = sum1 = 0;
         // S of tile m and P V of tile m - 1, of the slots that work on them, each as soon
         // as what it reads is there (a slot's S after its P V, which reads the P there):
@@ -990,14 +992,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first_row = x.alternate ? 0 : s * kTile;
         has_rows = first_row + (warp & 3) * 32 < x.rows;  // warp-uniform
         const RowAt a = row_at(p, x, cur.r.c, first_row + row);
-        if (s == 0 || !x.alternate) {
-          if (has_rows) {
-            copy_query<D>(p, x, a, q_tile, row & ~31);
-            q_scale[row] = convert_query<D>(p, q_tile, row);
-          }
-          __syncwarp();  // (the other slot may read what all lanes have written)
-          if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
+        if (has_rows && (s == 0 || !x.alternate)) {
+          copy_query<D>(p, x, a, q_tile, row & ~31);
+          q_scale[row] = convert_query<D>(p, q_tile, row);
         }
+        // (all lanes have stored the piece before and written what the other slot may read)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::bQFull + s]);
         hi = a.hi;
         lo = a.lo;
         count = x.count;

@@ -609,6 +609,39 @@ def test_queries_of_other_sizes_in_tiles_taken_in_turn(n, Hq, Hkv, d):
     assert same(a.forward(q, c, table, length), out)
 
 
+@pytest.mark.parametrize("n,G,d,causal,lens", [
+    (300, 1, 64, True, [513, 700, 385, 897, 640, 900]),   # 256 + 44 rows
+    (92, 4, 128, False, [300, 513, 1000, 129, 640, 256]),  # 256 + 112
+    (257, 1, 128, True, [200, 1000, 513, 650, 400, 900]),  # 256 + 1; rows without a key
+    (200, 3, 64, True, [800, 100, 300, 1000, 500, 129]),   # 512 + 88
+])
+def test_pairs_of_row_tiles_before_a_single_one(n, G, d, causal, lens):
+    """Rows that are some pairs of row tiles of 128 and a single one at the end, with so
+    many heads that a CTA goes from the one to the other with several tiles of keys in
+    each.  The heads hold the same and have the same scores, so their results differ by
+    what the cuts of their keys change: at most half a step of O (2^-8 of it) and 2^-11 of
+    the largest |v| (P's rounding and the exponential) each; LSE by the sums' 2^-18."""
+    B, page, per, Hkv = 6, 64, 16, 19
+    c, q, table, length = attn_case(B, n, per, page, G, 1, d, 42, lens)
+    many = csbp.QuantCache(c.k.shape[0], page, Hkv, d)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        getattr(many, name).copy_(getattr(c, name).expand_as(getattr(many, name)))
+    qm = q.repeat(1, 1, Hkv, 1)
+    a = csbp.PagedAttention(B, n, per, page, G * Hkv, Hkv, d, causal=causal)
+    o, lse = a.forward(qm, many, table, length)
+    a.check()
+    assert same(a.forward(qm, many, table, length), (o, lse))
+    # the first head against the oracle, the others against it
+    check_attn((o[:, :, :G], lse[:, :G]), q, c, table, length, causal, 0, 0, d ** -0.5)
+    k, v = values(c)
+    tol = 2.0 ** -7 * o[:, :, :G].float().abs() + 2.0 ** -10 * float(np.abs(v).max())
+    for h in range(1, Hkv):
+        assert ((o[:, :, h * G:h * G + G].float() - o[:, :, :G].float()).abs() <= tol).all(), h
+        z = lse[:, h * G:h * G + G]
+        assert torch.equal(z.isinf(), lse[:, :G].isinf())
+        assert ((z - lse[:, :G]).nan_to_num(0.0).abs() <= 2.0 ** -14).all()
+
+
 # --------------------------------------------------------------- as one runs
 def step_state(seed, B=3, n=4, Hq=8, Hkv=2, d=64, page=16, per=8, layers=2):
     g = gen(seed)
