@@ -1126,7 +1126,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
             make_int2(static_cast<int>(blockIdx.x),
                       1 + static_cast<int>((later + share.per - 1) / share.per));
-      const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
       const int part =
           starts && later == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
       Join* const other = reinterpret_cast<Join*>(smem + L::kJoin);
@@ -1138,6 +1137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s == 1 && sum.aside) __threadfence_block();
         softmax_sync();
       }
+      // (known when the last V is in its tile: both slots' last P V are done by now)
+      const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
       if (ok && has_rows && !(x.alternate && s == 1))
         store_sum<D>(p, x, cur.r, a, sum, o_at, s, row, part, redo, q_tile,
                      x.alternate ? other : nullptr);

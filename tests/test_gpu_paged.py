@@ -642,6 +642,43 @@ def test_pairs_of_row_tiles_before_a_single_one(n, G, d, causal, lens):
         assert ((z - lse[:, :G]).nan_to_num(0.0).abs() <= 2.0 ** -14).all()
 
 
+@pytest.mark.parametrize("n,G,d", [(32, 2, 64), (40, 3, 128), (64, 2, 128), (150, 1, 64),
+                                   (300, 1, 64), (200, 3, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_nan_at_the_end_of_a_text(n, G, d, causal):
+    """NaN in V's codes and scale bytes in the last, partial tile of one, two, three and
+    four: single row tiles, pairs, and both.  Rows that read the key are NaN in its features
+    and nowhere else, the others and all LSE stay as they are, bit by bit."""
+    page, per, Hkv = 16, 32, 19
+    lens = [70, 129, 200, 250, 300, 383, 400, 500, 510, 180, 255, 140]
+    B = len(lens)
+    c, q, table, length = attn_case(B, n, per, page, G * Hkv, Hkv, d, 43, lens)
+    a = csbp.PagedAttention(B, n, per, page, G * Hkv, Hkv, d, causal=causal)
+    clean = [x.clone() for x in a.forward(q, c, table, length)]
+    bad = torch.zeros((B, n, G * Hkv, d), dtype=torch.bool, device="cuda")
+    for b, m in enumerate(lens):
+        j = m - 1 - b % 4 * (n // 5 if causal else 1)     # in the last tile of keys, as a rule
+        pg = int(table[b, j // page])
+        for h in range(b % 2, Hkv, 2):
+            if h % 4 < 2:
+                c.v[pg, j % page, h, 7 * h % d] = 0xff
+                hit = slice(7 * h % d, 7 * h % d + 1)
+            else:
+                e = h % (d // 32)
+                c.v_scale[pg, j % page, h, e] = 255
+                hit = slice(32 * e, 32 * e + 32)
+            first = max(0, j - m + n) if causal else 0    # the first query that reads it
+            if j < 0:                                     # (a place behind the text: none)
+                first = n
+            bad[b, first:, h * G:h * G + G, hit] = True
+    for _ in range(3):
+        o, lse = a.forward(q, c, table, length)
+        assert torch.equal(lse, clean[1])
+        assert torch.equal(o.isnan(), bad)
+        assert torch.equal(torch.where(bad, 0, o), torch.where(bad, 0, clean[0]))
+    a.check()
+
+
 # --------------------------------------------------------------- as one runs
 def step_state(seed, B=3, n=4, Hq=8, Hkv=2, d=64, page=16, per=8, layers=2):
     g = gen(seed)
