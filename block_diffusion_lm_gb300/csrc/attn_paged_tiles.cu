@@ -248,6 +248,25 @@ __device__ __forceinline__ uint32_t operand_scale(int top, int byte) {
   return h | h << 16;
 }
 
+// Keys that all rows of a pair read, besides the sinks: [lo, hi).
+struct Common {
+  int lo, hi;
+};
+__device__ __forceinline__ Common common_of(const PagedParams& p, int c, int tile) {
+  const int first = tile * kPairRows, last = min(first + kPairRows, p.queries * p.G) - 1;
+  Common x;
+  x.hi = p.causal ? c - p.queries + static_cast<int>(p.by_G(first)) + 1 : c;
+  x.lo = p.window ? c - p.queries + static_cast<int>(p.by_G(last)) - p.window + 1 : 0;
+  return x;
+}
+// Whether some row of the pair does not read some key of a tile, going by the places of its
+// keys: the first `cut` are sinks, the others keys j0 + their place in it.  (The first
+// sinks are read by all rows.)
+__device__ __forceinline__ bool edge_of(const PagedParams& p, const Common& x, int cut, int j0) {
+  return cut < kTileKeys && !(j0 + kTileKeys <= x.hi &&
+                              (j0 + cut >= x.lo || j0 + kTileKeys <= p.sinks));
+}
+
 // -------------------------------------------------------------------- copies
 // Two warps: one looks keys up and copies K and the scale bytes, one copies V and works
 // the scales' maxima out once they are there.
@@ -306,7 +325,8 @@ struct Copier {
         if (i0 + 32 * x < end) page[x] = __ldg(p.table + static_cast<int64_t>(cur.b) * p.table_pages + entry);
       }
     };
-    int item = 0, hi = 0, lo = 0, m = 0;
+    int item = 0, m = 0;
+    Common common{};
     bool begins = true, alternate = false;
     look();
 #pragma unroll 1
@@ -315,19 +335,15 @@ struct Copier {
       // when the codes of K(t - 1) were copied)
       const int h = 2 * t;
       Info& info = reinterpret_cast<Info*>(smem + L::kInfo)[t % kInfos];
-      if (begins) {  // keys that all rows of the pair read
-        const int first = (cur.entry - cur.b * p.row_tiles) * kPairRows;
-        const int last = min(first + kPairRows, p.queries * p.G) - 1;
-        alternate = last - first < kTile;
+      if (begins) {
+        const int tile = cur.entry - cur.b * p.row_tiles;
+        alternate = p.queries * p.G - tile * kPairRows <= kTile;
         m = 0;
-        hi = p.causal ? cur.r.c - p.queries + static_cast<int>(p.by_G(first)) + 1 : cur.r.c;
-        lo = p.window ? cur.r.c - p.queries + static_cast<int>(p.by_G(last)) - p.window + 1 : 0;
+        common = common_of(p, cur.r.c, tile);
       }
       const int at = cur.step * kTileKeys, cut = min(max(cur.r.first - at, 0), kTileKeys);
       const int j0 = at - cur.r.first + cur.r.lo;  // (of a key that is no sink)
-      // (the first sinks are read by all rows)
-      bool edge = cut < kTileKeys && !(j0 + kTileKeys <= hi &&
-                                       (j0 + cut >= lo || j0 + kTileKeys <= p.sinks));
+      bool edge = edge_of(p, common, cut, j0);
       uint32_t rows = mem + L::kRows + (t % 3) * (kTile * 4) + lane * 4;
       uint32_t words = mem + L::kWords + (t % 3) * (2 * kTile * 4) + lane * 4;
       uint32_t there[4];
@@ -616,24 +632,46 @@ __device__ __noinline__ float convert_query(const PagedParams& p, uint32_t tile,
   return p.scale_log2 * ldexpf(1.f, ex - 7);
 }
 
-// Features (of chunk c, a bit each) that are NaN in some key of the piece that the row
-// reads.
+// Features (of chunk c, a bit each) that are NaN in some key that the row reads of those
+// tiles of the piece from which NaN has been taken out: those at an edge, or with a key
+// that is not there.  (The others carry it through the MMAs.  All keys of a long text, each
+// byte by itself, would take longer than the waits of the other roles allow.)
 template <int D>
 __device__ __noinline__ uint32_t nan_features(const PagedParams& p, const Piece x, const Range r,
                                               const RowAt a, int c) {
   uint32_t bad = 0;
+  const Common common = common_of(p, r.c, x.tile);
+  const int32_t* table = p.table + static_cast<int64_t>(x.b) * p.table_pages;
+  const auto missing = [&](int j, int end) {  // whether one of keys [j, end) is
+    bool some = false;
+    for (int entry = p.by_page(j); j < end && !some; j = ++entry * p.page_size)
+      some = static_cast<uint32_t>(__ldg(table + entry)) >= static_cast<uint32_t>(p.pages);
+    return some;
+  };
   for (int k = x.k0; k < x.k0 + x.count; ++k) {
-    for (int i = k * kTileKeys; i < min((k + 1) * kTileKeys, r.keys()); ++i) {
+    const int at = k * kTileKeys, cut = min(max(r.first - at, 0), kTileKeys);
+    const int j0 = at - r.first + r.lo, end = min(at + kTileKeys, r.keys());
+    if (!edge_of(p, common, cut, j0) && end == at + kTileKeys && !missing(at, at + cut) &&
+        !missing(j0 + cut, j0 + kTileKeys))
+      continue;
+    for (int i = at; i < end; ++i) {
       const int j = r.key(i);
       if (!(j < a.hi && (j >= a.lo || j < p.sinks))) continue;
       const int entry = p.by_page(j);
-      const int pg = __ldg(p.table + static_cast<int64_t>(x.b) * p.table_pages + entry);
+      const int pg = __ldg(table + entry);
       if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) continue;
       const uint64_t slot = static_cast<uint32_t>(pg * p.page_size + j - entry * p.page_size);
       const uint64_t place = slot * p.Hkv + x.head;
       if (__ldg(p.v_scale + place * (D / 32) + c) == 255) bad = ~0u;
-      for (int i = 0; i < 32; ++i)
-        if ((__ldg(p.v + place * D + c * 32 + i) & 0x7f) == 0x7f) bad |= 1u << i;
+      const uint4* codes = reinterpret_cast<const uint4*>(p.v + place * D + c * 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 v = __ldg(codes + h);
+        const uint32_t nan[4] = {nan_codes(v.x), nan_codes(v.y), nan_codes(v.z), nan_codes(v.w)};
+        if (nan[0] | nan[1] | nan[2] | nan[3])
+#pragma unroll
+          for (int e = 0; e < 16; ++e) bad |= (nan[e / 4] >> 8 * (e % 4) & 1) << (16 * h + e);
+      }
     }
   }
   return bad;

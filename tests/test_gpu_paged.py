@@ -679,6 +679,66 @@ def test_nan_at_the_end_of_a_text(n, G, d, causal):
     a.check()
 
 
+def test_nan_in_tiles_of_all_kinds():
+    """NaN in V at a window's edges, among sinks, beside a page that is not there, and in
+    tiles that all rows read: NaN for the rows that read it, the same as before for the
+    others."""
+    page, per, Hkv, G, d, n = 16, 80, 19, 1, 64, 100
+    B, m, window, sinks = 3, 1270, 700, 200
+    t = m - n + np.arange(n)
+    for causal in (True, False):
+        for j in (3, 198, 199, 460, 471, 490, 569, 570, 571, 700, 900, 1000, 1169, 1170, 1200, 1269):
+            c, q, table, length = attn_case(B, n, per, page, G * Hkv, Hkv, d, 44, [m] * B)
+            table[:, 915 // page] = -1
+            a = csbp.PagedAttention(B, n, per, page, G * Hkv, Hkv, d, causal=causal, window=window,
+                                    sinks=sinks)
+            clean = [x.clone() for x in a.forward(q, c, table, length)]
+            for b in range(B):
+                pg = int(table[b, j // page])
+                c.v[pg, j % page, ::2, 40 + b] = 0x7f
+                c.v_scale[pg, j % page, 1::2, 0] = 255
+            reads = torch.from_numpy(((j <= t) | (not causal)) & ((t - j < window) | (j < sinks))).cuda()
+            bad = torch.zeros((B, n, Hkv, d), dtype=torch.bool, device="cuda")
+            for b in range(B):
+                bad[b, :, ::2, 40 + b] = reads[:, None]
+                bad[b, :, 1::2, :32] = reads[:, None, None]
+            o, lse = a.forward(q, c, table, length)
+            assert torch.equal(lse, clean[1]) and torch.equal(o.isnan(), bad), (causal, j)
+            assert torch.equal(torch.where(bad, 0, o), torch.where(bad, 0, clean[0]))
+
+
+def test_nan_does_not_make_a_long_text_slow():
+    """A CTA with 150,000 keys of its own and NaN in the last of them works for as long as
+    without (four times is allowed)."""
+    page, per, B, n, Hkv, d = 64, 2400, 152, 64, 1, 128
+    c = filled(B + 8, page, Hkv, d, gen(45))
+    table = torch.randint(0, 8, (B, per), generator=gen(46), device="cuda").int()
+    table[:, -1] = 8 + torch.arange(B, device="cuda").int()
+    length = i32([per * page - 5] * B)
+    q = normal(gen(47), B, n, 1, d)
+    a = csbp.PagedAttention(B, n, per, page, 1, Hkv, d, causal=True)
+
+    def ms():
+        times = []
+        for _ in range(4):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            o, lse = a.forward(q, c, table, length)
+            end.record()
+            end.synchronize()
+            times.append(start.elapsed_time(end))
+        a.check()
+        return min(times), o, lse
+
+    clean, want, z = ms()
+    c.v[8:, page - 7, 0, 77] = 0xff          # read by the last two queries
+    slow, o, lse = ms()
+    assert o[:, -2:, 0, 77].isnan().all() and torch.equal(lse, z)
+    o[:, -2:, 0, 77] = want[:, -2:, 0, 77]
+    assert torch.equal(o, want)
+    assert slow <= 4 * clean, (slow, clean)
+
+
 # --------------------------------------------------------------- as one runs
 def step_state(seed, B=3, n=4, Hq=8, Hkv=2, d=64, page=16, per=8, layers=2):
     g = gen(seed)
