@@ -351,12 +351,12 @@ struct Kernel {
       for (int x = 0; x < 2; ++x) {
         const int at = cur.c - p.queries + static_cast<int>(p.by_G(min(row0 + 8 * n + 2 * t + x, rows - 1)));
         row_hi[2 * n + x] = p.causal ? at + 1 : cur.c;
-        row_lo[2 * n + x] = p.window ? at - p.window + 1 : 0;
+        row_lo[2 * n + x] = window_begin(p, at);
       }
     }
     const int i0 = p.by_G(row0), i1 = p.by_G(min(row0 + L::kRows, rows) - 1);
     all_hi = p.causal ? cur.c - p.queries + i0 + 1 : cur.c;
-    all_lo = p.window ? cur.c - p.queries + i1 - p.window + 1 : 0;
+    all_lo = window_begin(p, cur.c - p.queries + i1);
     aside = false;
     clear();
   }

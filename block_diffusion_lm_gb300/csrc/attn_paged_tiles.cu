@@ -256,7 +256,7 @@ __device__ __forceinline__ Common common_of(const PagedParams& p, int c, int til
   const int first = tile * kPairRows, last = min(first + kPairRows, p.queries * p.G) - 1;
   Common x;
   x.hi = p.causal ? c - p.queries + static_cast<int>(p.by_G(first)) + 1 : c;
-  x.lo = p.window ? c - p.queries + static_cast<int>(p.by_G(last)) - p.window + 1 : 0;
+  x.lo = window_begin(p, c - p.queries + static_cast<int>(p.by_G(last)));
   return x;
 }
 // Whether some row of the pair does not read some key of a tile, going by the places of its
@@ -578,7 +578,7 @@ __device__ __forceinline__ RowAt row_at(const PagedParams& p, const Piece& x, in
   a.h = x.head * p.G + r - a.i * p.G;
   const int at = c - p.queries + a.i;
   a.hi = p.causal ? at + 1 : c;
-  a.lo = p.window ? at - p.window + 1 : 0;
+  a.lo = window_begin(p, at);
   return a;
 }
 

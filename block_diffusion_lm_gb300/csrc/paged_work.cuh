@@ -131,6 +131,12 @@ struct Range {
   __device__ __forceinline__ int keys() const { return first + hi - lo; }
 };
 
+// First key of the window of a query at position t.  (No difference of t and the window
+// where it would be negative: with both near 2^31 it could pass 32 bits.)
+__device__ __forceinline__ int window_begin(const PagedParams& p, int t) {
+  return p.window == 0 || t < p.window ? 0 : t - p.window + 1;
+}
+
 __device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile, int tile_rows) {
   Range r;
   r.c = min(max(__ldg(p.length + b), 0), p.table_pages * p.page_size);
@@ -138,8 +144,7 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, int b, int tile,
   const int i1 = p.by_G(min((tile + 1) * tile_rows, p.queries * p.G) - 1);
   const int t0 = r.c - p.queries + i0, t1 = r.c - p.queries + i1;
   r.hi = p.causal ? max(t1 + 1, 0) : r.c;
-  r.lo = p.window ? max(t0 - p.window + 1, 0) : 0;
-  r.lo = min(r.lo, r.hi);
+  r.lo = min(window_begin(p, t0), r.hi);
   r.first = p.window ? min(p.sinks, r.lo) : 0;
   const int more = p.step_keys - 1;
   r.n_first = tile_rows == kPairRows ? 0 : p.by_step(r.first + more);

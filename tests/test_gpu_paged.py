@@ -480,6 +480,24 @@ def test_attention_reads_pages_past_32_bits():
         assert same(got, a.forward(q, small, i32([[0, 1, 2, 3]]), i32([250])))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows_next_to_31_bits(causal):
+    """The longest table and the widest window that it allows, for more queries than a text
+    has keys: positions run from below -1,500 on, and position less window past 32 bits."""
+    n, page, per, lens = 1600, 62145, 34556, [100, 1700]
+    assert 2 ** 31 - 1030 < page * per < 2 ** 31 - 1024
+    c, q, table, _ = attn_case(2, n, 1, page, 1, 1, 64, 48, [0, 0])
+    big = torch.full((2, per), -1, dtype=torch.int32, device="cuda")
+    big[:, :1] = table
+    length = i32(lens)
+    small = csbp.PagedAttention(2, n, 1, page, 1, 1, 64, causal=causal)
+    want = small.forward(q, c, table, length)
+    check_attn(want, q, c, table, length, causal, 0, 0, 64 ** -0.5)
+    for window in (page * per - 1, page * per - 400, 2 ** 31 - 1):
+        a = csbp.PagedAttention(2, n, per, page, 1, 1, 64, causal=causal, window=window, sinks=3)
+        assert same(a.forward(q, c, big, length), want)
+
+
 # ------------------------------------- keys that are not read, not finite
 @pytest.mark.parametrize("name", ["k", "v"])
 @pytest.mark.parametrize("kind", ["code", "scale"])
