@@ -11,8 +11,9 @@
 // Scales.  A rotated value has an error of up to 2^-21 (|a| + |b|) in fp32, which
 // is nothing to its code, but could decide a scale where the group's largest
 // magnitude lies next to 448 x 2^e.  Such groups (one in 10^5) are worked out
-// again in 64 bits, so that the scale is that of the rotation itself; after the
-// others, as a call among them cost the loop 50 registers.
+// again in 64 bits, so that the scale is that of the rotation itself, and written
+// once more where it is another; after the others, as a call among them cost the
+// loop 50 registers.
 //
 // HBM bounds it: 3 + 1/32 bytes per value of K and V, 4 of Q.  A warp holds one
 // token and goes through its heads, so that an angle's sine and cosine are worked
@@ -181,16 +182,20 @@ __device__ __forceinline__ Raw load(const __nv_bfloat16* row, int x0, int x1, bo
   return r;
 }
 
+// Codes of one of a lane's chunks, and the scale byte by the first lane of its group.
+__device__ __forceinline__ void store(uint8_t* codes, uint8_t* scales, int chunk, int byte,
+                                      uint2 code) {
+  reinterpret_cast<uint2*>(codes)[chunk] = code;
+  if ((chunk & 3) == 0) scales[chunk >> 2] = static_cast<uint8_t>(byte);
+}
 // Codes and scale bytes of a lane's two chunks.
 __device__ __forceinline__ void store(const AppendArgs& a, bool v, int64_t slot, int head, int x0,
                                       int x1, const Encoded& x) {
   const int64_t row = slot * a.Hkv + head;
   uint8_t* codes = (v ? a.c.codes[1] : a.c.codes[0]) + row * a.d;
   uint8_t* scales = (v ? a.c.scales[1] : a.c.scales[0]) + row * (a.d / kGroup);
-  reinterpret_cast<uint2*>(codes)[x0] = x.code[0];
-  reinterpret_cast<uint2*>(codes)[x1] = x.code[1];
-  if ((x0 & 3) == 0) scales[x0 >> 2] = static_cast<uint8_t>(x.byte[0]);
-  if ((x1 & 3) == 0) scales[x1 >> 2] = static_cast<uint8_t>(x.byte[1]);
+  store(codes, scales, x0, x.byte[0], x.code[0]);
+  store(codes, scales, x1, x.byte[1], x.code[1]);
 }
 
 __global__ void __launch_bounds__(kThreads, 6) cache_append_kernel(const __grid_constant__ AppendArgs a) {
@@ -374,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 6) cache_append_kernel(const __grid_
   // ------- scales next to a border, and their codes, once more
   again = __reduce_or_sync(0xffffffffu, again);
   if (again == 0) return;
+  __syncwarp();
 #pragma unroll 1
   for (int step = part; step < a.kv_steps; step += a.parts) {
     if (!(again >> ((step / a.parts) & 31) & 1)) continue;
@@ -383,7 +389,15 @@ __global__ void __launch_bounds__(kThreads, 6) cache_append_kernel(const __grid_
         a.c.src[0] + r.b * a.c.bat[0] + r.i * a.c.tok[0] + static_cast<int64_t>(head) * a.d;
     const Encoded x = encode_exact(turns, pos, turned, a.interleaved != 0, load(src, c0, c1, has),
                                    c0, c1, reinterpret_cast<double*>(mine));
-    if (has) store(a, false, slot, head, c0, c1, x);
+    // groups whose scale is another; the step's other groups keep the codes of their fp32
+    // values, whatever the heads are that share the step with them
+    const int64_t at = slot * a.Hkv + head;
+    uint8_t* scales = a.c.scales[0] + at * (a.d / kGroup);
+    const volatile uint8_t* is = scales;
+    const bool other0 = has && is[c0 >> 2] != x.byte[0], other1 = has && is[c1 >> 2] != x.byte[1];
+    __syncwarp();
+    if (other0) store(a.c.codes[0] + at * a.d, scales, c0, x.byte[0], x.code[0]);
+    if (other1) store(a.c.codes[0] + at * a.d, scales, c1, x.byte[1], x.code[1]);
   }
 }
 

@@ -228,6 +228,29 @@ def test_append_scales_next_to_where_they_change():
     check_append(c, before, None, None, k, v, i32([[0]]), i32([0]), None, f, True)
 
 
+@pytest.mark.parametrize("B,Hkv,d", [(20000, 8, 128), (30000, 5, 64), (2000, 40, 512)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_codes_do_not_depend_on_other_heads(B, Hkv, d, interleaved):
+    """A head whose scale lies next to where it changes alters no byte of the others."""
+    g = gen(9)
+    f = freqs(d)
+    f[0] = float(np.arccos(0.875) + 1e-9)       # at position 1, (2, 0) turns to next to 1.75
+    ro = csbp.Rotary(f, interleaved)
+    table, start = torch.arange(B, device="cuda").int()[:, None], i32([1] * B)
+    k = normal(g, B, 1, Hkv, d)
+    got = []
+    for first in (2.0, 1.5):
+        k[:, :, 0] = 0
+        k[:, :, 0, 0] = first
+        c = csbp.QuantCache(B, 2, Hkv, d)
+        c.append(k, k, table, start, rotary=ro)
+        got.append(stored(c))
+    # (in 64 bits the angle is above the border's, the magnitude below it)
+    want = O.quantise(O.rotate(np.eye(1, d)[None] * 2.0, O.angles([1], f), interleaved))[1]
+    assert (got[0][2][:, 1, 0, 0] == int(want[0, 0, 0])).all()
+    assert same([t[:, :, 1:] for t in got[0]], [t[:, :, 1:] for t in got[1]])
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 def test_append_values_that_are_not_finite(value):
     """Both of a pair are stored as NaN, the group's scale is the others'."""
