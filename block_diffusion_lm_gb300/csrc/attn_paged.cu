@@ -28,8 +28,13 @@
 //                of two per row (8 bits of mantissa, exact for elements down to
 //                2^-23 of the row's largest).
 //   O^T = V^T P^T  P is held in f16, as p 2^14 2^(e - E), with V's scale 2^e of the
-//                key and group and E the largest so far: its rounding is 2^-11 of
-//                p, or 2^-39 of the largest p v below f16's normal range.
+//                key and group and E the largest so far, at most 2^14 above it: its
+//                rounding is 2^-11 of p, or 2^-25 of the row's largest p below f16's
+//                normal range.
+// Scales of V farther apart than that would let a key wipe out others, in rows that do not
+// read it or give it next to no weight, too.  They are rare (of a step's 32 keys a value
+// 2^14 times another's largest): keys of a step that are near one another are summed by
+// themselves then, and the sums before and after are put aside and joined in fp32.
 // ldmatrix brings K's codes as four features of a key and, transposed, V's as four
 // keys of a feature; which of the 16 keys is which row of the first product is
 // chosen so that P^T needs one transposition of 8 x 8 for the second.
@@ -138,7 +143,7 @@ struct Rows {
   static constexpr int kWords = 2 * kCodes;
   static constexpr int kRecord = kWords + 2 * kKeys * 4;
   static constexpr int kStage = kRecord + 128;
-  // the step's scales: fp32 of K [key][group], f16 of V [group][key] in two factors
+  // the step's scales: fp32 of K [key][group], f16 of V [group][key]
   static constexpr int kScales = kStages * kStage;
   // and when an item ends, in their place, 4 rows of the result [row][D + 4] and their
   // LSE (log2)
@@ -147,7 +152,7 @@ struct Rows {
   static constexpr int kSumZ = kSum + 4 * kSumRow * 4;
   static constexpr int kWarpBytes = (kSumZ + 16 + 127) / 128 * 128;
   static_assert((kMostWarps * 4 + sizeof(Cursor)) <= 192, "find_share beside Pieces");
-  static_assert(kScales + kKeys * kGroups * 8 <= kSumZ, "shared memory of a warp");
+  static_assert(kScales + kKeys * kGroups * 6 <= kSumZ, "shared memory of a warp");
   static constexpr int kPieces = 192;
   static constexpr int kRoom = 256;  // find_share and Pieces, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
@@ -188,7 +193,7 @@ struct Record {
   int entry, block;  // (see Cursor)
   int step, n;       // of the entry's n
   int c;             // keys of the sequence
-  int pad;
+  uint32_t left;     // keys that are left of a step of which a part has been taken
 };
 
 // A step ahead: its record, and what the lane looked up for its key.
@@ -196,6 +201,15 @@ struct Ahead {
   Record r;
   int page, place;
 };
+
+// Weights of two sums with the LSE (log2) a and b in their join, and its LSE.  In full
+// precision: where scales of V lie far apart this is done for every step.
+__device__ __noinline__ float3 join_sums(float a, float b) {
+  const float most = fmaxf(a, b), ref = most == -INFINITY ? 0.f : most;
+  const float x = exp2f(a - ref), y = exp2f(b - ref), both = x + y;
+  const float f = both == 0.f ? 0.f : 1.f / both;
+  return make_float3(x * f, y * f, both == 0.f ? -INFINITY : ref + log2f(both));
+}
 
 template <int D, int NT>
 struct Kernel {
@@ -365,42 +379,55 @@ struct Kernel {
     return j < row_hi[x] && (j >= row_lo[x] || j < p.sinks);
   }
 
-  // Scales that are above E, far below it or NaN: E becomes the largest so far, and
-  // what was summed under the old one is scaled.  What is left of E - e beyond what
-  // one f16 factor holds goes to a second; whether there is any.
-  __device__ __forceinline__ bool odd_scales(uint32_t word, bool is_there, uint32_t& delta) {
-    uint32_t now = is_there ? word & ~__vcmpeq4(word, 0xffffffffu) : 0;
-    delta = now;
+  // Scales that are above E, far below it or NaN.  E becomes the largest so far, what was
+  // summed under the old one is scaled, and `delta` is E - e, or 15 where a scale is that far
+  // below because its byte is 0 (what is below 2^-118 counts as 0 there) or NaN.
+  //
+  // Where the scales do not lie within 2^14 of E, or E has risen by more than a sum in fp32
+  // can follow, the sum so far is to be put aside first: all of `there` is left for then.
+  // Where they do not lie within 2^14 of one another, `there` becomes those of the first key
+  // and the ones near it in each group.  Returns what is left.  (`fresh`: nothing has been
+  // summed yet.)
+  __device__ __forceinline__ uint32_t odd_scales(uint32_t word, bool fresh, uint32_t& there,
+                                                 uint32_t& delta) {
+    uint32_t left = 0, number, now;
+#pragma unroll 1
+    for (;;) {
+      number = there >> lane & 1 ? word & ~__vcmpeq4(word, 0xffffffffu) : 0;
+      const uint32_t or_none = number | __vcmpeq4(number, 0);  // 255 for 0
+      now = __vmaxu4(number, top);  // (fresh: top is 0)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) now = __vmaxu4(now, __shfl_xor_sync(0xffffffffu, now, o));
-    now = __vmaxu4(now, top);
-#pragma unroll
-    for (int e = 0; e < kG; ++e) {
-      const int by = static_cast<int>((now >> 8 * e & 255) - (top >> 8 * e & 255));
-      const float f = by < 127 ? __uint_as_float(static_cast<uint32_t>(127 - by) << 23) : 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[n][2 * e + k][c] *= f;
+      for (int o = 16; o > 0; o >>= 1) now = __vmaxu4(now, __shfl_xor_sync(0xffffffffu, now, o));
+      if (!__any_sync(0xffffffffu, at_least_u8x4(__vsubus4(now, or_none), 0x0f0f0f0fu) != 0)) break;
+      if (!fresh) return there;
+      const uint32_t first = __shfl_sync(0xffffffffu, number, __ffs(there) - 1);
+      const uint32_t none = __vcmpeq4(first, 0);  // groups of it that go by the largest
+      const uint32_t lo = __vsubus4((first & ~none) | (now & none), 0x07070707u + (0x07070707u & none));
+      const uint32_t hi = __vaddus4((first & ~none) | (now & none), 0x07070707u & ~none);
+      const bool near = at_least_u8x4(or_none, lo) == 0x80808080u &&
+                        at_least_u8x4(hi, number) == 0x80808080u;
+      const uint32_t part = __ballot_sync(0xffffffffu, near) & there;
+      left |= there & ~part;
+      there = part;
     }
-    top = now;
-    const uint32_t all = is_there ? top - delta : 0;  // byte by byte, nothing is borrowed
-    delta = __vminu4(all, 0x0e0e0e0eu);
-    const bool more = __any_sync(0xffffffffu, all != delta);
-    if (more) {
+    if (!fresh) {
+      const uint32_t rise = now - top;  // byte by byte, nothing is borrowed
+      if (at_least_u8x4(rise & ~__vcmpeq4(top, 0), 0x41414141u)) return there;
 #pragma unroll
-      for (int e = 0; e < kG; ++e) {  // 2^-rest, down to f16's last 2^-24, else 0
-        const int rest = static_cast<int>((all - delta) >> 8 * e & 255);
-        const uint32_t h = rest <= 14 ? 0x3c00u - (rest << 10) : rest <= 24 ? 1u << (24 - rest) : 0;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(mem + L::kScales + kKeys * kG * 6 +
-                                                     e * (2 * kKeys) + lane * 2),
-                     "h"(static_cast<uint16_t>(h))
-                     : "memory");
+      for (int e = 0; e < kG; ++e) {
+        const uint32_t by = rise >> 8 * e & 255;
+        const float f = by < 127 ? __uint_as_float((127 - by) << 23) : 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[n][2 * e + k][c] *= f;
       }
     }
-    return more;
+    top = now;
+    delta = there >> lane & 1 ? __vminu4(now - number, 0x0f0f0f0fu) : 0;
+    return left;
   }
 
   // NaN in V (codes, or `v_word`'s scales): NaN in the sums of the rows that read the
@@ -436,13 +463,16 @@ struct Kernel {
     __syncwarp();
   }
 
-  __device__ __forceinline__ void step(const Record& cur, int stage) {
+  // The keys `cur.there` of a step.  Those that are left for a sum of their own (see
+  // odd_scales; none as a rule) go to its record in the ring, and `in_sum`, the steps in the
+  // sum so far, becomes what has this one put aside.
+  __device__ __forceinline__ void step(const Record& cur, int stage, int& in_sum) {
     const uint32_t at = mem + stage * L::kStage;
     const uint32_t scales = mem + L::kScales, v_scales = scales + kKeys * kG * 4;
     // ------- the step's scales, a key per lane
     uint32_t k_word = lds32(at + L::kWords + lane * 4);
     uint32_t v_word = lds32(at + L::kWords + (kKeys + lane) * 4);
-    const uint32_t there = cur.there;
+    uint32_t there = cur.there;
     const bool upper = D == 64 && p.wide_scales && ((cur.block * p.heads + head_in) & 1);
     if (D == 64 && p.wide_scales) {  // its half of the word
       k_word = upper ? k_word >> 16 : k_word & 0xffffu;
@@ -450,15 +480,19 @@ struct Kernel {
     }
     const bool is_there = there >> lane & 1;
     uint32_t delta = is_there ? top - v_word : 0;
-    // f16 holds 2^-delta to delta = 14; two factors beyond
+    // f16 holds 2^-delta to delta = 14
     const uint32_t odd = (delta + (kG == 4 ? 0x71717171u : 0x7171u)) | delta;
-    bool two = is_there && ((odd | ~at_least_u8x4(top, v_word)) & 0x80808080u) != 0;
+    const bool other = is_there && ((odd | ~at_least_u8x4(top, v_word)) & 0x80808080u) != 0;
     bool bad = false;
-    if (__any_sync(0xffffffffu, two)) {
-      two = odd_scales(v_word, is_there, delta);
+    if (__any_sync(0xffffffffu, other)) {
       bad = __any_sync(0xffffffffu, is_there && any_byte_255(v_word));
-    } else {
-      two = false;
+      const uint32_t left = odd_scales(v_word, in_sum == 0, there, delta);
+      if (left) {
+        in_sum = kFlush - 1;
+        if (lane == 0) sts32(at + L::kRecord + 28, left);
+        __syncwarp();
+        if (left == cur.there) return;
+      }
     }
     {
       float f[4];
@@ -472,7 +506,7 @@ struct Kernel {
       } else {
         asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(f[0]), "f"(f[1]) : "memory");
       }
-      // 2^-delta in f16: only the upper byte, 4 (15 - delta)
+      // 2^-delta in f16: only the upper byte, 4 (15 - delta), 0 for 15
       const uint32_t h = 0x3c3c3c3cu - 4 * delta;
 #pragma unroll
       for (int e = 0; e < kG; ++e)
@@ -621,17 +655,6 @@ struct Kernel {
           }
         }
       }
-      if (two) {
-#pragma unroll
-        for (int e = 0; e < kG; ++e) {
-          const uint2 more = lds64(v_scales + kKeys * kG * 2 + e * (2 * kKeys) + 32 * u + 8 * t);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            b[n][e][0] = mul_f16x2(b[n][e][0], more.x);
-            b[n][e][1] = mul_f16x2(b[n][e][1], more.y);
-          }
-        }
-      }
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
         uint32_t w[4], a[8];
@@ -665,14 +688,10 @@ struct Kernel {
       z[x] = sum == 0.f ? -INFINITY : m[x] - kShift + lg2_approx(sum);
       float mine = 1.f, old = 0.f;
       if (aside) {
-        const float before = p.aside_z[at + row], most = fmaxf(before, z[x]);
-        const float ref = most == -INFINITY ? 0.f : most;
-        old = ex2_approx(before - ref);
-        mine = ex2_approx(z[x] - ref);
-        const float both = old + mine, f = both == 0.f ? 0.f : __fdividef(1.f, both);
-        z[x] = both == 0.f ? -INFINITY : ref + lg2_approx(both);
-        old *= f;
-        mine *= f;
+        const float3 both = join_sums(p.aside_z[at + row], z[x]);
+        old = both.x;
+        mine = both.y;
+        z[x] = both.z;
       }
       const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
 #pragma unroll
@@ -924,7 +943,7 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   int in_sum = 0, stage = 0;
   // two rounds that only start copies, then one for each step
 #pragma unroll 1
-  for (int i = -kStages; i < steps; ++i, stage ^= 1) {
+  for (int i = -kStages; i < steps;) {
     Record r;
     if (i >= 0) {
       __syncwarp();
@@ -933,45 +952,50 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
                    : "r"(k.mem + stage * L::kStage + L::kRecord)
                    : "memory");
       asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(r.step), "=r"(r.n), "=r"(r.c), "=r"(r.pad)
+                   : "=r"(r.step), "=r"(r.n), "=r"(r.c), "=r"(r.left)
                    : "r"(k.mem + stage * L::kStage + L::kRecord + 16)
                    : "memory");
-      if (i == 0 || r.step == 0) {
+      if (r.left) {
+        if (k.lane == 0) sts32(k.mem + stage * L::kStage + L::kRecord + 28, 0);
+      } else if (i == 0 || r.step == 0) {
         k.begin(r);
         in_sum = 0;
       }
       copies_wait<kStages - 1>();
       __syncwarp();
-      k.step(r, stage);
-    }
-    if (i >= 0) {
-    const bool ends = r.step + 1 == r.n || i + 1 == steps;
-    if (ends || ++in_sum == kFlush) {
-      float z[2 * NT];
-      k.normalise(z);
-      if (!ends) {
-        k.put_aside(z);
-        in_sum = 0;
-      } else {
-        // a CTA leaves at most two partials: where an item ends or goes through (0)
-        // and where one begins (1); the latter knows how many there are
-        const bool starts = r.step <= i;
-        const bool whole = starts && r.step + 1 == r.n;
-        k.finish(r, whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0), z, warps);
-        if (!kFused && starts && threadIdx.x == 0)
-          p.pieces[static_cast<int64_t>(r.entry) * p.head_blocks + r.block] =
-              make_int2(static_cast<int>(blockIdx.x),
-                        1 + static_cast<int>((r.n - 1 - r.step + share.per - 1) / share.per));
-        if (kFused && !whole && threadIdx.x == 0) {
-          const uint32_t first = share.begin + i - r.step, last = first + r.n - 1;
-          const int x = cut.count++, c = first / share.per;  // (of the lane's CTAs)
-          cut.entry[x] = r.entry;
-          cut.block[x] = r.block;
-          cut.first[x] = c * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
-          cut.n[x] = static_cast<int>(last / share.per) - c + 1;
+      k.step(r, stage, in_sum);
+      const bool ends = r.step + 1 == r.n || i + 1 == steps;
+      if (ends || ++in_sum == kFlush) {
+        float z[2 * NT];
+        k.normalise(z);
+        const uint32_t left = lds32(k.mem + stage * L::kStage + L::kRecord + 28);
+        if (!ends || left) {
+          k.put_aside(z);
+          in_sum = 0;
+          if (left) {  // the step once more, with the keys that are left
+            if (k.lane == 0) sts32(k.mem + stage * L::kStage + L::kRecord, left);
+            continue;
+          }
+        } else {
+          // a CTA leaves at most two partials: where an item ends or goes through (0)
+          // and where one begins (1); the latter knows how many there are
+          const bool starts = r.step <= i;
+          const bool whole = starts && r.step + 1 == r.n;
+          k.finish(r, whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0), z, warps);
+          if (!kFused && starts && threadIdx.x == 0)
+            p.pieces[static_cast<int64_t>(r.entry) * p.head_blocks + r.block] =
+                make_int2(static_cast<int>(blockIdx.x),
+                          1 + static_cast<int>((r.n - 1 - r.step + share.per - 1) / share.per));
+          if (kFused && !whole && threadIdx.x == 0) {
+            const uint32_t first = share.begin + i - r.step, last = first + r.n - 1;
+            const int x = cut.count++, c = first / share.per;  // (of the lane's CTAs)
+            cut.entry[x] = r.entry;
+            cut.block[x] = r.block;
+            cut.first[x] = c * p.lanes + static_cast<int>(blockIdx.x) % p.lanes;
+            cut.n[x] = static_cast<int>(last / share.per) - c + 1;
+          }
         }
       }
-    }
     }
     // (scale words of the step before: nobody waits for them)
     if (i > -kStages) k.store_pending(stage ^ 1, pending);
@@ -980,6 +1004,8 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
       if (i + kStages + 1 < steps) k.look(cursor, next);
     }
     copies_commit();
+    ++i;
+    stage ^= 1;
   }
   copies_wait<0>();
   if (kFused) join_pieces<D, L::kRows>(p, cut);

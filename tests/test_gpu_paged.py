@@ -617,6 +617,153 @@ def test_values_far_apart():
         check_attn(a.forward(q, c, table, length), q, c, table, length, True, 0, 0, d ** -0.5)
 
 
+def largest_terms(q, c, table, length, causal, window, sinks, scale):
+    """Of each O element, the largest weight x scale of V's group among the keys that its
+    query reads."""
+    k, _ = values(c)
+    page, Hkv = c.k.shape[1:3]
+    scales = np.repeat(np.exp2(c.v_scale.cpu().numpy().astype(float) - 127), 32, -1)
+    B, n, Hq, d = q.shape
+    out = np.zeros(q.shape)
+    for b in range(B):
+        m = int(length[b])
+        j = np.arange(m)
+        at = table[b].cpu().numpy()[j // page], j % page
+        for i in range(n):
+            t = m - n + i
+            ok = (j <= t) | (not causal)
+            if window:
+                ok &= (t - j < window) | (j < sinks)
+            for h in range(Hq if ok.any() else 0):
+                x = k[at][ok, h * Hkv // Hq] @ f64(q[b, i, h]) * scale
+                w = np.exp(x - x.max())
+                w /= w.sum()
+                out[b, i, h] = (w[:, None] * scales[at][ok, h * Hkv // Hq]).max(0)
+    return out
+
+
+def check_far(out, q, c, table, length, causal, window, sinks, scale):
+    """As check_attn, but what is lost of P below f16's normal range is allowed for by the
+    keys that a row reads: with p v 2^14 in units of 2^E, where E is at most 2^4 above
+    (largest weight x scale) or taken from it, 2^-24 of a code up to 2^9 for each key, which
+    is 2^-25 of that.  Scores are exact to their dot product's rounding, as there."""
+    k, v = values(c)
+    want, lse, A, T = O.paged_attention(f64(q), k, v, table.cpu().numpy(), length.tolist(),
+                                        c.k.shape[1], causal, window, sinks, scale)
+    d = q.shape[-1]
+    M = largest_terms(q, c, table, length, causal, window, sinks, scale)
+    tol = ((2.0 ** -8 + 2.0 ** -12 + 4 * d * 2.0 ** -24 * T.transpose(0, 2, 1)[..., None]) * A
+           + 2.0 ** -8 * np.abs(want) + 2.0 ** -25 * M * max(length.tolist()))
+    worst = float(np.max(np.abs(f64(out[0]) - want) / np.maximum(tol, 1e-300)))
+    assert worst <= 1, worst
+    z, none = f64(out[1]), lse == -np.inf
+    np.testing.assert_array_equal(z == -np.inf, none)
+    tol = 2 * d * 2.0 ** -24 * T + 2.0 ** -21 + 2.0 ** -22 * np.abs(np.where(none, 0, lse)) + 2.0 ** -16
+    assert (np.abs(z[~none] - lse[~none]) <= tol[~none]).all()
+
+
+# query rows per KV head of up to 8, up to 16 and more
+FAR = [(2, 8, 4, 64), (3, 8, 4, 128), (6, 4, 2, 128), (12, 8, 4, 64), (20, 4, 2, 128)]
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR)
+@pytest.mark.parametrize("by", [16, 40, 100, 124])
+def test_large_values_that_are_not_read(n, Hq, Hkv, d, by):
+    """V of a key, 2^16 to 2^124 times the others', has no part in the rows that do not
+    read it: drafts before it, or queries past its window."""
+    B, page, per = 3, 16, 30
+    lens = [470, 33, 257]
+    for causal, window, sinks, back in ((True, 0, 0, 0), (True, 0, 0, n // 2), (True, 60, 3, 59),
+                                        (True, 60, 3, 59 + n // 2), (False, 60, 0, 59 + n // 2)):
+        c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 51, lens)
+        for b in range(B):
+            j = lens[b] - 1 - back
+            if j >= 0:
+                c.v_scale[int(table[b, j // page]), j % page, :, b % (d // 32)] += by
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window, sinks=sinks)
+        check_far(a.forward(q, c, table, length), q, c, table, length, causal, window, sinks,
+                  d ** -0.5)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR)
+@pytest.mark.parametrize("by", [30, 45, 100])
+def test_large_values_of_next_to_no_weight(n, Hq, Hkv, d, by):
+    """V of a key, 2^30 to 2^100 times the others', with a weight of 2^-80 and less: the
+    others are what O is made of, or both, or the key alone."""
+    B, page, per = 2, 16, 20
+    lens = [300, 130]
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 52, lens)
+    q[..., 3] = 8
+    for b in range(B):
+        for j in (0, 77, lens[b] - n):
+            at = int(table[b, j // page]), j % page
+            c.k[at][:] = 0
+            c.k[at][:, 3] = 0xfe                      # -448
+            c.k_scale[at][:, 0] = 127 - 6             # -7: a score of -56
+            c.v_scale[at][:, 1] += by
+    for causal in (True, False):
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, scale=1.0)
+        check_far(a.forward(q, c, table, length), q, c, table, length, causal, 0, 0, 1.0)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR)
+def test_values_far_apart_in_every_step(n, Hq, Hkv, d):
+    """V's scales anywhere from 2^-100 to 2^100 and groups of zeros among them, in texts
+    of many steps for each warp: against what each row's own keys allow."""
+    B, page, per, pages = 24, 64, 256, 50
+    g = gen(54)
+    c = filled(pages, page, Hkv, d, g)
+    table = torch.randint(0, pages, (B, per), generator=g, device="cuda").int()
+    length = i32([page * per - 100 * b for b in range(B - 1)] + [n // 2])
+    q = normal(g, B, n, Hq, d)
+    c.v_scale.copy_(torch.randint(27, 228, c.v_scale.shape, generator=g, device="cuda"))
+    empty = torch.rand(c.v_scale.shape, generator=g, device="cuda") < 0.1
+    c.v_scale[empty] = 0
+    c.v.view(*c.v_scale.shape, 32)[empty] = 0
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+    out = a.forward(q, c, table, length)
+    assert same(a.forward(q, c, table, length), out)
+    for b in (0, 11, B - 1):
+        for i in {0, n // 2, n - 1}:                 # a row as if it were alone
+            at = slice(b, b + 1), slice(i, i + 1)
+            few = out[0][at], out[1][at[0], :, at[1]]
+            check_far(few, q[at], c, table[at[0]], (length[at[0]] - n + 1 + i).clamp(min=0), True,
+                      0, 0, d ** -0.5)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR)
+@pytest.mark.parametrize("kind", ["code", "scale"])
+def test_nan_beside_values_far_apart(n, Hq, Hkv, d, kind):
+    """A key with NaN in V among others whose values lie 2^60 apart: NaN for the rows that
+    read it, in its features; the others as without it."""
+    B, page, per = 2, 16, 20
+    lens = [300, 130]
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 55, lens)
+    for b in range(B):
+        for j, by in ((lens[b] - n, 60), (lens[b] - n - 2, 30), (lens[b] - n - 5, 90), (3, 70)):
+            c.v_scale[int(table[b, j // page]), j % page, :, ::2] += by
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+    clean = [x.clone() for x in a.forward(q, c, table, length)]
+    bad = torch.zeros(clean[0].shape, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        j = lens[b] - n + n // 2
+        at = int(table[b, j // page]), j % page
+        if kind == "code":
+            c.v[at][:, 5] = 0x7f
+            bad[b, n // 2:, :, 5] = True
+        else:
+            c.v_scale[at][:, 0] = 255
+            bad[b, n // 2:, :, :32] = True
+    o, lse = a.forward(q, c, table, length)
+    assert torch.equal(lse, clean[1]) or kind == "scale"
+    assert torch.equal(o.isnan(), bad)
+    if kind == "code":
+        assert torch.equal(torch.where(bad, 0, o), torch.where(bad, 0, clean[0]))
+    i = n // 2
+    check_far((o[:, :i].contiguous(), lse[:, :, :i].contiguous()), q[:, :i], c, table,
+              length - n + i, True, 0, 0, d ** -0.5)
+
+
 def test_queries_far_apart():
     """Rows of very large and very small queries."""
     B, n, per, page, Hq, Hkv, d = 1, 8, 4, 16, 4, 2, 128
