@@ -1011,21 +1011,185 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
   if (kFused) join_pieces<D, L::kRows>(p, cut);
 }
 
-// Joins the pieces where a launch does not do so itself; a CTA per head and 8 rows.
+// Two E4M3 codes of a word's low or high half as fp32.
+__device__ __forceinline__ float2 two_codes(uint32_t f16x2) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
+}
+
+// Rows from .. from + rows of a whole tile in fp32, from the keys themselves: where scales
+// lie too far apart for f16 operands, in K among the keys of a tile or in V.  Two rows to
+// each of 4 warps; a lane takes a key's scores, then D / 32 features of O.  (Rare, and not
+// made for speed: 16 sequences of 16,384 keys and 160 rows for each of 8 heads of 128, all
+// of them so, take 27 ms.)
+constexpr int kExactRows = 8;
 template <int D>
-__global__ void __launch_bounds__(128)
+__device__ __noinline__ void exact_rows(const PagedParams& p, int entry, int head, int from,
+                                        int rows) {
+  __shared__ float queries[kExactRows][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
+  const Range r = range_of(p, b, tile, kPairRows);
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_pages;
+  const bool has[2] = {2 * warp < rows, 2 * warp + 1 < rows};
+  float row_scale[2];
+  int lo[2], hi[2], token[2], h[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int row = tile * kPairRows + from + min(2 * warp + x, rows - 1);
+    token[x] = p.by_G(row);
+    h[x] = head * p.G + row - token[x] * p.G;
+    const int at = r.c - p.queries + token[x];
+    hi[x] = p.causal ? at + 1 : r.c;
+    lo[x] = window_begin(p, at);
+    // the largest element becomes 1 .. 2, so that no product passes fp32's range before the
+    // scales are in it
+    const __nv_bfloat16* q =
+        p.q + b * p.q_bat + token[x] * p.q_tok + static_cast<int64_t>(h[x]) * D;
+    float most = 0.f;
+    for (int c = lane; c < D; c += 32) most = fmaxf(most, fabsf(__bfloat162float(q[c])));
+    const int ex = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 127, -110);
+    const float scale = ldexpf(1.f, -ex);
+    for (int c = lane; c < D; c += 32) queries[2 * warp + x][c] = __bfloat162float(q[c]) * scale;
+    row_scale[x] = fmaxf(p.scale_log2 * ldexpf(1.f, ex), 1e-44f);
+  }
+  __syncwarp();
+  // sums of 32 x 32 keys and of all before them, so that no sum takes in very many terms; O
+  // in units of 2^-24, so that a sum of the largest values does not pass fp32's range
+  constexpr int F = D / 32;
+  float m[2] = {-INFINITY, -INFINITY}, l[2][2] = {}, o[2][2][F] = {};
+#pragma unroll 1
+  for (int i0 = 0; i0 < r.keys(); i0 += 32) {
+    // ------- a key per lane
+    const int i = i0 + lane, j = i < r.keys() ? r.key(i) : 0, page_at = p.by_page(j);
+    const int page = i < r.keys() ? __ldg(table + page_at) : -1;
+    const bool there = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+    const uint32_t place =
+        there ? static_cast<uint32_t>(page * p.page_size + j - page_at * p.page_size) * p.Hkv + head
+              : 0;
+    float s[2] = {0.f, 0.f};
+    if (there) {
+#pragma unroll 1
+      for (int e = 0; e < F; ++e) {
+        const uint4* codes = reinterpret_cast<const uint4*>(p.k + static_cast<uint64_t>(place) * D) + 2 * e;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const uint4 w = __ldg(codes + k);
+          const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+          const float* q = &queries[2 * warp][32 * e + 16 * k];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 a = two_codes(f16_low(word[y])), c = two_codes(f16_high(word[y]));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float4 f = *reinterpret_cast<const float4*>(q + x * D + 4 * y);
+              sum[x] = fmaf(a.x, f.x, fmaf(a.y, f.y, fmaf(c.x, f.z, fmaf(c.y, f.w, sum[x]))));
+            }
+          }
+        }
+        const int byte = __ldg(p.k_scale + static_cast<uint64_t>(place) * F + e);
+        const float scale = byte == 255 ? NAN : ldexpf(1.f, byte - 127);
+        s[0] = fmaf(sum[0], scale, s[0]);
+        s[1] = fmaf(sum[1], scale, s[1]);
+      }
+    }
+    uint32_t reads[2];
+    float w[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const bool read = has[x] && there && j < hi[x] && (j >= lo[x] || j < p.sinks);
+      reads[x] = __ballot_sync(0xffffffffu, read);
+      s[x] = read ? s[x] * row_scale[x] : -INFINITY;
+      float most = s[x];
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      most = fmaxf(most, m[x]);
+      const float ref = most == -INFINITY ? 0.f : most, old = exp2f(m[x] - ref);
+      m[x] = most;
+      w[x] = exp2f(s[x] - ref);
+      const bool full = (i0 & 1023) == 0;  // 32 x 32 keys are in the first sum
+      l[x][1] = (l[x][1] + (full ? l[x][0] : 0.f)) * old;
+      l[x][0] = fmaf(full ? 0.f : l[x][0], old, w[x]);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        o[x][1][f] = (o[x][1][f] + (full ? o[x][0][f] : 0.f)) * old;
+        o[x][0][f] = full ? 0.f : o[x][0][f] * old;
+      }
+    }
+    // ------- F features per lane
+    for (uint32_t any = reads[0] | reads[1]; any; any &= any - 1) {
+      const int k = __ffs(any) - 1;
+      const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, place, k));
+      const float w0 = __shfl_sync(0xffffffffu, w[0], k), w1 = __shfl_sync(0xffffffffu, w[1], k);
+      const int byte = __ldg(p.v_scale + at * F + lane * F / 32);
+      const float scale = byte == 255 ? NAN : ldexpf(1.f, byte - 127 - 24);
+      float v[F];
+      if constexpr (F == 4) {
+        const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(p.v + at * D) + lane);
+        const float2 a = two_codes(f16_low(word)), c = two_codes(f16_high(word));
+        v[0] = a.x;
+        v[1] = a.y;
+        v[2] = c.x;
+        v[3] = c.y;
+      } else {
+        const uint32_t word = __ldg(reinterpret_cast<const uint16_t*>(p.v + at * D) + lane);
+        const float2 a = two_codes(f16_low(word));
+        v[0] = a.x;
+        v[1] = a.y;
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        v[f] *= scale;
+        if (reads[0] >> k & 1) o[0][0][f] = fmaf(w0, v[f], o[0][0][f]);
+        if (reads[1] >> k & 1) o[1][0][f] = fmaf(w1, v[f], o[1][0][f]);
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    float sum = l[x][0] + l[x][1];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (!has[x]) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float y[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) y[f] = (o[x][0][f] + o[x][1][f]) * inv * 0x1p24f;
+    const int64_t at = (static_cast<int64_t>(b) * p.queries + token[x]) * p.Hq + h[x];
+    uint32_t* to = reinterpret_cast<uint32_t*>(p.o + at * D) + lane * (F / 2);
+#pragma unroll
+    for (int f = 0; f < F; f += 2) to[f / 2] = pack_bf16x2(y[f], y[f + 1]);
+    if (lane == 0)
+      p.lse[(static_cast<int64_t>(b) * p.Hq + h[x]) * p.queries + token[x]] =
+          sum == 0.f ? -INFINITY : (m[x] + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// Joins the pieces where a launch does not do so itself; a CTA per head and 8 rows.  (In 48
+// registers, so that 20,480 CTAs that find nothing to do take 18 us, not 20.)
+template <int D>
+__global__ void __launch_bounds__(128, 10)
     paged_join_kernel(const __grid_constant__ PagedParams p, int tile_rows) {
   constexpr int kLanes = D / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int item = blockIdx.x, chunks = tile_rows / 8;
   const int head_in = blockIdx.y / chunks, from = (blockIdx.y - head_in * chunks) * 8;
   const int2 piece = p.pieces[item];
-  if (piece.y <= 1) return;
+  if (piece.y == 1 || piece.y == 0) return;
   const int entry = item / p.head_blocks, block = item - entry * p.head_blocks;
   const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
   const int head = block * p.heads + head_in;
   const int rows = min(8, p.queries * p.G - tile * tile_rows - from);
   if (rows <= 0 || head >= p.Hkv) return;
+  if (tile_rows == kPairRows) {
+    bool far = piece.y < 0;
+    for (int k = threadIdx.x; k < piece.y; k += blockDim.x)
+      far |= p.far[2 * (piece.x + k * p.lanes) + (k == 0)] != 0;
+    if (__syncthreads_or(far)) {
+      exact_rows<D>(p, entry, head, from, rows);
+      return;
+    }
+  }
   constexpr int U = 8 * kLanes / 128;
   const int64_t size = static_cast<int64_t>(p.heads) * tile_rows;  // of a piece
   int64_t at[U];
@@ -1108,7 +1272,7 @@ bool device_sms(int& sms) {
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Places {
-  size_t part_z, aside_o, aside_z, pieces, bytes;
+  size_t part_z, aside_o, aside_z, far, pieces, bytes;
 };
 Places places(const Cut& cut, int d, int sms) {
   const size_t rows = static_cast<size_t>(2) * sms * cut.heads * cut.tile_rows;
@@ -1117,7 +1281,8 @@ Places places(const Cut& cut, int d, int sms) {
   const size_t sums = static_cast<size_t>(sms) * cut.heads * cut.slices * cut.tile_rows;
   r.aside_o = r.part_z + round256(rows * 4);
   r.aside_z = r.aside_o + round256(sums * d * 4);
-  r.pieces = r.aside_z + round256(sums * 4);
+  r.far = r.aside_z + round256(sums * 4);
+  r.pieces = r.far + round256(cut.tiles ? static_cast<size_t>(2) * sms * sizeof(int) : 0);
   r.bytes = r.pieces + round256(static_cast<size_t>(cut.items) * sizeof(int2));
   return r;
 }
@@ -1244,6 +1409,7 @@ extern "C" csbp_status csbp_attn_paged(const csbp_paged_problem* problem,
   a.part_z = reinterpret_cast<float*>(ws + at.part_z);
   a.aside_o = reinterpret_cast<float*>(ws + at.aside_o);
   a.aside_z = reinterpret_cast<float*>(ws + at.aside_z);
+  a.far = reinterpret_cast<int*>(ws + at.far);
   a.pieces = reinterpret_cast<int2*>(ws + at.pieces);
   a.arrived = reinterpret_cast<int*>(ws + at.pieces);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -12,11 +12,13 @@
 //
 // Operands.  K, V and Q are f16 in shared memory, P f16 in TMEM, all under powers of
 // two that fp32 takes back: E4M3 codes are exact in f16, and so are their group
-// scales 2^(e - E) down to 2^-24, with E the largest scale byte of the K tile, and of
+// scales 2^(e - E) to 2^-22, with E the largest scale byte of the K tile, and of
 // V twice the largest so far in the feature group (O is rescaled when one grows past
-// that, and when the maximum of a row has grown by 2^5.9).  An
-// operand below 2^-31 of the largest beside it becomes 0.  P is p 2^10, rounded to
-// 2^-11 of itself (2^-35 of the row's largest at least).
+// that, and when the maximum of a row has grown by 2^5.9).  P is p 2^10, rounded to
+// 2^-11 of itself (2^-35 of the row's largest at least).  Where scales lie farther apart
+// (a value 2^22 times the largest of another group of 32) the small ones would be lost, in
+// rows that do not read the large one too: such an item is worked out again in fp32, by the
+// kernel that joins the pieces.
 //
 // Keys.  One warp looks the pages up and starts the copies of K's codes and the scale
 // bytes into a ring of three half tiles, another those of V's (cp.async: one bulk copy
@@ -92,7 +94,8 @@ struct Tiles {
   static constexpr int kBars = bFree + kHalves;
   static constexpr int kMisc = kBar + kBars * 8;    // TMEM base, abort flag
   static constexpr int kRedo = kMisc + 8;           // [kInfos] by item
-  static constexpr int kCursor = (kRedo + kInfos * 4 + 15) / 16 * 16;  // of each softmax warp
+  static constexpr int kFar = kRedo + kInfos * 4;   // [kInfos] by item
+  static constexpr int kCursor = (kFar + kInfos * 4 + 15) / 16 * 16;  // of each softmax warp
   static constexpr int kScale = kCursor + 8 * 48;  // [2 slots][row] of Q
   static constexpr int kJoin = kScale + 2 * kTile * 4;  // [row] of an alternate piece's slot 1
   static constexpr int kSmem = kJoin + kTile * 16;
@@ -238,9 +241,12 @@ __device__ __forceinline__ Cursor kept_cursor(uint32_t at) {
   return c;
 }
 
-// 2^(kHeadroom - delta) in f16, both halves; 0 below 2^-24, NaN for a byte of 255.
-__device__ __forceinline__ uint32_t operand_scale(int top, int byte) {
+// 2^(kHeadroom - delta) in f16, both halves; 0 below 2^-24, NaN for a byte of 255.  Where
+// it takes E4M3's last bit below 2^-24 a 1 goes to `far` in shared memory (a byte of 0,
+// below 2^-118, aside).
+__device__ __noinline__ uint32_t operand_scale(int top, int byte, uint32_t far) {
   const int delta = top - byte;
+  if (delta > kHeadroom + 15 && byte != 0 && byte != 255) sts32(far, 1);
   const uint32_t h = byte == 255 ? 0x7fffu
                      : delta <= kHeadroom + 14 ? static_cast<uint32_t>(kHeadroom + 15 - delta) << 10
                      : delta <= kHeadroom + 24 ? 1u << (kHeadroom + 24 - delta)
@@ -438,12 +444,22 @@ struct Copier {
       k = max(max(k & 255, k >> 8 & 255), max(k >> 16 & 255, k >> 24));
       k = __reduce_max_sync(0xffffffffu, k);
       // (twice as much as now, so that a little growth does not rescale O)
-      if (begins || __vmaxu4(top, v) != top) top = __vmaxu4(begins ? 0 : top, __vaddus4(v, 0x01010101u));
+      bool far = false;
+      if (begins) {
+        top = __vaddus4(v, 0x01010101u);
+      } else if (__vmaxu4(top, v) != top) {
+        const uint32_t old = top;
+        top = __vmaxu4(top, __vaddus4(v, 0x01010101u));
+        // O follows E by 2^64 (or from a byte of 1, that of zeros: then it is nothing)
+        far = at_least_u8x4((top - old) & ~__vcmpleu4(old, 0x01010101u), 0x41414141u) != 0;
+      }
       if (lane == 0) {
         info.k_factor = ldexpf(1.f, static_cast<int>(k) - 127 - kHeadroom);
         info.k_top = k;
         info.top = top;
         if (begins) reinterpret_cast<volatile int*>(smem + L::kRedo)[info.item % kInfos] = 0;
+        if (begins || far)
+          reinterpret_cast<volatile int*>(smem + L::kFar)[info.item % kInfos] = far;
         mbar_arrive(&bars[L::bInfo + (t & 1)]);
       }
       __syncwarp();
@@ -468,7 +484,7 @@ struct Converter {
   // kEdge: NaN is written as 0; whether there was any.
   template <bool kEdge>
   __device__ __forceinline__ bool convert(uint32_t from, uint32_t bytes, uint32_t top,
-                                          uint32_t tile) const {
+                                          uint32_t tile, uint32_t far) const {
     // 4 rows of 8 pieces of 16 codes (D = 64: 8 of 4) at a time, so that 8 lanes read
     // and write different banks
     constexpr int kAtOnce = D == 128 ? 4 : 8;
@@ -510,7 +526,7 @@ struct Converter {
         // 2^(headroom - (E - e)) in f16, the normal ones at once
         const int field = kHeadroom + 15 - e + static_cast<int>(byte[x]);
         uint32_t s = static_cast<uint32_t>(field) * 0x04000400u;
-        if (field <= 0 || byte[x] == 255) s = operand_scale(e, static_cast<int>(byte[x]));
+        if (field <= 0 || byte[x] == 255) s = operand_scale(e, static_cast<int>(byte[x]), far);
         const uint32_t to = tile + sw128_offset(r, 2 * (c & 3));
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to),
                      "r"(mul_f16x2(f16_low(w[x][0]), s)), "r"(mul_f16x2(f16_high(w[x][0]), s)),
@@ -545,11 +561,12 @@ struct Converter {
                              (D == 64 && info.upper ? 2 : 0);
       const uint32_t top = kv ? info.top : info.k_top * 0x01010101u;
       const uint32_t tile = mem + (kv ? L::kV + (t & 1) * L::kTileBytes : info.k_at);
+      const uint32_t far = mem + L::kFar + info.item % kInfos * 4;
       if (kv && info.edge) {
-        if (convert<true>(from, bytes, top, tile))
+        if (convert<true>(from, bytes, top, tile, far))
           reinterpret_cast<volatile int*>(smem + L::kRedo)[info.item % kInfos] = 1;
       } else {
-        convert<false>(from, bytes, top, tile);
+        convert<false>(from, bytes, top, tile, far);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1160,10 +1177,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowAt a = row_at(p, x, cur.r.c, (x.alternate ? 0 : s * kTile) + row);
       const int later = x.n - x.k0 - x.count;  // steps of the item in later shares
       const bool starts = x.k0 == 0;
-      if (starts && threadIdx.x == 256)
-        p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
-            make_int2(static_cast<int>(blockIdx.x),
-                      1 + static_cast<int>((later + share.per - 1) / share.per));
       const int part =
           starts && later == 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
       Join* const other = reinterpret_cast<Join*>(smem + L::kJoin);
@@ -1177,6 +1190,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // (known when the last V is in its tile: both slots' last P V are done by now)
       const bool redo = reinterpret_cast<volatile int*>(smem + L::kRedo)[item % kInfos] != 0;
+      if (threadIdx.x == 256) {
+        const int far = reinterpret_cast<volatile int*>(smem + L::kFar)[item % kInfos];
+        if (part >= 0) p.far[part] = far;
+        if (starts)
+          p.pieces[static_cast<int64_t>(cur.entry) * p.head_blocks + cur.block] =
+              make_int2(static_cast<int>(blockIdx.x),
+                        part < 0 && far ? -1
+                                        : 1 + static_cast<int>((later + share.per - 1) / share.per));
+      }
       if (ok && has_rows && !(x.alternate && s == 1))
         store_sum<D>(p, x, cur.r, a, sum, o_at, s, row, part, redo, q_tile,
                      x.alternate ? other : nullptr);

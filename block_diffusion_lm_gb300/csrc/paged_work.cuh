@@ -33,12 +33,16 @@ struct PagedParams {
   Divisor by_page, by_G, by_row_tiles, by_lanes, by_step;  // (step_keys)
   float* part_o;  // [2 x CTAs][heads][tile rows][d]
   float* part_z;  // [2 x CTAs][heads][tile rows]
-  int2* pieces;   // per sequence, row tile and head block: first CTA, number of them
+  int2* pieces;   // per sequence, row tile and head block: first CTA, number of them (-1:
+                  // one whole tile, `far`)
   int* arrived;   // in their place where the CTAs join them: how many are there, 0
                   // between launches
   // sums put aside: [CTAs x warps][tile rows][d], or [CTAs][tile rows][d] where a CTA
   // works on whole tiles, and their LSE
   float *aside_o, *aside_z;
+  // of whole tiles, per partial: scales lie too far apart for f16 operands, the rows are
+  // worked out again where the pieces are joined
+  int* far;  // [2 x CTAs]
   int* status;
 };
 

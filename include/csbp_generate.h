@@ -176,11 +176,12 @@ size_t csbp_paged_workspace_bytes(const csbp_paged_problem* problem, const csbp_
  * of the same problem, and calls that can overlap need workspaces of their own.
  *  o    bf16 [batch][queries][Hq][d];  lse  fp32 [batch][Hq][queries]
  * Operands are held with 8 (q) and 4 (k, v) bits of significand under powers of
- * two (an element of q below 2^-24 of its row's largest: to 2^-32 of that; values of v
- * in groups with the scale byte 0, below 2^-118, may count as 0), weights with 11
- * bits and to 2^-25 of a row's largest.  With more than 48 query rows per KV head and
- * sequence, a value below 2^-31 of the largest scale beside it counts as 0 (k: among
- * 128 keys; v: in its group of features among the keys read so far).
+ * two (an element of q below 2^-24 of its row's largest: to 2^-32 of that; values in
+ * groups with the scale byte 0, below 2^-118, may count as 0), weights with 11 bits and
+ * to 2^-25 of a row's largest.  Scales far apart take longer: of v by more than 2^14
+ * among 32 keys a pass for each of them, and with more than 48 query rows per KV head
+ * and sequence, by more than 2^21 (of k among 128 keys, of v in a group of features), up
+ * to a hundred times as long for the 256 rows and the head concerned.
  * CSBP_ERR_UNSUPPORTED: another d; tokens x heads, keys or steps past 31 bits.  */
 csbp_status csbp_attn_paged(const csbp_paged_problem* problem, const csbp_kv_cache* cache,
                             const csbp_paged_inputs* in, void* o, float* lse, void* workspace,

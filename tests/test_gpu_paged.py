@@ -764,6 +764,129 @@ def test_nan_beside_values_far_apart(n, Hq, Hkv, d, kind):
               length - n + i, True, 0, 0, d ** -0.5)
 
 
+# more rows: 64, 160 and 256 + 44 per KV head
+FAR_TILES = [(32, 4, 2, 64), (40, 8, 2, 128), (100, 6, 2, 64)]
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR_TILES)
+@pytest.mark.parametrize("name,by", [("v", 16), ("v", 40), ("v", 124), ("k", 30), ("k", 100)])
+def test_large_keys_and_values_that_are_not_read_by_many_rows(n, Hq, Hkv, d, name, by):
+    """K or V of a key, 2^16 to 2^124 times the others', has no part in the rows that do
+    not read it."""
+    B, page, per = 3, 16, 30
+    lens = [470, n - 3, 257]
+    for causal, window, back in ((True, 0, 0), (True, 0, n // 2), (True, 60, 59 + n // 2),
+                                 (False, 60, 59 + n // 2)):
+        c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 56, lens)
+        rows = np.ones((B, n), bool)             # those that do not read it
+        for b in range(B):
+            j, t = lens[b] - 1 - back, lens[b] - n + np.arange(n)
+            if j >= 0:
+                getattr(c, name + "_scale")[int(table[b, j // page]), j % page, :, b % (d // 32)] += by
+                rows[b] = ((j > t) & causal) | ((t - j >= window) & bool(window))
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window)
+        o, lse = a.forward(q, c, table, length)
+        a.check()
+        if name == "v":
+            check_far((o, lse), q, c, table, length, causal, window, 0, d ** -0.5)
+            continue
+        # (a row that reads it has a score of 2^30 and more: all the others are nothing)
+        k, v = values(c)
+        want, z, A, T = O.paged_attention(f64(q), k, v, table.cpu().numpy(), lens, page, causal,
+                                          window, 0, d ** -0.5)
+        tol = ((2.0 ** -8 + 2.0 ** -12 + 4 * d * 2.0 ** -24 * T.transpose(0, 2, 1)[..., None]) * A
+               + 2.0 ** -8 * np.abs(want))
+        assert rows.any() and (np.abs(f64(o) - want)[rows] <= tol[rows]).all()
+        z, T, got = (x.transpose(0, 2, 1)[rows] for x in (z, T, f64(lse)))
+        none = z == -np.inf
+        np.testing.assert_array_equal(got == -np.inf, none)
+        tol = 2 * d * 2.0 ** -24 * T[~none] + 2.0 ** -15
+        assert (np.abs(got[~none] - z[~none]) <= tol).all()
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR_TILES + FAR[1:4])
+def test_large_keys_that_queries_are_zero_for(n, Hq, Hkv, d):
+    """K of a key, 2^60 times the others', in a feature where all queries are 0: its score
+    is 0, the others' are theirs."""
+    B, page, per = 2, 16, 30
+    lens = [470, 300]
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 57, lens)
+    q[..., 7] = 0
+    for b in range(B):
+        for j in (100, lens[b] - n):
+            at = int(table[b, j // page]), j % page
+            c.k[at][:, :32] = 0
+            c.k[at][:, 7] = 0x7e
+            c.k_scale[at][:, 0] = 127 + 50
+    for causal in (True, False):
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal)
+        check_far(a.forward(q, c, table, length), q, c, table, length, causal, 0, 0, d ** -0.5)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR_TILES)
+@pytest.mark.parametrize("by", [30, 100])
+def test_large_values_of_next_to_no_weight_for_many_rows(n, Hq, Hkv, d, by):
+    """As for few rows; in a text that is cut among CTAs, in one piece of it."""
+    B, page, per = 2, 64, 40
+    lens = [2500, 130]
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 58, lens)
+    q[..., 3] = 8
+    for b in range(B):
+        j = lens[b] * 2 // 3
+        at = int(table[b, j // page]), j % page
+        c.k[at][:] = 0
+        c.k[at][:, 3] = 0xfe
+        c.k_scale[at][:, 0] = 127 - 6
+        c.v_scale[at][:, 1] += by
+    for causal in (True, False):
+        a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, scale=1.0)
+        check_far(a.forward(q, c, table, length), q, c, table, length, causal, 0, 0, 1.0)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR_TILES)
+def test_scales_far_apart_and_near_again(n, Hq, Hkv, d):
+    """V's and K's scales anywhere, groups of zeros and NaN among them, for some sequences
+    of a call and not for others; the next call on the same handle finds them near."""
+    B, page, per = 6, 64, 20
+    lens = [1280, 1000, 64, 700, 1279, 0]
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 59, lens)
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+    want = [x.clone() for x in a.forward(q, c, table, length)]
+    old = stored(c)
+    g = gen(60)
+    for b in (0, 3, 4):
+        pages = table[b].long()
+        for name, lo, hi in (("k_scale", 100, 123), ("v_scale", 27, 228)):
+            t = getattr(c, name)
+            t[pages] = torch.randint(lo, hi, t[pages].shape, generator=g, device="cuda").byte()
+        empty = torch.rand(c.v_scale[pages].shape, generator=g, device="cuda") < 0.1
+        c.v_scale[pages] = torch.where(empty, 0, c.v_scale[pages])
+        codes = c.v[pages].view(*empty.shape, 32)
+        c.v[pages] = torch.where(empty[..., None], 0, codes).view(c.v[pages].shape)
+    o, lse = a.forward(q, c, table, length)
+    assert same(a.forward(q, c, table, length), (o, lse))
+    near = [1, 2, 5]
+    assert same((o[near], lse[near]), (want[0][near], want[1][near]))
+    for b in (0, 3, 4):
+        for i in (0, n // 2, n - 1):
+            at = slice(b, b + 1), slice(i, i + 1)
+            check_far((o[at], lse[at[0], :, at[1]]), q[at], c, table[at[0]],
+                      length[at[0]] - n + 1 + i, True, 0, 0, d ** -0.5)
+    # NaN beside them
+    clean = [o.clone(), lse.clone()]
+    bad = torch.zeros(o.shape, dtype=torch.bool, device="cuda")
+    for b in (0, 1, 3, 4):
+        j = lens[b] - n // 2
+        c.v[int(table[b, j // page]), j % page, :, 9] = 0xff
+        bad[b, n - n // 2:, :, 9] = True
+    o, lse = a.forward(q, c, table, length)
+    assert torch.equal(lse, clean[1]) and torch.equal(o.isnan(), bad)
+    assert torch.equal(torch.where(bad, 0, o), torch.where(bad, 0, clean[0]))
+    for t, x in zip((c.k, c.v, c.k_scale, c.v_scale), old):
+        t.copy_(x)
+    assert same(a.forward(q, c, table, length), want)
+
+
 def test_queries_far_apart():
     """Rows of very large and very small queries."""
     B, n, per, page, Hq, Hkv, d = 1, 8, 4, 16, 4, 2, 128
