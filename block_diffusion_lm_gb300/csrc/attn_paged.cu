@@ -956,6 +956,7 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
                    : "r"(k.mem + stage * L::kStage + L::kRecord + 16)
                    : "memory");
       if (r.left) {
+        __syncwarp();  // (all lanes have read the record)
         if (k.lane == 0) sts32(k.mem + stage * L::kStage + L::kRecord + 28, 0);
       } else if (i == 0 || r.step == 0) {
         k.begin(r);
