@@ -146,7 +146,8 @@ csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_cache_rows*
  * A key whose page is outside [0, pages) is not read.  O = softmax(scale Q K^T) V
  * and LSE as in csbp_attn_prefix (whose results they can be merged with); a
  * query that reads no key has O = 0, LSE = -inf, and a key that a query does not
- * read has no part in its result, whatever it holds.                       */
+ * read has no part in its result, whatever it holds (its scale can decide how a
+ * weight below 2^-10 of the row's largest is rounded).                     */
 typedef struct {
   int32_t batch, queries;  /* >= 1                                          */
   int32_t table_pages;     /* >= 1; x page_size below 2^31 - 1024           */
@@ -178,10 +179,11 @@ size_t csbp_paged_workspace_bytes(const csbp_paged_problem* problem, const csbp_
  * Operands are held with 8 (q) and 4 (k, v) bits of significand under powers of
  * two (an element of q below 2^-24 of its row's largest: to 2^-32 of that; values in
  * groups with the scale byte 0, below 2^-118, may count as 0), weights with 11 bits and
- * to 2^-25 of a row's largest.  Scales far apart take longer: of v by more than 2^14
- * among 32 keys a pass for each of them, and with more than 48 query rows per KV head
- * and sequence, by more than 2^21 (of k among 128 keys, of v in a group of features), up
- * to a hundred times as long for the 256 rows and the head concerned.
+ * to 2^-25 of a row's largest.  Scores are fp32: keys of 2^100 and more may take them
+ * past its range, whatever the queries are.  Scales far apart take longer: of v by more
+ * than 2^14 among 32 keys, a pass for each of them; with more than 48 query rows per KV
+ * head and sequence, by more than 2^21 (of k among 128 keys, of v in a group of
+ * features), up to a hundred times as long for the 256 rows and the head concerned.
  * CSBP_ERR_UNSUPPORTED: another d; tokens x heads, keys or steps past 31 bits.  */
 csbp_status csbp_attn_paged(const csbp_paged_problem* problem, const csbp_kv_cache* cache,
                             const csbp_paged_inputs* in, void* o, float* lse, void* workspace,

@@ -887,6 +887,44 @@ def test_scales_far_apart_and_near_again(n, Hq, Hkv, d):
     assert same(a.forward(q, c, table, length), want)
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,d", [(1, 4, 1, 64), (1, 8, 8, 128), (3, 8, 2, 128), (24, 4, 2, 64),
+                                        (32, 4, 2, 128), (110, 4, 2, 64)])
+def test_weights_have_eleven_bits(n, Hq, Hkv, d):
+    """V of one sign in half the features, of both in the others, where O is small beside
+    A = sum p |v|: P as f16 costs 2^-11 A, the exponential, the sums and weights below f16's
+    normal range (2^-25 of a row's largest) 2^-13 A more, and O's own rounding 2^-8 of it."""
+    B, page, per = 3, 16, 40
+    lens = [640, 37, 333]
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 62, lens)
+    c.v[..., ::2] &= 0x7f
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=True)
+    o, lse = a.forward(q, c, table, length)
+    k, v = values(c)
+    want, _, A, T = O.paged_attention(f64(q), k, v, table.cpu().numpy(), lens, page, True, 0, 0,
+                                      d ** -0.5)
+    tol = ((2.0 ** -11 + 2.0 ** -13 + 4 * d * 2.0 ** -24 * T.transpose(0, 2, 1)[..., None]) * A
+           + 2.0 ** -8 * np.abs(want))
+    assert (np.abs(f64(o) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("n", [1, 3, 12, 40])
+def test_values_far_apart_under_scale_bytes_anywhere(n):
+    """Scale bytes that are not loaded in words: at odd addresses, or of 3 heads of 64."""
+    for Hkv, d in ((4, 128), (3, 64)):
+        c, q, table, length = attn_case(3, n, 20, 16, 2 * Hkv, Hkv, d, 63, [320, 33, 200])
+        g = gen(64)
+        c.v_scale.copy_(torch.randint(60, 190, c.v_scale.shape, generator=g, device="cuda"))
+        a = csbp.PagedAttention(3, n, 20, 16, 2 * Hkv, Hkv, d, causal=True)
+        want = [x.clone() for x in a.forward(q, c, table, length)]
+        check_far(want, q, c, table, length, True, 0, 0, d ** -0.5)
+        room = [torch.zeros(t.numel() + 8, dtype=torch.uint8, device="cuda")
+                for t in (c.k_scale, c.v_scale)]
+        views = [r[x:x + t.numel()].view(t.shape).copy_(t)
+                 for r, t, x in zip(room, (c.k_scale, c.v_scale), (1, 3))]
+        odd = csbp.QuantCache(*c.k.shape, storage=(c.k, c.v, *views))
+        assert same(a.forward(q, odd, table, length), want)
+
+
 def test_queries_far_apart():
     """Rows of very large and very small queries."""
     B, n, per, page, Hq, Hkv, d = 1, 8, 4, 16, 4, 2, 128
