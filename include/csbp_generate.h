@@ -146,8 +146,9 @@ csbp_status csbp_cache_append(const csbp_kv_cache* cache, const csbp_cache_rows*
  * A key whose page is outside [0, pages) is not read.  O = softmax(scale Q K^T) V
  * and LSE as in csbp_attn_prefix (whose results they can be merged with); a
  * query that reads no key has O = 0, LSE = -inf, and a key that a query does not
- * read has no part in its result, whatever it holds (its scale can decide how a
- * weight below 2^-10 of the row's largest is rounded).                     */
+ * read has no part in its result, whatever it holds (but for last bits: scales
+ * decide how weights below 2^-14 of a row's largest are rounded, and far ones
+ * where its sum is cut).                                                   */
 typedef struct {
   int32_t batch, queries;  /* >= 1                                          */
   int32_t table_pages;     /* >= 1; x page_size below 2^31 - 1024           */
