@@ -143,8 +143,9 @@ struct Rows {
   static constexpr int kWords = 2 * kCodes;
   static constexpr int kRecord = kWords + 2 * kKeys * 4;
   static constexpr int kStage = kRecord + 128;
-  // the step's scales: fp32 of K [key][group], f16 of V [group][key]
+  // the step's scales: fp32 of K [key][group], f16 of V [group][key]; the sum's first E
   static constexpr int kScales = kStages * kStage;
+  static constexpr int kFirstTop = kScales + kKeys * kGroups * 6;
   // and when an item ends, in their place, 4 rows of the result [row][D + 4] and their
   // LSE (log2)
   static constexpr int kSum = kScales;
@@ -152,7 +153,7 @@ struct Rows {
   static constexpr int kSumZ = kSum + 4 * kSumRow * 4;
   static constexpr int kWarpBytes = (kSumZ + 16 + 127) / 128 * 128;
   static_assert((kMostWarps * 4 + sizeof(Cursor)) <= 192, "find_share beside Pieces");
-  static_assert(kScales + kKeys * kGroups * 6 <= kSumZ, "shared memory of a warp");
+  static_assert(kFirstTop + 4 <= kSumZ, "shared memory of a warp");
   static constexpr int kPieces = 192;
   static constexpr int kRoom = 256;  // find_share and Pieces, in front
   static constexpr int smem(int warps) { return kRoom + warps * kWarpBytes; }
@@ -324,6 +325,7 @@ struct Kernel {
       m[x] = -3e38f;
     }
     top = 0;
+    if (lane == 0) sts32(mem + L::kFirstTop, 0);
   }
 
   // Rows of a tile: queries to registers, and what each row reads.
@@ -383,8 +385,8 @@ struct Kernel {
   // summed under the old one is scaled, and `delta` is E - e, or 15 where a scale is that far
   // below because its byte is 0 (what is below 2^-118 counts as 0 there) or NaN.
   //
-  // Where the scales do not lie within 2^14 of E, or E has risen by more than a sum in fp32
-  // can follow, the sum so far is to be put aside first: all of `there` is left for then.
+  // Where the scales do not lie within 2^14 of E, or E has risen since the sum's begin by more
+  // than fp32 can follow, the sum so far is to be put aside first: all of `there` is left for then.
   // Where they do not lie within 2^14 of one another, `there` becomes those of the first key
   // and the ones near it in each group.  Returns what is left.  (`fresh`: nothing has been
   // summed yet.)
@@ -410,12 +412,15 @@ struct Kernel {
       left |= there & ~part;
       there = part;
     }
+    uint32_t first = lds32(mem + L::kFirstTop);
+    first |= now & __vcmpeq4(first, 0);
+    if (at_least_u8x4(now - first, 0x41414141u)) return there;  // (nothing is borrowed)
+    __syncwarp();
+    if (lane == 0) sts32(mem + L::kFirstTop, first);
     if (!fresh) {
-      const uint32_t rise = now - top;  // byte by byte, nothing is borrowed
-      if (at_least_u8x4(rise & ~__vcmpeq4(top, 0), 0x41414141u)) return there;
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
-        const uint32_t by = rise >> 8 * e & 255;
+        const uint32_t by = (now >> 8 * e & 255) - (top >> 8 * e & 255);
         const float f = by < 127 ? __uint_as_float((127 - by) << 23) : 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n)

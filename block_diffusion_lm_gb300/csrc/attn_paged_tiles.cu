@@ -417,7 +417,7 @@ struct Copier {
   }
 
   __device__ __forceinline__ void run_v(int steps) {
-    uint32_t top = 0;
+    uint32_t top = 0, first = 0;  // E, and E when a piece began
 #pragma unroll 1
     for (int t = 0; t < steps; ++t) {
       const int h = 2 * t + 1;
@@ -446,12 +446,13 @@ struct Copier {
       // (twice as much as now, so that a little growth does not rescale O)
       bool far = false;
       if (begins) {
-        top = __vaddus4(v, 0x01010101u);
+        top = first = __vaddus4(v, 0x01010101u);
       } else if (__vmaxu4(top, v) != top) {
-        const uint32_t old = top;
         top = __vmaxu4(top, __vaddus4(v, 0x01010101u));
-        // O follows E by 2^64 (or from a byte of 1, that of zeros: then it is nothing)
-        far = at_least_u8x4((top - old) & ~__vcmpleu4(old, 0x01010101u), 0x41414141u) != 0;
+        // O follows E by 2^64 (and any way from a byte of 1, that of zeros: then it is nothing)
+        const uint32_t zeros = __vcmpleu4(first, 0x01010101u);
+        first = (first & ~zeros) | (top & zeros);
+        far = at_least_u8x4(top - first, 0x41414141u) != 0;
       }
       if (lane == 0) {
         info.k_factor = ldexpf(1.f, static_cast<int>(k) - 127 - kHeadroom);

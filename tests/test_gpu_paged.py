@@ -925,6 +925,29 @@ def test_values_far_apart_under_scale_bytes_anywhere(n):
         assert same(a.forward(q, odd, table, length), want)
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,d", FAR_TILES + FAR)
+def test_values_that_grow_step_by_step(n, Hq, Hkv, d):
+    """V's scales rise by 2^40 every 256 keys, of keys without weight: what the first keys
+    gave remains, in texts that a CTA takes as wholes."""
+    B, page, per = 304, 64, 20
+    c = filled(per, page, Hkv, d, gen(65))
+    q = normal(gen(66), B, n, Hq, d)
+    q[..., 3] = 8
+    table = torch.arange(per, device="cuda").int().repeat(B, 1)
+    length = i32([1280 - b % 7 for b in range(B)])
+    c.v_scale.fill_(40)
+    c.k[4:] = 0
+    c.k[4:, :, :, 3] = 0xfe
+    c.k_scale[4:, :, :, 0] = 127 - 4                  # -28: a score of -224
+    for pg in range(4, per):
+        c.v_scale[pg] = 40 + 40 * (pg // 4)
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, scale=1.0)
+    o, lse = a.forward(q, c, table, length)
+    for b in (0, 150, 303):
+        at = slice(b, b + 1)
+        check_far((o[at], lse[at]), q[at], c, table[at], length[at], False, 0, 0, 1.0)
+
+
 def test_queries_far_apart():
     """Rows of very large and very small queries."""
     B, n, per, page, Hq, Hkv, d = 1, 8, 4, 16, 4, 2, 128
