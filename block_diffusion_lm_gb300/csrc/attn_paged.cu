@@ -212,6 +212,28 @@ __device__ __noinline__ float3 join_sums(float a, float b) {
   return make_float3(x * f, y * f, both == 0.f ? -INFINITY : ref + log2f(both));
 }
 
+// The largest of a warp's words, byte by byte.
+__device__ __forceinline__ uint32_t warp_max4(uint32_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = __vmaxu4(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+// Whether a scale byte is more than 14 below `most`; one of 0 is not.
+__device__ __forceinline__ bool far_below(uint32_t number, uint32_t most) {
+  return at_least_u8x4(__vsubus4(most, number | __vcmpeq4(number, 0)), 0x0f0f0f0fu) != 0;
+}
+// Of the keys `there`, a lane each, the first and those whose scale bytes all lie within 7
+// of its own; where its own is 0, within 14 of the largest.  (0 is near any.)
+__device__ __noinline__ uint32_t near_first(uint32_t number, uint32_t most, uint32_t there) {
+  const uint32_t first = __shfl_sync(0xffffffffu, number, __ffs(there) - 1);
+  const uint32_t none = __vcmpeq4(first, 0), of = first | (most & none);
+  const uint32_t lo = __vsubus4(of, 0x07070707u + (0x07070707u & none));
+  const uint32_t hi = __vaddus4(of, 0x07070707u & ~none);
+  return there & __ballot_sync(0xffffffffu,
+                               at_least_u8x4(number | __vcmpeq4(number, 0), lo) == 0x80808080u &&
+                                   at_least_u8x4(hi, number) == 0x80808080u);
+}
+
 template <int D, int NT>
 struct Kernel {
   using L = Rows<D, NT>;
@@ -392,29 +414,21 @@ struct Kernel {
   // summed yet.)
   __device__ __forceinline__ uint32_t odd_scales(uint32_t word, bool fresh, uint32_t& there,
                                                  uint32_t& delta) {
-    uint32_t left = 0, number, now;
-#pragma unroll 1
-    for (;;) {
-      number = there >> lane & 1 ? word & ~__vcmpeq4(word, 0xffffffffu) : 0;
-      const uint32_t or_none = number | __vcmpeq4(number, 0);  // 255 for 0
-      now = __vmaxu4(number, top);  // (fresh: top is 0)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) now = __vmaxu4(now, __shfl_xor_sync(0xffffffffu, now, o));
-      if (!__any_sync(0xffffffffu, at_least_u8x4(__vsubus4(now, or_none), 0x0f0f0f0fu) != 0)) break;
+    uint32_t left = 0;
+    uint32_t number = there >> lane & 1 ? word & ~__vcmpeq4(word, 0xffffffffu) : 0;
+    uint32_t now = warp_max4(__vmaxu4(number, top));  // (fresh: top is 0)
+    if (__any_sync(0xffffffffu, far_below(number, now))) {
       if (!fresh) return there;
-      const uint32_t first = __shfl_sync(0xffffffffu, number, __ffs(there) - 1);
-      const uint32_t none = __vcmpeq4(first, 0);  // groups of it that go by the largest
-      const uint32_t lo = __vsubus4((first & ~none) | (now & none), 0x07070707u + (0x07070707u & none));
-      const uint32_t hi = __vaddus4((first & ~none) | (now & none), 0x07070707u & ~none);
-      const bool near = at_least_u8x4(or_none, lo) == 0x80808080u &&
-                        at_least_u8x4(hi, number) == 0x80808080u;
-      const uint32_t part = __ballot_sync(0xffffffffu, near) & there;
-      left |= there & ~part;
-      there = part;
+      left = there;
+      there = near_first(number, now, there);
+      left &= ~there;
+      number = there >> lane & 1 ? number : 0;
+      now = warp_max4(number);
     }
     uint32_t first = lds32(mem + L::kFirstTop);
     first |= now & __vcmpeq4(first, 0);
-    if (at_least_u8x4(now - first, 0x41414141u)) return there;  // (nothing is borrowed)
+    // (nothing is borrowed; a fresh sum never waits for another)
+    if (!fresh && at_least_u8x4(now - first, 0x41414141u)) return there;
     __syncwarp();
     if (lane == 0) sts32(mem + L::kFirstTop, first);
     if (!fresh) {
@@ -960,12 +974,14 @@ __global__ void __launch_bounds__(most_warps(NT) * 32, 1)
                    : "=r"(r.step), "=r"(r.n), "=r"(r.c), "=r"(r.left)
                    : "r"(k.mem + stage * L::kStage + L::kRecord + 16)
                    : "memory");
-      if (r.left) {
-        __syncwarp();  // (all lanes have read the record)
-        if (k.lane == 0) sts32(k.mem + stage * L::kStage + L::kRecord + 28, 0);
-      } else if (i == 0 || r.step == 0) {
-        k.begin(r);
-        in_sum = 0;
+      if (i == 0 || r.step == 0 || r.left) {
+        if (!r.left) {
+          k.begin(r);
+          in_sum = 0;
+        } else {
+          __syncwarp();  // (all lanes have read the record)
+          if (k.lane == 0) sts32(k.mem + stage * L::kStage + L::kRecord + 28, 0);
+        }
       }
       copies_wait<kStages - 1>();
       __syncwarp();
