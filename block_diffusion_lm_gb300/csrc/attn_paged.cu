@@ -42,13 +42,13 @@
 // accumulator drops what is below its last place at every MMA of 16 keys: after
 // 2,048 of them (2^-13) O is put aside in the workspace and a new sum begun.
 //
-// What bounds it.  One query of 32 heads: 64 sequences of 8,192 keys, 8 heads of 128: 140
-// us, 5.9 TB/s; 4 of 1,048,576, 4 heads: 484 us, 6.8 TB/s, the rate of a copy.  Beside
+// What bounds it.  One query of 32 heads: 64 sequences of 8,192 keys, 8 heads of 128: 143
+// us, 5.8 TB/s; 4 of 1,048,576, 4 heads: 490 us, 6.8 TB/s, the rate of a copy.  Beside
 // the bytes a call has about 15 us: finding the share and the first pages (4), the ring
 // filling and draining, the end of a piece and its joining (3 each).  A window of 1,024
-// in 61 sequences takes 37.5 us of which the bytes are 20.  From 10 rows on, the MMAs, the
-// conversions and the softmax bound it: 16 sequences of 16,000 keys, 8 heads, take 98
-// us for 10 rows and 57 us more for every 16.
+// in 61 sequences takes 38.6 us of which the bytes are 20.  From 10 rows on, the MMAs, the
+// conversions and the softmax bound it: 16 sequences of 16,000 keys, 8 heads, take 96
+// us for 10 rows and 61 us more for every 16.
 //
 // Keys that a row does not read.  Steps at the edge of a row's range are masked;
 // there, NaN codes of V are taken out of the product and put back into the rows
@@ -80,9 +80,9 @@ constexpr int kStages = 2;
 constexpr int kKeys = 32;     // of a warp's step, two MMAs
 // Rows of a head and sequence that go to row tiles of 16, which read the keys again
 // each (from L2); more go to whole tiles (attn_paged_tiles.cu).  16 sequences of 16,000
-// keys, 8 heads of 128: 20 / 40 / 45 / 60 rows take 165 / 227 / 228 / 289 us here and
-// 275 / 280 / 282 / 282 there; 24 sequences with a window of 1,000, 2 heads of 64: 28 / 56
-// rows 18.2 / 26.9 and 24.1 / 24.7.
+// keys, 8 heads of 128: 20 / 40 / 45 / 60 rows take 153 / 217 / 218 / 279 us here and
+// 247 / 246 / 245 / 246 there; 24 sequences with a window of 1,000, 2 heads of 64: 28 / 56
+// rows 16.8 / 26.6 and 20.9 / 20.9.
 constexpr int kMostRows = 48;
 constexpr int kFlush = 1024;  // steps that one accumulator takes in
 constexpr float kShift = 14.f;  // p is held as p 2^14; a row's maximum may lag by 2^1

@@ -28,9 +28,9 @@
 // every other K in the place of the second.  One thread issues the MMAs, two warpgroups
 // do the softmax, a row per thread, as in the training forward.
 //
-// What bounds it.  16 sequences of 16,384 keys, 8 heads of 128, 160 rows: 255 us, where
+// What bounds it.  16 sequences of 16,384 keys, 8 heads of 128, 160 rows: 264 us, where
 // the bytes take 63 and the MMAs 115 (of 2 x 128 rows); a chunk of 2,000 tokens in a
-// window of 1,024: 178 us, MMAs 40.  A pair of row tiles takes a key tile in 4,600
+// window of 1,024: 180 us, MMAs 40.  A pair of row tiles takes a key tile in 4,600
 // clocks: two softmax rows of 128 scores per thread (1,800 clocks alone, 3,700 both at
 // once), P V, and the next S, with a handover of 300 to 400 clocks between them, and
 // beside that the conversion of K and V (3,500).  An item of a window costs 12,000 more
