@@ -407,8 +407,9 @@ struct Kernel {
   // summed under the old one is scaled, and `delta` is E - e, or 15 where a scale is that far
   // below because its byte is 0 (what is below 2^-118 counts as 0 there) or NaN.
   //
-  // Where the scales do not lie within 2^14 of E, or E has risen since the sum's begin by more
-  // than fp32 can follow, the sum so far is to be put aside first: all of `there` is left for then.
+  // Where the scales do not lie within 2^14 of E, or E has risen since the sum's begin by
+  // more than fp32 can follow, the sum so far is to be put aside first: all of `there` is left
+  // for then.
   // Where they do not lie within 2^14 of one another, `there` becomes those of the first key
   // and the ones near it in each group.  Returns what is left.  (`fresh`: nothing has been
   // summed yet.)
@@ -1047,7 +1048,7 @@ constexpr int kExactRows = 8;
 template <int D>
 __device__ __noinline__ void exact_rows(const PagedParams& p, int entry, int head, int from,
                                         int rows) {
-  __shared__ float queries[kExactRows][D];
+  __shared__ __align__(16) float queries[kExactRows][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = p.by_row_tiles(entry), tile = entry - b * p.row_tiles;
   const Range r = range_of(p, b, tile, kPairRows);
@@ -1069,7 +1070,8 @@ __device__ __noinline__ void exact_rows(const PagedParams& p, int entry, int hea
         p.q + b * p.q_bat + token[x] * p.q_tok + static_cast<int64_t>(h[x]) * D;
     float most = 0.f;
     for (int c = lane; c < D; c += 32) most = fmaxf(most, fabsf(__bfloat162float(q[c])));
-    const int ex = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 127, -110);
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    const int ex = max(static_cast<int>(bits >> 23) - 127, -110);
     const float scale = ldexpf(1.f, -ex);
     for (int c = lane; c < D; c += 32) queries[2 * warp + x][c] = __bfloat162float(q[c]) * scale;
     row_scale[x] = fmaxf(p.scale_log2 * ldexpf(1.f, ex), 1e-44f);
@@ -1092,7 +1094,8 @@ __device__ __noinline__ void exact_rows(const PagedParams& p, int entry, int hea
     if (there) {
 #pragma unroll 1
       for (int e = 0; e < F; ++e) {
-        const uint4* codes = reinterpret_cast<const uint4*>(p.k + static_cast<uint64_t>(place) * D) + 2 * e;
+        const uint4* codes =
+            reinterpret_cast<const uint4*>(p.k + static_cast<uint64_t>(place) * D) + 2 * e;
         float sum[2] = {0.f, 0.f};
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
