@@ -948,6 +948,90 @@ def test_values_that_grow_step_by_step(n, Hq, Hkv, d):
         check_far((o[at], lse[at]), q[at], c, table[at], length[at], False, 0, 0, 1.0)
 
 
+def zeros_of_large_scale(c, name="v"):
+    """Every 9th token of the cache: codes of 0 under a scale 2^60 above the others'.  It
+    alters no value, only the path that is taken."""
+    pages, page = c.k.shape[:2]
+    at = (torch.arange(pages * page, device="cuda").view(pages, page) * 7 % 9 == 0)
+    getattr(c, name)[at] = 0
+    getattr(c, name + "_scale")[at] += 60
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("causal,window,sinks", MASKS)
+def test_attention_where_scales_lie_far_apart(shape, causal, window, sinks):
+    """All shapes and masks in the paths of scales far apart; V's for one half, K's for the
+    other, where queries and pages are missing or not finite, too."""
+    B, n, per, page, Hq, Hkv, d, lens = shape
+    c, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 71, lens)
+    zeros_of_large_scale(c)
+    table[::2, per // 2] = -1
+    wide = normal(gen(72), B, n, Hq + 1, d)[:, :, :Hq]
+    wide.copy_(q)
+    a = csbp.PagedAttention(B, n, per, page, Hq, Hkv, d, causal=causal, window=window, sinks=sinks)
+    out = a.forward(wide, c, table, length)
+    check_attn(out, q, c, table, length, causal, window, sinks, d ** -0.5)
+    assert same(a.forward(q, c, table, length), out)
+    a.check()
+    c2, q, table, length = attn_case(B, n, per, page, Hq, Hkv, d, 73, lens)
+    zeros_of_large_scale(c2, "k")
+    out = a.forward(q, c2, table, length)
+    check_attn(out, q, c2, table, length, causal, window, sinks, d ** -0.5)
+    if n > 1:        # a query that is not finite has no part in the others
+        bad = q.clone()
+        bad[:, n // 2] = float("nan")
+        o, lse = a.forward(bad, c2, table, length)
+        others = [i for i in range(n) if i != n // 2]
+        assert same((o[:, others], lse[:, :, others]), (out[0][:, others], out[1][:, :, others]))
+
+
+@pytest.mark.parametrize("n", [4, 80])
+def test_captured_call_meets_scales_far_apart(n):
+    """One graph, replayed with scales that are near, far apart and near again."""
+    c, q, table, length = attn_case(3, n, 12, 64, 4, 2, 128, 74, [768, 100, 500])
+    far = csbp.QuantCache(*c.k.shape, storage=[t.clone() for t in stored(c)])
+    zeros_of_large_scale(far)
+    a = csbp.PagedAttention(3, n, 12, 64, 4, 2, 128, causal=True)
+    want = [[x.clone() for x in a.forward(q, y, table, length)] for y in (c, far)]
+    near = stored(c)
+    out = a.alloc_outputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.forward(q, c, table, length, out=out)
+    for k in (0, 1, 1, 0):
+        for t, x in zip((c.k, c.v, c.k_scale, c.v_scale), (near, stored(far))[k]):
+            t.copy_(x)
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, want[k])
+
+
+def test_sums_in_parts_over_a_long_text():
+    """q = 0 over a million keys of which some take the paths of scales far apart: O is the
+    mean of V, to 2^-8 for its rounding and 2^-10 for the sums, LSE the number's ln."""
+    page, per, Hkv, d = 64, 16384, 1, 64
+    c = csbp.QuantCache(64, page, Hkv, d)
+    x = (torch.rand((64, page, Hkv, d), generator=gen(75), device="cuda") + 0.5).bfloat16()
+    c.write(x, x, torch.arange(64, device="cuda").int()[:, None], i32([0] * 64))
+    zeros_of_large_scale(c)
+    table = torch.randint(0, 64, (2, per), generator=gen(76), device="cuda").int()
+    length = i32([per * page, 300000])
+    v = torch.from_numpy(values(c)[1]).cuda()[:, :, 0]
+    for n in (1, 50):
+        a = csbp.PagedAttention(2, n, per, page, 1, Hkv, d)
+        o, lse = a.forward(torch.zeros((2, n, 1, d), dtype=torch.bfloat16, device="cuda"), c, table,
+                           length)
+        a.check()
+        for b in range(2):
+            m = int(length[b])
+            want = v.sum(1)[table[b, :m // page].long()].sum(0)
+            want = (want + v[table[b, -(-m // page) - 1].long(), :m % page].sum(0)) / m
+            assert ((o[b].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want).all()
+            assert (lse[b].double() - np.log(m)).abs().max() <= 2.0 ** -10
+
+
 def test_queries_far_apart():
     """Rows of very large and very small queries."""
     B, n, per, page, Hq, Hkv, d = 1, 8, 4, 16, 4, 2, 128
